@@ -425,6 +425,132 @@ moe_status moe_router_backward(const void* logits, moe_dtype logits_dtype, const
                                int scoring, int renormalize, float scale, void* dlogits,
                                cudaStream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Training losses of the router.  No counterpart on the pages, whose router
+ * training ends at the gradient of the routing weights (moe_router_backward):
+ * what else a router is trained with, over the same logits [T,E].
+ *
+ * Shared by the calls below:
+ *   - A batch holds num_seqs packed sequences: sequence s is the rows
+ *     seq_offsets[s] <= t < seq_offsets[s+1] (device, uint32 [num_seqs+1],
+ *     non-decreasing, at most T; sequences of no rows are fine).  NULL: one
+ *     sequence of all T rows (num_seqs must be 1).  1 <= num_seqs <= 2^20.
+ *   - token_mask (device, one byte per row, NULL: all rows) is zero for rows
+ *     that do not count, such as padding.  Such rows, and rows outside every
+ *     sequence, may hold anything (their logits, indices and lists are not
+ *     read into any result): their statistics are 0, their gradient is 0.
+ *   - Losses are means over a sequence's counted rows; a sequence without any
+ *     has loss 0.  Statistics and sums are FP32, or integers, added in a fixed
+ *     order: results are bitwise reproducible.
+ *   - A forward checks the offsets on the device: an entry below its
+ *     predecessor or above T sets MOE_ERR_INVALID_INDEX in the workspace
+ *     status word; results are then undefined and no access leaves the
+ *     buffers.
+ *   - A backward writes dlogits [T,E] = base + gradient in the logits dtype,
+ *     added in FP32 and rounded once.  base [T,E] (logits dtype) may be NULL
+ *     (no addend) or dlogits itself, so that the gradients of the routing
+ *     weights and of several losses add up in one buffer.
+ *   - A backward takes what its forward wrote: row_stats as it is, and tokens
+ *     and counts as integers that the caller may first add up over the parts
+ *     of a larger batch.
+ *   - T == 0 is valid: a forward writes zero losses and counts.
+ * ---------------------------------------------------------------------- */
+
+/* Balance loss, expert counts and z-loss.  With idx [T,top_k] the routed
+ * experts, V_s the counted rows of sequence s, L_s = |V_s|, and scores p_te
+ * that sum to one over the experts (scoring 0: softmax of the row; 1: sigmoid
+ * of each logit, divided by the row's sum):
+ *   counts[s,e]      = number of slots of V_s routed to expert e      (uint32)
+ *   mean_scores[s,e] = 1/L_s sum_{t in V_s} p_te                      (nullable)
+ *   loss[s]          = E sum_e counts[s,e] / (top_k L_s) mean_scores[s,e]
+ *   z_loss[s]        = 1/L_s sum_{t in V_s} (log sum_e exp(l_te))^2   (nullable;
+ *                      scoring 0 only, else MOE_ERR_UNSUPPORTED)
+ *   tokens[s]        = L_s                                            (uint32)
+ *   row_stats[t]     = (shift, sum), FP32 [T,2], 8-byte aligned: the row's
+ *                      maximum and sum_e exp(l - maximum); for sigmoid scoring
+ *                      0 and the sum of the sigmoids, or, where no logit
+ *                      reaches -60, as for softmax; (0, 0) for rows that do
+ *                      not count.
+ * A slot counts once however often its row names the expert; an index >= E is
+ * counted nowhere and sets MOE_ERR_INVALID_INDEX in the status word.  A
+ * counted row holding a NaN (softmax: also +inf, or only -inf; sigmoid: also
+ * only -inf) makes its sequence's loss, mean_scores and z_loss NaN.
+ * workspace: moe_balance_loss_workspace_size(T, E, num_seqs) bytes. */
+size_t moe_balance_loss_workspace_size(int64_t T, int64_t E, int64_t num_seqs);
+moe_status moe_balance_loss(const void* logits, moe_dtype logits_dtype, const uint32_t* idx,
+                            const uint8_t* token_mask, const uint32_t* seq_offsets, int64_t T,
+                            int64_t E, int32_t top_k, int64_t num_seqs, int scoring, float* loss,
+                            float* z_loss, float* mean_scores, uint32_t* counts, uint32_t* tokens,
+                            float* row_stats, void* workspace, size_t workspace_bytes,
+                            cudaStream_t stream);
+
+/* Gradient of sum_s dloss[s] loss[s] + dz_loss[s] z_loss[s] (dloss and dz_loss
+ * FP32 [num_seqs] on the device; dz_loss NULL: none) with respect to the
+ * logits.  The counts are constants.  With g_se = dloss[s] E counts[s,e] /
+ * (top_k L_s^2):
+ *   softmax  dl_te = p_te (g_se - sum_i p_ti g_si + 2 dz_loss[s] lse_t / L_s)
+ *   sigmoid  dl_te = p_te (1 - sigmoid(l_te)) (g_se - sum_i p_ti g_si)
+ * A NaN row gets a NaN gradient and leaves the other rows alone. */
+moe_status moe_balance_loss_backward(const void* logits, moe_dtype logits_dtype,
+                                     const float* row_stats, const uint32_t* counts,
+                                     const uint32_t* tokens, const uint32_t* seq_offsets,
+                                     int64_t T, int64_t E, int32_t top_k, int64_t num_seqs,
+                                     int scoring, const float* dloss, const float* dz_loss,
+                                     const void* base, void* dlogits, cudaStream_t stream);
+
+/* A teacher router's top logits, for distillation: per row of teacher_logits
+ * [T,E] the top_m largest (ties to the lower expert id, +0 == -0) in
+ * descending order, idx [T,top_m] and top_logits [T,top_m] (teacher dtype),
+ * and the logit of all other experts together at the given temperature tau,
+ *   rest[t] = tau log sum_{e not in the list} exp(l_te / tau)   (FP32 [T]),
+ * -inf where they hold nothing.  A row holding a NaN or +inf gets
+ * idx = 0..top_m-1 and NaN logits and rest.  1 <= top_m <= min(E, 64),
+ * 0.001 <= tau <= 1000. */
+moe_status moe_distill_targets(const void* teacher_logits, moe_dtype teacher_dtype, int64_t T,
+                               int64_t E, int32_t top_m, float temperature, uint32_t* idx,
+                               void* top_logits, float* rest, cudaStream_t stream);
+
+/* Distillation loss of student logits [T,E] from a teacher's lists.  With
+ * a_j = teacher_logits[t,j] / tau, a_r = teacher_rest[t] / tau and
+ * b_e = logits[t,e] / tau:
+ *   q = softmax(a_1 .. a_m, a_r),  p = softmax(b),  R = sum_{e not in the list} p_e
+ *   KL_t = sum_j q_j log(q_j / p_idx_j) + q_r log(q_r / R)
+ * teacher_rest NULL: no rest, q = softmax(a_1 .. a_m).  A list entry of -inf
+ * is absent and its index is not read; a row whose list and rest hold nothing
+ * but -inf has no target and does not count.
+ *   loss[s] = mean of KL_t over the counted rows, tokens[s] = their number
+ *   row_loss [T]: KL_t (0 for rows that do not count)
+ *   row_stats [5,T]: max_e l_te, sum_e exp(b_e - max b), the maximum of the
+ *   list and rest, the sum of their exponentials about it, q_r / R (0 without
+ *   a rest; -q_r where R is below 1e-30 of exp(-max b)); 0 for rows that do
+ *   not count.
+ * A counted row with a NaN or +inf on either side, only -inf on the student's,
+ * or a listed expert >= E or listed twice gives NaN (the latter two also set
+ * MOE_ERR_INVALID_INDEX in the status word).  KL is +inf where the teacher
+ * gives mass to what the student has at -inf.
+ * The teacher's dtype may differ from the student's.
+ * workspace: moe_distill_loss_workspace_size(T, num_seqs) bytes. */
+size_t moe_distill_loss_workspace_size(int64_t T, int64_t num_seqs);
+moe_status moe_distill_loss(const void* logits, moe_dtype logits_dtype,
+                            const uint32_t* teacher_idx, const void* teacher_logits,
+                            moe_dtype teacher_dtype, const float* teacher_rest,
+                            const uint8_t* token_mask, const uint32_t* seq_offsets, int64_t T,
+                            int64_t E, int32_t top_m, int64_t num_seqs, float temperature,
+                            float* loss, uint32_t* tokens, float* row_loss, float* row_stats,
+                            void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* Gradient of sum_s dloss[s] loss[s] with respect to the student's logits:
+ *   dl_te = dloss[s] / (tokens[s] tau) (p_e - q_j)          for a listed e = idx_j
+ *         = dloss[s] / (tokens[s] tau) p_e (1 - q_r / R)     otherwise
+ * A NaN row gets a NaN gradient and leaves the other rows alone. */
+moe_status moe_distill_loss_backward(const void* logits, moe_dtype logits_dtype,
+                                     const uint32_t* teacher_idx, const void* teacher_logits,
+                                     moe_dtype teacher_dtype, const float* row_stats,
+                                     const uint32_t* tokens, const uint32_t* seq_offsets,
+                                     int64_t T, int64_t E, int32_t top_m, int64_t num_seqs,
+                                     float temperature, const float* dloss, const void* base,
+                                     void* dlogits, cudaStream_t stream);
+
 /* Diagnostics (no counterpart on the pages): exercises the failure path of
  * the bounded waits inside this library's kernels.  Enqueues one small kernel
  * that waits on a barrier nothing completes; after limit_ms (1..2000) the

@@ -24,6 +24,9 @@ import torch
 
 from . import _lib
 from ._lib import DTYPE_CODES, MoeError  # noqa: F401
+from .router_losses import (BalanceLoss, DistillLoss, DistillTargets, moe_balance_loss,
+                            moe_balance_loss_backward, moe_balance_loss_workspace, moe_distill_loss,
+                            moe_distill_loss_backward, moe_distill_loss_workspace, moe_distill_targets)
 
 _TORCH_CODES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 _CODE_TORCH = {v: k for k, v in _TORCH_CODES.items()}
@@ -31,6 +34,9 @@ _CODE_TORCH = {v: k for k, v in _TORCH_CODES.items()}
 __all__ = ["load", "moe_route", "moe_route_sigmoid_grouped", "moe_dispatch", "moe_combine",
            "SwiGluExperts", "Dispatched", "moe_combine_backward", "moe_dispatch_backward",
            "moe_router_weights", "moe_router_backward",
+           "moe_balance_loss", "moe_balance_loss_backward", "moe_balance_loss_workspace", "BalanceLoss",
+           "moe_distill_targets", "moe_distill_loss", "moe_distill_loss_backward",
+           "moe_distill_loss_workspace", "DistillTargets", "DistillLoss",
            "moe_get_device_status", "MoeError", "library_path", "HostPipeline"]
 
 

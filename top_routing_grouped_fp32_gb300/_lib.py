@@ -93,6 +93,15 @@ _SIGNATURES = {
     "moe_experts_backward_with_strategy": (ST, [P, P, I64, P, P, P, P, P, P, I32, P, SZ, P]),
     "moe_router_weights": (ST, [P, INT, P, I64, I64, I32, INT, INT, ctypes.c_float, P, P]),
     "moe_router_backward": (ST, [P, INT, P, P, I64, I64, I32, INT, INT, ctypes.c_float, P, P]),
+    "moe_balance_loss_workspace_size": (SZ, [I64, I64, I64]),
+    "moe_balance_loss": (ST, [P, INT, P, P, P, I64, I64, I32, I64, INT, P, P, P, P, P, P, P, SZ, P]),
+    "moe_balance_loss_backward": (ST, [P, INT, P, P, P, P, I64, I64, I32, I64, INT, P, P, P, P, P]),
+    "moe_distill_targets": (ST, [P, INT, I64, I64, I32, ctypes.c_float, P, P, P, P]),
+    "moe_distill_loss_workspace_size": (SZ, [I64, I64]),
+    "moe_distill_loss": (ST, [P, INT, P, P, INT, P, P, P, I64, I64, I32, I64, ctypes.c_float, P, P, P, P,
+                              P, SZ, P]),
+    "moe_distill_loss_backward": (ST, [P, INT, P, P, INT, P, P, P, I64, I64, I32, I64, ctypes.c_float, P,
+                                       P, P, P]),
     "moe_selftest_bounded_wait": (ST, [P, ctypes.c_uint32, P]),
 }
 

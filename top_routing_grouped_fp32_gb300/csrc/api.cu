@@ -922,6 +922,161 @@ moe_status moe_router_backward(const void* logits, moe_dtype ldt, const uint32_t
   return ok();
 }
 
+// ---- training losses of the router -----------------------------------------
+namespace {
+
+moe_status check_seqs(const uint32_t* offsets, int64_t num_seqs) {
+  if (num_seqs < 1) return fail(MOE_ERR_SHAPE, "num_seqs must be >= 1 (got %lld)", (long long)num_seqs);
+  if (num_seqs > kMaxDim) return fail(MOE_ERR_UNSUPPORTED, "num_seqs=%lld exceeds 2^20", (long long)num_seqs);
+  if (!offsets && num_seqs != 1)
+    return fail(MOE_ERR_INVALID_ARG, "num_seqs=%lld needs seq_offsets (without them the batch is one sequence)",
+                (long long)num_seqs);
+  if (reinterpret_cast<uintptr_t>(offsets) % 4 != 0)
+    return fail(MOE_ERR_INVALID_ARG, "seq_offsets must be 4-byte aligned");
+  return MOE_OK;
+}
+
+// m entries per row of a list: the rules of top_k under the list's name
+moe_status check_list(int64_t T, int64_t E, int32_t m, float temperature) {
+  if (T < 0) return fail(MOE_ERR_SHAPE, "T must be >= 0 (got %lld)", (long long)T);
+  if (E < 1) return fail(MOE_ERR_SHAPE, "E must be >= 1 (got %lld)", (long long)E);
+  if (m < 1 || m > E)
+    return fail(MOE_ERR_INVALID_ARG, "top_m must satisfy 1 <= top_m <= E (top_m=%d, E=%lld)", m, (long long)E);
+  if (E > kMaxE) return fail(MOE_ERR_UNSUPPORTED, "E=%lld exceeds the supported 1024", (long long)E);
+  if (m > kMaxK) return fail(MOE_ERR_UNSUPPORTED, "top_m=%d exceeds the supported 64", m);
+  if (T > kMaxRows / m) return fail(MOE_ERR_UNSUPPORTED, "T*top_m=%lld exceeds 2^31-1", (long long)T * m);
+  if (!(temperature >= 1e-3f && temperature <= 1e3f))
+    return fail(MOE_ERR_INVALID_ARG, "temperature must be in 0.001..=1000 (got %g)", (double)temperature);
+  return MOE_OK;
+}
+
+bool aligned4(const void* p) { return reinterpret_cast<uintptr_t>(p) % 4 == 0; }
+bool aligned_to(const void* p, moe_dtype d) { return reinterpret_cast<uintptr_t>(p) % dtype_size(d) == 0; }
+
+}  // namespace
+
+size_t moe_balance_loss_workspace_size(int64_t T, int64_t E, int64_t num_seqs) {
+  if (T < 0 || E < 1 || E > kMaxE || num_seqs < 1 || num_seqs > kMaxDim) return 0;
+  return kWsHeader + moe::balance_workspace_bytes(T, (int)E, num_seqs);
+}
+
+moe_status moe_balance_loss(const void* logits, moe_dtype ldt, const uint32_t* idx, const uint8_t* token_mask,
+                            const uint32_t* seq_offsets, int64_t T, int64_t E, int32_t top_k, int64_t num_seqs,
+                            int scoring, float* loss, float* z_loss, float* mean_scores, uint32_t* counts,
+                            uint32_t* tokens, float* row_stats, void* ws, size_t ws_bytes, cudaStream_t stream) {
+  if (!valid_dtype(ldt)) return fail(MOE_ERR_DTYPE, "logits dtype %d is not F32/F16/BF16", (int)ldt);
+  moe_status st = check_tek(T, E, top_k);
+  if (st != MOE_OK) return st;
+  if ((st = check_seqs(seq_offsets, num_seqs)) != MOE_OK) return st;
+  if (scoring != 0 && scoring != 1) return fail(MOE_ERR_INVALID_ARG, "scoring must be 0 (softmax) or 1 (sigmoid)");
+  if (scoring == 1 && z_loss) return fail(MOE_ERR_UNSUPPORTED, "the z-loss is that of softmax scoring");
+  if (!loss || !counts || !tokens) return fail(MOE_ERR_INVALID_ARG, "loss, counts and tokens must be non-NULL");
+  if (T > 0 && (!logits || !idx || !row_stats))
+    return fail(MOE_ERR_INVALID_ARG, "logits, idx and row_stats must be non-NULL");
+  if (!aligned_to(logits, ldt) || !aligned4(idx) || !aligned4(loss) || !aligned4(z_loss) || !aligned4(mean_scores) ||
+      !aligned4(counts) || !aligned4(tokens) || reinterpret_cast<uintptr_t>(row_stats) % 8 != 0)
+    return fail(MOE_ERR_INVALID_ARG, "misaligned pointer (elements; row_stats 8 bytes)");
+  if ((st = check_ws(ws, ws_bytes, moe_balance_loss_workspace_size(T, E, num_seqs))) != MOE_OK) return st;
+  moe::BalanceArgs b{logits, ldt, idx, token_mask, seq_offsets, T, (int)E, top_k, num_seqs, scoring == 1,
+                     loss, z_loss, mean_scores, counts, tokens, row_stats};
+  MOE_TRY_CUDA(moe::launch_balance_loss(b, at<void>(ws, kWsHeader), status_word(ws), stream),
+               "balance loss kernel launch");
+  return ok();
+}
+
+moe_status moe_balance_loss_backward(const void* logits, moe_dtype ldt, const float* row_stats,
+                                     const uint32_t* counts, const uint32_t* tokens, const uint32_t* seq_offsets,
+                                     int64_t T, int64_t E, int32_t top_k, int64_t num_seqs, int scoring,
+                                     const float* dloss, const float* dz_loss, const void* base, void* dlogits,
+                                     cudaStream_t stream) {
+  if (!valid_dtype(ldt)) return fail(MOE_ERR_DTYPE, "logits dtype %d is not F32/F16/BF16", (int)ldt);
+  moe_status st = check_tek(T, E, top_k);
+  if (st != MOE_OK) return st;
+  if ((st = check_seqs(seq_offsets, num_seqs)) != MOE_OK) return st;
+  if (scoring != 0 && scoring != 1) return fail(MOE_ERR_INVALID_ARG, "scoring must be 0 (softmax) or 1 (sigmoid)");
+  if (scoring == 1 && dz_loss) return fail(MOE_ERR_UNSUPPORTED, "the z-loss is that of softmax scoring");
+  if (T == 0) return ok();
+  if (!logits || !row_stats || !counts || !tokens || !dloss || !dlogits)
+    return fail(MOE_ERR_INVALID_ARG, "logits, row_stats, counts, tokens, dloss and dlogits must be non-NULL");
+  if (!aligned_to(logits, ldt) || !aligned_to(base, ldt) || !aligned_to(dlogits, ldt) || !aligned4(counts) ||
+      !aligned4(tokens) || !aligned4(dloss) || !aligned4(dz_loss) || reinterpret_cast<uintptr_t>(row_stats) % 8 != 0)
+    return fail(MOE_ERR_INVALID_ARG, "misaligned pointer (elements; row_stats 8 bytes)");
+  moe::BalanceBwdArgs b{logits, ldt, row_stats, counts, tokens, seq_offsets, T, (int)E, top_k, num_seqs,
+                        scoring == 1, dloss, dz_loss, base, dlogits};
+  MOE_TRY_CUDA(moe::launch_balance_loss_backward(b, stream), "balance loss backward kernel launch");
+  return ok();
+}
+
+moe_status moe_distill_targets(const void* teacher_logits, moe_dtype tdt, int64_t T, int64_t E, int32_t top_m,
+                               float temperature, uint32_t* idx, void* top_logits, float* rest, cudaStream_t stream) {
+  if (!valid_dtype(tdt)) return fail(MOE_ERR_DTYPE, "teacher logits dtype %d is not F32/F16/BF16", (int)tdt);
+  moe_status st = check_list(T, E, top_m, temperature);
+  if (st != MOE_OK) return st;
+  if (T == 0) return ok();
+  if (!teacher_logits || !idx || !top_logits || !rest)
+    return fail(MOE_ERR_INVALID_ARG, "teacher_logits, idx, top_logits and rest must be non-NULL");
+  if (!aligned_to(teacher_logits, tdt) || !aligned_to(top_logits, tdt) || !aligned4(idx) || !aligned4(rest))
+    return fail(MOE_ERR_INVALID_ARG, "misaligned pointer (elements)");
+  MOE_TRY_CUDA(moe::launch_distill_targets(teacher_logits, tdt, T, (int)E, top_m, temperature, idx, top_logits, rest,
+                                           stream),
+               "distillation targets kernel launch");
+  return ok();
+}
+
+size_t moe_distill_loss_workspace_size(int64_t T, int64_t num_seqs) {
+  if (T < 0 || num_seqs < 1 || num_seqs > kMaxDim) return 0;
+  return kWsHeader + moe::distill_workspace_bytes(T, num_seqs);
+}
+
+moe_status moe_distill_loss(const void* logits, moe_dtype ldt, const uint32_t* teacher_idx,
+                            const void* teacher_logits, moe_dtype tdt, const float* teacher_rest,
+                            const uint8_t* token_mask, const uint32_t* seq_offsets, int64_t T, int64_t E,
+                            int32_t top_m, int64_t num_seqs, float temperature, float* loss, uint32_t* tokens,
+                            float* row_loss, float* row_stats, void* ws, size_t ws_bytes, cudaStream_t stream) {
+  if (!valid_dtype(ldt)) return fail(MOE_ERR_DTYPE, "logits dtype %d is not F32/F16/BF16", (int)ldt);
+  if (!valid_dtype(tdt)) return fail(MOE_ERR_DTYPE, "teacher logits dtype %d is not F32/F16/BF16", (int)tdt);
+  moe_status st = check_list(T, E, top_m, temperature);
+  if (st != MOE_OK) return st;
+  if ((st = check_seqs(seq_offsets, num_seqs)) != MOE_OK) return st;
+  if (!loss || !tokens) return fail(MOE_ERR_INVALID_ARG, "loss and tokens must be non-NULL");
+  if (T > 0 && (!logits || !teacher_idx || !teacher_logits || !row_loss || !row_stats))
+    return fail(MOE_ERR_INVALID_ARG,
+                "logits, teacher_idx, teacher_logits, row_loss and row_stats must be non-NULL");
+  if (!aligned_to(logits, ldt) || !aligned_to(teacher_logits, tdt) || !aligned4(teacher_idx) ||
+      !aligned4(teacher_rest) || !aligned4(loss) || !aligned4(tokens) || !aligned4(row_loss) || !aligned4(row_stats))
+    return fail(MOE_ERR_INVALID_ARG, "misaligned pointer (elements)");
+  if ((st = check_ws(ws, ws_bytes, moe_distill_loss_workspace_size(T, num_seqs))) != MOE_OK) return st;
+  moe::DistillArgs d{logits, ldt, teacher_idx, teacher_logits, tdt, teacher_rest, token_mask, seq_offsets, T,
+                     (int)E, top_m, num_seqs, temperature, loss, tokens, row_loss, row_stats};
+  MOE_TRY_CUDA(moe::launch_distill_loss(d, at<void>(ws, kWsHeader), status_word(ws), stream),
+               "distillation loss kernel launch");
+  return ok();
+}
+
+moe_status moe_distill_loss_backward(const void* logits, moe_dtype ldt, const uint32_t* teacher_idx,
+                                     const void* teacher_logits, moe_dtype tdt, const float* row_stats,
+                                     const uint32_t* tokens, const uint32_t* seq_offsets, int64_t T, int64_t E,
+                                     int32_t top_m, int64_t num_seqs, float temperature, const float* dloss,
+                                     const void* base, void* dlogits, cudaStream_t stream) {
+  if (!valid_dtype(ldt)) return fail(MOE_ERR_DTYPE, "logits dtype %d is not F32/F16/BF16", (int)ldt);
+  if (!valid_dtype(tdt)) return fail(MOE_ERR_DTYPE, "teacher logits dtype %d is not F32/F16/BF16", (int)tdt);
+  moe_status st = check_list(T, E, top_m, temperature);
+  if (st != MOE_OK) return st;
+  if ((st = check_seqs(seq_offsets, num_seqs)) != MOE_OK) return st;
+  if (T == 0) return ok();
+  if (!logits || !teacher_idx || !teacher_logits || !row_stats || !tokens || !dloss || !dlogits)
+    return fail(MOE_ERR_INVALID_ARG,
+                "logits, teacher_idx, teacher_logits, row_stats, tokens, dloss and dlogits must be non-NULL");
+  if (!aligned_to(logits, ldt) || !aligned_to(teacher_logits, tdt) || !aligned_to(base, ldt) ||
+      !aligned_to(dlogits, ldt) || !aligned4(teacher_idx) || !aligned4(row_stats) || !aligned4(tokens) ||
+      !aligned4(dloss))
+    return fail(MOE_ERR_INVALID_ARG, "misaligned pointer (elements)");
+  moe::DistillBwdArgs d{logits, ldt, teacher_idx, teacher_logits, tdt, row_stats, tokens, seq_offsets, T,
+                        (int)E, top_m, num_seqs, temperature, dloss, base, dlogits};
+  MOE_TRY_CUDA(moe::launch_distill_loss_backward(d, stream), "distillation loss backward kernel launch");
+  return ok();
+}
+
 moe_status moe_selftest_bounded_wait(void* ws, uint32_t limit_ms, cudaStream_t stream) {
   if ((ws == nullptr) || !aligned256(ws))
     return fail(MOE_ERR_INVALID_ARG, "workspace must be non-NULL and 256-byte aligned");

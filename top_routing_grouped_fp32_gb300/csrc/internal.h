@@ -43,6 +43,86 @@ cudaError_t dispatch_noalloc_scratch(void** out);
 cudaError_t launch_gather(const void* x, moe_dtype dt, int64_t H, int k, const uint32_t* perm,
                           const uint32_t* offsets, int E, int64_t N, void* x_disp, cudaStream_t s);
 
+// ---- training losses of the router (balance.cu, distill.cu) -------------------
+struct BalanceArgs {
+  const void* logits;
+  moe_dtype dt;
+  const uint32_t* idx;
+  const uint8_t* mask;          // nullable
+  const uint32_t* seq_offsets;  // nullable
+  int64_t T;
+  int E, k;
+  int64_t num_seqs;
+  bool sigmoid;
+  float* loss;
+  float* z_loss;       // nullable
+  float* mean_scores;  // nullable
+  uint32_t* counts;
+  uint32_t* tokens;
+  float* row_stats;    // [T, 2], 8-byte aligned
+};
+struct BalanceBwdArgs {
+  const void* logits;
+  moe_dtype dt;
+  const float* row_stats;
+  const uint32_t* counts;
+  const uint32_t* tokens;
+  const uint32_t* seq_offsets;
+  int64_t T;
+  int E, k;
+  int64_t num_seqs;
+  bool sigmoid;
+  const float* dloss;
+  const float* dz_loss;  // nullable
+  const void* base;      // nullable
+  void* dlogits;
+};
+// partial sums of the forward (behind the workspace's header)
+size_t balance_workspace_bytes(int64_t T, int E, int64_t num_seqs);
+cudaError_t launch_balance_loss(const BalanceArgs& b, void* ws, uint32_t* status, cudaStream_t s);
+cudaError_t launch_balance_loss_backward(const BalanceBwdArgs& b, cudaStream_t s);
+
+struct DistillArgs {
+  const void* logits;
+  moe_dtype dt;
+  const uint32_t* t_idx;
+  const void* t_logits;
+  moe_dtype t_dt;
+  const float* t_rest;          // nullable
+  const uint8_t* mask;          // nullable
+  const uint32_t* seq_offsets;  // nullable
+  int64_t T;
+  int E, m;
+  int64_t num_seqs;
+  float temperature;
+  float* loss;
+  uint32_t* tokens;
+  float* row_loss;
+  float* row_stats;  // [5, T]
+};
+struct DistillBwdArgs {
+  const void* logits;
+  moe_dtype dt;
+  const uint32_t* t_idx;
+  const void* t_logits;
+  moe_dtype t_dt;
+  const float* row_stats;
+  const uint32_t* tokens;
+  const uint32_t* seq_offsets;
+  int64_t T;
+  int E, m;
+  int64_t num_seqs;
+  float temperature;
+  const float* dloss;
+  const void* base;  // nullable
+  void* dlogits;
+};
+size_t distill_workspace_bytes(int64_t T, int64_t num_seqs);
+cudaError_t launch_distill_loss(const DistillArgs& d, void* ws, uint32_t* status, cudaStream_t s);
+cudaError_t launch_distill_loss_backward(const DistillBwdArgs& d, cudaStream_t s);
+cudaError_t launch_distill_targets(const void* logits, moe_dtype dt, int64_t T, int E, int m, float temperature,
+                                   uint32_t* idx, void* top, float* rest, cudaStream_t s);
+
 // ---- combine (combine.cu) --------------------------------------------------
 cudaError_t launch_invert_perm(const uint32_t* perm, int64_t N, uint32_t* slot_row, cudaStream_t s);
 cudaError_t launch_combine(const void* expert_out, moe_dtype dt, const uint32_t* slot_row,

@@ -1,0 +1,303 @@
+"""Training losses of the router: balance loss with expert counts and z-loss,
+and distillation from a teacher's top logits (moe_balance_loss*,
+moe_distill_* in ``include/moe.h``).
+
+A router's training step, next to the gradient of the routing weights::
+
+    idx, w = moe_route(logits, top_k=6, renormalize=False)
+    bal = moe_balance_loss(logits, idx, z_loss=True)             # bal.loss [S], bal.counts [S,E]
+    tgt = moe_distill_targets(teacher_logits, top_m=8)
+    dis = moe_distill_loss(logits, tgt)                          # dis.loss [S], dis.row_loss [T]
+    ...
+    dl = moe_router_backward(logits, idx, dweights, "softmax", False)
+    moe_balance_loss_backward(logits, bal, 6, dloss, dz_loss=dz, base=dl, dlogits=dl)
+    moe_distill_loss_backward(logits, tgt, dis, ddistill, base=dl, dlogits=dl)
+
+All tensors of a call are contiguous and on one CUDA device, which need not be
+the current one.  A call works on ``stream``, or on the current stream of that
+device; what it allocates belongs to that stream.  ``out`` is a result of an
+earlier call of the same sizes to write into; ``workspace`` a buffer from the
+``*_workspace`` function to work in (calls that may overlap need one each).
+"""
+from __future__ import annotations
+
+import contextlib
+from dataclasses import dataclass
+
+import torch
+
+from . import _lib
+from ._lib import MoeError
+
+_CODES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+_SCORING = {"softmax": 0, "sigmoid": 1}
+_F32, _I32 = (torch.float32,), (torch.int32,)
+_MASK = (torch.bool, torch.uint8)
+_NOTHING = contextlib.nullcontext()
+
+
+def _code(t: torch.Tensor, what: str) -> int:
+    code = _CODES.get(t.dtype)
+    if code is None:
+        raise MoeError(3, f"{what} dtype {t.dtype} is not F32/F16/BF16")
+    return code
+
+
+def _scoring(name: str) -> int:
+    code = _SCORING.get(name)
+    if code is None:
+        raise MoeError(1, f"scoring must be 'softmax' or 'sigmoid' (got {name!r})")
+    return code
+
+
+def _rows_of(logits: torch.Tensor, what: str):
+    if logits.dim() != 2:
+        raise MoeError(2, f"{what} must have rank two (got {logits.dim()})")
+    if not logits.is_cuda:
+        raise ValueError(f"{what}: expected a CUDA tensor")
+    return logits.shape
+
+
+def _p(t, what: str, dtypes, shape, device):
+    """Data pointer of a checked tensor (None passes)."""
+    if t is None:
+        return None
+    if dtypes is not None and t.dtype not in dtypes:
+        raise MoeError(3, f"{what} dtype {t.dtype} is not one of {', '.join(str(d) for d in dtypes)}")
+    if t.shape != shape:
+        raise MoeError(2, f"{what} must have shape {tuple(shape)} (got {tuple(t.shape)})")
+    if t.device != device:
+        raise ValueError(f"{what} is on {t.device}, the logits are on {device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{what}: expected a contiguous tensor")
+    return t.data_ptr()
+
+
+def _ws(t, device):
+    if t.device != device or not t.is_contiguous():
+        raise ValueError(f"workspace: expected a contiguous tensor on {device}")
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
+def _num_seqs(seq_offsets) -> int:
+    if seq_offsets is None:
+        return 1
+    if seq_offsets.dim() != 1 or seq_offsets.shape[0] < 2:
+        raise MoeError(2, "seq_offsets must be [num_seqs + 1] with num_seqs >= 1")
+    return seq_offsets.shape[0] - 1
+
+
+def _on(device: torch.device, stream):
+    """Context in which `device` and `stream` are current."""
+    if stream is not None:
+        if stream.device != device:
+            raise ValueError(f"stream is on {stream.device}, the logits are on {device}")
+        return torch.cuda.stream(stream)
+    if torch.cuda.current_device() != device.index:
+        return torch.cuda.device(device)
+    return _NOTHING
+
+
+def _raw_stream(device, stream) -> int:
+    return (stream if stream is not None else torch.cuda.current_stream(device)).cuda_stream
+
+
+def _buffer(nbytes: int, device) -> torch.Tensor:
+    # torch allocations are 512-byte aligned, above the ABI's 256-byte rule
+    return torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device)
+
+
+@dataclass
+class BalanceLoss:
+    """What moe_balance_loss gives and moe_balance_loss_backward takes (it reads
+    counts, tokens and row_stats)."""
+    loss: torch.Tensor                # float32 [S]
+    z_loss: torch.Tensor | None       # float32 [S]
+    mean_scores: torch.Tensor | None  # float32 [S,E]
+    counts: torch.Tensor              # int32 [S,E]
+    tokens: torch.Tensor              # int32 [S]
+    row_stats: torch.Tensor           # float32 [T,2]
+    workspace: torch.Tensor | None = None  # holds the device status word
+
+    @classmethod
+    def empty(cls, T: int, E: int, num_seqs: int, device, z_loss: bool = False) -> "BalanceLoss":
+        def f32(*shape):
+            return torch.empty(shape, dtype=torch.float32, device=device)
+
+        def i32(*shape):
+            return torch.empty(shape, dtype=torch.int32, device=device)
+        S = num_seqs
+        return cls(f32(S), f32(S) if z_loss else None, f32(S, E), i32(S, E), i32(S), f32(T, 2))
+
+
+def moe_balance_loss_workspace(T: int, E: int, num_seqs: int = 1, device="cuda") -> torch.Tensor:
+    return _buffer(_lib.load().moe_balance_loss_workspace_size(T, E, num_seqs), device)
+
+
+def moe_balance_loss(logits: torch.Tensor, idx: torch.Tensor, scoring: str = "softmax",
+                     token_mask: torch.Tensor | None = None, seq_offsets: torch.Tensor | None = None,
+                     z_loss: bool = False, out: BalanceLoss | None = None,
+                     workspace: torch.Tensor | None = None, stream=None) -> BalanceLoss:
+    """Balance loss, per-expert counts, mean scores and (``z_loss``) the z-loss
+    of router logits [T,E] and their routed experts idx [T,k] (int32)."""
+    lib = _lib.load()
+    T, E = _rows_of(logits, "logits")
+    code, sc = _code(logits, "logits"), _scoring(scoring)
+    if idx.dim() != 2:
+        raise MoeError(2, "idx must be [T, top_k]")
+    k, S, dev = idx.shape[1], _num_seqs(seq_offsets), logits.device
+    args = (_p(logits, "logits", None, (T, E), dev), code, _p(idx, "idx", _I32, (T, k), dev),
+            _p(token_mask, "token_mask", _MASK, (T,), dev), _p(seq_offsets, "seq_offsets", _I32, (S + 1,), dev),
+            T, E, k, S, sc)
+    with _on(dev, stream):
+        if out is None:
+            out = BalanceLoss.empty(T, E, S, dev, z_loss)
+        elif (out.z_loss is not None) != z_loss:
+            raise MoeError(1, "out was made with another z_loss")
+        if workspace is None:
+            workspace = moe_balance_loss_workspace(T, E, S, dev)
+        out.workspace = workspace
+        ws, nbytes = _ws(workspace, dev)
+        _lib.check(lib.moe_balance_loss(
+            *args, _p(out.loss, "loss", _F32, (S,), dev), _p(out.z_loss, "z_loss", _F32, (S,), dev),
+            _p(out.mean_scores, "mean_scores", _F32, (S, E), dev), _p(out.counts, "counts", _I32, (S, E), dev),
+            _p(out.tokens, "tokens", _I32, (S,), dev), _p(out.row_stats, "row_stats", _F32, (T, 2), dev),
+            ws, nbytes, _raw_stream(dev, stream)))
+    return out
+
+
+def moe_balance_loss_backward(logits: torch.Tensor, forward: BalanceLoss, top_k: int, dloss: torch.Tensor,
+                              scoring: str = "softmax", seq_offsets: torch.Tensor | None = None,
+                              dz_loss: torch.Tensor | None = None, base: torch.Tensor | None = None,
+                              dlogits: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """dlogits [T,E] = base + gradient of sum(dloss * loss) (+ sum(dz_loss *
+    z_loss)), dloss and dz_loss float32 [S].  ``dlogits`` is written if given
+    (it may be ``base``)."""
+    lib = _lib.load()
+    T, E = _rows_of(logits, "logits")
+    code, sc = _code(logits, "logits"), _scoring(scoring)
+    S, dev, dt = _num_seqs(seq_offsets), logits.device, (logits.dtype,)
+    args = (_p(logits, "logits", None, (T, E), dev), code, _p(forward.row_stats, "row_stats", _F32, (T, 2), dev),
+            _p(forward.counts, "counts", _I32, (S, E), dev), _p(forward.tokens, "tokens", _I32, (S,), dev),
+            _p(seq_offsets, "seq_offsets", _I32, (S + 1,), dev), T, E, top_k, S, sc,
+            _p(dloss, "dloss", _F32, (S,), dev), _p(dz_loss, "dz_loss", _F32, (S,), dev),
+            _p(base, "base", dt, (T, E), dev))
+    with _on(dev, stream):
+        if dlogits is None:
+            dlogits = torch.empty((T, E), dtype=logits.dtype, device=dev)
+        _lib.check(lib.moe_balance_loss_backward(*args, _p(dlogits, "dlogits", dt, (T, E), dev),
+                                                 _raw_stream(dev, stream)))
+    return dlogits
+
+
+@dataclass
+class DistillTargets:
+    """A teacher's top logits: what moe_distill_targets gives and the
+    distillation loss takes.  ``rest`` may be None: no mass outside the list."""
+    idx: torch.Tensor           # int32 [T,m]
+    logits: torch.Tensor        # [T,m] in the teacher's dtype
+    rest: torch.Tensor | None   # float32 [T]
+
+    @classmethod
+    def empty(cls, T: int, top_m: int, dtype, device) -> "DistillTargets":
+        return cls(torch.empty((T, top_m), dtype=torch.int32, device=device),
+                   torch.empty((T, top_m), dtype=dtype, device=device),
+                   torch.empty((T,), dtype=torch.float32, device=device))
+
+
+def moe_distill_targets(teacher_logits: torch.Tensor, top_m: int, temperature: float = 1.0,
+                        out: DistillTargets | None = None, stream=None) -> DistillTargets:
+    """The top_m largest of each row of a teacher's logits [T,E] and the logit of
+    all its other experts together at ``temperature``."""
+    lib = _lib.load()
+    T, E = _rows_of(teacher_logits, "teacher_logits")
+    code, dev, dt = _code(teacher_logits, "teacher_logits"), teacher_logits.device, teacher_logits.dtype
+    if out is None and not 1 <= top_m <= E:
+        raise MoeError(1, f"top_m must satisfy 1 <= top_m <= E (top_m={top_m}, E={E})")
+    with _on(dev, stream):
+        if out is None:
+            out = DistillTargets.empty(T, top_m, dt, dev)
+        if out.rest is None:
+            raise MoeError(1, "out has no rest")
+        _lib.check(lib.moe_distill_targets(
+            _p(teacher_logits, "teacher_logits", None, (T, E), dev), code, T, E, top_m, temperature,
+            _p(out.idx, "idx", _I32, (T, top_m), dev), _p(out.logits, "logits", (dt,), (T, top_m), dev),
+            _p(out.rest, "rest", _F32, (T,), dev), _raw_stream(dev, stream)))
+    return out
+
+
+@dataclass
+class DistillLoss:
+    """What moe_distill_loss gives and moe_distill_loss_backward takes (it reads
+    tokens and row_stats)."""
+    loss: torch.Tensor       # float32 [S]
+    tokens: torch.Tensor     # int32 [S]
+    row_loss: torch.Tensor   # float32 [T]
+    row_stats: torch.Tensor  # float32 [5,T]
+    workspace: torch.Tensor | None = None  # holds the device status word
+
+    @classmethod
+    def empty(cls, T: int, num_seqs: int, device) -> "DistillLoss":
+        def f32(*shape):
+            return torch.empty(shape, dtype=torch.float32, device=device)
+        return cls(f32(num_seqs), torch.empty((num_seqs,), dtype=torch.int32, device=device), f32(T), f32(5, T))
+
+
+def _list_args(targets: DistillTargets, T: int, dev):
+    if targets.idx.dim() != 2:
+        raise MoeError(2, "targets.idx must be [T, top_m]")
+    m = targets.idx.shape[1]
+    return m, (_p(targets.idx, "targets.idx", _I32, (T, m), dev),
+               _p(targets.logits, "targets.logits", None, (T, m), dev), _code(targets.logits, "targets.logits"))
+
+
+def moe_distill_loss_workspace(T: int, num_seqs: int = 1, device="cuda") -> torch.Tensor:
+    return _buffer(_lib.load().moe_distill_loss_workspace_size(T, num_seqs), device)
+
+
+def moe_distill_loss(logits: torch.Tensor, targets: DistillTargets, temperature: float = 1.0,
+                     token_mask: torch.Tensor | None = None, seq_offsets: torch.Tensor | None = None,
+                     out: DistillLoss | None = None, workspace: torch.Tensor | None = None,
+                     stream=None) -> DistillLoss:
+    """Mean KL divergence of student logits [T,E] from a teacher's lists."""
+    lib = _lib.load()
+    T, E = _rows_of(logits, "logits")
+    code, S, dev = _code(logits, "logits"), _num_seqs(seq_offsets), logits.device
+    m, lists = _list_args(targets, T, dev)
+    args = (_p(logits, "logits", None, (T, E), dev), code, *lists,
+            _p(targets.rest, "targets.rest", _F32, (T,), dev), _p(token_mask, "token_mask", _MASK, (T,), dev),
+            _p(seq_offsets, "seq_offsets", _I32, (S + 1,), dev), T, E, m, S, temperature)
+    with _on(dev, stream):
+        if out is None:
+            out = DistillLoss.empty(T, S, dev)
+        if workspace is None:
+            workspace = moe_distill_loss_workspace(T, S, dev)
+        out.workspace = workspace
+        ws, nbytes = _ws(workspace, dev)
+        _lib.check(lib.moe_distill_loss(
+            *args, _p(out.loss, "loss", _F32, (S,), dev), _p(out.tokens, "tokens", _I32, (S,), dev),
+            _p(out.row_loss, "row_loss", _F32, (T,), dev), _p(out.row_stats, "row_stats", _F32, (5, T), dev),
+            ws, nbytes, _raw_stream(dev, stream)))
+    return out
+
+
+def moe_distill_loss_backward(logits: torch.Tensor, targets: DistillTargets, forward: DistillLoss,
+                              dloss: torch.Tensor, temperature: float = 1.0,
+                              seq_offsets: torch.Tensor | None = None, base: torch.Tensor | None = None,
+                              dlogits: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """dlogits [T,E] = base + gradient of sum(dloss * loss), dloss float32 [S].
+    ``dlogits`` is written if given (it may be ``base``)."""
+    lib = _lib.load()
+    T, E = _rows_of(logits, "logits")
+    code, S, dev, dt = _code(logits, "logits"), _num_seqs(seq_offsets), logits.device, (logits.dtype,)
+    m, lists = _list_args(targets, T, dev)
+    args = (_p(logits, "logits", None, (T, E), dev), code, *lists,
+            _p(forward.row_stats, "row_stats", _F32, (5, T), dev), _p(forward.tokens, "tokens", _I32, (S,), dev),
+            _p(seq_offsets, "seq_offsets", _I32, (S + 1,), dev), T, E, m, S, temperature,
+            _p(dloss, "dloss", _F32, (S,), dev), _p(base, "base", dt, (T, E), dev))
+    with _on(dev, stream):
+        if dlogits is None:
+            dlogits = torch.empty((T, E), dtype=logits.dtype, device=dev)
+        _lib.check(lib.moe_distill_loss_backward(*args, _p(dlogits, "dlogits", dt, (T, E), dev),
+                                                 _raw_stream(dev, stream)))
+    return dlogits
