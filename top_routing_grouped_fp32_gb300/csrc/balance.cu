@@ -17,15 +17,19 @@
 // at slot block + sequence (unique, since rows and sequences both ascend).  A
 // second kernel adds each sequence's slots in a fixed order.  The counts are
 // integers, so shared-memory atomics leave them reproducible.
+#include <cooperative_groups.h>
+
 #include "internal.h"
 #include "rows.cuh"
 
 namespace moe {
 namespace {
 
+namespace cg = cooperative_groups;
+
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kMaxChunks = 608;    // partials a sequence may have: four blocks per SM
+constexpr int kMaxChunks = 304;    // partials a sequence may have: two blocks per SM
 constexpr int kHistWords = 2048;   // copies of the block's histogram share this many words
 
 struct Partials {
@@ -49,59 +53,41 @@ struct FwdArgs {
   uint32_t k_magic;  // floor(2^32 / k) + 1 (k > 1): i / k = umulhi(i, magic) while i * k < 2^32
 };
 
-// Shift and sum of a row, and its normalised scores: softmax about the row's
-// maximum; sigmoid about 0, or about the maximum where all scores are so small
-// that their FP32 sum would lose them (sigmoid(l) = exp(l) there).
+// Sigmoid scores are normalised about 0, or about the row's maximum where all of
+// them are so small that their FP32 sum would lose them (sigmoid(l) = exp(l) there).
 constexpr float kFarBelow = -60.f;
 
-template <typename T, int VEC, int NV, bool FULL, bool SIG>
-__device__ __forceinline__ void row_scores(const RowRegs<T, VEC, NV>& r, const Lanes<FULL>& L, int E, bool ok,
-                                           float& shift, float& s, float (&p)[VEC * NV]) {
-  constexpr int N = VEC * NV;
-  float m = -INFINITY;
-#pragma unroll
-  for (int n = 0; n < N; ++n) m = fmaxf(m, r[n]);
-  m = L.max(m);
-  if (!ok) m = 0.f;
-  s = 0.f;
+// Scores of a row about `shift`, not normalised, and their sum over this lane.
+template <typename Row, bool SIG>
+__device__ __forceinline__ float lane_scores(const Row& r, int lpr, int E, float m, float& shift,
+                                             float (&p)[Row::N]) {
+  float s = 0.f;
   if (SIG && m >= kFarBelow) {
     shift = 0.f;
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      if (!RowRegs<T, VEC, NV>::used(v, L.lpr, E)) {
-        p[v] = 0.f;
-        continue;
-      }
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) {
-        const int n = v * VEC + i;
-        p[n] = rcp_fast(1.f + exp2_fast(-r[n] * kLog2e));
-        s += p[n];
-      }
+    for (int n = 0; n < Row::N; ++n) {
+      p[n] = rcp_fast(1.f + exp2_fast(r[n] * -kLog2e));
+      s += p[n];
     }
-  } else {
-    shift = m;
-#pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      if (!RowRegs<T, VEC, NV>::used(v, L.lpr, E)) {
-        p[v] = 0.f;
-        continue;
-      }
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) {
-        const int n = v * VEC + i;
-        p[n] = exp2_fast((r[n] - m) * kLog2e);
-        s += p[n];
-      }
-    }
+    return s;
   }
-  s = L.sum(s);
+  shift = m;
+  const RowExp ex(m, kLog2e);
+  if (ex.wide) {
+#pragma unroll
+    for (int n = 0; n < Row::N; ++n) s += p[n] = ex.far(r[n]);
+  } else {
+#pragma unroll
+    for (int n = 0; n < Row::N; ++n) s += p[n] = ex(r[n]);
+  }
+  return s;
 }
 
 template <typename T, int VEC, int NV, bool FULL, bool SIG>
-__global__ void __launch_bounds__(kThreads) balance_fwd_kernel(FwdArgs a) {
+__global__ void __launch_bounds__(kThreads, VEC * NV <= 16 ? 2 : 1) balance_fwd_kernel(FwdArgs a) {
   extern __shared__ float smem[];
-  constexpr int N = VEC * NV;
+  constexpr int N = VEC * NV, R = rows_at_once<VEC, NV>();
+  constexpr int NI = 4;  // indices of a batch that a lane holds ahead of their use
   using Row = RowRegs<T, VEC, NV>;
   float* red = smem;                                             // [kWarps][E]
   uint32_t* hist = reinterpret_cast<uint32_t*>(smem + kWarps * a.E);  // [E][copies]
@@ -116,6 +102,8 @@ __global__ void __launch_bounds__(kThreads) balance_fwd_kernel(FwdArgs a) {
   const T* logits = static_cast<const T*>(a.logits);
   const int64_t c0 = (int64_t)blockIdx.x * a.chunk_rows;
   const int64_t c1 = min(c0 + a.chunk_rows, a.T);
+  const int batch = R * L.rows;            // rows a warp takes at once, at most 128
+  const int copy = lane & (a.copies - 1);  // its copy of the histogram
 
   auto gap = [&](int64_t lo, int64_t hi) {
     for (int64_t t = lo + threadIdx.x; t < hi; t += kThreads) a.row_stats[t] = make_float2(0.f, 0.f);
@@ -123,44 +111,88 @@ __global__ void __launch_bounds__(kThreads) balance_fwd_kernel(FwdArgs a) {
   auto piece = [&](int seq, int64_t lo, int64_t hi) {
     for (int i = threadIdx.x; i < a.E * a.copies; i += kThreads) hist[i] = 0u;
     __syncthreads();
-    // counts of the piece's slots; each thread adds to one of the copies
     uint32_t bad = 0, valid = 0;
-    {
-      const uint32_t* ip = a.idx + lo * a.k;
-      const uint32_t n = (uint32_t)(hi - lo) * (uint32_t)a.k;
-      const int copy = lane & (a.copies - 1);
-      for (uint32_t i = threadIdx.x; i < n; i += kThreads) {
-        if (a.mask && !__ldg(a.mask + lo + (a.k == 1 ? i : __umulhi(i, a.k_magic)))) continue;
-        const uint32_t e = __ldg(ip + i);
-        if (e < (uint32_t)a.E) atomicAdd(hist + e * a.copies + copy, 1u);
-        else ++bad;
-      }
-    }
-    float acc[N];
+    float acc[N], zacc = 0.f;
 #pragma unroll
     for (int n = 0; n < N; ++n) acc[n] = 0.f;
-    float zacc = 0.f;
-    for (int64_t t0 = lo + warp * L.rows; t0 < hi; t0 += kWarps * L.rows) {
-      const int64_t t = t0 + L.grp;
-      const bool in = t < hi;
-      const bool ok = in && (!a.mask || __ldg(a.mask + t));
-      Row r;
-      r.load(logits + t * a.E, a.E, L.lpr, L.sub, ok, from_f32<T>(-INFINITY));
-      float p[N], m, s;
-      row_scores<T, VEC, NV, FULL, SIG>(r, L, a.E, ok, m, s, p);
-      const float inv = ok ? 1.f / s : 0.f;
+
+    // which rows count, as a bit per row of a batch: loaded a batch before the rows
+    auto live = [&](int64_t t) {
+      uint32_t bits = 0;
 #pragma unroll
-      for (int n = 0; n < N; ++n) acc[n] = fmaf(p[n], inv, acc[n]);
-      if (L.sub == 0 && in) {
-        a.row_stats[t] = ok ? make_float2(m, s) : make_float2(0.f, 0.f);
-        if (ok) {
-          ++valid;
-          if (!SIG) {
-            const float lse = m + logf(s);
-            zacc = fmaf(lse, lse, zacc);
+      for (int r = 0; r < R; ++r) {
+        const int64_t tr = t + r * L.rows + L.grp;
+        bits |= (uint32_t)(tr < hi && (!a.mask || __ldg(a.mask + tr))) << r;
+      }
+      return bits;
+    };
+    auto load = [&](Row& r, int64_t t, bool ok) {
+      r.load(logits + t * a.E, a.E, L.lpr, L.sub, ok, from_f32<T>(-INFINITY));
+    };
+    int64_t t0 = lo + (int64_t)warp * batch;
+    Row cur[R], nxt[R];
+    uint32_t ok = live(t0), ok1 = live(t0 + (int64_t)kWarps * batch);
+#pragma unroll
+    for (int r = 0; r < R; ++r) load(cur[r], t0 + r * L.rows + L.grp, ok >> r & 1u);
+    for (; t0 < hi; t0 += (int64_t)kWarps * batch) {
+      // the next batch's rows and this batch's indices are on their way during the arithmetic
+      const int64_t t1 = t0 + (int64_t)kWarps * batch;
+      const int slots = (int)(min((int64_t)batch, hi - t0)) * a.k;
+      const uint32_t* ip = a.idx + t0 * a.k;
+      uint32_t id[NI];
+#pragma unroll
+      for (int i = 0; i < NI; ++i) id[i] = lane + 32 * i < slots ? __ldg(ip + lane + 32 * i) : 0u;
+#pragma unroll
+      for (int r = 0; r < R; ++r) load(nxt[r], t1 + r * L.rows + L.grp, ok1 >> r & 1u);
+      const uint32_t ok2 = live(t1 + (int64_t)kWarps * batch);
+
+      float p[R][N], s[R], m[R];
+#pragma unroll
+      for (int r = 0; r < R; ++r) m[r] = L.max(cur[r].lane_max());
+#pragma unroll
+      for (int r = 0; r < R; ++r) s[r] = lane_scores<Row, SIG>(cur[r], L.lpr, a.E, m[r], m[r], p[r]);
+      L.sums(s);
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const float inv = rcp_fast(s[r]);  // p carries the factor that fix takes out, too
+        if (!SIG || m[r] != 0.f) s[r] *= RowExp(m[r], kLog2e).fix;
+        if (ok >> r & 1u) {
+#pragma unroll
+          for (int n = 0; n < N; ++n) acc[n] = fmaf(p[r][n], inv, acc[n]);
+        }
+      }
+      // a row's statistics leave from its lane r (of few lanes: r, r + lpr, ..)
+      for (int q = 0; q < R; q += L.lpr) {
+        float mr = 0.f, sr = 0.f;
+        bool o = false;
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+          if (r == q + L.sub) mr = m[r], sr = s[r], o = ok >> r & 1u;
+        const int64_t t = t0 + (q + L.sub) * L.rows + L.grp;
+        if (q + L.sub < R && t < hi) {
+          a.row_stats[t] = o ? make_float2(mr, sr) : make_float2(0.f, 0.f);
+          if (o) {
+            ++valid;
+            if (!SIG) {
+              const float lse = mr + logf(sr);
+              zacc = fmaf(lse, lse, zacc);
+            }
           }
         }
       }
+      // counts of the batch's slots; a lane adds to its copy
+      auto count = [&](int i, uint32_t e) {
+        if (a.mask && !__ldg(a.mask + t0 + (a.k == 1 ? i : (int)__umulhi(i, a.k_magic)))) return;
+        if (e < (uint32_t)a.E) atomicAdd(hist + e * a.copies + copy, 1u);
+        else ++bad;
+      };
+#pragma unroll
+      for (int i = 0; i < NI; ++i)
+        if (lane + 32 * i < slots) count(lane + 32 * i, id[i]);
+      for (int i = lane + 32 * NI; i < slots; i += 32) count(i, __ldg(ip + i));
+#pragma unroll
+      for (int r = 0; r < R; ++r) cur[r] = nxt[r];
+      ok = ok1, ok1 = ok2;
     }
     // the rows of a warp, then the warps, in a fixed order
 #pragma unroll
@@ -218,19 +250,26 @@ struct FinishArgs {
   uint32_t* status;
 };
 
-// One block per sequence: 32 experts x 8 slot lanes at a time.
-__global__ void __launch_bounds__(kThreads) balance_finish_kernel(FinishArgs a) {
-  __shared__ float sp[kWarps][33];
-  __shared__ uint32_t sn[kWarps][33];
-  __shared__ double sl[32];
-  __shared__ float sz[kThreads];
-  __shared__ uint32_t sv[kThreads], sb[kThreads];
+// A cluster of blocks per sequence, each for every CL-th group of 32 experts:
+// 32 experts x 32 slot lanes at a time.  Block 0 adds the blocks' shares of the
+// loss in order.
+constexpr int kFinishThreads = 1024;
+constexpr int kFinishWarps = kFinishThreads / 32;
+
+__global__ void __launch_bounds__(kFinishThreads) balance_finish_kernel(FinishArgs a) {
+  __shared__ float sp[kFinishWarps][33];
+  __shared__ uint32_t sn[kFinishWarps][33];
+  __shared__ float sz[kFinishWarps];
+  __shared__ uint32_t sv[kFinishWarps], sb[kFinishWarps];
+  __shared__ double share;
+  cg::cluster_group cl = cg::this_cluster();
+  const int rank = (int)cl.block_rank(), blocks = (int)cl.num_blocks();
+  const int s = blockIdx.x / blocks;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_wait();
   pdl_trigger();
-  const int s = blockIdx.x;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t lo = a.seqs.at(s), hi = a.seqs.at(s + 1);
-  if (threadIdx.x == 0 && a.seqs.off &&
+  if (rank == 0 && threadIdx.x == 0 && a.seqs.off &&
       (hi < lo || (int64_t)__ldg(a.seqs.off + s) > a.seqs.T || (int64_t)__ldg(a.seqs.off + s + 1) > a.seqs.T))
     set_status(a.status, MOE_ERR_INVALID_INDEX);
   // slots first..last hold the sequence
@@ -241,57 +280,76 @@ __global__ void __launch_bounds__(kThreads) balance_finish_kernel(FinishArgs a) 
   }
   float z = 0.f;
   uint32_t valid = 0, bad = 0;
-  for (int64_t i = first + threadIdx.x; i <= last; i += kThreads) {
+  for (int64_t i = first + threadIdx.x; i <= last; i += kFinishThreads) {
     z += a.part.z[i];
     valid += a.part.rows[i];
     bad += a.part.bad[i];
   }
-  sz[threadIdx.x] = z, sv[threadIdx.x] = valid, sb[threadIdx.x] = bad;
-  __syncthreads();
-  for (int d = kThreads / 2; d > 0; d >>= 1) {
-    if (threadIdx.x < d) {
-      sz[threadIdx.x] += sz[threadIdx.x + d];
-      sv[threadIdx.x] += sv[threadIdx.x + d];
-      sb[threadIdx.x] += sb[threadIdx.x + d];
-    }
-    __syncthreads();
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) {
+    z += __shfl_xor_sync(0xffffffffu, z, d);
+    valid += __shfl_xor_sync(0xffffffffu, valid, d);
+    bad += __shfl_xor_sync(0xffffffffu, bad, d);
   }
-  const uint32_t rows = sv[0];
-  if (threadIdx.x == 0 && sb[0]) set_status(a.status, MOE_ERR_INVALID_INDEX);
-  const float inv = rows ? 1.f / (float)rows : 0.f;
+  if (lane == 0) sz[warp] = z, sv[warp] = valid, sb[warp] = bad;
   double dot = 0.0;
-  for (int e0 = 0; e0 < a.E; e0 += 32) {
+  uint32_t rows = 0;
+  for (int e0 = rank * 32; e0 < a.E; e0 += blocks * 32) {
     const int e = e0 + lane;
     float p = 0.f;
     uint32_t n = 0;
-    if (e < a.E)
-      for (int64_t i = first + warp; i <= last; i += kWarps) {
+    if (e < a.E) {
+#pragma unroll 4
+      for (int64_t i = first + warp; i <= last; i += kFinishWarps) {
         p += a.part.p[i * a.E + e];
         n += a.part.n[i * a.E + e];
       }
+    }
     sp[warp][lane] = p;
     sn[warp][lane] = n;
     __syncthreads();
-    if (warp == 0 && e < a.E) {
-      p = 0.f, n = 0;
+    // warp w now adds the slot lanes of expert w
+    p = sp[lane][warp], n = sn[lane][warp];
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) p += sp[w][lane], n += sn[w][lane];
-      a.counts[(int64_t)s * a.E + e] = n;
-      if (a.mean_scores) a.mean_scores[(int64_t)s * a.E + e] = p * inv;
-      dot += (double)n * (double)p;
+    for (int d = 16; d > 0; d >>= 1) {
+      p += __shfl_xor_sync(0xffffffffu, p, d);
+      n += __shfl_xor_sync(0xffffffffu, n, d);
+    }
+    __syncthreads();
+    if (lane == 0) sp[0][warp] = p, sn[0][warp] = n;
+    __syncthreads();
+    if (warp == 0) {
+      rows = 0;
+      for (int w = 0; w < kFinishWarps; ++w) rows += sv[w];
+      p = sp[0][lane], n = sn[0][lane];
+      if (e < a.E) {
+        a.counts[(int64_t)s * a.E + e] = n;
+        if (a.mean_scores) a.mean_scores[(int64_t)s * a.E + e] = rows ? p / (float)rows : 0.f;
+        dot += (double)n * (double)p;
+      }
     }
     __syncthreads();
   }
-  if (warp == 0) sl[lane] = dot;
-  __syncwarp();
-  if (threadIdx.x == 0) {
-    dot = 0.0;
-    for (int i = 0; i < 32; ++i) dot += sl[i];
-    const double L = (double)rows;
-    a.loss[s] = rows ? (float)((double)a.E * dot / ((double)a.k * L * L)) : 0.f;
-    if (a.z_loss) a.z_loss[s] = rows ? sz[0] / (float)rows : 0.f;
-    a.tokens[s] = rows;
+  if (warp == 0) {
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, d);
+    if (lane == 0) share = dot;
   }
+  cl.sync();
+  if (rank == 0 && threadIdx.x == 0) {
+    dot = 0.0;
+    for (int b = 0; b < blocks; ++b) dot += *cl.map_shared_rank(&share, b);
+    float zz = 0.f;
+    uint32_t b = 0;
+    rows = 0;
+    for (int w = 0; w < kFinishWarps; ++w) zz += sz[w], rows += sv[w], b += sb[w];
+    const double len = (double)rows;
+    a.loss[s] = rows ? (float)((double)a.E * dot / ((double)a.k * len * len)) : 0.f;
+    if (a.z_loss) a.z_loss[s] = rows ? zz / (float)rows : 0.f;
+    a.tokens[s] = rows;
+    if (b) set_status(a.status, MOE_ERR_INVALID_INDEX);
+  }
+  cl.sync();  // the shares are read
 }
 
 struct BwdArgs {
@@ -309,8 +367,8 @@ struct BwdArgs {
 };
 
 template <typename T, int VEC, int NV, bool FULL, bool SIG>
-__global__ void __launch_bounds__(kThreads) balance_bwd_kernel(BwdArgs a) {
-  constexpr int N = VEC * NV;
+__global__ void __launch_bounds__(kThreads, VEC * NV <= 16 ? 2 : 1) balance_bwd_kernel(BwdArgs a) {
+  constexpr int N = VEC * NV, R = rows_at_once<VEC, NV>();
   using Row = RowRegs<T, VEC, NV>;
   pdl_wait();
   pdl_trigger();
@@ -321,6 +379,7 @@ __global__ void __launch_bounds__(kThreads) balance_bwd_kernel(BwdArgs a) {
   T* out = static_cast<T*>(a.out);
   const int64_t c0 = (int64_t)blockIdx.x * a.chunk_rows;
   const int64_t c1 = min(c0 + a.chunk_rows, a.T);
+  const int batch = R * L.rows;
 
   auto finish = [&](int64_t t, bool in, float (&d)[N]) {
     if (!in) return;
@@ -354,36 +413,71 @@ __global__ void __launch_bounds__(kThreads) balance_bwd_kernel(BwdArgs a) {
       const int64_t c = e < a.E ? (int64_t)__ldg(a.counts + (int64_t)seq * a.E + e) : 0;
       g[n] = up * (float)(c * a.E - rows * a.k);
     }
-    for (int64_t t0 = lo + warp * L.rows; t0 < hi; t0 += kWarps * L.rows) {
-      const int64_t t = t0 + L.grp;
-      const bool in = t < hi;
-      const float2 st = in ? __ldg(a.row_stats + t) : make_float2(0.f, 0.f);
-      const bool ok = st.y != 0.f;  // NaN sums count: their rows get NaN
-      Row r;
-      r.load(logits + t * a.E, a.E, L.lpr, L.sub, in && ok, from_f32<T>(-INFINITY));
-      const float inv = ok ? 1.f / st.y : 0.f;
-      float d[N], dot = 0.f;
+    auto stats = [&](int64_t t) { return t < hi ? __ldg(a.row_stats + t) : make_float2(0.f, 0.f); };
+    // rows that do not count (a sum of 0) are not read
+    auto load = [&](Row& r, int64_t t, float2 st) {
+      r.load(logits + t * a.E, a.E, L.lpr, L.sub, st.y != 0.f, from_f32<T>(-INFINITY));
+    };
+    int64_t t0 = lo + (int64_t)warp * batch;
+    Row cur[R], nxt[R];
+    float2 st[R], st1[R];  // a batch ahead of the rows
 #pragma unroll
-      for (int n = 0; n < N; ++n) {
-        float p, up1 = 1.f;
-        if (SIG && st.x == 0.f) {
-          const float ex = exp2_fast(-fabsf(r[n]) * kLog2e);  // sigmoid(|l|) = 1 / (1 + ex)
-          const float hi1 = rcp_fast(1.f + ex);
-          const float lo1 = ex * hi1;
-          p = (r[n] > 0.f ? hi1 : lo1) * inv;
-          up1 = r[n] > 0.f ? lo1 : hi1;
-          if (r[n] != r[n]) p = r[n];
-        } else {
-          p = exp2_fast((r[n] - st.x) * kLog2e) * inv;
-        }
-        dot = fmaf(p, g[n], dot);
-        d[n] = p * up1;
+    for (int r = 0; r < R; ++r) {
+      st[r] = stats(t0 + r * L.rows + L.grp);
+      st1[r] = stats(t0 + (int64_t)kWarps * batch + r * L.rows + L.grp);
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) load(cur[r], t0 + r * L.rows + L.grp, st[r]);
+    for (; t0 < hi; t0 += (int64_t)kWarps * batch) {
+      const int64_t t1 = t0 + (int64_t)kWarps * batch;
+      float2 st2[R];
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        load(nxt[r], t1 + r * L.rows + L.grp, st1[r]);
+        st2[r] = stats(t1 + (int64_t)kWarps * batch + r * L.rows + L.grp);
       }
-      dot = L.sum(dot);
-      if (!SIG) dot -= zc * (st.x + logf(st.y));
+      float d[R][N], dot[R];
 #pragma unroll
-      for (int n = 0; n < N; ++n) d[n] = ok ? d[n] * (g[n] - dot) : 0.f;
-      finish(t, in, d);
+      for (int r = 0; r < R; ++r) {
+        dot[r] = 0.f;
+        if (SIG && st[r].x == 0.f) {
+          const float inv = rcp_fast(st[r].y);
+#pragma unroll
+          for (int n = 0; n < N; ++n) {
+            const float x = cur[r][n];
+            const float ex = exp2_fast(fabsf(x) * -kLog2e);  // sigmoid(|l|) = 1 / (1 + ex)
+            const float up1 = rcp_fast(1.f + ex), lo1 = ex * up1;
+            const float p = (x < 0.f ? lo1 : up1) * inv;
+            dot[r] = fmaf(p, g[n], dot[r]);
+            d[r][n] = p * (x < 0.f ? up1 : lo1);
+          }
+        } else {
+          const RowExp ex(st[r].x, kLog2e);
+          const float inv = rcp_fast(st[r].y) * ex.fix;
+          if (ex.wide) {
+#pragma unroll
+            for (int n = 0; n < N; ++n) d[r][n] = ex.far(cur[r][n]) * inv;
+          } else {
+#pragma unroll
+            for (int n = 0; n < N; ++n) d[r][n] = ex(cur[r][n]) * inv;
+          }
+#pragma unroll
+          for (int n = 0; n < N; ++n) dot[r] = fmaf(d[r][n], g[n], dot[r]);
+        }
+      }
+      L.sums(dot);
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        // rows that do not count have a sum of 0; NaN sums leave NaN
+        const bool ok = st[r].y != 0.f;
+        if (!SIG && a.dz) dot[r] -= zc * (st[r].x + logf(st[r].y));
+#pragma unroll
+        for (int n = 0; n < N; ++n) d[r][n] = ok ? d[r][n] * (g[n] - dot[r]) : 0.f;
+        const int64_t t = t0 + r * L.rows + L.grp;
+        finish(t, t < hi, d[r]);
+      }
+#pragma unroll
+      for (int r = 0; r < R; ++r) cur[r] = nxt[r], st[r] = st1[r], st1[r] = st2[r];
     }
   };
   walk_sequences(a.seqs, c0, c1, piece, gap);
@@ -462,13 +556,28 @@ cudaError_t launch_balance_loss(const BalanceArgs& b, void* ws, uint32_t* status
   }
   if (e != cudaSuccess) return e;
   FinishArgs f{part, a.seqs, b.E, b.k, ch.rows, b.loss, b.z_loss, b.mean_scores, b.counts, b.tokens, status};
-  return launch_pdl(balance_finish_kernel, dim3((unsigned)b.num_seqs), dim3(kThreads), 0, s, f);
+  // one block per group of experts while that leaves SMs without work, at most eight
+  int blocks = 1;
+  while (blocks < 8 && blocks * 32 < b.E && b.num_seqs * blocks < 152) blocks *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(b.num_seqs * blocks));
+  cfg.blockDim = dim3(kFinishThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)blocks;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, balance_finish_kernel, f);
 }
 
 cudaError_t launch_balance_loss_backward(const BalanceBwdArgs& b, cudaStream_t s) {
   const void* ptrs[] = {b.logits, b.base, b.dlogits};
   const RowPlan plan = row_plan(ptrs, 3, b.dt, b.E);
-  const Chunks ch = cut_rows(b.T, (int64_t)kWarps * (32 / plan.lpr), 152 * 8);
+  const Chunks ch = cut_rows(b.T, (int64_t)kWarps * (32 / plan.lpr), 2 * kMaxChunks);
   BwdArgs a{};
   a.logits = b.logits;
   a.row_stats = reinterpret_cast<const float2*>(b.row_stats);

@@ -9,6 +9,8 @@
 
 #include <math.h>
 
+#include <type_traits>
+
 #include "common.cuh"
 
 namespace moe {
@@ -54,10 +56,52 @@ struct Lanes {
   __device__ __forceinline__ float sum(float x) const {
     return all(x, [](float a, float b) { return a + b; });
   }
-  __device__ __forceinline__ float max(float x) const {
-    return all(x, [](float a, float b) { return fmaxf(a, b); });
+  __device__ __forceinline__ float max(float x) const {  // passes over NaN
+    if constexpr (FULL) {
+      float y;
+      asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+      return y;
+    } else {
+      return all(x, [](float a, float b) { return fmaxf(a, b); });
+    }
+  }
+  // R sums at once.  Two values share one exchange: of x[0] and x[1] a lane
+  // keeps one and sends the other, so that R sums over 32 lanes cost about
+  // 2 R + 3 shuffles where R butterflies cost 5 R.
+  template <int R>
+  __device__ __forceinline__ void sums(float (&x)[R]) const {
+    if constexpr (FULL && R == 4) {
+      const int lane = threadIdx.x & 31;
+      const bool h = lane & 16, q = lane & 8;
+      float a = (h ? x[1] : x[0]) + __shfl_xor_sync(0xffffffffu, h ? x[0] : x[1], 16);
+      const float b = (h ? x[3] : x[2]) + __shfl_xor_sync(0xffffffffu, h ? x[2] : x[3], 16);
+      a = (q ? b : a) + __shfl_xor_sync(0xffffffffu, q ? a : b, 8);
+#pragma unroll
+      for (int d = 4; d > 0; d >>= 1) a += __shfl_xor_sync(0xffffffffu, a, d);
+      x[0] = __shfl_sync(0xffffffffu, a, 0);
+      x[1] = __shfl_sync(0xffffffffu, a, 16);
+      x[2] = __shfl_sync(0xffffffffu, a, 8);
+      x[3] = __shfl_sync(0xffffffffu, a, 24);
+    } else if constexpr (FULL && R == 2) {
+      const bool h = threadIdx.x & 16;
+      float a = (h ? x[1] : x[0]) + __shfl_xor_sync(0xffffffffu, h ? x[0] : x[1], 16);
+#pragma unroll
+      for (int d = 8; d > 0; d >>= 1) a += __shfl_xor_sync(0xffffffffu, a, d);
+      x[0] = __shfl_sync(0xffffffffu, a, 0);
+      x[1] = __shfl_sync(0xffffffffu, a, 16);
+    } else {
+#pragma unroll
+      for (int r = 0; r < R; ++r) x[r] = sum(x[r]);
+    }
   }
 };
+
+// Rows (of each lane group) that a warp works on at once: enough independent
+// loads in flight for HBM, within the registers.
+template <int VEC, int NV>
+constexpr int rows_at_once() {
+  return VEC * NV <= 8 ? 4 : VEC * NV <= 16 ? 2 : 1;
+}
 
 // One row's elements of this lane.
 template <typename T, int VEC, int NV>
@@ -67,7 +111,7 @@ struct RowRegs {
   static __device__ __forceinline__ bool used(int v, int lpr, int E) { return VEC > 1 || v * lpr < E; }
   static __device__ __forceinline__ int elem(int v, int i, int lpr, int sub) { return (v * lpr + sub) * VEC + i; }
 
-  T raw[N];
+  alignas(16) T raw[N];
 
   __device__ __forceinline__ void load(const T* row, int E, int lpr, int sub, bool ok, T fill) {
 #pragma unroll
@@ -87,6 +131,39 @@ struct RowRegs {
     }
   }
   __device__ __forceinline__ float operator[](int n) const { return to_f32<T>(raw[n]); }
+
+  // This lane's maximum; passes over NaN.
+  __device__ __forceinline__ float lane_max() const {
+    if constexpr (sizeof(T) == 2 && VEC == 8) {  // two elements an instruction
+      using T2 = typename std::conditional<std::is_same<T, __half>::value, __half2, __nv_bfloat162>::type;
+      T2 m = reinterpret_cast<const T2*>(raw)[0];
+#pragma unroll
+      for (int i = 1; i < N / 2; ++i) m = __hmax2(m, reinterpret_cast<const T2*>(raw)[i]);
+      return fmaxf(to_f32<T>(m.x), to_f32<T>(m.y));
+    } else {
+      float m = (*this)[0];
+#pragma unroll
+      for (int n = 1; n < N; ++n) m = fmaxf(m, (*this)[n]);
+      return m;
+    }
+  }
+};
+
+// exp((x - m) / tau) as 2^(x c - m c), c = log2(e) / tau, in one FMA an element.
+// mc = m c is rounded, which leaves a factor 2^(m c - mc) on every element of the
+// row: `fix` takes it out of their sum (to first order: |m c - mc| < 2^-12).
+// Rows that lie farther out (masked with a large negative value, say) form x - m
+// first.
+struct RowExp {
+  float c, mc, m, fix;
+  bool wide;
+  __device__ __forceinline__ RowExp(float m_, float c_) : c(c_), m(m_) {
+    mc = m_ * c_;
+    wide = fabsf(mc) > 4096.f && fabsf(m_) < INFINITY;
+    fix = fabsf(mc) <= 4096.f ? fmaf(fmaf(m_, c_, -mc), -kLn2, 1.f) : 1.f;
+  }
+  __device__ __forceinline__ float operator()(float x) const { return exp2_fast(fmaf(x, c, -mc)); }
+  __device__ __forceinline__ float far(float x) const { return exp2_fast((x - m) * c); }
 };
 
 // Stores N values of a lane at `row` (16-byte vectors or single elements).
