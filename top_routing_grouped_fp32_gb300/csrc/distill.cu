@@ -27,6 +27,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxChunks = 1216;  // eight blocks per SM
+constexpr int kMaxList = 64;
 
 // Below this share of the row's maximum the student's mass outside the list is
 // taken about its own maximum, and -q_r stands in the place of q_r / R.
@@ -417,69 +418,171 @@ struct TargetArgs {
   float* rest;
 };
 
-// (va, ia) comes before (vb, ib): larger logit, then lower id.
-__device__ __forceinline__ bool before(float va, int ia, float vb, int ib) {
-  return va > vb || (va == vb && ia < ib);
+// A logit and its expert as one unsigned key: larger logit first, then the lower
+// id; keys of a row differ.  Adding +0 makes -0 a +0 and a NaN the positive one,
+// which lies above +inf: a row is broken where its largest key is not below +inf's.
+template <typename T>
+struct SortKey {  // 16-bit logits: order-preserving bits above 0xffff - id
+  using Key = uint32_t;
+  static constexpr uint32_t kInf = (std::is_same<T, __half>::value ? 0xfc00u : 0xff80u) << 16;
+  static __device__ __forceinline__ Key make(T x, int id) {
+    uint32_t b;
+    if constexpr (std::is_same<T, __half>::value) b = __half_as_ushort(__hadd(x, __ushort_as_half(0)));
+    else b = __float_as_uint(__bfloat162float(x) + 0.f) >> 16;
+    const uint32_t o = b ^ ((b & 0x8000u) ? 0xffffu : 0x8000u);
+    return (o << 16) | (0xffffu - (uint32_t)id);
+  }
+  static __device__ __forceinline__ bool broken(Key k) { return k >= kInf; }
+  static __device__ __forceinline__ uint32_t id(Key k) { return 0xffffu - (k & 0xffffu); }
+  static __device__ __forceinline__ T logit(Key k) {
+    const uint16_t b = (uint16_t)((k >> 16) ^ ((k & 0x80000000u) ? 0x8000u : 0xffffu));
+    if constexpr (std::is_same<T, __half>::value) return __ushort_as_half(b);
+    else return __ushort_as_bfloat16(b);
+  }
+};
+template <>
+struct SortKey<float> {
+  using Key = uint64_t;
+  static __device__ __forceinline__ Key make(float x, int id) {
+    const uint32_t b = __float_as_uint(x + 0.f);
+    const uint32_t o = b ^ ((b & 0x80000000u) ? 0xffffffffu : 0x80000000u);
+    return ((uint64_t)o << 32) | (0xffffffffu - (uint32_t)id);
+  }
+  static __device__ __forceinline__ bool broken(Key k) { return (uint32_t)(k >> 32) >= 0xff800000u; }
+  static __device__ __forceinline__ uint32_t id(Key k) { return 0xffffffffu - (uint32_t)k; }
+  static __device__ __forceinline__ float logit(Key k) {
+    const uint32_t o = (uint32_t)(k >> 32);
+    return __uint_as_float(o ^ ((o & 0x80000000u) ? 0x80000000u : 0xffffffffu));
+  }
+};
+
+// Descending order of N = 2^i keys: Batcher's odd-even merge network.
+template <typename Key>
+__device__ __forceinline__ void order(Key& x, Key& y) {
+  const Key a = x, b = y;
+  x = a > b ? a : b;
+  y = a > b ? b : a;
+}
+template <int LO, int CNT, int GAP, typename Key, int N>
+__device__ __forceinline__ void odd_even_merge(Key (&k)[N]) {
+  if constexpr (2 * GAP < CNT) {
+    odd_even_merge<LO, CNT, 2 * GAP>(k);
+    odd_even_merge<LO + GAP, CNT, 2 * GAP>(k);
+#pragma unroll
+    for (int i = LO + GAP; i + GAP < LO + CNT; i += 2 * GAP) order(k[i], k[i + GAP]);
+  } else {
+    order(k[LO], k[LO + GAP]);
+  }
+}
+template <int LO, int CNT, typename Key, int N>
+__device__ __forceinline__ void sort_descending(Key (&k)[N]) {
+  if constexpr (CNT > 1) {
+    sort_descending<LO, CNT / 2>(k);
+    sort_descending<LO + CNT / 2, CNT / 2>(k);
+    odd_even_merge<LO, CNT, 1>(k);
+  }
 }
 
-// m rounds of arg-max over the experts that are left, then the log-sum-exp of
-// those that stay.
+template <bool FULL>
+__device__ __forceinline__ uint32_t row_max(const Lanes<FULL>& L, uint32_t k) {
+  if constexpr (FULL) return __reduce_max_sync(0xffffffffu, k);
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1)
+    if (d < L.lpr) k = max(k, __shfl_xor_sync(0xffffffffu, k, d));
+  return k;
+}
+template <bool FULL>
+__device__ __forceinline__ uint64_t row_max(const Lanes<FULL>& L, uint64_t k) {
+  const uint32_t hi = row_max(L, (uint32_t)(k >> 32));
+  const uint32_t lo = row_max(L, (uint32_t)(k >> 32) == hi ? (uint32_t)k : 0u);
+  return ((uint64_t)hi << 32) | lo;
+}
+
+// Each lane sorts its share of the row; then m rounds take the largest head of
+// the lanes' lists.  A round is one reduction, a compare and the winner's next
+// entry from shared memory: its cost does not grow with the row.
+constexpr int kTargetThreads = 128;
 template <typename T, int VEC, int NV, bool FULL>
-__global__ void __launch_bounds__(kThreads) distill_targets_kernel(TargetArgs a) {
-  constexpr int N = VEC * NV;
+__global__ void __launch_bounds__(kTargetThreads) distill_targets_kernel(TargetArgs a) {
+  constexpr int N = VEC * NV, W = kTargetThreads / 32;
   using Row = RowRegs<T, VEC, NV>;
+  using SK = SortKey<T>;
+  using Key = typename SK::Key;
+  __shared__ Key lists[W][N + 1][32];               // entry N ends a list: below every key
+  __shared__ Key taken[W][FULL ? kMaxList : 32 * N];  // [rows][m], in order
   pdl_wait();
   pdl_trigger();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const Lanes<FULL> L(a.lpr);
-  const int64_t t = ((int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5)) * L.rows + L.grp;
-  const bool in = t < a.T;
-  Row r;
-  r.load(static_cast<const T*>(a.logits) + t * a.E, a.E, L.lpr, L.sub, in, from_f32<T>(-INFINITY));
+  const T* logits = static_cast<const T*>(a.logits);
   T* top = static_cast<T*>(a.top);
-  float bad = 0.f;
-#pragma unroll
-  for (int n = 0; n < N; ++n)
-    if (isnan(r[n]) || r[n] == INFINITY) bad = 1.f;
-  bad = L.max(bad);
-  uint32_t taken = 0;
-#pragma unroll
-  for (int n = 0; n < N; ++n)
-    if (Row::elem(n / VEC, n % VEC, L.lpr, L.sub) >= a.E) taken |= 1u << n;
-  for (int j = 0; j < a.m; ++j) {
-    float bv = -INFINITY;
-    int bi = 0x7fffffff;
-#pragma unroll
-    for (int n = 0; n < N; ++n) {
-      const int e = Row::elem(n / VEC, n % VEC, L.lpr, L.sub);
-      if (!(taken >> n & 1u) && before(r[n], e, bv, bi)) bv = r[n], bi = e;
-    }
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) {
-      if (!FULL && d >= L.lpr) continue;
-      const float ov = __shfl_xor_sync(0xffffffffu, bv, d);
-      const int oi = __shfl_xor_sync(0xffffffffu, bi, d);
-      if (before(ov, oi, bv, bi)) bv = ov, bi = oi;
-    }
+  lists[warp][N][lane] = 0;
+  const int64_t step = (int64_t)gridDim.x * W * L.rows;
+  int64_t t0 = ((int64_t)blockIdx.x * W + warp) * L.rows;
+  auto load = [&](Row& r, int64_t t) { r.load(logits + t * a.E, a.E, L.lpr, L.sub, t < a.T, from_f32<T>(-INFINITY)); };
+  Row cur, nxt;
+  load(cur, t0 + L.grp);
+  for (; t0 < a.T; t0 += step) {
+    load(nxt, t0 + step + L.grp);
+    const int64_t t = t0 + L.grp;
+    const bool in = t < a.T;
+    Key key[N], list[N];
 #pragma unroll
     for (int n = 0; n < N; ++n)
-      if (Row::elem(n / VEC, n % VEC, L.lpr, L.sub) == bi) taken |= 1u << n;
-    if (in && L.sub == 0) {
-      a.idx[t * a.m + j] = bad != 0.f ? (uint32_t)j : (uint32_t)bi;
-      top[t * a.m + j] = from_f32<T>(bad != 0.f ? NAN : bv);
+      list[n] = key[n] = SK::make(cur.raw[n], Row::elem(n / VEC, n % VEC, L.lpr, L.sub));
+    sort_descending<0, N>(list);
+#pragma unroll
+    for (int n = 0; n < N; ++n) lists[warp][n][lane] = list[n];
+    Key head = list[0];
+    const Key* next = &lists[warp][1][lane];
+    Key* out = &taken[warp][L.grp * a.m];
+    const bool broken = SK::broken(row_max(L, head));
+#pragma unroll 4
+    for (int j = 0; j < a.m; ++j) {
+      if (head == row_max(L, head)) {
+        out[j] = head;
+        head = *next;
+        next += 32;
+      }
     }
+    __syncwarp();
+    // what stays, about the last one taken
+    const Key last = out[a.m - 1];
+    const float v = to_f32<T>(SK::logit(last));
+    const RowExp ex(v, a.c);
+    float s = 0.f;
+    if (ex.wide) {
+#pragma unroll
+      for (int n = 0; n < N; ++n) s += key[n] < last ? ex.far(cur[n]) : 0.f;
+    } else {
+#pragma unroll
+      for (int n = 0; n < N; ++n) s += key[n] < last ? ex(cur[n]) : 0.f;
+    }
+    s = L.sum(s) * ex.fix;
+    float rest = fmaf(a.tau, logf(s), v);
+    // far below it (or nothing, or -inf): about the maximum of what stays
+    if (__any_sync(0xffffffffu, !(s >= 1e-30f))) {
+      float mr = -INFINITY;
+#pragma unroll
+      for (int n = 0; n < N; ++n) mr = key[n] < last ? fmaxf(mr, cur[n]) : mr;
+      mr = L.max(mr);
+      float sr = 0.f;
+#pragma unroll
+      for (int n = 0; n < N; ++n) sr += key[n] < last ? exp2_fast((cur[n] - mr) * a.c) : 0.f;
+      sr = L.sum(sr);
+      if (!(s >= 1e-30f)) rest = mr == -INFINITY ? -INFINITY : fmaf(a.tau, logf(sr), mr);
+    }
+    if (in) {
+      for (int j = L.sub; j < a.m; j += L.lpr) {
+        const Key k = out[j];
+        a.idx[t * a.m + j] = broken ? (uint32_t)j : SK::id(k);
+        top[t * a.m + j] = broken ? from_f32<T>(NAN) : SK::logit(k);
+      }
+      if (L.sub == 0) a.rest[t] = broken ? NAN : rest;
+    }
+    __syncwarp();  // before the next row's lists
+    cur = nxt;
   }
-  float mr = -INFINITY;
-#pragma unroll
-  for (int n = 0; n < N; ++n)
-    if (!(taken >> n & 1u)) mr = fmaxf(mr, r[n]);
-  mr = L.max(mr);
-  float s = 0.f;
-#pragma unroll
-  for (int n = 0; n < N; ++n)
-    if (!(taken >> n & 1u)) s += exp2_fast((r[n] - mr) * a.c);
-  s = L.sum(s);
-  if (in && L.sub == 0)
-    a.rest[t] = bad != 0.f ? NAN : mr == -INFINITY ? -INFINITY : fmaf(a.tau, logf(s), mr);
 }
 
 struct LaunchFwd {
@@ -507,9 +610,10 @@ struct LaunchTargets {
   cudaStream_t s;
   template <typename T, int VEC, int NV, bool FULL>
   cudaError_t run() {
-    const int64_t per = (int64_t)kWarps * (32 / a.lpr);
-    return launch_pdl(distill_targets_kernel<T, VEC, NV, FULL>, dim3((unsigned)((a.T + per - 1) / per)),
-                      dim3(kThreads), 0, s, a);
+    const int64_t per = (int64_t)(kTargetThreads / 32) * (32 / a.lpr);
+    const int64_t blocks = (a.T + per - 1) / per;
+    return launch_pdl(distill_targets_kernel<T, VEC, NV, FULL>,
+                      dim3((unsigned)(blocks < kMaxChunks ? blocks : kMaxChunks)), dim3(kTargetThreads), 0, s, a);
   }
 };
 
