@@ -1,5 +1,5 @@
-// balance.cu -- the router's balance loss with per-expert counts, its z-loss
-// and their gradient.
+// balance.cu -- the router's balance loss with per-expert counts and its z-loss
+// (their gradient is in balance_bwd.cu).
 //
 // For the valid rows V_s of a sequence s (L_s of them), row scores p_te that sum
 // to one over the experts and the routed slots idx [T,k]:
@@ -7,38 +7,50 @@
 //   P_se   = 1/L_s sum_{t in V_s} p_te
 //   loss_s = E sum_e n_se / (k L_s) P_se
 //   z_s    = 1/L_s sum_{t in V_s} (log sum_e exp l_te)^2
-// The counts are not differentiated.  With g_se = dloss_s E n_se / (k L_s^2),
-//   softmax: dl_te = p_te (g_se - sum_i p_ti g_si) + dz_s 2 lse_t p_te / L_s
-//   sigmoid: dl_te = p_te (1 - sigmoid(l_te)) (g_se - sum_i p_ti g_si)
 //
-// Forward: one pass over the logits.  A block owns a range of rows; each lane
+// One pass over the logits.  A block owns a range of rows; each lane
 // keeps the sum of p for its own experts in registers, the block adds its warps
 // in a fixed order and writes one partial per (block, sequence) that it meets,
 // at slot block + sequence (unique, since rows and sequences both ascend).  A
-// second kernel adds each sequence's slots in a fixed order.  The counts are
-// integers, so shared-memory atomics leave them reproducible.
-#include <cooperative_groups.h>
-
+// second kernel adds each sequence's slots in a fixed order; a batch that one
+// block holds needs none.  The counts are integers, so shared-memory atomics
+// leave them reproducible.
 #include "internal.h"
 #include "rows.cuh"
 
 namespace moe {
 namespace {
 
-namespace cg = cooperative_groups;
-
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kMaxChunks = 304;    // partials a sequence may have: two blocks per SM
+constexpr int kMaxChunks = 304;    // blocks, and partials of a sequence: two per SM
 constexpr int kHistWords = 2048;   // copies of the block's histogram share this many words
 
 struct Partials {
-  float* p;        // [slots, E] sums of the scores
-  uint32_t* n;     // [slots, E] counts
-  float* z;        // [slots] sums of squared log-sum-exps
-  uint32_t* rows;  // [slots] valid rows
-  uint32_t* bad;   // [slots] indices that are no expert
+  float* p;           // [slots, E] sums of the scores
+  uint32_t* n;        // [slots, E] counts
+  float* z;           // [slots] sums of squared log-sum-exps
+  uint32_t* rows;     // [slots] valid rows
+  uint32_t* bad;      // [slots] indices that are no expert
+  float* share;       // [num_seqs, kMaxShares] a finishing block's part of the loss
+  uint32_t* ticket;   // [num_seqs] finishing blocks that are done
 };
+constexpr int kMaxShares = 32;
+
+struct Results {
+  float* loss;
+  float* z_loss;       // nullable
+  float* mean_scores;  // nullable
+  uint32_t* counts;
+  uint32_t* tokens;
+  uint32_t* status;
+};
+
+// E sum n/(k L) P/L from the sum of n P_sum, without the products of large numbers
+__device__ __forceinline__ float balance_of(float sum_np, int E, int k, uint32_t rows) {
+  const float len = (float)rows;
+  return rows ? sum_np / len * ((float)E / (float)k) / len : 0.f;
+}
 
 struct FwdArgs {
   const void* logits;
@@ -49,60 +61,54 @@ struct FwdArgs {
   int64_t T, chunk_rows;
   Partials part;
   float2* row_stats;
-  uint32_t* status;
   uint32_t k_magic;  // floor(2^32 / k) + 1 (k > 1): i / k = umulhi(i, magic) while i * k < 2^32
+  bool alone;        // the only block of one sequence: it writes the results
+  Results res;
 };
 
 // Sigmoid scores are normalised about 0, or about the row's maximum where all of
 // them are so small that their FP32 sum would lose them (sigmoid(l) = exp(l) there).
 constexpr float kFarBelow = -60.f;
 
-// Scores of a row about `shift`, not normalised, and their sum over this lane.
-template <typename Row, bool SIG>
-__device__ __forceinline__ float lane_scores(const Row& r, int lpr, int E, float m, float& shift,
-                                             float (&p)[Row::N]) {
-  float s = 0.f;
+// Scores of a row about `shift`, not normalised.
+template <bool SIG, typename Row>
+__device__ __forceinline__ void row_scores(const Row& r, float m, float& shift, float (&p)[Row::N]) {
   if (SIG && m >= kFarBelow) {
     shift = 0.f;
-#pragma unroll
-    for (int n = 0; n < Row::N; ++n) {
-      p[n] = rcp_fast(1.f + exp2_fast(r[n] * -kLog2e));
-      s += p[n];
-    }
-    return s;
-  }
-  shift = m;
-  const RowExp ex(m, kLog2e);
-  if (ex.wide) {
-#pragma unroll
-    for (int n = 0; n < Row::N; ++n) s += p[n] = ex.far(r[n]);
+    pairwise<Row::N>(
+        [&](int n) {
+          const float2 x = mul2(make_float2(r[n], r[n + 1]), both(-kLog2e));
+          const float2 y = add2(make_float2(exp2_fast(x.x), exp2_fast(x.y)), both(1.f));
+          p[n] = rcp_fast(y.x);
+          p[n + 1] = rcp_fast(y.y);
+        },
+        [&](int n) { p[n] = rcp_fast(1.f + exp2_fast(r[n] * -kLog2e)); });
   } else {
-#pragma unroll
-    for (int n = 0; n < Row::N; ++n) s += p[n] = ex(r[n]);
+    shift = m;
+    RowExp(m, kLog2e).row(r, p);
   }
-  return s;
 }
 
-template <typename T, int VEC, int NV, bool FULL, bool SIG>
-__global__ void __launch_bounds__(kThreads, VEC * NV <= 16 ? 2 : 1) balance_fwd_kernel(FwdArgs a) {
+template <typename T, int VEC, int NV, int LPR, bool SIG>
+__global__ void __launch_bounds__(kThreads, blocks_per_sm<T, VEC, NV>()) balance_fwd_kernel(FwdArgs a) {
   extern __shared__ float smem[];
   constexpr int N = VEC * NV, R = rows_at_once<VEC, NV>();
   constexpr int NI = 4;  // indices of a batch that a lane holds ahead of their use
   using Row = RowRegs<T, VEC, NV>;
-  float* red = smem;                                             // [kWarps][E]
+  float* red = smem;                                                  // [kWarps][E]
   uint32_t* hist = reinterpret_cast<uint32_t*>(smem + kWarps * a.E);  // [E][copies]
-  __shared__ float red_z[kWarps];
+  __shared__ float red_z[kWarps], red_np[kWarps];
   __shared__ uint32_t red_rows[kWarps], red_bad[kWarps];
 
   pdl_wait();
   pdl_trigger();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (blockIdx.x == 0 && threadIdx.x == 0) *a.status = 0u;
-  const Lanes<FULL> L(a.lpr);
-  const T* logits = static_cast<const T*>(a.logits);
-  const int64_t c0 = (int64_t)blockIdx.x * a.chunk_rows;
-  const int64_t c1 = min(c0 + a.chunk_rows, a.T);
-  const int batch = R * L.rows;            // rows a warp takes at once, at most 128
+  if (blockIdx.x == 0 && threadIdx.x == 0) *a.res.status = 0u;
+  if (!a.alone)
+    for (int i = blockIdx.x * kThreads + threadIdx.x; i < a.seqs.num; i += gridDim.x * kThreads) a.part.ticket[i] = 0u;
+  const Lanes<LPR> L(a.lpr);
+  const int room = a.E - L.sub * VEC;
+  const int batch = R * L.rows;            // consecutive rows that a warp takes at once, at most 128
   const int copy = lane & (a.copies - 1);  // its copy of the histogram
 
   auto gap = [&](int64_t lo, int64_t hi) {
@@ -116,65 +122,63 @@ __global__ void __launch_bounds__(kThreads, VEC * NV <= 16 ? 2 : 1) balance_fwd_
 #pragma unroll
     for (int n = 0; n < N; ++n) acc[n] = 0.f;
 
-    // which rows count, as a bit per row of a batch: loaded a batch before the rows
-    auto live = [&](int64_t t) {
+    int64_t t0 = lo + warp * batch;     // the batch's first row
+    int left = (int)(hi - t0);          // rows from there on (a block has far fewer than 2^31)
+    const int64_t stride = (int64_t)kWarps * batch * a.E;
+    const T* lp = static_cast<const T*>(a.logits) + (t0 + L.grp) * a.E + L.sub * VEC;
+    // which rows of a batch count, a bit for each r: known a batch before the rows are loaded
+    auto live = [&](int ahead) {
       uint32_t bits = 0;
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        const int64_t tr = t + r * L.rows + L.grp;
-        bits |= (uint32_t)(tr < hi && (!a.mask || __ldg(a.mask + tr))) << r;
+        const int i = ahead * kWarps * batch + r * L.rows + L.grp;
+        bits |= (uint32_t)(i < left && (!a.mask || __ldg(a.mask + t0 + i))) << r;
       }
       return bits;
     };
-    auto load = [&](Row& r, int64_t t, bool ok) {
-      r.load(logits + t * a.E, a.E, L.lpr, L.sub, ok, from_f32<T>(-INFINITY));
-    };
-    int64_t t0 = lo + (int64_t)warp * batch;
     Row cur[R], nxt[R];
-    uint32_t ok = live(t0), ok1 = live(t0 + (int64_t)kWarps * batch);
+    uint32_t ok = live(0), ok1 = live(1);
 #pragma unroll
-    for (int r = 0; r < R; ++r) load(cur[r], t0 + r * L.rows + L.grp, ok >> r & 1u);
-    for (; t0 < hi; t0 += (int64_t)kWarps * batch) {
+    for (int r = 0; r < R; ++r) {
+      cur[r].fill(from_f32<T>(-INFINITY));
+      nxt[r].fill(from_f32<T>(-INFINITY));
+      cur[r].load(lp + r * L.rows * a.E, room, L.lpr, ok >> r & 1u);
+    }
+    while (left > 0) {
       // the next batch's rows and this batch's indices are on their way during the arithmetic
-      const int64_t t1 = t0 + (int64_t)kWarps * batch;
-      const int slots = (int)(min((int64_t)batch, hi - t0)) * a.k;
+      const int slots = min(batch, left) * a.k;
       const uint32_t* ip = a.idx + t0 * a.k;
       uint32_t id[NI];
 #pragma unroll
       for (int i = 0; i < NI; ++i) id[i] = lane + 32 * i < slots ? __ldg(ip + lane + 32 * i) : 0u;
+      lp += stride;
 #pragma unroll
-      for (int r = 0; r < R; ++r) load(nxt[r], t1 + r * L.rows + L.grp, ok1 >> r & 1u);
-      const uint32_t ok2 = live(t1 + (int64_t)kWarps * batch);
+      for (int r = 0; r < R; ++r) nxt[r].load(lp + r * L.rows * a.E, room, L.lpr, ok1 >> r & 1u);
+      const uint32_t ok2 = live(2);
 
-      float p[R][N], s[R], m[R];
-#pragma unroll
-      for (int r = 0; r < R; ++r) m[r] = L.max(cur[r].lane_max());
-#pragma unroll
-      for (int r = 0; r < R; ++r) s[r] = lane_scores<Row, SIG>(cur[r], L.lpr, a.E, m[r], m[r], p[r]);
-      L.sums(s);
+      float mine_m = 0.f, mine_s = 0.f;  // the row that this lane writes the statistics of
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        const float inv = rcp_fast(s[r]);  // p carries the factor that fix takes out, too
-        if (!SIG || m[r] != 0.f) s[r] *= RowExp(m[r], kLog2e).fix;
+        float p[N], m = L.max(cur[r].lane_max());
+        row_scores<SIG>(cur[r], m, m, p);
+        const float s = L.sum(lane_sum(p));
         if (ok >> r & 1u) {
-#pragma unroll
-          for (int n = 0; n < N; ++n) acc[n] = fmaf(p[r][n], inv, acc[n]);
+          const float inv = rcp_fast(s);  // p carries the factor that fix() takes out, too
+          pairwise<N>([&](int n) { put(acc, n, fma2(pair(p, n), both(inv), pair(acc, n))); },
+                      [&](int n) { acc[n] = fmaf(p[n], inv, acc[n]); });
         }
-      }
-      // a row's statistics leave from its lane r (of few lanes: r, r + lpr, ..)
-      for (int q = 0; q < R; q += L.lpr) {
-        float mr = 0.f, sr = 0.f;
-        bool o = false;
-#pragma unroll
-        for (int r = 0; r < R; ++r)
-          if (r == q + L.sub) mr = m[r], sr = s[r], o = ok >> r & 1u;
-        const int64_t t = t0 + (q + L.sub) * L.rows + L.grp;
-        if (q + L.sub < R && t < hi) {
-          a.row_stats[t] = o ? make_float2(mr, sr) : make_float2(0.f, 0.f);
-          if (o) {
-            ++valid;
-            if (!SIG) {
-              const float lse = mr + logf(sr);
+        // (groups of fewer than R lanes write row after row)
+        const int owner = L.lpr >= R ? r : 0;
+        if (L.sub == owner) mine_m = m, mine_s = s;
+        if ((r == R - 1 || L.lpr < R) && L.sub < R) {
+          const int mr = L.lpr >= R ? L.sub : r, i = mr * L.rows + L.grp;
+          if (i < left && (L.lpr >= R || L.sub == 0)) {
+            const bool o = ok >> mr & 1u;
+            if (!SIG || mine_m != 0.f) mine_s *= RowExp(mine_m, kLog2e).fix();
+            a.row_stats[t0 + i] = o ? make_float2(mine_m, mine_s) : make_float2(0.f, 0.f);
+            valid += o;
+            if (!SIG && o) {
+              const float lse = fmaf(log2_fast(mine_s), kLn2, mine_m);
               zacc = fmaf(lse, lse, zacc);
             }
           }
@@ -193,11 +197,13 @@ __global__ void __launch_bounds__(kThreads, VEC * NV <= 16 ? 2 : 1) balance_fwd_
 #pragma unroll
       for (int r = 0; r < R; ++r) cur[r] = nxt[r];
       ok = ok1, ok1 = ok2;
+      t0 += kWarps * batch;
+      left -= kWarps * batch;
     }
     // the rows of a warp, then the warps, in a fixed order
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-      if (!FULL && d >= L.lpr) {
+      if (d >= L.lpr) {
 #pragma unroll
         for (int n = 0; n < N; ++n) acc[n] += __shfl_xor_sync(0xffffffffu, acc[n], d);
       }
@@ -208,12 +214,17 @@ __global__ void __launch_bounds__(kThreads, VEC * NV <= 16 ? 2 : 1) balance_fwd_
     if (L.grp == 0) {
 #pragma unroll
       for (int n = 0; n < N; ++n) {
-        const int e = Row::elem(n / VEC, n % VEC, L.lpr, L.sub);
+        const int e = Row::elem(n, L.lpr, L.sub);
         if (e < a.E) red[warp * a.E + e] = acc[n];
       }
     }
     if (lane == 0) red_z[warp] = zacc, red_rows[warp] = valid, red_bad[warp] = bad;
     __syncthreads();
+    float z = 0.f, np = 0.f;
+    uint32_t rows = 0, wrong = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) z += red_z[w], rows += red_rows[w], wrong += red_bad[w];
+    const float inv = rows ? 1.f / (float)rows : 0.f;
     const int64_t slot = (int64_t)blockIdx.x + seq;
     for (int e = threadIdx.x; e < a.E; e += kThreads) {
       float s = 0.f;
@@ -221,57 +232,70 @@ __global__ void __launch_bounds__(kThreads, VEC * NV <= 16 ? 2 : 1) balance_fwd_
       for (int w = 0; w < kWarps; ++w) s += red[w * a.E + e];
       uint32_t c = 0;
       for (int i = 0; i < a.copies; ++i) c += hist[e * a.copies + i];
-      a.part.p[slot * a.E + e] = s;
-      a.part.n[slot * a.E + e] = c;
+      if (a.alone) {
+        a.res.counts[e] = c;
+        if (a.res.mean_scores) a.res.mean_scores[e] = rows ? s * inv : 0.f;
+        np = fmaf((float)c, s, np);
+      } else {
+        a.part.p[slot * a.E + e] = s;
+        a.part.n[slot * a.E + e] = c;
+      }
+    }
+    if (a.alone) {
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) np += __shfl_xor_sync(0xffffffffu, np, d);
+      if (lane == 0) red_np[warp] = np;
+      __syncthreads();
     }
     if (threadIdx.x == 0) {
-      float z = 0.f;
-      uint32_t v = 0, b = 0;
-      for (int w = 0; w < kWarps; ++w) z += red_z[w], v += red_rows[w], b += red_bad[w];
-      a.part.z[slot] = z;
-      a.part.rows[slot] = v;
-      a.part.bad[slot] = b;
+      if (a.alone) {
+        np = 0.f;
+        for (int w = 0; w < kWarps; ++w) np += red_np[w];
+        a.res.loss[0] = balance_of(np, a.E, a.k, rows);
+        if (a.res.z_loss) a.res.z_loss[0] = rows ? z * inv : 0.f;
+        a.res.tokens[0] = rows;
+        if (wrong) set_status(a.res.status, MOE_ERR_INVALID_INDEX);
+      } else {
+        a.part.z[slot] = z;
+        a.part.rows[slot] = rows;
+        a.part.bad[slot] = wrong;
+      }
     }
     __syncthreads();  // before the next piece writes the shared arrays
   };
-  walk_sequences(a.seqs, c0, c1, piece, gap);
+  if (a.alone) {
+    piece(0, 0, a.T);
+    return;
+  }
+  const int64_t c0 = (int64_t)blockIdx.x * a.chunk_rows;
+  walk_sequences(a.seqs, c0, min(c0 + a.chunk_rows, a.T), piece, gap);
 }
 
 struct FinishArgs {
   Partials part;
   Seqs seqs;
-  int E, k;
+  int E, k, blocks;  // blocks of a sequence
   int64_t chunk_rows;
-  float* loss;
-  float* z_loss;
-  float* mean_scores;
-  uint32_t* counts;
-  uint32_t* tokens;
-  uint32_t* status;
+  Results res;
 };
 
-// A cluster of blocks per sequence, each for every CL-th group of 32 experts:
-// 32 experts x 32 slot lanes at a time.  Block 0 adds the blocks' shares of the
-// loss in order.
-constexpr int kFinishThreads = 1024;
-constexpr int kFinishWarps = kFinishThreads / 32;
-
-__global__ void __launch_bounds__(kFinishThreads) balance_finish_kernel(FinishArgs a) {
-  __shared__ float sp[kFinishWarps][33];
-  __shared__ uint32_t sn[kFinishWarps][33];
-  __shared__ float sz[kFinishWarps];
-  __shared__ uint32_t sv[kFinishWarps], sb[kFinishWarps];
-  __shared__ double share;
-  cg::cluster_group cl = cg::this_cluster();
-  const int rank = (int)cl.block_rank(), blocks = (int)cl.num_blocks();
-  const int s = blockIdx.x / blocks;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+// Adds a sequence's slots, 32 experts x one slot lane a warp at a time.  A
+// sequence has `blocks` blocks, each with every blocks-th group of 32 experts; the
+// one that finishes last adds their shares of the loss, in order.
+template <int W>
+__global__ void __launch_bounds__(32 * W) balance_finish_kernel(FinishArgs a) {
+  __shared__ float sp[W][33];
+  __shared__ uint32_t sn[W][33];
+  __shared__ float sz[W];
+  __shared__ uint32_t sv[W], sb[W];
   pdl_wait();
   pdl_trigger();
+  const int s = blockIdx.x / a.blocks, part = blockIdx.x % a.blocks;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t lo = a.seqs.at(s), hi = a.seqs.at(s + 1);
-  if (rank == 0 && threadIdx.x == 0 && a.seqs.off &&
+  if (part == 0 && threadIdx.x == 0 && a.seqs.off &&
       (hi < lo || (int64_t)__ldg(a.seqs.off + s) > a.seqs.T || (int64_t)__ldg(a.seqs.off + s + 1) > a.seqs.T))
-    set_status(a.status, MOE_ERR_INVALID_INDEX);
+    set_status(a.res.status, MOE_ERR_INVALID_INDEX);
   // slots first..last hold the sequence
   int64_t first = 0, last = -1;
   if (hi > lo) {
@@ -279,28 +303,27 @@ __global__ void __launch_bounds__(kFinishThreads) balance_finish_kernel(FinishAr
     last = (hi - 1) / a.chunk_rows + s;
   }
   float z = 0.f;
-  uint32_t valid = 0, bad = 0;
-  for (int64_t i = first + threadIdx.x; i <= last; i += kFinishThreads) {
+  uint32_t rows = 0, bad = 0;
+  for (int64_t i = first + threadIdx.x; i <= last; i += 32 * W) {
     z += a.part.z[i];
-    valid += a.part.rows[i];
+    rows += a.part.rows[i];
     bad += a.part.bad[i];
   }
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) {
     z += __shfl_xor_sync(0xffffffffu, z, d);
-    valid += __shfl_xor_sync(0xffffffffu, valid, d);
+    rows += __shfl_xor_sync(0xffffffffu, rows, d);
     bad += __shfl_xor_sync(0xffffffffu, bad, d);
   }
-  if (lane == 0) sz[warp] = z, sv[warp] = valid, sb[warp] = bad;
-  double dot = 0.0;
-  uint32_t rows = 0;
-  for (int e0 = rank * 32; e0 < a.E; e0 += blocks * 32) {
+  if (lane == 0) sz[warp] = z, sv[warp] = rows, sb[warp] = bad;
+  float np = 0.f;
+  for (int e0 = part * 32; e0 < a.E; e0 += a.blocks * 32) {
     const int e = e0 + lane;
     float p = 0.f;
     uint32_t n = 0;
     if (e < a.E) {
 #pragma unroll 4
-      for (int64_t i = first + warp; i <= last; i += kFinishWarps) {
+      for (int64_t i = first + warp; i <= last; i += W) {
         p += a.part.p[i * a.E + e];
         n += a.part.n[i * a.E + e];
       }
@@ -308,179 +331,39 @@ __global__ void __launch_bounds__(kFinishThreads) balance_finish_kernel(FinishAr
     sp[warp][lane] = p;
     sn[warp][lane] = n;
     __syncthreads();
-    // warp w now adds the slot lanes of expert w
-    p = sp[lane][warp], n = sn[lane][warp];
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) {
-      p += __shfl_xor_sync(0xffffffffu, p, d);
-      n += __shfl_xor_sync(0xffffffffu, n, d);
-    }
-    __syncthreads();
-    if (lane == 0) sp[0][warp] = p, sn[0][warp] = n;
-    __syncthreads();
     if (warp == 0) {
-      rows = 0;
-      for (int w = 0; w < kFinishWarps; ++w) rows += sv[w];
-      p = sp[0][lane], n = sn[0][lane];
+      rows = 0, p = 0.f, n = 0;
+#pragma unroll
+      for (int w = 0; w < W; ++w) rows += sv[w], p += sp[w][lane], n += sn[w][lane];
       if (e < a.E) {
-        a.counts[(int64_t)s * a.E + e] = n;
-        if (a.mean_scores) a.mean_scores[(int64_t)s * a.E + e] = rows ? p / (float)rows : 0.f;
-        dot += (double)n * (double)p;
+        a.res.counts[(int64_t)s * a.E + e] = n;
+        if (a.res.mean_scores) a.res.mean_scores[(int64_t)s * a.E + e] = rows ? p / (float)rows : 0.f;
+        np = fmaf((float)n, p, np);
       }
     }
     __syncthreads();
   }
-  if (warp == 0) {
+  if (warp != 0) return;
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, d);
-    if (lane == 0) share = dot;
+  for (int d = 16; d > 0; d >>= 1) np += __shfl_xor_sync(0xffffffffu, np, d);
+  if (lane != 0) return;
+  if (part == 0) {
+    z = 0.f, bad = 0;
+    for (int w = 0; w < W; ++w) z += sz[w], bad += sb[w];
+    if (a.res.z_loss) a.res.z_loss[s] = rows ? z / (float)rows : 0.f;
+    a.res.tokens[s] = rows;
+    if (bad) set_status(a.res.status, MOE_ERR_INVALID_INDEX);
   }
-  cl.sync();
-  if (rank == 0 && threadIdx.x == 0) {
-    dot = 0.0;
-    for (int b = 0; b < blocks; ++b) dot += *cl.map_shared_rank(&share, b);
-    float zz = 0.f;
-    uint32_t b = 0;
-    rows = 0;
-    for (int w = 0; w < kFinishWarps; ++w) zz += sz[w], rows += sv[w], b += sb[w];
-    const double len = (double)rows;
-    a.loss[s] = rows ? (float)((double)a.E * dot / ((double)a.k * len * len)) : 0.f;
-    if (a.z_loss) a.z_loss[s] = rows ? zz / (float)rows : 0.f;
-    a.tokens[s] = rows;
-    if (b) set_status(a.status, MOE_ERR_INVALID_INDEX);
+  if (a.blocks > 1) {
+    float* share = a.part.share + (int64_t)s * kMaxShares;
+    __stcg(share + part, np);
+    __threadfence();
+    if (atomicAdd(a.part.ticket + s, 1u) != (uint32_t)a.blocks - 1u) return;
+    __threadfence();
+    np = 0.f;
+    for (int b = 0; b < a.blocks; ++b) np += __ldcg(share + b);
   }
-  cl.sync();  // the shares are read
-}
-
-struct BwdArgs {
-  const void* logits;
-  const float2* row_stats;
-  const uint32_t* counts;
-  const uint32_t* tokens;
-  const float* dloss;
-  const float* dz;
-  Seqs seqs;
-  int E, k, lpr;
-  int64_t T, chunk_rows;
-  const void* base;
-  void* out;
-};
-
-template <typename T, int VEC, int NV, bool FULL, bool SIG>
-__global__ void __launch_bounds__(kThreads, VEC * NV <= 16 ? 2 : 1) balance_bwd_kernel(BwdArgs a) {
-  constexpr int N = VEC * NV, R = rows_at_once<VEC, NV>();
-  using Row = RowRegs<T, VEC, NV>;
-  pdl_wait();
-  pdl_trigger();
-  const int warp = threadIdx.x >> 5;
-  const Lanes<FULL> L(a.lpr);
-  const T* logits = static_cast<const T*>(a.logits);
-  const T* base = static_cast<const T*>(a.base);
-  T* out = static_cast<T*>(a.out);
-  const int64_t c0 = (int64_t)blockIdx.x * a.chunk_rows;
-  const int64_t c1 = min(c0 + a.chunk_rows, a.T);
-  const int batch = R * L.rows;
-
-  auto finish = [&](int64_t t, bool in, float (&d)[N]) {
-    if (!in) return;
-    if (base) {
-      Row b;
-      b.load(base + t * a.E, a.E, L.lpr, L.sub, true, from_f32<T>(0.f));
-#pragma unroll
-      for (int n = 0; n < N; ++n) d[n] += b[n];
-    }
-    store_row<T, VEC, NV>(out + t * a.E, a.E, L.lpr, L.sub, d);
-  };
-  auto gap = [&](int64_t lo, int64_t hi) {
-    for (int64_t t0 = lo + warp * L.rows; t0 < hi; t0 += kWarps * L.rows) {
-      float d[N];
-#pragma unroll
-      for (int n = 0; n < N; ++n) d[n] = 0.f;
-      finish(t0 + L.grp, t0 + L.grp < hi, d);
-    }
-  };
-  auto piece = [&](int seq, int64_t lo, int64_t hi) {
-    // g about an even load, (E n - k L) / (k L^2): exact in integers, and the
-    // scores sum to one, so a constant taken from g changes nothing
-    const int64_t rows = (int64_t)__ldg(a.tokens + seq);
-    const double kl = (double)a.k * (double)rows;
-    const float up = rows ? (float)((double)__ldg(a.dloss + seq) / (kl * (double)rows)) : 0.f;
-    const float zc = !SIG && a.dz && rows ? 2.f * __ldg(a.dz + seq) / (float)rows : 0.f;
-    float g[N];
-#pragma unroll
-    for (int n = 0; n < N; ++n) {
-      const int e = Row::elem(n / VEC, n % VEC, L.lpr, L.sub);
-      const int64_t c = e < a.E ? (int64_t)__ldg(a.counts + (int64_t)seq * a.E + e) : 0;
-      g[n] = up * (float)(c * a.E - rows * a.k);
-    }
-    auto stats = [&](int64_t t) { return t < hi ? __ldg(a.row_stats + t) : make_float2(0.f, 0.f); };
-    // rows that do not count (a sum of 0) are not read
-    auto load = [&](Row& r, int64_t t, float2 st) {
-      r.load(logits + t * a.E, a.E, L.lpr, L.sub, st.y != 0.f, from_f32<T>(-INFINITY));
-    };
-    int64_t t0 = lo + (int64_t)warp * batch;
-    Row cur[R], nxt[R];
-    float2 st[R], st1[R];  // a batch ahead of the rows
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      st[r] = stats(t0 + r * L.rows + L.grp);
-      st1[r] = stats(t0 + (int64_t)kWarps * batch + r * L.rows + L.grp);
-    }
-#pragma unroll
-    for (int r = 0; r < R; ++r) load(cur[r], t0 + r * L.rows + L.grp, st[r]);
-    for (; t0 < hi; t0 += (int64_t)kWarps * batch) {
-      const int64_t t1 = t0 + (int64_t)kWarps * batch;
-      float2 st2[R];
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        load(nxt[r], t1 + r * L.rows + L.grp, st1[r]);
-        st2[r] = stats(t1 + (int64_t)kWarps * batch + r * L.rows + L.grp);
-      }
-      float d[R][N], dot[R];
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        dot[r] = 0.f;
-        if (SIG && st[r].x == 0.f) {
-          const float inv = rcp_fast(st[r].y);
-#pragma unroll
-          for (int n = 0; n < N; ++n) {
-            const float x = cur[r][n];
-            const float ex = exp2_fast(fabsf(x) * -kLog2e);  // sigmoid(|l|) = 1 / (1 + ex)
-            const float up1 = rcp_fast(1.f + ex), lo1 = ex * up1;
-            const float p = (x < 0.f ? lo1 : up1) * inv;
-            dot[r] = fmaf(p, g[n], dot[r]);
-            d[r][n] = p * (x < 0.f ? up1 : lo1);
-          }
-        } else {
-          const RowExp ex(st[r].x, kLog2e);
-          const float inv = rcp_fast(st[r].y) * ex.fix;
-          if (ex.wide) {
-#pragma unroll
-            for (int n = 0; n < N; ++n) d[r][n] = ex.far(cur[r][n]) * inv;
-          } else {
-#pragma unroll
-            for (int n = 0; n < N; ++n) d[r][n] = ex(cur[r][n]) * inv;
-          }
-#pragma unroll
-          for (int n = 0; n < N; ++n) dot[r] = fmaf(d[r][n], g[n], dot[r]);
-        }
-      }
-      L.sums(dot);
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        // rows that do not count have a sum of 0; NaN sums leave NaN
-        const bool ok = st[r].y != 0.f;
-        if (!SIG && a.dz) dot[r] -= zc * (st[r].x + logf(st[r].y));
-#pragma unroll
-        for (int n = 0; n < N; ++n) d[r][n] = ok ? d[r][n] * (g[n] - dot[r]) : 0.f;
-        const int64_t t = t0 + r * L.rows + L.grp;
-        finish(t, t < hi, d[r]);
-      }
-#pragma unroll
-      for (int r = 0; r < R; ++r) cur[r] = nxt[r], st[r] = st1[r], st1[r] = st2[r];
-    }
-  };
-  walk_sequences(a.seqs, c0, c1, piece, gap);
+  a.res.loss[s] = balance_of(np, a.E, a.k, rows);
 }
 
 int hist_copies(int E) {
@@ -495,41 +378,36 @@ struct LaunchFwd {
   int chunks;
   size_t smem;
   cudaStream_t s;
-  template <typename T, int VEC, int NV, bool FULL>
+  template <typename T, int VEC, int NV, int LPR>
   cudaError_t run() {
-    return launch_pdl(balance_fwd_kernel<T, VEC, NV, FULL, SIG>, dim3((unsigned)chunks), dim3(kThreads), smem, s, a);
+    return launch_pdl(balance_fwd_kernel<T, VEC, NV, LPR, SIG>, dim3((unsigned)chunks), dim3(kThreads), smem, s, a);
   }
 };
 
-template <bool SIG>
-struct LaunchBwd {
-  BwdArgs a;
-  int chunks;
-  cudaStream_t s;
-  template <typename T, int VEC, int NV, bool FULL>
-  cudaError_t run() {
-    return launch_pdl(balance_bwd_kernel<T, VEC, NV, FULL, SIG>, dim3((unsigned)chunks), dim3(kThreads), 0, s, a);
-  }
-};
+size_t slot_count(int64_t T, int64_t num_seqs) {
+  return (size_t)(kMaxChunks < T ? kMaxChunks : T) + (size_t)num_seqs;
+}
 
 }  // namespace
 
 size_t balance_workspace_bytes(int64_t T, int E, int64_t num_seqs) {
-  const size_t slots = (size_t)(kMaxChunks < T ? kMaxChunks : T) + (size_t)num_seqs;
-  return align_up(slots * (size_t)E * 8 + slots * 12, 256);
+  const size_t slots = slot_count(T, num_seqs);
+  return align_up(slots * (size_t)E * 8 + slots * 12 + (size_t)num_seqs * 4 * (kMaxShares + 1), 256);
 }
 
 cudaError_t launch_balance_loss(const BalanceArgs& b, void* ws, uint32_t* status, cudaStream_t s) {
   const void* ptrs[] = {b.logits};
   const RowPlan plan = row_plan(ptrs, 1, b.dt, b.E);
-  const Chunks ch = cut_rows(b.T, (int64_t)kWarps * (32 / plan.lpr), kMaxChunks);
-  const size_t slots = (size_t)(kMaxChunks < b.T ? kMaxChunks : b.T) + (size_t)b.num_seqs;
+  const Chunks ch = cut_rows(b.T, plan_batch(plan, b.dt), kMaxChunks);
+  const size_t slots = slot_count(b.T, b.num_seqs);
   Partials part;
   part.p = static_cast<float*>(ws);
   part.n = reinterpret_cast<uint32_t*>(part.p + slots * b.E);
   part.z = reinterpret_cast<float*>(part.n + slots * b.E);
   part.rows = reinterpret_cast<uint32_t*>(part.z + slots);
   part.bad = part.rows + slots;
+  part.share = reinterpret_cast<float*>(part.bad + slots);
+  part.ticket = reinterpret_cast<uint32_t*>(part.share + b.num_seqs * kMaxShares);
   FwdArgs a{};
   a.logits = b.logits;
   a.idx = b.idx;
@@ -543,8 +421,9 @@ cudaError_t launch_balance_loss(const BalanceArgs& b, void* ws, uint32_t* status
   a.chunk_rows = ch.rows;
   a.part = part;
   a.row_stats = reinterpret_cast<float2*>(b.row_stats);
-  a.status = status;
   a.k_magic = b.k == 1 ? 0u : (uint32_t)((1ull << 32) / (uint32_t)b.k) + 1u;
+  a.alone = ch.chunks == 1 && !b.seq_offsets;
+  a.res = Results{b.loss, b.z_loss, b.mean_scores, b.counts, b.tokens, status};
   const size_t smem = (size_t)kWarps * b.E * 4 + (size_t)a.copies * b.E * 4;
   cudaError_t e;
   if (b.sigmoid) {
@@ -554,51 +433,16 @@ cudaError_t launch_balance_loss(const BalanceArgs& b, void* ws, uint32_t* status
     LaunchFwd<false> f{a, ch.chunks, smem, s};
     e = with_row_variant(b.dt, plan, f);
   }
-  if (e != cudaSuccess) return e;
-  FinishArgs f{part, a.seqs, b.E, b.k, ch.rows, b.loss, b.z_loss, b.mean_scores, b.counts, b.tokens, status};
-  // one block per group of experts while that leaves SMs without work, at most eight
-  int blocks = 1;
-  while (blocks < 8 && blocks * 32 < b.E && b.num_seqs * blocks < 152) blocks *= 2;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(b.num_seqs * blocks));
-  cfg.blockDim = dim3(kFinishThreads);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = (unsigned)blocks;
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, balance_finish_kernel, f);
-}
-
-cudaError_t launch_balance_loss_backward(const BalanceBwdArgs& b, cudaStream_t s) {
-  const void* ptrs[] = {b.logits, b.base, b.dlogits};
-  const RowPlan plan = row_plan(ptrs, 3, b.dt, b.E);
-  const Chunks ch = cut_rows(b.T, (int64_t)kWarps * (32 / plan.lpr), 2 * kMaxChunks);
-  BwdArgs a{};
-  a.logits = b.logits;
-  a.row_stats = reinterpret_cast<const float2*>(b.row_stats);
-  a.counts = b.counts;
-  a.tokens = b.tokens;
-  a.dloss = b.dloss;
-  a.dz = b.dz_loss;
-  a.seqs = Seqs{b.seq_offsets, (int)b.num_seqs, b.T};
-  a.E = b.E;
-  a.k = b.k;
-  a.lpr = plan.lpr;
-  a.T = b.T;
-  a.chunk_rows = ch.rows;
-  a.base = b.base;
-  a.out = b.dlogits;
-  if (b.sigmoid) {
-    LaunchBwd<true> f{a, ch.chunks, s};
-    return with_row_variant(b.dt, plan, f);
-  }
-  LaunchBwd<false> f{a, ch.chunks, s};
-  return with_row_variant(b.dt, plan, f);
+  if (e != cudaSuccess || a.alone) return e;
+  // a block for each group of experts while the blocks fit the GPU at once; many
+  // slots a sequence are added by more warps
+  const int64_t groups = (b.E + 31) / 32;
+  const int64_t fit = 304 / b.num_seqs;
+  const int blocks = (int)(groups < fit ? groups : fit > 1 ? fit : 1);
+  const FinishArgs f{part, a.seqs, b.E, b.k, blocks, ch.rows, a.res};
+  const dim3 grid((unsigned)(b.num_seqs * blocks));
+  if (ch.chunks / b.num_seqs >= 32) return launch_pdl(balance_finish_kernel<32>, grid, dim3(1024), 0, s, f);
+  return launch_pdl(balance_finish_kernel<8>, grid, dim3(256), 0, s, f);
 }
 
 }  // namespace moe

@@ -3,8 +3,8 @@
 // Shared by the router's training losses (balance.cu, distill.cu).  A row of
 // E <= 1024 logits is held by `lpr` lanes (a power of two), NV vectors of VEC
 // elements per lane: vector v of lane `sub` starts at element
-// (v * lpr + sub) * VEC, so that one warp load reads a contiguous piece.  With
-// fewer than 32 lanes a row (NV == 1) a warp holds 32 / lpr rows at once.
+// (v * lpr + sub) * VEC, so that one load reads contiguous pieces.  A warp holds
+// 32 / lpr rows at once.
 #pragma once
 
 #include <math.h>
@@ -18,7 +18,7 @@ namespace moe {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
-// 2^x and log2(x), within 2 ulp and 2^-22 absolute; subnormals are zero.
+// 2^x, 1 / x and log2(x), within 2 ulp, 1 ulp and 2^-22; subnormals are zero.
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -30,34 +30,87 @@ __device__ __forceinline__ float rcp_fast(float x) {
   return y;
 }
 
-// How the lanes of a warp are laid over rows.  FULL: all 32 lanes hold one row.
-template <bool FULL>
+__device__ __forceinline__ float log2_fast(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Two FP32 operations an instruction (x[n], x[n + 1] in a register pair).
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n .reg .b64 a, b, c, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mov.b64 c, {%6, %7};\n"
+      " fma.rn.f32x2 d, a, b, c;\n mov.b64 {%0, %1}, d;\n}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n .reg .b64 a, b, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n add.rn.f32x2 d, a, b;\n"
+      " mov.b64 {%0, %1}, d;\n}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n .reg .b64 a, b, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mul.rn.f32x2 d, a, b;\n"
+      " mov.b64 {%0, %1}, d;\n}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
+// Calls f2(n) for pairs of 0..N-1 (f1(0) where N == 1).
+template <int N, typename F2, typename F1>
+__device__ __forceinline__ void pairwise(F2 f2, F1 f1) {
+  if constexpr (N == 1) {
+    f1(0);
+  } else {
+#pragma unroll
+    for (int n = 0; n < N; n += 2) f2(n);
+  }
+}
+template <int N>
+__device__ __forceinline__ float2 pair(const float (&x)[N], int n) {
+  return make_float2(x[n], x[n + 1]);
+}
+template <int N>
+__device__ __forceinline__ void put(float (&x)[N], int n, float2 v) {
+  x[n] = v.x;
+  x[n + 1] = v.y;
+}
+
+// How the lanes of a warp are laid over rows: LPR lanes a row (0: `lpr` of them).
+template <int LPR>
 struct Lanes {
   int lpr, sub, grp, rows;  // lanes per row, lane in its row, row in the warp, rows per warp
   __device__ __forceinline__ explicit Lanes(int lpr_) {
     const int lane = threadIdx.x & 31;
-    lpr = FULL ? 32 : lpr_;
-    sub = FULL ? lane : lane & (lpr - 1);
-    grp = FULL ? 0 : lane / lpr;
-    rows = FULL ? 1 : 32 / lpr;
+    lpr = LPR ? LPR : lpr_;
+    sub = lane & (lpr - 1);
+    grp = lane / lpr;
+    rows = 32 / lpr;
   }
   __device__ __forceinline__ unsigned mask() const {
-    return FULL ? 0xffffffffu : (lpr == 32 ? 0xffffffffu : ((1u << lpr) - 1u) << (grp * lpr));
+    return lpr == 32 ? 0xffffffffu : ((1u << lpr) - 1u) << (grp * lpr);
   }
   // Butterflies over the lanes of a row: every lane gets the same bits.  All
   // lanes of the warp take part.
-  template <typename F>
-  __device__ __forceinline__ float all(float x, F f) const {
+  template <typename V, typename F>
+  __device__ __forceinline__ V all(V x, F f) const {
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1)
-      if (FULL || d < lpr) x = f(x, __shfl_xor_sync(0xffffffffu, x, d));
+      if (d < lpr) x = f(x, __shfl_xor_sync(0xffffffffu, x, d));
     return x;
   }
   __device__ __forceinline__ float sum(float x) const {
     return all(x, [](float a, float b) { return a + b; });
   }
   __device__ __forceinline__ float max(float x) const {  // passes over NaN
-    if constexpr (FULL) {
+    if constexpr (LPR == 32) {
       float y;
       asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
       return y;
@@ -65,68 +118,50 @@ struct Lanes {
       return all(x, [](float a, float b) { return fmaxf(a, b); });
     }
   }
-  // R sums at once.  Two values share one exchange: of x[0] and x[1] a lane
-  // keeps one and sends the other, so that R sums over 32 lanes cost about
-  // 2 R + 3 shuffles where R butterflies cost 5 R.
-  template <int R>
-  __device__ __forceinline__ void sums(float (&x)[R]) const {
-    if constexpr (FULL && R == 4) {
-      const int lane = threadIdx.x & 31;
-      const bool h = lane & 16, q = lane & 8;
-      float a = (h ? x[1] : x[0]) + __shfl_xor_sync(0xffffffffu, h ? x[0] : x[1], 16);
-      const float b = (h ? x[3] : x[2]) + __shfl_xor_sync(0xffffffffu, h ? x[2] : x[3], 16);
-      a = (q ? b : a) + __shfl_xor_sync(0xffffffffu, q ? a : b, 8);
-#pragma unroll
-      for (int d = 4; d > 0; d >>= 1) a += __shfl_xor_sync(0xffffffffu, a, d);
-      x[0] = __shfl_sync(0xffffffffu, a, 0);
-      x[1] = __shfl_sync(0xffffffffu, a, 16);
-      x[2] = __shfl_sync(0xffffffffu, a, 8);
-      x[3] = __shfl_sync(0xffffffffu, a, 24);
-    } else if constexpr (FULL && R == 2) {
-      const bool h = threadIdx.x & 16;
-      float a = (h ? x[1] : x[0]) + __shfl_xor_sync(0xffffffffu, h ? x[0] : x[1], 16);
-#pragma unroll
-      for (int d = 8; d > 0; d >>= 1) a += __shfl_xor_sync(0xffffffffu, a, d);
-      x[0] = __shfl_sync(0xffffffffu, a, 0);
-      x[1] = __shfl_sync(0xffffffffu, a, 16);
-    } else {
-#pragma unroll
-      for (int r = 0; r < R; ++r) x[r] = sum(x[r]);
-    }
-  }
+  // Does it hold on any lane of the row?
+  __device__ __forceinline__ bool any(bool x) const { return (__ballot_sync(0xffffffffu, x) & mask()) != 0; }
 };
 
-// Rows (of each lane group) that a warp works on at once: enough independent
-// loads in flight for HBM, within the registers.
+// Rows of a lane group that a warp works on at once: with few elements a lane,
+// several rows keep enough loads in flight for HBM.
 template <int VEC, int NV>
 constexpr int rows_at_once() {
   return VEC * NV <= 8 ? 4 : VEC * NV <= 16 ? 2 : 1;
+}
+
+// Blocks of 256 threads that a SM is to hold: two, but for the longest rows
+// (whose registers would spill).
+template <typename T, int VEC, int NV>
+constexpr int blocks_per_sm() {
+  return VEC * NV <= 16 || VEC == 8 ? 2 : 1;
 }
 
 // One row's elements of this lane.
 template <typename T, int VEC, int NV>
 struct RowRegs {
   static constexpr int N = VEC * NV;
-  // VEC == 1 rows skip the vectors that lie behind their end
-  static __device__ __forceinline__ bool used(int v, int lpr, int E) { return VEC > 1 || v * lpr < E; }
-  static __device__ __forceinline__ int elem(int v, int i, int lpr, int sub) { return (v * lpr + sub) * VEC + i; }
+  static __device__ __forceinline__ int elem(int n, int lpr, int sub) {
+    return (n / VEC * lpr + sub) * VEC + n % VEC;
+  }
 
   alignas(16) T raw[N];
 
-  __device__ __forceinline__ void load(const T* row, int E, int lpr, int sub, bool ok, T fill) {
+  __device__ __forceinline__ void fill(T x) {
+#pragma unroll
+    for (int n = 0; n < N; ++n) raw[n] = x;
+  }
+  // `row` is the row at this lane's first element, of which `room` = E - sub * VEC
+  // lie before the row's end.  Vectors behind it, and rows that are not loaded,
+  // keep what they hold.
+  __device__ __forceinline__ void load(const T* row, int room, int lpr, bool ok) {
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      const int e = elem(v, 0, lpr, sub);
+      if (!ok || v * lpr * VEC >= room) continue;
       if constexpr (VEC > 1) {
         static_assert(VEC * sizeof(T) == 16, "16-byte vectors");
-        if (ok && e < E) {
-          *reinterpret_cast<uint4*>(raw + v * VEC) = __ldg(reinterpret_cast<const uint4*>(row + e));
-        } else {
-#pragma unroll
-          for (int i = 0; i < VEC; ++i) raw[v * VEC + i] = fill;
-        }
+        *reinterpret_cast<uint4*>(raw + v * VEC) = __ldg(reinterpret_cast<const uint4*>(row + v * lpr * VEC));
       } else {
-        raw[v] = ok && e < E ? __ldg(row + e) : fill;
+        raw[v] = __ldg(row + v * lpr);
       }
     }
   }
@@ -151,34 +186,60 @@ struct RowRegs {
 
 // exp((x - m) / tau) as 2^(x c - m c), c = log2(e) / tau, in one FMA an element.
 // mc = m c is rounded, which leaves a factor 2^(m c - mc) on every element of the
-// row: `fix` takes it out of their sum (to first order: |m c - mc| < 2^-12).
-// Rows that lie farther out (masked with a large negative value, say) form x - m
-// first.
+// row: fix() takes it out of their sum (to first order: |m c - mc| < 2^-12).
+// Rows that lie farther out (`wide`: masked with a large negative value, say; or
+// infinite) form x - m first.
 struct RowExp {
-  float c, mc, m, fix;
-  bool wide;
-  __device__ __forceinline__ RowExp(float m_, float c_) : c(c_), m(m_) {
-    mc = m_ * c_;
-    wide = fabsf(mc) > 4096.f && fabsf(m_) < INFINITY;
-    fix = fabsf(mc) <= 4096.f ? fmaf(fmaf(m_, c_, -mc), -kLn2, 1.f) : 1.f;
+  float c, mc, m;
+  __device__ __forceinline__ RowExp(float m_, float c_) : c(c_), mc(m_ * c_), m(m_) {}
+  __device__ __forceinline__ bool wide() const { return !(fabsf(mc) <= 4096.f); }
+  __device__ __forceinline__ float fix() const { return wide() ? 1.f : fmaf(fmaf(m, c, -mc), -kLn2, 1.f); }
+  __device__ __forceinline__ float at(float x) const {
+    return exp2_fast(wide() ? (x - m) * c : fmaf(x, c, -mc));
   }
-  __device__ __forceinline__ float operator()(float x) const { return exp2_fast(fmaf(x, c, -mc)); }
-  __device__ __forceinline__ float far(float x) const { return exp2_fast((x - m) * c); }
+  // p = the exponentials of a lane's elements
+  template <typename Row>
+  __device__ __forceinline__ void row(const Row& r, float (&p)[Row::N]) const {
+    if (wide()) {
+#pragma unroll
+      for (int n = 0; n < Row::N; ++n) p[n] = exp2_fast((r[n] - m) * c);
+    } else {
+      pairwise<Row::N>(
+          [&](int n) {
+            const float2 x = fma2(make_float2(r[n], r[n + 1]), both(c), both(-mc));
+            p[n] = exp2_fast(x.x);
+            p[n + 1] = exp2_fast(x.y);
+          },
+          [&](int n) { p[n] = exp2_fast(fmaf(r[n], c, -mc)); });
+    }
+  }
 };
+template <int N>
+__device__ __forceinline__ float lane_sum(const float (&p)[N]) {
+  if constexpr (N == 1) {
+    return p[0];
+  } else {
+    float2 s = pair(p, 0);
+#pragma unroll
+    for (int n = 2; n < N; n += 2) s = add2(s, pair(p, n));
+    return s.x + s.y;
+  }
+}
 
-// Stores N values of a lane at `row` (16-byte vectors or single elements).
+// Stores a lane's values at `row` (as RowRegs::load has it), in 16-byte vectors
+// or single elements.
 template <typename T, int VEC, int NV>
-__device__ __forceinline__ void store_row(T* row, int E, int lpr, int sub, const float (&f)[VEC * NV]) {
+__device__ __forceinline__ void store_row(T* row, int room, int lpr, const float (&f)[VEC * NV]) {
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
-    const int e = (v * lpr + sub) * VEC;
-    if (e >= E) continue;
+    if (v * lpr * VEC >= room) continue;
     if constexpr (VEC == 8) {
-      *reinterpret_cast<uint4*>(row + e) = pack8<T>(f + v * VEC);
+      *reinterpret_cast<uint4*>(row + v * lpr * VEC) = pack8<T>(f + v * VEC);
     } else if constexpr (VEC == 4) {
-      *reinterpret_cast<float4*>(row + e) = make_float4(f[v * 4], f[v * 4 + 1], f[v * 4 + 2], f[v * 4 + 3]);
+      *reinterpret_cast<float4*>(row + v * lpr * VEC) =
+          make_float4(f[v * 4], f[v * 4 + 1], f[v * 4 + 2], f[v * 4 + 3]);
     } else {
-      row[e] = from_f32<T>(f[v]);
+      row[v * lpr] = from_f32<T>(f[v]);
     }
   }
 }
@@ -234,9 +295,13 @@ __device__ __forceinline__ void walk_sequences(const Seqs& q, int64_t a, int64_t
 }
 
 // ---- variants by row length ------------------------------------------------------
-// 16-byte vectors where every row starts on a 16-byte boundary, else single
-// elements; the fewest lanes that hold a row in one vector each, else 32 lanes
-// and more vectors.
+// Vectors of 16 bytes where every row starts on a 16-byte boundary: up to eight
+// lanes a row (a load then covers whole 128-byte lines), then up to 64 bytes of
+// 16-bit or FP32 logits a lane, then more lanes.  Few lanes a row make its
+// reductions and its scalar work cheap, since a warp does them for several rows
+// at once: a forward over 256 BF16 logits a row took 136 instructions a row with
+// a warp each and about half of it with eight lanes each.  Rows that start on
+// any element are read in single elements, 32 lanes a row.
 struct RowPlan {
   bool vec;
   int lpr;
@@ -248,34 +313,35 @@ inline RowPlan row_plan(const void* const* ptrs, int n_ptrs, moe_dtype dt, int E
   for (int i = 0; i < n_ptrs; ++i) vec = vec && reinterpret_cast<uintptr_t>(ptrs[i]) % 16 == 0;
   const int units = vec ? E * esz / 16 : E;
   RowPlan p{vec, 1, 1};
-  while (p.lpr < 32 && p.lpr < units) p.lpr *= 2;
+  while (p.lpr < (vec ? 8 : 32) && p.lpr < units) p.lpr *= 2;
+  while (p.nv < 4 && p.lpr * p.nv < units) p.nv *= 2;
+  while (p.lpr < 32 && p.lpr * p.nv < units) p.lpr *= 2;
   while (p.lpr * p.nv < units) p.nv *= 2;
   return p;
 }
 
-// Calls f.template run<T, VEC, NV, FULL>() for a plan.
+// Calls f.template run<T, VEC, NV, LPR>() for a plan.
 template <typename T, typename F>
 cudaError_t with_row_variant(const RowPlan& p, F&& f) {
   constexpr int V = 16 / sizeof(T);
   if (p.vec) {
-    if (p.lpr < 32) return f.template run<T, V, 1, false>();
-    switch (p.nv) {
-      case 1: return f.template run<T, V, 1, true>();
-      case 2: return f.template run<T, V, 2, true>();
-      case 4: return f.template run<T, V, 4, true>();
-      default:
-        if constexpr (V == 4) return f.template run<T, V, 8, true>();
-        return cudaErrorInvalidValue;
+    if (p.nv == 1) return f.template run<T, V, 1, 0>();
+    if (p.nv == 2) return f.template run<T, V, 2, 8>();
+    if (p.nv == 4) {
+      if (p.lpr == 8) return f.template run<T, V, 4, 8>();
+      if (p.lpr == 16) return f.template run<T, V, 4, 16>();
+      return f.template run<T, V, 4, 32>();
     }
+    if constexpr (V == 4) return f.template run<T, V, 8, 32>();
+    return cudaErrorInvalidValue;
   }
-  if (p.lpr < 32) return f.template run<T, 1, 1, false>();
   switch (p.nv) {
-    case 1: return f.template run<T, 1, 1, true>();
-    case 2: return f.template run<T, 1, 2, true>();
-    case 4: return f.template run<T, 1, 4, true>();
-    case 8: return f.template run<T, 1, 8, true>();
-    case 16: return f.template run<T, 1, 16, true>();
-    default: return f.template run<T, 1, 32, true>();
+    case 1: return f.template run<T, 1, 1, 0>();
+    case 2: return f.template run<T, 1, 2, 32>();
+    case 4: return f.template run<T, 1, 4, 32>();
+    case 8: return f.template run<T, 1, 8, 32>();
+    case 16: return f.template run<T, 1, 16, 32>();
+    default: return f.template run<T, 1, 32, 32>();
   }
 }
 template <typename F>
@@ -283,6 +349,11 @@ cudaError_t with_row_variant(moe_dtype dt, const RowPlan& p, F&& f) {
   if (dt == MOE_F32) return with_row_variant<float>(p, f);
   if (dt == MOE_F16) return with_row_variant<__half>(p, f);
   return with_row_variant<__nv_bfloat16>(p, f);
+}
+// Rows that a warp of a plan takes at once.
+inline int plan_batch(const RowPlan& p, moe_dtype dt) {
+  const int n = (p.vec ? 16 / (int)dtype_size(dt) : 1) * p.nv;
+  return (n <= 8 ? 4 : n <= 16 ? 2 : 1) * (32 / p.lpr);
 }
 
 // How a batch of rows is cut over blocks: `chunks` blocks of `rows` rows.
