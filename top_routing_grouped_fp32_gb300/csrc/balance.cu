@@ -92,7 +92,7 @@ __device__ __forceinline__ void row_scores(const Row& r, float m, float& shift, 
 template <typename T, int VEC, int NV, int LPR, bool SIG>
 __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, VEC, NV>()) balance_fwd_kernel(FwdArgs a) {
   extern __shared__ float smem[];
-  constexpr int N = VEC * NV, R = rows_at_once<VEC, NV>();
+  constexpr int N = VEC * NV, R = rows_at_once<T, VEC, NV>();
   constexpr int NI = 4;  // indices of a batch that a lane holds ahead of their use
   using Row = RowRegs<T, VEC, NV>;
   float* red = smem;                                                  // [kWarps][E]
@@ -126,18 +126,10 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, VEC, NV>()) balance
     int left = (int)(hi - t0);          // rows from there on (a block has far fewer than 2^31)
     const int64_t stride = (int64_t)kWarps * batch * a.E;
     const T* lp = static_cast<const T*>(a.logits) + (t0 + L.grp) * a.E + L.sub * VEC;
-    // which rows of a batch count, a bit for each r: known a batch before the rows are loaded
-    auto live = [&](int ahead) {
-      uint32_t bits = 0;
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        const int i = ahead * kWarps * batch + r * L.rows + L.grp;
-        bits |= (uint32_t)(i < left && (!a.mask || __ldg(a.mask + t0 + i))) << r;
-      }
-      return bits;
-    };
     Row cur[R], nxt[R];
-    uint32_t ok = live(0), ok1 = live(1);
+    LiveRows<R> live{a.mask, kWarps * batch, L.rows, L.grp};
+    uint32_t ok = live.now(t0, left, 0), ok1 = live.now(t0, left, 1);
+    live.fetch(t0, left, 2);
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       cur[r].fill(from_f32<T>(-INFINITY));
@@ -154,7 +146,8 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, VEC, NV>()) balance
       lp += stride;
 #pragma unroll
       for (int r = 0; r < R; ++r) nxt[r].load(lp + r * L.rows * a.E, room, L.lpr, ok1 >> r & 1u);
-      const uint32_t ok2 = live(2);
+      const uint32_t ok2 = live.bits(left, 2);
+      live.fetch(t0, left, 3);
 
       float mine_m = 0.f, mine_s = 0.f;  // the row that this lane writes the statistics of
 #pragma unroll
@@ -398,7 +391,7 @@ size_t balance_workspace_bytes(int64_t T, int E, int64_t num_seqs) {
 cudaError_t launch_balance_loss(const BalanceArgs& b, void* ws, uint32_t* status, cudaStream_t s) {
   const void* ptrs[] = {b.logits};
   const RowPlan plan = row_plan(ptrs, 1, b.dt, b.E);
-  const Chunks ch = cut_rows(b.T, plan_batch(plan, b.dt), kMaxChunks);
+  const Chunks ch = cut_rows(b.T, plan_batch(plan), kMaxChunks);
   const size_t slots = slot_count(b.T, b.num_seqs);
   Partials part;
   part.p = static_cast<float*>(ws);

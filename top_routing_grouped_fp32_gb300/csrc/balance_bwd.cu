@@ -29,7 +29,7 @@ struct BwdArgs {
 
 template <typename T, int VEC, int NV, int LPR, bool SIG>
 __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, VEC, NV>()) balance_bwd_kernel(BwdArgs a) {
-  constexpr int N = VEC * NV, R = rows_at_once<VEC, NV>();
+  constexpr int N = VEC * NV, R = rows_at_once<T, VEC, NV>();
   using Row = RowRegs<T, VEC, NV>;
   pdl_wait();
   pdl_trigger();
@@ -162,7 +162,7 @@ struct LaunchBwd {
 cudaError_t launch_balance_loss_backward(const BalanceBwdArgs& b, cudaStream_t s) {
   const void* ptrs[] = {b.logits, b.base, b.dlogits};
   const RowPlan plan = row_plan(ptrs, 3, b.dt, b.E);
-  const Chunks ch = cut_rows(b.T, plan_batch(plan, b.dt), kMaxBlocks);
+  const Chunks ch = cut_rows(b.T, plan_batch(plan), kMaxBlocks);
   BwdArgs a{};
   a.logits = b.logits;
   a.row_stats = reinterpret_cast<const float2*>(b.row_stats);

@@ -74,9 +74,9 @@ struct FwdArgs {
 
 // Entries of a row's list that a lane keeps in registers; more are read again
 // where they are needed.
-template <int VEC, int NV>
+template <typename T, int VEC, int NV>
 constexpr int list_regs() {
-  return 4 / rows_at_once<VEC, NV>();
+  return 4 / rows_at_once<T, VEC, NV>();
 }
 
 // A row's lanes hold its logits and, entry sub, sub + lpr, .., its list.  Which of
@@ -86,7 +86,7 @@ constexpr int list_regs() {
 template <typename T, int VEC, int NV, int LPR>
 __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, VEC, NV>()) distill_fwd_kernel(FwdArgs a) {
   using Row = RowRegs<T, VEC, NV>;
-  constexpr int N = Row::N, R = rows_at_once<VEC, NV>(), J = list_regs<VEC, NV>();
+  constexpr int N = Row::N, R = rows_at_once<T, VEC, NV>(), J = list_regs<T, VEC, NV>();
   __shared__ uint32_t listed[kWarps][R][32];
   __shared__ float red_l[kWarps];
   __shared__ uint32_t red_n[kWarps], red_b[kWarps];
@@ -99,11 +99,11 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, VEC, NV>()) distill
   const int batch = R * L.rows;
   const int lpr_log = 31 - __clz(L.lpr);
 
+  float* const own_stat = L.sub == 0 ? a.row_loss : a.row_stats + (L.sub - 1) * a.T;
   auto write_row = [&](int64_t t, float kl, float m, float s, float mt, float st, float ratio) {
-    for (int f = L.sub; f < 6; f += L.lpr) {
-      const float v = f == 0 ? kl : f == 1 ? m : f == 2 ? s : f == 3 ? mt : f == 4 ? st : ratio;
-      (f == 0 ? a.row_loss : a.row_stats + (f - 1) * a.T)[t] = v;
-    }
+    auto value = [&](int f) { return f == 0 ? kl : f == 1 ? m : f == 2 ? s : f == 3 ? mt : f == 4 ? st : ratio; };
+    if (L.sub < 6) own_stat[t] = value(L.sub);
+    for (int f = L.sub + L.lpr; f < 6; f += L.lpr) a.row_stats[(f - 1) * a.T + t] = value(f);
   };
   auto gap = [&](int64_t lo, int64_t hi) {
     for (int64_t t = lo + threadIdx.x; t < hi; t += kThreads) {
@@ -119,37 +119,32 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, VEC, NV>()) distill
     int left = (int)(hi - t0);
     const int64_t stride = (int64_t)kWarps * batch * a.E;
     const T* lp = static_cast<const T*>(a.logits) + (t0 + L.grp) * a.E + L.sub * VEC;
-    auto live = [&](int ahead) {
-      uint32_t bits = 0;
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        const int i = ahead * kWarps * batch + r * L.rows + L.grp;
-        bits |= (uint32_t)(i < left && (!a.mask || __ldg(a.mask + t0 + i))) << r;
-      }
-      return bits;
-    };
-    // entry j of the list of the r-th row, `ahead` batches on
-    auto entry = [&](int64_t t, int j, float& x, uint32_t& e) {
-      x = load_dyn(a.t_logits, a.t_dt, (size_t)(t * a.m + j));
-      e = __ldg(a.t_idx + t * a.m + j);
-    };
+    // this lane's entries of the rows' lists (a row's lanes hold entries sub, sub + lpr, ..)
+    const ListEntries list{a.t_logits, a.t_idx, a.t_dt};
+    int64_t li = (t0 + L.grp) * a.m + L.sub;
     Row cur[R], nxt[R];
-    float x[R][J], x1[R][J], rest[R], rest1[R];
-    uint32_t e[R][J], e1[R][J];
-    auto lists = [&](int ahead, uint32_t on, float (&x)[R][J], uint32_t (&e)[R][J], float (&rest)[R]) {
+    float rest[R], rest1[R];
+    uint32_t x[R][J], x1[R][J], e[R][J], e1[R][J];
+    auto lists = [&](int ahead, uint32_t on, uint32_t (&x)[R][J], uint32_t (&e)[R][J], float (&rest)[R]) {
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        const int64_t t = t0 + ahead * kWarps * batch + r * L.rows + L.grp;
-        rest[r] = (on >> r & 1u) && a.t_rest ? __ldg(a.t_rest + t) : -INFINITY;
+        const int i = ahead * kWarps * batch + r * L.rows;
+        rest[r] = (on >> r & 1u) && a.t_rest ? __ldg(a.t_rest + t0 + i + L.grp) : -INFINITY;
 #pragma unroll
         for (int j = 0; j < J; ++j) {
-          x[r][j] = -INFINITY;
+          if (j * L.lpr >= a.m) break;
+          x[r][j] = list.none();
           e[r][j] = 0u;
-          if ((on >> r & 1u) && L.sub + j * L.lpr < a.m) entry(t, L.sub + j * L.lpr, x[r][j], e[r][j]);
+          if ((on >> r & 1u) && L.sub + j * L.lpr < a.m) {
+            x[r][j] = list.bits(li + i * a.m + j * L.lpr);
+            e[r][j] = list.expert(li + i * a.m + j * L.lpr);
+          }
         }
       }
     };
-    uint32_t on = live(0), on1 = live(1);
+    LiveRows<R> live{a.mask, kWarps * batch, L.rows, L.grp};
+    uint32_t on = live.now(t0, left, 0), on1 = live.now(t0, left, 1);
+    live.fetch(t0, left, 2);
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       cur[r].fill(from_f32<T>(-INFINITY));
@@ -162,7 +157,8 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, VEC, NV>()) distill
 #pragma unroll
       for (int r = 0; r < R; ++r) nxt[r].load(lp + r * L.rows * a.E, room, L.lpr, on1 >> r & 1u);
       lists(1, on1, x1, e1, rest1);
-      const uint32_t on2 = live(2);
+      const uint32_t on2 = live.bits(left, 2);
+      live.fetch(t0, left, 3);
 #pragma unroll
       for (int r = 0; r < R; ++r) listed[warp][r][lane] = 0u;
       __syncwarp();
@@ -173,14 +169,14 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, VEC, NV>()) distill
         // calls f(x, e) for this lane's entries that are there
         auto each = [&](auto f) {
 #pragma unroll
-          for (int j = 0; j < J; ++j)
-            if (x[r][j] != -INFINITY) f(x[r][j], e[r][j]);
+          for (int j = 0; j < J; ++j) {
+            if (j * L.lpr >= a.m) break;
+            if (x[r][j] != list.none()) f(list.value(x[r][j]), e[r][j]);
+          }
           if (ok)
             for (int j = L.sub + J * L.lpr; j < a.m; j += L.lpr) {
-              float xx;
-              uint32_t ee;
-              entry(t, j, xx, ee);
-              if (xx != -INFINITY) f(xx, ee);
+              const uint32_t b = list.bits(t * a.m + j);
+              if (b != list.none()) f(list.value(b), list.expert(t * a.m + j));
             }
         };
         // the teacher's maximum, and the bits of the list's experts
@@ -207,7 +203,8 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, VEC, NV>()) distill
           float p[N], odd = 0.f;
           ex.row(cur[r], p);
 #pragma unroll
-          for (int n = 0; n < N; ++n) (n % 2 ? odd : out) += mine >> n & 1u ? 0.f : p[n];
+          for (int n = 0; n < N; ++n)
+            if (!(mine & (1u << n))) (n % 2 ? odd : out) += p[n];
           out += odd;
         }
         float st = L.sub == 0 ? exp2_fast((rest[r] - mt) * a.c) : 0.f, sp = 0.f;
@@ -224,15 +221,18 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, VEC, NV>()) distill
         float ln_out = log2_fast(out * fix) * kLn2;
         const bool far = ok && a.t_rest && out < kFarBelow;
         if (far) {
-          float mo = -INFINITY;
-#pragma unroll
-          for (int n = 0; n < N; ++n)
-            if (!(mine >> n & 1u)) mo = fmaxf(mo, cur[r][n]);
+          auto outside = [&](int el) {
+            const int q = el / VEC;
+            return !(words[q & (L.lpr - 1)] >> ((q >> lpr_log) * VEC + el % VEC) & 1u);
+          };
+          float mo = -INFINITY, so = 0.f;
+#pragma unroll 1
+          for (int el = L.sub; el < a.E; el += L.lpr)
+            if (outside(el)) mo = fmaxf(mo, to_f32<T>(__ldg(row + el)));
           for (int d = L.lpr / 2; d > 0; d >>= 1) mo = fmaxf(mo, __shfl_xor_sync(L.mask(), mo, d));
-          float so = 0.f;
-#pragma unroll
-          for (int n = 0; n < N; ++n)
-            if (!(mine >> n & 1u)) so += exp2_fast((cur[r][n] - mo) * a.c);
+#pragma unroll 1
+          for (int el = L.sub; el < a.E; el += L.lpr)
+            if (outside(el)) so += exp2_fast((to_f32<T>(__ldg(row + el)) - mo) * a.c);
           for (int d = L.lpr / 2; d > 0; d >>= 1) so += __shfl_xor_sync(L.mask(), so, d);
           ln_out = mo == -INFINITY ? -INFINITY : (mo - m) * a.inv_tau + logf(so);
         }
@@ -276,6 +276,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, VEC, NV>()) distill
       }
       on = on1, on1 = on2;
       t0 += kWarps * batch;
+      li += (int64_t)kWarps * batch * a.m;
       left -= kWarps * batch;
     }
 #pragma unroll
@@ -375,7 +376,7 @@ size_t distill_workspace_bytes(int64_t T, int64_t num_seqs) { return align_up(sl
 cudaError_t launch_distill_loss(const DistillArgs& d, void* ws, uint32_t* status, cudaStream_t s) {
   const void* ptrs[] = {d.logits};
   const RowPlan plan = row_plan(ptrs, 1, d.dt, d.E);
-  const Chunks ch = cut_rows(d.T, plan_batch(plan, d.dt), kMaxChunks);
+  const Chunks ch = cut_rows(d.T, plan_batch(plan), kMaxChunks);
   const size_t slots = slot_count(d.T, d.num_seqs);
   FwdArgs a{};
   a.logits = d.logits;

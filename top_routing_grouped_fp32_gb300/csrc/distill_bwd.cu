@@ -15,9 +15,9 @@ constexpr int kMaxBlocks = 304;  // two per SM
 
 // Entries of a row's list that a lane keeps in registers; more are read again
 // where they are needed.
-template <int VEC, int NV>
+template <typename T, int VEC, int NV>
 constexpr int list_regs() {
-  return 4 / rows_at_once<VEC, NV>();
+  return 4 / rows_at_once<T, VEC, NV>();
 }
 
 struct BwdArgs {
@@ -42,7 +42,7 @@ struct BwdArgs {
 template <typename T, int VEC, int NV, int LPR>
 __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, VEC, NV>()) distill_bwd_kernel(BwdArgs a) {
   using Row = RowRegs<T, VEC, NV>;
-  constexpr int N = Row::N, R = rows_at_once<VEC, NV>(), J = list_regs<VEC, NV>();
+  constexpr int N = Row::N, R = rows_at_once<T, VEC, NV>(), J = list_regs<T, VEC, NV>();
   constexpr int F = 5;  // statistics of a row
   extern __shared__ __align__(16) unsigned char row_smem[];
   pdl_wait();
@@ -78,21 +78,23 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, VEC, NV>()) distill
       return ok ? __ldg(a.row_stats + f * a.T + t) : 0.f;
     };
     auto sum_of = [&](float own) { return L.lpr >= 8 ? __shfl_sync(0xffffffffu, own, L.grp * L.lpr + 1) : own; };
-    auto entry = [&](int64_t t, int j, float& x, uint32_t& e) {
-      x = load_dyn(a.t_logits, a.t_dt, (size_t)(t * a.m + j));
-      e = __ldg(a.t_idx + t * a.m + j);
-    };
-    float x[R][J], x1[R][J], st[R], st1[R], s[R], s1[R];
-    uint32_t e[R][J], e1[R][J];
-    auto lists = [&](int ahead, const float (&s)[R], float (&x)[R][J], uint32_t (&e)[R][J]) {
+    const ListEntries list{a.t_logits, a.t_idx, a.t_dt};
+    int64_t li = (t0 + L.grp) * a.m + L.sub;
+    float st[R], st1[R], s[R], s1[R];
+    uint32_t x[R][J], x1[R][J], e[R][J], e1[R][J];
+    auto lists = [&](int ahead, const float (&s)[R], uint32_t (&x)[R][J], uint32_t (&e)[R][J]) {
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        const int64_t t = t0 + ahead * kWarps * batch + r * L.rows + L.grp;
+        const int64_t i = li + (int64_t)(ahead * kWarps * batch + r * L.rows) * a.m;
 #pragma unroll
         for (int j = 0; j < J; ++j) {
-          x[r][j] = -INFINITY;
+          if (j * L.lpr >= a.m) break;
+          x[r][j] = list.none();
           e[r][j] = 0u;
-          if (s[r] != 0.f && L.sub + j * L.lpr < a.m) entry(t, L.sub + j * L.lpr, x[r][j], e[r][j]);
+          if (s[r] != 0.f && L.sub + j * L.lpr < a.m) {
+            x[r][j] = list.bits(i + j * L.lpr);
+            e[r][j] = list.expert(i + j * L.lpr);
+          }
         }
       }
     };
@@ -131,43 +133,16 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, VEC, NV>()) distill
         // calls f(x, e) for this lane's entries that are there
         auto each = [&](auto f) {
 #pragma unroll
-          for (int j = 0; j < J; ++j)
-            if (x[r][j] != -INFINITY) f(x[r][j], e[r][j]);
+          for (int j = 0; j < J; ++j) {
+            if (j * L.lpr >= a.m) break;
+            if (x[r][j] != list.none()) f(list.value(x[r][j]), e[r][j]);
+          }
           if (ok)
             for (int j = L.sub + J * L.lpr; j < a.m; j += L.lpr) {
-              float xx;
-              uint32_t ee;
-              entry(t, j, xx, ee);
-              if (xx != -INFINITY) f(xx, ee);
+              const uint32_t b = list.bits(t * a.m + j);
+              if (b != list.none()) f(list.value(b), list.expert(t * a.m + j));
             }
         };
-        if (ratio < 0.f) {  // the shares of the rest about their own maximum
-          float mo = -INFINITY;
-#pragma unroll
-          for (int n = 0; n < N; ++n) {
-            const int el = Row::elem(n, L.lpr, L.sub);
-            bool in_list = el >= a.E;
-            for (int j = 0; j < a.m && !in_list; ++j) {
-              float xx;
-              uint32_t ee;
-              entry(t, j, xx, ee);
-              in_list = ee == (uint32_t)el && xx != -INFINITY;
-            }
-            d[n] = in_list ? -INFINITY : cur[r][n];
-            mo = fmaxf(mo, d[n]);
-          }
-          for (int k = L.lpr / 2; k > 0; k >>= 1) mo = fmaxf(mo, __shfl_xor_sync(L.mask(), mo, k));
-          float so = 0.f;
-#pragma unroll
-          for (int n = 0; n < N; ++n) {
-            d[n] = mo == -INFINITY ? 0.f : exp2_fast((d[n] - mo) * a.c);
-            so += d[n];
-          }
-          for (int k = L.lpr / 2; k > 0; k >>= 1) so += __shfl_xor_sync(L.mask(), so, k);
-          const float f = so > 0.f ? c * ratio / so : 0.f;
-#pragma unroll
-          for (int n = 0; n < N; ++n) d[n] *= f;
-        }
         if (!ok) {
 #pragma unroll
           for (int n = 0; n < N; ++n) d[n] = 0.f;
@@ -180,6 +155,32 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, VEC, NV>()) distill
         T* out = buf + r * L.rows * pitch;
         store_row<T, VEC, NV>(out + L.sub * VEC, room, L.lpr, d);
         __syncwarp();
+        if (ratio < 0.f) {  // -q_r: the shares of the rest about their own maximum
+          auto listed = [&](int el) {
+#pragma unroll 1
+            for (int j = 0; j < a.m; ++j)
+              if (list.expert(t * a.m + j) == (uint32_t)el && list.bits(t * a.m + j) != list.none()) return true;
+            return false;
+          };
+          const T* row = lp + r * L.rows * a.E;
+          float mo = -INFINITY, so = 0.f;
+#pragma unroll 1
+          for (int el = L.sub; el < a.E; el += L.lpr)
+            if (!listed(el)) mo = fmaxf(mo, to_f32<T>(__ldg(row + el)));
+          for (int k = L.lpr / 2; k > 0; k >>= 1) mo = fmaxf(mo, __shfl_xor_sync(L.mask(), mo, k));
+#pragma unroll 1
+          for (int el = L.sub; el < a.E; el += L.lpr)
+            if (!listed(el)) so += exp2_fast((to_f32<T>(__ldg(row + el)) - mo) * a.c);
+          for (int k = L.lpr / 2; k > 0; k >>= 1) so += __shfl_xor_sync(L.mask(), so, k);
+#pragma unroll 1
+          for (int el = L.sub; el < a.E; el += L.lpr) {
+            // nothing outside but -inf: no share to give
+            float g = mo == -INFINITY ? 0.f : c * ratio / so * exp2_fast((to_f32<T>(__ldg(row + el)) - mo) * a.c);
+            if (a.base) g += to_f32<T>(__ldg(bp + r * L.rows * a.E + el));
+            out[el] = from_f32<T>(g);  // the list's are overwritten below
+          }
+          __syncwarp(L.mask());
+        }
         const float qs = c * rcp_fast(sum_t);
         each([&](float xx, uint32_t ee) {
           if (ee >= (uint32_t)a.E) return;  // the row is NaN already
@@ -213,6 +214,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, VEC, NV>()) distill
       bp += stride;
       op += stride;
       t0 += kWarps * batch;
+      li += (int64_t)kWarps * batch * a.m;
       left -= kWarps * batch;
     }
   };
@@ -236,7 +238,7 @@ struct LaunchBwd {
 cudaError_t launch_distill_loss_backward(const DistillBwdArgs& d, cudaStream_t s) {
   const void* ptrs[] = {d.logits, d.base, d.dlogits};
   const RowPlan plan = row_plan(ptrs, 3, d.dt, d.E);
-  const int batch = plan_batch(plan, d.dt);
+  const int batch = plan_batch(plan);
   const Chunks ch = cut_rows(d.T, batch, kMaxBlocks);
   BwdArgs a{};
   a.logits = d.logits;

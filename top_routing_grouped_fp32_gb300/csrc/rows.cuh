@@ -123,10 +123,11 @@ struct Lanes {
 };
 
 // Rows of a lane group that a warp works on at once: with few elements a lane,
-// several rows keep enough loads in flight for HBM.
-template <int VEC, int NV>
+// several rows keep enough loads in flight for HBM (64 bytes a lane).
+template <typename T, int VEC, int NV>
 constexpr int rows_at_once() {
-  return VEC * NV <= 8 ? 4 : VEC * NV <= 16 ? 2 : 1;
+  constexpr int bytes = VEC == 1 ? NV * 4 : VEC * NV * (int)sizeof(T);
+  return bytes <= 16 ? 4 : bytes <= 32 ? 2 : 1;
 }
 
 // Blocks of 256 threads that a SM is to hold: two, but for the longest rows
@@ -226,6 +227,27 @@ __device__ __forceinline__ float lane_sum(const float (&p)[N]) {
   }
 }
 
+// A teacher's list in its own dtype.  An entry is kept as it was loaded (bits) and
+// converted where it is used: a conversion next to the load would wait for it.
+struct ListEntries {
+  const void* logits;
+  const uint32_t* idx;
+  int dt;
+  __device__ __forceinline__ uint32_t bits(int64_t i) const {
+    if (dt == MOE_F32) return __ldg(static_cast<const uint32_t*>(logits) + i);
+    return __ldg(static_cast<const uint16_t*>(logits) + i);
+  }
+  __device__ __forceinline__ uint32_t expert(int64_t i) const { return __ldg(idx + i); }
+  // bits of -inf: no entry
+  __device__ __forceinline__ uint32_t none() const {
+    return dt == MOE_F32 ? 0xff800000u : dt == MOE_F16 ? 0xfc00u : 0xff80u;
+  }
+  __device__ __forceinline__ float value(uint32_t b) const {
+    if (dt == MOE_F16) return __half2float(__ushort_as_half((unsigned short)b));
+    return __uint_as_float(dt == MOE_F32 ? b : b << 16);
+  }
+};
+
 // Stores a lane's values at `row` (as RowRegs::load has it), in 16-byte vectors
 // or single elements.
 template <typename T, int VEC, int NV>
@@ -294,6 +316,34 @@ __device__ __forceinline__ void walk_sequences(const Seqs& q, int64_t a, int64_t
   }
 }
 
+// Which rows of a warp's batch count: bit r for the r-th row of each lane group.
+// The mask's bytes are fetched a batch before their bits are needed.
+template <int R>
+struct LiveRows {
+  const uint8_t* mask;
+  int step, rows, grp;  // rows between a warp's batches, rows per warp, this lane's group
+  uint8_t byte[R];
+  __device__ __forceinline__ void fetch(int64_t t0, int left, int ahead) {
+    if (!mask) return;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int i = ahead * step + r * rows + grp;
+      byte[r] = i < left ? __ldg(mask + t0 + i) : 0;
+    }
+  }
+  __device__ __forceinline__ uint32_t bits(int left, int ahead) const {
+    uint32_t b = 0;
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+      b |= (uint32_t)(ahead * step + r * rows + grp < left && (!mask || byte[r])) << r;
+    return b;
+  }
+  __device__ __forceinline__ uint32_t now(int64_t t0, int left, int ahead) {
+    fetch(t0, left, ahead);
+    return bits(left, ahead);
+  }
+};
+
 // ---- variants by row length ------------------------------------------------------
 // Vectors of 16 bytes where every row starts on a 16-byte boundary: up to eight
 // lanes a row (a load then covers whole 128-byte lines), then up to 64 bytes of
@@ -351,9 +401,9 @@ cudaError_t with_row_variant(moe_dtype dt, const RowPlan& p, F&& f) {
   return with_row_variant<__nv_bfloat16>(p, f);
 }
 // Rows that a warp of a plan takes at once.
-inline int plan_batch(const RowPlan& p, moe_dtype dt) {
-  const int n = (p.vec ? 16 / (int)dtype_size(dt) : 1) * p.nv;
-  return (n <= 8 ? 4 : n <= 16 ? 2 : 1) * (32 / p.lpr);
+inline int plan_batch(const RowPlan& p) {
+  const int bytes = p.nv * (p.vec ? 16 : 4);
+  return (bytes <= 16 ? 4 : bytes <= 32 ? 2 : 1) * (32 / p.lpr);
 }
 
 // How a batch of rows is cut over blocks: `chunks` blocks of `rows` rows.
