@@ -88,6 +88,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, VEC, NV>()) distill
   using Row = RowRegs<T, VEC, NV>;
   constexpr int N = Row::N, R = rows_at_once<T, VEC, NV>(), J = list_regs<T, VEC, NV>();
   __shared__ uint32_t listed[kWarps][R][32];
+  extern __shared__ __align__(16) unsigned char row_smem[];  // the batch's rows, for the lists' lanes
   __shared__ float red_l[kWarps];
   __shared__ uint32_t red_n[kWarps], red_b[kWarps];
   pdl_wait();
@@ -98,6 +99,8 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, VEC, NV>()) distill
   const int room = a.E - L.sub * VEC;
   const int batch = R * L.rows;
   const int lpr_log = 31 - __clz(L.lpr);
+  const int pitch = (int)align_up((size_t)a.E * sizeof(T), 16) / (int)sizeof(T);
+  T* const copy = reinterpret_cast<T*>(row_smem) + (warp * batch + L.grp) * pitch;  // r-th row: + r * rows * pitch
 
   float* const own_stat = L.sub == 0 ? a.row_loss : a.row_stats + (L.sub - 1) * a.T;
   auto write_row = [&](int64_t t, float kl, float m, float s, float mt, float st, float ratio) {
@@ -160,19 +163,18 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, VEC, NV>()) distill
       const uint32_t on2 = live.bits(left, 2);
       live.fetch(t0, left, 3);
 #pragma unroll
-      for (int r = 0; r < R; ++r) listed[warp][r][lane] = 0u;
+      for (int r = 0; r < R; ++r) {
+        listed[warp][r][lane] = 0u;
+        cur[r].keep(copy + r * L.rows * pitch + L.sub * VEC, room, L.lpr);
+      }
       __syncwarp();
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         const int64_t t = t0 + r * L.rows + L.grp;
         bool ok = on >> r & 1u;
-        // calls f(x, e) for this lane's entries that are there
-        auto each = [&](auto f) {
-#pragma unroll
-          for (int j = 0; j < J; ++j) {
-            if (j * L.lpr >= a.m) break;
-            if (x[r][j] != list.none()) f(list.value(x[r][j]), e[r][j]);
-          }
+        const T* row = copy + r * L.rows * pitch;
+        // calls f(x, e) for this lane's entries behind those in registers
+        auto others = [&](auto f) {
           if (ok)
             for (int j = L.sub + J * L.lpr; j < a.m; j += L.lpr) {
               const uint32_t b = list.bits(t * a.m + j);
@@ -183,12 +185,22 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, VEC, NV>()) distill
         float mt = rest[r];
         bool nan = rest[r] != rest[r] || rest[r] == INFINITY, bad = false;
         uint32_t* words = &listed[warp][r][L.grp * L.lpr];
-        each([&](float xx, uint32_t ee) {
+        auto note = [&](float xx, uint32_t ee) {
           mt = fmaxf(mt, xx);  // passes over NaN
           nan |= xx != xx || xx == INFINITY;
           const uint32_t q = ee / VEC, bit = 1u << ((q >> lpr_log) * VEC + ee % VEC);
           if (ee >= (uint32_t)a.E || (atomicOr(words + (q & (L.lpr - 1)), bit) & bit)) bad = true;
-        });
+        };
+        float xs[J], ys[J];  // an entry that is not there has xs = -inf
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+          xs[j] = -INFINITY;
+          if (j * L.lpr >= a.m) break;
+          xs[j] = list.value(x[r][j]);
+          ys[j] = to_f32<T>(row[min(e[r][j], (uint32_t)a.E - 1u)]);
+          if (xs[j] != -INFINITY) note(xs[j], e[r][j]);
+        }
+        others(note);
         mt = L.max(mt);
         nan = L.any(nan);
         bad = L.any(bad);
@@ -207,11 +219,20 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, VEC, NV>()) distill
             if (!(mine & (1u << n))) (n % 2 ? odd : out) += p[n];
           out += odd;
         }
-        float st = L.sub == 0 ? exp2_fast((rest[r] - mt) * a.c) : 0.f, sp = 0.f;
-        const T* row = static_cast<const T*>(a.logits) + t * a.E;
-        each([&](float xx, uint32_t ee) {
+        const float eq_rest = exp2_fast((rest[r] - mt) * a.c);
+        float st = L.sub == 0 ? eq_rest : 0.f, sp = 0.f;
+        float eq[J], ep[J];
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+          if (j * L.lpr >= a.m) break;
+          eq[j] = exp2_fast((xs[j] - mt) * a.c);
+          ep[j] = xs[j] != -INFINITY ? ex.at(ys[j]) : 0.f;
+          st += eq[j];
+          sp += ep[j];
+        }
+        others([&](float xx, uint32_t ee) {
           st += exp2_fast((xx - mt) * a.c);
-          if (ee < (uint32_t)a.E) sp += ex.at(to_f32<T>(__ldg(row + ee)));
+          if (ee < (uint32_t)a.E) sp += ex.at(to_f32<T>(row[ee]));
         });
         out = L.sum(out);
         st = L.sum(st);
@@ -228,11 +249,11 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, VEC, NV>()) distill
           float mo = -INFINITY, so = 0.f;
 #pragma unroll 1
           for (int el = L.sub; el < a.E; el += L.lpr)
-            if (outside(el)) mo = fmaxf(mo, to_f32<T>(__ldg(row + el)));
+            if (outside(el)) mo = fmaxf(mo, to_f32<T>(row[el]));
           for (int d = L.lpr / 2; d > 0; d >>= 1) mo = fmaxf(mo, __shfl_xor_sync(L.mask(), mo, d));
 #pragma unroll 1
           for (int el = L.sub; el < a.E; el += L.lpr)
-            if (outside(el)) so += exp2_fast((to_f32<T>(__ldg(row + el)) - mo) * a.c);
+            if (outside(el)) so += exp2_fast((to_f32<T>(row[el]) - mo) * a.c);
           for (int d = L.lpr / 2; d > 0; d >>= 1) so += __shfl_xor_sync(L.mask(), so, d);
           ln_out = mo == -INFINITY ? -INFINITY : (mo - m) * a.inv_tau + logf(so);
         }
@@ -240,15 +261,21 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, VEC, NV>()) distill
         const float inv_s = rcp_fast(s0), inv_st = rcp_fast(st);
         const float dz = (log2_fast(s) - log2_fast(st)) * kLn2;
         float kl = 0.f, ratio = 0.f;
-        if (ok)
-          each([&](float xx, uint32_t ee) {
-            if (ee >= (uint32_t)a.E) return;
-            const float y = to_f32<T>(__ldg(row + ee));
-            kl += kl_term(exp2_fast((xx - mt) * a.c) * inv_st, ex.at(y) * inv_s,
-                          ((xx - mt) - (y - m)) * a.inv_tau + dz);
-          });
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+          if (j * L.lpr >= a.m) break;
+          const float term =
+              kl_term(eq[j] * inv_st, ep[j] * inv_s, ((xs[j] - mt) - (ys[j] - m)) * a.inv_tau + dz);
+          kl += xs[j] != -INFINITY ? term : 0.f;
+        }
+        others([&](float xx, uint32_t ee) {
+          if (ee >= (uint32_t)a.E) return;
+          const float y = to_f32<T>(row[ee]);
+          kl += kl_term(exp2_fast((xx - mt) * a.c) * inv_st, ex.at(y) * inv_s,
+                        ((xx - mt) - (y - m)) * a.inv_tau + dz);
+        });
         if (a.t_rest) {
-          const float q = exp2_fast((rest[r] - mt) * a.c) * inv_st, p = out * inv_s;
+          const float q = eq_rest * inv_st, p = out * inv_s;
           if (L.sub == 0) kl += kl_term(q, p, (rest[r] - mt) * a.inv_tau - ln_out + dz);
           ratio = far ? -q : q * rcp_fast(p);
         } else if (L.sub == 0) {
@@ -402,7 +429,8 @@ cudaError_t launch_distill_loss(const DistillArgs& d, void* ws, uint32_t* status
   a.row_loss = d.row_loss;
   a.row_stats = d.row_stats;
   a.status = status;
-  LaunchFwd f{a, ch.chunks, 0, s};
+  const size_t smem = (size_t)kWarps * plan_batch(plan) * align_up((size_t)d.E * dtype_size(d.dt), 16);
+  LaunchFwd f{a, ch.chunks, smem, s};
   const cudaError_t e = with_row_variant(d.dt, plan, f);
   if (e != cudaSuccess || a.alone) return e;
   FinishArgs fin{a.part_loss, a.part_rows, a.part_bad, a.seqs, ch.rows, d.loss, d.tokens, status};

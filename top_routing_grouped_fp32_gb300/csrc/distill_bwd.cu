@@ -61,10 +61,9 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, VEC, NV>()) distill
     int64_t t0 = lo + warp * batch;
     int left = (int)(hi - t0);
     const int64_t stride = (int64_t)kWarps * batch * a.E;
-    const int64_t at = (t0 + L.grp) * a.E;
-    const T* lp = static_cast<const T*>(a.logits) + at;
-    const T* bp = static_cast<const T*>(a.base) + at;
-    T* op = static_cast<T*>(a.out) + at;
+    int64_t at = (t0 + L.grp) * a.E;  // this group's first row of the batch, in elements
+    const T* const logits = static_cast<const T*>(a.logits);
+    const T* const base = static_cast<const T*>(a.base);
     Row cur[R], nxt[R];
     // statistics: lane sub = f holds the f-th (rows of eight lanes or more), or
     // the sum alone, which says whether the row counts
@@ -105,7 +104,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, VEC, NV>()) distill
       s[r] = sum_of(st[r]);
       cur[r].fill(from_f32<T>(-INFINITY));
       nxt[r].fill(from_f32<T>(-INFINITY));
-      cur[r].load(lp + L.sub * VEC + r * L.rows * a.E, room, L.lpr, s[r] != 0.f);
+      cur[r].load(logits + at + (L.sub * VEC + r * L.rows * a.E), room, L.lpr, s[r] != 0.f);
     }
     lists(0, s, x, e);
     while (left > 0) {
@@ -113,7 +112,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, VEC, NV>()) distill
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         s1[r] = sum_of(st1[r]);
-        nxt[r].load(lp + stride + L.sub * VEC + r * L.rows * a.E, room, L.lpr, s1[r] != 0.f);
+        nxt[r].load(logits + at + stride + (L.sub * VEC + r * L.rows * a.E), room, L.lpr, s1[r] != 0.f);
         st2[r] = stats(2, r);
       }
       lists(1, s1, x1, e1);
@@ -125,34 +124,41 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, VEC, NV>()) distill
         const float m = stat(st[r], t, ok, 0), mt = stat(st[r], t, ok, 2), sum_t = stat(st[r], t, ok, 3),
                     ratio = stat(st[r], t, ok, 4);
         const RowExp ex(m, a.c);
-        const float ps = c * rcp_fast(s[r]) * ex.fix();
+        const float ps = c * rcp_fast(s[r]) * ex.fix(), qs = c * rcp_fast(sum_t);
+        T* out = buf + r * L.rows * pitch;
+        // the list's gradients, from the row's logits (and then the base's elements)
+        // laid out in shared memory
+        cur[r].keep(out + L.sub * VEC, room, L.lpr);
+        __syncwarp();
+        float gs[J];
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+          if (j * L.lpr >= a.m) break;
+          gs[j] = ex.at(to_f32<T>(out[min(e[r][j], (uint32_t)a.E - 1u)])) * ps -
+                  exp2_fast((list.value(x[r][j]) - mt) * a.c) * qs;
+        }
         float d[N];
         ex.row(cur[r], d);
         const float w = ps * (1.f - ratio);
         pairwise<N>([&](int n) { put(d, n, mul2(pair(d, n), both(w))); }, [&](int n) { d[n] *= w; });
-        // calls f(x, e) for this lane's entries that are there
-        auto each = [&](auto f) {
-#pragma unroll
-          for (int j = 0; j < J; ++j) {
-            if (j * L.lpr >= a.m) break;
-            if (x[r][j] != list.none()) f(list.value(x[r][j]), e[r][j]);
-          }
-          if (ok)
-            for (int j = L.sub + J * L.lpr; j < a.m; j += L.lpr) {
-              const uint32_t b = list.bits(t * a.m + j);
-              if (b != list.none()) f(list.value(b), list.expert(t * a.m + j));
-            }
-        };
         if (!ok) {
 #pragma unroll
           for (int n = 0; n < N; ++n) d[n] = 0.f;
         }
         if (a.base) {  // into the logits' registers (vectors behind the row's end stay)
-          cur[r].load(bp + L.sub * VEC + r * L.rows * a.E, room, L.lpr, in);
+          cur[r].load(base + at + (L.sub * VEC + r * L.rows * a.E), room, L.lpr, in);
 #pragma unroll
           for (int n = 0; n < N; ++n) d[n] += cur[r][n];
+          __syncwarp();
+          cur[r].keep(out + L.sub * VEC, room, L.lpr);
+          __syncwarp();
+#pragma unroll
+          for (int j = 0; j < J; ++j) {
+            if (j * L.lpr >= a.m) break;
+            gs[j] += to_f32<T>(out[min(e[r][j], (uint32_t)a.E - 1u)]);
+          }
         }
-        T* out = buf + r * L.rows * pitch;
+        __syncwarp();
         store_row<T, VEC, NV>(out + L.sub * VEC, room, L.lpr, d);
         __syncwarp();
         if (ratio < 0.f) {  // -q_r: the shares of the rest about their own maximum
@@ -162,7 +168,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, VEC, NV>()) distill
               if (list.expert(t * a.m + j) == (uint32_t)el && list.bits(t * a.m + j) != list.none()) return true;
             return false;
           };
-          const T* row = lp + r * L.rows * a.E;
+          const T* row = logits + at + r * L.rows * a.E;
           float mo = -INFINITY, so = 0.f;
 #pragma unroll 1
           for (int el = L.sub; el < a.E; el += L.lpr)
@@ -176,25 +182,33 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, VEC, NV>()) distill
           for (int el = L.sub; el < a.E; el += L.lpr) {
             // nothing outside but -inf: no share to give
             float g = mo == -INFINITY ? 0.f : c * ratio / so * exp2_fast((to_f32<T>(__ldg(row + el)) - mo) * a.c);
-            if (a.base) g += to_f32<T>(__ldg(bp + r * L.rows * a.E + el));
+            if (a.base) g += to_f32<T>(__ldg(base + at + r * L.rows * a.E + el));
             out[el] = from_f32<T>(g);  // the list's are overwritten below
           }
           __syncwarp(L.mask());
         }
-        const float qs = c * rcp_fast(sum_t);
-        each([&](float xx, uint32_t ee) {
-          if (ee >= (uint32_t)a.E) return;  // the row is NaN already
-          float g = ex.at(to_f32<T>(__ldg(lp + r * L.rows * a.E + ee))) * ps - exp2_fast((xx - mt) * a.c) * qs;
-          if (a.base) g += to_f32<T>(__ldg(bp + r * L.rows * a.E + ee));
-          out[ee] = from_f32<T>(g);
-        });
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+          if (j * L.lpr >= a.m) break;
+          if (x[r][j] != list.none() && e[r][j] < (uint32_t)a.E)  // (an expert that is none: the row is NaN)
+            out[e[r][j]] = from_f32<T>(gs[j]);
+        }
+        if (ok)
+          for (int j = L.sub + J * L.lpr; j < a.m; j += L.lpr) {
+            const uint32_t b = list.bits(t * a.m + j), ee = list.expert(t * a.m + j);
+            if (b == list.none() || ee >= (uint32_t)a.E) continue;
+            float g = ex.at(to_f32<T>(__ldg(logits + at + r * L.rows * a.E + ee))) * ps -
+                      exp2_fast((list.value(b) - mt) * a.c) * qs;
+            if (a.base) g += to_f32<T>(__ldg(base + at + r * L.rows * a.E + ee));
+            out[ee] = from_f32<T>(g);
+          }
       }
       __syncwarp();
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         if (r * L.rows + L.grp < left) {
           const T* from = buf + r * L.rows * pitch + L.sub * VEC;
-          T* to = op + r * L.rows * a.E + L.sub * VEC;
+          T* to = static_cast<T*>(a.out) + at + (L.sub * VEC + r * L.rows * a.E);
 #pragma unroll
           for (int v = 0; v < NV; ++v) {
             if (v * L.lpr * VEC >= room) continue;
@@ -210,9 +224,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, VEC, NV>()) distill
         for (int j = 0; j < J; ++j) x[r][j] = x1[r][j], e[r][j] = e1[r][j];
       }
       __syncwarp();  // before the next batch is laid out
-      lp += stride;
-      bp += stride;
-      op += stride;
+      at += stride;
       t0 += kWarps * batch;
       li += (int64_t)kWarps * batch * a.m;
       left -= kWarps * batch;

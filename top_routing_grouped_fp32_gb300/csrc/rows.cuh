@@ -167,6 +167,17 @@ struct RowRegs {
     }
   }
   __device__ __forceinline__ float operator[](int n) const { return to_f32<T>(raw[n]); }
+  // Lays the elements out in shared memory, as load() has them.
+  __device__ __forceinline__ void keep(T* row, int room, int lpr) const {
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      if (v * lpr * VEC >= room) continue;
+      if constexpr (VEC > 1)
+        *reinterpret_cast<uint4*>(row + v * lpr * VEC) = *reinterpret_cast<const uint4*>(raw + v * VEC);
+      else
+        row[v * lpr] = raw[v];
+    }
+  }
 
   // This lane's maximum; passes over NaN.
   __device__ __forceinline__ float lane_max() const {
