@@ -469,7 +469,7 @@ moe_status moe_router_backward(const void* logits, moe_dtype logits_dtype, const
  *   row_stats[t]     = (shift, sum), FP32 [T,2], 8-byte aligned: the row's
  *                      maximum and sum_e exp(l - maximum); for sigmoid scoring
  *                      0 and the sum of the sigmoids, or, where no logit
- *                      reaches -60, as for softmax; (0, 0) for rows that do
+ *                      reaches -20, as for softmax; (0, 0) for rows that do
  *                      not count.
  * A slot counts once however often its row names the expert; an index >= E is
  * counted nowhere and sets MOE_ERR_INVALID_INDEX in the status word.  A

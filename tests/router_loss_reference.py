@@ -64,7 +64,7 @@ def balance_row_stats(logits, scoring, mask=None, offsets=None):
         soft = torch.stack([m, torch.exp(l - m[:, None]).sum(1)], 1)
         if scoring == "sigmoid":
             sig = torch.stack([torch.zeros_like(m), torch.sigmoid(l).sum(1)], 1)
-            soft = torch.where((m >= -60)[:, None], sig, soft)
+            soft = torch.where((m >= -20)[:, None], sig, soft)
         st[rows] = soft
     return st
 

@@ -23,7 +23,6 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kMaxChunks = 304;    // blocks, and partials of a sequence: two per SM
 constexpr int kHistWords = 2048;   // copies of the block's histogram share this many words
 
 struct Partials {
@@ -67,8 +66,8 @@ struct FwdArgs {
 };
 
 // Sigmoid scores are normalised about 0, or about the row's maximum where all of
-// them are so small that their FP32 sum would lose them (sigmoid(l) = exp(l) there).
-constexpr float kFarBelow = -60.f;
+// them are so small that sigmoid(l) = exp(l) to FP32.
+constexpr float kFarBelow = -20.f;
 
 // Scores of a row about `shift`, not normalised.
 template <bool SIG, typename Row>
@@ -77,10 +76,14 @@ __device__ __forceinline__ void row_scores(const Row& r, float m, float& shift, 
     shift = 0.f;
     pairwise<Row::N>(
         [&](int n) {
+          // one reciprocal for two scores: 1/a = b / (a b).  2^63 bounds the product; a
+          // score below 2^-63 (its row's largest is above 1e-9) is 0, a NaN stays
+          auto cut = [](float q, float x) { return x <= 63.f ? q : x > 63.f ? 0.f : x; };
           const float2 x = mul2(make_float2(r[n], r[n + 1]), both(-kLog2e));
-          const float2 y = add2(make_float2(exp2_fast(x.x), exp2_fast(x.y)), both(1.f));
-          p[n] = rcp_fast(y.x);
-          p[n + 1] = rcp_fast(y.y);
+          const float2 y = add2(make_float2(exp2_fast(fminf(x.x, 63.f)), exp2_fast(fminf(x.y, 63.f))), both(1.f));
+          const float2 q = mul2(make_float2(y.y, y.x), both(rcp_fast(y.x * y.y)));
+          p[n] = cut(q.x, x.x);
+          p[n + 1] = cut(q.y, x.y);
         },
         [&](int n) { p[n] = rcp_fast(1.f + exp2_fast(r[n] * -kLog2e)); });
   } else {
@@ -91,12 +94,13 @@ __device__ __forceinline__ void row_scores(const Row& r, float m, float& shift, 
 
 template <typename T, int VEC, int NV, int LPR, bool SIG>
 __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, VEC, NV>()) balance_fwd_kernel(FwdArgs a) {
-  extern __shared__ float smem[];
-  constexpr int N = VEC * NV, R = rows_at_once<T, VEC, NV>();
-  constexpr int NI = 4;  // indices of a batch that a lane holds ahead of their use
-  using Row = RowRegs<T, VEC, NV>;
-  float* red = smem;                                                  // [kWarps][E]
-  uint32_t* hist = reinterpret_cast<uint32_t*>(smem + kWarps * a.E);  // [E][copies]
+  extern __shared__ __align__(16) unsigned char smem[];
+  constexpr int NI = 2;  // indices of a batch that a lane holds ahead of their use
+  using Stream = RowStream<T, VEC, NV, LPR>;
+  using Row = typename Stream::Row;
+  constexpr int N = Row::N, S = Stream::kStages;
+  float* red = reinterpret_cast<float*>(smem + kWarps * Stream::kWarpBytes);  // [kWarps][E]
+  uint32_t* hist = reinterpret_cast<uint32_t*>(red + kWarps * a.E);           // [E][copies]
   __shared__ float red_z[kWarps], red_np[kWarps];
   __shared__ uint32_t red_rows[kWarps], red_bad[kWarps];
 
@@ -107,9 +111,10 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, VEC, NV>()) balance
   if (!a.alone)
     for (int i = blockIdx.x * kThreads + threadIdx.x; i < a.seqs.num; i += gridDim.x * kThreads) a.part.ticket[i] = 0u;
   const Lanes<LPR> L(a.lpr);
-  const int room = a.E - L.sub * VEC;
-  const int batch = R * L.rows;            // consecutive rows that a warp takes at once, at most 128
+  Stream rows(L, smem, a.E);
   const int copy = lane & (a.copies - 1);  // its copy of the histogram
+  const int batch = L.rows;                // consecutive rows that a warp takes at once
+  const int step = kWarps * batch;
 
   auto gap = [&](int64_t lo, int64_t hi) {
     for (int64_t t = lo + threadIdx.x; t < hi; t += kThreads) a.row_stats[t] = make_float2(0.f, 0.f);
@@ -124,60 +129,58 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, VEC, NV>()) balance
 
     int64_t t0 = lo + warp * batch;     // the batch's first row
     int left = (int)(hi - t0);          // rows from there on (a block has far fewer than 2^31)
-    const int64_t stride = (int64_t)kWarps * batch * a.E;
-    const T* lp = static_cast<const T*>(a.logits) + (t0 + L.grp) * a.E + L.sub * VEC;
-    Row cur[R], nxt[R];
-    LiveRows<R> live{a.mask, kWarps * batch, L.rows, L.grp};
-    uint32_t ok = live.now(t0, left, 0), ok1 = live.now(t0, left, 1);
-    live.fetch(t0, left, 2);
+    rows.start(static_cast<const T*>(a.logits), t0 + L.grp, step);
+    // does this group's row of a batch count: bit i for the i-th batch from here.
+    // The mask's byte is fetched a batch before its bit is needed.
+    uint32_t on = 0;
+    uint8_t byte = 1;
+    auto fetch = [&](int ahead) {
+      const int i = ahead * step + L.grp;
+      if (a.mask) byte = i < left ? __ldg(a.mask + t0 + i) : 0;
+    };
+    auto bit = [&](int ahead) { return (uint32_t)(ahead * step + L.grp < left && byte) << ahead; };
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      cur[r].fill(from_f32<T>(-INFINITY));
-      nxt[r].fill(from_f32<T>(-INFINITY));
-      cur[r].load(lp + r * L.rows * a.E, room, L.lpr, ok >> r & 1u);
+    for (int i = 0; i < S - 1; ++i) {
+      fetch(i);
+      on |= bit(i);
+      rows.issue(on >> i & 1u);
     }
-    while (left > 0) {
-      // the next batch's rows and this batch's indices are on their way during the arithmetic
-      const int slots = min(batch, left) * a.k;
-      const uint32_t* ip = a.idx + t0 * a.k;
-      uint32_t id[NI];
+    fetch(S - 1);
+    uint32_t id[NI];
+    auto indices = [&](int ahead) {
+      const int slots = min(batch, left - ahead * step) * a.k;
+      const uint32_t* ip = a.idx + (t0 + ahead * step) * a.k;
 #pragma unroll
       for (int i = 0; i < NI; ++i) id[i] = lane + 32 * i < slots ? __ldg(ip + lane + 32 * i) : 0u;
-      lp += stride;
-#pragma unroll
-      for (int r = 0; r < R; ++r) nxt[r].load(lp + r * L.rows * a.E, room, L.lpr, ok1 >> r & 1u);
-      const uint32_t ok2 = live.bits(left, 2);
-      live.fetch(t0, left, 3);
-
-      float mine_m = 0.f, mine_s = 0.f;  // the row that this lane writes the statistics of
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        float p[N], m = L.max(cur[r].lane_max());
-        row_scores<SIG>(cur[r], m, m, p);
-        const float s = L.sum(lane_sum(p));
-        if (ok >> r & 1u) {
-          const float inv = rcp_fast(s);  // p carries the factor that fix() takes out, too
-          pairwise<N>([&](int n) { put(acc, n, fma2(pair(p, n), both(inv), pair(acc, n))); },
-                      [&](int n) { acc[n] = fmaf(p[n], inv, acc[n]); });
-        }
-        // (groups of fewer than R lanes write row after row)
-        const int owner = L.lpr >= R ? r : 0;
-        if (L.sub == owner) mine_m = m, mine_s = s;
-        if ((r == R - 1 || L.lpr < R) && L.sub < R) {
-          const int mr = L.lpr >= R ? L.sub : r, i = mr * L.rows + L.grp;
-          if (i < left && (L.lpr >= R || L.sub == 0)) {
-            const bool o = ok >> mr & 1u;
-            if (!SIG || mine_m != 0.f) mine_s *= RowExp(mine_m, kLog2e).fix();
-            a.row_stats[t0 + i] = o ? make_float2(mine_m, mine_s) : make_float2(0.f, 0.f);
-            valid += o;
-            if (!SIG && o) {
-              const float lse = fmaf(log2_fast(mine_s), kLn2, mine_m);
-              zacc = fmaf(lse, lse, zacc);
-            }
-          }
+    };
+    if (left > 0) indices(0);
+    Row cur;
+    cur.fill(from_f32<T>(-INFINITY));
+    while (left > 0) {
+      rows.take(cur);
+      on |= bit(S - 1);
+      rows.issue(on >> (S - 1) & 1u);
+      fetch(S);
+      const bool ok = on & 1u;
+      float p[N], m = L.max(cur.lane_max());
+      row_scores<SIG>(cur, m, m, p);
+      float s = L.sum(lane_sum(p));
+      if (ok) {
+        const float inv = rcp_fast(s);  // p carries the factor that fix() takes out, too
+        pairwise<N>([&](int n) { put(acc, n, fma2(pair(p, n), both(inv), pair(acc, n))); },
+                    [&](int n) { acc[n] = fmaf(p[n], inv, acc[n]); });
+      }
+      if (L.sub == 0 && L.grp < left) {
+        if (!SIG || m != 0.f) s *= RowExp(m, kLog2e).fix();
+        a.row_stats[t0 + L.grp] = ok ? make_float2(m, s) : make_float2(0.f, 0.f);
+        valid += ok;
+        if (!SIG && ok) {
+          const float lse = fmaf(log2_fast(s), kLn2, m);
+          zacc = fmaf(lse, lse, zacc);
         }
       }
       // counts of the batch's slots; a lane adds to its copy
+      const int slots = min(batch, left) * a.k;
       auto count = [&](int i, uint32_t e) {
         if (a.mask && !__ldg(a.mask + t0 + (a.k == 1 ? i : (int)__umulhi(i, a.k_magic)))) return;
         if (e < (uint32_t)a.E) atomicAdd(hist + e * a.copies + copy, 1u);
@@ -186,13 +189,13 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, VEC, NV>()) balance
 #pragma unroll
       for (int i = 0; i < NI; ++i)
         if (lane + 32 * i < slots) count(lane + 32 * i, id[i]);
-      for (int i = lane + 32 * NI; i < slots; i += 32) count(i, __ldg(ip + i));
-#pragma unroll
-      for (int r = 0; r < R; ++r) cur[r] = nxt[r];
-      ok = ok1, ok1 = ok2;
-      t0 += kWarps * batch;
-      left -= kWarps * batch;
+      for (int i = lane + 32 * NI; i < slots; i += 32) count(i, __ldg(a.idx + t0 * a.k + i));
+      indices(1);
+      on >>= 1;
+      t0 += step;
+      left -= step;
     }
+    rows.drain();
     // the rows of a warp, then the warps, in a fixed order
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -373,12 +376,14 @@ struct LaunchFwd {
   cudaStream_t s;
   template <typename T, int VEC, int NV, int LPR>
   cudaError_t run() {
-    return launch_pdl(balance_fwd_kernel<T, VEC, NV, LPR, SIG>, dim3((unsigned)chunks), dim3(kThreads), smem, s, a);
+    static std::atomic<uint64_t> asked{0};
+    return launch_rows(balance_fwd_kernel<T, VEC, NV, LPR, SIG>, chunks, kThreads,
+                       smem + kWarps * RowStream<T, VEC, NV, LPR>::kWarpBytes, asked, s, a);
   }
 };
 
 size_t slot_count(int64_t T, int64_t num_seqs) {
-  return (size_t)(kMaxChunks < T ? kMaxChunks : T) + (size_t)num_seqs;
+  return (size_t)(kMaxBlocks < T ? kMaxBlocks : T) + (size_t)num_seqs;
 }
 
 }  // namespace
@@ -391,7 +396,7 @@ size_t balance_workspace_bytes(int64_t T, int E, int64_t num_seqs) {
 cudaError_t launch_balance_loss(const BalanceArgs& b, void* ws, uint32_t* status, cudaStream_t s) {
   const void* ptrs[] = {b.logits};
   const RowPlan plan = row_plan(ptrs, 1, b.dt, b.E);
-  const Chunks ch = cut_rows(b.T, plan_batch(plan), kMaxChunks);
+  const Chunks ch = cut_rows(b.T, plan_batch(plan), plan_blocks(plan));
   const size_t slots = slot_count(b.T, b.num_seqs);
   Partials part;
   part.p = static_cast<float*>(ws);

@@ -27,7 +27,6 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kMaxChunks = 304;  // blocks, and partials of a sequence: two per SM
 
 // Below this share of the row's maximum the student's mass outside the list is
 // taken about its own maximum, and -q_r stands in the place of q_r / R.
@@ -74,10 +73,7 @@ struct FwdArgs {
 
 // Entries of a row's list that a lane keeps in registers; more are read again
 // where they are needed.
-template <typename T, int VEC, int NV>
-constexpr int list_regs() {
-  return 4 / rows_at_once<T, VEC, NV>();
-}
+constexpr int kListRegs = 4;
 
 // A row's lanes hold its logits and, entry sub, sub + lpr, .., its list.  Which of
 // its elements are listed is a word of bits for each lane, set by the list's
@@ -85,10 +81,11 @@ constexpr int list_regs() {
 // not as a difference.
 template <typename T, int VEC, int NV, int LPR>
 __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, VEC, NV>()) distill_fwd_kernel(FwdArgs a) {
-  using Row = RowRegs<T, VEC, NV>;
-  constexpr int N = Row::N, R = rows_at_once<T, VEC, NV>(), J = list_regs<T, VEC, NV>();
-  __shared__ uint32_t listed[kWarps][R][32];
-  extern __shared__ __align__(16) unsigned char row_smem[];  // the batch's rows, for the lists' lanes
+  extern __shared__ __align__(16) unsigned char smem[];
+  using Stream = RowStream<T, VEC, NV, LPR>;
+  using Row = typename Stream::Row;
+  constexpr int N = Row::N, S = Stream::kStages, J = kListRegs;
+  __shared__ uint32_t listed[kWarps][32];
   __shared__ float red_l[kWarps];
   __shared__ uint32_t red_n[kWarps], red_b[kWarps];
   pdl_wait();
@@ -96,11 +93,11 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, VEC, NV>()) distill
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (blockIdx.x == 0 && threadIdx.x == 0) *a.status = 0u;
   const Lanes<LPR> L(a.lpr);
-  const int room = a.E - L.sub * VEC;
-  const int batch = R * L.rows;
-  const int lpr_log = 31 - __clz(L.lpr);
-  const int pitch = (int)align_up((size_t)a.E * sizeof(T), 16) / (int)sizeof(T);
-  T* const copy = reinterpret_cast<T*>(row_smem) + (warp * batch + L.grp) * pitch;  // r-th row: + r * rows * pitch
+  Stream rows(L, smem, a.E);
+  const int step = kWarps * L.rows;
+  uint32_t* const words = &listed[warp][L.grp * L.lpr];
+  auto owner = [&](uint32_t e) { return (e / VEC) & (L.lpr - 1); };  // the lane that holds element e
+  auto bit_of = [&](uint32_t e) { return 1u << ((e / VEC >> rows.lpr_log) * VEC + e % VEC); };
 
   float* const own_stat = L.sub == 0 ? a.row_loss : a.row_stats + (L.sub - 1) * a.T;
   auto write_row = [&](int64_t t, float kl, float m, float s, float mt, float st, float ratio) {
@@ -118,194 +115,181 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, VEC, NV>()) distill
   auto piece = [&](int seq, int64_t lo, int64_t hi) {
     float loss = 0.f;
     uint32_t counted = 0, broken = 0;
-    int64_t t0 = lo + warp * batch;
+    int64_t t0 = lo + warp * L.rows;
     int left = (int)(hi - t0);
-    const int64_t stride = (int64_t)kWarps * batch * a.E;
-    const T* lp = static_cast<const T*>(a.logits) + (t0 + L.grp) * a.E + L.sub * VEC;
-    // this lane's entries of the rows' lists (a row's lanes hold entries sub, sub + lpr, ..)
+    rows.start(static_cast<const T*>(a.logits), t0 + L.grp, step);
+    // does this group's row of a batch count: bit i for the i-th batch from here.
+    // The mask's byte is fetched a batch before its bit is needed.
+    uint32_t on = 0;
+    uint8_t byte = 1;
+    auto fetch = [&](int ahead) {
+      const int i = ahead * step + L.grp;
+      if (a.mask) byte = i < left ? __ldg(a.mask + t0 + i) : 0;
+    };
+    auto bit = [&](int ahead) { return (uint32_t)(ahead * step + L.grp < left && byte) << ahead; };
+#pragma unroll
+    for (int i = 0; i < S - 1; ++i) {
+      fetch(i);
+      on |= bit(i);
+      rows.issue(on >> i & 1u);
+    }
+    fetch(S - 1);
+    // this lane's entries of its row's list, a batch ahead
     const ListEntries list{a.t_logits, a.t_idx, a.t_dt};
     int64_t li = (t0 + L.grp) * a.m + L.sub;
-    Row cur[R], nxt[R];
-    float rest[R], rest1[R];
-    uint32_t x[R][J], x1[R][J], e[R][J], e1[R][J];
-    auto lists = [&](int ahead, uint32_t on, uint32_t (&x)[R][J], uint32_t (&e)[R][J], float (&rest)[R]) {
+    auto entries = [&](int ahead, uint32_t (&x)[J], uint32_t (&e)[J], float& rest) {
+      const bool ok = on >> ahead & 1u;
+      rest = ok && a.t_rest ? __ldg(a.t_rest + t0 + ahead * step + L.grp) : -INFINITY;
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
-        const int i = ahead * kWarps * batch + r * L.rows;
-        rest[r] = (on >> r & 1u) && a.t_rest ? __ldg(a.t_rest + t0 + i + L.grp) : -INFINITY;
-#pragma unroll
-        for (int j = 0; j < J; ++j) {
-          if (j * L.lpr >= a.m) break;
-          x[r][j] = list.none();
-          e[r][j] = 0u;
-          if ((on >> r & 1u) && L.sub + j * L.lpr < a.m) {
-            x[r][j] = list.bits(li + i * a.m + j * L.lpr);
-            e[r][j] = list.expert(li + i * a.m + j * L.lpr);
-          }
+      for (int j = 0; j < J; ++j) {
+        if (j * L.lpr >= a.m) break;
+        x[j] = list.none();
+        e[j] = 0u;
+        if (ok && L.sub + j * L.lpr < a.m) {
+          x[j] = list.bits(li + ahead * step * a.m + j * L.lpr);
+          e[j] = list.expert(li + ahead * step * a.m + j * L.lpr);
         }
       }
     };
-    LiveRows<R> live{a.mask, kWarps * batch, L.rows, L.grp};
-    uint32_t on = live.now(t0, left, 0), on1 = live.now(t0, left, 1);
-    live.fetch(t0, left, 2);
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      cur[r].fill(from_f32<T>(-INFINITY));
-      nxt[r].fill(from_f32<T>(-INFINITY));
-      cur[r].load(lp + r * L.rows * a.E, room, L.lpr, on >> r & 1u);
-    }
-    lists(0, on, x, e, rest);
+    uint32_t x[J], e[J];
+    float rest;
+    entries(0, x, e, rest);
+    Row cur;
+    cur.fill(from_f32<T>(-INFINITY));
     while (left > 0) {
-      lp += stride;
-#pragma unroll
-      for (int r = 0; r < R; ++r) nxt[r].load(lp + r * L.rows * a.E, room, L.lpr, on1 >> r & 1u);
-      lists(1, on1, x1, e1, rest1);
-      const uint32_t on2 = live.bits(left, 2);
-      live.fetch(t0, left, 3);
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        listed[warp][r][lane] = 0u;
-        cur[r].keep(copy + r * L.rows * pitch + L.sub * VEC, room, L.lpr);
-      }
-      __syncwarp();
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        const int64_t t = t0 + r * L.rows + L.grp;
-        bool ok = on >> r & 1u;
-        const T* row = copy + r * L.rows * pitch;
-        // calls f(x, e) for this lane's entries behind those in registers
-        auto others = [&](auto f) {
-          if (ok)
-            for (int j = L.sub + J * L.lpr; j < a.m; j += L.lpr) {
-              const uint32_t b = list.bits(t * a.m + j);
-              if (b != list.none()) f(list.value(b), list.expert(t * a.m + j));
-            }
-        };
-        // the teacher's maximum, and the bits of the list's experts
-        float mt = rest[r];
-        bool nan = rest[r] != rest[r] || rest[r] == INFINITY, bad = false;
-        uint32_t* words = &listed[warp][r][L.grp * L.lpr];
-        auto note = [&](float xx, uint32_t ee) {
-          mt = fmaxf(mt, xx);  // passes over NaN
-          nan |= xx != xx || xx == INFINITY;
-          const uint32_t q = ee / VEC, bit = 1u << ((q >> lpr_log) * VEC + ee % VEC);
-          if (ee >= (uint32_t)a.E || (atomicOr(words + (q & (L.lpr - 1)), bit) & bit)) bad = true;
-        };
-        float xs[J], ys[J];  // an entry that is not there has xs = -inf
-#pragma unroll
-        for (int j = 0; j < J; ++j) {
-          xs[j] = -INFINITY;
-          if (j * L.lpr >= a.m) break;
-          xs[j] = list.value(x[r][j]);
-          ys[j] = to_f32<T>(row[min(e[r][j], (uint32_t)a.E - 1u)]);
-          if (xs[j] != -INFINITY) note(xs[j], e[r][j]);
-        }
-        others(note);
-        mt = L.max(mt);
-        nan = L.any(nan);
-        bad = L.any(bad);
-        ok = ok && (mt != -INFINITY || nan);  // else no target
-        const float m = L.max(cur[r].lane_max());
-        __syncwarp();
-        const uint32_t mine = listed[warp][r][lane];
-        // the student's mass outside the list, and both sides' masses in it
-        const RowExp ex(m, a.c);
-        float out = 0.f;
-        {
-          float p[N], odd = 0.f;
-          ex.row(cur[r], p);
-#pragma unroll
-          for (int n = 0; n < N; ++n)
-            if (!(mine & (1u << n))) (n % 2 ? odd : out) += p[n];
-          out += odd;
-        }
-        const float eq_rest = exp2_fast((rest[r] - mt) * a.c);
-        float st = L.sub == 0 ? eq_rest : 0.f, sp = 0.f;
-        float eq[J], ep[J];
-#pragma unroll
-        for (int j = 0; j < J; ++j) {
-          if (j * L.lpr >= a.m) break;
-          eq[j] = exp2_fast((xs[j] - mt) * a.c);
-          ep[j] = xs[j] != -INFINITY ? ex.at(ys[j]) : 0.f;
-          st += eq[j];
-          sp += ep[j];
-        }
-        others([&](float xx, uint32_t ee) {
-          st += exp2_fast((xx - mt) * a.c);
-          if (ee < (uint32_t)a.E) sp += ex.at(to_f32<T>(row[ee]));
-        });
-        out = L.sum(out);
-        st = L.sum(st);
-        const float s0 = out + L.sum(sp);  // with the factor that fix() takes out
-        const float fix = ex.fix();
-        // log of the mass outside the list, about its own maximum where it is far below the row's
-        float ln_out = log2_fast(out * fix) * kLn2;
-        const bool far = ok && a.t_rest && out < kFarBelow;
-        if (far) {
-          auto outside = [&](int el) {
-            const int q = el / VEC;
-            return !(words[q & (L.lpr - 1)] >> ((q >> lpr_log) * VEC + el % VEC) & 1u);
-          };
-          float mo = -INFINITY, so = 0.f;
-#pragma unroll 1
-          for (int el = L.sub; el < a.E; el += L.lpr)
-            if (outside(el)) mo = fmaxf(mo, to_f32<T>(row[el]));
-          for (int d = L.lpr / 2; d > 0; d >>= 1) mo = fmaxf(mo, __shfl_xor_sync(L.mask(), mo, d));
-#pragma unroll 1
-          for (int el = L.sub; el < a.E; el += L.lpr)
-            if (outside(el)) so += exp2_fast((to_f32<T>(row[el]) - mo) * a.c);
-          for (int d = L.lpr / 2; d > 0; d >>= 1) so += __shfl_xor_sync(L.mask(), so, d);
-          ln_out = mo == -INFINITY ? -INFINITY : (mo - m) * a.inv_tau + logf(so);
-        }
-        const float s = bad || nan ? NAN : s0 * fix;
-        const float inv_s = rcp_fast(s0), inv_st = rcp_fast(st);
-        const float dz = (log2_fast(s) - log2_fast(st)) * kLn2;
-        float kl = 0.f, ratio = 0.f;
-#pragma unroll
-        for (int j = 0; j < J; ++j) {
-          if (j * L.lpr >= a.m) break;
-          const float term =
-              kl_term(eq[j] * inv_st, ep[j] * inv_s, ((xs[j] - mt) - (ys[j] - m)) * a.inv_tau + dz);
-          kl += xs[j] != -INFINITY ? term : 0.f;
-        }
-        others([&](float xx, uint32_t ee) {
-          if (ee >= (uint32_t)a.E) return;
-          const float y = to_f32<T>(row[ee]);
-          kl += kl_term(exp2_fast((xx - mt) * a.c) * inv_st, ex.at(y) * inv_s,
-                        ((xx - mt) - (y - m)) * a.inv_tau + dz);
-        });
-        if (a.t_rest) {
-          const float q = eq_rest * inv_st, p = out * inv_s;
-          if (L.sub == 0) kl += kl_term(q, p, (rest[r] - mt) * a.inv_tau - ln_out + dz);
-          ratio = far ? -q : q * rcp_fast(p);
-        } else if (L.sub == 0) {
-          kl += out * inv_s;
-        }
-        kl = L.sum(kl);
-        if (s != s || st != st) kl = NAN;
-        if (r * L.rows + L.grp < left) {
-          if (ok) write_row(t, kl, m, s, mt, st, ratio);
-          else write_row(t, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f);
-          if (ok && L.sub == 0) {
-            loss += kl;
-            ++counted;
-            broken += bad;
+      rows.take(cur);
+      listed[warp][lane] = 0u;
+      __syncwarp();  // the rows and the words lie in shared memory
+      on |= bit(S - 1);
+      rows.issue(on >> (S - 1) & 1u);
+      fetch(S);
+      uint32_t x1[J], e1[J];
+      float rest1;
+      entries(1, x1, e1, rest1);
+      const int64_t t = t0 + L.grp;
+      bool ok = on & 1u;
+      // calls f(x, e) for this lane's entries behind those in registers
+      auto others = [&](auto f) {
+        if (ok)
+          for (int j = L.sub + J * L.lpr; j < a.m; j += L.lpr) {
+            const uint32_t b = list.bits(t * a.m + j);
+            if (b != list.none()) f(list.value(b), list.expert(t * a.m + j));
           }
+      };
+      // the teacher's maximum, and the bits of the list's experts
+      float mt = rest;
+      bool nan = rest != rest || rest == INFINITY, bad = false;
+      auto note = [&](float xx, uint32_t ee) {
+        mt = fmaxf(mt, xx);  // passes over NaN
+        nan |= xx != xx || xx == INFINITY;
+        if (ee >= (uint32_t)a.E || (atomicOr(words + owner(ee), bit_of(ee)) & bit_of(ee))) bad = true;
+      };
+      float xs[J], ys[J];  // an entry that is not there has xs = -inf
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        xs[j] = -INFINITY;
+        if (j * L.lpr >= a.m) break;
+        xs[j] = list.value(x[j]);
+        ys[j] = to_f32<T>(rows.cell((int)min(e[j], (uint32_t)a.E - 1u)));
+        if (xs[j] != -INFINITY) note(xs[j], e[j]);
+      }
+      others(note);
+      mt = L.max(mt);
+      nan = L.any(nan);
+      bad = L.any(bad);
+      ok = ok && (mt != -INFINITY || nan);  // else no target
+      const float m = L.max(cur.lane_max());
+      __syncwarp();
+      const uint32_t mine = listed[warp][lane];
+      // the student's mass outside the list, and both sides' masses in it
+      const RowExp ex(m, a.c);
+      float out = 0.f;
+      {
+        float p[N], odd = 0.f;
+        ex.row(cur, p);
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+          if (!(mine & (1u << n))) (n % 2 ? odd : out) += p[n];
+        out += odd;
+      }
+      const float eq_rest = exp2_fast((rest - mt) * a.c);
+      float st = L.sub == 0 ? eq_rest : 0.f, sp = 0.f;
+      float eq[J], ep[J];
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        if (j * L.lpr >= a.m) break;
+        eq[j] = exp2_fast((xs[j] - mt) * a.c);
+        ep[j] = xs[j] != -INFINITY ? ex.at(ys[j]) : 0.f;
+        st += eq[j];
+        sp += ep[j];
+      }
+      others([&](float xx, uint32_t ee) {
+        st += exp2_fast((xx - mt) * a.c);
+        if (ee < (uint32_t)a.E) sp += ex.at(to_f32<T>(rows.cell((int)ee)));
+      });
+      out = L.sum(out);
+      st = L.sum(st);
+      const float s0 = out + L.sum(sp);  // with the factor that fix() takes out
+      const float fix = ex.fix();
+      // log of the mass outside the list, about its own maximum where it is far below the row's
+      float ln_out = log2_fast(out * fix) * kLn2;
+      const bool far = ok && a.t_rest && out < kFarBelow;
+      if (far) {
+        float mo = -INFINITY, so = 0.f;
+#pragma unroll 1
+        for (int el = L.sub; el < a.E; el += L.lpr)
+          if (!(words[owner(el)] & bit_of(el))) mo = fmaxf(mo, to_f32<T>(rows.cell(el)));
+        for (int d = L.lpr / 2; d > 0; d >>= 1) mo = fmaxf(mo, __shfl_xor_sync(L.mask(), mo, d));
+#pragma unroll 1
+        for (int el = L.sub; el < a.E; el += L.lpr)
+          if (!(words[owner(el)] & bit_of(el))) so += exp2_fast((to_f32<T>(rows.cell(el)) - mo) * a.c);
+        for (int d = L.lpr / 2; d > 0; d >>= 1) so += __shfl_xor_sync(L.mask(), so, d);
+        ln_out = mo == -INFINITY ? -INFINITY : (mo - m) * a.inv_tau + logf(so);
+      }
+      const float s = bad || nan ? NAN : s0 * fix;
+      const float inv_s = rcp_fast(s0), inv_st = rcp_fast(st);
+      const float dz = (log2_fast(s) - log2_fast(st)) * kLn2;
+      float kl = 0.f, ratio = 0.f;
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        if (j * L.lpr >= a.m) break;
+        const float term = kl_term(eq[j] * inv_st, ep[j] * inv_s, ((xs[j] - mt) - (ys[j] - m)) * a.inv_tau + dz);
+        kl += xs[j] != -INFINITY ? term : 0.f;
+      }
+      others([&](float xx, uint32_t ee) {
+        if (ee >= (uint32_t)a.E) return;
+        const float y = to_f32<T>(rows.cell((int)ee));
+        kl += kl_term(exp2_fast((xx - mt) * a.c) * inv_st, ex.at(y) * inv_s,
+                      ((xx - mt) - (y - m)) * a.inv_tau + dz);
+      });
+      if (a.t_rest) {
+        const float q = eq_rest * inv_st, p = out * inv_s;
+        if (L.sub == 0) kl += kl_term(q, p, (rest - mt) * a.inv_tau - ln_out + dz);
+        ratio = far ? -q : q * rcp_fast(p);
+      } else if (L.sub == 0) {
+        kl += out * inv_s;
+      }
+      kl = L.sum(kl);
+      if (s != s || st != st) kl = NAN;
+      if (L.grp < left) {
+        if (ok) write_row(t, kl, m, s, mt, st, ratio);
+        else write_row(t, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f);
+        if (ok && L.sub == 0) {
+          loss += kl;
+          ++counted;
+          broken += bad;
         }
       }
-      __syncwarp();  // before the next batch clears the bits
+      __syncwarp();  // before the next batch takes this one's place
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
-        cur[r] = nxt[r];
-        rest[r] = rest1[r];
-#pragma unroll
-        for (int j = 0; j < J; ++j) x[r][j] = x1[r][j], e[r][j] = e1[r][j];
-      }
-      on = on1, on1 = on2;
-      t0 += kWarps * batch;
-      li += (int64_t)kWarps * batch * a.m;
-      left -= kWarps * batch;
+      for (int j = 0; j < J; ++j) x[j] = x1[j], e[j] = e1[j];
+      rest = rest1;
+      on >>= 1;
+      t0 += step;
+      li += (int64_t)step * a.m;
+      left -= step;
     }
+    rows.drain();
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) {
       loss += __shfl_xor_sync(0xffffffffu, loss, d);
@@ -387,14 +371,16 @@ __global__ void __launch_bounds__(kThreads) distill_finish_kernel(FinishArgs a) 
 struct LaunchFwd {
   FwdArgs a;
   int chunks;
-  size_t smem;
   cudaStream_t s;
   template <typename T, int VEC, int NV, int LPR>
   cudaError_t run() {
-    return launch_pdl(distill_fwd_kernel<T, VEC, NV, LPR>, dim3((unsigned)chunks), dim3(kThreads), smem, s, a);
+    static std::atomic<uint64_t> asked{0};
+    return launch_rows(distill_fwd_kernel<T, VEC, NV, LPR>, chunks, kThreads,
+                       kWarps * RowStream<T, VEC, NV, LPR>::kWarpBytes, asked, s, a);
   }
 };
-size_t slot_count(int64_t T, int64_t num_seqs) { return (size_t)(kMaxChunks < T ? kMaxChunks : T) + (size_t)num_seqs; }
+
+size_t slot_count(int64_t T, int64_t num_seqs) { return (size_t)(kMaxBlocks < T ? kMaxBlocks : T) + (size_t)num_seqs; }
 
 }  // namespace
 
@@ -403,7 +389,7 @@ size_t distill_workspace_bytes(int64_t T, int64_t num_seqs) { return align_up(sl
 cudaError_t launch_distill_loss(const DistillArgs& d, void* ws, uint32_t* status, cudaStream_t s) {
   const void* ptrs[] = {d.logits};
   const RowPlan plan = row_plan(ptrs, 1, d.dt, d.E);
-  const Chunks ch = cut_rows(d.T, plan_batch(plan), kMaxChunks);
+  const Chunks ch = cut_rows(d.T, plan_batch(plan), plan_blocks(plan));
   const size_t slots = slot_count(d.T, d.num_seqs);
   FwdArgs a{};
   a.logits = d.logits;
@@ -429,8 +415,7 @@ cudaError_t launch_distill_loss(const DistillArgs& d, void* ws, uint32_t* status
   a.row_loss = d.row_loss;
   a.row_stats = d.row_stats;
   a.status = status;
-  const size_t smem = (size_t)kWarps * plan_batch(plan) * align_up((size_t)d.E * dtype_size(d.dt), 16);
-  LaunchFwd f{a, ch.chunks, smem, s};
+  LaunchFwd f{a, ch.chunks, s};
   const cudaError_t e = with_row_variant(d.dt, plan, f);
   if (e != cudaSuccess || a.alone) return e;
   FinishArgs fin{a.part_loss, a.part_rows, a.part_bad, a.seqs, ch.rows, d.loss, d.tokens, status};

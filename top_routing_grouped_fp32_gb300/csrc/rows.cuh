@@ -9,7 +9,9 @@
 
 #include <math.h>
 
+#include <atomic>
 #include <type_traits>
+#include <utility>
 
 #include "common.cuh"
 
@@ -122,19 +124,12 @@ struct Lanes {
   __device__ __forceinline__ bool any(bool x) const { return (__ballot_sync(0xffffffffu, x) & mask()) != 0; }
 };
 
-// Rows of a lane group that a warp works on at once: with few elements a lane,
-// several rows keep enough loads in flight for HBM (64 bytes a lane).
-template <typename T, int VEC, int NV>
-constexpr int rows_at_once() {
-  constexpr int bytes = VEC == 1 ? NV * 4 : VEC * NV * (int)sizeof(T);
-  return bytes <= 16 ? 4 : bytes <= 32 ? 2 : 1;
-}
-
-// Blocks of 256 threads that a SM is to hold: two, but for the longest rows
-// (whose registers would spill).
+// Blocks of 256 threads that a SM is to hold, by the bytes of a row that a lane
+// holds (its registers follow them).
 template <typename T, int VEC, int NV>
 constexpr int blocks_per_sm() {
-  return VEC * NV <= 16 || VEC == 8 ? 2 : 1;
+  constexpr int bytes = VEC == 1 ? NV * 4 : NV * 16;
+  return bytes <= 16 ? 4 : bytes <= 32 ? 3 : bytes <= 64 ? 2 : 1;
 }
 
 // One row's elements of this lane.
@@ -167,18 +162,6 @@ struct RowRegs {
     }
   }
   __device__ __forceinline__ float operator[](int n) const { return to_f32<T>(raw[n]); }
-  // Lays the elements out in shared memory, as load() has them.
-  __device__ __forceinline__ void keep(T* row, int room, int lpr) const {
-#pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      if (v * lpr * VEC >= room) continue;
-      if constexpr (VEC > 1)
-        *reinterpret_cast<uint4*>(row + v * lpr * VEC) = *reinterpret_cast<const uint4*>(raw + v * VEC);
-      else
-        row[v * lpr] = raw[v];
-    }
-  }
-
   // This lane's maximum; passes over NaN.
   __device__ __forceinline__ float lane_max() const {
     if constexpr (sizeof(T) == 2 && VEC == 8) {  // two elements an instruction
@@ -192,6 +175,129 @@ struct RowRegs {
 #pragma unroll
       for (int n = 1; n < N; ++n) m = fmaxf(m, (*this)[n]);
       return m;
+    }
+  }
+};
+
+// Stores a lane's values at `row` (as RowRegs::load has it), in 16-byte vectors
+// or single elements.
+template <typename T, int VEC, int NV>
+__device__ __forceinline__ void store_row(T* row, int room, int lpr, const float (&f)[VEC * NV]) {
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    if (v * lpr * VEC >= room) continue;
+    if constexpr (VEC == 8) {
+      *reinterpret_cast<uint4*>(row + v * lpr * VEC) = pack8<T>(f + v * VEC);
+    } else if constexpr (VEC == 4) {
+      *reinterpret_cast<float4*>(row + v * lpr * VEC) =
+          make_float4(f[v * 4], f[v * 4 + 1], f[v * 4 + 2], f[v * 4 + 3]);
+    } else {
+      row[v * lpr] = from_f32<T>(f[v]);
+    }
+  }
+}
+
+// The rows of a warp, a batch of 32 / lpr after another.  Vectors of 16 bytes come
+// through a ring of kStages batches in the warp's shared memory by asynchronous
+// copies, so that kStages - 1 batches are in flight without registers: 256 BF16
+// logits a row with one batch ahead in registers ran at 66 % of the copy
+// bandwidth (16 warps of 128 registers on a SM do not cover the latency).  A lane
+// copies and reads the same 16 bytes, so no lane waits for another.  Single
+// elements come through registers, one batch ahead.
+//
+// The current batch also lies in shared memory by vector and lane: cell(e) is
+// element e of this lane's row.  It may be written (each lane its own row's) until
+// the next issue().
+template <typename T, int VEC, int NV, int LPR>
+struct RowStream {
+  static constexpr int kStages = VEC > 1 ? 4 : 2;
+  static constexpr int kStageElems = 32 * VEC * NV;
+  static constexpr int kWarpBytes = (VEC > 1 ? kStages : 1) * kStageElems * (int)sizeof(T);
+  using Row = RowRegs<T, VEC, NV>;
+  const Lanes<LPR>& L;
+  T* ring;      // of this warp
+  const T* p;   // this lane's first element of the batch that is issued next
+  int64_t step; // elements between a warp's batches
+  int room, E, lpr_log;
+  int head, tail;  // stages: current, issued next
+  Row nxt;
+
+  __device__ __forceinline__ RowStream(const Lanes<LPR>& L_, void* smem, int E_) : L(L_), E(E_) {
+    ring = reinterpret_cast<T*>(static_cast<char*>(smem) + (threadIdx.x >> 5) * kWarpBytes);
+    room = E - L.sub * VEC;
+    lpr_log = 31 - __clz(L.lpr);
+  }
+  // `first`: this group's row of the warp's first batch; a batch every `rows` rows
+  __device__ __forceinline__ void start(const T* logits, int64_t first, int64_t rows) {
+    p = logits + first * E + L.sub * VEC;
+    step = rows * E;
+    head = tail = 0;
+    nxt.fill(from_f32<T>(-INFINITY));
+  }
+  __device__ __forceinline__ void issue(bool ok) {
+    if constexpr (VEC > 1) {
+      const uint32_t to =
+          (uint32_t)__cvta_generic_to_shared(ring + tail * kStageElems) + (threadIdx.x & 31) * 16;
+#pragma unroll
+      for (int v = 0; v < NV; ++v)
+        if (ok && v * L.lpr * VEC < room)
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + v * 512), "l"(p + v * L.lpr * VEC)
+                       : "memory");
+      asm volatile("cp.async.commit_group;" ::: "memory");
+      tail = tail + 1 == kStages ? 0 : tail + 1;
+    } else {
+      nxt.load(p, room, L.lpr, ok);
+    }
+    p += step;
+  }
+  // The oldest batch issued becomes the current one.  Elements behind a row's end
+  // keep what `cur` holds; rows that were not loaded hold anything.
+  __device__ __forceinline__ void take(Row& cur) {
+    if constexpr (VEC > 1) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+      head = tail == kStages - 1 ? 0 : tail + 1;  // issued kStages - 1 ago
+      const T* from = ring + head * kStageElems + (threadIdx.x & 31) * VEC;
+#pragma unroll
+      for (int v = 0; v < NV; ++v)
+        if (v * L.lpr * VEC < room)
+          *reinterpret_cast<uint4*>(cur.raw + v * VEC) = *reinterpret_cast<const uint4*>(from + v * 32 * VEC);
+    } else {
+      cur = nxt;
+      put(cur);
+    }
+  }
+  __device__ __forceinline__ void drain() {
+    if constexpr (VEC > 1) asm volatile("cp.async.wait_all;" ::: "memory");
+  }
+  __device__ __forceinline__ T* stage() const { return ring + (VEC > 1 ? head * kStageElems : 0); }
+  __device__ __forceinline__ T& cell(int e) const {
+    const int q = e / VEC;
+    return stage()[((q >> lpr_log) * 32 + L.grp * L.lpr + (q & (L.lpr - 1))) * VEC + e % VEC];
+  }
+  // Writes this lane's elements of the current batch.
+  __device__ __forceinline__ void put(const Row& r) const {
+    T* to = stage() + (threadIdx.x & 31) * VEC;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      if constexpr (VEC > 1)
+        *reinterpret_cast<uint4*>(to + v * 32 * VEC) = *reinterpret_cast<const uint4*>(r.raw + v * VEC);
+      else
+        to[v * 32] = r.raw[v];
+    }
+  }
+  __device__ __forceinline__ void put(const float (&f)[VEC * NV]) const {
+    store_row<T, VEC, NV>(stage() + (threadIdx.x & 31) * VEC, 32 * VEC * NV, 32, f);
+  }
+  // Stores this lane's elements of the current batch to `row` (this lane's first).
+  __device__ __forceinline__ void store(T* row) const {
+    const T* from = stage() + (threadIdx.x & 31) * VEC;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      if (v * L.lpr * VEC >= room) continue;
+      if constexpr (VEC > 1)
+        *reinterpret_cast<uint4*>(row + v * L.lpr * VEC) = *reinterpret_cast<const uint4*>(from + v * 32 * VEC);
+      else
+        row[v * L.lpr] = from[v * 32];
     }
   }
 };
@@ -259,24 +365,6 @@ struct ListEntries {
   }
 };
 
-// Stores a lane's values at `row` (as RowRegs::load has it), in 16-byte vectors
-// or single elements.
-template <typename T, int VEC, int NV>
-__device__ __forceinline__ void store_row(T* row, int room, int lpr, const float (&f)[VEC * NV]) {
-#pragma unroll
-  for (int v = 0; v < NV; ++v) {
-    if (v * lpr * VEC >= room) continue;
-    if constexpr (VEC == 8) {
-      *reinterpret_cast<uint4*>(row + v * lpr * VEC) = pack8<T>(f + v * VEC);
-    } else if constexpr (VEC == 4) {
-      *reinterpret_cast<float4*>(row + v * lpr * VEC) =
-          make_float4(f[v * 4], f[v * 4 + 1], f[v * 4 + 2], f[v * 4 + 3]);
-    } else {
-      row[v * lpr] = from_f32<T>(f[v]);
-    }
-  }
-}
-
 // ---- packed sequences --------------------------------------------------------
 // Sequence s holds the rows off[s] <= t < off[s+1] of a batch of T rows; a null
 // `off` is one sequence of all rows.  Offsets come from the device and are
@@ -326,34 +414,6 @@ __device__ __forceinline__ void walk_sequences(const Seqs& q, int64_t a, int64_t
     cur = hi;
   }
 }
-
-// Which rows of a warp's batch count: bit r for the r-th row of each lane group.
-// The mask's bytes are fetched a batch before their bits are needed.
-template <int R>
-struct LiveRows {
-  const uint8_t* mask;
-  int step, rows, grp;  // rows between a warp's batches, rows per warp, this lane's group
-  uint8_t byte[R];
-  __device__ __forceinline__ void fetch(int64_t t0, int left, int ahead) {
-    if (!mask) return;
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const int i = ahead * step + r * rows + grp;
-      byte[r] = i < left ? __ldg(mask + t0 + i) : 0;
-    }
-  }
-  __device__ __forceinline__ uint32_t bits(int left, int ahead) const {
-    uint32_t b = 0;
-#pragma unroll
-    for (int r = 0; r < R; ++r)
-      b |= (uint32_t)(ahead * step + r * rows + grp < left && (!mask || byte[r])) << r;
-    return b;
-  }
-  __device__ __forceinline__ uint32_t now(int64_t t0, int left, int ahead) {
-    fetch(t0, left, ahead);
-    return bits(left, ahead);
-  }
-};
 
 // ---- variants by row length ------------------------------------------------------
 // Vectors of 16 bytes where every row starts on a 16-byte boundary: up to eight
@@ -411,10 +471,33 @@ cudaError_t with_row_variant(moe_dtype dt, const RowPlan& p, F&& f) {
   if (dt == MOE_F16) return with_row_variant<__half>(p, f);
   return with_row_variant<__nv_bfloat16>(p, f);
 }
-// Rows that a warp of a plan takes at once.
-inline int plan_batch(const RowPlan& p) {
+// Rows that a warp of a plan takes at once, and the blocks that a GPU of 152 SMs
+// holds of its kernels (blocks_per_sm).
+constexpr int kMaxBlocks = 152 * 4;
+inline int plan_batch(const RowPlan& p) { return 32 / p.lpr; }
+inline int plan_blocks(const RowPlan& p) {
   const int bytes = p.nv * (p.vec ? 16 : 4);
-  return (bytes <= 16 ? 4 : bytes <= 32 ? 2 : 1) * (32 / p.lpr);
+  return 152 * (bytes <= 16 ? 4 : bytes <= 32 ? 3 : bytes <= 64 ? 2 : 1);
+}
+
+// Launches a kernel that may need more shared memory than the default, which is
+// asked for once per kernel and device.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_rows(void (*kernel)(KArgs...), int blocks, int threads, size_t smem, std::atomic<uint64_t>& asked,
+                        cudaStream_t s, Args&&... args) {
+  if (smem > 48 * 1024) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = 1ull << (dev & 63);
+    if (dev > 63 || !(asked.load(std::memory_order_acquire) & bit)) {
+      e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               220 * 1024);  // the kernels' own arrays take less than 7 KB
+      if (e != cudaSuccess) return e;
+      asked.fetch_or(bit, std::memory_order_release);
+    }
+  }
+  return launch_pdl(kernel, dim3((unsigned)blocks), dim3((unsigned)threads), smem, s, std::forward<Args>(args)...);
 }
 
 // How a batch of rows is cut over blocks: `chunks` blocks of `rows` rows.
