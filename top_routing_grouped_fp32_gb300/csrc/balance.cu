@@ -146,14 +146,19 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, VEC, NV>()) balance
       rows.issue(on >> i & 1u);
     }
     fetch(S - 1);
-    uint32_t id[NI];
-    auto indices = [&](int ahead) {
+    // the batch's indices, two batches ahead
+    uint32_t id[NI], id1[NI], id2[NI];
+    auto indices = [&](int ahead, uint32_t (&id)[NI]) {
       const int slots = min(batch, left - ahead * step) * a.k;
-      const uint32_t* ip = a.idx + (t0 + ahead * step) * a.k;
+      const uint32_t* ip = a.idx + (t0 + ahead * step) * a.k + lane;
 #pragma unroll
-      for (int i = 0; i < NI; ++i) id[i] = lane + 32 * i < slots ? __ldg(ip + lane + 32 * i) : 0u;
+      for (int i = 0; i < NI; ++i) {
+        if (32 * i >= batch * a.k) break;
+        id[i] = lane + 32 * i < slots ? __ldg(ip + 32 * i) : 0u;
+      }
     };
-    if (left > 0) indices(0);
+    indices(0, id);
+    indices(1, id1);
     Row cur;
     cur.fill(from_f32<T>(-INFINITY));
     while (left > 0) {
@@ -161,6 +166,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, VEC, NV>()) balance
       on |= bit(S - 1);
       rows.issue(on >> (S - 1) & 1u);
       fetch(S);
+      indices(2, id2);
       const bool ok = on & 1u;
       float p[N], m = L.max(cur.lane_max());
       row_scores<SIG>(cur, m, m, p);
@@ -187,10 +193,13 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, VEC, NV>()) balance
         else ++bad;
       };
 #pragma unroll
-      for (int i = 0; i < NI; ++i)
+      for (int i = 0; i < NI; ++i) {
+        if (32 * i >= batch * a.k) break;
         if (lane + 32 * i < slots) count(lane + 32 * i, id[i]);
+      }
       for (int i = lane + 32 * NI; i < slots; i += 32) count(i, __ldg(a.idx + t0 * a.k + i));
-      indices(1);
+#pragma unroll
+      for (int i = 0; i < NI; ++i) id[i] = id1[i], id1[i] = id2[i];
       on >>= 1;
       t0 += step;
       left -= step;

@@ -57,27 +57,29 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, VEC, NV>()) balance
     int64_t t0 = lo + warp * L.rows;
     int left = (int)(hi - t0);
     rows.start(static_cast<const T*>(a.logits), t0 + L.grp, step);
-    // Rows that do not count (a sum of 0) are not read: their sums are fetched
-    // S batches ahead, the statistics again a batch ahead.
+    // Rows that do not count (a sum of 0) are not read.  A row's sum is fetched two
+    // batches before its row is asked for, its statistics (again) two before their use:
+    // one batch does not cover the latency.
     auto inside = [&](int ahead) { return seq >= 0 && ahead * step + L.grp < left; };
     auto sum_at = [&](int ahead) { return inside(ahead) ? __ldg(&a.row_stats[t0 + ahead * step + L.grp].y) : 0.f; };
     auto stats = [&](int ahead) {
       return inside(ahead) ? __ldg(a.row_stats + t0 + ahead * step + L.grp) : make_float2(0.f, 0.f);
     };
-    float sum[S];
+    float sum[S + 1];
 #pragma unroll
-    for (int i = 0; i < S; ++i) sum[i] = sum_at(i);
+    for (int i = 0; i <= S; ++i) sum[i] = sum_at(i);
+    float2 st = stats(0), st1 = stats(1);
 #pragma unroll
     for (int i = 0; i < S - 1; ++i) rows.issue(sum[i] != 0.f);
-    float ahead_sum = sum[S - 1];
-    float2 st = stats(0);
+    float sum0 = sum[S - 1], sum1 = sum[S];
     Row cur;
     cur.fill(from_f32<T>(-INFINITY));
     while (left > 0) {
       rows.take(cur);
-      rows.issue(ahead_sum != 0.f);
-      ahead_sum = sum_at(S);
-      const float2 st1 = stats(1);
+      rows.issue(sum0 != 0.f);
+      sum0 = sum1;
+      sum1 = sum_at(S + 1);
+      const float2 st2 = stats(2);
       const bool in = L.grp < left;
       const bool ok = st.y != 0.f;  // NaN sums leave NaN
       float d[N], dot;
@@ -135,7 +137,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, VEC, NV>()) balance
         for (int n = 0; n < N; ++n) d[n] += cur[n];
       }
       if (in) store_row<T, VEC, NV>(static_cast<T*>(a.out) + at, rows.room, L.lpr, d);
-      st = st1;
+      st = st1, st1 = st2;
       t0 += step;
       left -= step;
     }

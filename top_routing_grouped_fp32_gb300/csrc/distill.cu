@@ -34,19 +34,17 @@ constexpr float kFarBelow = 1e-30f;
 
 // q log(q/p) - q + p from d = log(q/p); its series where the terms nearly cancel
 // (|d| < 1/2: the first term left out is below 2^-24 of the sum).
+// Without branches: both forms cost less than the divergence between them.
 __device__ __forceinline__ float kl_term(float q, float p, float d) {
-  if (!(q > 0.f)) return q == 0.f ? p : q;  // no mass (its limit), or NaN
-  if (fabsf(d) < 0.5f) {
-    float h = fmaf(d, -1.f / 362880.f, 1.f / 40320.f);
-    h = fmaf(-d, h, 1.f / 5040.f);
-    h = fmaf(-d, h, 1.f / 720.f);
-    h = fmaf(-d, h, 1.f / 120.f);
-    h = fmaf(-d, h, 1.f / 24.f);
-    h = fmaf(-d, h, 1.f / 6.f);
-    h = fmaf(-d, h, 1.f / 2.f);
-    return q * d * d * h;
-  }
-  return fmaf(q, d, p - q);
+  float h = fmaf(d, -1.f / 362880.f, 1.f / 40320.f);
+  h = fmaf(-d, h, 1.f / 5040.f);
+  h = fmaf(-d, h, 1.f / 720.f);
+  h = fmaf(-d, h, 1.f / 120.f);
+  h = fmaf(-d, h, 1.f / 24.f);
+  h = fmaf(-d, h, 1.f / 6.f);
+  h = fmaf(-d, h, 1.f / 2.f);
+  const float t = fabsf(d) < 0.5f ? q * d * d * h : fmaf(q, d, p - q);
+  return q == 0.f ? p : t;  // no mass: its limit
 }
 
 struct FwdArgs {

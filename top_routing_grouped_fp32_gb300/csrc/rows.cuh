@@ -360,8 +360,8 @@ struct ListEntries {
     return dt == MOE_F32 ? 0xff800000u : dt == MOE_F16 ? 0xfc00u : 0xff80u;
   }
   __device__ __forceinline__ float value(uint32_t b) const {
-    if (dt == MOE_F16) return __half2float(__ushort_as_half((unsigned short)b));
-    return __uint_as_float(dt == MOE_F32 ? b : b << 16);
+    const float h = __half2float(__ushort_as_half((unsigned short)b));
+    return dt == MOE_F16 ? h : __uint_as_float(b << (dt == MOE_F32 ? 0 : 16));
   }
 };
 
