@@ -95,7 +95,7 @@ __device__ __forceinline__ void row_scores(const Row& r, float m, float& shift, 
 template <typename T, int VEC, int NV, int LPR, bool SIG>
 __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, VEC, NV>()) balance_fwd_kernel(FwdArgs a) {
   extern __shared__ __align__(16) unsigned char smem[];
-  constexpr int NI = 2;  // indices of a batch that a lane holds ahead of their use
+  constexpr int NI = 4;  // slots that a lane counts at once
   using Stream = RowStream<T, VEC, NV, LPR>;
   using Row = typename Stream::Row;
   constexpr int N = Row::N, S = Stream::kStages;
@@ -146,27 +146,37 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, VEC, NV>()) balance
       rows.issue(on >> i & 1u);
     }
     fetch(S - 1);
-    // the batch's indices, two batches ahead
-    uint32_t id[NI], id1[NI], id2[NI];
-    auto indices = [&](int ahead, uint32_t (&id)[NI]) {
-      const int slots = min(batch, left - ahead * step) * a.k;
-      const uint32_t* ip = a.idx + (t0 + ahead * step) * a.k + lane;
+    // Counts of the piece's slots, 32 NI a warp at a time and behind the rows: 256
+    // experts' rows with top-8 take a turn in four batches.  A turn's indices are on
+    // their way since the last one; a lane adds to its copy.
+    const int slots = (int)(hi - lo) * a.k;
+    int at = warp * 32 * NI;
+    uint32_t id[NI];
+    const uint32_t* ip = a.idx + lo * a.k + lane;
+    auto indices = [&]() {
+#pragma unroll
+      for (int i = 0; i < NI; ++i) id[i] = at + lane + 32 * i < slots ? __ldg(ip + at + 32 * i) : 0u;
+    };
+    auto count = [&]() {
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
-        if (32 * i >= batch * a.k) break;
-        id[i] = lane + 32 * i < slots ? __ldg(ip + 32 * i) : 0u;
+        const int slot = at + lane + 32 * i;
+        bool on = slot < slots;
+        if (a.mask && on) on = __ldg(a.mask + lo + (a.k == 1 ? slot : (int)__umulhi(slot, a.k_magic)));
+        if (on && id[i] < (uint32_t)a.E) atomicAdd(hist + id[i] * a.copies + copy, 1u);
+        bad += on && id[i] >= (uint32_t)a.E;
       }
+      at += kWarps * 32 * NI;
+      indices();
     };
-    indices(0, id);
-    indices(1, id1);
-    Row cur;
-    cur.fill(from_f32<T>(-INFINITY));
+    indices();
+    int due = 0;  // slots of the rows that the block's warps have taken
     while (left > 0) {
+      Row cur;
       rows.take(cur);
       on |= bit(S - 1);
       rows.issue(on >> (S - 1) & 1u);
       fetch(S);
-      indices(2, id2);
       const bool ok = on & 1u;
       float p[N], m = L.max(cur.lane_max());
       row_scores<SIG>(cur, m, m, p);
@@ -185,25 +195,13 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, VEC, NV>()) balance
           zacc = fmaf(lse, lse, zacc);
         }
       }
-      // counts of the batch's slots; a lane adds to its copy
-      const int slots = min(batch, left) * a.k;
-      auto count = [&](int i, uint32_t e) {
-        if (a.mask && !__ldg(a.mask + t0 + (a.k == 1 ? i : (int)__umulhi(i, a.k_magic)))) return;
-        if (e < (uint32_t)a.E) atomicAdd(hist + e * a.copies + copy, 1u);
-        else ++bad;
-      };
-#pragma unroll
-      for (int i = 0; i < NI; ++i) {
-        if (32 * i >= batch * a.k) break;
-        if (lane + 32 * i < slots) count(lane + 32 * i, id[i]);
-      }
-      for (int i = lane + 32 * NI; i < slots; i += 32) count(i, __ldg(a.idx + t0 * a.k + i));
-#pragma unroll
-      for (int i = 0; i < NI; ++i) id[i] = id1[i], id1[i] = id2[i];
+      due += step * a.k;
+      while (at < min(due, slots)) count();
       on >>= 1;
       t0 += step;
       left -= step;
     }
+    while (at < slots) count();
     rows.drain();
     // the rows of a warp, then the warps, in a fixed order
 #pragma unroll

@@ -72,9 +72,8 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, VEC, NV>()) balance
 #pragma unroll
     for (int i = 0; i < S - 1; ++i) rows.issue(sum[i] != 0.f);
     float sum0 = sum[S - 1], sum1 = sum[S];
-    Row cur;
-    cur.fill(from_f32<T>(-INFINITY));
     while (left > 0) {
+      Row cur;
       rows.take(cur);
       rows.issue(sum0 != 0.f);
       sum0 = sum1;
@@ -109,13 +108,14 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, VEC, NV>()) balance
         const float inv = rcp_fast(st.y) * ex.fix();
         ex.row(cur, d);
         if constexpr (N > 1) {
-          float2 dots = both(0.f);
+          float2 dots[2] = {both(0.f), both(0.f)};
 #pragma unroll
           for (int n = 0; n < N; n += 2) {
             put(d, n, mul2(pair(d, n), both(inv)));
-            dots = fma2(pair(d, n), pair(g, n), dots);
+            dots[n / 2 % 2] = fma2(pair(d, n), pair(g, n), dots[n / 2 % 2]);
           }
-          dot = dots.x + dots.y;
+          dots[0] = add2(dots[0], dots[1]);
+          dot = dots[0].x + dots[0].y;
         } else {
           d[0] *= inv;
           dot = d[0] * g[0];

@@ -152,9 +152,8 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, VEC, NV>()) distill
     uint32_t x[J], e[J];
     float rest;
     entries(0, x, e, rest);
-    Row cur;
-    cur.fill(from_f32<T>(-INFINITY));
     while (left > 0) {
+      Row cur;
       rows.take(cur);
       listed[warp][lane] = 0u;
       __syncwarp();  // the rows and the words lie in shared memory
@@ -203,12 +202,12 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, VEC, NV>()) distill
       const RowExp ex(m, a.c);
       float out = 0.f;
       {
-        float p[N], odd = 0.f;
+        float p[N], part[4] = {0.f, 0.f, 0.f, 0.f};
         ex.row(cur, p);
 #pragma unroll
         for (int n = 0; n < N; ++n)
-          if (!(mine & (1u << n))) (n % 2 ? odd : out) += p[n];
-        out += odd;
+          if (!(mine & (1u << n))) part[n % 4] += p[n];
+        out = (part[0] + part[1]) + (part[2] + part[3]);
       }
       const float eq_rest = exp2_fast((rest - mt) * a.c);
       float st = L.sub == 0 ? eq_rest : 0.f, sp = 0.f;

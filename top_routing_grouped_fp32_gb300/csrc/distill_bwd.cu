@@ -96,9 +96,8 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, VEC, NV>()) distill
     uint32_t x[J], e[J];
     entries(0, x, e);
     float st = stat_at(0);
-    Row cur;
-    cur.fill(from_f32<T>(-INFINITY));
     while (left > 0) {
+      Row cur;
       rows.take(cur);
       __syncwarp();  // the rows lie in shared memory; the last batch has left it
       rows.issue(on >> (S - 1) & 1u);

@@ -226,11 +226,11 @@ __global__ void __launch_bounds__(kTargetThreads) distill_targets_kernel(TargetA
     const Key last = out[a.m - 1];
     const float v = to_f32<T>(SK::logit(last));
     const RowExp ex(v, a.c);
-    float p[N], s = 0.f, odd = 0.f;
+    float p[N], part[4] = {0.f, 0.f, 0.f, 0.f};
     ex.row(cur, p);
 #pragma unroll
-    for (int n = 0; n < N; ++n) (n % 2 ? odd : s) += keys[n] < last ? p[n] : 0.f;
-    s = L.sum(s + odd) * ex.fix();
+    for (int n = 0; n < N; ++n) part[n % 4] += keys[n] < last ? p[n] : 0.f;
+    float s = L.sum((part[0] + part[1]) + (part[2] + part[3])) * ex.fix();
     float rest = fmaf(a.tau, logf(s), v);
     // far below it (or nothing, or -inf): about the maximum of what stays
     if (__any_sync(0xffffffffu, !(s >= 1e-30f))) {

@@ -166,15 +166,23 @@ struct RowRegs {
   __device__ __forceinline__ float lane_max() const {
     if constexpr (sizeof(T) == 2 && VEC == 8) {  // two elements an instruction
       using T2 = typename std::conditional<std::is_same<T, __half>::value, __half2, __nv_bfloat162>::type;
-      T2 m = reinterpret_cast<const T2*>(raw)[0];
+      T2 m[N / 2];  // a tree: a chain of N / 2 would wait for itself
 #pragma unroll
-      for (int i = 1; i < N / 2; ++i) m = __hmax2(m, reinterpret_cast<const T2*>(raw)[i]);
-      return fmaxf(to_f32<T>(m.x), to_f32<T>(m.y));
+      for (int i = 0; i < N / 2; ++i) m[i] = reinterpret_cast<const T2*>(raw)[i];
+#pragma unroll
+      for (int w = N / 4; w > 0; w /= 2)
+#pragma unroll
+        for (int i = 0; i < w; ++i) m[i] = __hmax2(m[i], m[i + w]);
+      return fmaxf(to_f32<T>(m[0].x), to_f32<T>(m[0].y));
     } else {
-      float m = (*this)[0];
+      float m[N];
 #pragma unroll
-      for (int n = 1; n < N; ++n) m = fmaxf(m, (*this)[n]);
-      return m;
+      for (int n = 0; n < N; ++n) m[n] = (*this)[n];
+#pragma unroll
+      for (int w = N / 2; w > 0; w /= 2)
+#pragma unroll
+        for (int n = 0; n < w; ++n) m[n] = fmaxf(m[n], m[n + w]);
+      return m[0];
     }
   }
 };
@@ -226,6 +234,17 @@ struct RowStream {
     ring = reinterpret_cast<T*>(static_cast<char*>(smem) + (threadIdx.x >> 5) * kWarpBytes);
     room = E - L.sub * VEC;
     lpr_log = 31 - __clz(L.lpr);
+    if constexpr (VEC > 1) {  // vectors behind the row's end are never copied: they hold -inf
+      Row low;
+      low.fill(from_f32<T>(-INFINITY));
+#pragma unroll
+      for (int i = 0; i < kStages; ++i)
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+          if (v * L.lpr * VEC >= room)
+            *reinterpret_cast<uint4*>(ring + i * kStageElems + (v * 32 + (threadIdx.x & 31)) * VEC) =
+                *reinterpret_cast<const uint4*>(low.raw);
+    }
   }
   // `first`: this group's row of the warp's first batch; a batch every `rows` rows
   __device__ __forceinline__ void start(const T* logits, int64_t first, int64_t rows) {
@@ -251,7 +270,7 @@ struct RowStream {
     p += step;
   }
   // The oldest batch issued becomes the current one.  Elements behind a row's end
-  // keep what `cur` holds; rows that were not loaded hold anything.
+  // are -inf; rows that were not loaded hold anything.
   __device__ __forceinline__ void take(Row& cur) {
     if constexpr (VEC > 1) {
       asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
@@ -259,8 +278,7 @@ struct RowStream {
       const T* from = ring + head * kStageElems + (threadIdx.x & 31) * VEC;
 #pragma unroll
       for (int v = 0; v < NV; ++v)
-        if (v * L.lpr * VEC < room)
-          *reinterpret_cast<uint4*>(cur.raw + v * VEC) = *reinterpret_cast<const uint4*>(from + v * 32 * VEC);
+        *reinterpret_cast<uint4*>(cur.raw + v * VEC) = *reinterpret_cast<const uint4*>(from + v * 32 * VEC);
     } else {
       cur = nxt;
       put(cur);
@@ -279,6 +297,7 @@ struct RowStream {
     T* to = stage() + (threadIdx.x & 31) * VEC;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
+      if (v * L.lpr * VEC >= room) continue;
       if constexpr (VEC > 1)
         *reinterpret_cast<uint4*>(to + v * 32 * VEC) = *reinterpret_cast<const uint4*>(r.raw + v * VEC);
       else
@@ -286,7 +305,15 @@ struct RowStream {
     }
   }
   __device__ __forceinline__ void put(const float (&f)[VEC * NV]) const {
-    store_row<T, VEC, NV>(stage() + (threadIdx.x & 31) * VEC, 32 * VEC * NV, 32, f);
+    T* to = stage() + (threadIdx.x & 31) * VEC;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      if (v * L.lpr * VEC >= room) continue;
+      float g[VEC];
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) g[i] = f[v * VEC + i];
+      store_row<T, VEC, 1>(to + v * 32 * VEC, VEC, 1, g);
+    }
   }
   // Stores this lane's elements of the current batch to `row` (this lane's first).
   __device__ __forceinline__ void store(T* row) const {
@@ -337,10 +364,14 @@ __device__ __forceinline__ float lane_sum(const float (&p)[N]) {
   if constexpr (N == 1) {
     return p[0];
   } else {
-    float2 s = pair(p, 0);
+    float2 s[N / 2];
 #pragma unroll
-    for (int n = 2; n < N; n += 2) s = add2(s, pair(p, n));
-    return s.x + s.y;
+    for (int i = 0; i < N / 2; ++i) s[i] = pair(p, 2 * i);
+#pragma unroll
+    for (int w = N / 4; w > 0; w /= 2)
+#pragma unroll
+      for (int i = 0; i < w; ++i) s[i] = add2(s[i], s[i + w]);
+    return s[0].x + s[0].y;
   }
 }
 
