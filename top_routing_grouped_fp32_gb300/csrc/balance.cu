@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, VEC, NV>()) balance
     for (int i = blockIdx.x * kThreads + threadIdx.x; i < a.seqs.num; i += gridDim.x * kThreads) a.part.ticket[i] = 0u;
   const Lanes<LPR> L(a.lpr);
   Stream rows(L, smem, a.E);
-  const int copy = lane & (a.copies - 1);  // its copy of the histogram
+  const int copy = lane & (a.copies - 1), copies_log = __popc(a.copies - 1);  // its copy of the histogram
   const int batch = L.rows;                // consecutive rows that a warp takes at once
   const int step = kWarps * batch;
 
@@ -133,74 +133,102 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, VEC, NV>()) balance
     // does this group's row of a batch count: bit i for the i-th batch from here.
     // The mask's byte is fetched a batch before its bit is needed.
     uint32_t on = 0;
-    uint8_t byte = 1;
+    uint8_t byte = 1, early[S];
     auto fetch = [&](int ahead) {
       const int i = ahead * step + L.grp;
       if (a.mask) byte = i < left ? __ldg(a.mask + t0 + i) : 0;
     };
     auto bit = [&](int ahead) { return (uint32_t)(ahead * step + L.grp < left && byte) << ahead; };
 #pragma unroll
-    for (int i = 0; i < S - 1; ++i) {
+    for (int i = 0; i < S; ++i) {
       fetch(i);
-      on |= bit(i);
-      rows.issue(on >> i & 1u);
+      early[i] = byte;
     }
-    fetch(S - 1);
+#pragma unroll
+    for (int i = 0; i < S - 1; ++i) {
+      byte = early[i];
+      on |= bit(i);
+      rows.template issue<true>(on >> i & 1u);
+    }
+    byte = early[S - 1];
     // Counts of the piece's slots, 32 NI a warp at a time and behind the rows: 256
     // experts' rows with top-8 take a turn in four batches.  A turn's indices are on
     // their way since the last one; a lane adds to its copy.
     const int slots = (int)(hi - lo) * a.k;
     int at = warp * 32 * NI;
     uint32_t id[NI];
-    const uint32_t* ip = a.idx + lo * a.k + lane;
+    const uint32_t* const ip = a.idx + lo * a.k + lane;
     auto indices = [&]() {
+      if (at + 32 * NI <= slots) {
 #pragma unroll
-      for (int i = 0; i < NI; ++i) id[i] = at + lane + 32 * i < slots ? __ldg(ip + at + 32 * i) : 0u;
+        for (int i = 0; i < NI; ++i) id[i] = __ldg(ip + at + 32 * i);
+      } else {
+#pragma unroll
+        for (int i = 0; i < NI; ++i) id[i] = at + lane + 32 * i < slots ? __ldg(ip + at + 32 * i) : 0u;
+      }
     };
     auto count = [&]() {
+      if (!a.mask && at + 32 * NI <= slots) {
 #pragma unroll
-      for (int i = 0; i < NI; ++i) {
-        const int slot = at + lane + 32 * i;
-        bool on = slot < slots;
-        if (a.mask && on) on = __ldg(a.mask + lo + (a.k == 1 ? slot : (int)__umulhi(slot, a.k_magic)));
-        if (on && id[i] < (uint32_t)a.E) atomicAdd(hist + id[i] * a.copies + copy, 1u);
-        bad += on && id[i] >= (uint32_t)a.E;
+        for (int i = 0; i < NI; ++i) {
+          if (id[i] < (uint32_t)a.E) atomicAdd(hist + (id[i] << copies_log) + copy, 1u);
+          else ++bad;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+          const int slot = at + lane + 32 * i;
+          bool counts = slot < slots;
+          if (a.mask && counts) counts = __ldg(a.mask + lo + (a.k == 1 ? slot : (int)__umulhi(slot, a.k_magic)));
+          if (counts && id[i] < (uint32_t)a.E) atomicAdd(hist + (id[i] << copies_log) + copy, 1u);
+          bad += counts && id[i] >= (uint32_t)a.E;
+        }
       }
       at += kWarps * 32 * NI;
       indices();
     };
     indices();
     int due = 0;  // slots of the rows that the block's warps have taken
+    // A lane keeps the maximum and sum of its group's row of every lpr-th batch; then
+    // the whole warp writes a row's statistics a lane.
+    int turn = 0;
+    float kept_m = 0.f, kept_s = 0.f;
+    auto flush = [&]() {  // the batches from t0 - turn * step on
+      const int64_t t = t0 + (L.sub - turn) * step + L.grp;
+      const bool o = kept_s != 0.f;  // NaN sums count
+      const float s = !SIG || kept_m != 0.f ? kept_s * RowExp(kept_m, kLog2e).fix() : kept_s;
+      if (L.sub < turn && t < hi) {
+        a.row_stats[t] = make_float2(kept_m, s);
+        valid += o;
+        if (!SIG && o) {
+          const float lse = fmaf(log2_fast(s), kLn2, kept_m);
+          zacc = fmaf(lse, lse, zacc);
+        }
+      }
+      turn = 0;
+    };
     while (left > 0) {
       Row cur;
       rows.take(cur);
       on |= bit(S - 1);
-      rows.issue(on >> (S - 1) & 1u);
+      rows.template issue<true>(on >> (S - 1) & 1u);  // (a zero row's scores times 0: no branch)
       fetch(S);
       const bool ok = on & 1u;
       float p[N], m = L.max(cur.lane_max());
       row_scores<SIG>(cur, m, m, p);
-      float s = L.sum(lane_sum(p));
-      if (ok) {
-        const float inv = rcp_fast(s);  // p carries the factor that fix() takes out, too
-        pairwise<N>([&](int n) { put(acc, n, fma2(pair(p, n), both(inv), pair(acc, n))); },
-                    [&](int n) { acc[n] = fmaf(p[n], inv, acc[n]); });
-      }
-      if (L.sub == 0 && L.grp < left) {
-        if (!SIG || m != 0.f) s *= RowExp(m, kLog2e).fix();
-        a.row_stats[t0 + L.grp] = ok ? make_float2(m, s) : make_float2(0.f, 0.f);
-        valid += ok;
-        if (!SIG && ok) {
-          const float lse = fmaf(log2_fast(s), kLn2, m);
-          zacc = fmaf(lse, lse, zacc);
-        }
-      }
+      const float s = L.sum(lane_sum(p));
+      const float inv = ok ? rcp_fast(s) : 0.f;  // p carries the factor that fix() takes out, too
+      pairwise<N>([&](int n) { put(acc, n, fma2(pair(p, n), both(inv), pair(acc, n))); },
+                  [&](int n) { acc[n] = fmaf(p[n], inv, acc[n]); });
+      if (L.sub == turn) kept_m = ok ? m : 0.f, kept_s = ok ? s : 0.f;
       due += step * a.k;
       while (at < min(due, slots)) count();
       on >>= 1;
       t0 += step;
       left -= step;
+      if (++turn == L.lpr) flush();
     }
+    flush();
     while (at < slots) count();
     rows.drain();
     // the rows of a warp, then the warps, in a fixed order

@@ -119,19 +119,24 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, VEC, NV>()) distill
     // does this group's row of a batch count: bit i for the i-th batch from here.
     // The mask's byte is fetched a batch before its bit is needed.
     uint32_t on = 0;
-    uint8_t byte = 1;
+    uint8_t byte = 1, early[S];
     auto fetch = [&](int ahead) {
       const int i = ahead * step + L.grp;
       if (a.mask) byte = i < left ? __ldg(a.mask + t0 + i) : 0;
     };
     auto bit = [&](int ahead) { return (uint32_t)(ahead * step + L.grp < left && byte) << ahead; };
 #pragma unroll
-    for (int i = 0; i < S - 1; ++i) {
+    for (int i = 0; i < S; ++i) {
       fetch(i);
+      early[i] = byte;
+    }
+#pragma unroll
+    for (int i = 0; i < S - 1; ++i) {
+      byte = early[i];
       on |= bit(i);
       rows.issue(on >> i & 1u);
     }
-    fetch(S - 1);
+    byte = early[S - 1];
     // this lane's entries of its row's list, a batch ahead
     const ListEntries list{a.t_logits, a.t_idx, a.t_dt};
     int64_t li = (t0 + L.grp) * a.m + L.sub;

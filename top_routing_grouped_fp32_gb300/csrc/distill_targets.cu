@@ -6,8 +6,6 @@
 namespace moe {
 namespace {
 
-constexpr int kMaxList = 64;
-
 struct TargetArgs {
   const void* logits;
   int E, m, lpr;
@@ -16,6 +14,7 @@ struct TargetArgs {
   uint32_t* idx;
   void* top;
   float* rest;
+  bool vec_out;  // rows of idx and top are whole 16- and 8-byte vectors
 };
 
 // A logit and its expert as one unsigned key: larger logit first, then the lower
@@ -131,63 +130,111 @@ __device__ __forceinline__ void sort_descending(Key (&k)[N]) {
   }
 }
 
-template <int LPR>
-__device__ __forceinline__ uint32_t row_max(const Lanes<LPR>& L, uint32_t k) {
-  if constexpr (LPR == 32) return __reduce_max_sync(0xffffffffu, k);
-  return L.all(k, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
+// ---- merging the lanes' lists --------------------------------------------------
+// A group of S lanes holds a descending list, P keys a lane: lane a of the group has
+// keys a P .. a P + P - 1.  merge() joins the lists of neighbouring groups until a
+// group is a row, and keeps the K largest of a list that gets longer: bitonic
+// networks over registers and shuffles, with nothing that waits for a result of
+// another row.  (Rounds that each take the row's largest head cost as many
+// instructions for a list of 32, and wait for one another.)
+template <typename Key>
+__device__ __forceinline__ Key shfl_xor(Key k, int mask) { return __shfl_xor_sync(0xffffffffu, k, mask); }
+template <typename Key>
+__device__ __forceinline__ Key larger(Key a, Key b) { return a > b ? a : b; }
+template <typename Key>
+__device__ __forceinline__ Key pick(Key a, Key b, bool large) {
+  const Key lo = a > b ? b : a, hi = a > b ? a : b;
+  return large ? hi : lo;
 }
-template <int LPR>
-__device__ __forceinline__ uint64_t row_max(const Lanes<LPR>& L, uint64_t k) {
-  if constexpr (LPR == 32) {
-    const uint32_t hi = row_max(L, (uint32_t)(k >> 32));
-    const uint32_t lo = row_max(L, (uint32_t)(k >> 32) == hi ? (uint32_t)k : 0u);
-    return ((uint64_t)hi << 32) | lo;
+
+// Descending order of a bitonic sequence over the lanes of a group (lane `a` of it,
+// lanes a and a ^ d hold keys P d apart) and the lane's own P keys.
+template <int S, int P, typename Key>
+__device__ __forceinline__ void clean(Key (&x)[P], int a) {
+#pragma unroll
+  for (int d = S / 2; d > 0; d /= 2)
+#pragma unroll
+    for (int p = 0; p < P; ++p) x[p] = pick(x[p], shfl_xor(x[p], d), (a & d) == 0);
+#pragma unroll
+  for (int d = P / 2; d > 0; d /= 2)
+#pragma unroll
+    for (int p = 0; p < P; ++p)
+      if (!(p & d)) order(x[p], x[p + d]);
+}
+
+// `lane`: lane of the warp; `lpr`: lanes of a row.  Calls done(x, P) with the row's
+// list; where K lanes hold it with a key each (P = 1), other lanes hold copies.
+template <int S, int P, int K, int LPR, typename Key, typename F>
+__device__ __forceinline__ void merge(const Key (&x)[P], int lane, int lpr, F done) {
+  if constexpr (S == 32 || (LPR && S == LPR)) {
+    done(x, lane & (S < K ? S - 1 : K - 1));
   } else {
-    return L.all(k, [](uint64_t a, uint64_t b) { return a > b ? a : b; });
+    if (!LPR && S == lpr) {
+      done(x, lane & (S < K ? S - 1 : K - 1));
+      return;
+    }
+    const bool upper = lane & S;
+    if constexpr (2 * S * P <= K) {  // the whole of both lists
+      Key y[P];
+#pragma unroll
+      for (int p = 0; p < P; ++p) y[p] = pick(x[p], shfl_xor(x[P - 1 - p], 2 * S - 1), !upper);
+      clean<S, P>(y, lane & (S - 1));
+      merge<2 * S, P, K, LPR>(y, lane, lpr, done);
+    } else if constexpr (P > 1) {
+      // The K largest are the larger of x_i and the other's x_(K-1-i), a bitonic
+      // sequence.  Lane a of the lower group takes its first P/2 keys, its mirror
+      // lane the others, in descending places.
+      static_assert(S * P == K, "lists of K keys");
+      constexpr int H = P / 2;
+      Key y[H], z[H];
+#pragma unroll
+      for (int p = 0; p < H; ++p) y[p] = larger(x[p], shfl_xor(x[P - 1 - p], 2 * S - 1));
+#pragma unroll
+      for (int p = 0; p < H; ++p) z[p] = upper ? y[H - 1 - p] : y[p];
+      // place of z[p]: a P + p, or a P + H + p on the mirror lane of a
+      const int a = (upper ? ~lane : lane) & (S - 1);
+#pragma unroll
+      for (int d = S / 2; d > 0; d /= 2)
+#pragma unroll
+        for (int p = 0; p < H; ++p) z[p] = pick(z[p], shfl_xor(z[p], d), (a & d) == 0);
+#pragma unroll
+      for (int p = 0; p < H; ++p) z[p] = pick(z[p], shfl_xor(z[p], 2 * S - 1), !upper);
+#pragma unroll
+      for (int d = H / 2; d > 0; d /= 2)
+#pragma unroll
+        for (int p = 0; p < H; ++p)
+          if (!(p & d)) order(z[p], z[p + d]);
+      // lane q of the joined group takes the keys from place q H on
+      const int q = lane & (2 * S - 1), from = (q & 1) ? 2 * S - 1 - q / 2 : q / 2;
+#pragma unroll
+      for (int p = 0; p < H; ++p) z[p] = __shfl_sync(0xffffffffu, z[p], (lane & ~(2 * S - 1)) | from);
+      merge<2 * S, H, K, LPR>(z, lane, lpr, done);
+    } else {
+      // a key a lane on K lanes, with copies on the other lanes of the group
+      Key y[1] = {larger(x[0], shfl_xor(x[0], S | (K - 1)))};
+      clean<K, 1>(y, lane & (K - 1));
+      merge<2 * S, 1, K, LPR>(y, lane, lpr, done);
+    }
   }
 }
 
-// One round: where this lane's head is the row's largest, it goes to out[j] and
-// the next of the lane's list takes its place.  (Written out so that no lane
-// branches.)
-__device__ __forceinline__ void take(uint32_t best, uint32_t& head, uint32_t& next, uint32_t out) {
-  asm volatile("{\n .reg .pred p;\n setp.eq.u32 p, %0, %2;\n @p st.shared.u32 [%3], %0;\n @p ld.shared.u32 %0, [%1];\n"
-               " @p add.u32 %1, %1, 128;\n}"
-               : "+r"(head), "+r"(next)
-               : "r"(best), "r"(out)
-               : "memory");
-}
-__device__ __forceinline__ void take(uint64_t best, uint64_t& head, uint32_t& next, uint32_t out) {
-  asm volatile("{\n .reg .pred p;\n setp.eq.u64 p, %0, %2;\n @p st.shared.u64 [%3], %0;\n @p ld.shared.u64 %0, [%1];\n"
-               " @p add.u32 %1, %1, 256;\n}"
-               : "+l"(head), "+r"(next)
-               : "l"(best), "r"(out)
-               : "memory");
-}
-
-// Each lane sorts its share of the row; then m rounds take the largest head of
-// the row's lanes.  A round is one reduction, a compare and the winner's next
-// entry from shared memory: its cost does not grow with the row, and with eight
-// lanes a row a warp takes four rows' entries in a round.
+// Each lane sorts its share of the row, the lanes' lists are merged, and the rest is
+// summed about the last key that was taken.
 constexpr int kTargetThreads = 128;
 constexpr int kTargetBlocks = 152 * 8;
-template <typename T, int VEC, int NV, int LPR>
-__global__ void __launch_bounds__(kTargetThreads) distill_targets_kernel(TargetArgs a) {
-  constexpr int N = VEC * NV, W = kTargetThreads / 32;
+template <typename T, int VEC, int NV, int LPR, int K>
+__global__ void __launch_bounds__(kTargetThreads, VEC * NV * sizeof(T) <= 64 ? 4 : 2) distill_targets_kernel(TargetArgs a) {
+  constexpr int W = kTargetThreads / 32;
   using Row = RowRegs<T, VEC, NV>;
   using SK = SortKey<T>;
   using Key = typename SK::Key;
-  // taken[]: [rows][m] in order; m <= E bounds it where a row has few lanes
-  constexpr int kTaken = LPR ? 32 / (LPR ? LPR : 1) * kMaxList : 32 * N;
-  __shared__ Key lists[W][N + 1][32];  // entry N ends a list: below every key
-  __shared__ Key taken[W][kTaken];
+  constexpr int N = Row::N, P0 = N < K ? N : K;
   pdl_wait();
   pdl_trigger();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const Lanes<LPR> L(a.lpr);
   const int room = a.E - L.sub * VEC;
   T* top = static_cast<T*>(a.top);
-  lists[warp][N][lane] = 0;
   const int64_t step = (int64_t)gridDim.x * W * L.rows;
   int64_t t0 = ((int64_t)blockIdx.x * W + warp) * L.rows;
   const T* lp = static_cast<const T*>(a.logits) + (t0 + L.grp) * a.E + L.sub * VEC;
@@ -201,58 +248,73 @@ __global__ void __launch_bounds__(kTargetThreads) distill_targets_kernel(TargetA
     const int64_t t = t0 + L.grp;
     const bool in = t < a.T;
     typename SK::template Keys<VEC, NV> keys(cur, L.lpr, L.sub);
-    Key head;
-    {
-      Key list[N];
+    Key list[N], best[P0];
 #pragma unroll
-      for (int n = 0; n < N; ++n) list[n] = keys[n];
-      sort_descending<0, N>(list);
+    for (int n = 0; n < N; ++n) list[n] = keys[n];
+    sort_descending<0, N>(list);
 #pragma unroll
-      for (int n = 0; n < N; ++n) lists[warp][n][lane] = list[n];
-      head = list[0];
-    }
-    Key* out = &taken[warp][L.grp * a.m];
-    uint32_t next = (uint32_t)__cvta_generic_to_shared(&lists[warp][1][lane]);
-    const uint32_t out_at = (uint32_t)__cvta_generic_to_shared(out);
-    Key best = row_max(L, head);
-    const bool broken = SK::broken(best);
-#pragma unroll 4
-    for (int j = 0; j < a.m; ++j) {
-      take(best, head, next, out_at + j * (int)sizeof(Key));
-      best = row_max(L, head);
-    }
-    __syncwarp();
-    // what stays, about the last one taken
-    const Key last = out[a.m - 1];
-    const float v = to_f32<T>(SK::logit(last));
-    const RowExp ex(v, a.c);
-    float p[N], part[4] = {0.f, 0.f, 0.f, 0.f};
-    ex.row(cur, p);
+    for (int p = 0; p < P0; ++p) best[p] = list[p];
+    merge<1, P0, K, LPR>(best, lane, L.lpr, [&](const auto& x, int q) {
+      constexpr int P = sizeof(x) / sizeof(Key);
+      const bool broken = SK::broken(__shfl_sync(0xffffffffu, x[0], L.grp * L.lpr));
+      Key last = x[0];
 #pragma unroll
-    for (int n = 0; n < N; ++n) part[n % 4] += keys[n] < last ? p[n] : 0.f;
-    float s = L.sum((part[0] + part[1]) + (part[2] + part[3])) * ex.fix();
-    float rest = fmaf(a.tau, logf(s), v);
-    // far below it (or nothing, or -inf): about the maximum of what stays
-    if (__any_sync(0xffffffffu, !(s >= 1e-30f))) {
-      float mr = -INFINITY;
+      for (int p = 1; p < P; ++p)
+        if (p == (a.m - 1) % P) last = x[p];
+      last = __shfl_sync(0xffffffffu, last, L.grp * L.lpr + (a.m - 1) / P);
+      const float v = to_f32<T>(SK::logit(last));
+      const RowExp ex(v, a.c);
+      float e[N], s = 0.f, odd = 0.f;
+      ex.row(cur, e);
 #pragma unroll
-      for (int n = 0; n < N; ++n) mr = keys[n] < last ? fmaxf(mr, cur[n]) : mr;
-      mr = L.max(mr);
-      float sr = 0.f;
+      for (int n = 0; n < N; ++n) (n % 2 ? odd : s) += keys[n] < last ? e[n] : 0.f;
+      s = L.sum(s + odd) * ex.fix();
+      float rest = fmaf(a.tau, logf(s), v);
+      // far below it (or nothing, or -inf): about the maximum of what stays
+      if (__any_sync(0xffffffffu, !(s >= 1e-30f))) {
+        float mr = -INFINITY;
 #pragma unroll
-      for (int n = 0; n < N; ++n) sr += keys[n] < last ? exp2_fast((cur[n] - mr) * a.c) : 0.f;
-      sr = L.sum(sr);
-      if (!(s >= 1e-30f)) rest = mr == -INFINITY ? -INFINITY : fmaf(a.tau, logf(sr), mr);
-    }
-    if (in) {
-      for (int j = L.sub; j < a.m; j += L.lpr) {
-        const Key k = out[j];
-        a.idx[t * a.m + j] = broken ? (uint32_t)j : SK::id(k);
-        top[t * a.m + j] = broken ? from_f32<T>(NAN) : SK::logit(k);
+        for (int n = 0; n < N; ++n) mr = keys[n] < last ? fmaxf(mr, cur[n]) : mr;
+        mr = L.max(mr);
+        float sr = 0.f;
+#pragma unroll
+        for (int n = 0; n < N; ++n) sr += keys[n] < last ? exp2_fast((cur[n] - mr) * a.c) : 0.f;
+        sr = L.sum(sr);
+        if (!(s >= 1e-30f)) rest = mr == -INFINITY ? -INFINITY : fmaf(a.tau, logf(sr), mr);
       }
+      if (!in) return;
       if (L.sub == 0) a.rest[t] = broken ? NAN : rest;
-    }
-    __syncwarp();  // before the next row's lists
+      if (L.sub != q) return;  // a copy
+      uint32_t ids[P];
+      T tops[P];
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        ids[p] = broken ? (uint32_t)(q * P + p) : SK::id(x[p]);
+        tops[p] = broken ? from_f32<T>(NAN) : SK::logit(x[p]);
+      }
+      uint32_t* const to = a.idx + t * a.m + q * P;
+      T* const tl = top + t * a.m + q * P;
+      if (P >= 4 && a.vec_out && a.m % P == 0) {  // whole vectors
+        if (q * P < a.m) {
+          if constexpr (P >= 4) {
+#pragma unroll
+            for (int p = 0; p < P; p += 4) {
+              *reinterpret_cast<uint4*>(to + p) = make_uint4(ids[p], ids[p + 1], ids[p + 2], ids[p + 3]);
+              if constexpr (sizeof(T) == 4) {
+                *reinterpret_cast<float4*>(tl + p) = make_float4(tops[p], tops[p + 1], tops[p + 2], tops[p + 3]);
+              } else {
+                alignas(8) T h[4] = {tops[p], tops[p + 1], tops[p + 2], tops[p + 3]};
+                *reinterpret_cast<uint2*>(tl + p) = *reinterpret_cast<const uint2*>(h);
+              }
+            }
+          }
+        }
+      } else {
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+          if (q * P + p < a.m) to[p] = ids[p], tl[p] = tops[p];
+      }
+    });
     cur = nxt;
   }
 }
@@ -260,12 +322,23 @@ __global__ void __launch_bounds__(kTargetThreads) distill_targets_kernel(TargetA
 struct LaunchTargets {
   TargetArgs a;
   cudaStream_t s;
-  template <typename T, int VEC, int NV, int LPR>
-  cudaError_t run() {
+  template <typename T, int VEC, int NV, int LPR, int K>
+  cudaError_t with() {
     const int64_t per = (int64_t)(kTargetThreads / 32) * (32 / a.lpr);
     const int64_t blocks = (a.T + per - 1) / per;
-    return launch_pdl(distill_targets_kernel<T, VEC, NV, LPR>,
-                      dim3((unsigned)(blocks < kTargetBlocks ? blocks : kTargetBlocks)), dim3(kTargetThreads), 0, s, a);
+    return launch_pdl(distill_targets_kernel<T, VEC, NV, LPR, K>,
+                      dim3((unsigned)(blocks < kTargetBlocks ? blocks : kTargetBlocks)), dim3(kTargetThreads), 0, s,
+                      a);
+  }
+  // the shortest kept list that holds m keys (fewer lengths where rows are rarer)
+  template <typename T, int VEC, int NV, int LPR>
+  cudaError_t run() {
+    if constexpr (VEC > 1) {
+      if (a.m <= 8) return with<T, VEC, NV, LPR, 8>();
+      if constexpr (sizeof(T) == 2)
+        if (a.m <= 32) return with<T, VEC, NV, LPR, 32>();
+    }
+    return with<T, VEC, NV, LPR, 64>();
   }
 };
 
@@ -275,7 +348,10 @@ cudaError_t launch_distill_targets(const void* logits, moe_dtype dt, int64_t T, 
                                    uint32_t* idx, void* top, float* rest, cudaStream_t s) {
   const void* ptrs[] = {logits};
   const RowPlan plan = row_plan(ptrs, 1, dt, E);
-  LaunchTargets f{TargetArgs{logits, E, m, plan.lpr, T, temperature, kLog2e / temperature, idx, top, rest}, s};
+  const bool vec_out = m % 4 == 0 && reinterpret_cast<uintptr_t>(idx) % 16 == 0 &&
+                       reinterpret_cast<uintptr_t>(top) % (4 * dtype_size(dt)) == 0;
+  LaunchTargets f{TargetArgs{logits, E, m, plan.lpr, T, temperature, kLog2e / temperature, idx, top, rest, vec_out},
+                  s};
   return with_row_variant(dt, plan, f);
 }
 

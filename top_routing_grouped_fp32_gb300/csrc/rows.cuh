@@ -161,6 +161,11 @@ struct RowRegs {
       }
     }
   }
+  __device__ __forceinline__ void zero(int room, int lpr) {
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+      if (n / VEC * lpr * VEC < room) raw[n] = from_f32<T>(0.f);
+  }
   __device__ __forceinline__ float operator[](int n) const { return to_f32<T>(raw[n]); }
   // This lane's maximum; passes over NaN.
   __device__ __forceinline__ float lane_max() const {
@@ -253,24 +258,29 @@ struct RowStream {
     head = tail = 0;
     nxt.fill(from_f32<T>(-INFINITY));
   }
+  // Rows that are not `ok` are not read: their cells keep what they hold, or are
+  // zeroed (ZERO).
+  template <bool ZERO = false>
   __device__ __forceinline__ void issue(bool ok) {
     if constexpr (VEC > 1) {
       const uint32_t to =
           (uint32_t)__cvta_generic_to_shared(ring + tail * kStageElems) + (threadIdx.x & 31) * 16;
 #pragma unroll
       for (int v = 0; v < NV; ++v)
-        if (ok && v * L.lpr * VEC < room)
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + v * 512), "l"(p + v * L.lpr * VEC)
+        if ((ZERO || ok) && v * L.lpr * VEC < room)  // (a copy of 0 bytes writes zeros)
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + v * 512),
+                       "l"(p + v * L.lpr * VEC), "r"(ok ? 16 : 0)
                        : "memory");
       asm volatile("cp.async.commit_group;" ::: "memory");
       tail = tail + 1 == kStages ? 0 : tail + 1;
     } else {
       nxt.load(p, room, L.lpr, ok);
+      if (ZERO && !ok) nxt.zero(room, L.lpr);
     }
     p += step;
   }
   // The oldest batch issued becomes the current one.  Elements behind a row's end
-  // are -inf; rows that were not loaded hold anything.
+  // are -inf.
   __device__ __forceinline__ void take(Row& cur) {
     if constexpr (VEC > 1) {
       asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
