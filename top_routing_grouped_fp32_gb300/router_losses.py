@@ -27,7 +27,7 @@ from dataclasses import dataclass
 import torch
 
 from . import _lib
-from ._lib import MoeError
+from ._lib import MoeError, check as _check
 
 _CODES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 _SCORING = {"softmax": 0, "sigmoid": 1}
@@ -62,15 +62,46 @@ def _p(t, what: str, dtypes, shape, device):
     """Data pointer of a checked tensor (None passes)."""
     if t is None:
         return None
-    if dtypes is not None and t.dtype not in dtypes:
+    if t.dtype in dtypes and t.shape == shape and t.device == device and t.is_contiguous():
+        return t.data_ptr()
+    if t.dtype not in dtypes:
         raise MoeError(3, f"{what} dtype {t.dtype} is not one of {', '.join(str(d) for d in dtypes)}")
     if t.shape != shape:
         raise MoeError(2, f"{what} must have shape {tuple(shape)} (got {tuple(t.shape)})")
     if t.device != device:
         raise ValueError(f"{what} is on {t.device}, the logits are on {device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{what}: expected a contiguous tensor")
-    return t.data_ptr()
+    raise ValueError(f"{what}: expected a contiguous tensor")
+
+
+class _Checked:
+    """Tensors that a call writes or hands on, checked once for their sizes and
+    again whenever one of them is replaced; a training step passes them call
+    after call.  Pointers are read anew each time."""
+
+    def __setattr__(self, name, value):
+        self.__dict__[name] = value
+        if name != "workspace":
+            self.__dict__["_checked"] = None
+
+    def _pointers(self, device, *sizes):
+        """Data pointers of _tensors(*sizes) in their order."""
+        d = self.__dict__
+        if d.get("_checked") != (device, sizes):
+            named = [(n, dt, shape) for n, dt, shape in self._tensors(*sizes) if d[n] is not None]
+            for n, dt, shape in named:
+                _p(d[n], n, dt, shape, device)
+            d["_elements"] = [(d[n], d[n].numel()) if d[n] is not None else None
+                              for n, _, _ in self._tensors(*sizes)]
+            d["_checked"] = (device, sizes)
+        out = []
+        for e in d["_elements"]:
+            if e is None:
+                out.append(None)
+            elif e[0].numel() != e[1]:
+                raise MoeError(2, "a tensor of the results was resized")
+            else:
+                out.append(e[0].data_ptr())
+        return out
 
 
 def _ws(t, device):
@@ -98,8 +129,26 @@ def _on(device: torch.device, stream):
     return _NOTHING
 
 
+# the current stream's handle without a Stream object around it, where torch offers it
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _raw_stream(device, stream) -> int:
-    return (stream if stream is not None else torch.cuda.current_stream(device)).cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    if _current_raw_stream is not None:
+        return _current_raw_stream(device.index)
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+_lib_handle = None
+
+
+def _load():
+    global _lib_handle
+    if _lib_handle is None:
+        _lib_handle = _lib.load()
+    return _lib_handle
 
 
 def _buffer(nbytes: int, device) -> torch.Tensor:
@@ -108,7 +157,7 @@ def _buffer(nbytes: int, device) -> torch.Tensor:
 
 
 @dataclass
-class BalanceLoss:
+class BalanceLoss(_Checked):
     """What moe_balance_loss gives and moe_balance_loss_backward takes (it reads
     counts, tokens and row_stats)."""
     loss: torch.Tensor                # float32 [S]
@@ -129,9 +178,14 @@ class BalanceLoss:
         S = num_seqs
         return cls(f32(S), f32(S) if z_loss else None, f32(S, E), i32(S, E), i32(S), f32(T, 2))
 
+    @staticmethod
+    def _tensors(T, E, S):
+        return (("loss", _F32, (S,)), ("z_loss", _F32, (S,)), ("mean_scores", _F32, (S, E)),
+                ("counts", _I32, (S, E)), ("tokens", _I32, (S,)), ("row_stats", _F32, (T, 2)))
+
 
 def moe_balance_loss_workspace(T: int, E: int, num_seqs: int = 1, device="cuda") -> torch.Tensor:
-    return _buffer(_lib.load().moe_balance_loss_workspace_size(T, E, num_seqs), device)
+    return _buffer(_load().moe_balance_loss_workspace_size(T, E, num_seqs), device)
 
 
 def moe_balance_loss(logits: torch.Tensor, idx: torch.Tensor, scoring: str = "softmax",
@@ -140,13 +194,13 @@ def moe_balance_loss(logits: torch.Tensor, idx: torch.Tensor, scoring: str = "so
                      workspace: torch.Tensor | None = None, stream=None) -> BalanceLoss:
     """Balance loss, per-expert counts, mean scores and (``z_loss``) the z-loss
     of router logits [T,E] and their routed experts idx [T,k] (int32)."""
-    lib = _lib.load()
+    lib = _load()
     T, E = _rows_of(logits, "logits")
     code, sc = _code(logits, "logits"), _scoring(scoring)
     if idx.dim() != 2:
         raise MoeError(2, "idx must be [T, top_k]")
     k, S, dev = idx.shape[1], _num_seqs(seq_offsets), logits.device
-    args = (_p(logits, "logits", None, (T, E), dev), code, _p(idx, "idx", _I32, (T, k), dev),
+    args = (_p(logits, "logits", (logits.dtype,), (T, E), dev), code, _p(idx, "idx", _I32, (T, k), dev),
             _p(token_mask, "token_mask", _MASK, (T,), dev), _p(seq_offsets, "seq_offsets", _I32, (S + 1,), dev),
             T, E, k, S, sc)
     with _on(dev, stream):
@@ -158,11 +212,7 @@ def moe_balance_loss(logits: torch.Tensor, idx: torch.Tensor, scoring: str = "so
             workspace = moe_balance_loss_workspace(T, E, S, dev)
         out.workspace = workspace
         ws, nbytes = _ws(workspace, dev)
-        _lib.check(lib.moe_balance_loss(
-            *args, _p(out.loss, "loss", _F32, (S,), dev), _p(out.z_loss, "z_loss", _F32, (S,), dev),
-            _p(out.mean_scores, "mean_scores", _F32, (S, E), dev), _p(out.counts, "counts", _I32, (S, E), dev),
-            _p(out.tokens, "tokens", _I32, (S,), dev), _p(out.row_stats, "row_stats", _F32, (T, 2), dev),
-            ws, nbytes, _raw_stream(dev, stream)))
+        _check(lib.moe_balance_loss(*args, *out._pointers(dev, T, E, S), ws, nbytes, _raw_stream(dev, stream)))
     return out
 
 
@@ -173,25 +223,25 @@ def moe_balance_loss_backward(logits: torch.Tensor, forward: BalanceLoss, top_k:
     """dlogits [T,E] = base + gradient of sum(dloss * loss) (+ sum(dz_loss *
     z_loss)), dloss and dz_loss float32 [S].  ``dlogits`` is written if given
     (it may be ``base``)."""
-    lib = _lib.load()
+    lib = _load()
     T, E = _rows_of(logits, "logits")
     code, sc = _code(logits, "logits"), _scoring(scoring)
     S, dev, dt = _num_seqs(seq_offsets), logits.device, (logits.dtype,)
-    args = (_p(logits, "logits", None, (T, E), dev), code, _p(forward.row_stats, "row_stats", _F32, (T, 2), dev),
-            _p(forward.counts, "counts", _I32, (S, E), dev), _p(forward.tokens, "tokens", _I32, (S,), dev),
+    _, _, _, counts, tokens, row_stats = forward._pointers(dev, T, E, S)
+    args = (_p(logits, "logits", dt, (T, E), dev), code, row_stats, counts, tokens,
             _p(seq_offsets, "seq_offsets", _I32, (S + 1,), dev), T, E, top_k, S, sc,
             _p(dloss, "dloss", _F32, (S,), dev), _p(dz_loss, "dz_loss", _F32, (S,), dev),
             _p(base, "base", dt, (T, E), dev))
     with _on(dev, stream):
         if dlogits is None:
             dlogits = torch.empty((T, E), dtype=logits.dtype, device=dev)
-        _lib.check(lib.moe_balance_loss_backward(*args, _p(dlogits, "dlogits", dt, (T, E), dev),
-                                                 _raw_stream(dev, stream)))
+        _check(lib.moe_balance_loss_backward(*args, _p(dlogits, "dlogits", dt, (T, E), dev),
+                                             _raw_stream(dev, stream)))
     return dlogits
 
 
 @dataclass
-class DistillTargets:
+class DistillTargets(_Checked):
     """A teacher's top logits: what moe_distill_targets gives and the
     distillation loss takes.  ``rest`` may be None: no mass outside the list."""
     idx: torch.Tensor           # int32 [T,m]
@@ -204,12 +254,15 @@ class DistillTargets:
                    torch.empty((T, top_m), dtype=dtype, device=device),
                    torch.empty((T,), dtype=torch.float32, device=device))
 
+    def _tensors(self, T, m):
+        return ("idx", _I32, (T, m)), ("logits", (self.logits.dtype,), (T, m)), ("rest", _F32, (T,))
+
 
 def moe_distill_targets(teacher_logits: torch.Tensor, top_m: int, temperature: float = 1.0,
                         out: DistillTargets | None = None, stream=None) -> DistillTargets:
     """The top_m largest of each row of a teacher's logits [T,E] and the logit of
     all its other experts together at ``temperature``."""
-    lib = _lib.load()
+    lib = _load()
     T, E = _rows_of(teacher_logits, "teacher_logits")
     code, dev, dt = _code(teacher_logits, "teacher_logits"), teacher_logits.device, teacher_logits.dtype
     if out is None and not 1 <= top_m <= E:
@@ -219,15 +272,15 @@ def moe_distill_targets(teacher_logits: torch.Tensor, top_m: int, temperature: f
             out = DistillTargets.empty(T, top_m, dt, dev)
         if out.rest is None:
             raise MoeError(1, "out has no rest")
-        _lib.check(lib.moe_distill_targets(
-            _p(teacher_logits, "teacher_logits", None, (T, E), dev), code, T, E, top_m, temperature,
-            _p(out.idx, "idx", _I32, (T, top_m), dev), _p(out.logits, "logits", (dt,), (T, top_m), dev),
-            _p(out.rest, "rest", _F32, (T,), dev), _raw_stream(dev, stream)))
+        if out.logits.dtype != dt:
+            raise MoeError(3, f"out.logits dtype {out.logits.dtype} is not the teacher logits' {dt}")
+        _check(lib.moe_distill_targets(_p(teacher_logits, "teacher_logits", (dt,), (T, E), dev), code, T, E, top_m,
+                                       temperature, *out._pointers(dev, T, top_m), _raw_stream(dev, stream)))
     return out
 
 
 @dataclass
-class DistillLoss:
+class DistillLoss(_Checked):
     """What moe_distill_loss gives and moe_distill_loss_backward takes (it reads
     tokens and row_stats)."""
     loss: torch.Tensor       # float32 [S]
@@ -242,17 +295,21 @@ class DistillLoss:
             return torch.empty(shape, dtype=torch.float32, device=device)
         return cls(f32(num_seqs), torch.empty((num_seqs,), dtype=torch.int32, device=device), f32(T), f32(5, T))
 
+    @staticmethod
+    def _tensors(T, S):
+        return ("loss", _F32, (S,)), ("tokens", _I32, (S,)), ("row_loss", _F32, (T,)), ("row_stats", _F32, (5, T))
+
 
 def _list_args(targets: DistillTargets, T: int, dev):
     if targets.idx.dim() != 2:
         raise MoeError(2, "targets.idx must be [T, top_m]")
     m = targets.idx.shape[1]
-    return m, (_p(targets.idx, "targets.idx", _I32, (T, m), dev),
-               _p(targets.logits, "targets.logits", None, (T, m), dev), _code(targets.logits, "targets.logits"))
+    idx, logits, rest = targets._pointers(dev, T, m)
+    return m, (idx, logits, _code(targets.logits, "targets.logits")), rest
 
 
 def moe_distill_loss_workspace(T: int, num_seqs: int = 1, device="cuda") -> torch.Tensor:
-    return _buffer(_lib.load().moe_distill_loss_workspace_size(T, num_seqs), device)
+    return _buffer(_load().moe_distill_loss_workspace_size(T, num_seqs), device)
 
 
 def moe_distill_loss(logits: torch.Tensor, targets: DistillTargets, temperature: float = 1.0,
@@ -260,12 +317,12 @@ def moe_distill_loss(logits: torch.Tensor, targets: DistillTargets, temperature:
                      out: DistillLoss | None = None, workspace: torch.Tensor | None = None,
                      stream=None) -> DistillLoss:
     """Mean KL divergence of student logits [T,E] from a teacher's lists."""
-    lib = _lib.load()
+    lib = _load()
     T, E = _rows_of(logits, "logits")
     code, S, dev = _code(logits, "logits"), _num_seqs(seq_offsets), logits.device
-    m, lists = _list_args(targets, T, dev)
-    args = (_p(logits, "logits", None, (T, E), dev), code, *lists,
-            _p(targets.rest, "targets.rest", _F32, (T,), dev), _p(token_mask, "token_mask", _MASK, (T,), dev),
+    m, lists, rest = _list_args(targets, T, dev)
+    args = (_p(logits, "logits", (logits.dtype,), (T, E), dev), code, *lists, rest,
+            _p(token_mask, "token_mask", _MASK, (T,), dev),
             _p(seq_offsets, "seq_offsets", _I32, (S + 1,), dev), T, E, m, S, temperature)
     with _on(dev, stream):
         if out is None:
@@ -274,10 +331,7 @@ def moe_distill_loss(logits: torch.Tensor, targets: DistillTargets, temperature:
             workspace = moe_distill_loss_workspace(T, S, dev)
         out.workspace = workspace
         ws, nbytes = _ws(workspace, dev)
-        _lib.check(lib.moe_distill_loss(
-            *args, _p(out.loss, "loss", _F32, (S,), dev), _p(out.tokens, "tokens", _I32, (S,), dev),
-            _p(out.row_loss, "row_loss", _F32, (T,), dev), _p(out.row_stats, "row_stats", _F32, (5, T), dev),
-            ws, nbytes, _raw_stream(dev, stream)))
+        _check(lib.moe_distill_loss(*args, *out._pointers(dev, T, S), ws, nbytes, _raw_stream(dev, stream)))
     return out
 
 
@@ -287,17 +341,17 @@ def moe_distill_loss_backward(logits: torch.Tensor, targets: DistillTargets, for
                               dlogits: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """dlogits [T,E] = base + gradient of sum(dloss * loss), dloss float32 [S].
     ``dlogits`` is written if given (it may be ``base``)."""
-    lib = _lib.load()
+    lib = _load()
     T, E = _rows_of(logits, "logits")
     code, S, dev, dt = _code(logits, "logits"), _num_seqs(seq_offsets), logits.device, (logits.dtype,)
-    m, lists = _list_args(targets, T, dev)
-    args = (_p(logits, "logits", None, (T, E), dev), code, *lists,
-            _p(forward.row_stats, "row_stats", _F32, (5, T), dev), _p(forward.tokens, "tokens", _I32, (S,), dev),
+    m, lists, _ = _list_args(targets, T, dev)
+    _, tokens, _, row_stats = forward._pointers(dev, T, S)
+    args = (_p(logits, "logits", dt, (T, E), dev), code, *lists, row_stats, tokens,
             _p(seq_offsets, "seq_offsets", _I32, (S + 1,), dev), T, E, m, S, temperature,
             _p(dloss, "dloss", _F32, (S,), dev), _p(base, "base", dt, (T, E), dev))
     with _on(dev, stream):
         if dlogits is None:
             dlogits = torch.empty((T, E), dtype=logits.dtype, device=dev)
-        _lib.check(lib.moe_distill_loss_backward(*args, _p(dlogits, "dlogits", dt, (T, E), dev),
-                                                 _raw_stream(dev, stream)))
+        _check(lib.moe_distill_loss_backward(*args, _p(dlogits, "dlogits", dt, (T, E), dev),
+                                             _raw_stream(dev, stream)))
     return dlogits
