@@ -15,11 +15,15 @@
 // second kernel adds each sequence's slots in a fixed order; a batch that one
 // block holds needs none.  The counts are integers, so shared-memory atomics
 // leave them reproducible.
+#include <cooperative_groups.h>
+
 #include "internal.h"
 #include "rows.cuh"
 
 namespace moe {
 namespace {
+
+namespace cg = cooperative_groups;
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
@@ -31,10 +35,7 @@ struct Partials {
   float* z;           // [slots] sums of squared log-sum-exps
   uint32_t* rows;     // [slots] valid rows
   uint32_t* bad;      // [slots] indices that are no expert
-  float* share;       // [num_seqs, kMaxShares] a finishing block's part of the loss
-  uint32_t* ticket;   // [num_seqs] finishing blocks that are done
 };
-constexpr int kMaxShares = 32;
 
 struct Results {
   float* loss;
@@ -108,8 +109,6 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, VEC, NV>()) balance
   pdl_trigger();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (blockIdx.x == 0 && threadIdx.x == 0) *a.res.status = 0u;
-  if (!a.alone)
-    for (int i = blockIdx.x * kThreads + threadIdx.x; i < a.seqs.num; i += gridDim.x * kThreads) a.part.ticket[i] = 0u;
   const Lanes<LPR> L(a.lpr);
   Stream rows(L, smem, a.E);
   const int copy = lane & (a.copies - 1), copies_log = __popc(a.copies - 1);  // its copy of the histogram
@@ -120,8 +119,6 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, VEC, NV>()) balance
     for (int64_t t = lo + threadIdx.x; t < hi; t += kThreads) a.row_stats[t] = make_float2(0.f, 0.f);
   };
   auto piece = [&](int seq, int64_t lo, int64_t hi) {
-    for (int i = threadIdx.x; i < a.E * a.copies; i += kThreads) hist[i] = 0u;
-    __syncthreads();
     uint32_t bad = 0, valid = 0;
     float acc[N], zacc = 0.f;
 #pragma unroll
@@ -188,6 +185,8 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, VEC, NV>()) balance
       indices();
     };
     indices();
+    for (int i = threadIdx.x; i < a.E * a.copies; i += kThreads) hist[i] = 0u;
+    __syncthreads();
     int due = 0;  // slots of the rows that the block's warps have taken
     // A lane keeps the maximum and sum of its group's row of every lpr-th batch; then
     // the whole warp writes a row's statistics a lane.
@@ -305,96 +304,106 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, VEC, NV>()) balance
 struct FinishArgs {
   Partials part;
   Seqs seqs;
-  int E, k, blocks;  // blocks of a sequence
+  int E, k;
   int64_t chunk_rows;
   Results res;
 };
 
-// Adds a sequence's slots, 32 experts x one slot lane a warp at a time.  A
-// sequence has `blocks` blocks, each with every blocks-th group of 32 experts; the
-// one that finishes last adds their shares of the loss, in order.
+// Adds a sequence's slots, 32 experts x W slot lanes at a time.  A sequence has a
+// cluster of blocks, each with every blocks-th group of 32 experts; block 0 adds
+// their shares of the loss in order.
 template <int W>
 __global__ void __launch_bounds__(32 * W) balance_finish_kernel(FinishArgs a) {
-  __shared__ float sp[W][33];
-  __shared__ uint32_t sn[W][33];
-  __shared__ float sz[W];
+  __shared__ float sp[32][W + 1];
+  __shared__ uint32_t sn[32][W + 1];
+  __shared__ float sz[W], snp[W], share;
   __shared__ uint32_t sv[W], sb[W];
+  cg::cluster_group cl = cg::this_cluster();
+  const uint32_t part = cl.block_rank(), blocks = cl.num_blocks();
+  const uint32_t s = blockIdx.x / blocks;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  auto add = [](auto x) {
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
+    return x;
+  };
   pdl_wait();
   pdl_trigger();
-  const int s = blockIdx.x / a.blocks, part = blockIdx.x % a.blocks;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t lo = a.seqs.at(s), hi = a.seqs.at(s + 1);
-  if (part == 0 && threadIdx.x == 0 && a.seqs.off &&
-      (hi < lo || (int64_t)__ldg(a.seqs.off + s) > a.seqs.T || (int64_t)__ldg(a.seqs.off + s + 1) > a.seqs.T))
-    set_status(a.res.status, MOE_ERR_INVALID_INDEX);
-  // slots first..last hold the sequence
-  int64_t first = 0, last = -1;
-  if (hi > lo) {
-    first = lo / a.chunk_rows + s;
-    last = (hi - 1) / a.chunk_rows + s;
-  }
-  float z = 0.f;
-  uint32_t rows = 0, bad = 0;
-  for (int64_t i = first + threadIdx.x; i <= last; i += 32 * W) {
-    z += a.part.z[i];
-    rows += a.part.rows[i];
-    bad += a.part.bad[i];
-  }
+  // slots first, .., first + count - 1 hold the sequence (rows fit 32 bits)
+  const uint32_t lo = (uint32_t)a.seqs.at(s), hi = (uint32_t)a.seqs.at(s + 1), chunk = (uint32_t)a.chunk_rows;
+  const uint32_t from = lo / chunk;
+  const int count = hi > lo ? (int)((hi - 1) / chunk - from) + 1 : 0;
+  const int64_t first = (int64_t)from + s;
+  // every load of a thread is on its way before the first is used: U slots a lane
+  constexpr int U = 10;
+  auto load = [&](uint32_t e, int i0, float (&p)[U], uint32_t (&n)[U]) {
+    const float* pp = a.part.p + (first + i0) * a.E + e;
+    const uint32_t* pn = a.part.n + (first + i0) * a.E + e;
 #pragma unroll
-  for (int d = 16; d > 0; d >>= 1) {
-    z += __shfl_xor_sync(0xffffffffu, z, d);
-    rows += __shfl_xor_sync(0xffffffffu, rows, d);
-    bad += __shfl_xor_sync(0xffffffffu, bad, d);
+    for (int u = 0; u < U; ++u) {
+      const bool in = e < (uint32_t)a.E && i0 + u * W < count;
+      p[u] = in ? __ldcg(pp + u * W * a.E) : 0.f;
+      n[u] = in ? __ldcg(pn + u * W * a.E) : 0u;
+    }
+  };
+  float p[U], z = 0.f, np = 0.f;
+  uint32_t n[U], rows = 0, bad = 0;
+  load(part * 32 + lane, warp, p, n);
+  for (int i = threadIdx.x; i < count; i += 32 * W) {
+    z += a.part.z[first + i];
+    rows += a.part.rows[first + i];
+    bad += a.part.bad[first + i];
   }
+  z = add(z), rows = add(rows), bad = add(bad);
   if (lane == 0) sz[warp] = z, sv[warp] = rows, sb[warp] = bad;
-  float np = 0.f;
-  for (int e0 = part * 32; e0 < a.E; e0 += a.blocks * 32) {
-    const int e = e0 + lane;
-    float p = 0.f;
-    uint32_t n = 0;
-    if (e < a.E) {
-#pragma unroll 4
-      for (int64_t i = first + warp; i <= last; i += W) {
-        p += a.part.p[i * a.E + e];
-        n += a.part.n[i * a.E + e];
+  for (uint32_t e0 = part * 32; e0 < (uint32_t)a.E; e0 += blocks * 32) {
+    float ps = 0.f;
+    uint32_t ns = 0;
+    for (int i0 = warp; i0 < count; i0 += U * W) {
+      if (i0 != warp || e0 != part * 32) load(e0 + lane, i0, p, n);
+#pragma unroll
+      for (int u = 0; u < U; ++u) ps += p[u], ns += n[u];
+    }
+    sp[lane][warp] = ps;
+    sn[lane][warp] = ns;
+    __syncthreads();
+    // a warp for each expert's slot lanes; every W experts
+    rows = add(lane < W ? sv[lane] : 0u);
+    const float inv = rows ? 1.f / (float)rows : 0.f;
+#pragma unroll
+    for (int x = warp; x < 32; x += W) {
+      const float px = add(lane < W ? sp[x][lane] : 0.f);
+      const uint32_t nx = add(lane < W ? sn[x][lane] : 0u);
+      if (lane == 0 && e0 + x < (uint32_t)a.E) {
+        a.res.counts[(int64_t)s * a.E + e0 + x] = nx;
+        if (a.res.mean_scores) a.res.mean_scores[(int64_t)s * a.E + e0 + x] = rows ? px * inv : 0.f;
+        np = fmaf((float)nx, px, np);
       }
     }
-    sp[warp][lane] = p;
-    sn[warp][lane] = n;
     __syncthreads();
-    if (warp == 0) {
-      rows = 0, p = 0.f, n = 0;
-#pragma unroll
-      for (int w = 0; w < W; ++w) rows += sv[w], p += sp[w][lane], n += sn[w][lane];
-      if (e < a.E) {
-        a.res.counts[(int64_t)s * a.E + e] = n;
-        if (a.res.mean_scores) a.res.mean_scores[(int64_t)s * a.E + e] = rows ? p / (float)rows : 0.f;
-        np = fmaf((float)n, p, np);
-      }
+  }
+  if (lane == 0) snp[warp] = np;
+  __syncthreads();
+  if (warp == 0) {
+    np = add(lane < W ? snp[lane] : 0.f);
+    if (lane == 0) share = np;
+  }
+  if (blocks > 1) cl.sync();
+  if (part == 0 && warp == 0) {
+    if (blocks > 1) np = add(lane < (int)blocks ? *cl.map_shared_rank(&share, lane) : 0.f);
+    z = add(lane < W ? sz[lane] : 0.f);
+    bad = add(lane < W ? sb[lane] : 0u);
+    rows = add(lane < W ? sv[lane] : 0u);
+    if (lane == 0) {
+      a.res.loss[s] = balance_of(np, a.E, a.k, rows);
+      if (a.res.z_loss) a.res.z_loss[s] = rows ? z / (float)rows : 0.f;
+      a.res.tokens[s] = rows;
+      const bool malformed = a.seqs.off && (hi < lo || (int64_t)__ldg(a.seqs.off + s) > a.seqs.T ||
+                                            (int64_t)__ldg(a.seqs.off + s + 1) > a.seqs.T);
+      if (bad || malformed) set_status(a.res.status, MOE_ERR_INVALID_INDEX);
     }
-    __syncthreads();
   }
-  if (warp != 0) return;
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) np += __shfl_xor_sync(0xffffffffu, np, d);
-  if (lane != 0) return;
-  if (part == 0) {
-    z = 0.f, bad = 0;
-    for (int w = 0; w < W; ++w) z += sz[w], bad += sb[w];
-    if (a.res.z_loss) a.res.z_loss[s] = rows ? z / (float)rows : 0.f;
-    a.res.tokens[s] = rows;
-    if (bad) set_status(a.res.status, MOE_ERR_INVALID_INDEX);
-  }
-  if (a.blocks > 1) {
-    float* share = a.part.share + (int64_t)s * kMaxShares;
-    __stcg(share + part, np);
-    __threadfence();
-    if (atomicAdd(a.part.ticket + s, 1u) != (uint32_t)a.blocks - 1u) return;
-    __threadfence();
-    np = 0.f;
-    for (int b = 0; b < a.blocks; ++b) np += __ldcg(share + b);
-  }
-  a.res.loss[s] = balance_of(np, a.E, a.k, rows);
+  if (blocks > 1) cl.sync();  // the shares are read
 }
 
 int hist_copies(int E) {
@@ -425,13 +434,15 @@ size_t slot_count(int64_t T, int64_t num_seqs) {
 
 size_t balance_workspace_bytes(int64_t T, int E, int64_t num_seqs) {
   const size_t slots = slot_count(T, num_seqs);
-  return align_up(slots * (size_t)E * 8 + slots * 12 + (size_t)num_seqs * 4 * (kMaxShares + 1), 256);
+  return align_up(slots * (size_t)E * 8 + slots * 12, 256);
 }
 
 cudaError_t launch_balance_loss(const BalanceArgs& b, void* ws, uint32_t* status, cudaStream_t s) {
   const void* ptrs[] = {b.logits};
   const RowPlan plan = row_plan(ptrs, 1, b.dt, b.E);
-  const Chunks ch = cut_rows(b.T, plan_batch(plan), plan_blocks(plan));
+  // sequences are worked off one after another in a block: finer cuts where there are any
+  const Chunks ch = b.seq_offsets ? cut_rows(b.T, plan_batch(plan), plan_blocks(plan), 1)
+                                  : cut_rows(b.T, (int64_t)kWarps * plan_batch(plan), plan_blocks(plan));
   const size_t slots = slot_count(b.T, b.num_seqs);
   Partials part;
   part.p = static_cast<float*>(ws);
@@ -439,8 +450,6 @@ cudaError_t launch_balance_loss(const BalanceArgs& b, void* ws, uint32_t* status
   part.z = reinterpret_cast<float*>(part.n + slots * b.E);
   part.rows = reinterpret_cast<uint32_t*>(part.z + slots);
   part.bad = part.rows + slots;
-  part.share = reinterpret_cast<float*>(part.bad + slots);
-  part.ticket = reinterpret_cast<uint32_t*>(part.share + b.num_seqs * kMaxShares);
   FwdArgs a{};
   a.logits = b.logits;
   a.idx = b.idx;
@@ -467,15 +476,25 @@ cudaError_t launch_balance_loss(const BalanceArgs& b, void* ws, uint32_t* status
     e = with_row_variant(b.dt, plan, f);
   }
   if (e != cudaSuccess || a.alone) return e;
-  // a block for each group of experts while the blocks fit the GPU at once; many
-  // slots a sequence are added by more warps
-  const int64_t groups = (b.E + 31) / 32;
-  const int64_t fit = 304 / b.num_seqs;
-  const int blocks = (int)(groups < fit ? groups : fit > 1 ? fit : 1);
-  const FinishArgs f{part, a.seqs, b.E, b.k, blocks, ch.rows, a.res};
-  const dim3 grid((unsigned)(b.num_seqs * blocks));
-  if (ch.chunks / b.num_seqs >= 32) return launch_pdl(balance_finish_kernel<32>, grid, dim3(1024), 0, s, f);
-  return launch_pdl(balance_finish_kernel<8>, grid, dim3(256), 0, s, f);
+  // a block for each group of experts while the blocks fit the GPU at once, at most
+  // eight (a cluster); many slots a sequence are added by more warps
+  int blocks = 1;
+  while (blocks < 8 && blocks * 32 < b.E && b.num_seqs * blocks < 152) blocks *= 2;
+  const FinishArgs f{part, a.seqs, b.E, b.k, ch.rows, a.res};
+  const bool many = ch.chunks / b.num_seqs >= 32;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(b.num_seqs * blocks));
+  cfg.blockDim = dim3(many ? 1024 : 256);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)blocks;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = blocks > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, many ? balance_finish_kernel<32> : balance_finish_kernel<8>, f);
 }
 
 }  // namespace moe

@@ -165,7 +165,7 @@ struct LaunchBwd {
 cudaError_t launch_balance_loss_backward(const BalanceBwdArgs& b, cudaStream_t s) {
   const void* ptrs[] = {b.logits, b.base, b.dlogits};
   const RowPlan plan = row_plan(ptrs, 3, b.dt, b.E);
-  const Chunks ch = cut_rows(b.T, plan_batch(plan), plan_blocks(plan));
+  const Chunks ch = cut_rows(b.T, (b.seq_offsets ? 1 : kWarps) * (int64_t)plan_batch(plan), plan_blocks(plan), 1);
   BwdArgs a{};
   a.logits = b.logits;
   a.row_stats = reinterpret_cast<const float2*>(b.row_stats);

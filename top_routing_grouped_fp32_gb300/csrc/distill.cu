@@ -391,7 +391,9 @@ size_t distill_workspace_bytes(int64_t T, int64_t num_seqs) { return align_up(sl
 cudaError_t launch_distill_loss(const DistillArgs& d, void* ws, uint32_t* status, cudaStream_t s) {
   const void* ptrs[] = {d.logits};
   const RowPlan plan = row_plan(ptrs, 1, d.dt, d.E);
-  const Chunks ch = cut_rows(d.T, plan_batch(plan), plan_blocks(plan));
+  // sequences are worked off one after another in a block: finer cuts where there are any
+  const Chunks ch = d.seq_offsets ? cut_rows(d.T, plan_batch(plan), plan_blocks(plan), 1)
+                                  : cut_rows(d.T, (int64_t)kWarps * plan_batch(plan), plan_blocks(plan));
   const size_t slots = slot_count(d.T, d.num_seqs);
   FwdArgs a{};
   a.logits = d.logits;

@@ -223,7 +223,7 @@ struct LaunchBwd {
 cudaError_t launch_distill_loss_backward(const DistillBwdArgs& d, cudaStream_t s) {
   const void* ptrs[] = {d.logits, d.base, d.dlogits};
   const RowPlan plan = row_plan(ptrs, 3, d.dt, d.E);
-  const Chunks ch = cut_rows(d.T, plan_batch(plan), plan_blocks(plan));
+  const Chunks ch = cut_rows(d.T, (d.seq_offsets ? 1 : kWarps) * (int64_t)plan_batch(plan), plan_blocks(plan), 1);
   BwdArgs a{};
   a.logits = d.logits;
   a.t_idx = d.t_idx;

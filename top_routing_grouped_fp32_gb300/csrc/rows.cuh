@@ -541,18 +541,21 @@ cudaError_t launch_rows(void (*kernel)(KArgs...), int blocks, int threads, size_
   return launch_pdl(kernel, dim3((unsigned)blocks), dim3((unsigned)threads), smem, s, std::forward<Args>(args)...);
 }
 
-// How a batch of rows is cut over blocks: `chunks` blocks of `rows` rows.
+// How a batch of rows is cut over blocks: `chunks` blocks of `rows` rows, whole
+// rounds of a block's warps (`round` rows); one block where it has few rounds to
+// make, since it then needs no second kernel.
 struct Chunks {
   int64_t rows;
   int chunks;
 };
-inline Chunks cut_rows(int64_t T, int64_t step, int64_t max_chunks) {
-  int64_t steps = (T + step - 1) / step;
-  if (steps < 1) steps = 1;
-  const int64_t per = (steps + max_chunks - 1) / max_chunks;
+constexpr int64_t kRoundsAlone = 4;
+inline Chunks cut_rows(int64_t T, int64_t round, int64_t max_chunks, int64_t alone = kRoundsAlone) {
+  int64_t rounds = (T + round - 1) / round;
+  if (rounds < 1) rounds = 1;
+  const int64_t per = rounds <= alone ? rounds : (rounds + max_chunks - 1) / max_chunks;
   Chunks c;
-  c.rows = per * step;
-  c.chunks = (int)((steps + per - 1) / per);
+  c.rows = per * round;
+  c.chunks = (int)((rounds + per - 1) / per);
   return c;
 }
 
