@@ -69,20 +69,19 @@ struct FwdArgs {
   uint32_t* status;
 };
 
-// Entries of a row's list that a lane keeps in registers; more are read again
-// where they are needed.
-constexpr int kListRegs = 4;
-
 // A row's lanes hold its logits and, entry sub, sub + lpr, .., its list.  Which of
 // its elements are listed is a word of bits for each lane, set by the list's
 // lanes in shared memory, so that the mass outside the list is summed as it is and
-// not as a difference.
-template <typename T, int VEC, int NV, int LPR>
-__global__ void __launch_bounds__(kThreads, blocks_per_sm<T, VEC, NV>()) distill_fwd_kernel(FwdArgs a) {
+// not as a difference.  A lane keeps J entries in registers (1 where that holds the
+// list: 98 us against 106 for lists of 8 of 256, 524288 rows); more are read again
+// where they are needed.  What a row needs once, and no other lane waits for, is
+// left until a warp can do it for a row a lane.
+template <typename T, int VEC, int NV, int LPR, int J>
+__global__ void __launch_bounds__(kThreads, blocks_per_sm<T, VEC, NV>(kListBlocks)) distill_fwd_kernel(FwdArgs a) {
   extern __shared__ __align__(16) unsigned char smem[];
   using Stream = RowStream<T, VEC, NV, LPR>;
   using Row = typename Stream::Row;
-  constexpr int N = Row::N, S = Stream::kStages, J = kListRegs;
+  constexpr int N = Row::N, S = Stream::kStages;
   __shared__ uint32_t listed[kWarps][32];
   __shared__ float red_l[kWarps];
   __shared__ uint32_t red_n[kWarps], red_b[kWarps];
@@ -97,12 +96,6 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, VEC, NV>()) distill
   auto owner = [&](uint32_t e) { return (e / VEC) & (L.lpr - 1); };  // the lane that holds element e
   auto bit_of = [&](uint32_t e) { return 1u << ((e / VEC >> rows.lpr_log) * VEC + e % VEC); };
 
-  float* const own_stat = L.sub == 0 ? a.row_loss : a.row_stats + (L.sub - 1) * a.T;
-  auto write_row = [&](int64_t t, float kl, float m, float s, float mt, float st, float ratio) {
-    auto value = [&](int f) { return f == 0 ? kl : f == 1 ? m : f == 2 ? s : f == 3 ? mt : f == 4 ? st : ratio; };
-    if (L.sub < 6) own_stat[t] = value(L.sub);
-    for (int f = L.sub + L.lpr; f < 6; f += L.lpr) a.row_stats[(f - 1) * a.T + t] = value(f);
-  };
   auto gap = [&](int64_t lo, int64_t hi) {
     for (int64_t t = lo + threadIdx.x; t < hi; t += kThreads) {
       a.row_loss[t] = 0.f;
@@ -157,6 +150,43 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, VEC, NV>()) distill
     uint32_t x[J], e[J];
     float rest;
     entries(0, x, e, rest);
+    // A lane keeps its group's row of every lpr-th batch: the list's part of KL, the
+    // maxima and sums of both sides (student's sum 0: the row does not count), the mass
+    // outside the list (or, far below the row, its log, which is negative) and the rest.
+    struct Kept {
+      float kl, m, s, mt, st, out, rest;
+    } kept = {};
+    int turn = 0;
+    auto flush = [&]() {  // the batches from t0 - turn * step on
+      const int64_t t = t0 + (L.sub - turn) * step + L.grp;
+      if (L.sub < turn && t < hi) {
+        const float fix = RowExp(kept.m, a.c).fix();
+        const float s = kept.s * fix;
+        float kl = kept.kl, ratio = 0.f;
+        const bool far = kept.out < 0.f;
+        const float p = far ? 0.f : kept.out * rcp_fast(kept.s);
+        if (a.t_rest) {
+          const float ln_out = far ? kept.out : log2_fast(kept.out * fix) * kLn2;
+          const float q = exp2_fast((kept.rest - kept.mt) * a.c) * rcp_fast(kept.st);
+          kl += kl_term(q, p, (kept.rest - kept.mt) * a.inv_tau - ln_out +
+                                  (log2_fast(s) - log2_fast(kept.st)) * kLn2);
+          ratio = far ? -q : q * rcp_fast(p);
+        } else {
+          kl += p;
+        }
+        if (s != s || kept.st != kept.st) kl = NAN;
+        const bool ok = kept.s != 0.f;
+        a.row_loss[t] = ok ? kl : 0.f;
+        a.row_stats[t] = kept.m;
+        a.row_stats[a.T + t] = ok ? s : 0.f;
+        a.row_stats[2 * a.T + t] = kept.mt;
+        a.row_stats[3 * a.T + t] = kept.st;
+        a.row_stats[4 * a.T + t] = ok ? ratio : 0.f;
+        if (ok) loss += kl;
+        counted += ok;
+      }
+      turn = 0;
+    };
     while (left > 0) {
       Row cur;
       rows.take(cur);
@@ -232,11 +262,9 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, VEC, NV>()) distill
       out = L.sum(out);
       st = L.sum(st);
       const float s0 = out + L.sum(sp);  // with the factor that fix() takes out
-      const float fix = ex.fix();
-      // log of the mass outside the list, about its own maximum where it is far below the row's
-      float ln_out = log2_fast(out * fix) * kLn2;
-      const bool far = ok && a.t_rest && out < kFarBelow;
-      if (far) {
+      // log of the mass outside the list about its own maximum where it is far below the row's
+      float kept_out = out;
+      if (ok && a.t_rest && out < kFarBelow) {
         float mo = -INFINITY, so = 0.f;
 #pragma unroll 1
         for (int el = L.sub; el < a.E; el += L.lpr)
@@ -246,12 +274,11 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, VEC, NV>()) distill
         for (int el = L.sub; el < a.E; el += L.lpr)
           if (!(words[owner(el)] & bit_of(el))) so += exp2_fast((to_f32<T>(rows.cell(el)) - mo) * a.c);
         for (int d = L.lpr / 2; d > 0; d >>= 1) so += __shfl_xor_sync(L.mask(), so, d);
-        ln_out = mo == -INFINITY ? -INFINITY : (mo - m) * a.inv_tau + logf(so);
+        kept_out = mo == -INFINITY ? -INFINITY : (mo - m) * a.inv_tau + logf(so);
       }
-      const float s = bad || nan ? NAN : s0 * fix;
       const float inv_s = rcp_fast(s0), inv_st = rcp_fast(st);
-      const float dz = (log2_fast(s) - log2_fast(st)) * kLn2;
-      float kl = 0.f, ratio = 0.f;
+      const float dz = (log2_fast(s0 * ex.fix()) - log2_fast(st)) * kLn2;
+      float kl = 0.f;
 #pragma unroll
       for (int j = 0; j < J; ++j) {
         if (j * L.lpr >= a.m) break;
@@ -264,23 +291,10 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, VEC, NV>()) distill
         kl += kl_term(exp2_fast((xx - mt) * a.c) * inv_st, ex.at(y) * inv_s,
                       ((xx - mt) - (y - m)) * a.inv_tau + dz);
       });
-      if (a.t_rest) {
-        const float q = eq_rest * inv_st, p = out * inv_s;
-        if (L.sub == 0) kl += kl_term(q, p, (rest - mt) * a.inv_tau - ln_out + dz);
-        ratio = far ? -q : q * rcp_fast(p);
-      } else if (L.sub == 0) {
-        kl += out * inv_s;
-      }
       kl = L.sum(kl);
-      if (s != s || st != st) kl = NAN;
-      if (L.grp < left) {
-        if (ok) write_row(t, kl, m, s, mt, st, ratio);
-        else write_row(t, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f);
-        if (ok && L.sub == 0) {
-          loss += kl;
-          ++counted;
-          broken += bad;
-        }
+      if (L.sub == turn) {
+        kept = ok ? Kept{kl, m, bad || nan ? NAN : s0, mt, st, kept_out, rest} : Kept{};
+        broken += ok && bad;
       }
       __syncwarp();  // before the next batch takes this one's place
 #pragma unroll
@@ -290,7 +304,9 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, VEC, NV>()) distill
       t0 += step;
       li += (int64_t)step * a.m;
       left -= step;
+      if (++turn == L.lpr) flush();
     }
+    flush();
     rows.drain();
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) {
@@ -376,8 +392,14 @@ struct LaunchFwd {
   cudaStream_t s;
   template <typename T, int VEC, int NV, int LPR>
   cudaError_t run() {
+    if constexpr (VEC > 1)
+      if (a.m <= a.lpr) return with<T, VEC, NV, LPR, 1>();
+    return with<T, VEC, NV, LPR, 4>();
+  }
+  template <typename T, int VEC, int NV, int LPR, int J>
+  cudaError_t with() {
     static std::atomic<uint64_t> asked{0};
-    return launch_rows(distill_fwd_kernel<T, VEC, NV, LPR>, chunks, kThreads,
+    return launch_rows(distill_fwd_kernel<T, VEC, NV, LPR, J>, chunks, kThreads,
                        kWarps * RowStream<T, VEC, NV, LPR>::kWarpBytes, asked, s, a);
   }
 };
@@ -392,8 +414,8 @@ cudaError_t launch_distill_loss(const DistillArgs& d, void* ws, uint32_t* status
   const void* ptrs[] = {d.logits};
   const RowPlan plan = row_plan(ptrs, 1, d.dt, d.E);
   // sequences are worked off one after another in a block: finer cuts where there are any
-  const Chunks ch = d.seq_offsets ? cut_rows(d.T, plan_batch(plan), plan_blocks(plan), 1)
-                                  : cut_rows(d.T, (int64_t)kWarps * plan_batch(plan), plan_blocks(plan));
+  const Chunks ch = d.seq_offsets ? cut_rows(d.T, plan_batch(plan), plan_blocks(plan, kListBlocks), 1)
+                                  : cut_rows(d.T, (int64_t)kWarps * plan_batch(plan), plan_blocks(plan, kListBlocks));
   const size_t slots = slot_count(d.T, d.num_seqs);
   FwdArgs a{};
   a.logits = d.logits;

@@ -12,10 +12,6 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 
-// Entries of a row's list that a lane keeps in registers; more are read again
-// where they are needed.
-constexpr int kListRegs = 4;
-
 struct BwdArgs {
   const void* logits;
   const uint32_t* t_idx;
@@ -34,13 +30,14 @@ struct BwdArgs {
 
 // The list's entries differ from p_e (1 - ratio): the row's gradient is laid out in
 // its logits' place in shared memory, in its final type, the lanes of the list
-// overwrite their entries, and the row leaves in full vectors.
-template <typename T, int VEC, int NV, int LPR>
-__global__ void __launch_bounds__(kThreads, blocks_per_sm<T, VEC, NV>()) distill_bwd_kernel(BwdArgs a) {
+// overwrite their entries, and the row leaves in full vectors.  A lane keeps J
+// entries in registers; more are read again where they are needed.
+template <typename T, int VEC, int NV, int LPR, int J>
+__global__ void __launch_bounds__(kThreads, blocks_per_sm<T, VEC, NV>(kListBlocks)) distill_bwd_kernel(BwdArgs a) {
   extern __shared__ __align__(16) unsigned char smem[];
   using Stream = RowStream<T, VEC, NV, LPR>;
   using Row = typename Stream::Row;
-  constexpr int N = Row::N, S = Stream::kStages, J = kListRegs;
+  constexpr int N = Row::N, S = Stream::kStages;
   constexpr int F = 5;  // statistics of a row
   pdl_wait();
   pdl_trigger();
@@ -212,8 +209,14 @@ struct LaunchBwd {
   cudaStream_t s;
   template <typename T, int VEC, int NV, int LPR>
   cudaError_t run() {
+    if constexpr (VEC > 1)
+      if (a.m <= a.lpr) return with<T, VEC, NV, LPR, 1>();
+    return with<T, VEC, NV, LPR, 4>();
+  }
+  template <typename T, int VEC, int NV, int LPR, int J>
+  cudaError_t with() {
     static std::atomic<uint64_t> asked{0};
-    return launch_rows(distill_bwd_kernel<T, VEC, NV, LPR>, chunks, kThreads,
+    return launch_rows(distill_bwd_kernel<T, VEC, NV, LPR, J>, chunks, kThreads,
                        kWarps * RowStream<T, VEC, NV, LPR>::kWarpBytes, asked, s, a);
   }
 };
@@ -223,7 +226,7 @@ struct LaunchBwd {
 cudaError_t launch_distill_loss_backward(const DistillBwdArgs& d, cudaStream_t s) {
   const void* ptrs[] = {d.logits, d.base, d.dlogits};
   const RowPlan plan = row_plan(ptrs, 3, d.dt, d.E);
-  const Chunks ch = cut_rows(d.T, (d.seq_offsets ? 1 : kWarps) * (int64_t)plan_batch(plan), plan_blocks(plan), 1);
+  const Chunks ch = cut_rows(d.T, (d.seq_offsets ? 1 : kWarps) * (int64_t)plan_batch(plan), plan_blocks(plan, kListBlocks), 1);
   BwdArgs a{};
   a.logits = d.logits;
   a.t_idx = d.t_idx;

@@ -125,11 +125,16 @@ struct Lanes {
 };
 
 // Blocks of 256 threads that a SM is to hold, by the bytes of a row that a lane
-// holds (its registers follow them).
+// holds (its registers follow them).  Kernels that keep a list's entries as well
+// hold three at most.
+constexpr int blocks_for(int bytes, int most) {
+  const int n = bytes <= 16 ? 4 : bytes <= 32 ? 3 : bytes <= 64 ? 2 : 1;
+  return n < most ? n : most;
+}
+constexpr int kListBlocks = 3;
 template <typename T, int VEC, int NV>
-constexpr int blocks_per_sm() {
-  constexpr int bytes = VEC == 1 ? NV * 4 : NV * 16;
-  return bytes <= 16 ? 4 : bytes <= 32 ? 3 : bytes <= 64 ? 2 : 1;
+constexpr int blocks_per_sm(int most = 4) {
+  return blocks_for(VEC == 1 ? NV * 4 : NV * 16, most);
 }
 
 // One row's elements of this lane.
@@ -516,10 +521,7 @@ cudaError_t with_row_variant(moe_dtype dt, const RowPlan& p, F&& f) {
 // holds of its kernels (blocks_per_sm).
 constexpr int kMaxBlocks = 152 * 4;
 inline int plan_batch(const RowPlan& p) { return 32 / p.lpr; }
-inline int plan_blocks(const RowPlan& p) {
-  const int bytes = p.nv * (p.vec ? 16 : 4);
-  return 152 * (bytes <= 16 ? 4 : bytes <= 32 ? 3 : bytes <= 64 ? 2 : 1);
-}
+inline int plan_blocks(const RowPlan& p, int most = 4) { return 152 * blocks_for(p.nv * (p.vec ? 16 : 4), most); }
 
 // Launches a kernel that may need more shared memory than the default, which is
 // asked for once per kernel and device.
