@@ -166,10 +166,10 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, VEC, NV>(kListBlock
         const bool far = kept.out < 0.f;
         const float p = far ? 0.f : kept.out * rcp_fast(kept.s);
         if (a.t_rest) {
-          const float ln_out = far ? kept.out : log2_fast(kept.out * fix) * kLn2;
-          const float q = exp2_fast((kept.rest - kept.mt) * a.c) * rcp_fast(kept.st);
-          kl += kl_term(q, p, (kept.rest - kept.mt) * a.inv_tau - ln_out +
-                                  (log2_fast(s) - log2_fast(kept.st)) * kLn2);
+          const float ln_out = far ? kept.out : logf(kept.out * fix);
+          const float inv_st = rcp_fast(kept.st);
+          const float q = exp2_fast((kept.rest - kept.mt) * a.c) * inv_st;
+          kl += kl_term(q, p, (kept.rest - kept.mt) * a.inv_tau - ln_out + log2_fast(s * inv_st) * kLn2);
           ratio = far ? -q : q * rcp_fast(p);
         } else {
           kl += p;
@@ -277,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, VEC, NV>(kListBlock
         kept_out = mo == -INFINITY ? -INFINITY : (mo - m) * a.inv_tau + logf(so);
       }
       const float inv_s = rcp_fast(s0), inv_st = rcp_fast(st);
-      const float dz = (log2_fast(s0 * ex.fix()) - log2_fast(st)) * kLn2;
+      const float dz = log2_fast(s0 * ex.fix() * inv_st) * kLn2;  // as in flush()
       float kl = 0.f;
 #pragma unroll
       for (int j = 0; j < J; ++j) {
