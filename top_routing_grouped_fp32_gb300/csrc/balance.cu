@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, VEC, NV>()) balance
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (blockIdx.x == 0 && threadIdx.x == 0) *a.res.status = 0u;
   const Lanes<LPR> L(a.lpr);
-  Stream rows(L, smem, a.E);
+  Stream rows(L, smem, a.logits, a.E, a.T);
   const int copy = lane & (a.copies - 1), copies_log = __popc(a.copies - 1);  // its copy of the histogram
   const int batch = L.rows;                // consecutive rows that a warp takes at once
   const int step = kWarps * batch;
@@ -126,7 +126,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, VEC, NV>()) balance
 
     int64_t t0 = lo + warp * batch;     // the batch's first row
     int left = (int)(hi - t0);          // rows from there on (a block has far fewer than 2^31)
-    rows.start(static_cast<const T*>(a.logits), t0 + L.grp, step);
+    rows.start(t0, step);
     // does this group's row of a batch count: bit i for the i-th batch from here.
     // The mask's byte is fetched a batch before its bit is needed.
     uint32_t on = 0;
@@ -213,6 +213,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, VEC, NV>()) balance
       rows.template issue<true>(on >> (S - 1) & 1u);  // (a zero row's scores times 0: no branch)
       fetch(S);
       const bool ok = on & 1u;
+      if (Stream::kImage && !ok) cur.zero(rows.room, L.lpr);
       float p[N], m = L.max(cur.lane_max());
       row_scores<SIG>(cur, m, m, p);
       const float s = L.sum(lane_sum(p));

@@ -36,7 +36,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, VEC, NV>()) balance
   pdl_trigger();
   const int warp = threadIdx.x >> 5;
   const Lanes<LPR> L(a.lpr);
-  Stream rows(L, smem, a.E);
+  Stream rows(L, smem, a.logits, a.E, a.T);
   const int step = kWarps * L.rows;
 
   // rows [lo, hi) of a sequence, or (seq < 0) of none: nothing but the base
@@ -56,7 +56,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, VEC, NV>()) balance
     }
     int64_t t0 = lo + warp * L.rows;
     int left = (int)(hi - t0);
-    rows.start(static_cast<const T*>(a.logits), t0 + L.grp, step);
+    rows.start(t0, step);
     // Rows that do not count (a sum of 0) are not read.  A row's sum is fetched two
     // batches before its row is asked for, its statistics (again) two before their use:
     // one batch does not cover the latency.
@@ -136,7 +136,14 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, VEC, NV>()) balance
 #pragma unroll
         for (int n = 0; n < N; ++n) d[n] += cur[n];
       }
-      if (in) store_row<T, VEC, NV>(static_cast<T*>(a.out) + at, rows.room, L.lpr, d);
+      if constexpr (Stream::kImage) {
+        __syncwarp();  // every lane has read its logits
+        rows.put(d);
+        __syncwarp();
+        rows.store(static_cast<T*>(a.out), t0, left);
+      } else if (in) {
+        store_row<T, VEC, NV>(static_cast<T*>(a.out) + at, rows.room, L.lpr, d);
+      }
       st = st1, st1 = st2;
       t0 += step;
       left -= step;

@@ -90,7 +90,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, VEC, NV>(kListBlock
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (blockIdx.x == 0 && threadIdx.x == 0) *a.status = 0u;
   const Lanes<LPR> L(a.lpr);
-  Stream rows(L, smem, a.E);
+  Stream rows(L, smem, a.logits, a.E, a.T);
   const int step = kWarps * L.rows;
   uint32_t* const words = &listed[warp][L.grp * L.lpr];
   auto owner = [&](uint32_t e) { return (e / VEC) & (L.lpr - 1); };  // the lane that holds element e
@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, VEC, NV>(kListBlock
     uint32_t counted = 0, broken = 0;
     int64_t t0 = lo + warp * L.rows;
     int left = (int)(hi - t0);
-    rows.start(static_cast<const T*>(a.logits), t0 + L.grp, step);
+    rows.start(t0, step);
     // does this group's row of a batch count: bit i for the i-th batch from here.
     // The mask's byte is fetched a batch before its bit is needed.
     uint32_t on = 0;

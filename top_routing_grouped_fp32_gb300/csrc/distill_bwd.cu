@@ -43,7 +43,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, VEC, NV>(kListBlock
   pdl_trigger();
   const int warp = threadIdx.x >> 5;
   const Lanes<LPR> L(a.lpr);
-  Stream rows(L, smem, a.E);
+  Stream rows(L, smem, a.logits, a.E, a.T);
   const int step = kWarps * L.rows;
 
   // rows [lo, hi) of a sequence, or (seq < 0) of none: nothing but the base
@@ -52,7 +52,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, VEC, NV>(kListBlock
     const float c = tokens ? __ldg(a.dloss + seq) * a.inv_tau / (float)tokens : 0.f;
     int64_t t0 = lo + warp * L.rows;
     int left = (int)(hi - t0);
-    rows.start(static_cast<const T*>(a.logits), t0 + L.grp, step);
+    rows.start(t0, step);
     // A row's sum says whether it counts: the rest of it is read only then.  Bit i
     // is the i-th batch from here; sums are fetched a batch before their bit.
     auto inside = [&](int ahead) { return seq >= 0 && ahead * step + L.grp < left; };
@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, VEC, NV>(kListBlock
           rows.cell((int)ee) = from_f32<T>(g);
         }
       __syncwarp();
-      if (in) rows.store(static_cast<T*>(a.out) + at + L.sub * VEC);
+      rows.store(static_cast<T*>(a.out), t0, left);
       st = st1;
 #pragma unroll
       for (int j = 0; j < J; ++j) x[j] = x1[j], e[j] = e1[j];

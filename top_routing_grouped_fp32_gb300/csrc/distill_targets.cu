@@ -233,18 +233,19 @@ __global__ void __launch_bounds__(kTargetThreads, VEC * NV * sizeof(T) <= 64 ? 4
   pdl_trigger();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const Lanes<LPR> L(a.lpr);
-  const int room = a.E - L.sub * VEC;
+  extern __shared__ __align__(16) unsigned char smem[];
+  using Stream = RowStream<T, VEC, NV, LPR>;
+  Stream rows(L, smem, a.logits, a.E, a.T);
   T* top = static_cast<T*>(a.top);
   const int64_t step = (int64_t)gridDim.x * W * L.rows;
   int64_t t0 = ((int64_t)blockIdx.x * W + warp) * L.rows;
-  const T* lp = static_cast<const T*>(a.logits) + (t0 + L.grp) * a.E + L.sub * VEC;
-  Row cur, nxt;
-  cur.fill(from_f32<T>(-INFINITY));
-  nxt.fill(from_f32<T>(-INFINITY));
-  cur.load(lp, room, L.lpr, t0 + L.grp < a.T);
+  rows.start(t0, step);
+#pragma unroll
+  for (int i = 0; i < Stream::kStages - 1; ++i) rows.issue(t0 + i * step + L.grp < a.T);
   for (; t0 < a.T; t0 += step) {
-    lp += step * a.E;
-    nxt.load(lp, room, L.lpr, t0 + step + L.grp < a.T);
+    Row cur;
+    rows.take(cur);
+    rows.issue(t0 + (Stream::kStages - 1) * step + L.grp < a.T);
     const int64_t t = t0 + L.grp;
     const bool in = t < a.T;
     typename SK::template Keys<VEC, NV> keys(cur, L.lpr, L.sub);
@@ -315,8 +316,8 @@ __global__ void __launch_bounds__(kTargetThreads, VEC * NV * sizeof(T) <= 64 ? 4
           if (q * P + p < a.m) to[p] = ids[p], tl[p] = tops[p];
       }
     });
-    cur = nxt;
   }
+  rows.drain();
 }
 
 struct LaunchTargets {
@@ -326,18 +327,17 @@ struct LaunchTargets {
   cudaError_t with() {
     const int64_t per = (int64_t)(kTargetThreads / 32) * (32 / a.lpr);
     const int64_t blocks = (a.T + per - 1) / per;
-    return launch_pdl(distill_targets_kernel<T, VEC, NV, LPR, K>,
-                      dim3((unsigned)(blocks < kTargetBlocks ? blocks : kTargetBlocks)), dim3(kTargetThreads), 0, s,
-                      a);
+    static std::atomic<uint64_t> asked{0};
+    return launch_rows(distill_targets_kernel<T, VEC, NV, LPR, K>,
+                       (int)(blocks < kTargetBlocks ? blocks : kTargetBlocks), kTargetThreads,
+                       kTargetThreads / 32 * RowStream<T, VEC, NV, LPR>::kWarpBytes, asked, s, a);
   }
   // the shortest kept list that holds m keys (fewer lengths where rows are rarer)
   template <typename T, int VEC, int NV, int LPR>
   cudaError_t run() {
-    if constexpr (VEC > 1) {
-      if (a.m <= 8) return with<T, VEC, NV, LPR, 8>();
-      if constexpr (sizeof(T) == 2)
-        if (a.m <= 32) return with<T, VEC, NV, LPR, 32>();
-    }
+    if (a.m <= 8) return with<T, VEC, NV, LPR, 8>();
+    if constexpr (sizeof(T) == 2)
+      if (a.m <= 32) return with<T, VEC, NV, LPR, 32>();
     return with<T, VEC, NV, LPR, 64>();
   }
 };

@@ -134,7 +134,7 @@ constexpr int blocks_for(int bytes, int most) {
 constexpr int kListBlocks = 3;
 template <typename T, int VEC, int NV>
 constexpr int blocks_per_sm(int most = 4) {
-  return blocks_for(VEC == 1 ? NV * 4 : NV * 16, most);
+  return blocks_for(VEC == 1 ? NV * 2 : NV * 16, most);
 }
 
 // One row's elements of this lane.
@@ -215,36 +215,43 @@ __device__ __forceinline__ void store_row(T* row, int room, int lpr, const float
   }
 }
 
-// The rows of a warp, a batch of 32 / lpr after another.  Vectors of 16 bytes come
-// through a ring of kStages batches in the warp's shared memory by asynchronous
-// copies, so that kStages - 1 batches are in flight without registers: 256 BF16
-// logits a row with one batch ahead in registers ran at 66 % of the copy
-// bandwidth (16 warps of 128 registers on a SM do not cover the latency).  A lane
-// copies and reads the same 16 bytes, so no lane waits for another.  Single
-// elements come through registers, one batch ahead.
+// The rows of a warp, a batch of 32 / lpr consecutive rows after another, through a
+// ring of kStages batches in the warp's shared memory by asynchronous copies, so
+// that kStages - 1 batches are in flight without registers: 256 BF16 logits a row
+// with one batch ahead in registers ran at 66 % of the copy bandwidth (16 warps of
+// 128 registers on a SM do not cover the latency).
 //
-// The current batch also lies in shared memory by vector and lane: cell(e) is
-// element e of this lane's row.  It may be written (each lane its own row's) until
-// the next issue().
+// Whole vectors (VEC > 1): a lane copies and reads the same 16 bytes, by vector and
+// lane, so that no lane waits for another.  Single elements (VEC == 1: rows that
+// start on any element): a batch is copied as it lies in memory, in the 16-byte
+// pieces that hold it, and a lane reads its elements from there.
+//
+// cell(e) is element e of this lane's row in the current batch.  It may be written
+// (each lane its own row's) until the next issue().
 template <typename T, int VEC, int NV, int LPR>
 struct RowStream {
-  static constexpr int kStages = VEC > 1 ? 4 : 2;
-  static constexpr int kStageElems = 32 * VEC * NV;
-  static constexpr int kWarpBytes = (VEC > 1 ? kStages : 1) * kStageElems * (int)sizeof(T);
   using Row = RowRegs<T, VEC, NV>;
+  static constexpr bool kImage = VEC == 1;
+  static constexpr int kStageBytes = 32 * VEC * NV * (int)sizeof(T) + (kImage ? 32 : 0);
+  static constexpr int kStages = kStageBytes > 4096 ? 2 : 4;  // (two blocks of 64 KB fit a SM)
+  static constexpr int kWarpBytes = (kStages * kStageBytes + 15) / 16 * 16;
   const Lanes<LPR>& L;
-  T* ring;      // of this warp
-  const T* p;   // this lane's first element of the batch that is issued next
-  int64_t step; // elements between a warp's batches
+  char* ring;        // of this warp
+  const T* logits;
+  const T* p;        // next to issue: this lane's first element, or (kImage) the batch's
+  int64_t step;      // elements between a warp's batches
+  int64_t elements;  // of all rows
   int room, E, lpr_log;
-  int head, tail;  // stages: current, issued next
-  Row nxt;
+  int head, tail;    // stages: current, issued next
+  int shift;         // kImage: place of the current batch's first element in its stage
 
-  __device__ __forceinline__ RowStream(const Lanes<LPR>& L_, void* smem, int E_) : L(L_), E(E_) {
-    ring = reinterpret_cast<T*>(static_cast<char*>(smem) + (threadIdx.x >> 5) * kWarpBytes);
+  __device__ __forceinline__ RowStream(const Lanes<LPR>& L_, void* smem, const void* logits_, int E_, int64_t T_rows)
+      : L(L_), logits(static_cast<const T*>(logits_)), E(E_) {
+    ring = static_cast<char*>(smem) + (threadIdx.x >> 5) * kWarpBytes;
     room = E - L.sub * VEC;
     lpr_log = 31 - __clz(L.lpr);
-    if constexpr (VEC > 1) {  // vectors behind the row's end are never copied: they hold -inf
+    elements = T_rows * E;
+    if constexpr (!kImage) {  // vectors behind the row's end are never copied: they hold -inf
       Row low;
       low.fill(from_f32<T>(-INFINITY));
 #pragma unroll
@@ -252,94 +259,141 @@ struct RowStream {
 #pragma unroll
         for (int v = 0; v < NV; ++v)
           if (v * L.lpr * VEC >= room)
-            *reinterpret_cast<uint4*>(ring + i * kStageElems + (v * 32 + (threadIdx.x & 31)) * VEC) =
+            *reinterpret_cast<uint4*>(ring + i * kStageBytes + (v * 32 + (threadIdx.x & 31)) * 16) =
                 *reinterpret_cast<const uint4*>(low.raw);
     }
   }
-  // `first`: this group's row of the warp's first batch; a batch every `rows` rows
-  __device__ __forceinline__ void start(const T* logits, int64_t first, int64_t rows) {
-    p = logits + first * E + L.sub * VEC;
+  // `first`: the warp's first row; a batch every `rows` rows
+  __device__ __forceinline__ void start(int64_t first, int64_t rows) {
+    p = logits + (kImage ? first * E : (first + L.grp) * E + L.sub * VEC);
     step = rows * E;
     head = tail = 0;
-    nxt.fill(from_f32<T>(-INFINITY));
   }
-  // Rows that are not `ok` are not read: their cells keep what they hold, or are
-  // zeroed (ZERO).
+  static __device__ __forceinline__ int place(const T* q) {
+    return (int)(reinterpret_cast<uintptr_t>(q) % 16 / sizeof(T));
+  }
+  // Rows that are not `ok` are not read (unless they lie beside others, kImage):
+  // their cells hold anything, or (ZERO, vectors) zeros.
   template <bool ZERO = false>
   __device__ __forceinline__ void issue(bool ok) {
-    if constexpr (VEC > 1) {
-      const uint32_t to =
-          (uint32_t)__cvta_generic_to_shared(ring + tail * kStageElems) + (threadIdx.x & 31) * 16;
+    const uint32_t to = (uint32_t)__cvta_generic_to_shared(ring) + tail * kStageBytes;
+    const int lane = threadIdx.x & 31;
+    if constexpr (!kImage) {
 #pragma unroll
       for (int v = 0; v < NV; ++v)
         if ((ZERO || ok) && v * L.lpr * VEC < room)  // (a copy of 0 bytes writes zeros)
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + v * 512),
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + (v * 32 + lane) * 16),
                        "l"(p + v * L.lpr * VEC), "r"(ok ? 16 : 0)
                        : "memory");
-      asm volatile("cp.async.commit_group;" ::: "memory");
-      tail = tail + 1 == kStages ? 0 : tail + 1;
     } else {
-      nxt.load(p, room, L.lpr, ok);
-      if (ZERO && !ok) nxt.zero(room, L.lpr);
+      __syncwarp();  // every lane has read what lay here
+      if (__any_sync(0xffffffffu, ok)) {
+        constexpr int C = 16 / (int)sizeof(T);
+        const int at = place(p);
+        const int64_t from = p - logits - at;  // element of the first piece (may lie before the first row)
+        const int pieces = (at + L.rows * E + C - 1) / C;
+        for (int c = lane; c < pieces; c += 32) {
+          const int64_t e = from + c * C;
+          if (e >= 0 && e + C <= elements) {
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + c * 16), "l"(logits + e) : "memory");
+          } else {  // the first or the last piece of all rows: only what is theirs
+            T* out = reinterpret_cast<T*>(ring + tail * kStageBytes) + c * C;
+            for (int i = 0; i < C; ++i)
+              if (e + i >= 0 && e + i < elements) out[i] = __ldg(logits + e + i);
+          }
+        }
+      }
     }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    tail = tail + 1 == kStages ? 0 : tail + 1;
     p += step;
   }
-  // The oldest batch issued becomes the current one.  Elements behind a row's end
-  // are -inf.
-  __device__ __forceinline__ void take(Row& cur) {
-    if constexpr (VEC > 1) {
-      asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
-      head = tail == kStages - 1 ? 0 : tail + 1;  // issued kStages - 1 ago
-      const T* from = ring + head * kStageElems + (threadIdx.x & 31) * VEC;
+  // The oldest batch issued becomes the current one: wait() lets it lie in shared
+  // memory, get() reads this lane's elements.  Those behind a row's end are -inf.
+  __device__ __forceinline__ void wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+    head = tail == kStages - 1 ? 0 : tail + 1;  // issued kStages - 1 ago
+    if constexpr (kImage) {
+      shift = place(p - (kStages - 1) * step);
+      __syncwarp();
+    }
+  }
+  __device__ __forceinline__ void get(Row& cur) const {
+    if constexpr (!kImage) {
+      const T* from = stage() + (threadIdx.x & 31) * VEC;
 #pragma unroll
       for (int v = 0; v < NV; ++v)
         *reinterpret_cast<uint4*>(cur.raw + v * VEC) = *reinterpret_cast<const uint4*>(from + v * 32 * VEC);
     } else {
-      cur = nxt;
-      put(cur);
+      const T* from = stage() + shift + L.grp * E + L.sub;
+#pragma unroll
+      for (int v = 0; v < NV; ++v) cur.raw[v] = v * L.lpr < room ? from[v * L.lpr] : from_f32<T>(-INFINITY);
     }
   }
-  __device__ __forceinline__ void drain() {
-    if constexpr (VEC > 1) asm volatile("cp.async.wait_all;" ::: "memory");
+  __device__ __forceinline__ void take(Row& cur) {
+    wait();
+    get(cur);
   }
-  __device__ __forceinline__ T* stage() const { return ring + (VEC > 1 ? head * kStageElems : 0); }
+  __device__ __forceinline__ void drain() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+  __device__ __forceinline__ T* stage() const { return reinterpret_cast<T*>(ring + head * kStageBytes); }
   __device__ __forceinline__ T& cell(int e) const {
+    if constexpr (kImage) return stage()[shift + L.grp * E + e];
     const int q = e / VEC;
     return stage()[((q >> lpr_log) * 32 + L.grp * L.lpr + (q & (L.lpr - 1))) * VEC + e % VEC];
   }
   // Writes this lane's elements of the current batch.
   __device__ __forceinline__ void put(const Row& r) const {
-    T* to = stage() + (threadIdx.x & 31) * VEC;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       if (v * L.lpr * VEC >= room) continue;
-      if constexpr (VEC > 1)
-        *reinterpret_cast<uint4*>(to + v * 32 * VEC) = *reinterpret_cast<const uint4*>(r.raw + v * VEC);
+      if constexpr (!kImage)
+        *reinterpret_cast<uint4*>(stage() + (v * 32 + (threadIdx.x & 31)) * VEC) =
+            *reinterpret_cast<const uint4*>(r.raw + v * VEC);
       else
-        to[v * 32] = r.raw[v];
+        cell(v * L.lpr + L.sub) = r.raw[v];
     }
   }
   __device__ __forceinline__ void put(const float (&f)[VEC * NV]) const {
-    T* to = stage() + (threadIdx.x & 31) * VEC;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       if (v * L.lpr * VEC >= room) continue;
       float g[VEC];
 #pragma unroll
       for (int i = 0; i < VEC; ++i) g[i] = f[v * VEC + i];
-      store_row<T, VEC, 1>(to + v * 32 * VEC, VEC, 1, g);
+      store_row<T, VEC, 1>(kImage ? &cell(v * L.lpr + L.sub) : stage() + (v * 32 + (threadIdx.x & 31)) * VEC, VEC, 1, g);
     }
   }
-  // Stores this lane's elements of the current batch to `row` (this lane's first).
-  __device__ __forceinline__ void store(T* row) const {
-    const T* from = stage() + (threadIdx.x & 31) * VEC;
+  // Stores the current batch, the first `left` rows from row t0 on, to `out`.  All
+  // lanes take part; what they put() lies in shared memory (a __syncwarp before).
+  __device__ __forceinline__ void store(T* out, int64_t t0, int left) const {
+    const int lane = threadIdx.x & 31;
+    if constexpr (!kImage) {
+      if (L.grp >= left) return;
+      T* row = out + (t0 + L.grp) * E + L.sub * VEC;
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      if (v * L.lpr * VEC >= room) continue;
-      if constexpr (VEC > 1)
-        *reinterpret_cast<uint4*>(row + v * L.lpr * VEC) = *reinterpret_cast<const uint4*>(from + v * 32 * VEC);
-      else
-        row[v * L.lpr] = from[v * 32];
+      for (int v = 0; v < NV; ++v)
+        if (v * L.lpr * VEC < room)
+          *reinterpret_cast<uint4*>(row + v * L.lpr * VEC) =
+              *reinterpret_cast<const uint4*>(stage() + (v * 32 + lane) * VEC);
+    } else {
+      constexpr int C = 16 / (int)sizeof(T);
+      T* to = out + t0 * E;
+      const T* from = stage() + shift;
+      const int n = min(L.rows, left) * E;
+      if (place(to) == shift) {  // as the logits lie: whole pieces
+        const int pieces = (shift + n + C - 1) / C;
+        for (int c = lane; c < pieces; c += 32) {
+          const int e = c * C - shift;
+          if (e >= 0 && e + C <= n) {
+            *reinterpret_cast<uint4*>(to + e) = *reinterpret_cast<const uint4*>(from + e);
+          } else {
+            for (int i = 0; i < C; ++i)
+              if (e + i >= 0 && e + i < n) to[e + i] = from[e + i];
+          }
+        }
+      } else {
+        for (int e = lane; e < n; e += 32) to[e] = from[e];
+      }
     }
   }
 };
@@ -462,13 +516,12 @@ __device__ __forceinline__ void walk_sequences(const Seqs& q, int64_t a, int64_t
 }
 
 // ---- variants by row length ------------------------------------------------------
-// Vectors of 16 bytes where every row starts on a 16-byte boundary: up to eight
-// lanes a row (a load then covers whole 128-byte lines), then up to 64 bytes of
-// 16-bit or FP32 logits a lane, then more lanes.  Few lanes a row make its
-// reductions and its scalar work cheap, since a warp does them for several rows
-// at once: a forward over 256 BF16 logits a row took 136 instructions a row with
-// a warp each and about half of it with eight lanes each.  Rows that start on
-// any element are read in single elements, 32 lanes a row.
+// Vectors of 16 bytes where every row starts on a 16-byte boundary, else single
+// elements.  Up to eight lanes a row (a copy then covers whole 128-byte lines), then
+// up to 64 bytes or 32 single elements a lane, then more lanes.  Few lanes a row make
+// its reductions and its scalar work cheap, since a warp does them for several rows
+// at once: a forward over 256 BF16 logits a row took 136 instructions a row with a
+// warp each and about half of it with eight lanes each.
 struct RowPlan {
   bool vec;
   int lpr;
@@ -480,8 +533,9 @@ inline RowPlan row_plan(const void* const* ptrs, int n_ptrs, moe_dtype dt, int E
   for (int i = 0; i < n_ptrs; ++i) vec = vec && reinterpret_cast<uintptr_t>(ptrs[i]) % 16 == 0;
   const int units = vec ? E * esz / 16 : E;
   RowPlan p{vec, 1, 1};
-  while (p.lpr < (vec ? 8 : 32) && p.lpr < units) p.lpr *= 2;
-  while (p.nv < 4 && p.lpr * p.nv < units) p.nv *= 2;
+  while (p.lpr < 8 && p.lpr < units) p.lpr *= 2;
+  if (!vec && p.lpr < units) p.nv = 4;  // (1, 4, 8, 16 or 32 elements a lane)
+  while (p.nv < (vec ? 4 : 32) && p.lpr * p.nv < units) p.nv *= 2;
   while (p.lpr < 32 && p.lpr * p.nv < units) p.lpr *= 2;
   while (p.lpr * p.nv < units) p.nv *= 2;
   return p;
@@ -504,11 +558,13 @@ cudaError_t with_row_variant(const RowPlan& p, F&& f) {
   }
   switch (p.nv) {
     case 1: return f.template run<T, 1, 1, 0>();
-    case 2: return f.template run<T, 1, 2, 32>();
-    case 4: return f.template run<T, 1, 4, 32>();
-    case 8: return f.template run<T, 1, 8, 32>();
-    case 16: return f.template run<T, 1, 16, 32>();
-    default: return f.template run<T, 1, 32, 32>();
+    case 4: return f.template run<T, 1, 4, 8>();
+    case 8: return f.template run<T, 1, 8, 8>();
+    case 16: return f.template run<T, 1, 16, 8>();
+    default:
+      if (p.lpr == 8) return f.template run<T, 1, 32, 8>();
+      if (p.lpr == 16) return f.template run<T, 1, 32, 16>();
+      return f.template run<T, 1, 32, 32>();
   }
 }
 template <typename F>
@@ -521,7 +577,7 @@ cudaError_t with_row_variant(moe_dtype dt, const RowPlan& p, F&& f) {
 // holds of its kernels (blocks_per_sm).
 constexpr int kMaxBlocks = 152 * 4;
 inline int plan_batch(const RowPlan& p) { return 32 / p.lpr; }
-inline int plan_blocks(const RowPlan& p, int most = 4) { return 152 * blocks_for(p.nv * (p.vec ? 16 : 4), most); }
+inline int plan_blocks(const RowPlan& p, int most = 4) { return 152 * blocks_for(p.nv * (p.vec ? 16 : 2), most); }
 
 // Launches a kernel that may need more shared memory than the default, which is
 // asked for once per kernel and device.
