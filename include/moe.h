@@ -338,9 +338,10 @@ moe_status moe_forward_layout(moe_experts_t experts, int64_t T, int32_t top_k,
                               moe_dtype logits_dtype, moe_forward_layout_t* out);
 
 /* Reads the device status word at the start of `workspace` after
- * synchronising `stream`: MOE_OK, MOE_ERR_INVALID_INDEX (dispatch met an
- * index >= E, or a staged expert call met offsets that are not
- * non-decreasing within N) or MOE_ERR_DEVICE_TIMEOUT (a kernel's bounded wait
+ * synchronising `stream`: MOE_OK, MOE_ERR_INVALID_INDEX (dispatch or a router
+ * loss met an index >= E or a teacher's list with an expert twice, or a staged
+ * expert call or a router loss met offsets that are not non-decreasing within
+ * their rows) or MOE_ERR_DEVICE_TIMEOUT (a kernel's bounded wait
  * expired and the kernel returned early; its outputs are undefined).
  * MOE_ERR_CUDA if the synchronisation itself fails. */
 moe_status moe_get_device_status(const void* workspace, cudaStream_t stream);

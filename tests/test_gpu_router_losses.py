@@ -521,6 +521,75 @@ def test_malformed_offsets_stay_inside_and_are_reported(cuda_lib, bad):
     assert cuda_lib.moe_get_device_status(bal.workspace) == 0 and int(good.tokens[0]) == T
 
 
+@pytest.mark.parametrize("T,E,k,dt", [(90000, 24, 3, "bf16"), (70000, 64, 6, "f32"), (60000, 96, 8, "f16"),
+                                      (50000, 131, 5, "bf16"), (40000, 200, 9, "f32"), (50000, 257, 20, "f16"),
+                                      (50000, 256, 40, "bf16"), (20000, 1000, 12, "bf16"), (15000, 999, 7, "f32")])
+def test_long_batches_match_their_parts(cuda_lib, T, E, k, dt):
+    """Batches long enough that every warp goes round its ring of rows several
+    times: a row's results do not depend on the batch around it, and the sums are
+    those of the rows (in 64 bits)."""
+    l, teacher, g = _step_inputs(T, E, k, dt, 20)
+    idx, _ = cuda_lib.moe_route(l, k, False)
+    mask = (torch.rand(T, generator=g) < 0.9).cuda()
+    off = torch.tensor([3, 1000, T // 2 + 1, T // 2 + 1, T - 5], dtype=torch.int32, device="cuda")
+    one = torch.linspace(0.5, 1.5, 4, device="cuda")
+    bal = cuda_lib.moe_balance_loss(l, idx, token_mask=mask, seq_offsets=off, z_loss=True)
+    tg = cuda_lib.moe_distill_targets(teacher, k)
+    dis = cuda_lib.moe_distill_loss(l, tg, token_mask=mask, seq_offsets=off)
+    db = cuda_lib.moe_balance_loss_backward(l, bal, k, one, seq_offsets=off, dz_loss=one)
+    dd = cuda_lib.moe_distill_loss_backward(l, tg, dis, one, seq_offsets=off)
+    assert cuda_lib.moe_get_device_status(bal.workspace) == 0
+    for s, (a, b) in enumerate(zip([3, 1000, T // 2 + 1, T // 2 + 1], [1000, T // 2 + 1, T // 2 + 1, T - 5])):
+        rows = torch.arange(a, b, device="cuda")[mask[a:b]]
+        n = len(rows)
+        assert int(bal.tokens[s]) == n and int(dis.tokens[s]) == n
+        if n == 0:
+            continue
+        assert torch.equal(bal.counts[s].long(), torch.bincount(idx[rows].long().flatten(), minlength=E))
+        p = torch.softmax(l[rows].double(), 1).mean(0)
+        _close(bal.mean_scores[s], p.cpu(), what="mean_scores")
+        _close(dis.loss[s], dis.row_loss[rows].double().mean().cpu(), what="distillation loss")
+        z = (torch.logsumexp(l[rows].double(), 1) ** 2).mean()
+        _close(bal.z_loss[s], z.cpu(), at=32 * 2.0 ** -20, what="z_loss")
+        for c in (a, (a + b) // 2, b - 200):  # the same rows alone
+            part = slice(c, c + 200)
+            m = mask[part].contiguous()
+            pl, pi = l[part].clone(), idx[part].clone()
+            pb = cuda_lib.moe_balance_loss(pl, pi, token_mask=m)
+            assert torch.equal(_bits(pb.row_stats), _bits(bal.row_stats[part]))
+            pt = cuda_lib.moe_distill_targets(teacher[part].clone(), k)
+            for x, y in ((pt.idx, tg.idx), (pt.logits, tg.logits), (pt.rest, tg.rest)):
+                assert torch.equal(_bits(x), _bits(y[part]))
+            pd = cuda_lib.moe_distill_loss(pl, pt, token_mask=m)
+            assert torch.equal(_bits(pd.row_loss), _bits(dis.row_loss[part]))
+            assert torch.equal(_bits(pd.row_stats), _bits(dis.row_stats[:, part]))
+            pb.counts, pb.tokens, pd.tokens = bal.counts[s:s + 1], bal.tokens[s:s + 1], dis.tokens[s:s + 1]
+            w = one[s:s + 1].contiguous()
+            assert torch.equal(_bits(cuda_lib.moe_balance_loss_backward(pl, pb, k, w, dz_loss=w)), _bits(db[part]))
+            assert torch.equal(_bits(cuda_lib.moe_distill_loss_backward(pl, pt, pd, w)), _bits(dd[part]))
+    for out in (bal.row_stats, db, dd):  # rows outside every sequence
+        assert not out[:3].any() and not out[T - 5:].any()
+
+
+def test_results_that_are_replaced_are_checked_again(cuda_lib):
+    l, idx = torch.randn((8, 6), device="cuda"), torch.zeros((8, 2), dtype=torch.int32, device="cuda")
+    bal = cuda_lib.moe_balance_loss(l, idx)
+    one = torch.ones(1, device="cuda")
+    bal.counts = bal.counts.long()
+    with pytest.raises(cuda_lib.MoeError):
+        cuda_lib.moe_balance_loss_backward(l, bal, 2, one)
+    bal.counts = torch.zeros((1, 5), dtype=torch.int32, device="cuda")
+    with pytest.raises(cuda_lib.MoeError):
+        cuda_lib.moe_balance_loss_backward(l, bal, 2, one)
+    bal = cuda_lib.moe_balance_loss(l, idx)
+    cuda_lib.moe_balance_loss(l, idx, out=bal)
+    bal.row_stats.resize_(4, 2)
+    with pytest.raises(cuda_lib.MoeError):
+        cuda_lib.moe_balance_loss(l, idx, out=bal)
+    with pytest.raises(cuda_lib.MoeError):
+        cuda_lib.moe_balance_loss(l[:4].contiguous(), idx[:4].contiguous(), out=bal, z_loss=True)
+
+
 def test_no_rows(cuda_lib):
     """T = 0, and sequences that hold nothing."""
     l, idx = torch.empty((0, 8), device="cuda"), torch.empty((0, 2), dtype=torch.int32, device="cuda")

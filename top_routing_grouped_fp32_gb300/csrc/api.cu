@@ -1093,7 +1093,7 @@ moe_status moe_get_device_status(const void* ws, cudaStream_t stream) {
   MOE_TRY_CUDA(cudaMemcpyAsync(&v, ws, 4, cudaMemcpyDeviceToHost, stream), "cudaMemcpyAsync status");
   MOE_TRY_CUDA(cudaStreamSynchronize(stream), "cudaStreamSynchronize");
   if (v == MOE_OK) return ok();
-  if (v == MOE_ERR_INVALID_INDEX) return fail(MOE_ERR_INVALID_INDEX, "an expert index >= E reached dispatch");
+  if (v == MOE_ERR_INVALID_INDEX) return fail(MOE_ERR_INVALID_INDEX, "an expert index >= E, an expert listed twice or malformed offsets");
   if (v == MOE_ERR_DEVICE_TIMEOUT)
     return fail(MOE_ERR_DEVICE_TIMEOUT, "a bounded wait inside a kernel expired");
   return fail(MOE_ERR_CUDA, "unknown device status %u", v);

@@ -118,24 +118,44 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, VEC, NV>()) balance
   auto gap = [&](int64_t lo, int64_t hi) {
     for (int64_t t = lo + threadIdx.x; t < hi; t += kThreads) a.row_stats[t] = make_float2(0.f, 0.f);
   };
-  auto piece = [&](int seq, int64_t lo, int64_t hi) {
-    uint32_t bad = 0, valid = 0;
-    float acc[N], zacc = 0.f;
+  // The piece of a sequence that the block works on, and the state of this warp in it.
+  const int64_t c0 = (int64_t)blockIdx.x * a.chunk_rows, c1 = min(c0 + a.chunk_rows, a.T);
+  int seq = 0;
+  int64_t lo = 0, hi = a.T;
+  int64_t t0;  // the batch's first row
+  int left;    // rows from there on (a block has far fewer than 2^31)
+  // does this group's row of a batch count: bit i for the i-th batch from here.
+  // The mask's byte is fetched a batch before its bit is needed.
+  uint32_t on;
+  uint8_t byte;
+  auto fetch = [&](int ahead) {
+    const int i = ahead * step + L.grp;
+    if (a.mask) byte = i < left ? __ldg(a.mask + t0 + i) : 0;
+  };
+  auto bit = [&](int ahead) { return (uint32_t)(ahead * step + L.grp < left && byte) << ahead; };
+  // Counts of the piece's slots, 32 NI a warp at a time and behind the rows: 256
+  // experts' rows with top-8 take a turn in four batches.  A turn's indices are on
+  // their way since the last one; a lane adds to its copy.
+  int slots, at;
+  const uint32_t* ip;
+  uint32_t id[NI];
+  auto indices = [&]() {
+    if (at + 32 * NI <= slots) {
 #pragma unroll
-    for (int n = 0; n < N; ++n) acc[n] = 0.f;
-
-    int64_t t0 = lo + warp * batch;     // the batch's first row
-    int left = (int)(hi - t0);          // rows from there on (a block has far fewer than 2^31)
+      for (int i = 0; i < NI; ++i) id[i] = __ldg(ip + at + 32 * i);
+    } else {
+#pragma unroll
+      for (int i = 0; i < NI; ++i) id[i] = at + lane + 32 * i < slots ? __ldg(ip + at + 32 * i) : 0u;
+    }
+  };
+  // Asks for a piece's first rows and indices.
+  auto begin = [&]() {
+    t0 = lo + warp * batch;
+    left = (int)(hi - t0);
     rows.start(t0, step);
-    // does this group's row of a batch count: bit i for the i-th batch from here.
-    // The mask's byte is fetched a batch before its bit is needed.
-    uint32_t on = 0;
-    uint8_t byte = 1, early[S];
-    auto fetch = [&](int ahead) {
-      const int i = ahead * step + L.grp;
-      if (a.mask) byte = i < left ? __ldg(a.mask + t0 + i) : 0;
-    };
-    auto bit = [&](int ahead) { return (uint32_t)(ahead * step + L.grp < left && byte) << ahead; };
+    on = 0;
+    byte = 1;
+    uint8_t early[S];
 #pragma unroll
     for (int i = 0; i < S; ++i) {
       fetch(i);
@@ -148,22 +168,38 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, VEC, NV>()) balance
       rows.template issue<true>(on >> i & 1u);
     }
     byte = early[S - 1];
-    // Counts of the piece's slots, 32 NI a warp at a time and behind the rows: 256
-    // experts' rows with top-8 take a turn in four batches.  A turn's indices are on
-    // their way since the last one; a lane adds to its copy.
-    const int slots = (int)(hi - lo) * a.k;
-    int at = warp * 32 * NI;
-    uint32_t id[NI];
-    const uint32_t* const ip = a.idx + lo * a.k + lane;
-    auto indices = [&]() {
-      if (at + 32 * NI <= slots) {
-#pragma unroll
-        for (int i = 0; i < NI; ++i) id[i] = __ldg(ip + at + 32 * i);
-      } else {
-#pragma unroll
-        for (int i = 0; i < NI; ++i) id[i] = at + lane + 32 * i < slots ? __ldg(ip + at + 32 * i) : 0u;
+    slots = (int)(hi - lo) * a.k;
+    at = warp * 32 * NI;
+    ip = a.idx + lo * a.k + lane;
+    indices();
+  };
+  // The next piece from sequence s and row `from` on, if the block has one; rows
+  // before it that lie in no sequence get their zeros.
+  auto advance = [&](int s, int64_t from) {
+    for (; from < c1; ++s) {
+      if (s >= a.seqs.num) {
+        gap(from, c1);
+        return false;
       }
-    };
+      lo = min(max(a.seqs.at(s), from), c1);
+      hi = min(max(a.seqs.at(s + 1), lo), c1);
+      if (lo > from) gap(from, lo);
+      from = hi;
+      seq = s;
+      if (hi > lo) return true;
+    }
+    return false;
+  };
+
+  bool more = a.alone || advance(a.seqs.first(c0), c0);
+  if (more) begin();
+  while (more) {
+    for (int i = threadIdx.x; i < a.E * a.copies; i += kThreads) hist[i] = 0u;
+    __syncthreads();
+    uint32_t bad = 0, valid = 0;
+    float acc[N], zacc = 0.f;
+#pragma unroll
+    for (int n = 0; n < N; ++n) acc[n] = 0.f;
     auto count = [&]() {
       if (!a.mask && at + 32 * NI <= slots) {
 #pragma unroll
@@ -184,9 +220,6 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, VEC, NV>()) balance
       at += kWarps * 32 * NI;
       indices();
     };
-    indices();
-    for (int i = threadIdx.x; i < a.E * a.copies; i += kThreads) hist[i] = 0u;
-    __syncthreads();
     int due = 0;  // slots of the rows that the block's warps have taken
     // A lane keeps the maximum and sum of its group's row of every lpr-th batch; then
     // the whole warp writes a row's statistics a lane.
@@ -231,6 +264,10 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, VEC, NV>()) balance
     flush();
     while (at < slots) count();
     rows.drain();
+    // the next piece's rows are on their way while this one's sums are added
+    const int64_t slot = (int64_t)blockIdx.x + seq;
+    more = !a.alone && advance(seq + 1, hi);
+    if (more) begin();
     // the rows of a warp, then the warps, in a fixed order
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -256,7 +293,6 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, VEC, NV>()) balance
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) z += red_z[w], rows += red_rows[w], wrong += red_bad[w];
     const float inv = rows ? 1.f / (float)rows : 0.f;
-    const int64_t slot = (int64_t)blockIdx.x + seq;
     for (int e = threadIdx.x; e < a.E; e += kThreads) {
       float s = 0.f;
 #pragma unroll
@@ -293,13 +329,8 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, VEC, NV>()) balance
       }
     }
     __syncthreads();  // before the next piece writes the shared arrays
-  };
-  if (a.alone) {
-    piece(0, 0, a.T);
-    return;
   }
-  const int64_t c0 = (int64_t)blockIdx.x * a.chunk_rows;
-  walk_sequences(a.seqs, c0, min(c0 + a.chunk_rows, a.T), piece, gap);
+  rows.drain();
 }
 
 struct FinishArgs {
@@ -479,10 +510,10 @@ cudaError_t launch_balance_loss(const BalanceArgs& b, void* ws, uint32_t* status
   if (e != cudaSuccess || a.alone) return e;
   // a block for each group of experts while the blocks fit the GPU at once, at most
   // eight (a cluster); many slots a sequence are added by more warps
-  int blocks = 1;
-  while (blocks < 8 && blocks * 32 < b.E && b.num_seqs * blocks < 152) blocks *= 2;
   const FinishArgs f{part, a.seqs, b.E, b.k, ch.rows, a.res};
   const bool many = ch.chunks / b.num_seqs >= 32;
+  int blocks = 1;
+  while (blocks < 8 && blocks * 32 < b.E && b.num_seqs * blocks < (many ? 152 : 152 * 4)) blocks *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(b.num_seqs * blocks));
   cfg.blockDim = dim3(many ? 1024 : 256);
