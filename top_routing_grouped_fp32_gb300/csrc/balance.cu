@@ -341,6 +341,74 @@ struct FinishArgs {
   Results res;
 };
 
+// Slots first, .., first + count - 1 hold sequence s (rows fit 32 bits).
+struct SlotRange {
+  int64_t first;
+  int count;
+  __device__ __forceinline__ SlotRange(const FinishArgs& a, uint32_t s, uint32_t lo, uint32_t hi) {
+    const uint32_t chunk = (uint32_t)a.chunk_rows, from = lo / chunk;
+    count = hi > lo ? (int)((hi - 1) / chunk - from) + 1 : 0;
+    first = (int64_t)from + s;
+  }
+};
+__device__ __forceinline__ bool malformed(const Seqs& q, uint32_t s, uint32_t lo, uint32_t hi) {
+  return q.off && (hi < lo || (int64_t)__ldg(q.off + s) > q.T || (int64_t)__ldg(q.off + s + 1) > q.T);
+}
+template <typename V>
+__device__ __forceinline__ V warp_sum(V x) {
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
+  return x;
+}
+
+// Few slots a sequence: a block for each, a thread for each expert, which adds the
+// slots one after another, 16 on their way at a time.  The whole loss of 65537 rows
+// of 256 FP32 logits in 128 sequences (2.4 slots each) takes 24 us with it and 31 us
+// with the kernel below; in 37 sequences (8.2 each, some of them long) 27 and 25 us.
+__global__ void __launch_bounds__(1024) balance_finish_few_kernel(FinishArgs a) {
+  __shared__ float snp[32];
+  pdl_wait();
+  pdl_trigger();
+  const uint32_t s = blockIdx.x;
+  const int e = threadIdx.x, warp = e >> 5, lane = e & 31;
+  const uint32_t lo = (uint32_t)a.seqs.at(s), hi = (uint32_t)a.seqs.at(s + 1);
+  const SlotRange r(a, s, lo, hi);
+  constexpr int U = 16;
+  float ps = 0.f, z = 0.f;
+  uint32_t ns = 0, rows = 0, bad = 0;
+  for (int i0 = 0; i0 < r.count; i0 += U) {
+    float p[U], zz[U];
+    uint32_t n[U], v[U], b[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t i = r.first + i0 + u;
+      const bool in = i0 + u < r.count;
+      p[u] = in && e < a.E ? __ldcg(a.part.p + i * a.E + e) : 0.f;
+      n[u] = in && e < a.E ? __ldcg(a.part.n + i * a.E + e) : 0u;
+      v[u] = in ? __ldcg(a.part.rows + i) : 0u;
+      zz[u] = in && e == 0 ? __ldcg(a.part.z + i) : 0.f;
+      b[u] = in && e == 0 ? __ldcg(a.part.bad + i) : 0u;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) ps += p[u], ns += n[u], rows += v[u], z += zz[u], bad += b[u];
+  }
+  if (e < a.E) {
+    a.res.counts[(int64_t)s * a.E + e] = ns;
+    if (a.res.mean_scores) a.res.mean_scores[(int64_t)s * a.E + e] = rows ? ps / (float)rows : 0.f;
+  }
+  float np = warp_sum((float)ns * ps);
+  if (lane == 0) snp[warp] = np;
+  __syncthreads();
+  if (warp != 0) return;
+  np = warp_sum(lane < (int)(blockDim.x >> 5) ? snp[lane] : 0.f);
+  if (lane == 0) {
+    a.res.loss[s] = balance_of(np, a.E, a.k, rows);
+    if (a.res.z_loss) a.res.z_loss[s] = rows ? z / (float)rows : 0.f;
+    a.res.tokens[s] = rows;
+    if (bad || malformed(a.seqs, s, lo, hi)) set_status(a.res.status, MOE_ERR_INVALID_INDEX);
+  }
+}
+
 // Adds a sequence's slots, 32 experts x W slot lanes at a time.  A sequence has a
 // cluster of blocks, each with every blocks-th group of 32 experts; block 0 adds
 // their shares of the loss in order.
@@ -354,18 +422,12 @@ __global__ void __launch_bounds__(32 * W) balance_finish_kernel(FinishArgs a) {
   const uint32_t part = cl.block_rank(), blocks = cl.num_blocks();
   const uint32_t s = blockIdx.x / blocks;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  auto add = [](auto x) {
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
-    return x;
-  };
   pdl_wait();
   pdl_trigger();
-  // slots first, .., first + count - 1 hold the sequence (rows fit 32 bits)
-  const uint32_t lo = (uint32_t)a.seqs.at(s), hi = (uint32_t)a.seqs.at(s + 1), chunk = (uint32_t)a.chunk_rows;
-  const uint32_t from = lo / chunk;
-  const int count = hi > lo ? (int)((hi - 1) / chunk - from) + 1 : 0;
-  const int64_t first = (int64_t)from + s;
+  const uint32_t lo = (uint32_t)a.seqs.at(s), hi = (uint32_t)a.seqs.at(s + 1);
+  const SlotRange r(a, s, lo, hi);
+  const int64_t first = r.first;
+  const int count = r.count;
   // every load of a thread is on its way before the first is used: U slots a lane
   constexpr int U = 10;
   auto load = [&](uint32_t e, int i0, float (&p)[U], uint32_t (&n)[U]) {
@@ -386,7 +448,7 @@ __global__ void __launch_bounds__(32 * W) balance_finish_kernel(FinishArgs a) {
     rows += a.part.rows[first + i];
     bad += a.part.bad[first + i];
   }
-  z = add(z), rows = add(rows), bad = add(bad);
+  z = warp_sum(z), rows = warp_sum(rows), bad = warp_sum(bad);
   if (lane == 0) sz[warp] = z, sv[warp] = rows, sb[warp] = bad;
   for (uint32_t e0 = part * 32; e0 < (uint32_t)a.E; e0 += blocks * 32) {
     float ps = 0.f;
@@ -400,12 +462,12 @@ __global__ void __launch_bounds__(32 * W) balance_finish_kernel(FinishArgs a) {
     sn[lane][warp] = ns;
     __syncthreads();
     // a warp for each expert's slot lanes; every W experts
-    rows = add(lane < W ? sv[lane] : 0u);
+    rows = warp_sum(lane < W ? sv[lane] : 0u);
     const float inv = rows ? 1.f / (float)rows : 0.f;
 #pragma unroll
     for (int x = warp; x < 32; x += W) {
-      const float px = add(lane < W ? sp[x][lane] : 0.f);
-      const uint32_t nx = add(lane < W ? sn[x][lane] : 0u);
+      const float px = warp_sum(lane < W ? sp[x][lane] : 0.f);
+      const uint32_t nx = warp_sum(lane < W ? sn[x][lane] : 0u);
       if (lane == 0 && e0 + x < (uint32_t)a.E) {
         a.res.counts[(int64_t)s * a.E + e0 + x] = nx;
         if (a.res.mean_scores) a.res.mean_scores[(int64_t)s * a.E + e0 + x] = rows ? px * inv : 0.f;
@@ -417,22 +479,20 @@ __global__ void __launch_bounds__(32 * W) balance_finish_kernel(FinishArgs a) {
   if (lane == 0) snp[warp] = np;
   __syncthreads();
   if (warp == 0) {
-    np = add(lane < W ? snp[lane] : 0.f);
+    np = warp_sum(lane < W ? snp[lane] : 0.f);
     if (lane == 0) share = np;
   }
   if (blocks > 1) cl.sync();
   if (part == 0 && warp == 0) {
-    if (blocks > 1) np = add(lane < (int)blocks ? *cl.map_shared_rank(&share, lane) : 0.f);
-    z = add(lane < W ? sz[lane] : 0.f);
-    bad = add(lane < W ? sb[lane] : 0u);
-    rows = add(lane < W ? sv[lane] : 0u);
+    if (blocks > 1) np = warp_sum(lane < (int)blocks ? *cl.map_shared_rank(&share, lane) : 0.f);
+    z = warp_sum(lane < W ? sz[lane] : 0.f);
+    bad = warp_sum(lane < W ? sb[lane] : 0u);
+    rows = warp_sum(lane < W ? sv[lane] : 0u);
     if (lane == 0) {
       a.res.loss[s] = balance_of(np, a.E, a.k, rows);
       if (a.res.z_loss) a.res.z_loss[s] = rows ? z / (float)rows : 0.f;
       a.res.tokens[s] = rows;
-      const bool malformed = a.seqs.off && (hi < lo || (int64_t)__ldg(a.seqs.off + s) > a.seqs.T ||
-                                            (int64_t)__ldg(a.seqs.off + s + 1) > a.seqs.T);
-      if (bad || malformed) set_status(a.res.status, MOE_ERR_INVALID_INDEX);
+      if (bad || malformed(a.seqs, s, lo, hi)) set_status(a.res.status, MOE_ERR_INVALID_INDEX);
     }
   }
   if (blocks > 1) cl.sync();  // the shares are read
@@ -508,12 +568,14 @@ cudaError_t launch_balance_loss(const BalanceArgs& b, void* ws, uint32_t* status
     e = with_row_variant(b.dt, plan, f);
   }
   if (e != cudaSuccess || a.alone) return e;
-  // a block for each group of experts while the blocks fit the GPU at once, at most
-  // eight (a cluster); many slots a sequence are added by more warps
   const FinishArgs f{part, a.seqs, b.E, b.k, ch.rows, a.res};
-  const bool many = ch.chunks / b.num_seqs >= 32;
+  if (ch.chunks <= 4 * b.num_seqs)
+    return launch_pdl(balance_finish_few_kernel, dim3((unsigned)b.num_seqs), dim3((unsigned)(b.E + 31) / 32 * 32), 0, s,
+                      f);
+  // a block for each group of experts, at most eight (a cluster)
   int blocks = 1;
-  while (blocks < 8 && blocks * 32 < b.E && b.num_seqs * blocks < (many ? 152 : 152 * 4)) blocks *= 2;
+  while (blocks < 8 && blocks * 32 < b.E) blocks *= 2;
+  const bool many = ch.chunks / b.num_seqs >= 32;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(b.num_seqs * blocks));
   cfg.blockDim = dim3(many ? 1024 : 256);
