@@ -8,13 +8,16 @@
 //   loss_s = E sum_e n_se / (k L_s) P_se
 //   z_s    = 1/L_s sum_{t in V_s} (log sum_e exp l_te)^2
 //
-// One pass over the logits.  A block owns a range of rows; each lane
-// keeps the sum of p for its own experts in registers, the block adds its warps
-// in a fixed order and writes one partial per (block, sequence) that it meets,
-// at slot block + sequence (unique, since rows and sequences both ascend).  A
-// second kernel adds each sequence's slots in a fixed order; a batch that one
-// block holds needs none.  The counts are integers, so shared-memory atomics
-// leave them reproducible.
+// One pass over the logits.  A block owns a range of rows; each lane keeps the sum
+// of p for its own experts in registers, the block adds its warps in a fixed order
+// and writes one partial per (block, sequence) that it meets, at slot
+// block + sequence (unique, since rows and sequences both ascend).  A second kernel
+// adds each sequence's slots in a fixed order; a batch that one block holds needs
+// none.  The counts are integers, so shared-memory atomics leave them reproducible.
+//
+// 524288 rows of 256 BF16 logits, top-8: 57 us, 75 % of the copy bandwidth; the main
+// kernel alone takes 54 us (285 MB read, 69 instructions a row, 2.4 a cycle of a SM).
+// The sums and the scores of a lane's 32 elements leave room for 16 warps a SM.
 #include <cooperative_groups.h>
 
 #include "internal.h"

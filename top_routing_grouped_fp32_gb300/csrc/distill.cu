@@ -19,6 +19,9 @@
 // rest (over the mass outside the list, p alone, without a rest).  Every term is
 // >= 0 and of second order in log(q/p), so a student near its teacher loses no
 // digits and errors of the two normalisers cancel to first order.
+//
+// 524288 rows of 256 BF16 logits with lists of 8 and a rest: 84 us, 54 % of the copy
+// bandwidth.  Bound by issue: 130 instructions a row, 2.7 a cycle of a SM.
 #include "internal.h"
 #include "rows.cuh"
 
@@ -73,7 +76,7 @@ struct FwdArgs {
 // its elements are listed is a word of bits for each lane, set by the list's
 // lanes in shared memory, so that the mass outside the list is summed as it is and
 // not as a difference.  A lane keeps J entries in registers (1 where that holds the
-// list: 98 us against 106 for lists of 8 of 256, 524288 rows); more are read again
+// list: for lists of 8 of 256 and 524288 rows it took 98 us where 4 took 106); more are read again
 // where they are needed.  What a row needs once, and no other lane waits for, is
 // left until a warp can do it for a row a lane.
 template <typename T, int VEC, int NV, int LPR, int J>

@@ -43,7 +43,7 @@ cudaError_t dispatch_noalloc_scratch(void** out);
 cudaError_t launch_gather(const void* x, moe_dtype dt, int64_t H, int k, const uint32_t* perm,
                           const uint32_t* offsets, int E, int64_t N, void* x_disp, cudaStream_t s);
 
-// ---- training losses of the router (balance.cu, distill.cu) -------------------
+// ---- training losses of the router (balance*.cu, distill*.cu) -----------------
 struct BalanceArgs {
   const void* logits;
   moe_dtype dt;

@@ -520,8 +520,8 @@ __device__ __forceinline__ void walk_sequences(const Seqs& q, int64_t a, int64_t
 // elements.  Up to eight lanes a row (a copy then covers whole 128-byte lines), then
 // up to 64 bytes or 32 single elements a lane, then more lanes.  Few lanes a row make
 // its reductions and its scalar work cheap, since a warp does them for several rows
-// at once: a forward over 256 BF16 logits a row took 136 instructions a row with a
-// warp each and about half of it with eight lanes each.
+// at once: with it the balance loss of 524288 rows of 256 BF16 logits went from 84 to
+// 65 us and the distillation loss from 438 to 163.
 struct RowPlan {
   bool vec;
   int lpr;
