@@ -450,7 +450,8 @@ moe_status moe_router_backward(const void* logits, moe_dtype logits_dtype, const
  *   - A backward writes dlogits [T,E] = base + gradient in the logits dtype,
  *     added in FP32 and rounded once.  base [T,E] (logits dtype) may be NULL
  *     (no addend) or dlogits itself, so that the gradients of the routing
- *     weights and of several losses add up in one buffer.
+ *     weights and of several losses add up in one buffer.  Otherwise dlogits
+ *     overlaps neither logits nor base (MOE_ERR_INVALID_ARG).
  *   - A backward takes what its forward wrote: row_stats as it is, and tokens
  *     and counts as integers that the caller may first add up over the parts
  *     of a larger batch.

@@ -189,6 +189,18 @@ def test_distill_loss_backward_refusals(lib, kw, want):
     assert _distill_bwd(lib, **kw) == want, lib.moe_last_error().decode()
 
 
+FAR = ctypes.c_void_p(0x40000)  # 8 x 8 BF16 elements are 128 bytes
+
+
+@pytest.mark.parametrize("kw", [
+    dict(out=FAKE), dict(out=ctypes.c_void_p(FAKE.value + 126)), dict(out=ctypes.c_void_p(FAKE.value - 126)),
+    dict(out=FAR, base=ctypes.c_void_p(FAR.value + 16)), dict(out=FAR, base=ctypes.c_void_p(FAR.value - 126))])
+def test_backward_refuses_overlapping_gradients(lib, kw):
+    for call in (_balance_bwd, _distill_bwd):
+        assert call(lib, **kw) == INVALID_ARG
+        assert b"overlap" in lib.moe_last_error()
+
+
 def test_empty_backward_and_targets_are_noops(lib):
     assert _balance_bwd(lib, logits=None, stats=None, counts=None, tokens=None, dloss=None, out=None, T=0) == OK
     assert _distill_bwd(lib, logits=None, idx=None, tl=None, stats=None, tokens=None, dloss=None, out=None, T=0) == OK

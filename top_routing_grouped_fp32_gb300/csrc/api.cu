@@ -953,6 +953,18 @@ moe_status check_list(int64_t T, int64_t E, int32_t m, float temperature) {
 bool aligned4(const void* p) { return reinterpret_cast<uintptr_t>(p) % 4 == 0; }
 bool aligned_to(const void* p, moe_dtype d) { return reinterpret_cast<uintptr_t>(p) % dtype_size(d) == 0; }
 
+// The gradient's rows are written while others' logits and base are still read.
+moe_status check_gradient(const void* logits, const void* base, const void* dlogits, int64_t n, moe_dtype d) {
+  auto overlap = [&](const void* p) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(dlogits);
+    return (a > b ? a - b : b - a) < (uintptr_t)n * dtype_size(d);
+  };
+  if (overlap(logits)) return fail(MOE_ERR_INVALID_ARG, "dlogits must not overlap logits");
+  if (base && base != dlogits && overlap(base))
+    return fail(MOE_ERR_INVALID_ARG, "base must be dlogits itself or not overlap it");
+  return MOE_OK;
+}
+
 }  // namespace
 
 size_t moe_balance_loss_workspace_size(int64_t T, int64_t E, int64_t num_seqs) {
@@ -1001,6 +1013,7 @@ moe_status moe_balance_loss_backward(const void* logits, moe_dtype ldt, const fl
   if (!aligned_to(logits, ldt) || !aligned_to(base, ldt) || !aligned_to(dlogits, ldt) || !aligned4(counts) ||
       !aligned4(tokens) || !aligned4(dloss) || !aligned4(dz_loss) || reinterpret_cast<uintptr_t>(row_stats) % 8 != 0)
     return fail(MOE_ERR_INVALID_ARG, "misaligned pointer (elements; row_stats 8 bytes)");
+  if ((st = check_gradient(logits, base, dlogits, T * E, ldt)) != MOE_OK) return st;
   moe::BalanceBwdArgs b{logits, ldt, row_stats, counts, tokens, seq_offsets, T, (int)E, top_k, num_seqs,
                         scoring == 1, dloss, dz_loss, base, dlogits};
   MOE_TRY_CUDA(moe::launch_balance_loss_backward(b, stream), "balance loss backward kernel launch");
@@ -1071,6 +1084,7 @@ moe_status moe_distill_loss_backward(const void* logits, moe_dtype ldt, const ui
       !aligned_to(dlogits, ldt) || !aligned4(teacher_idx) || !aligned4(row_stats) || !aligned4(tokens) ||
       !aligned4(dloss))
     return fail(MOE_ERR_INVALID_ARG, "misaligned pointer (elements)");
+  if ((st = check_gradient(logits, base, dlogits, T * E, ldt)) != MOE_OK) return st;
   moe::DistillBwdArgs d{logits, ldt, teacher_idx, teacher_logits, tdt, row_stats, tokens, seq_offsets, T,
                         (int)E, top_m, num_seqs, temperature, dloss, base, dlogits};
   MOE_TRY_CUDA(moe::launch_distill_loss_backward(d, stream), "distillation loss backward kernel launch");

@@ -81,7 +81,7 @@ class _Checked:
     def __setattr__(self, name, value):
         self.__dict__[name] = value
         if name != "workspace":
-            self.__dict__["_checked"] = None
+            self.__dict__["_checked"] = self.__dict__["_elements"] = None
 
     def _pointers(self, device, *sizes):
         """Data pointers of _tensors(*sizes) in their order."""
