@@ -51,11 +51,19 @@ def _scoring(name: str) -> int:
 
 
 def _rows_of(logits: torch.Tensor, what: str):
-    if logits.dim() != 2:
-        raise MoeError(2, f"{what} must have rank two (got {logits.dim()})")
+    shape = logits.shape
+    if len(shape) != 2:
+        raise MoeError(2, f"{what} must have rank two (got {len(shape)})")
     if not logits.is_cuda:
         raise ValueError(f"{what}: expected a CUDA tensor")
-    return logits.shape
+    return shape
+
+
+def _start(logits: torch.Tensor, what: str):
+    """Data pointer of the tensor that the others are checked against."""
+    if not logits.is_contiguous():
+        raise ValueError(f"{what}: expected a contiguous tensor")
+    return logits.data_ptr()
 
 
 def _p(t, what: str, dtypes, shape, device):
@@ -74,33 +82,38 @@ def _p(t, what: str, dtypes, shape, device):
 
 
 class _Checked:
-    """Tensors that a call writes or hands on, checked once for their sizes and
-    again whenever one of them is replaced; a training step passes them call
-    after call.  Pointers are read anew each time."""
+    """Tensors that a call writes or hands on; a training step passes them call
+    after call.  What was checked of each is remembered, and each call compares
+    it with what the tensor is then (its memory can be exchanged behind it, by
+    ``.data``, ``set_`` or an in-place transpose): a difference is checked anew."""
 
     def __setattr__(self, name, value):
         self.__dict__[name] = value
         if name != "workspace":
-            self.__dict__["_checked"] = self.__dict__["_elements"] = None
+            self.__dict__["_checked"] = None
 
     def _pointers(self, device, *sizes):
         """Data pointers of _tensors(*sizes) in their order."""
         d = self.__dict__
-        if d.get("_checked") != (device, sizes):
-            named = [(n, dt, shape) for n, dt, shape in self._tensors(*sizes) if d[n] is not None]
-            for n, dt, shape in named:
-                _p(d[n], n, dt, shape, device)
-            d["_elements"] = [(d[n], d[n].numel()) if d[n] is not None else None
-                              for n, _, _ in self._tensors(*sizes)]
-            d["_checked"] = (device, sizes)
-        out = []
-        for e in d["_elements"]:
-            if e is None:
-                out.append(None)
-            elif e[0].numel() != e[1]:
-                raise MoeError(2, "a tensor of the results was resized")
+        known = d.get("_checked")
+        if known is not None and known[0] == sizes and known[1] == device:
+            out = []
+            for t, dtype, shape, index in known[2]:
+                if t is None:
+                    out.append(None)
+                elif (t.dtype is dtype and t.shape == shape and t.get_device() == index
+                        and t.is_contiguous()):
+                    out.append(t.data_ptr())
+                else:
+                    break
             else:
-                out.append(e[0].data_ptr())
+                return out
+        d["_checked"] = None
+        named = self._tensors(*sizes)
+        out = [_p(d[n], n, dtypes, shape, device) for n, dtypes, shape in named]
+        tensors = [d[n] for n, _, _ in named]
+        d["_checked"] = (sizes, device, [(None,) * 4 if t is None else (t, t.dtype, t.shape, t.get_device())
+                                         for t in tensors])
         return out
 
 
@@ -124,12 +137,14 @@ def _on(device: torch.device, stream):
         if stream.device != device:
             raise ValueError(f"stream is on {stream.device}, the logits are on {device}")
         return torch.cuda.stream(stream)
-    if torch.cuda.current_device() != device.index:
+    if _current_device() != device.index:
         return torch.cuda.device(device)
     return _NOTHING
 
 
-# the current stream's handle without a Stream object around it, where torch offers it
+# the current device, and the current stream's handle without a Stream object around
+# it, where torch offers them (CUDA is initialised: the logits are on a device)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 _current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
@@ -200,7 +215,7 @@ def moe_balance_loss(logits: torch.Tensor, idx: torch.Tensor, scoring: str = "so
     if idx.dim() != 2:
         raise MoeError(2, "idx must be [T, top_k]")
     k, S, dev = idx.shape[1], _num_seqs(seq_offsets), logits.device
-    args = (_p(logits, "logits", (logits.dtype,), (T, E), dev), code, _p(idx, "idx", _I32, (T, k), dev),
+    args = (_start(logits, "logits"), code, _p(idx, "idx", _I32, (T, k), dev),
             _p(token_mask, "token_mask", _MASK, (T,), dev), _p(seq_offsets, "seq_offsets", _I32, (S + 1,), dev),
             T, E, k, S, sc)
     with _on(dev, stream):
@@ -210,7 +225,7 @@ def moe_balance_loss(logits: torch.Tensor, idx: torch.Tensor, scoring: str = "so
             raise MoeError(1, "out was made with another z_loss")
         if workspace is None:
             workspace = moe_balance_loss_workspace(T, E, S, dev)
-        out.workspace = workspace
+        out.__dict__["workspace"] = workspace
         ws, nbytes = _ws(workspace, dev)
         _check(lib.moe_balance_loss(*args, *out._pointers(dev, T, E, S), ws, nbytes, _raw_stream(dev, stream)))
     return out
@@ -228,7 +243,7 @@ def moe_balance_loss_backward(logits: torch.Tensor, forward: BalanceLoss, top_k:
     code, sc = _code(logits, "logits"), _scoring(scoring)
     S, dev, dt = _num_seqs(seq_offsets), logits.device, (logits.dtype,)
     _, _, _, counts, tokens, row_stats = forward._pointers(dev, T, E, S)
-    args = (_p(logits, "logits", dt, (T, E), dev), code, row_stats, counts, tokens,
+    args = (_start(logits, "logits"), code, row_stats, counts, tokens,
             _p(seq_offsets, "seq_offsets", _I32, (S + 1,), dev), T, E, top_k, S, sc,
             _p(dloss, "dloss", _F32, (S,), dev), _p(dz_loss, "dz_loss", _F32, (S,), dev),
             _p(base, "base", dt, (T, E), dev))
@@ -274,7 +289,7 @@ def moe_distill_targets(teacher_logits: torch.Tensor, top_m: int, temperature: f
             raise MoeError(1, "out has no rest")
         if out.logits.dtype != dt:
             raise MoeError(3, f"out.logits dtype {out.logits.dtype} is not the teacher logits' {dt}")
-        _check(lib.moe_distill_targets(_p(teacher_logits, "teacher_logits", (dt,), (T, E), dev), code, T, E, top_m,
+        _check(lib.moe_distill_targets(_start(teacher_logits, "teacher_logits"), code, T, E, top_m,
                                        temperature, *out._pointers(dev, T, top_m), _raw_stream(dev, stream)))
     return out
 
@@ -321,7 +336,7 @@ def moe_distill_loss(logits: torch.Tensor, targets: DistillTargets, temperature:
     T, E = _rows_of(logits, "logits")
     code, S, dev = _code(logits, "logits"), _num_seqs(seq_offsets), logits.device
     m, lists, rest = _list_args(targets, T, dev)
-    args = (_p(logits, "logits", (logits.dtype,), (T, E), dev), code, *lists, rest,
+    args = (_start(logits, "logits"), code, *lists, rest,
             _p(token_mask, "token_mask", _MASK, (T,), dev),
             _p(seq_offsets, "seq_offsets", _I32, (S + 1,), dev), T, E, m, S, temperature)
     with _on(dev, stream):
@@ -329,7 +344,7 @@ def moe_distill_loss(logits: torch.Tensor, targets: DistillTargets, temperature:
             out = DistillLoss.empty(T, S, dev)
         if workspace is None:
             workspace = moe_distill_loss_workspace(T, S, dev)
-        out.workspace = workspace
+        out.__dict__["workspace"] = workspace
         ws, nbytes = _ws(workspace, dev)
         _check(lib.moe_distill_loss(*args, *out._pointers(dev, T, S), ws, nbytes, _raw_stream(dev, stream)))
     return out
@@ -346,7 +361,7 @@ def moe_distill_loss_backward(logits: torch.Tensor, targets: DistillTargets, for
     code, S, dev, dt = _code(logits, "logits"), _num_seqs(seq_offsets), logits.device, (logits.dtype,)
     m, lists, _ = _list_args(targets, T, dev)
     _, tokens, _, row_stats = forward._pointers(dev, T, S)
-    args = (_p(logits, "logits", dt, (T, E), dev), code, *lists, row_stats, tokens,
+    args = (_start(logits, "logits"), code, *lists, row_stats, tokens,
             _p(seq_offsets, "seq_offsets", _I32, (S + 1,), dev), T, E, m, S, temperature,
             _p(dloss, "dloss", _F32, (S,), dev), _p(base, "base", dt, (T, E), dev))
     with _on(dev, stream):
