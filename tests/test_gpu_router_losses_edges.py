@@ -3,6 +3,8 @@ masks of the main tests; tolerances as derived there."""
 import pytest
 import torch
 
+from test_gpu_router_losses import DT, _bits, _logits
+
 pytestmark = pytest.mark.gpu
 
 
@@ -27,3 +29,35 @@ def test_results_whose_memory_was_exchanged_are_refused(cuda_lib):
         cuda_lib.moe_distill_loss(l, tg, out=dis)
     with pytest.raises(ValueError):
         cuda_lib.moe_distill_loss_backward(l, tg, dis, one)
+
+
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("T,E,m", [(3000, 64, 6), (2000, 101, 40), (5000, 100, 7), (700, 999, 5)])
+def test_gradient_in_place_is_the_one_beside_it(cuda_lib, T, E, m, dt):
+    """A chain of gradients added in one buffer, launched back to back, against
+    the same chain through buffers of its own: to the bit.  Rows of 400 bytes and
+    odd ones share their lines with other warps' and blocks' rows."""
+    g = torch.Generator().manual_seed(T + E)
+    l = _logits(T, E, dt, g)
+    far = torch.arange(0, T, 7)  # rows whose list holds all but exp(-200) of the student's mass
+    teacher = l.clone()
+    teacher[far, m:], l[far, m:] = -50.0, -200.0
+    l, teacher = l.cuda(), teacher.cuda()
+    idx, _ = cuda_lib.moe_route(l, min(m, 8), True)
+    off = torch.tensor([0, T // 3, T // 3, T - 17], dtype=torch.int32, device="cuda")
+    one = torch.linspace(0.5, 1.5, 3, device="cuda")
+    bal = cuda_lib.moe_balance_loss(l, idx, seq_offsets=off, z_loss=True)
+    tg = cuda_lib.moe_distill_targets(teacher, m)
+    dis = cuda_lib.moe_distill_loss(l, tg, seq_offsets=off)
+    base = (1e-3 * torch.randn((T, E), generator=g)).to(DT[dt]).cuda()
+    there, kept = base.clone(), base.clone()
+    for _ in range(4):
+        out = cuda_lib.moe_balance_loss_backward(l, bal, min(m, 8), one, seq_offsets=off, dz_loss=one, base=kept)
+        kept = cuda_lib.moe_distill_loss_backward(l, tg, dis, one, seq_offsets=off, base=out)
+    for _ in range(4):
+        cuda_lib.moe_balance_loss_backward(l, bal, min(m, 8), one, seq_offsets=off, dz_loss=one, base=there,
+                                           dlogits=there)
+        cuda_lib.moe_distill_loss_backward(l, tg, dis, one, seq_offsets=off, base=there, dlogits=there)
+    assert torch.equal(_bits(there), _bits(kept))
+    assert torch.equal(_bits(there[T - 17:]), _bits(base[T - 17:])) and torch.isfinite(there.float()).all()
+    assert bool((dis.row_stats[4][far[far < T - 17].cuda()] < 0).all())  # they took the branch of their own

@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, VEC, NV>(kListBlock
         for (int n = 0; n < N; ++n) d[n] = 0.f;
       }
       const int64_t at = (t0 + L.grp) * a.E;
-      const T* const base = static_cast<const T*>(a.base);
+      const T* const base = static_cast<const T*>(a.base);  // may be what this kernel writes: plain loads
       if (base) {  // into the logits' registers and their place
         cur.load(base + at + L.sub * VEC, rows.room, L.lpr, in);
 #pragma unroll
@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, VEC, NV>(kListBlock
         for (int el = L.sub; el < a.E; el += L.lpr) {
           // nothing outside but -inf: no share to give
           float g = mo == -INFINITY ? 0.f : c * ratio / so * exp2_fast((to_f32<T>(__ldg(row + el)) - mo) * a.c);
-          if (base) g += to_f32<T>(__ldg(base + at + el));
+          if (base) g += to_f32<T>(base[at + el]);
           rows.cell(el) = from_f32<T>(g);  // the list's are overwritten below
         }
         __syncwarp(L.mask());
@@ -185,7 +185,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, VEC, NV>(kListBlock
           const uint32_t b = list.bits(t * a.m + j), ee = list.expert(t * a.m + j);
           if (b == list.none() || ee >= (uint32_t)a.E) continue;
           float g = ex.at(to_f32<T>(__ldg(row + ee))) * ps - exp2_fast((list.value(b) - mt) * a.c) * qs;
-          if (base) g += to_f32<T>(__ldg(base + at + ee));
+          if (base) g += to_f32<T>(base[at + ee]);
           rows.cell((int)ee) = from_f32<T>(g);
         }
       __syncwarp();

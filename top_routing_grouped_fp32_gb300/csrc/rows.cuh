@@ -153,16 +153,17 @@ struct RowRegs {
   }
   // `row` is the row at this lane's first element, of which `room` = E - sub * VEC
   // lie before the row's end.  Vectors behind it, and rows that are not loaded,
-  // keep what they hold.
+  // keep what they hold.  Plain loads: the kernel may write the row later on, and
+  // the kernel before it may have written it (no data that stays as it is).
   __device__ __forceinline__ void load(const T* row, int room, int lpr, bool ok) {
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       if (!ok || v * lpr * VEC >= room) continue;
       if constexpr (VEC > 1) {
         static_assert(VEC * sizeof(T) == 16, "16-byte vectors");
-        *reinterpret_cast<uint4*>(raw + v * VEC) = __ldg(reinterpret_cast<const uint4*>(row + v * lpr * VEC));
+        *reinterpret_cast<uint4*>(raw + v * VEC) = *reinterpret_cast<const uint4*>(row + v * lpr * VEC);
       } else {
-        raw[v] = __ldg(row + v * lpr);
+        raw[v] = row[v * lpr];
       }
     }
   }
