@@ -3,7 +3,8 @@ masks of the main tests; tolerances as derived there."""
 import pytest
 import torch
 
-from test_gpu_router_losses import DT, _bits, _logits
+import router_loss_reference as ref
+from test_gpu_router_losses import DELTA, DT, F64, RT, _bits, _check, _check_grad, _logits
 
 pytestmark = pytest.mark.gpu
 
@@ -61,3 +62,31 @@ def test_gradient_in_place_is_the_one_beside_it(cuda_lib, T, E, m, dt):
     assert torch.equal(_bits(there), _bits(kept))
     assert torch.equal(_bits(there[T - 17:]), _bits(base[T - 17:])) and torch.isfinite(there.float()).all()
     assert bool((dis.row_stats[4][far[far < T - 17].cuda()] < 0).all())  # they took the branch of their own
+
+
+@pytest.mark.parametrize("tau", [1.0, 0.01])
+@pytest.mark.parametrize("E", [16, 13])
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_distill_rest_far_below_the_row(cuda_lib, dt, E, tau):
+    """A student whose experts outside the list lie ever farther below the row,
+    with a gradient scaled up: q_rest / p_rest alone is up to 1e30, its product
+    with the scale leaves FP32, the gradient does not.  (Exponents up to 110 in
+    base two: half a step of 2^-17 and log2(e)'s own, 2^-24, are 8e-6 relative in
+    a score; the ratio carries as much again: RT = 2e-5 holds.)"""
+    g = torch.Generator().manual_seed(E)
+    levels = torch.tensor([-20.0, -30.0, -40.0, -44.0, -46.0, -50.0, -60.0, -68.0, -75.0, -150.0])
+    T, m = len(levels), 4
+    l = 0.5 * torch.randn((T, E), generator=g)
+    l[:, m:] += levels[:, None]
+    l = (tau * l).to(DT[dt])
+    ti = torch.arange(m).expand(T, m).contiguous()
+    tl = (0.5 * tau * torch.randn((T, m), generator=g)).to(DT[dt])
+    tr = torch.zeros(T)
+    dloss = torch.tensor([1e13])
+    tg = cuda_lib.DistillTargets(ti.int().cuda(), tl.cuda(), tr.cuda())
+    out = cuda_lib.moe_distill_loss(l.cuda(), tg, temperature=tau)
+    _, tokens, row, diff = ref.distill(l.to(F64), ti, tl.to(F64), tr.to(F64), tau)
+    _check(out.row_loss, row, RT * row + DELTA * diff + DELTA ** 2, "row_loss")
+    d = cuda_lib.moe_distill_loss_backward(l.cuda(), tg, out, dloss.cuda(), temperature=tau)
+    grad, size = ref.distill_grad(l.to(F64), ti, tl.to(F64), tr.to(F64), tau, tokens, dloss.to(F64))
+    _check_grad(d, grad, size, dt, "dlogits")
