@@ -1,5 +1,7 @@
 """The router's training losses where they can go wrong beside the sizes and
 masks of the main tests; tolerances as derived there."""
+import math
+
 import pytest
 import torch
 
@@ -90,3 +92,33 @@ def test_distill_rest_far_below_the_row(cuda_lib, dt, E, tau):
     d = cuda_lib.moe_distill_loss_backward(l.cuda(), tg, out, dloss.cuda(), temperature=tau)
     grad, size = ref.distill_grad(l.to(F64), ti, tl.to(F64), tr.to(F64), tau, tokens, dloss.to(F64))
     _check_grad(d, grad, size, dt, "dlogits")
+
+
+@pytest.mark.parametrize("E,m", [(16, 4), (13, 4), (256, 40), (101, 40)])
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+def test_nan_rows_whose_rest_lies_far_below(cuda_lib, dt, E, m):
+    """A row without a value has none at any expert, also where the experts outside
+    its list lie so far below that their gradient is taken by itself."""
+    g = torch.Generator().manual_seed(E)
+    T = 9
+    l = _logits(T, E, dt, g)
+    l[:, m:] = -200.0
+    ti = torch.arange(m).expand(T, m).clone()
+    tl = torch.randn((T, m), generator=g).to(DT[dt])
+    tr = torch.zeros(T)
+    l[1, 1] = math.inf
+    l[2, 0] = math.nan
+    tl[3, 2] = math.nan
+    tl[4, 0] = math.inf
+    tr[5] = math.nan
+    ti[6, 1] = E
+    ti[7, 1] = ti[7, 2]
+    tg = cuda_lib.DistillTargets(ti.int().cuda(), tl.cuda(), tr.cuda())
+    off = torch.arange(T + 1, dtype=torch.int32, device="cuda")
+    out = cuda_lib.moe_distill_loss(l.cuda(), tg, seq_offsets=off)
+    assert torch.isnan(out.row_loss).tolist() == [False] + 7 * [True] + [False]
+    for base in (None, torch.ones((T, E), dtype=DT[dt], device="cuda")):
+        d = cuda_lib.moe_distill_loss_backward(l.cuda(), tg, out, torch.ones(T, device="cuda"), seq_offsets=off,
+                                               base=base)
+        assert torch.isnan(d[1:8]).all()
+        assert torch.isfinite(d[0].float()).all() and torch.isfinite(d[8].float()).all()

@@ -179,7 +179,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, VEC, NV>(kListBlock
         } else {
           kl += p;
         }
-        if (s != s || kept.st != kept.st) kl = NAN;
+        if (s != s || kept.st != kept.st) kl = ratio = NAN;  // (a far rest would leave -q_r)
         const bool ok = kept.s != 0.f;
         a.row_loss[t] = ok ? kl : 0.f;
         a.row_stats[t] = kept.m;
