@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import router_loss_reference as ref
-from test_gpu_router_losses import DELTA, DT, F64, RT, _bits, _check, _check_grad, _logits
+from test_gpu_router_losses import DELTA, DT, F64, RT, _bits, _check, _check_grad, _close, _logits
 
 pytestmark = pytest.mark.gpu
 
@@ -122,3 +122,26 @@ def test_nan_rows_whose_rest_lies_far_below(cuda_lib, dt, E, m):
                                                base=base)
         assert torch.isnan(d[1:8]).all()
         assert torch.isfinite(d[0].float()).all() and torch.isfinite(d[8].float()).all()
+
+
+@pytest.mark.parametrize("E", [5, 8, 41, 64, 101, 256, 1000])
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+def test_sigmoid_scores_far_below_their_row(cuda_lib, dt, E):
+    """Experts that every row puts at -45, -60 and -80: small scores, not none.
+    (Exponents up to 117 in base two: half a step of 2^-17 and log2(e)'s own, 2^-24,
+    are 8e-6 relative in a score, within RT.)"""
+    g = torch.Generator().manual_seed(E)
+    T, k = 75, 3
+    level = torch.tensor([0.0, -45.0, -60.0, -80.0])[torch.arange(E) % 4]
+    l = (0.3 * torch.randn((T, E), generator=g) + level).to(DT[dt])
+    idx = torch.topk(l.float(), k, dim=1).indices
+    out = cuda_lib.moe_balance_loss(l.cuda(), idx.int().cuda(), scoring="sigmoid")
+    want = ref.balance(l.to(F64), idx, "sigmoid")
+    _close(out.mean_scores, want["mean_scores"], what="mean_scores")
+    _close(out.loss, want["loss"], what="loss")
+    _close(out.row_stats, ref.balance_row_stats(l.to(F64), "sigmoid"), what="row_stats")
+    assert bool((out.mean_scores > 0).all())
+    dloss = torch.tensor([float(T * E)])
+    grad, size = ref.balance_grad(l.to(F64), want["counts"], want["tokens"], k, "sigmoid", dloss.to(F64))
+    d = cuda_lib.moe_balance_loss_backward(l.cuda(), out, k, dloss.cuda(), scoring="sigmoid")
+    _check_grad(d, grad, size, dt, "dlogits")
