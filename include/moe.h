@@ -452,8 +452,9 @@ moe_status moe_router_backward(const void* logits, moe_dtype logits_dtype, const
  *     (no addend) or dlogits itself, so that the gradients of the routing
  *     weights and of several losses add up in one buffer.  Otherwise dlogits
  *     overlaps neither logits nor base (MOE_ERR_INVALID_ARG).
- *   - A backward takes what its forward wrote: row_stats as it is, and tokens
- *     and counts as integers that the caller may first add up over the parts
+ *   - A backward takes its forward's arguments (offsets, top_k, scoring, lists,
+ *     temperature) and what it wrote: row_stats as it is, and tokens and counts
+ *     as integers that the caller may first add up over the parts
  *     of a larger batch.
  *   - T == 0 is valid: a forward writes zero losses and counts.
  * ---------------------------------------------------------------------- */
@@ -517,7 +518,8 @@ moe_status moe_distill_targets(const void* teacher_logits, moe_dtype teacher_dty
  * b_e = logits[t,e] / tau:
  *   q = softmax(a_1 .. a_m, a_r),  p = softmax(b),  R = sum_{e not in the list} p_e
  *   KL_t = sum_j q_j log(q_j / p_idx_j) + q_r log(q_r / R)
- * teacher_rest NULL: no rest, q = softmax(a_1 .. a_m).  A list entry of -inf
+ * teacher_rest is a rest at this temperature (another one is another rest);
+ * NULL: no rest, q = softmax(a_1 .. a_m).  A list entry of -inf
  * is absent and its index is not read; a row whose list and rest hold nothing
  * but -inf has no target and does not count.
  *   loss[s] = mean of KL_t over the counted rows, tokens[s] = their number

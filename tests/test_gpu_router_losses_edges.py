@@ -145,3 +145,25 @@ def test_sigmoid_scores_far_below_their_row(cuda_lib, dt, E):
     grad, size = ref.balance_grad(l.to(F64), want["counts"], want["tokens"], k, "sigmoid", dloss.to(F64))
     d = cuda_lib.moe_balance_loss_backward(l.cuda(), out, k, dloss.cuda(), scoring="sigmoid")
     _check_grad(d, grad, size, dt, "dlogits")
+
+
+def test_another_temperature_than_the_rest_s_or_the_forward_s_is_refused(cuda_lib):
+    l = torch.randn((8, 6), device="cuda")
+    one = torch.ones(1, device="cuda")
+    tg = cuda_lib.moe_distill_targets(l, 3, temperature=2.0)
+    assert tg.temperature == 2.0
+    with pytest.raises(cuda_lib.MoeError):
+        cuda_lib.moe_distill_loss(l, tg)
+    dis = cuda_lib.moe_distill_loss(l, tg, temperature=2.0)
+    with pytest.raises(cuda_lib.MoeError):
+        cuda_lib.moe_distill_loss_backward(l, tg, dis, one)
+    cuda_lib.moe_distill_loss_backward(l, tg, dis, one, temperature=2.0)
+    # the results of a call follow the call
+    cuda_lib.moe_distill_targets(l, 3, out=tg)
+    cuda_lib.moe_distill_loss(l, tg, out=dis)
+    cuda_lib.moe_distill_loss_backward(l, tg, dis, one)
+    # a list alone serves every temperature
+    tg.rest = None
+    for tau in (0.5, 3.0):
+        dis = cuda_lib.moe_distill_loss(l, tg, temperature=tau)
+        cuda_lib.moe_distill_loss_backward(l, tg, dis, one, temperature=tau)

@@ -57,3 +57,29 @@ def test_pointers_follow_their_tensors():
     assert rl._list_args(tg, T, CPU)[1][2] == 2
     tg.logits.data = tg.logits.data.half()
     assert rl._list_args(tg, T, CPU)[1][1:] == (tg.logits.data_ptr(), 1)
+
+
+def test_a_rest_knows_its_temperature():
+    tg = rl.DistillTargets.empty(T, M, torch.bfloat16, CPU)
+    assert tg.temperature is None
+    assert rl.DistillTargets(tg.idx, tg.logits, tg.rest, 2.0).temperature == 2.0
+    tg.temperature = 2.0
+    tg.logits = tg.logits.clone()
+    assert tg.temperature == 2.0
+    tg.rest = tg.rest.clone()
+    assert tg.temperature is None
+    dis = rl.DistillLoss.empty(T, S, CPU)
+    dis.temperature = 0.5
+    dis.tokens = dis.tokens.clone()
+    assert dis.temperature == 0.5
+    dis.row_stats = dis.row_stats.clone()
+    assert dis.temperature is None
+
+
+def test_other_temperatures_are_refused():
+    for kept, given in ((None, 2.0), (1, 1.0), (2.0, 2.0), (0.1, float(torch.tensor(0.1)))):  # the same in FP32
+        rl._same_temperature(kept, given, "the forward")
+    for kept, given in ((2.0, 1.0), (1.0, 1.0 + 2.0 ** -22), (1.0, float("nan"))):
+        with pytest.raises(rl.MoeError) as e:
+            rl._same_temperature(kept, given, "the forward")
+        assert e.value.status == 1 and "temperature" in str(e.value)

@@ -22,6 +22,7 @@ earlier call of the same sizes to write into; ``workspace`` a buffer from the
 from __future__ import annotations
 
 import contextlib
+import ctypes
 from dataclasses import dataclass
 
 import torch
@@ -121,6 +122,14 @@ def _ws(t, device):
     if t.device != device or not t.is_contiguous():
         raise ValueError(f"workspace: expected a contiguous tensor on {device}")
     return t.data_ptr(), t.numel() * t.element_size()
+
+
+def _same_temperature(kept, temperature, what: str) -> None:
+    """`kept`: the temperature that `what` was made at (None: not known)."""
+    if kept is None or kept == temperature:
+        return
+    if ctypes.c_float(kept).value != ctypes.c_float(temperature).value:  # what the library gets
+        raise MoeError(1, f"temperature is {temperature}, {what} was made at {kept}")
 
 
 def _num_seqs(seq_offsets) -> int:
@@ -258,10 +267,18 @@ def moe_balance_loss_backward(logits: torch.Tensor, forward: BalanceLoss, top_k:
 @dataclass
 class DistillTargets(_Checked):
     """A teacher's top logits: what moe_distill_targets gives and the
-    distillation loss takes.  ``rest`` may be None: no mass outside the list."""
+    distillation loss takes.  ``rest`` may be None: no mass outside the list.  A
+    rest belongs to the temperature that it was summed at, which moe_distill_targets
+    notes here (another ``rest`` in its place: not known)."""
     idx: torch.Tensor           # int32 [T,m]
     logits: torch.Tensor        # [T,m] in the teacher's dtype
     rest: torch.Tensor | None   # float32 [T]
+    temperature: float | None = None
+
+    def __setattr__(self, name, value):
+        super().__setattr__(name, value)
+        if name == "rest":
+            self.__dict__["temperature"] = None
 
     @classmethod
     def empty(cls, T: int, top_m: int, dtype, device) -> "DistillTargets":
@@ -291,18 +308,25 @@ def moe_distill_targets(teacher_logits: torch.Tensor, top_m: int, temperature: f
             raise MoeError(3, f"out.logits dtype {out.logits.dtype} is not the teacher logits' {dt}")
         _check(lib.moe_distill_targets(_start(teacher_logits, "teacher_logits"), code, T, E, top_m,
                                        temperature, *out._pointers(dev, T, top_m), _raw_stream(dev, stream)))
+    out.__dict__["temperature"] = temperature
     return out
 
 
 @dataclass
 class DistillLoss(_Checked):
     """What moe_distill_loss gives and moe_distill_loss_backward takes (it reads
-    tokens and row_stats)."""
+    tokens and row_stats, which belong to a temperature as a teacher's rest does)."""
     loss: torch.Tensor       # float32 [S]
     tokens: torch.Tensor     # int32 [S]
     row_loss: torch.Tensor   # float32 [T]
     row_stats: torch.Tensor  # float32 [5,T]
     workspace: torch.Tensor | None = None  # holds the device status word
+    temperature: float | None = None
+
+    def __setattr__(self, name, value):
+        super().__setattr__(name, value)
+        if name == "row_stats":
+            self.__dict__["temperature"] = None
 
     @classmethod
     def empty(cls, T: int, num_seqs: int, device) -> "DistillLoss":
@@ -331,9 +355,12 @@ def moe_distill_loss(logits: torch.Tensor, targets: DistillTargets, temperature:
                      token_mask: torch.Tensor | None = None, seq_offsets: torch.Tensor | None = None,
                      out: DistillLoss | None = None, workspace: torch.Tensor | None = None,
                      stream=None) -> DistillLoss:
-    """Mean KL divergence of student logits [T,E] from a teacher's lists."""
+    """Mean KL divergence of student logits [T,E] from a teacher's lists, at the
+    temperature of their rest."""
     lib = _load()
     T, E = _rows_of(logits, "logits")
+    if targets.rest is not None:
+        _same_temperature(targets.temperature, temperature, "the teacher's rest")
     code, S, dev = _code(logits, "logits"), _num_seqs(seq_offsets), logits.device
     m, lists, rest = _list_args(targets, T, dev)
     args = (_start(logits, "logits"), code, *lists, rest,
@@ -347,6 +374,7 @@ def moe_distill_loss(logits: torch.Tensor, targets: DistillTargets, temperature:
         out.__dict__["workspace"] = workspace
         ws, nbytes = _ws(workspace, dev)
         _check(lib.moe_distill_loss(*args, *out._pointers(dev, T, S), ws, nbytes, _raw_stream(dev, stream)))
+    out.__dict__["temperature"] = temperature
     return out
 
 
@@ -354,10 +382,11 @@ def moe_distill_loss_backward(logits: torch.Tensor, targets: DistillTargets, for
                               dloss: torch.Tensor, temperature: float = 1.0,
                               seq_offsets: torch.Tensor | None = None, base: torch.Tensor | None = None,
                               dlogits: torch.Tensor | None = None, stream=None) -> torch.Tensor:
-    """dlogits [T,E] = base + gradient of sum(dloss * loss), dloss float32 [S].
-    ``dlogits`` is written if given (it may be ``base``)."""
+    """dlogits [T,E] = base + gradient of sum(dloss * loss), dloss float32 [S], at
+    the forward's temperature.  ``dlogits`` is written if given (it may be ``base``)."""
     lib = _load()
     T, E = _rows_of(logits, "logits")
+    _same_temperature(forward.temperature, temperature, "the forward")
     code, S, dev, dt = _code(logits, "logits"), _num_seqs(seq_offsets), logits.device, (logits.dtype,)
     m, lists, _ = _list_args(targets, T, dev)
     _, tokens, _, row_stats = forward._pointers(dev, T, S)
