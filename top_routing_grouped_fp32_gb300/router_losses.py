@@ -35,6 +35,10 @@ _SCORING = {"softmax": 0, "sigmoid": 1}
 _F32, _I32 = (torch.float32,), (torch.int32,)
 _MASK = (torch.bool, torch.uint8)
 _NOTHING = contextlib.nullcontext()
+# what the backwards read of a forward's results
+_BALANCE_READS = ("counts", "tokens", "row_stats")
+_DISTILL_READS = ("tokens", "row_stats")
+_LIST_READS = ("idx", "logits")
 
 
 def _code(t: torch.Tensor, what: str) -> int:
@@ -52,19 +56,17 @@ def _scoring(name: str) -> int:
 
 
 def _rows_of(logits: torch.Tensor, what: str):
+    """T, E, type code, data pointer and device of the rows of a call, which its
+    other tensors are checked against."""
     shape = logits.shape
     if len(shape) != 2:
         raise MoeError(2, f"{what} must have rank two (got {len(shape)})")
     if not logits.is_cuda:
         raise ValueError(f"{what}: expected a CUDA tensor")
-    return shape
-
-
-def _start(logits: torch.Tensor, what: str):
-    """Data pointer of the tensor that the others are checked against."""
+    code = _code(logits, what)
     if not logits.is_contiguous():
         raise ValueError(f"{what}: expected a contiguous tensor")
-    return logits.data_ptr()
+    return (*shape, code, logits.data_ptr(), logits.device)
 
 
 def _p(t, what: str, dtypes, shape, device):
@@ -91,12 +93,12 @@ class _Checked:
     def __setattr__(self, name, value):
         self.__dict__[name] = value
         if name != "workspace":
-            self.__dict__["_checked"] = None
+            self.__dict__["_checked"] = {}
 
-    def _pointers(self, device, *sizes):
-        """Data pointers of _tensors(*sizes) in their order."""
+    def _pointers(self, device, *sizes, of=None):
+        """Data pointers of _tensors(*sizes) in their order (of those named in `of`)."""
         d = self.__dict__
-        known = d.get("_checked")
+        known = d["_checked"].get(of)
         if known is not None and known[0] == sizes and known[1] == device:
             out = []
             for t, dtype, shape, index in known[2]:
@@ -109,26 +111,23 @@ class _Checked:
                     break
             else:
                 return out
-        d["_checked"] = None
-        named = self._tensors(*sizes)
+        named = [x for x in self._tensors(*sizes) if of is None or x[0] in of]
         out = [_p(d[n], n, dtypes, shape, device) for n, dtypes, shape in named]
         tensors = [d[n] for n, _, _ in named]
-        d["_checked"] = (sizes, device, [(None,) * 4 if t is None else (t, t.dtype, t.shape, t.get_device())
-                                         for t in tensors])
+        d["_checked"][of] = (sizes, device, [(None,) * 4 if t is None else (t, t.dtype, t.shape, t.get_device())
+                                             for t in tensors])
         return out
 
 
 def _ws(t, device):
     if t.device != device or not t.is_contiguous():
         raise ValueError(f"workspace: expected a contiguous tensor on {device}")
-    return t.data_ptr(), t.numel() * t.element_size()
+    return t.data_ptr(), t.nbytes
 
 
 def _same_temperature(kept, temperature, what: str) -> None:
     """`kept`: the temperature that `what` was made at (None: not known)."""
-    if kept is None or kept == temperature:
-        return
-    if ctypes.c_float(kept).value != ctypes.c_float(temperature).value:  # what the library gets
+    if kept is not None and ctypes.c_float(kept).value != ctypes.c_float(temperature).value:  # what the library gets
         raise MoeError(1, f"temperature is {temperature}, {what} was made at {kept}")
 
 
@@ -140,29 +139,22 @@ def _num_seqs(seq_offsets) -> int:
     return seq_offsets.shape[0] - 1
 
 
-def _on(device: torch.device, stream):
-    """Context in which `device` and `stream` are current."""
-    if stream is not None:
-        if stream.device != device:
-            raise ValueError(f"stream is on {stream.device}, the logits are on {device}")
-        return torch.cuda.stream(stream)
-    if _current_device() != device.index:
-        return torch.cuda.device(device)
-    return _NOTHING
-
-
 # the current device, and the current stream's handle without a Stream object around
 # it, where torch offers them (CUDA is initialised: the logits are on a device)
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
-_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                              lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def _raw_stream(device, stream) -> int:
+def _on(device: torch.device, stream):
+    """A context in which `device` and `stream` (None: the device's current one)
+    are current, and the stream's handle."""
     if stream is not None:
-        return stream.cuda_stream
-    if _current_raw_stream is not None:
-        return _current_raw_stream(device.index)
-    return torch.cuda.current_stream(device).cuda_stream
+        if stream.device != device:
+            raise ValueError(f"stream is on {stream.device}, the logits are on {device}")
+        return torch.cuda.stream(stream), stream.cuda_stream
+    index = device.index
+    return _NOTHING if _current_device() == index else torch.cuda.device(device), _current_raw_stream(index)
 
 
 _lib_handle = None
@@ -219,15 +211,16 @@ def moe_balance_loss(logits: torch.Tensor, idx: torch.Tensor, scoring: str = "so
     """Balance loss, per-expert counts, mean scores and (``z_loss``) the z-loss
     of router logits [T,E] and their routed experts idx [T,k] (int32)."""
     lib = _load()
-    T, E = _rows_of(logits, "logits")
-    code, sc = _code(logits, "logits"), _scoring(scoring)
+    T, E, code, rows, dev = _rows_of(logits, "logits")
+    sc = _scoring(scoring)
     if idx.dim() != 2:
         raise MoeError(2, "idx must be [T, top_k]")
-    k, S, dev = idx.shape[1], _num_seqs(seq_offsets), logits.device
-    args = (_start(logits, "logits"), code, _p(idx, "idx", _I32, (T, k), dev),
+    k, S = idx.shape[1], _num_seqs(seq_offsets)
+    args = (rows, code, _p(idx, "idx", _I32, (T, k), dev),
             _p(token_mask, "token_mask", _MASK, (T,), dev), _p(seq_offsets, "seq_offsets", _I32, (S + 1,), dev),
             T, E, k, S, sc)
-    with _on(dev, stream):
+    current, raw = _on(dev, stream)
+    with current:
         if out is None:
             out = BalanceLoss.empty(T, E, S, dev, z_loss)
         elif (out.z_loss is not None) != z_loss:
@@ -236,7 +229,7 @@ def moe_balance_loss(logits: torch.Tensor, idx: torch.Tensor, scoring: str = "so
             workspace = moe_balance_loss_workspace(T, E, S, dev)
         out.__dict__["workspace"] = workspace
         ws, nbytes = _ws(workspace, dev)
-        _check(lib.moe_balance_loss(*args, *out._pointers(dev, T, E, S), ws, nbytes, _raw_stream(dev, stream)))
+        _check(lib.moe_balance_loss(*args, *out._pointers(dev, T, E, S), ws, nbytes, raw))
     return out
 
 
@@ -248,19 +241,19 @@ def moe_balance_loss_backward(logits: torch.Tensor, forward: BalanceLoss, top_k:
     z_loss)), dloss and dz_loss float32 [S].  ``dlogits`` is written if given
     (it may be ``base``)."""
     lib = _load()
-    T, E = _rows_of(logits, "logits")
-    code, sc = _code(logits, "logits"), _scoring(scoring)
-    S, dev, dt = _num_seqs(seq_offsets), logits.device, (logits.dtype,)
-    _, _, _, counts, tokens, row_stats = forward._pointers(dev, T, E, S)
-    args = (_start(logits, "logits"), code, row_stats, counts, tokens,
+    T, E, code, rows, dev = _rows_of(logits, "logits")
+    sc, S, dt = _scoring(scoring), _num_seqs(seq_offsets), (logits.dtype,)
+    counts, tokens, row_stats = forward._pointers(dev, T, E, S, of=_BALANCE_READS)
+    args = (rows, code, row_stats, counts, tokens,
             _p(seq_offsets, "seq_offsets", _I32, (S + 1,), dev), T, E, top_k, S, sc,
             _p(dloss, "dloss", _F32, (S,), dev), _p(dz_loss, "dz_loss", _F32, (S,), dev),
             _p(base, "base", dt, (T, E), dev))
-    with _on(dev, stream):
+    current, raw = _on(dev, stream)
+    with current:
         if dlogits is None:
             dlogits = torch.empty((T, E), dtype=logits.dtype, device=dev)
         _check(lib.moe_balance_loss_backward(*args, _p(dlogits, "dlogits", dt, (T, E), dev),
-                                             _raw_stream(dev, stream)))
+                                             raw))
     return dlogits
 
 
@@ -295,19 +288,20 @@ def moe_distill_targets(teacher_logits: torch.Tensor, top_m: int, temperature: f
     """The top_m largest of each row of a teacher's logits [T,E] and the logit of
     all its other experts together at ``temperature``."""
     lib = _load()
-    T, E = _rows_of(teacher_logits, "teacher_logits")
-    code, dev, dt = _code(teacher_logits, "teacher_logits"), teacher_logits.device, teacher_logits.dtype
+    T, E, code, rows, dev = _rows_of(teacher_logits, "teacher_logits")
+    dt = teacher_logits.dtype
     if out is None and not 1 <= top_m <= E:
         raise MoeError(1, f"top_m must satisfy 1 <= top_m <= E (top_m={top_m}, E={E})")
-    with _on(dev, stream):
+    current, raw = _on(dev, stream)
+    with current:
         if out is None:
             out = DistillTargets.empty(T, top_m, dt, dev)
         if out.rest is None:
             raise MoeError(1, "out has no rest")
         if out.logits.dtype != dt:
             raise MoeError(3, f"out.logits dtype {out.logits.dtype} is not the teacher logits' {dt}")
-        _check(lib.moe_distill_targets(_start(teacher_logits, "teacher_logits"), code, T, E, top_m,
-                                       temperature, *out._pointers(dev, T, top_m), _raw_stream(dev, stream)))
+        _check(lib.moe_distill_targets(rows, code, T, E, top_m,
+                                       temperature, *out._pointers(dev, T, top_m), raw))
     out.__dict__["temperature"] = temperature
     return out
 
@@ -339,12 +333,13 @@ class DistillLoss(_Checked):
         return ("loss", _F32, (S,)), ("tokens", _I32, (S,)), ("row_loss", _F32, (T,)), ("row_stats", _F32, (5, T))
 
 
-def _list_args(targets: DistillTargets, T: int, dev):
-    if targets.idx.dim() != 2:
+def _list_args(targets: DistillTargets, T: int, dev, of=None):
+    shape = targets.idx.shape
+    if len(shape) != 2:
         raise MoeError(2, "targets.idx must be [T, top_m]")
-    m = targets.idx.shape[1]
-    idx, logits, rest = targets._pointers(dev, T, m)
-    return m, (idx, logits, _code(targets.logits, "targets.logits")), rest
+    m = shape[1]
+    idx, logits, *rest = targets._pointers(dev, T, m, of=of)
+    return m, (idx, logits, _code(targets.logits, "targets.logits")), *rest
 
 
 def moe_distill_loss_workspace(T: int, num_seqs: int = 1, device="cuda") -> torch.Tensor:
@@ -358,22 +353,23 @@ def moe_distill_loss(logits: torch.Tensor, targets: DistillTargets, temperature:
     """Mean KL divergence of student logits [T,E] from a teacher's lists, at the
     temperature of their rest."""
     lib = _load()
-    T, E = _rows_of(logits, "logits")
-    if targets.rest is not None:
-        _same_temperature(targets.temperature, temperature, "the teacher's rest")
-    code, S, dev = _code(logits, "logits"), _num_seqs(seq_offsets), logits.device
+    T, E, code, rows, dev = _rows_of(logits, "logits")
+    kept = targets.temperature
+    if kept is not None and kept != temperature and targets.rest is not None:
+        _same_temperature(kept, temperature, "the teacher's rest")
+    S = _num_seqs(seq_offsets)
     m, lists, rest = _list_args(targets, T, dev)
-    args = (_start(logits, "logits"), code, *lists, rest,
-            _p(token_mask, "token_mask", _MASK, (T,), dev),
+    args = (rows, code, *lists, rest, _p(token_mask, "token_mask", _MASK, (T,), dev),
             _p(seq_offsets, "seq_offsets", _I32, (S + 1,), dev), T, E, m, S, temperature)
-    with _on(dev, stream):
+    current, raw = _on(dev, stream)
+    with current:
         if out is None:
             out = DistillLoss.empty(T, S, dev)
         if workspace is None:
             workspace = moe_distill_loss_workspace(T, S, dev)
         out.__dict__["workspace"] = workspace
         ws, nbytes = _ws(workspace, dev)
-        _check(lib.moe_distill_loss(*args, *out._pointers(dev, T, S), ws, nbytes, _raw_stream(dev, stream)))
+        _check(lib.moe_distill_loss(*args, *out._pointers(dev, T, S), ws, nbytes, raw))
     out.__dict__["temperature"] = temperature
     return out
 
@@ -385,17 +381,20 @@ def moe_distill_loss_backward(logits: torch.Tensor, targets: DistillTargets, for
     """dlogits [T,E] = base + gradient of sum(dloss * loss), dloss float32 [S], at
     the forward's temperature.  ``dlogits`` is written if given (it may be ``base``)."""
     lib = _load()
-    T, E = _rows_of(logits, "logits")
-    _same_temperature(forward.temperature, temperature, "the forward")
-    code, S, dev, dt = _code(logits, "logits"), _num_seqs(seq_offsets), logits.device, (logits.dtype,)
-    m, lists, _ = _list_args(targets, T, dev)
-    _, tokens, _, row_stats = forward._pointers(dev, T, S)
-    args = (_start(logits, "logits"), code, *lists, row_stats, tokens,
+    T, E, code, rows, dev = _rows_of(logits, "logits")
+    kept = forward.temperature
+    if kept is not None and kept != temperature:
+        _same_temperature(kept, temperature, "the forward")
+    S, dt = _num_seqs(seq_offsets), (logits.dtype,)
+    m, lists = _list_args(targets, T, dev, of=_LIST_READS)
+    tokens, row_stats = forward._pointers(dev, T, S, of=_DISTILL_READS)
+    args = (rows, code, *lists, row_stats, tokens,
             _p(seq_offsets, "seq_offsets", _I32, (S + 1,), dev), T, E, m, S, temperature,
             _p(dloss, "dloss", _F32, (S,), dev), _p(base, "base", dt, (T, E), dev))
-    with _on(dev, stream):
+    current, raw = _on(dev, stream)
+    with current:
         if dlogits is None:
             dlogits = torch.empty((T, E), dtype=logits.dtype, device=dev)
         _check(lib.moe_distill_loss_backward(*args, _p(dlogits, "dlogits", dt, (T, E), dev),
-                                             _raw_stream(dev, stream)))
+                                             raw))
     return dlogits
