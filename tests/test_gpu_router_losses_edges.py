@@ -6,7 +6,8 @@ import pytest
 import torch
 
 import router_loss_reference as ref
-from test_gpu_router_losses import DELTA, DT, F64, RT, _bits, _check, _check_grad, _close, _logits
+from test_gpu_router_losses import (DELTA, DT, F64, RT, _bits, _check, _check_grad, _close, _dev, _lists, _logits,
+                                    _rounded, _step_inputs)
 
 pytestmark = pytest.mark.gpu
 
@@ -167,3 +168,200 @@ def test_another_temperature_than_the_rest_s_or_the_forward_s_is_refused(cuda_li
     for tau in (0.5, 3.0):
         dis = cuda_lib.moe_distill_loss(l, tg, temperature=tau)
         cuda_lib.moe_distill_loss_backward(l, tg, dis, one, temperature=tau)
+
+
+def _shifted(t, by):
+    """A copy that starts `by` elements behind a 16-byte boundary."""
+    buf = torch.empty(t.numel() + by, dtype=t.dtype, device=t.device)[by:].view(t.shape)
+    return buf.copy_(t)
+
+
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("E,k", [(64, 6), (101, 9), (256, 40)])
+@pytest.mark.parametrize("at,to", [(0, 1), (1, 0), (1, 1), (3, 2), (2, 3)])
+def test_gradients_from_and_to_any_element(cuda_lib, at, to, E, k, dt):
+    """Logits and gradient that start on different elements, each loss by itself."""
+    T = 70
+    g = torch.Generator().manual_seed(12 + E)
+    l = _logits(T, E, dt, g)
+    _, ti, tl, tr = _lists(l, k, 1.0, dt, g)
+    idx = torch.topk(l.float(), k, dim=1).indices
+    dl = _shifted(l.cuda(), at)
+    tg = cuda_lib.DistillTargets(_shifted(ti.int().cuda(), 1), _shifted(tl.cuda(), 1), tr.cuda())
+    bal = cuda_lib.moe_balance_loss(dl, _shifted(idx.int().cuda(), 1))
+    dis = cuda_lib.moe_distill_loss(dl, tg)
+    dloss = torch.tensor([float(T)])
+    want = ref.balance(l.to(F64), idx, "softmax")
+    _, tokens, _, _ = ref.distill(l.to(F64), ti, tl.to(F64), tr.to(F64), 1.0)
+    base = torch.randn((T, E), generator=g).to(DT[dt])
+    for grad, size, call in (
+            (*ref.balance_grad(l.to(F64), want["counts"], want["tokens"], k, "softmax", dloss.to(F64)),
+             lambda **kw: cuda_lib.moe_balance_loss_backward(dl, bal, k, dloss.cuda(), **kw)),
+            (*ref.distill_grad(l.to(F64), ti, tl.to(F64), tr.to(F64), 1.0, tokens, dloss.to(F64)),
+             lambda **kw: cuda_lib.moe_distill_loss_backward(dl, tg, dis, dloss.cuda(), **kw))):
+        buf = torch.full((T * E + to + 9,), 7.0, dtype=DT[dt], device="cuda")
+        out = buf[to:to + T * E].view(T, E)
+        _check_grad(call(dlogits=out), grad, size, dt, "dlogits")
+        assert bool((buf[:to] == 7).all()) and bool((buf[to + T * E:] == 7).all())
+        # (the sum with base is rounded once in FP32 and once to its type)
+        total, size = grad + base.to(F64), size + base.to(F64).abs() * 2.0 ** -24 / RT
+        _check_grad(call(dlogits=out, base=_shifted(base.cuda(), at)), total, size, dt, "base + dlogits")
+        buf = torch.full((T * E + to + 9,), 7.0, dtype=DT[dt], device="cuda")
+        out = buf[to:to + T * E].view(T, E).copy_(base)
+        _check_grad(call(dlogits=out, base=out), total, size, dt, "base + dlogits in place")
+        assert bool((buf[:to] == 7).all()) and bool((buf[to + T * E:] == 7).all())
+
+
+@pytest.mark.parametrize("T,E,k", [(64, 4, 2), (3000, 64, 6), (1500, 100, 8), (900, 257, 9)])
+def test_what_each_loss_adds_to_a_step(cuda_lib, T, E, k):
+    """Each gradient of a training step by what it adds to the one before it, with
+    tolerances of its own size: the terms' RT and one rounding of the sum."""
+    l, teacher, _ = _step_inputs(T, E, k, "f32", 4)
+    idx, _ = cuda_lib.moe_route(l, k, True)
+    half = torch.full((1,), 0.5, device="cuda")
+    bal = cuda_lib.moe_balance_loss(l, idx, z_loss=True)
+    tg = cuda_lib.moe_distill_targets(teacher, k)
+    dis = cuda_lib.moe_distill_loss(l, tg)
+    dw = torch.linspace(-1, 1, T * k, device="cuda").view(T, k)
+    d = [cuda_lib.moe_router_backward(l, idx, dw, "softmax", True)]
+    d.append(cuda_lib.moe_balance_loss_backward(l, bal, k, half, dz_loss=0.1 * half, base=d[0]))
+    d.append(cuda_lib.moe_distill_loss_backward(l, tg, dis, half, base=d[1]))
+    d = [x.cpu().to(F64) for x in d]
+    x, ix = l.cpu().to(F64), idx.cpu().long()
+    want = ref.balance(x, ix, "softmax")
+    h = torch.tensor([0.5], dtype=F64)
+    ti, tl, tr = ref.targets(teacher.cpu().to(F64), k, 1.0)
+    # (a rest in FP32, as the loss takes it)
+    parts = (ref.balance_grad(x, want["counts"], want["tokens"], k, "softmax", h, 0.1 * h),
+             ref.distill_grad(x, ti, tl, tr.float().to(F64), 1.0, torch.tensor([T]), h))
+    for (grad, size), before, after in zip(parts, d, d[1:]):
+        tol = RT * size + after.abs() * 2.0 ** -24 + 2.0 ** -126
+        _check(after - before, grad, tol, "what was added")
+        assert float((grad.abs() > 10 * tol).double().mean()) > 0.9  # a gradient that is left out shows
+    p = torch.softmax(x, 1)
+    w = p.gather(1, ix)
+    total = w.sum(1, keepdim=True)
+    w, gw = w / total, dw.cpu().to(F64)
+    mean = (w * gw).sum(1, keepdim=True)
+    task = torch.zeros_like(x).scatter_(1, ix, w * (gw - mean))
+    # the selected experts' terms, and p times their sum for every expert
+    terms = gw.abs() + (w * gw.abs()).sum(1, keepdim=True)
+    size = torch.zeros_like(x).scatter_(1, ix, w * terms) + p * (w * terms).sum(1, keepdim=True)
+    _check(d[0], task, RT * size + 2.0 ** -126, "the routing weights' gradient")
+
+
+ODD = [(40, "f16"), (41, "f32"), (41, "f16"), (41, "bf16"), (257, "f32"), (257, "f16"), (257, "bf16"), (7, "bf16")]
+
+
+@pytest.mark.parametrize("E,dt", ODD)
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+def test_balance_rows_at_the_edge_of_other_layouts(cuda_lib, scoring, E, dt):
+    """Masked experts, far rows, poisoned rows and poison in rows that do not count,
+    beside each other in rows that are no whole vectors."""
+    T, k = 40, 4
+    g = torch.Generator().manual_seed(5 + E)
+    l = _logits(T, E, dt, g)
+    low = torch.finfo(DT[dt]).min
+    l[0, 3:] = -math.inf
+    l[1, ::2] = low
+    l[2, :] = low
+    l[3, :] = -1000.0
+    l[4] = l[4] - 300.0
+    l[5] = l[5] + 300.0
+    l[6, E // 2] = 500.0
+    off = [0, 8, 9, 10, 11, 36]
+    l[8, 3] = math.nan
+    l[9, 3] = math.inf
+    l[10] = -math.inf
+    mask = torch.ones(T, dtype=torch.bool)
+    for i, t in enumerate(range(12, 34, 3)):  # poison on both sides of rows that count
+        l[t], mask[t] = (math.nan, math.inf, -math.inf, low)[i % 4], False
+    l[36:] = math.nan  # behind the last sequence
+    idx = torch.randint(0, E, (T, k), generator=g)
+    idx[12], idx[37] = -1, 2 ** 31 - 1  # not read: their rows do not count
+    z = scoring == "softmax"
+    dl, doff = l.cuda(), _dev(off, torch.int32)
+    out = cuda_lib.moe_balance_loss(dl, idx.int().cuda(), scoring=scoring, token_mask=mask.cuda(), seq_offsets=doff,
+                                    z_loss=z)
+    want = ref.balance(l.to(F64), idx, scoring, mask, off)
+    assert cuda_lib.moe_get_device_status(out.workspace) == 0
+    assert torch.equal(out.counts.cpu().long(), want["counts"])
+    assert torch.equal(out.tokens.cpu().long(), want["tokens"])
+    _close(out.loss, want["loss"], what="loss")
+    _close(out.mean_scores, want["mean_scores"], at=1e-30, what="mean_scores")
+    if z:  # the last sequence's rows are within the bound that `at` stands for; squares of `low` leave FP32
+        _close(out.z_loss[4:], want["z_loss"][4:], at=32 * 2.0 ** -20, what="z_loss")
+        assert torch.isnan(out.z_loss[1:4]).all()
+    dloss = torch.ones(5)
+    grad, size = ref.balance_grad(l.to(F64), want["counts"], want["tokens"], k, scoring, dloss.to(F64), None, mask,
+                                  off)
+    gone = torch.tensor([t for t in range(T) if not mask[t] or t >= 36])
+    base = torch.randn((T, E), generator=g).to(DT[dt])
+    for b in (None, base):
+        d = cuda_lib.moe_balance_loss_backward(dl, out, k, dloss.cuda(), scoring=scoring, seq_offsets=doff,
+                                               base=_dev(b)).cpu()
+        w, s = (grad, size) if b is None else (grad + b.to(F64), size + b.to(F64).abs() * 2.0 ** -24 / RT)
+        _check(d, w, _rounded(torch.nan_to_num(s), torch.nan_to_num(w), dt), "dlogits")
+        assert torch.equal(d[gone], torch.zeros_like(d[gone]) if b is None else b[gone])
+
+
+@pytest.mark.parametrize("m", [5, 40])
+@pytest.mark.parametrize("E,dt", [(48, "f32"), (48, "f16")] + ODD[1:-1])
+def test_distill_rows_at_the_edge_of_other_layouts(cuda_lib, E, dt, m):
+    """The same for the distillation, with lists longer than a row's lanes keep, and
+    rows whose rest lies far below them added to a gradient that is there."""
+    T = 32
+    g = torch.Generator().manual_seed(9 + E + m)
+    l = _logits(T, E, dt, g)
+    _, ti, tl, tr = _lists(l, m, 1.0, dt, g)
+    low = torch.finfo(DT[dt]).min
+    outside = [torch.ones(E, dtype=torch.bool).index_fill(0, ti[t], False).nonzero()[:, 0] for t in range(T)]
+    tl[0] = -math.inf                      # only a rest
+    tr[1] = -math.inf                      # only a list
+    tl[2], tr[2] = -math.inf, -math.inf    # no target
+    l[3, int(ti[3, 0])] = -math.inf        # the teacher gives mass to it: +inf
+    for t in (4, 11):                      # the student's rest underflows
+        l[t, outside[t]] = (-200.0 - torch.arange(len(outside[t])) % 4).to(DT[dt])
+    tl[11, m - 1] = -math.inf              # and an absent entry belongs to the rest
+    l[11, int(ti[11, m - 1])] = -190.0
+    l[5, outside[5][1:]] = -math.inf       # a part of the row only
+    l[6] = low
+    l[7, E // 2:] = low
+    tl[8] = low
+    l[9] = l[9] + 300
+    off = [0, 13, 14, 15, 16, 17, 18, 19, 30]
+    l[13, 3] = math.nan
+    l[14, 3] = math.inf
+    l[15] = -math.inf
+    tl[16, 2] = math.nan
+    tr[17] = math.inf
+    ti[18, 1] = E
+    mask = torch.ones(T, dtype=torch.bool)
+    for i, t in enumerate((10, 20, 23, 26, 29)):
+        l[t], tl[t], ti[t], mask[t] = (math.nan, math.inf, -math.inf)[i % 3], math.nan, -1, False
+    l[30:], tl[30:], tr[30:] = math.nan, math.inf, math.nan
+    tg = cuda_lib.DistillTargets(ti.int().cuda(), tl.cuda(), tr.cuda())
+    doff = _dev(off, torch.int32)
+    out = cuda_lib.moe_distill_loss(l.cuda(), tg, token_mask=mask.cuda(), seq_offsets=doff)
+    row = out.row_loss.cpu()
+    tokens = [11, 1, 1, 1, 1, 1, 1, 7]
+    assert out.tokens.tolist() == tokens
+    assert torch.isnan(row[13:19]).all() and torch.isnan(out.loss[1:7]).all()
+    gone = [t for t in range(T) if t == 2 or not mask[t] or t >= 30]
+    assert not row[gone].any() and not out.row_stats[:, gone].any()
+    assert row[3] == math.inf and out.loss[0] == math.inf
+    assert cuda_lib.moe_get_device_status(out.workspace) == 6  # row 18
+    dloss = torch.ones(8)
+    base = torch.randn((T, E), generator=g).to(DT[dt])
+    for fine, s in (([0, 1, 4, 5, 6, 7, 8, 9, 11, 12], 0), ([19, 21, 22, 24, 25, 27, 28], 7)):
+        x, i, a, r = l.to(F64)[fine], ti[fine], tl.to(F64)[fine], tr.to(F64)[fine]
+        _, _, want, diff = ref.distill(x, i, a, r, 1.0)
+        _check(row[fine], want, RT * want + DELTA * diff + DELTA ** 2, "row_loss")
+        grad, size = ref.distill_grad(x, i, a, r, 1.0, torch.tensor([tokens[s]]), dloss.to(F64))
+        for b in (None, base):
+            d = cuda_lib.moe_distill_loss_backward(l.cuda(), tg, out, dloss.cuda(), seq_offsets=doff,
+                                                   base=_dev(b)).cpu()
+            assert torch.isnan(d[13:19]).all() and torch.isfinite(d[3].float()).all()
+            assert torch.equal(d[gone], torch.zeros_like(d[gone]) if b is None else b[gone])
+            w, sz = (grad, size) if b is None else (grad + b.to(F64)[fine], size + b.to(F64)[fine].abs() * 2.0 ** -24 / RT)
+            _check(d[fine], w, _rounded(sz, w, dt), "dlogits")
