@@ -365,3 +365,61 @@ def test_distill_rows_at_the_edge_of_other_layouts(cuda_lib, E, dt, m):
             assert torch.equal(d[gone], torch.zeros_like(d[gone]) if b is None else b[gone])
             w, sz = (grad, size) if b is None else (grad + b.to(F64)[fine], size + b.to(F64)[fine].abs() * 2.0 ** -24 / RT)
             _check(d[fine], w, _rounded(sz, w, dt), "dlogits")
+
+
+@pytest.mark.parametrize("tau", [1e-3, 1e3])
+@pytest.mark.parametrize("E,m", [(64, 6), (101, 40)])
+def test_temperatures_at_their_limits(cuda_lib, E, m, tau):
+    """Logits of the temperature's size: what is exponentiated is as at 1, and so
+    are its errors (the rest carries tau times its logarithm's)."""
+    T = 200
+    g = torch.Generator().manual_seed(E)
+    l = tau * _logits(T, E, "f32", g)
+    teacher = l + tau * 0.7 * torch.randn((T, E), generator=g)
+    tg = cuda_lib.moe_distill_targets(teacher.cuda(), m, temperature=tau)
+    ti, tl, tr = ref.targets(teacher.to(F64), m, tau)
+    assert torch.equal(tg.idx.cpu().long(), ti)
+    _close(tg.rest, tr, at=tau * DELTA, what="rest")
+    tr = tg.rest.cpu().to(F64)
+    out = cuda_lib.moe_distill_loss(l.cuda(), tg, temperature=tau)
+    loss, tokens, row, diff = ref.distill(l.to(F64), ti, tl, tr, tau)
+    _check(out.row_loss, row, RT * row + DELTA * diff + DELTA ** 2, "row_loss")
+    dloss = torch.tensor([float(T)])
+    grad, size = ref.distill_grad(l.to(F64), ti, tl, tr, tau, tokens, dloss.to(F64))
+    d = cuda_lib.moe_distill_loss_backward(l.cuda(), tg, out, dloss.cuda(), temperature=tau)
+    _check_grad(d, grad, size, "f32", "dlogits")
+
+
+@pytest.mark.parametrize("T,E,k", [(50, 8, 2), (3, 100, 7)])
+def test_more_sequences_than_rows(cuda_lib, T, E, k):
+    """70000 sequences, nearly all of them empty, before, between and behind the rows."""
+    g = torch.Generator().manual_seed(T)
+    l = _logits(T, E, "f32", g)
+    idx = torch.topk(l, k, dim=1).indices
+    _, ti, tl, tr = _lists(l, k, 1.0, "f32", g)
+    S = 70000
+    off = torch.cat([torch.zeros(S // 3, dtype=torch.int64), torch.randint(0, T + 1, (S // 3,), generator=g)])
+    off = torch.cat([off, torch.full((S + 1 - len(off),), T)]).sort().values
+    doff, dl = off.int().cuda(), l.cuda()
+    rows = off[1:] - off[:-1]
+    some = rows.nonzero()[:, 0]
+    where = torch.cat([off[some], off[-1:]]).tolist()  # the sequences that hold rows
+    bal = cuda_lib.moe_balance_loss(dl, idx.int().cuda(), seq_offsets=doff, z_loss=True)
+    tg = cuda_lib.DistillTargets(ti.int().cuda(), tl.cuda(), tr.cuda())
+    dis = cuda_lib.moe_distill_loss(dl, tg, seq_offsets=doff)
+    assert torch.equal(bal.tokens.cpu().long(), rows) and torch.equal(dis.tokens.cpu().long(), rows)
+    empty = (rows == 0).cuda()
+    for t in (bal.loss, bal.z_loss, bal.mean_scores, bal.counts, dis.loss):
+        assert not t[empty].any()
+    want = ref.balance(l.to(F64), idx, "softmax", None, where)
+    _close(bal.loss[some.cuda()], want["loss"], what="loss")
+    loss, tokens, _, diff = ref.distill(l.to(F64), ti, tl.to(F64), tr.to(F64), 1.0, None, where)
+    _check(dis.loss[some.cuda()], loss, RT * loss + DELTA * diff.max() + DELTA ** 2, "distillation loss")
+    dloss = torch.linspace(0.5, 1.5, S)
+    grad, size = ref.balance_grad(l.to(F64), want["counts"], want["tokens"], k, "softmax", dloss[some].to(F64), None,
+                                  None, where)
+    d = cuda_lib.moe_balance_loss_backward(dl, bal, k, dloss.cuda(), seq_offsets=doff)
+    _check_grad(d, grad, size, "f32", "dlogits")
+    grad, size = ref.distill_grad(l.to(F64), ti, tl.to(F64), tr.to(F64), 1.0, tokens, dloss[some].to(F64), None, where)
+    d = cuda_lib.moe_distill_loss_backward(dl, tg, dis, dloss.cuda(), seq_offsets=doff)
+    _check_grad(d, grad, size, "f32", "dlogits")
