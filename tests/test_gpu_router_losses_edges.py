@@ -423,3 +423,72 @@ def test_more_sequences_than_rows(cuda_lib, T, E, k):
     grad, size = ref.distill_grad(l.to(F64), ti, tl.to(F64), tr.to(F64), 1.0, tokens, dloss[some].to(F64), None, where)
     d = cuda_lib.moe_distill_loss_backward(dl, tg, dis, dloss.cuda(), seq_offsets=doff)
     _check_grad(d, grad, size, "f32", "dlogits")
+
+
+@pytest.mark.parametrize("m", [4, 12, 40])
+@pytest.mark.parametrize("E", [48, 41, 256, 257, 1000])
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+def test_targets_at_the_edge_of_other_layouts(cuda_lib, dt, E, m):
+    """Ties, masked rows and rows that are none, between others; results that start
+    on any element."""
+    T = 37
+    g = torch.Generator().manual_seed(E + m)
+    l = (2 * _logits(T, E, "f32", g)).round().div(2).to(DT[dt])  # many ties
+    low = torch.finfo(DT[dt]).min
+    l[0] = -math.inf
+    l[1, 2:] = -math.inf
+    l[2] = low
+    l[3, 1:] = low
+    l[4] = 3.0
+    l[5, ::2] = -math.inf
+    l[6] = l[6] - 300.0
+    l[7, : E // 2], l[7, E // 2:] = 0.0, -0.0
+    broken = [9, 12, 15, 20]
+    l[9, E // 2] = math.nan
+    l[12, E - 1] = math.inf
+    l[15, 0] = math.copysign(math.nan, -1.0)
+    l[20] = math.inf
+    fine = torch.tensor([t for t in range(T) if t not in broken])
+    ti, tl, tr = ref.targets(l.to(F64)[fine], m, 1.0)
+    for by in (0, 1):
+        out = cuda_lib.DistillTargets(_shifted(torch.empty((T, m), dtype=torch.int32, device="cuda"), by),
+                                      _shifted(torch.empty((T, m), dtype=DT[dt], device="cuda"), by),
+                                      _shifted(torch.empty(T, device="cuda"), by))
+        cuda_lib.moe_distill_targets(_shifted(l.cuda(), by), m, out=out)
+        assert torch.equal(out.idx.cpu().long()[fine], ti)
+        assert torch.equal(out.logits.cpu().to(F64)[fine], tl)
+        _close(out.rest.cpu()[fine], tr, at=DELTA, what="rest")
+        for t in broken:
+            assert out.idx[t].tolist() == list(range(m))
+            assert torch.isnan(out.logits[t]).all() and torch.isnan(out.rest[t])
+
+
+def test_two_graphs_that_share_a_workspace(cuda_lib):
+    """Replayed in turn, each gives its own results, and each call its own status."""
+    T, E, k = 3000, 64, 6
+    bal_ws, dis_ws = cuda_lib.moe_balance_loss_workspace(T, E), cuda_lib.moe_distill_loss_workspace(T)
+    graphs, results, wants, inputs = [], [], [], []
+    for seed in (1, 2):
+        l, teacher, _ = _step_inputs(T, E, k, "bf16", seed)
+        idx, _ = cuda_lib.moe_route(l, k, True)
+        if seed == 2:
+            idx[5, 1] = E  # reported by this one alone
+        tg = cuda_lib.moe_distill_targets(teacher, k)
+        call = lambda: (cuda_lib.moe_balance_loss(l, idx, z_loss=True, workspace=bal_ws),
+                        cuda_lib.moe_distill_loss(l, tg, workspace=dis_ws))
+        wants.append([x.clone() for r in call() for x in (r.loss, r.row_stats)])
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            b, d = call()
+        inputs.append((l, idx, tg))  # what a graph reads has to live
+        graphs.append(graph)
+        results.append([b.loss, b.row_stats, d.loss, d.row_stats])
+    for _ in range(3):
+        for graph, result, want, status in zip(graphs, results, wants, (0, 6)):
+            graph.replay()
+            torch.cuda.synchronize()
+            for a, b in zip(result, want):
+                assert torch.equal(_bits(a), _bits(b))
+            assert cuda_lib.moe_get_device_status(bal_ws) == status
+            assert cuda_lib.moe_get_device_status(dis_ws) == 0
