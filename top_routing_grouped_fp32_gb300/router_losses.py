@@ -101,10 +101,10 @@ class _Checked:
         known = d["_checked"].get(of)
         if known is not None and known[0] == sizes and known[1] == device:
             out = []
-            for t, dtype, shape, index in known[2]:
+            for t, dtype, flat, size, index in known[2]:
                 if t is None:
                     out.append(None)
-                elif (t.dtype is dtype and t.shape == shape and t.get_device() == index
+                elif (t.dtype is dtype and (t.nbytes if flat else t.shape) == size and t.get_device() == index
                         and t.is_contiguous()):
                     out.append(t.data_ptr())
                 else:
@@ -113,9 +113,11 @@ class _Checked:
                 return out
         named = [x for x in self._tensors(*sizes) if of is None or x[0] in of]
         out = [_p(d[n], n, dtypes, shape, device) for n, dtypes, shape in named]
-        tensors = [d[n] for n, _, _ in named]
-        d["_checked"][of] = (sizes, device, [(None,) * 4 if t is None else (t, t.dtype, t.shape, t.get_device())
-                                             for t in tensors])
+        # (a vector's bytes in a row are the same vector in every shape)
+        d["_checked"][of] = (sizes, device, [
+            (None,) * 5 if t is None else
+            (t, t.dtype, t.dim() == 1, t.nbytes if t.dim() == 1 else t.shape, t.get_device())
+            for t in (d[n] for n, _, _ in named)])
         return out
 
 
@@ -132,8 +134,6 @@ def _same_temperature(kept, temperature, what: str) -> None:
 
 
 def _num_seqs(seq_offsets) -> int:
-    if seq_offsets is None:
-        return 1
     if seq_offsets.dim() != 1 or seq_offsets.shape[0] < 2:
         raise MoeError(2, "seq_offsets must be [num_seqs + 1] with num_seqs >= 1")
     return seq_offsets.shape[0] - 1
@@ -215,7 +215,7 @@ def moe_balance_loss(logits: torch.Tensor, idx: torch.Tensor, scoring: str = "so
     sc = _scoring(scoring)
     if idx.dim() != 2:
         raise MoeError(2, "idx must be [T, top_k]")
-    k, S = idx.shape[1], _num_seqs(seq_offsets)
+    k, S = idx.shape[1], 1 if seq_offsets is None else _num_seqs(seq_offsets)
     args = (rows, code, _p(idx, "idx", _I32, (T, k), dev),
             _p(token_mask, "token_mask", _MASK, (T,), dev), _p(seq_offsets, "seq_offsets", _I32, (S + 1,), dev),
             T, E, k, S, sc)
@@ -242,7 +242,7 @@ def moe_balance_loss_backward(logits: torch.Tensor, forward: BalanceLoss, top_k:
     (it may be ``base``)."""
     lib = _load()
     T, E, code, rows, dev = _rows_of(logits, "logits")
-    sc, S, dt = _scoring(scoring), _num_seqs(seq_offsets), (logits.dtype,)
+    sc, S, dt = _scoring(scoring), 1 if seq_offsets is None else _num_seqs(seq_offsets), (logits.dtype,)
     counts, tokens, row_stats = forward._pointers(dev, T, E, S, of=_BALANCE_READS)
     args = (rows, code, row_stats, counts, tokens,
             _p(seq_offsets, "seq_offsets", _I32, (S + 1,), dev), T, E, top_k, S, sc,
@@ -357,7 +357,7 @@ def moe_distill_loss(logits: torch.Tensor, targets: DistillTargets, temperature:
     kept = targets.temperature
     if kept is not None and kept != temperature and targets.rest is not None:
         _same_temperature(kept, temperature, "the teacher's rest")
-    S = _num_seqs(seq_offsets)
+    S = 1 if seq_offsets is None else _num_seqs(seq_offsets)
     m, lists, rest = _list_args(targets, T, dev)
     args = (rows, code, *lists, rest, _p(token_mask, "token_mask", _MASK, (T,), dev),
             _p(seq_offsets, "seq_offsets", _I32, (S + 1,), dev), T, E, m, S, temperature)
@@ -385,7 +385,7 @@ def moe_distill_loss_backward(logits: torch.Tensor, targets: DistillTargets, for
     kept = forward.temperature
     if kept is not None and kept != temperature:
         _same_temperature(kept, temperature, "the forward")
-    S, dt = _num_seqs(seq_offsets), (logits.dtype,)
+    S, dt = 1 if seq_offsets is None else _num_seqs(seq_offsets), (logits.dtype,)
     m, lists = _list_args(targets, T, dev, of=_LIST_READS)
     tokens, row_stats = forward._pointers(dev, T, S, of=_DISTILL_READS)
     args = (rows, code, *lists, row_stats, tokens,
