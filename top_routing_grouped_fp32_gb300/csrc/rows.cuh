@@ -125,8 +125,11 @@ struct Lanes {
 };
 
 // Blocks of 256 threads that a SM is to hold, by the bytes of a row that a lane
-// holds (its registers follow them).  Kernels that keep a list's entries as well
-// hold three at most.
+// holds, where a single element counts as two, in FP32 too.  Kernels that keep a
+// list's entries as well hold three at most.  What else a lane holds (scores, sums)
+// is not counted: of the 356 variants of the losses' kernels 107 spill registers, 71 of
+// these among the 182 for single elements, 32 more than 100 bytes (one 832).  The balance loss
+// of 524288 rows takes 95 us for 101 FP32 logits, single elements, and 48 for 100.
 constexpr int blocks_for(int bytes, int most) {
   const int n = bytes <= 16 ? 4 : bytes <= 32 ? 3 : bytes <= 64 ? 2 : 1;
   return n < most ? n : most;
@@ -602,7 +605,8 @@ cudaError_t launch_rows(void (*kernel)(KArgs...), int blocks, int threads, size_
 
 // How a batch of rows is cut over blocks: `chunks` blocks of `rows` rows, whole
 // rounds of a block's warps (`round` rows); one block where it has few rounds to
-// make, since it then needs no second kernel.
+// make, since it then needs no second kernel: the balance loss of 64 rows of 256
+// BF16 logits takes 4.6 us of the GPU, of 1024 rows in 32 blocks 8.6.
 struct Chunks {
   int64_t rows;
   int chunks;
