@@ -526,7 +526,7 @@ moe_status moe_distill_targets(const void* teacher_logits, moe_dtype teacher_dty
  *   row_loss [T]: KL_t (0 for rows that do not count)
  *   row_stats [5,T]: max_e l_te, sum_e exp(b_e - max b), the maximum of the
  *   list and rest, the sum of their exponentials about it, q_r / R (0 without
- *   a rest; -q_r where sum_{e not in the list} exp(b_e - max b) < 1e-20); 0
+ *   a rest; -q_r where sum_{e not in the list} exp(b_e - max b) < 1e-30); 0
  *   for rows that do not count.
  * A counted row with a NaN or +inf on either side, only -inf on the student's,
  * or a listed expert >= E or listed twice gives NaN (the latter two also set

@@ -33,9 +33,7 @@ constexpr int kWarps = kThreads / 32;
 
 // Below this, beside the exponential of the row's maximum, the student's mass outside
 // the list is taken about its own maximum, and -q_r stands in the place of q_r / R.
-// q_r / R is then at most 1e23, which leaves a scaled gradient (times dloss / tau)
-// room in FP32, and the shares that are left have exponents far from FP32's smallest.
-constexpr float kFarBelow = 1e-20f;
+constexpr float kFarBelow = 1e-30f;
 
 // q log(q/p) - q + p from d = log(q/p); its series where the terms nearly cancel
 // (|d| < 1/2: the first term left out is below 2^-24 of the sum).

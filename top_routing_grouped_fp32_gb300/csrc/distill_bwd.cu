@@ -124,7 +124,12 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm<T, VEC, NV>(kListBlock
       }
       float d[N];
       ex.row(cur, d);
-      const float w = ps * (1.f - ratio);
+      float w = ps * (1.f - ratio);
+      if (isinf(w)) {  // q_r / R (1e33 at most) meets the small exponentials before a scaled dloss
+        w = ps;        // (an infinity at a listed expert is overwritten)
+#pragma unroll
+        for (int n = 0; n < N; ++n) d[n] *= 1.f - ratio;
+      }
       pairwise<N>([&](int n) { put(d, n, mul2(pair(d, n), both(w))); }, [&](int n) { d[n] *= w; });
       if (!ok) {
 #pragma unroll
