@@ -58,11 +58,10 @@ FALLBACK_PEAKS = {"hbm_gbs": 6800.0, "bf16_tflops": 1900.0, "bf16_tflops_sustain
 # white space left out) it was taken on; it is reported as null once that
 # code changes.
 GEMM_TRAFFIC = {
-    # ncu --set full, one launch each on the headline workload: gate/up reads
-    # 1.141058 GB and writes 265.725696 MB, down reads 0.646926 GB and writes
-    # 373.762816 MB (ncu's units; the GB figures are rounded to the kilobyte)
-    "finegrained_bf16": {"bytes_per_launch": (1141058000 + 265725696 + 646926000 + 373762816) / 2,
-                         "code_sha256": "e15a00f4548dfbd7a723e0d81565253554c1d21e59cb26ec407440f0a3802ee4"},
+    # one launch each on the headline workload: gate/up reads 1.141139200 GB and
+    # writes 265.018112 MB, down reads 0.646926336 GB and writes 370.292224 MB
+    "finegrained_bf16": {"bytes_per_launch": (1141139200 + 265018112 + 646926336 + 370292224) / 2,
+                         "code_sha256": "d6f7f148123b64e049afe4fe315430a976743e79ac7a56c57570d3b3863b6b55"},
 }
 
 

@@ -555,6 +555,129 @@ moe_status moe_distill_loss_backward(const void* logits, moe_dtype logits_dtype,
                                      float temperature, const float* dloss, const void* base,
                                      void* dlogits, cudaStream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Microscaled (MX) rows.  No counterpart on the pages: the experts' operands
+ * in 4 and 8 bits, for serving (moe_mx4_*) and for the activations that a
+ * training step keeps (moe_experts_*_checkpoint).
+ *
+ * A row of C values is held as blocks of 32 (the last one may be shorter),
+ * each with one scale 2^(b-127), b its byte in scales [R, ceil(C/32)]:
+ *   MOE_MXFP4  e2m1 elements (0, 0.5, 1, 1.5, 2, 3, 4, 6 and negatives), two a
+ *              byte, the first in the low half: values [R, ceil(C/2)]
+ *   MOE_MXFP8  e4m3 elements (three mantissa bits, up to 448): values [R, C]
+ * moe_mx_quantize: with a the largest magnitude of a block, 2^p <= a <
+ * 2^(p+1), the scale is 2^(p-2) (MXFP4) or 2^(p-8) (MXFP8), the next power
+ * from a = 1.75 2^p (1.8125 2^p) on, and at least 2^-127 (b = 0; also where a
+ * = 0).  Elements are x / scale, rounded once to nearest even, saturating.  A
+ * block holding a NaN or an infinity gets b = 255 and elements 0, and reads
+ * back as NaN.  The unused half of an odd row's last byte is 0.
+ * moe_mx_dequantize: out [n, C] = element * scale rounded to out_dtype; row r
+ * is held row r (perm NULL, n = R), or held row perm[r] / top_k (0 where that
+ * is not below R): tokens in dispatch order.  top_k is 1 where perm is NULL.
+ * Any C in [1, 2^20]; rows are dense and may start at any element (16-byte
+ * aligned x, out and values with C a multiple of 32 are the fast case).  R and
+ * n below 2^31; R == 0 or n == 0 is valid and enqueues nothing.
+ * ---------------------------------------------------------------------- */
+typedef enum { MOE_MXFP4 = 0, MOE_MXFP8 = 1 } moe_mx_format;
+
+moe_status moe_mx_quantize(const void* x, moe_dtype x_dtype, int64_t R, int64_t C,
+                           moe_mx_format format, uint8_t* values, uint8_t* scales,
+                           cudaStream_t stream);
+moe_status moe_mx_dequantize(const uint8_t* values, const uint8_t* scales, moe_mx_format format,
+                             int64_t R, int64_t C, const uint32_t* perm, int32_t top_k, int64_t n,
+                             void* out, moe_dtype out_dtype, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * SwiGLU experts on 4-bit operands (beside moe_experts_*): gate and up
+ * [E,I,H], down [E,H,I] as MOE_MXFP4 rows along the last dimension.  With Q4
+ * the rounding of moe_mx_quantize to MOE_MXFP4,
+ *   xq = Q4(x), g = xq . W_gate[e]^T, u = xq . W_up[e]^T (FP32),
+ *   hq = Q4(silu(g) * u), out = hq . W_down[e]^T (FP32, rounded once to dtype).
+ * dtype (F16 or BF16, else MOE_ERR_DTYPE) is that of x and the outputs.  H and
+ * I are multiples of 32 (else MOE_ERR_UNSUPPORTED); other limits as for
+ * moe_experts_create.  Row NaN or infinity makes that row NaN; a weight block
+ * with scale byte 255 makes its output column (gate, up: the rows) NaN.
+ *
+ * The handle does not own the weights: gate, up and down values (16-byte
+ * aligned) must stay alive and unchanged while it is used.  Their scales are
+ * re-ordered once, on `stream`, into the caller's scale_buffer of
+ * moe_mx4_experts_scale_bytes(E, I, H) bytes (256-byte aligned), which must
+ * stay alive too; the given scales are not read after that.  Calls on other
+ * streams must be ordered behind it by the caller.
+ * ---------------------------------------------------------------------- */
+typedef struct moe_mx4_experts* moe_mx4_experts_t;
+size_t moe_mx4_experts_scale_bytes(int64_t E, int64_t I, int64_t H);
+moe_status moe_mx4_experts_create(const uint8_t* gate, const uint8_t* gate_scales,
+                                  const uint8_t* up, const uint8_t* up_scales,
+                                  const uint8_t* down, const uint8_t* down_scales, moe_dtype dtype,
+                                  int64_t E, int64_t I, int64_t H, void* scale_buffer,
+                                  size_t scale_buffer_bytes, cudaStream_t stream,
+                                  moe_mx4_experts_t* out);
+void moe_mx4_experts_destroy(moe_mx4_experts_t experts);
+
+/* Dispatched rows x_disp [N,H] -> expert_out [N,H], as moe_experts_forward
+ * (offsets checked and clamped on the device in the same way; rows outside
+ * the segments are not written).  workspace:
+ * moe_mx4_experts_workspace_size(experts, N) bytes. */
+size_t moe_mx4_experts_workspace_size(moe_mx4_experts_t experts, int64_t N);
+moe_status moe_mx4_experts_forward(moe_mx4_experts_t experts, const void* x_disp, int64_t N,
+                                   const uint32_t* offsets, void* expert_out, void* workspace,
+                                   size_t workspace_bytes, cudaStream_t stream);
+
+/* Fused route -> dispatch -> 4-bit experts -> combine, as moe_forward: a token
+ * is rounded to 4 bits once and goes to its experts in that form; the weighted
+ * slots are FP32 and are added in ascending j.  workspace:
+ * moe_mx4_forward_workspace_size(...) bytes.  The second form routes as
+ * moe_route_sigmoid_grouped (top_k = options->top_k). */
+size_t moe_mx4_forward_workspace_size(moe_mx4_experts_t experts, int64_t T, int32_t top_k,
+                                      moe_dtype logits_dtype);
+moe_status moe_mx4_forward(moe_mx4_experts_t experts, const void* x, const void* logits,
+                           moe_dtype logits_dtype, int64_t T, int32_t top_k, int renormalize,
+                           void* y, void* workspace, size_t workspace_bytes, cudaStream_t stream);
+moe_status moe_mx4_forward_sigmoid_grouped(moe_mx4_experts_t experts, const void* x,
+                                           const void* logits, moe_dtype logits_dtype, int64_t T,
+                                           const float* bias,
+                                           const moe_group_routing_options* options, void* y,
+                                           void* workspace, size_t workspace_bytes,
+                                           cudaStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Training with activations kept in 8 bits (F16/BF16 experts with H and I
+ * multiples of 8; MOE_ERR_UNSUPPORTED otherwise).  What the backward needs of
+ * the forward is held as MOE_MXFP8 rows: the tokens x [T,H] (moe_mx_quantize)
+ * and the two projections g, u [N,I] of the dispatched rows.
+ *
+ * moe_experts_forward_checkpoint: moe_experts_forward (the same expert_out,
+ * the same workspace), which also writes g and u, rounded from FP32, and their
+ * scales [N, ceil(I/32)].  Rows outside the segments are not written.
+ *
+ * moe_experts_backward_checkpoint: with x^, g^, u^ the held values (x^ of the
+ * dispatched row r is token perm[r] / top_k; 0 where that is not below T), s =
+ * sigmoid(g^):
+ *   da = dout W_down, dg = da u^ s (1 + g^ (1 - s)), du = da g^ s, a = g^ s u^,
+ *   dinput = dg W_gate + du W_up, dgate = sum_r dg_r^T x^_r,
+ *   dup = sum_r du_r^T x^_r, ddown = sum_r dout_r^T a_r.
+ * All gradients are in the weights' dtype (dinput [N,H], dgate and dup
+ * [E,I,H], ddown [E,H,I]; experts without rows get zeros).  da and all sums
+ * are FP32; dg, du and a are rounded once to the dtype as operands of the
+ * products, x^ too (its four significant bits fit).  N = T*top_k.  g and u are
+ * not recomputed: six of the eight products of moe_experts_backward are left.
+ * ---------------------------------------------------------------------- */
+moe_status moe_experts_forward_checkpoint(moe_experts_t experts, const void* x_disp, int64_t N,
+                                          const uint32_t* offsets, void* expert_out,
+                                          uint8_t* gate_values, uint8_t* gate_scales,
+                                          uint8_t* up_values, uint8_t* up_scales, void* workspace,
+                                          size_t workspace_bytes, cudaStream_t stream);
+size_t moe_experts_backward_checkpoint_workspace_size(moe_experts_t experts, int64_t N);
+moe_status moe_experts_backward_checkpoint(moe_experts_t experts, const uint8_t* x_values,
+                                           const uint8_t* x_scales, int64_t T, int32_t top_k,
+                                           const uint32_t* perm, const uint32_t* offsets,
+                                           const uint8_t* gate_values, const uint8_t* gate_scales,
+                                           const uint8_t* up_values, const uint8_t* up_scales,
+                                           const void* dout, void* dinput, void* dgate, void* dup,
+                                           void* ddown, void* workspace, size_t workspace_bytes,
+                                           cudaStream_t stream);
+
 /* Diagnostics (no counterpart on the pages): exercises the failure path of
  * the bounded waits inside this library's kernels.  Enqueues one small kernel
  * that waits on a barrier nothing completes; after limit_ms (1..2000) the

@@ -27,6 +27,8 @@ from ._lib import DTYPE_CODES, MoeError  # noqa: F401
 from .router_losses import (BalanceLoss, DistillLoss, DistillTargets, moe_balance_loss,
                             moe_balance_loss_backward, moe_balance_loss_workspace, moe_distill_loss,
                             moe_distill_loss_backward, moe_distill_loss_workspace, moe_distill_targets)
+from . import microscaling as _mx
+from .microscaling import ExpertCheckpoint, Mx4SwiGluExperts, MxRows, moe_mx_dequantize, moe_mx_quantize
 
 _TORCH_CODES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 _CODE_TORCH = {v: k for k, v in _TORCH_CODES.items()}
@@ -37,6 +39,7 @@ __all__ = ["load", "moe_route", "moe_route_sigmoid_grouped", "moe_dispatch", "mo
            "moe_balance_loss", "moe_balance_loss_backward", "moe_balance_loss_workspace", "BalanceLoss",
            "moe_distill_targets", "moe_distill_loss", "moe_distill_loss_backward",
            "moe_distill_loss_workspace", "DistillTargets", "DistillLoss",
+           "moe_mx_quantize", "moe_mx_dequantize", "MxRows", "Mx4SwiGluExperts", "ExpertCheckpoint",
            "moe_get_device_status", "MoeError", "library_path", "HostPipeline"]
 
 
@@ -326,6 +329,65 @@ class SwiGluExperts:
             self.handle, _ptr(x_disp), N, _ptr(offsets), _ptr(dout), _ptr(dinput), _ptr(dgate), _ptr(dup),
             _ptr(ddown), code, _ptr(workspace), workspace.numel(), _stream(stream)))
         return dinput, dgate, dup, ddown
+
+    # -- training with activations kept in 8 bits ---------------------------------
+    def checkpoint_workspace(self, N: int) -> torch.Tensor:
+        """A workspace for forward_checkpoint of up to N rows."""
+        return _workspace(self._lib.moe_experts_workspace_size(self.handle, N), self.gate.device)
+
+    def forward_checkpoint(self, x_disp: torch.Tensor, offsets: torch.Tensor, out=None,
+                           checkpoint: ExpertCheckpoint | None = None, workspace=None, stream=None):
+        """forward_dispatched that also keeps what backward_checkpoint needs:
+        (expert outputs [N,H], the gate and up projections [N,I] in 8 bits)."""
+        dev, dt = self.gate.device, (self.dtype,)
+        if x_disp.dim() != 2:
+            raise MoeError(2, "x_disp must be [N, H]")
+        N = x_disp.shape[0]
+        args = (self.handle, _mx._p(x_disp, "x_disp", dt, (N, self.H), dev), N,
+                _mx._p(offsets, "offsets", (torch.int32,), (self.E + 1,), dev))
+        current, raw = _mx._on(dev, stream)
+        with current:
+            if out is None:
+                out = torch.empty((N, self.H), dtype=self.dtype, device=dev)
+            if checkpoint is None:
+                checkpoint = ExpertCheckpoint.empty(N, self.I, dev)
+            if workspace is None:
+                workspace = self.checkpoint_workspace(N)
+            _lib.check(self._lib.moe_experts_forward_checkpoint(
+                *args, _mx._p(out, "out", dt, (N, self.H), dev), *checkpoint._checked(N, self.I, dev),
+                *_mx._ws(workspace, dev), raw))
+        return out, checkpoint
+
+    def backward_checkpoint_workspace(self, N: int) -> torch.Tensor:
+        return _workspace(self._lib.moe_experts_backward_checkpoint_workspace_size(self.handle, N),
+                          self.gate.device)
+
+    def backward_checkpoint(self, x: MxRows, perm: torch.Tensor, offsets: torch.Tensor,
+                            checkpoint: ExpertCheckpoint, dout: torch.Tensor, top_k: int, grads=None,
+                            workspace=None, stream=None):
+        """Expert backward from 8-bit activations: tokens x [T,H] ("mxfp8"), the
+        dispatch map and a forward's checkpoint.  Returns (dinput [N,H], dgate
+        [E,I,H], dup [E,I,H], ddown [E,H,I]), all in the weight dtype; ``grads``
+        is such a tuple to write into."""
+        dev, dt = self.gate.device, (self.dtype,)
+        if len(x.shape) != 2:
+            raise MoeError(2, "x must be [T, H] rows")
+        T = x.shape[0]
+        N = T * top_k
+        args = (self.handle, *x._checked("x", (T, self.H), "mxfp8", dev), T, top_k,
+                _mx._p(perm, "perm", (torch.int32,), (N,), dev),
+                _mx._p(offsets, "offsets", (torch.int32,), (self.E + 1,), dev),
+                *checkpoint._checked(N, self.I, dev), _mx._p(dout, "dout", dt, (N, self.H), dev))
+        shapes = ((N, self.H), (self.E, self.I, self.H), (self.E, self.I, self.H), (self.E, self.H, self.I))
+        current, raw = _mx._on(dev, stream)
+        with current:
+            if grads is None:
+                grads = tuple(torch.empty(s, dtype=self.dtype, device=dev) for s in shapes)
+            if workspace is None:
+                workspace = self.backward_checkpoint_workspace(N)
+            out = [_mx._p(g, n, dt, s, dev) for g, n, s in zip(grads, ("dinput", "dgate", "dup", "ddown"), shapes)]
+            _lib.check(self._lib.moe_experts_backward_checkpoint(*args, *out, *_mx._ws(workspace, dev), raw))
+        return tuple(grads)
 
     def forward_sigmoid_grouped(self, x: torch.Tensor, logits: torch.Tensor, top_k: int, groups: int,
                                 selected_groups: int, group_top_two: bool, renormalize: bool,

@@ -102,6 +102,20 @@ _SIGNATURES = {
                               P, SZ, P]),
     "moe_distill_loss_backward": (ST, [P, INT, P, P, INT, P, P, P, I64, I64, I32, I64, ctypes.c_float, P,
                                        P, P, P]),
+    "moe_mx_quantize": (ST, [P, INT, I64, I64, INT, P, P, P]),
+    "moe_mx_dequantize": (ST, [P, P, INT, I64, I64, P, I32, I64, P, INT, P]),
+    "moe_mx4_experts_scale_bytes": (SZ, [I64, I64, I64]),
+    "moe_mx4_experts_create": (ST, [P, P, P, P, P, P, INT, I64, I64, I64, P, SZ, P, ctypes.POINTER(P)]),
+    "moe_mx4_experts_destroy": (None, [P]),
+    "moe_mx4_experts_workspace_size": (SZ, [P, I64]),
+    "moe_mx4_experts_forward": (ST, [P, P, I64, P, P, P, SZ, P]),
+    "moe_mx4_forward_workspace_size": (SZ, [P, I64, I32, INT]),
+    "moe_mx4_forward": (ST, [P, P, P, INT, I64, I32, INT, P, P, SZ, P]),
+    "moe_mx4_forward_sigmoid_grouped": (ST, [P, P, P, INT, I64, P, ctypes.POINTER(GroupRoutingOptions),
+                                             P, P, SZ, P]),
+    "moe_experts_forward_checkpoint": (ST, [P, P, I64, P, P, P, P, P, P, P, SZ, P]),
+    "moe_experts_backward_checkpoint_workspace_size": (SZ, [P, I64]),
+    "moe_experts_backward_checkpoint": (ST, [P, P, P, I64, I32, P, P, P, P, P, P, P, P, P, P, P, P, SZ, P]),
     "moe_selftest_bounded_wait": (ST, [P, ctypes.c_uint32, P]),
 }
 

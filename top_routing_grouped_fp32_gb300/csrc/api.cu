@@ -18,136 +18,13 @@
 #include <functional>
 #include <string>
 
-#include "common.cuh"
-#include "internal.h"
-
-struct moe_experts {
-  const void* gate;
-  const void* up;
-  const void* down;
-  moe_dtype dt;
-  int64_t E, I, H;
-  int device;
-  int num_sms;
-  moe::TcWeights* tc;  // null when the tcgen05 path does not apply (FP32, odd sizes)
-};
+#include "api.h"
 
 namespace {
 
-using moe::align_up;
-using moe::dtype_size;
-using moe::kWsHeader;
-
-thread_local std::string g_error;
-
-moe_status fail(moe_status st, const char* fmt, ...) {
-  char buf[512];
-  va_list ap;
-  va_start(ap, fmt);
-  vsnprintf(buf, sizeof buf, fmt, ap);
-  va_end(ap);
-  g_error = buf;
-  return st;
-}
-
-moe_status ok() {
-  g_error.clear();
-  return MOE_OK;
-}
-
-moe_status cuda_fail(cudaError_t e, const char* what) {
-  return fail(MOE_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
-}
-
-#define MOE_TRY_CUDA(expr, what)                   \
-  do {                                             \
-    cudaError_t _e = (expr);                       \
-    if (_e != cudaSuccess) return cuda_fail(_e, what); \
-  } while (0)
-
-constexpr int64_t kMaxE = 1024, kMaxK = 64, kMaxDim = int64_t(1) << 20;
-constexpr int64_t kMaxRows = (int64_t(1) << 31) - 1;
-
-bool valid_dtype(moe_dtype d) { return d == MOE_F32 || d == MOE_F16 || d == MOE_BF16; }
-bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
-bool aligned256(const void* p) { return reinterpret_cast<uintptr_t>(p) % 256 == 0; }
-
-// Checks shared by the calls that take (T, E, top_k).
-moe_status check_tek(int64_t T, int64_t E, int32_t k) {
-  if (T < 0) return fail(MOE_ERR_SHAPE, "T must be >= 0 (got %lld)", (long long)T);
-  if (E < 1) return fail(MOE_ERR_SHAPE, "E must be >= 1 (got %lld)", (long long)E);
-  if (k < 1 || k > E)
-    return fail(MOE_ERR_INVALID_ARG, "top_k must satisfy 1 <= top_k <= E (top_k=%d, E=%lld)", k,
-                (long long)E);
-  if (E > kMaxE) return fail(MOE_ERR_UNSUPPORTED, "E=%lld exceeds the supported 1024", (long long)E);
-  if (k > kMaxK) return fail(MOE_ERR_UNSUPPORTED, "top_k=%d exceeds the supported 64", k);
-  if (T > kMaxRows / k)
-    return fail(MOE_ERR_UNSUPPORTED, "T*top_k=%lld exceeds 2^31-1", (long long)T * k);
-  return MOE_OK;
-}
-
-// GroupRoutingOptions rules of the user guide, section 10.
-moe_status check_group_options(int64_t T, int64_t E, const moe_group_routing_options* o) {
-  if (!o) return fail(MOE_ERR_INVALID_ARG, "group routing options are NULL");
-  if (T < 0) return fail(MOE_ERR_SHAPE, "T must be >= 0 (got %lld)", (long long)T);
-  if (E < 1 || E > kMaxE)
-    return fail(E < 1 ? MOE_ERR_SHAPE : MOE_ERR_UNSUPPORTED, "expert count must be in 1..=1024 (got %lld)",
-                (long long)E);
-  if (o->groups < 1 || o->groups > 128)
-    return fail(MOE_ERR_INVALID_ARG, "group count must be in 1..=128 (got %d)", o->groups);
-  if (E % o->groups != 0)
-    return fail(MOE_ERR_INVALID_ARG, "expert count %lld is not divisible by %d groups", (long long)E, o->groups);
-  if (o->selected_groups < 1 || o->selected_groups > o->groups)
-    return fail(MOE_ERR_INVALID_ARG, "selected_groups must be in 1..=groups (got %d of %d)",
-                o->selected_groups, o->groups);
-  const int64_t per = E / o->groups;
-  if (o->top_k < 1 || o->top_k > 64)
-    return fail(MOE_ERR_INVALID_ARG, "top_k must be in 1..=64 (got %d)", o->top_k);
-  if (o->top_k > o->selected_groups * per)
-    return fail(MOE_ERR_INVALID_ARG, "top_k=%d exceeds the %lld experts of the selected groups", o->top_k,
-                (long long)(o->selected_groups * per));
-  if (o->group_top_two && per < 2)
-    return fail(MOE_ERR_INVALID_ARG, "group_top_two needs at least two experts per group");
-  if (!(o->scale > 0.f) || !std::isfinite(o->scale))
-    return fail(MOE_ERR_INVALID_ARG, "scale must be finite and positive");
-  if (T > kMaxRows / o->top_k) return fail(MOE_ERR_UNSUPPORTED, "T*top_k exceeds 2^31-1");
-  return MOE_OK;
-}
-
-moe_status check_dim(int64_t v, const char* name) {
-  if (v < 1) return fail(MOE_ERR_SHAPE, "%s must be >= 1 (got %lld)", name, (long long)v);
-  if (v > kMaxDim) return fail(MOE_ERR_UNSUPPORTED, "%s=%lld exceeds 2^20", name, (long long)v);
-  return MOE_OK;
-}
-
-moe_status check_ws(const void* ws, size_t have, size_t need) {
-  if (!ws) return fail(MOE_ERR_INVALID_ARG, "workspace is NULL");
-  if (!aligned256(ws)) return fail(MOE_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
-  if (have < need)
-    return fail(MOE_ERR_INVALID_ARG, "workspace too small: %zu bytes given, %zu needed", have, need);
-  return MOE_OK;
-}
-
-moe_status check_handle(const moe_experts* x) {
-  if (!x) return fail(MOE_ERR_INVALID_ARG, "experts handle is NULL");
-  int dev = -1;
-  MOE_TRY_CUDA(cudaGetDevice(&dev), "cudaGetDevice");
-  if (dev != x->device)
-    return fail(MOE_ERR_INVALID_ARG, "experts live on device %d but device %d is current", x->device,
-                dev);
-  return MOE_OK;
-}
+using namespace moe::api;
 
 // ---- workspace layouts -----------------------------------------------------
-struct Cursor {
-  size_t off = kWsHeader;
-  size_t take(size_t bytes) {
-    const size_t at = off;
-    off = align_up(off + bytes, 1024);
-    return at;
-  }
-};
-
 struct ForwardLayout {
   size_t idx, weights, offsets, perm, scratch, x_disp, h, slots, slot_row, total;
 };
@@ -169,18 +46,23 @@ ForwardLayout forward_layout(const moe_experts* x, int64_t T, int32_t k, moe_dty
   return L;
 }
 
-template <typename P>
-P* at(void* base, size_t off) {
-  return reinterpret_cast<P*>(static_cast<char*>(base) + off);
-}
-
-uint32_t* status_word(void* ws) { return static_cast<uint32_t*>(ws); }
+// 8-bit copies of the gate and up products that a forward keeps for its backward.
+struct Checkpoint {
+  uint8_t *g, *g_scales, *u, *u_scales;
+};
 
 // Runs the two expert GEMMs: gate/up + SwiGLU into h, then down.
 moe_status run_experts(const moe_experts* x, const void* x_disp, int64_t N, const uint32_t* offsets,
                        void* h, void* out, int down_mode, const uint32_t* perm, const void* weights,
-                       moe_dtype wdt, uint32_t* status, cudaStream_t s, void* ev_mid) {
+                       moe_dtype wdt, uint32_t* status, cudaStream_t s, void* ev_mid,
+                       const Checkpoint* ck) {
   moe::GemmArgs g{};
+  if (ck) {
+    g.ck_g = ck->g;
+    g.ck_u = ck->u;
+    g.ck_gs = ck->g_scales;
+    g.ck_us = ck->u_scales;
+  }
   g.dt = x->dt;
   g.E = (int)x->E;
   g.N = N;
@@ -196,6 +78,7 @@ moe_status run_experts(const moe_experts* x, const void* x_disp, int64_t N, cons
   cudaError_t e = x->tc ? moe::launch_gemm_tc(g, x->tc, x->num_sms, s) : moe::launch_gemm_simt(g, s);
   if (e != cudaSuccess) return cuda_fail(e, "gate/up grouped GEMM launch");
   if (ev_mid) MOE_TRY_CUDA(cudaEventRecord((cudaEvent_t)ev_mid, s), "cudaEventRecord");
+  g.ck_g = nullptr;
   g.mode = down_mode;
   g.A = h;
   g.K = x->I;
@@ -272,7 +155,7 @@ moe_status forward_core(moe_experts_t x, const void* xin, const void* logits, mo
                  "gather kernel launch");
   MOE_TRY_CUDA(rec(2), "cudaEventRecord");
   st = run_experts(x, at<void>(ws, L.x_disp), N, offsets, at<void>(ws, L.h), at<void>(ws, L.slots),
-                   moe::kDownWeighted, perm, w, ldt, status, s, ev ? ev[3] : nullptr);
+                   moe::kDownWeighted, perm, w, ldt, status, s, ev ? ev[3] : nullptr, nullptr);
   if (st != MOE_OK) return st;
   MOE_TRY_CUDA(rec(4), "cudaEventRecord");
   MOE_TRY_CUDA(moe::launch_slot_sum(at<void>(ws, L.slots), x->dt, T, k, x->H, y, s),
@@ -464,8 +347,9 @@ size_t moe_experts_workspace_size(moe_experts_t x, int64_t N) {
   return kWsHeader + align_up((size_t)N * x->I * dtype_size(x->dt), 1024) + offsets_copy_bytes(x);
 }
 
-moe_status moe_experts_forward(moe_experts_t x, const void* x_disp, int64_t N, const uint32_t* offsets,
-                               void* expert_out, void* ws, size_t ws_bytes, cudaStream_t stream) {
+static moe_status experts_forward(moe_experts_t x, const void* x_disp, int64_t N, const uint32_t* offsets,
+                                  void* expert_out, const Checkpoint* ck, void* ws, size_t ws_bytes,
+                                  cudaStream_t stream) {
   moe_status st = check_handle(x);
   if (st != MOE_OK) return st;
   if (N < 0 || N > kMaxRows) return fail(MOE_ERR_SHAPE, "N=%lld out of range", (long long)N);
@@ -481,8 +365,29 @@ moe_status moe_experts_forward(moe_experts_t x, const void* x_disp, int64_t N, c
   MOE_TRY_CUDA(moe::launch_sanitize_offsets(offsets, (int)x->E, N, off_ok, status_word(ws), stream),
                "offsets check launch");
   st = run_experts(x, x_disp, N, off_ok, static_cast<char*>(ws) + kWsHeader, expert_out,
-                   moe::kDownPlain, nullptr, nullptr, MOE_F32, status_word(ws), stream, nullptr);
+                   moe::kDownPlain, nullptr, nullptr, MOE_F32, status_word(ws), stream, nullptr, ck);
   return st == MOE_OK ? ok() : st;
+}
+
+moe_status moe_experts_forward(moe_experts_t x, const void* x_disp, int64_t N, const uint32_t* offsets,
+                               void* expert_out, void* ws, size_t ws_bytes, cudaStream_t stream) {
+  return experts_forward(x, x_disp, N, offsets, expert_out, nullptr, ws, ws_bytes, stream);
+}
+
+moe_status moe_experts_forward_checkpoint(moe_experts_t x, const void* x_disp, int64_t N, const uint32_t* offsets,
+                                          void* expert_out, uint8_t* gate_values, uint8_t* gate_scales,
+                                          uint8_t* up_values, uint8_t* up_scales, void* ws, size_t ws_bytes,
+                                          cudaStream_t stream) {
+  moe_status st = check_handle(x);
+  if (st != MOE_OK) return st;
+  if (!x->tc)
+    return fail(MOE_ERR_UNSUPPORTED, "checkpoints need F16/BF16 experts with H, I multiples of 8");
+  if (N > 0 && (!gate_values || !gate_scales || !up_values || !up_scales))
+    return fail(MOE_ERR_INVALID_ARG, "the checkpoint's values and scales must be non-NULL");
+  if (!aligned16(gate_values) || !aligned16(up_values))
+    return fail(MOE_ERR_INVALID_ARG, "checkpoint values must be 16-byte aligned");
+  const Checkpoint ck{gate_values, gate_scales, up_values, up_scales};
+  return experts_forward(x, x_disp, N, offsets, expert_out, &ck, ws, ws_bytes, stream);
 }
 
 // ---- combine -------------------------------------------------------------
@@ -873,6 +778,78 @@ moe_status moe_experts_backward_with_strategy(moe_experts_t x, const void* x_dis
   } else {
     MOE_TRY_CUDA(moe::launch_experts_backward(a, stream), "expert backward launch");
   }
+  return ok();
+}
+
+size_t moe_experts_backward_checkpoint_workspace_size(moe_experts_t x, int64_t N) {
+  if (!x || N < 0 || !bwd_tc_ok(x, N)) return 0;
+  return kWsHeader + align_up(moe::experts_backward_ck_workspace(N, (int)x->E, x->H, x->I), 1024) +
+         offsets_copy_bytes(x) + 1024;
+}
+
+moe_status moe_experts_backward_checkpoint(moe_experts_t x, const uint8_t* x_values, const uint8_t* x_scales,
+                                           int64_t T, int32_t top_k, const uint32_t* perm, const uint32_t* offsets,
+                                           const uint8_t* gate_values, const uint8_t* gate_scales,
+                                           const uint8_t* up_values, const uint8_t* up_scales, const void* dout,
+                                           void* dinput, void* dgate, void* dup, void* ddown, void* ws,
+                                           size_t ws_bytes, cudaStream_t stream) {
+  moe_status st = check_handle(x);
+  if (st != MOE_OK) return st;
+  if (T < 0) return fail(MOE_ERR_SHAPE, "T must be >= 0 (got %lld)", (long long)T);
+  if (top_k < 1 || top_k > kMaxK) return fail(MOE_ERR_INVALID_ARG, "top_k must be in 1..=64");
+  if (T > kMaxRows / top_k) return fail(MOE_ERR_UNSUPPORTED, "T*top_k exceeds 2^31-1");
+  const int64_t N = T * top_k;
+  if (!bwd_tc_ok(x, N))
+    return fail(MOE_ERR_UNSUPPORTED, "checkpoints need F16/BF16 experts with H, I multiples of 8");
+  if (!offsets || !dgate || !dup || !ddown)
+    return fail(MOE_ERR_INVALID_ARG, "offsets, dgate, dup and ddown must be non-NULL");
+  if (!aligned16(dgate) || !aligned16(dup) || !aligned16(ddown))
+    return fail(MOE_ERR_INVALID_ARG, "dgate, dup and ddown must be 16-byte aligned");
+  if (N > 0 && (!x_values || !x_scales || !perm || !gate_values || !gate_scales || !up_values || !up_scales ||
+                !dout || !dinput))
+    return fail(MOE_ERR_INVALID_ARG, "x, perm, the checkpoint, dout and dinput must be non-NULL");
+  if (!aligned16(x_values) || !aligned16(gate_values) || !aligned16(up_values) || !aligned16(dout) ||
+      !aligned16(dinput))
+    return fail(MOE_ERR_INVALID_ARG, "x, the checkpoint's values, dout and dinput must be 16-byte aligned");
+  if ((st = check_ws(ws, ws_bytes, moe_experts_backward_checkpoint_workspace_size(x, N))) != MOE_OK) return st;
+  MOE_TRY_CUDA(cudaMemsetAsync(ws, 0, 4, stream), "cudaMemsetAsync");
+  if (N == 0) {  // no rows: every weight gradient is zero
+    const size_t wb = (size_t)x->E * x->I * x->H * 2;
+    MOE_TRY_CUDA(cudaMemsetAsync(dgate, 0, wb, stream), "cudaMemsetAsync");
+    MOE_TRY_CUDA(cudaMemsetAsync(dup, 0, wb, stream), "cudaMemsetAsync");
+    MOE_TRY_CUDA(cudaMemsetAsync(ddown, 0, wb, stream), "cudaMemsetAsync");
+    return ok();
+  }
+  char* base = static_cast<char*>(ws) + align_up(kWsHeader + offsets_copy_bytes(x), 1024);
+  uint32_t* off_ok = reinterpret_cast<uint32_t*>(static_cast<char*>(ws) + kWsHeader);
+  MOE_TRY_CUDA(moe::launch_sanitize_offsets(offsets, (int)x->E, N, off_ok, status_word(ws), stream),
+               "offsets check launch");
+  moe::ExpertsCkBwdArgs a{};
+  a.dt = x->dt;
+  a.E = (int)x->E;
+  a.k = top_k;
+  a.T = T;
+  a.N = N;
+  a.H = x->H;
+  a.I = x->I;
+  a.x = x_values;
+  a.x_scales = x_scales;
+  a.perm = perm;
+  a.offsets = off_ok;
+  a.g = gate_values;
+  a.g_scales = gate_scales;
+  a.u = up_values;
+  a.u_scales = up_scales;
+  a.dout = dout;
+  a.gate = x->gate;
+  a.up = x->up;
+  a.down = x->down;
+  a.dinput = dinput;
+  a.dgate = dgate;
+  a.dup = dup;
+  a.ddown = ddown;
+  a.status = status_word(ws);
+  MOE_TRY_CUDA(moe::launch_experts_backward_ck(a, base, x->num_sms, stream), "checkpointed expert backward launch");
   return ok();
 }
 

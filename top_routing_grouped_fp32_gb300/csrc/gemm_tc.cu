@@ -60,6 +60,8 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "mx.cuh"
+#include "tcgen05.cuh"
 
 namespace moe {
 
@@ -84,7 +86,6 @@ constexpr uint32_t B_HALF_BYTES = 128 * BK * 2;  // 16 KiB
 constexpr int THREADS = 192;
 constexpr uint32_t TMEM_COLS = 2 * BN;
 constexpr int MAX_E = 1024;
-constexpr uint64_t kWaitLimitNs = 2000000000ull;
 
 // KS: 64-deep K sub-blocks per ring stage.  KS = 2 (forward CTA-pair GEMMs,
 // K-major operands) halves the barrier round trips and commits per MMA: one
@@ -139,262 +140,19 @@ struct Params {
   // gate and up values of the same features in both tile forms
   int b_inter;
   int v8_out;  // out rows are 32-byte aligned segments (n_out % 16 == 0, 32-byte base)
+  // 8-bit checkpoints of the gate and up products [rows, I] with a scale a
+  // 32-column block: written by the gate/up product (CK = kSave), read by the
+  // da product (CK = kUse)
+  uint8_t* ck_g;
+  uint8_t* ck_u;
+  uint8_t* ck_gs;
+  uint8_t* ck_us;
   // single CTAs (decode-sized batches): a tile of at most 32 rows loads A
   // through a 32-row box (the mapA64 slot); the MMA still runs M = 128, and
   // its other 96 rows multiply whatever the ring stage held before -- rows
   // that are never stored
   int thin_a;
 };
-
-// ---------------------------------------------------------------- PTX wrappers
-__device__ __forceinline__ uint32_t smem_u32(const void* p) {
-  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
-}
-__device__ __forceinline__ uint64_t global_timer() {
-  uint64_t t;
-  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-  return t;
-}
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-// shared::cluster address of the same shared variable in CTA `rank` of the cluster
-__device__ __forceinline__ uint32_t mapa(uint32_t saddr, uint32_t rank) {
-  uint32_t r;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
-  return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" :::
-                   "memory");
-}
-__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
-  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
-}
-template <bool CLUSTER>
-__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  if constexpr (CLUSTER) {
-    asm volatile(
-        "{\n\t.reg .pred P;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 P, [%1], %2;\n\t"
-        "selp.b32 %0, 1, 0, P;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-  } else {
-    asm volatile(
-        "{\n\t.reg .pred P;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 P, [%1], %2;\n\t"
-        "selp.b32 %0, 1, 0, P;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-  }
-  return ok != 0;
-}
-__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-// arrival on a barrier of another CTA of the cluster (shared::cluster address)
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t cbar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cbar) : "memory");
-}
-__device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
-               : "memory");
-}
-// Bounded wait for phase `parity` of `bar`.  Returns false if the CTA is
-// aborting or the time limit passed (then the abort flag and status are set).
-template <bool CLUSTER>
-__device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag,
-                                            uint32_t* status, uint64_t limit_ns) {
-  const uint64_t t0 = global_timer();
-  for (uint32_t n = 1;; ++n) {
-    if (mbar_test<CLUSTER>(bar, parity)) return true;
-    if ((n & 127u) == 0) {
-      if (*abort_flag) return false;
-      if (global_timer() - t0 > limit_ns) {
-        *abort_flag = 1u;
-        set_status(status, (uint32_t)MOE_ERR_DEVICE_TIMEOUT);
-        return false;
-      }
-    }
-  }
-}
-template <bool CLUSTER>
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag,
-                                          uint32_t* status, uint64_t limit_ns = kWaitLimitNs) {
-  if (mbar_test<CLUSTER>(bar, parity)) return true;  // fast path, inline
-  return mbar_wait_slow<CLUSTER>(bar, parity, abort_flag, status, limit_ns);
-}
-// TMA tile loads into this CTA's shared memory.  PAIR == 2: the completion is
-// counted on `bar`, a shared::cluster address that may be the leader CTA's.
-template <int PAIR>
-__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int c0, int c1,
-                                            uint32_t bar) {
-  if constexpr (PAIR == 2) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
-        : "memory");
-  } else {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
-        : "memory");
-  }
-}
-template <int PAIR>
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int c0, int c1,
-                                            int c2, uint32_t bar) {
-  if constexpr (PAIR == 2) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
-        : "memory");
-  } else {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
-        : "memory");
-  }
-}
-__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
-  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
-}
-__device__ __forceinline__ void tc_fence_before() {
-  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-}
-__device__ __forceinline__ void tc_fence_after() {
-  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-}
-// TMEM allocation: PAIR == 2 allocates the same columns in both CTAs of the
-// pair and is executed by one warp of each CTA.
-template <int PAIR>
-__device__ __forceinline__ void tmem_alloc(uint32_t slot, uint32_t cols) {
-  if constexpr (PAIR == 2) {
-    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot),
-                 "r"(cols)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
-  } else {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot),
-                 "r"(cols)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-  }
-}
-template <int PAIR>
-__device__ __forceinline__ void tmem_dealloc(uint32_t taddr, uint32_t cols) {
-  if constexpr (PAIR == 2) {
-    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(cols)
-                 : "memory");
-  } else {
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(cols)
-                 : "memory");
-  }
-}
-// D[tmem] (+)= A[smem] * B[smem]^T, both K-major, one (128*PAIR) x 256 x 16 step.
-template <int PAIR>
-__device__ __forceinline__ void umma_f16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
-                                         uint32_t idesc, uint32_t accumulate) {
-  if constexpr (PAIR == 2) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-        : "memory");
-  } else {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-        : "memory");
-  }
-}
-// Arrive on `bar` (same offset in every CTA of the pair) once all MMAs this
-// thread issued have completed.  PAIR == 2: the arrival goes to both CTAs.
-template <int PAIR>
-__device__ __forceinline__ void umma_commit(uint32_t bar) {
-  if constexpr (PAIR == 2) {
-    const uint16_t both = 3;
-    asm volatile(
-        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
-        " [%0], %1;" ::"r"(bar),
-        "h"(both)
-        : "memory");
-  } else {
-    asm volatile(
-        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
-        : "memory");
-  }
-}
-// Arrive on the issuing CTA's own `bar` once all its MMAs have completed.
-template <int PAIR>
-__device__ __forceinline__ void umma_commit_local(uint32_t bar) {
-  if constexpr (PAIR == 2) {
-    asm volatile(
-        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
-        : "memory");
-  } else {
-    asm volatile(
-        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
-        : "memory");
-  }
-}
-// 32 consecutive FP32 columns of this warp's 32 TMEM lanes.
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
-        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
-        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(taddr));
-}
-// An empty statement that the compiler must treat as rewriting r: placed after
-// a wait, it keeps every use of r after that wait.
-__device__ __forceinline__ void reg_fence(uint32_t (&r)[32]) {
-  asm volatile(""
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
-                 "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]),
-                 "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]),
-                 "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]),
-                 "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]),
-                 "+r"(r[31]));
-}
-// The same wait, naming the registers of a load still in flight as operands so
-// that no use of them can be scheduled before it.
-__device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.wait::ld.sync.aligned;"
-      : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
-        "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]),
-        "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]),
-        "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]),
-        "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
-      :
-      : "memory");
-}
-
-// 32 bytes (8 words) to a 32-byte-aligned global address: a whole sector per lane
-__device__ __forceinline__ void st_v8(uint32_t* dst, const uint32_t* w) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]), "r"(w[1]),
-               "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-               : "memory");
-}
 
 // ---------------------------------------------------------------- epilogue stores
 // Each lane of an epilogue warp holds one tile row; storing straight from
@@ -444,16 +202,7 @@ __device__ __forceinline__ void staged_store(uint32_t* stg, const uint32_t* w, u
   __syncwarp();
 }
 
-// Shared-memory matrix descriptor of a K-major tile written by TMA with the
-// 128-byte swizzle: rows of 128 bytes, 8-row groups 1024 bytes apart.
-__device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr) {
-  return (uint64_t)((saddr & 0x3FFFFu) >> 4)      // start address
-         | ((uint64_t)1 << 16)                     // leading offset (unused here)
-         | ((uint64_t)(1024 >> 4) << 32)           // stride offset between 8-row groups
-         | ((uint64_t)1 << 46)                     // descriptor version
-         | ((uint64_t)2 << 61);                    // 128-byte swizzle
-}
-// The same for an MN-major tile: each TMA box holds 64 K rows of 64
+// The descriptor of sw128_desc for an MN-major tile: each TMA box holds 64 K rows of 64
 // consecutive M (or N) elements, 128 bytes a row, swizzled in 8-row groups
 // 1024 bytes apart (stride offset); boxes for the next 64 M/N elements follow
 // 8 KiB apart (leading offset).
@@ -465,6 +214,50 @@ __device__ __forceinline__ uint64_t sw128_mn_desc(uint32_t saddr) {
          | ((uint64_t)1 << 46)
          | ((uint64_t)2 << 61);
 }
+// A 32-column block of a row in 8 bits: `left` of its columns (a multiple of 8)
+// lie inside the row; those behind hold zeros and do not move the scale.
+__device__ __forceinline__ void store_mx8(const uint32_t (&r)[32], uint8_t* dst, int64_t left, uint8_t* scale) {
+  uint32_t a = 0;
+#pragma unroll
+  for (int i = 0; i < 32; ++i) a = max(a, r[i] & 0x7FFFFFFFu);
+  const uint32_t sb = mx::scale_byte<MOE_MXFP8>(a);
+  const float inv = mx::inverse_scale(sb);
+  uint32_t w[8];
+#pragma unroll
+  for (int v = 0; v < 8; ++v) {
+    float q[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) q[i] = sb == 255u ? 0.f : __uint_as_float(r[4 * v + i]) * inv;
+    w[v] = mx::to_e4m3x4(q);
+  }
+  if (left >= 32 && reinterpret_cast<uintptr_t>(dst) % 16 == 0) {
+    reinterpret_cast<uint4*>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    reinterpret_cast<uint4*>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  } else {
+#pragma unroll
+    for (int v = 0; v < 4; ++v)
+      if (left >= 8 * v + 8) reinterpret_cast<uint2*>(dst)[v] = make_uint2(w[2 * v], w[2 * v + 1]);
+  }
+  *scale = (uint8_t)sb;
+}
+// The elements of such a block (zeros past `left`)
+__device__ __forceinline__ void load_mx8(const uint8_t* src, int64_t left, uint32_t (&w)[8]) {
+  if (left >= 32 && reinterpret_cast<uintptr_t>(src) % 16 == 0) {
+    const uint4 a = __ldg(reinterpret_cast<const uint4*>(src)), b = __ldg(reinterpret_cast<const uint4*>(src) + 1);
+    put4(w, a);
+    put4(w + 4, b);
+  } else {
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      const uint2 a = left >= 8 * v + 8 ? __ldg(reinterpret_cast<const uint2*>(src) + v) : make_uint2(0u, 0u);
+      w[2 * v] = a.x;
+      w[2 * v + 1] = a.y;
+    }
+  }
+}
+
+// What a kernel does with the 8-bit checkpoints of the gate and up products
+enum Checkpoint { kNone = 0, kSave = 1, kUse = 2 };
 enum BForm { kBKmajor3d = 0, kBMNmajor3d = 1, kBMNmajor2d = 2 };
 // Instruction descriptor: FP32 accumulator, 16-bit A/B (bf16 or f16), both
 // K-major (bits 15/16 set below make A/B MN-major), M = 128*PAIR, N = 256.
@@ -527,7 +320,10 @@ __device__ __forceinline__ Tile decode_wgrad(uint32_t tile, const Params& p, int
 }
 
 // ---------------------------------------------------------------- the kernel
-template <typename T, int PAIR, int KS>
+// CK = kSave: the gate/up product also writes its checkpoints.  CK = kUse: the
+// da product of the checkpointed backward (kSwigluBwd on da's own accumulators)
+// and weight gradients stored in T.
+template <typename T, int PAIR, int KS, int CK>
 __global__ void __launch_bounds__(THREADS, 1)
 grouped_gemm_tc(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapB0,
                 const __grid_constant__ CUtensorMap mapB1, const __grid_constant__ CUtensorMap mapA64,
@@ -811,7 +607,98 @@ grouped_gemm_tc(const __grid_constant__ CUtensorMap mapA, const __grid_constant_
       if (!ok) break;
       tc_fence_after();
       const uint32_t taddr = tmem_base + ((uint32_t)(quarter * 32) << 16) + acc * BN;
-      if (p.mode == kGateUpSwiglu) {
+      if constexpr (CK == kUse) {
+        if (p.mode == kSwigluBwd) {
+          // accumulator da = dout . W_down[e]; g and u of the forward from
+          // their 8-bit checkpoints: dg = da u silu'(g), du = da silu(g) and a
+          // = silu(g) u in the 16-bit dtype, in the 64-padded row space (its
+          // padding rows zero).  da itself stays in FP32 and in TMEM.
+          const int64_t I = p.n_out, nblk = (I + 31) / 32;
+          const int64_t col0 = (int64_t)t.nb * 256 + (int64_t)nhalf * 128;
+          const int64_t local = grow - (int64_t)s_off[t.e];
+          const uint32_t pe = __ldg(p.pad + t.e);
+          const bool zero_row = !row_ok && local < (int64_t)(__ldg(p.pad + t.e + 1) - pe);
+          const bool store = row_ok || zero_row;
+          const int64_t prow = (int64_t)pe + local;
+          uint32_t* dgp = store ? reinterpret_cast<uint32_t*>(out + prow * 2 * I + col0) : nullptr;
+          uint32_t* dup_p = store ? reinterpret_cast<uint32_t*>(out + prow * 2 * I + I + col0) : nullptr;
+          uint32_t* ap = store ? reinterpret_cast<uint32_t*>(static_cast<T*>(p.out2) + prow * I + col0) : nullptr;
+          const int nch = t.half ? 4 : 8;
+          // the next block's elements and scales are asked for before this one is computed
+          uint32_t gq[8], uq[8], gb = 0, ub = 0;
+          auto load = [&](int ci) {
+            const int64_t c = col0 + 32 * ci, left = row_ok ? I - c : 0;
+            load_mx8(p.ck_g + grow * I + c, left, gq);
+            load_mx8(p.ck_u + grow * I + c, left, uq);
+            gb = left > 0 ? (uint32_t)__ldg(p.ck_gs + grow * nblk + c / 32) : 0u;
+            ub = left > 0 ? (uint32_t)__ldg(p.ck_us + grow * nblk + c / 32) : 0u;
+          };
+          load(0);
+#pragma unroll 1
+          for (int ci = 0; ci < nch; ++ci) {
+            if (col0 + 32 * ci >= I) break;
+            uint32_t d[32];
+            tmem_ld32(taddr + 32 * ci, d);
+            float g[32], u[32];
+            const float gs = mx::scale_value(gb), us = mx::scale_value(ub);
+#pragma unroll
+            for (int v = 0; v < 8; ++v) {
+              mx::from_e4m3x4(gq[v], g + 4 * v);
+              mx::from_e4m3x4(uq[v], u + 4 * v);
+            }
+            if (ci + 1 < nch) load(ci + 1);
+            tmem_wait_ld(d);
+            uint32_t wdg[16], wdu[16], wa[16];
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+              float fdg[8], fdu[8], fa[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const float gg = g[v * 8 + i] * gs, uu = u[v * 8 + i] * us;  // 0 in rows not stored
+                const float dv = row_ok ? __uint_as_float(d[v * 8 + i]) : 0.f;
+                const float sg = __fdividef(1.f, 1.f + __expf(-gg));  // 16-bit outputs
+                const float silu = gg * sg;
+                fdg[i] = dv * uu * (sg + silu * (1.f - sg));
+                fdu[i] = dv * silu;
+                fa[i] = silu * uu;
+              }
+              put4(wdg + 4 * v, pack8<T>(fdg));
+              put4(wdu + 4 * v, pack8<T>(fdu));
+              put4(wa + 4 * v, pack8<T>(fa));
+            }
+            const int vw = min(16, valid_words<T>(I - col0 - 32 * ci));
+            staged_store<16>(stg, wdg, dgp ? dgp + 16 * ci : nullptr, vw, lane);
+            staged_store<16>(stg, wdu, dup_p ? dup_p + 16 * ci : nullptr, vw, lane);
+            staged_store<16>(stg, wa, ap ? ap + 16 * ci : nullptr, vw, lane);
+          }
+        } else {
+          // kWgrad: rows of a weight-gradient tile, rounded once to T (an
+          // expert without rows gets zeros)
+          const int64_t col0 = (int64_t)t.nb * 256;
+          T* rowt = nullptr;
+          if (row_ok) {
+            if (grow < p.split)
+              rowt = out + ((int64_t)t.e * p.split + grow) * p.n_out + col0;
+            else
+              rowt = static_cast<T*>(p.out2) + ((int64_t)t.e * (p.m_total - p.split) + grow - p.split) * p.n_out + col0;
+          }
+          uint32_t* rowp = reinterpret_cast<uint32_t*>(rowt);
+#pragma unroll 1
+          for (int c = 0; c < 256; c += 32) {
+            uint32_t o[32], w[16];
+            tmem_ld32(taddr + c, o);
+            tmem_wait_ld(o);
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+              float f[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) f[i] = t.nk == 0 ? 0.f : __uint_as_float(o[v * 8 + i]);
+              put4(w + 4 * v, pack8<T>(f));
+            }
+            staged_store<16>(stg, w, rowp ? rowp + c / 2 : nullptr, valid_words<T>(p.n_out - col0 - c), lane);
+          }
+        }
+      } else if (p.mode == kGateUpSwiglu) {
         // h = silu(g) * u: stored straight from registers (one 16-byte vector
         // per 8 columns); this epilogue is not store-bound, and measured
         // faster without the staging round trip.  Interleaved B: accumulator
@@ -832,6 +719,13 @@ grouped_gemm_tc(const __grid_constant__ CUtensorMap mapA, const __grid_constant_
           tmem_ld32(taddr + gcol + fw, u);
           tmem_wait_ld(g);
           reg_fence(u);
+          if constexpr (CK == kSave) {
+            if (row_ok && col0 + i32 < p.n_out) {
+              const int64_t c = col0 + i32, at = grow * ((p.n_out + 31) / 32) + c / 32;
+              store_mx8(g, p.ck_g + grow * p.n_out + c, p.n_out - c, p.ck_gs + at);
+              store_mx8(u, p.ck_u + grow * p.n_out + c, p.n_out - c, p.ck_us + at);
+            }
+          }
           if (row_ok) {
             uint32_t hw[16];
 #pragma unroll
@@ -859,7 +753,7 @@ grouped_gemm_tc(const __grid_constant__ CUtensorMap mapA, const __grid_constant_
             }
           }
         }
-      } else if (p.mode == kSwigluBwd) {
+      } else if (CK == kNone && p.mode == kSwigluBwd) {
         // accumulators g = x . W_gate[e]^T, u = x . W_up[e]^T (recomputed); with
         // da = dout . W_down[e] (16-bit, from the previous product):
         // dg = da * u * silu'(g), du = da * silu(g) and the activation
@@ -938,7 +832,7 @@ grouped_gemm_tc(const __grid_constant__ CUtensorMap mapA, const __grid_constant_
         };
         if (t.half) features(std::integral_constant<int, 64>{});
         else features(std::integral_constant<int, 128>{});
-      } else if (p.mode == kWgrad) {
+      } else if (CK == kNone && p.mode == kWgrad) {
         // FP32 rows of a weight-gradient tile (rows at or past `split` go to
         // out2; an expert without rows gets zeros).  A half tile's warp holds
         // 128 of the 256 columns.
@@ -1111,13 +1005,13 @@ size_t smem_bytes(int E) {
 }
 
 // Clusters of PAIR CTAs that can be resident at once (one CTA per SM).
-template <typename T, int PAIR, int KS = 1>
+template <typename T, int PAIR, int KS = 1, int CK = kNone>
 cudaError_t resident_clusters(int num_sms, int* out) {
   static std::once_flag once;
   static cudaError_t err = cudaSuccess;
   static int clusters = 0;
   std::call_once(once, [num_sms] {
-    err = cudaFuncSetAttribute(grouped_gemm_tc<T, PAIR, KS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    err = cudaFuncSetAttribute(grouped_gemm_tc<T, PAIR, KS, CK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                (int)smem_bytes<PAIR, KS>(MAX_E));
     if (err != cudaSuccess) return;
     if (PAIR == 1) {
@@ -1135,21 +1029,21 @@ cudaError_t resident_clusters(int num_sms, int* out) {
     cfg.dynamicSmemBytes = smem_bytes<PAIR, KS>(MAX_E);
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    err = cudaOccupancyMaxActiveClusters(&clusters, grouped_gemm_tc<T, PAIR, KS>, &cfg);
+    err = cudaOccupancyMaxActiveClusters(&clusters, grouped_gemm_tc<T, PAIR, KS, CK>, &cfg);
   });
   *out = clusters;
   return err;
 }
 
 // mA64: A with 64-row boxes, for the half tiles of p.half_tails (else unused)
-template <typename T, int PAIR, int KS = 1>
+template <typename T, int PAIR, int KS = 1, int CK = kNone>
 cudaError_t launch_t(int64_t N, int E, const CUtensorMap& mA, const CUtensorMap& mB0,
                      const CUtensorMap& mB1, Params p, int num_sms, cudaStream_t s,
                      const CUtensorMap* mA64 = nullptr) {
   if (!mA64 || PAIR != 2) p.half_tails = 0;
   if (!mA64 || PAIR != 1) p.thin_a = 0;
   int clusters = 0;
-  cudaError_t err = resident_clusters<T, PAIR, KS>(num_sms, &clusters);
+  cudaError_t err = resident_clusters<T, PAIR, KS, CK>(num_sms, &clusters);
   if (err != cudaSuccess) return err;
   if (clusters < 1) return cudaErrorLaunchOutOfResources;
   constexpr int TM = Cfg<PAIR>::TILE_M;
@@ -1178,15 +1072,15 @@ cudaError_t launch_t(int64_t N, int E, const CUtensorMap& mA, const CUtensorMap&
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, grouped_gemm_tc<T, PAIR, KS>, mA, mB0, mB1, mA64 ? *mA64 : mA, p);
+  return cudaLaunchKernelEx(&cfg, grouped_gemm_tc<T, PAIR, KS, CK>, mA, mB0, mB1, mA64 ? *mA64 : mA, p);
 }
 
-template <typename T>
+template <typename T, int CK = kNone>
 cudaError_t launch_any(bool pair, int64_t N, int E, const CUtensorMap& mA, const CUtensorMap& mB0,
                        const CUtensorMap& mB1, const Params& p, int num_sms, cudaStream_t s,
                        const CUtensorMap* mA64 = nullptr) {
-  return pair ? launch_t<T, 2>(N, E, mA, mB0, mB1, p, num_sms, s, mA64)
-              : launch_t<T, 1>(N, E, mA, mB0, mB1, p, num_sms, s);
+  return pair ? launch_t<T, 2, 1, CK>(N, E, mA, mB0, mB1, p, num_sms, s, mA64)
+              : launch_t<T, 1, 1, CK>(N, E, mA, mB0, mB1, p, num_sms, s);
 }
 
 // ---------------------------------------------------------------- backward
@@ -1389,6 +1283,157 @@ cudaError_t backward_t(const ExpertsBwdArgs& a, const TcWeights* w, char* ws, in
   return cudaSuccess;
 }
 
+// Work beside the caller's stream: run() forks it off `s` onto a stream of its
+// own, join() makes `s` wait for it.  While `s` is being captured into a graph
+// run() works on `s` itself.
+struct SideStream {
+  cudaEvent_t done = nullptr;
+  ~SideStream() {
+    if (done) cudaEventDestroy(done);
+  }
+  template <typename F>
+  cudaError_t run(cudaStream_t s, F&& work) {
+    cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+    cudaError_t err = cudaStreamIsCapturing(s, &capture);
+    if (err != cudaSuccess) return err;
+    if (capture != cudaStreamCaptureStatusNone) return work(s);
+    cudaStream_t side = nullptr;
+    cudaEvent_t fork = nullptr;
+    if ((err = cudaStreamCreateWithFlags(&side, cudaStreamNonBlocking)) != cudaSuccess) return err;
+    err = cudaEventCreateWithFlags(&fork, cudaEventDisableTiming);
+    if (err == cudaSuccess) err = cudaEventCreateWithFlags(&done, cudaEventDisableTiming);
+    if (err == cudaSuccess) err = cudaEventRecord(fork, s);
+    if (err == cudaSuccess) err = cudaStreamWaitEvent(side, fork, 0);
+    if (err == cudaSuccess) err = work(side);
+    if (err == cudaSuccess) err = cudaEventRecord(done, side);
+    cudaStreamDestroy(side);  // its resources go once the work is done
+    if (fork) cudaEventDestroy(fork);
+    return err;
+  }
+  cudaError_t join(cudaStream_t s) { return done ? cudaStreamWaitEvent(s, done, 0) : cudaSuccess; }
+};
+
+// The checkpointed backward: products 1 and 2 above become one (da stays in
+// the accumulators, g and u come from the checkpoint), x's padded rows are read
+// from its 8-bit tokens, and the weight gradients are stored in T.
+struct CkLayout {
+  int64_t npad;
+  size_t pad, dgduP, actP, xP, doutP, total;
+};
+
+CkLayout ck_layout(int64_t N, int E, int64_t H, int64_t I) {
+  CkLayout L{};
+  L.npad = N + 63 * (int64_t)E;
+  size_t off = 0;
+  auto take = [&off](size_t bytes) {
+    const size_t at = off;
+    off += (bytes + 1023) & ~(size_t)1023;
+    return at;
+  };
+  L.pad = take((size_t)(E + 1) * 4);
+  L.dgduP = take((size_t)L.npad * 2 * I * 2);
+  L.actP = take((size_t)L.npad * I * 2);
+  L.xP = take((size_t)L.npad * H * 2);
+  L.doutP = take((size_t)L.npad * H * 2);
+  L.total = off;
+  return L;
+}
+
+template <typename T>
+cudaError_t backward_ck_t(const ExpertsCkBwdArgs& a, char* ws, int num_sms, cudaStream_t s) {
+  const int64_t N = a.N, H = a.H, I = a.I;
+  const int E = a.E;
+  const moe_dtype dt = a.dt;
+  const CkLayout L = ck_layout(N, E, H, I);
+  uint32_t* pad = reinterpret_cast<uint32_t*>(ws + L.pad);
+  void* dgduP = ws + L.dgduP;
+  void* actP = ws + L.actP;
+  void* xP = ws + L.xP;
+  void* doutP = ws + L.doutP;
+  CUtensorMap mDo, mDo64, mDgduP, mDgduP64, mWdMN, mWgMN, mWuMN, mDgduMN, mXMN, mDoMN, mActMN;
+  if (!encode_2d(&mDo, a.dout, dt, N, H) || !encode_2d(&mDo64, a.dout, dt, N, H, 64) ||
+      !encode_2d(&mDgduP, dgduP, dt, L.npad, 2 * I) || !encode_2d(&mDgduP64, dgduP, dt, L.npad, 2 * I, 64) ||
+      !encode_3d_mn(&mWdMN, a.down, dt, E, H, I) || !encode_3d_mn(&mWgMN, a.gate, dt, E, I, H) ||
+      !encode_3d_mn(&mWuMN, a.up, dt, E, I, H) || !encode_2d_mn(&mDgduMN, dgduP, dt, L.npad, 2 * I) ||
+      !encode_2d_mn(&mXMN, xP, dt, L.npad, H) || !encode_2d_mn(&mDoMN, doutP, dt, L.npad, H) ||
+      !encode_2d_mn(&mActMN, actP, dt, L.npad, I))
+    return cudaErrorInvalidValue;
+  cudaError_t err;
+#define MOE_TC_TRY(x) \
+  if ((err = (x)) != cudaSuccess) return err
+  MOE_TC_TRY(launch_pad_offsets(a.offsets, E, pad, s));
+  auto pad_both = [&](cudaStream_t q) {
+    cudaError_t e = launch_pad_rows_mx8(a.x, a.x_scales, a.T, H, a.perm, a.k, a.offsets, pad, E, L.npad, xP, dt, q);
+    return e == cudaSuccess ? launch_pad_rows(a.dout, H, a.offsets, pad, E, L.npad, doutP, q) : e;
+  };
+  // the padded rows are needed by the weight gradients only: on a side stream
+  // they co-run with the products before (on `s` itself while it is captured)
+  SideStream side;
+  MOE_TC_TRY(side.run(s, pad_both));
+  const bool pair = N >= (int64_t)BM * E;
+  Params base{};
+  base.offsets = a.offsets;
+  base.E = E;
+  base.status = a.status;
+  base.wdt = (int)MOE_F32;
+  base.pad = pad;
+  base.half_tails = 1;
+  base.b_form = kBMNmajor3d;
+  base.cols_per_tile = 256;
+  // dg, du, a from da = dout W_down
+  Params p = base;
+  p.mode = kSwigluBwd;
+  p.k_blocks = (int)((H + BK - 1) / BK);
+  p.n_out = I;
+  p.nb = (int)((I + 255) / 256);
+  p.out = dgduP;
+  p.out2 = actP;
+  p.ck_g = const_cast<uint8_t*>(a.g);
+  p.ck_u = const_cast<uint8_t*>(a.u);
+  p.ck_gs = const_cast<uint8_t*>(a.g_scales);
+  p.ck_us = const_cast<uint8_t*>(a.u_scales);
+  MOE_TC_TRY((launch_any<T, kUse>(pair, N, E, mDo, mWdMN, mWdMN, p, num_sms, s, &mDo64)));
+  // dinput = dg W_gate + du W_up
+  const int kbI = (int)((I + BK - 1) / BK);
+  p = base;
+  p.mode = kDownPlain;
+  p.a_row_pad = 1;
+  p.kb_split = kbI;
+  p.a_k2 = (int)I;
+  p.k_blocks = 2 * kbI;
+  p.n_out = H;
+  p.nb = (int)((H + 255) / 256);
+  p.out = a.dinput;
+  MOE_TC_TRY(launch_any<T>(pair, N, E, mDgduP, mWgMN, mWuMN, p, num_sms, s, &mDgduP64));
+  // weight gradients over the padded rows
+  MOE_TC_TRY(side.join(s));
+  constexpr int TM = Cfg<2>::TILE_M;
+  p = base;
+  p.half_tails = 0;
+  p.mode = kWgrad;
+  p.wgrad = 1;
+  p.a_mn = 1;
+  p.b_form = kBMNmajor2d;
+  p.m_total = 2 * I;
+  p.split = I;
+  p.mb = (int)((2 * I + TM - 1) / TM);
+  p.n_out = H;
+  p.nb = (int)((H + 255) / 256);
+  p.out = a.dgate;
+  p.out2 = a.dup;
+  MOE_TC_TRY((launch_t<T, 2, 1, kUse>(N, E, mDgduMN, mXMN, mXMN, p, num_sms, s)));
+  p.m_total = H;
+  p.split = H;
+  p.mb = (int)((H + TM - 1) / TM);
+  p.n_out = I;
+  p.nb = (int)((I + 255) / 256);
+  p.out = a.ddown;
+  p.out2 = a.ddown;
+  MOE_TC_TRY((launch_t<T, 2, 1, kUse>(N, E, mDoMN, mActMN, mActMN, p, num_sms, s)));
+#undef MOE_TC_TRY
+  return cudaSuccess;
+}
+
 }  // namespace tc
 
 bool tc_supported(moe_dtype dt, int64_t I, int64_t H) {
@@ -1439,6 +1484,11 @@ cudaError_t launch_gemm_tc(const GemmArgs& a, const TcWeights* w, int num_sms, c
   p.status = a.status;
   p.k_blocks = (int)((a.K + tc::BK - 1) / tc::BK);
   p.half_tails = 1;
+  p.ck_g = a.ck_g;
+  p.ck_u = a.ck_u;
+  p.ck_gs = a.ck_gs;
+  p.ck_us = a.ck_us;
+  const bool save = a.ck_g != nullptr;
   p.v8_out = a.n_out % 16 == 0 && reinterpret_cast<uintptr_t>(a.out) % 32 == 0;
   // CTA pairs halve the B bytes each SM stages per k-block; they pay off when
   // experts hold at least a full 128-row tile on average.  With fewer rows per
@@ -1469,6 +1519,10 @@ cudaError_t launch_gemm_tc(const GemmArgs& a, const TcWeights* w, int num_sms, c
   }
   if (pair) {  // 128-deep k-blocks, two 64-deep sub-blocks per ring stage
     p.k_blocks = (int)((a.K + 2 * tc::BK - 1) / (2 * tc::BK));
+    if (save)
+      return a.dt == MOE_BF16
+                 ? tc::launch_t<__nv_bfloat16, 2, 2, tc::kSave>(a.N, a.E, mA, *b0, *b1, p, num_sms, s, &mA64)
+                 : tc::launch_t<__half, 2, 2, tc::kSave>(a.N, a.E, mA, *b0, *b1, p, num_sms, s, &mA64);
     if (a.dt == MOE_BF16)
       return tc::launch_t<__nv_bfloat16, 2, 2>(a.N, a.E, mA, *b0, *b1, p, num_sms, s, &mA64);
     return tc::launch_t<__half, 2, 2>(a.N, a.E, mA, *b0, *b1, p, num_sms, s, &mA64);
@@ -1476,6 +1530,10 @@ cudaError_t launch_gemm_tc(const GemmArgs& a, const TcWeights* w, int num_sms, c
   CUtensorMap mA32;
   if (!tc::encode_2d(&mA32, a.A, a.dt, (uint64_t)a.N, (uint64_t)a.K, 32)) return cudaErrorInvalidValue;
   p.thin_a = 1;
+  if (save)
+    return a.dt == MOE_BF16
+               ? tc::launch_t<__nv_bfloat16, 1, 1, tc::kSave>(a.N, a.E, mA, *b0, *b1, p, num_sms, s, &mA32)
+               : tc::launch_t<__half, 1, 1, tc::kSave>(a.N, a.E, mA, *b0, *b1, p, num_sms, s, &mA32);
   if (a.dt == MOE_BF16) return tc::launch_t<__nv_bfloat16, 1>(a.N, a.E, mA, *b0, *b1, p, num_sms, s, &mA32);
   return tc::launch_t<__half, 1>(a.N, a.E, mA, *b0, *b1, p, num_sms, s, &mA32);
 }
@@ -1489,6 +1547,16 @@ cudaError_t launch_experts_backward_tc(const ExpertsBwdArgs& a, const TcWeights*
   char* base = static_cast<char*>(ws);
   if (a.dt == MOE_BF16) return tc::backward_t<__nv_bfloat16>(a, w, base, num_sms, s);
   return tc::backward_t<__half>(a, w, base, num_sms, s);
+}
+
+size_t experts_backward_ck_workspace(int64_t N, int E, int64_t H, int64_t I) {
+  return tc::ck_layout(N, E, H, I).total;
+}
+
+cudaError_t launch_experts_backward_ck(const ExpertsCkBwdArgs& a, void* ws, int num_sms, cudaStream_t s) {
+  char* base = static_cast<char*>(ws);
+  if (a.dt == MOE_BF16) return tc::backward_ck_t<__nv_bfloat16>(a, base, num_sms, s);
+  return tc::backward_ck_t<__half>(a, base, num_sms, s);
 }
 
 }  // namespace moe

@@ -123,6 +123,54 @@ cudaError_t launch_distill_loss_backward(const DistillBwdArgs& d, cudaStream_t s
 cudaError_t launch_distill_targets(const void* logits, moe_dtype dt, int64_t T, int E, int m, float temperature,
                                    uint32_t* idx, void* top, float* rest, cudaStream_t s);
 
+// ---- microscaled rows (mx.cu) ------------------------------------------------
+cudaError_t launch_mx_quantize(const void* x, moe_dtype dt, int64_t R, int64_t C, moe_mx_format fmt,
+                               uint8_t* values, uint8_t* scales, cudaStream_t s);
+// n output rows: row r of the R held ones, or row perm[r] / k (zero past R)
+cudaError_t launch_mx_dequantize(const uint8_t* values, const uint8_t* scales, moe_mx_format fmt, int64_t R,
+                                 int64_t C, const uint32_t* perm, int k, int64_t n, void* out, moe_dtype dt,
+                                 cudaStream_t s);
+// 16-bit rows to e2m1 in dispatch order, scales in the order of the products
+// (slot_row: source row t goes to rows slot_row[t k + j]; else rows are in order)
+cudaError_t launch_mx4_rows(const void* x, moe_dtype dt, int64_t rows, int64_t C, const uint32_t* slot_row, int k,
+                            const uint32_t* offsets, int E, uint8_t* values, uint8_t* scales, cudaStream_t s);
+// weight scales [E, rows, C/32] in the order of the products (s1: up beside gate)
+cudaError_t launch_mx4_weight_scales(const uint8_t* s0, const uint8_t* s1, int64_t E, int64_t rows, int64_t C,
+                                     int64_t pieces, uint8_t* out, cudaStream_t s);
+cudaError_t launch_slot_sum_f32(const float* slots, int64_t T, int k, int64_t H, void* y, moe_dtype dt,
+                                cudaStream_t s);
+
+// ---- 4-bit experts (gemm_mx4.cu) ----------------------------------------------
+struct Mx4Weights;  // prebuilt tensor maps of one 4-bit expert-weight set
+// gate, up [E,I,H/2] and down [E,H,I/2] packed; sgu, sd: scales in product order
+Mx4Weights* mx4_weights_create(const void* gate, const void* up, const void* down, const void* sgu, const void* sd,
+                               int64_t E, int64_t I, int64_t H, const char** err);
+void mx4_weights_destroy(Mx4Weights* w);
+// bytes of the re-ordered scales of gate and up together, and of down
+size_t mx4_gate_up_scale_bytes(int64_t E, int64_t I, int64_t H);
+size_t mx4_down_scale_bytes(int64_t E, int64_t I, int64_t H);
+int64_t mx4_gate_up_pieces(int64_t I);
+int64_t mx4_down_pieces(int64_t H);
+// bytes of the scales of N activation rows of C values in product order
+size_t mx4_row_scale_bytes(int64_t N, int64_t E, int64_t C);
+struct Mx4Args {
+  bool gate_up;             // h = silu(g) u, in 4 bits (hq, hs); else out = A . W_down^T
+  int E;
+  int64_t N, I, H;
+  const void* a;            // packed rows [N, K/2]
+  const void* a_scales;
+  const uint32_t* offsets;
+  void* hq;
+  void* hs;
+  void* out;                // [N, H] in dt, or FP32 slots [T*k, H] (perm given)
+  moe_dtype dt;
+  const uint32_t* perm;     // with weights: row r goes to slot perm[r], times its weight
+  const void* weights;
+  moe_dtype wdt;
+  uint32_t* status;
+};
+cudaError_t launch_gemm_mx4(const Mx4Args& a, const Mx4Weights* w, int num_sms, cudaStream_t s);
+
 // ---- combine (combine.cu) --------------------------------------------------
 cudaError_t launch_invert_perm(const uint32_t* perm, int64_t N, uint32_t* slot_row, cudaStream_t s);
 cudaError_t launch_combine(const void* expert_out, moe_dtype dt, const uint32_t* slot_row,
@@ -162,6 +210,11 @@ struct GemmArgs {
   const void* weights;
   moe_dtype wdt;
   uint32_t* status;
+  // gate/up of the tcgen05 path: also hold g and u in 8 bits (mx.cuh), or null
+  uint8_t* ck_g;
+  uint8_t* ck_u;
+  uint8_t* ck_gs;
+  uint8_t* ck_us;
 };
 
 // Backward of the SwiGLU experts (gemm_bwd.cu): FP32 accumulate, any dtype.
@@ -197,6 +250,11 @@ cudaError_t launch_pad_offsets(const uint32_t* offsets, int E, uint32_t* pad, cu
 cudaError_t launch_pad_rows(const void* src, int64_t C, const uint32_t* offsets, const uint32_t* pad,
                             int E, int64_t npad_max, void* dst, cudaStream_t s);
 
+// the same from 8-bit tokens: dispatched row r is token perm[r] / k (zeros past T)
+cudaError_t launch_pad_rows_mx8(const uint8_t* x, const uint8_t* scales, int64_t T, int64_t C, const uint32_t* perm,
+                                int k, const uint32_t* offsets, const uint32_t* pad, int E, int64_t npad_max,
+                                void* dst, moe_dtype dt, cudaStream_t s);
+
 // SIMT FP32-accumulate path (gemm_simt.cu): any dtype and shape
 cudaError_t launch_gemm_simt(const GemmArgs& a, cudaStream_t s);
 
@@ -213,6 +271,32 @@ bool tc_supported(moe_dtype dt, int64_t I, int64_t H);
 size_t experts_backward_tc_workspace(int64_t N, int E, int64_t H, int64_t I);
 cudaError_t launch_experts_backward_tc(const ExpertsBwdArgs& a, const TcWeights* w, void* ws,
                                        int num_sms, cudaStream_t s);
+// Expert backward from 8-bit checkpoints (F16/BF16, tcgen05); weight gradients
+// in dt; scratch of experts_backward_ck_workspace(...) bytes, 1024-byte aligned
+struct ExpertsCkBwdArgs {
+  moe_dtype dt;
+  int E, k;
+  int64_t T, N, H, I;
+  const uint8_t* x;         // e4m3 tokens [T, H]
+  const uint8_t* x_scales;  // [T, ceil(H/32)]
+  const uint32_t* perm;
+  const uint32_t* offsets;
+  const uint8_t* g;         // e4m3 [N, I]
+  const uint8_t* g_scales;  // [N, ceil(I/32)]
+  const uint8_t* u;
+  const uint8_t* u_scales;
+  const void* dout;
+  const void* gate;
+  const void* up;
+  const void* down;
+  void* dinput;
+  void* dgate;
+  void* dup;
+  void* ddown;
+  uint32_t* status;
+};
+size_t experts_backward_ck_workspace(int64_t N, int E, int64_t H, int64_t I);
+cudaError_t launch_experts_backward_ck(const ExpertsCkBwdArgs& a, void* ws, int num_sms, cudaStream_t s);
 // a kernel whose bounded wait is made to expire (failure-path self-test)
 cudaError_t launch_bounded_wait_selftest(uint32_t* status, uint64_t limit_ns, cudaStream_t s);
 

@@ -1,0 +1,444 @@
+// mx.cu -- rows to microscaled (MX) form and back (the format: mx.cuh), and the
+// re-ordering of scale bytes for the block-scaled products (gemm_mx4.cu).
+//
+// Each of these kernels is bound by memory: every input is read once and every
+// output written once, a few operations a value between.  Where rows are whole
+// blocks and the pointers are aligned, blocks lie one behind the other in all
+// three tensors and rows do not matter: four lanes share a block (8 values
+// each), a warp holds 32 blocks.  Other rows take a warp per row and a lane per
+// value.
+#include "common.cuh"
+#include "internal.h"
+#include "mx.cuh"
+
+namespace moe {
+namespace {
+
+// 8 consecutive values as FP32 (16-byte aligned)
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, float* v) {
+  if constexpr (sizeof(T) == 4) {
+    const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  } else {
+    unpack8<T>(*reinterpret_cast<const uint4*>(p), v);
+  }
+}
+template <typename T>
+__device__ __forceinline__ void store8(T* p, const float* v) {
+  if constexpr (sizeof(T) == 4) {
+    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+    *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
+  } else {
+    *reinterpret_cast<uint4*>(p) = pack8<T>(v);
+  }
+}
+
+__device__ __forceinline__ uint32_t max8(const float* v) {
+  uint32_t a = mx::abs_bits(v[0]);
+#pragma unroll
+  for (int i = 1; i < 8; ++i) a = max(a, mx::abs_bits(v[i]));
+  return a;
+}
+// 8 values over the scale of byte b, as elements (uint32 for e2m1, uint2 for e4m3)
+template <int FMT>
+__device__ __forceinline__ uint2 encode8(const float* v, uint32_t b) {
+  const float inv = mx::inverse_scale(b);
+  float q[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) q[i] = b == 255u ? 0.f : v[i] * inv;
+  if constexpr (FMT == MOE_MXFP4) return make_uint2(mx::to_e2m1x8(q), 0u);
+  else return make_uint2(mx::to_e4m3x4(q), mx::to_e4m3x4(q + 4));
+}
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+
+// whole blocks: warp w takes blocks 32 w .. 32 w + 31 (1024 values), four loads
+// of 8 values a lane in flight
+template <typename T, int FMT>
+__global__ void __launch_bounds__(kThreads)
+mx_quantize_blocks(const T* __restrict__ x, int64_t blocks, uint8_t* __restrict__ values,
+                   uint8_t* __restrict__ scales) {
+  const int lane = threadIdx.x & 31;
+  const int64_t b0 = ((int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5)) * 32;
+  if (b0 >= blocks) return;
+  const int64_t n8 = blocks * 4;        // groups of 8 values
+  const int64_t g0 = b0 * 4 + lane;
+  float v[4][8];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int64_t g = g0 + 32 * j;
+    if (g < n8) load8(x + g * 8, v[j]);
+    else
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[j][i] = 0.f;
+  }
+  uint32_t mine = 0;  // the byte of block b0 + lane
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    uint32_t a = max8(v[j]);
+    a = max(a, __shfl_xor_sync(0xffffffffu, a, 1));
+    a = max(a, __shfl_xor_sync(0xffffffffu, a, 2));
+    const uint32_t b = mx::scale_byte<FMT>(a);
+    const int64_t g = g0 + 32 * j;
+    const uint2 q = encode8<FMT>(v[j], b);
+    if (g < n8) {
+      if constexpr (FMT == MOE_MXFP4) reinterpret_cast<uint32_t*>(values)[g] = q.x;
+      else reinterpret_cast<uint2*>(values)[g] = q;
+    }
+    const uint32_t o = __shfl_sync(0xffffffffu, b, (lane & 7) * 4);
+    if (lane >> 3 == j) mine = o;
+  }
+  if (b0 + lane < blocks) scales[b0 + lane] = (uint8_t)mine;
+}
+
+// any row length and alignment: a warp per row, a lane per value of a block
+template <typename T, int FMT>
+__global__ void __launch_bounds__(kThreads)
+mx_quantize_rows(const T* __restrict__ x, int64_t R, int64_t C, uint8_t* __restrict__ values,
+                 uint8_t* __restrict__ scales) {
+  const int lane = threadIdx.x & 31;
+  const int64_t r = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  if (r >= R) return;
+  const T* xr = x + r * C;
+  const int64_t nb = (C + 31) / 32;
+  uint8_t* sr = scales + r * nb;
+  uint8_t* vr = values + r * (FMT == MOE_MXFP4 ? (C + 1) / 2 : C);
+  constexpr int U = 4;  // blocks in flight
+  for (int64_t b0 = 0; b0 < nb; b0 += U) {
+    float v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t c = (b0 + u) * 32 + lane;
+      v[u] = c < C ? to_f32<T>(xr[c]) : 0.f;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t c = (b0 + u) * 32 + lane;
+      const uint32_t a = __reduce_max_sync(0xffffffffu, mx::abs_bits(v[u]));
+      const uint32_t b = mx::scale_byte<FMT>(a);
+      const float q[4] = {b == 255u ? 0.f : v[u] * mx::inverse_scale(b), 0.f, 0.f, 0.f};
+      if constexpr (FMT == MOE_MXFP8) {
+        if (c < C) vr[c] = (uint8_t)mx::to_e4m3x4(q);
+      } else {
+        const float q1 = __shfl_down_sync(0xffffffffu, q[0], 1);
+        const float both[8] = {q[0], q1, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        if (c < C && (lane & 1) == 0) vr[c >> 1] = (uint8_t)mx::to_e2m1x8(both);
+      }
+      if (b0 + u < nb && lane == 0) sr[b0 + u] = (uint8_t)b;
+    }
+  }
+}
+
+template <int FMT>
+__device__ __forceinline__ void decode8(const uint8_t* values, int64_t g, uint32_t b, float* v) {
+  if constexpr (FMT == MOE_MXFP4) {
+    mx::from_e2m1x8(__ldg(reinterpret_cast<const uint32_t*>(values) + g), v);
+  } else {
+    const uint2 q = __ldg(reinterpret_cast<const uint2*>(values) + g);
+    mx::from_e4m3x4(q.x, v);
+    mx::from_e4m3x4(q.y, v + 4);
+  }
+  const float s = mx::scale_value(b);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] *= s;
+}
+
+// whole blocks, in order: four groups of 8 values a lane
+template <typename T, int FMT>
+__global__ void __launch_bounds__(kThreads)
+mx_dequantize_blocks(const uint8_t* __restrict__ values, const uint8_t* __restrict__ scales, int64_t blocks,
+                     T* __restrict__ out) {
+  const int64_t n8 = blocks * 4;
+  const int64_t g0 = (int64_t)blockIdx.x * kThreads * 4 + threadIdx.x;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int64_t g = g0 + (int64_t)kThreads * j;
+    if (g < n8) {
+      float v[8];
+      decode8<FMT>(values, g, __ldg(scales + (g >> 2)), v);
+      store8(out + g * 8, v);
+    }
+  }
+}
+
+// rows of whole blocks through a dispatch map: output row r is row perm[r] / k,
+// zero where perm[r] names none
+template <typename T, int FMT>
+__global__ void __launch_bounds__(kThreads)
+mx_dequantize_gather(const uint8_t* __restrict__ values, const uint8_t* __restrict__ scales, int64_t R, int64_t C,
+                     const uint32_t* __restrict__ perm, uint32_t k, int64_t n, T* __restrict__ out) {
+  const int lane = threadIdx.x & 31;
+  const int64_t r = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  if (r >= n) return;
+  const int64_t src = (int64_t)(__ldg(perm + r) / k);
+  const int64_t g8 = C / 8;
+  T* o = out + r * C;
+  if (src >= R) {
+    const float z[8] = {};
+    for (int64_t g = lane; g < g8; g += 32) store8(o + g * 8, z);
+    return;
+  }
+#pragma unroll 4
+  for (int64_t g = lane; g < g8; g += 32) {
+    float v[8];
+    decode8<FMT>(values, src * g8 + g, __ldg(scales + src * (C / 32) + (g >> 2)), v);
+    store8(o + g * 8, v);
+  }
+}
+
+// any row length and alignment, with or without a map
+template <typename T, int FMT>
+__global__ void __launch_bounds__(kThreads)
+mx_dequantize_rows(const uint8_t* __restrict__ values, const uint8_t* __restrict__ scales, int64_t R, int64_t C,
+                   const uint32_t* __restrict__ perm, uint32_t k, int64_t n, T* __restrict__ out) {
+  const int lane = threadIdx.x & 31;
+  const int64_t r = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  if (r >= n) return;
+  const int64_t src = perm ? (int64_t)(__ldg(perm + r) / k) : r;
+  const int64_t nb = (C + 31) / 32, vb = FMT == MOE_MXFP4 ? (C + 1) / 2 : C;
+  T* o = out + r * C;
+#pragma unroll 4
+  for (int64_t c = lane; c < C; c += 32) {
+    float f = 0.f;
+    if (src < R) {
+      const float s = mx::scale_value(__ldg(scales + src * nb + (c >> 5)));
+      float v[8];
+      if constexpr (FMT == MOE_MXFP4) {
+        mx::from_e2m1x8((uint32_t)__ldg(values + src * vb + (c >> 1)) >> (4 * (c & 1)), v);
+      } else {
+        mx::from_e4m3x4((uint32_t)__ldg(values + src * vb + c), v);
+      }
+      f = v[0] * s;
+    }
+    o[c] = from_f32<T>(f);
+  }
+}
+
+// ---- activations of the 4-bit products ---------------------------------------
+// 256-row units of experts < e (ceil per expert): expert e's scale pieces begin
+// at twice that.  One block; s_off [E+1] is filled, s_unit [E+1] written.
+__device__ __forceinline__ void unit_starts(const uint32_t* s_off, int E, uint32_t* s_unit) {
+  if (threadIdx.x < 32) {
+    const int lane = threadIdx.x, per = (E + 31) / 32;
+    uint32_t loc = 0;
+    for (int i = 0; i < per; ++i) {
+      const int e = lane * per + i;
+      if (e < E) loc += (s_off[e + 1] - s_off[e] + 255u) >> 8;
+    }
+    uint32_t incl = loc;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const uint32_t o = __shfl_up_sync(0xffffffffu, incl, d);
+      if (lane >= d) incl += o;
+    }
+    uint32_t run = incl - loc;
+    for (int i = 0; i < per; ++i) {
+      const int e = lane * per + i;
+      if (e < E) {
+        s_unit[e] = run;
+        run += (s_off[e + 1] - s_off[e] + 255u) >> 8;
+      }
+    }
+    if (lane == 31) s_unit[E] = incl;
+  }
+}
+
+// Rows of C values (C a multiple of 32) to e2m1 in dispatch order, scales in
+// the order of the products.  A warp per source row; a lane holds 8 values of
+// each 256.  With slot_row, source row t goes to the dispatch rows
+// slot_row[t k + j]: a token is read and rounded once however many experts it
+// goes to.
+template <typename T>
+__global__ void __launch_bounds__(kThreads)
+mx4_rows_kernel(const T* __restrict__ x, int64_t rows, int64_t C, const uint32_t* __restrict__ slot_row, int k,
+                const uint32_t* __restrict__ offsets, int E, uint8_t* __restrict__ values,
+                uint8_t* __restrict__ scales) {
+  extern __shared__ uint32_t s_mem[];
+  uint32_t* s_off = s_mem;
+  uint32_t* s_unit = s_mem + E + 1;
+  pdl_wait();
+  pdl_trigger();
+  for (int i = threadIdx.x; i <= E; i += kThreads) s_off[i] = offsets[i];
+  __syncthreads();
+  unit_starts(s_off, E, s_unit);
+  __syncthreads();
+  const int lane = threadIdx.x & 31;
+  const int64_t src = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  if (src >= rows) return;
+  const int64_t steps = mx::depth_steps(C), vb = C / 2;
+  const uint32_t first = s_off[0], last = s_off[E];
+  for (int64_t st0 = 0; st0 < steps; st0 += 4) {
+    uint32_t q[4], w[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int64_t c = (st0 + u) * 256 + lane * 8;
+      float v[8];
+      if (c < C) load8(x + src * C + c, v);
+      else
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = 0.f;
+      uint32_t a = max8(v);
+      a = max(a, __shfl_xor_sync(0xffffffffu, a, 1));
+      a = max(a, __shfl_xor_sync(0xffffffffu, a, 2));
+      const uint32_t b = mx::scale_byte<MOE_MXFP4>(a);
+      q[u] = encode8<MOE_MXFP4>(v, b).x;
+      uint32_t word = b << (8 * ((lane >> 2) & 3));  // four blocks of 16 lanes in one word
+      word |= __shfl_xor_sync(0xffffffffu, word, 4);
+      word |= __shfl_xor_sync(0xffffffffu, word, 8);
+      w[u] = word;
+    }
+    for (int j = 0; j < k; ++j) {
+      const uint32_t r = slot_row ? __ldg(slot_row + src * k + j) : (uint32_t)src;
+      if (r < first || r >= last) continue;
+      int lo = 0, hi = E;  // s_off[lo] <= r < s_off[hi]
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (s_off[mid] <= r) lo = mid; else hi = mid;
+      }
+      const uint32_t local = r - s_off[lo];
+      uint8_t* vr = values + (int64_t)r * vb;
+      uint8_t* sr = scales + ((int64_t)(2 * s_unit[lo] + (local >> 7)) * steps + st0) * 1024 +
+                    mx::pair_byte(local & 127u, (uint32_t)(lane >> 4) * 4u);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int64_t c = (st0 + u) * 256 + lane * 8;
+        if (c < C) *reinterpret_cast<uint32_t*>(vr + c / 2) = q[u];
+        if (st0 + u < steps && (lane & 15) == 0) *reinterpret_cast<uint32_t*>(sr + u * 1024) = w[u];
+      }
+    }
+  }
+}
+
+// Weight scales [E, rows, C/32] (two such tensors, interleaved by 32 rows, for
+// gate and up) in the order of the products: [E][step][128-row piece] pairs.
+// A thread per (expert, step, row of a piece, half of a pair).
+__global__ void __launch_bounds__(kThreads)
+mx4_weight_scales_kernel(const uint8_t* __restrict__ s0, const uint8_t* __restrict__ s1, int64_t E, int64_t rows,
+                         int64_t C, int64_t steps, int64_t pieces, uint8_t* __restrict__ out) {
+  const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  if (i >= E * steps * pieces * 256) return;
+  const uint32_t half = (uint32_t)(i & 1), r = (uint32_t)(i >> 1) & 127u;
+  const int64_t pair = i >> 8;  // (e * steps + step) * pieces + piece
+  const int64_t piece = pair % pieces, step = pair / pieces % steps, e = pair / pieces / steps;
+  int64_t n = piece * 128 + r;  // row of the product's operand
+  const uint8_t* s = s0;
+  if (s1) {  // 32-row groups: gate, up, gate, up ...
+    const int64_t grp = n >> 5;
+    if (grp & 1) s = s1;
+    n = (grp >> 1) * 32 + (n & 31);
+  }
+  const int64_t nb = C / 32, c0 = step * 8 + half * 4;
+  uint32_t w = 0;
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    const uint32_t b = n < rows && c0 + c < nb ? s[(e * rows + n) * nb + c0 + c] : 127u;
+    w |= b << (8 * c);
+  }
+  *reinterpret_cast<uint32_t*>(out + pair * 1024 + mx::pair_byte(r, half * 4u)) = w;
+}
+
+// y[t] = sum_j slots[t k + j] (FP32, ascending j), rounded once
+template <typename T>
+__global__ void __launch_bounds__(kThreads)
+slot_sum_f32_kernel(const float* __restrict__ slots, int64_t T_, int k, int64_t H, T* __restrict__ y) {
+  pdl_wait();
+  pdl_trigger();
+  const int64_t g8 = H / 8;
+  const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  if (i >= T_ * g8) return;
+  const int64_t t = i / g8, c = (i - t * g8) * 8;
+  float acc[8] = {};
+  const float* s = slots + t * k * H + c;
+#pragma unroll 4
+  for (int j = 0; j < k; ++j, s += H) {
+    float v[8];
+    load8(s, v);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) acc[q] += v[q];
+  }
+  store8(y + t * H + c, acc);
+}
+
+template <typename T, int FMT>
+cudaError_t quantize_t(const void* x, int64_t R, int64_t C, uint8_t* values, uint8_t* scales, cudaStream_t s) {
+  const T* xp = static_cast<const T*>(x);
+  if (C % 32 == 0 && (reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(values)) % 16 == 0) {
+    const int64_t blocks = R * (C / 32);
+    const int64_t grid = (blocks + 32 * kWarps - 1) / (32 * kWarps);
+    mx_quantize_blocks<T, FMT><<<(unsigned)grid, kThreads, 0, s>>>(xp, blocks, values, scales);
+  } else {
+    mx_quantize_rows<T, FMT><<<(unsigned)((R + kWarps - 1) / kWarps), kThreads, 0, s>>>(xp, R, C, values, scales);
+  }
+  return cudaGetLastError();
+}
+
+template <typename T, int FMT>
+cudaError_t dequantize_t(const uint8_t* values, const uint8_t* scales, int64_t R, int64_t C, const uint32_t* perm,
+                         int k, int64_t n, void* out, cudaStream_t s) {
+  T* o = static_cast<T*>(out);
+  const unsigned by_row = (unsigned)((n + kWarps - 1) / kWarps);
+  const bool whole = C % 32 == 0 && (reinterpret_cast<uintptr_t>(out) | reinterpret_cast<uintptr_t>(values)) % 16 == 0;
+  if (whole && !perm) {
+    const int64_t blocks = R * (C / 32), per = kThreads;  // 4 groups a thread, 4 groups a block
+    mx_dequantize_blocks<T, FMT><<<(unsigned)((blocks + per - 1) / per), kThreads, 0, s>>>(values, scales, blocks, o);
+  } else if (whole) {
+    mx_dequantize_gather<T, FMT><<<by_row, kThreads, 0, s>>>(values, scales, R, C, perm, (uint32_t)k, n, o);
+  } else {
+    mx_dequantize_rows<T, FMT><<<by_row, kThreads, 0, s>>>(values, scales, R, C, perm, (uint32_t)k, n, o);
+  }
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+#define MOE_MX_DISPATCH(fn, ...)                                                                             \
+  (dt == MOE_F32 ? (fmt == MOE_MXFP4 ? fn<float, MOE_MXFP4>(__VA_ARGS__) : fn<float, MOE_MXFP8>(__VA_ARGS__)) \
+   : dt == MOE_F16                                                                                           \
+       ? (fmt == MOE_MXFP4 ? fn<__half, MOE_MXFP4>(__VA_ARGS__) : fn<__half, MOE_MXFP8>(__VA_ARGS__))        \
+       : (fmt == MOE_MXFP4 ? fn<__nv_bfloat16, MOE_MXFP4>(__VA_ARGS__) : fn<__nv_bfloat16, MOE_MXFP8>(__VA_ARGS__)))
+
+cudaError_t launch_mx_quantize(const void* x, moe_dtype dt, int64_t R, int64_t C, moe_mx_format fmt,
+                               uint8_t* values, uint8_t* scales, cudaStream_t s) {
+  return MOE_MX_DISPATCH(quantize_t, x, R, C, values, scales, s);
+}
+
+cudaError_t launch_mx_dequantize(const uint8_t* values, const uint8_t* scales, moe_mx_format fmt, int64_t R,
+                                 int64_t C, const uint32_t* perm, int k, int64_t n, void* out, moe_dtype dt,
+                                 cudaStream_t s) {
+  return MOE_MX_DISPATCH(dequantize_t, values, scales, R, C, perm, k, n, out, s);
+}
+#undef MOE_MX_DISPATCH
+
+cudaError_t launch_mx4_rows(const void* x, moe_dtype dt, int64_t rows, int64_t C, const uint32_t* slot_row, int k,
+                            const uint32_t* offsets, int E, uint8_t* values, uint8_t* scales, cudaStream_t s) {
+  const unsigned grid = (unsigned)((rows + kWarps - 1) / kWarps);
+  const size_t smem = 8 * (size_t)(E + 1);
+  if (!slot_row) k = 1;
+  return dt == MOE_BF16 ? launch_pdl(mx4_rows_kernel<__nv_bfloat16>, dim3(grid), dim3(kThreads), smem, s,
+                                     static_cast<const __nv_bfloat16*>(x), rows, C, slot_row, k, offsets, E, values,
+                                     scales)
+                        : launch_pdl(mx4_rows_kernel<__half>, dim3(grid), dim3(kThreads), smem, s,
+                                     static_cast<const __half*>(x), rows, C, slot_row, k, offsets, E, values, scales);
+}
+
+cudaError_t launch_mx4_weight_scales(const uint8_t* s0, const uint8_t* s1, int64_t E, int64_t rows, int64_t C,
+                                     int64_t pieces, uint8_t* out, cudaStream_t s) {
+  const int64_t steps = mx::depth_steps(C), n = E * steps * pieces * 256;
+  mx4_weight_scales_kernel<<<(unsigned)((n + kThreads - 1) / kThreads), kThreads, 0, s>>>(s0, s1, E, rows, C, steps,
+                                                                                         pieces, out);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_slot_sum_f32(const float* slots, int64_t T, int k, int64_t H, void* y, moe_dtype dt,
+                                cudaStream_t s) {
+  const unsigned grid = (unsigned)((T * (H / 8) + kThreads - 1) / kThreads);
+  return dt == MOE_BF16 ? launch_pdl(slot_sum_f32_kernel<__nv_bfloat16>, dim3(grid), dim3(kThreads), 0, s, slots, T,
+                                     k, H, static_cast<__nv_bfloat16*>(y))
+                        : launch_pdl(slot_sum_f32_kernel<__half>, dim3(grid), dim3(kThreads), 0, s, slots, T, k, H,
+                                     static_cast<__half*>(y));
+}
+
+}  // namespace moe

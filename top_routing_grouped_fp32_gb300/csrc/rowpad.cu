@@ -13,6 +13,7 @@
 //    C a multiple of 8, copied in 16-byte vectors: one warp per row).
 #include "common.cuh"
 #include "internal.h"
+#include "mx.cuh"
 
 namespace moe {
 namespace {
@@ -105,7 +106,60 @@ pad_rows_kernel(const uint4* __restrict__ src, int64_t vecs, const uint32_t* __r
   }
 }
 
+// pad_rows of 8-bit tokens (e4m3, a scale a 32-column block), read through the
+// dispatch map and written as T: a warp per row, 8 values a lane.
+template <typename T>
+__global__ void __launch_bounds__(32 * kRowsPerBlock)
+pad_rows_mx8_kernel(const uint2* __restrict__ x, const uint8_t* __restrict__ scales, int64_t tokens, int64_t vecs,
+                    const uint32_t* __restrict__ perm, uint32_t k, const uint32_t* __restrict__ offsets,
+                    const uint32_t* __restrict__ pad, int E, uint4* __restrict__ dst) {
+  const int64_t j = (int64_t)blockIdx.x * kRowsPerBlock + (threadIdx.x >> 5);  // padded row
+  const int lane = threadIdx.x & 31;
+  if (j >= (int64_t)pad[E]) return;
+  int lo = 0, hi = E;  // pad[lo] <= j < pad[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if ((int64_t)pad[mid] <= j) lo = mid; else hi = mid;
+  }
+  const int64_t r = (int64_t)offsets[lo] + (j - (int64_t)pad[lo]);
+  uint4* d = dst + j * vecs;
+  int64_t t = tokens;
+  if (r < (int64_t)offsets[lo + 1]) t = (int64_t)(__ldg(perm + r) / k);
+  if (t < tokens) {
+    const uint2* s = x + t * vecs;
+    const uint8_t* sc = scales + t * ((vecs + 3) / 4);
+#pragma unroll 4
+    for (int64_t v = lane; v < vecs; v += 32) {
+      const uint2 q = __ldg(s + v);
+      const float f = mx::scale_value(__ldg(sc + (v >> 2)));
+      float o[8];
+      mx::from_e4m3x4(q.x, o);
+      mx::from_e4m3x4(q.y, o + 4);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) o[i] *= f;
+      d[v] = pack8<T>(o);
+    }
+  } else {
+    for (int64_t v = lane; v < vecs; v += 32) d[v] = make_uint4(0u, 0u, 0u, 0u);
+  }
+}
+
 }  // namespace
+
+cudaError_t launch_pad_rows_mx8(const uint8_t* x, const uint8_t* scales, int64_t T, int64_t C, const uint32_t* perm,
+                                int k, const uint32_t* offsets, const uint32_t* pad, int E, int64_t npad_max,
+                                void* dst, moe_dtype dt, cudaStream_t s) {
+  const unsigned blocks = (unsigned)((npad_max + kRowsPerBlock - 1) / kRowsPerBlock);
+  const uint2* xp = reinterpret_cast<const uint2*>(x);
+  uint4* dp = static_cast<uint4*>(dst);
+  if (dt == MOE_BF16)
+    pad_rows_mx8_kernel<__nv_bfloat16><<<blocks, 32 * kRowsPerBlock, 0, s>>>(xp, scales, T, C / 8, perm, (uint32_t)k,
+                                                                            offsets, pad, E, dp);
+  else
+    pad_rows_mx8_kernel<__half><<<blocks, 32 * kRowsPerBlock, 0, s>>>(xp, scales, T, C / 8, perm, (uint32_t)k, offsets,
+                                                                     pad, E, dp);
+  return cudaGetLastError();
+}
 
 cudaError_t launch_sanitize_offsets(const uint32_t* offsets, int E, int64_t N, uint32_t* out,
                                    uint32_t* status, cudaStream_t s) {
