@@ -173,7 +173,7 @@ moe_status moe_mx_dequantize(const uint8_t* values, const uint8_t* scales, moe_m
 // ---- 4-bit experts -----------------------------------------------------------
 size_t moe_mx4_experts_scale_bytes(int64_t E, int64_t I, int64_t H) {
   if (E < 1 || E > kMaxE || I < 1 || I > kMaxDim || H < 1 || H > kMaxDim) return 0;
-  return moe::mx4_gate_up_scale_bytes(E, I, H) + moe::mx4_down_scale_bytes(E, I, H);
+  return 2 * moe::mx4_weight_scale_bytes(E * I, H) + moe::mx4_weight_scale_bytes(E * H, I);
 }
 
 moe_status moe_mx4_experts_create(const uint8_t* gate, const uint8_t* gate_scales, const uint8_t* up,
@@ -190,9 +190,6 @@ moe_status moe_mx4_experts_create(const uint8_t* gate, const uint8_t* gate_scale
   if (I % 32 != 0 || H % 32 != 0)
     return fail(MOE_ERR_UNSUPPORTED, "4-bit experts need H and I in whole blocks of 32 (I=%lld H=%lld)", (long long)I,
                 (long long)H);
-  // coordinates of the scale maps are 32-bit
-  if (moe_mx4_experts_scale_bytes(E, I, H) / 1024 > (size_t)INT32_MAX)
-    return fail(MOE_ERR_UNSUPPORTED, "expert weight element count is too large");
   if (!gate || !up || !down || !gate_scales || !up_scales || !down_scales)
     return fail(MOE_ERR_INVALID_ARG, "gate, up, down and their scales must be non-NULL");
   if (!aligned16(gate) || !aligned16(up) || !aligned16(down))
@@ -213,16 +210,16 @@ moe_status moe_mx4_experts_create(const uint8_t* gate, const uint8_t* gate_scale
   }
   int sms = 0;
   MOE_TRY_CUDA(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev), "cudaDeviceGetAttribute");
-  uint8_t* sgu = static_cast<uint8_t*>(buffer);
-  uint8_t* sd = sgu + moe::mx4_gate_up_scale_bytes(E, I, H);
+  uint8_t* sg = static_cast<uint8_t*>(buffer);
+  uint8_t* su = sg + moe::mx4_weight_scale_bytes(E * I, H);
+  uint8_t* sd = su + moe::mx4_weight_scale_bytes(E * I, H);
   const char* err = "";
-  moe::Mx4Weights* w = moe::mx4_weights_create(gate, up, down, sgu, sd, E, I, H, &err);
+  moe::Mx4Weights* w = moe::mx4_weights_create(gate, up, down, sg, su, sd, E, I, H, &err);
   if (!w) return fail(MOE_ERR_CUDA, "%s", err);
   moe_mx4_experts* x = new (std::nothrow) moe_mx4_experts{dt, E, I, H, dev, sms, w};
-  cudaError_t e = x ? moe::launch_mx4_weight_scales(gate_scales, up_scales, E, I, H, moe::mx4_gate_up_pieces(I), sgu, stream)
-                    : cudaErrorMemoryAllocation;
-  if (e == cudaSuccess)
-    e = moe::launch_mx4_weight_scales(down_scales, nullptr, E, H, I, moe::mx4_down_pieces(H), sd, stream);
+  cudaError_t e = x ? moe::launch_mx4_weight_scales(gate_scales, E, I, H, sg, stream) : cudaErrorMemoryAllocation;
+  if (e == cudaSuccess) e = moe::launch_mx4_weight_scales(up_scales, E, I, H, su, stream);
+  if (e == cudaSuccess) e = moe::launch_mx4_weight_scales(down_scales, E, H, I, sd, stream);
   if (e != cudaSuccess) {
     moe::mx4_weights_destroy(w);
     delete x;

@@ -16,23 +16,34 @@
 // The kernel is the segmented, persistent one of the 16-bit products (tiles
 // visited expert by expert, a TMA warp, an MMA thread, four epilogue warps,
 // two accumulators, bounded waits), with these differences:
-//   * a 128-byte swizzled row holds 256 values, so a ring stage is 256 deep;
-//   * scales travel with their stage: one kilobyte for 128 rows, copied from
-//     shared memory to TMEM (tcgen05.cp, 32 lanes by 16 bytes, replicated to
-//     the four lane quarters) by the thread that issues the MMAs, in order
-//     with them.  Two sets of scale columns are used in turn;
+//   * a 128-byte swizzled row holds 256 values, so a ring slot is 256 deep, and
+//     its four MMAs take about 400 cycles: what the issuing thread does between
+//     them counts.  Slots are therefore filled and freed one by one but handed
+//     over in pairs (512 columns, a span): one wait for eight MMAs.  The TMA and
+//     the MMA warp run their loops as whole warps and elect a lane to issue, so
+//     that operands are known to be uniform;
+//   * four more warps bring the scales of a span at a time: bulk copies several
+//     spans ahead put them into a ring of their own, each warp reads them (16
+//     bytes a lane for 32 rows), writes them to its quarter of the TMEM lanes
+//     with tcgen05.st (the MMA reads scales from all four), one set of columns
+//     for each slot pair, and arrives on the barrier of the pair's copies.
+//     (Read ahead into registers instead, two spans do not fit beside eight
+//     epilogue warps, and with one the loads' latency is the kernel's pace.)
+//     Copying them from shared memory (tcgen05.cp) instead holds up the MMAs:
+//     about 100 cycles a copy, six copies a stage, 404 us against 250 us of
+//     MMAs alone for the headline gate/up, and loading them by TMA takes a
+//     fifth of the loads' time;
 //   * N = 192 on CTA pairs: two accumulators of 256 columns would leave no
 //     TMEM for the scales, and accumulators that share columns would stop the
-//     MMAs at every tile's end until the epilogue has read the shared part.
-//     192 columns are three blocks of 32 gate features with their up features;
-//   * gate and up rows alternate by 32 (gate, up, gate, up ...), so that a
-//     tile's columns hold both values of the same features in blocks.  Weight
-//     scales are laid out once in that order, 128 rows a piece: a tile that
-//     begins in the middle of a piece addresses its scales two columns on.
-// Single CTAs with N = 64 serve batches that hold few rows an expert: they are
-// bound by reading weights, and many small tiles spread over the SMs.
+//     MMAs at every tile's end until the epilogue has read the shared part;
+//   * a gate/up tile's columns are its gate features, then the same up
+//     features (on CTA pairs the leader stages the gate rows, its peer the up
+//     rows), so that a lane holds both values of a feature.
+// Single CTAs serve batches that hold few rows an expert: they are bound by
+// reading weights, and many small tiles spread over the SMs.
 #include <algorithm>
 #include <mutex>
+#include <new>
 #include <type_traits>
 
 #include "common.cuh"
@@ -43,10 +54,9 @@
 namespace moe {
 
 struct Mx4Weights {
-  CUtensorMap gate32, up32;    // boxes of 32 rows by 256 values
-  CUtensorMap down96, down64;  // boxes of 96 and 64 rows
-  CUtensorMap sgu2, sgu1;      // scale pairs of two pieces, of one
-  CUtensorMap sd2, sd1;
+  CUtensorMap gate96, up96, down96;  // boxes of 96 rows by 256 values
+  CUtensorMap gate64, up64, down128;  // boxes of 64 and 128 rows
+  const uint8_t *sg, *su, *sd;       // scales in product order
   int64_t E, I, H;
 };
 
@@ -57,8 +67,7 @@ using namespace tc;
 constexpr int BM = 128;
 constexpr uint32_t ROW_BYTES = 128;              // 256 values of a row
 constexpr uint32_t A_BYTES = BM * ROW_BYTES;     // 16 KiB
-constexpr uint32_t SF_BYTES = 1024;              // scales of 128 rows by 256 values
-constexpr int THREADS = 192;
+constexpr int THREADS = 448;  // TMA, MMA, eight epilogue and four scale warps
 constexpr uint32_t TMEM_COLS = 512;
 constexpr int MAX_E = 1024;
 
@@ -66,15 +75,23 @@ template <int PAIR, int BN>
 struct Cfg {
   static constexpr int B_ROWS = BN / PAIR;
   static constexpr uint32_t B_BYTES = B_ROWS * ROW_BYTES;
-  static constexpr int SFB_PIECES = BN > 128 ? 2 : 1;
-  static constexpr uint32_t STAGE_BYTES = A_BYTES + B_BYTES + SF_BYTES * (1 + SFB_PIECES);
-  static constexpr int STAGES = (int)(222208 / STAGE_BYTES);
+  static constexpr uint32_t SLOT_BYTES = A_BYTES + B_BYTES;  // 256 columns
+  // pairs of slots in what 227 KiB hold beside the tables of MAX_E experts and the barriers
+  static constexpr int PAIRS =
+      (int)((232448 - 1024 - 512 - 4 * (PAIR == 2 ? 2 : 3) * (MAX_E + 1)) / SLOT_BYTES) / 2;
+  static constexpr uint32_t SF_BYTES = (4 + BN / 32) * mx::kGroupBytes;  // a span's scales
+  // depth of their ring, in what is left
+  static constexpr int SF_RING = std::min<int>(
+      8, (int)(232448 - 1024 - 512 - 4 * (PAIR == 2 ? 2 : 3) * (MAX_E + 1) - 2 * PAIRS * SLOT_BYTES) / (int)SF_BYTES);
+  static_assert(SF_RING >= 4, "scales are read ahead");
   static constexpr int TILE_M = BM * PAIR;
-  // TMEM columns: two accumulators, then two sets of scales (A: 2 x 4, B: 2 x 8)
+  static constexpr int GROUPS = BN / 32;  // 32-row groups of B
+  // TMEM columns: two accumulators, then a set of a span's scales for each slot
+  // pair (A: four words of 4 groups, B: four words of GROUPS groups)
   static constexpr uint32_t SF_COL = 2 * BN;
-  static constexpr uint32_t SF_SET = 32;
-  static_assert(SF_COL + 2 * SF_SET <= TMEM_COLS, "TMEM");
-  static_assert(STAGE_BYTES % 1024 == 0, "stages keep the swizzle's alignment");
+  static constexpr int SF_WORDS = 16 + 4 * GROUPS;
+  static_assert(SF_COL + PAIRS * SF_WORDS <= TMEM_COLS, "TMEM");
+  static_assert(SLOT_BYTES % 1024 == 0, "slots keep the swizzle's alignment");
 };
 
 struct Params {
@@ -82,11 +99,13 @@ struct Params {
   int E;
   int nb;         // n-tiles per m-tile
   int panel;
-  int steps;      // 256-deep steps
+  int steps;      // slots of a row: 256 columns each
   int gate_up;
-  int b_pieces;   // 128-row scale pieces per expert and step
+  const uint8_t* sa;   // scales in product order
+  const uint8_t* sb0;  // gate, or down
+  const uint8_t* sb1;  // up, or down again
   int64_t n_out;  // I (gate/up) or H (down)
-  int h_steps;    // depth steps of h (gate/up)
+  int h_spans;    // spans of a row of h (gate/up)
   uint8_t* hq;
   uint8_t* hs;
   void* out;
@@ -94,6 +113,7 @@ struct Params {
   const void* weights;
   int wdt;
   int thin_a;
+  int v8_out;  // out is 32-byte aligned
   uint32_t* status;
 };
 
@@ -117,18 +137,26 @@ __device__ __forceinline__ void umma_mx4(uint32_t d, uint64_t a, uint64_t b, uin
         : "memory");
   }
 }
-// 32 lanes by 16 bytes of shared memory to four TMEM columns, in every lane quarter
-template <int PAIR>
-__device__ __forceinline__ void copy_scales(uint32_t taddr, uint64_t desc) {
-  if constexpr (PAIR == 2)
-    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
-  else
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+// R consecutive words of this warp's 32 TMEM lanes
+template <int R>
+__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t* r) {
+  static_assert(R == 8 || R == 32, "");
+  if constexpr (R == 8) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+  } else {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+  }
 }
-// 512 contiguous bytes without swizzle: groups of 8 rows of 16 bytes, 128 bytes apart
-__device__ __forceinline__ uint64_t scale_desc(uint32_t saddr) {
-  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(128 >> 4) << 32) | ((uint64_t)1 << 46);
-}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 // e2m1 A and B, both K-major, exponent scales, FP32 accumulator; the scale ids
 // (which pair of a column's four bytes a step uses) are added per step
 __host__ __device__ constexpr uint32_t make_idesc(int M, int N) {
@@ -138,12 +166,13 @@ __host__ __device__ constexpr uint32_t make_idesc(int M, int N) {
 struct Tile {
   int e, nb;
   int64_t m0;
-  uint32_t piece;  // scale piece of the tile's first row
+  uint32_t unit;  // 256-row unit of scales, and the tile's first group in it
+  uint32_t group;
   bool thin;
 };
 
 __device__ __forceinline__ Tile decode_tile(uint32_t tile, const Params& p, const uint32_t* s_pref,
-                                            const uint32_t* s_piece, const uint32_t* s_off, int tile_m) {
+                                            const uint32_t* s_unit, const uint32_t* s_off, int tile_m) {
   const uint32_t q = tile / (uint32_t)p.nb;
   int lo = 0, hi = p.E;
   while (hi - lo > 1) {
@@ -161,7 +190,8 @@ __device__ __forceinline__ Tile decode_tile(uint32_t tile, const Params& p, cons
   t.e = lo;
   t.nb = (int)(pid * w + rem % width);
   t.m0 = (int64_t)s_off[lo] + (int64_t)mt * tile_m;
-  t.piece = tile_m == 256 ? 2 * (s_pref[lo] + mt) : 2 * s_piece[lo] + mt;
+  t.unit = tile_m == 256 ? s_pref[lo] + mt : s_unit[lo] + (mt >> 1);
+  t.group = tile_m == 256 ? 0u : 4u * (mt & 1u);
   t.thin = p.thin_a && (int64_t)s_off[lo + 1] - t.m0 <= 32;
   return t;
 }
@@ -169,43 +199,50 @@ __device__ __forceinline__ Tile decode_tile(uint32_t tile, const Params& p, cons
 template <typename T, int PAIR, int BN>
 __global__ void __launch_bounds__(THREADS, 1)
 gemm_mx4_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapA32,
-                const __grid_constant__ CUtensorMap mapB0, const __grid_constant__ CUtensorMap mapB1,
-                const __grid_constant__ CUtensorMap mapSA, const __grid_constant__ CUtensorMap mapSB, const Params p) {
+                const __grid_constant__ CUtensorMap mapB0, const __grid_constant__ CUtensorMap mapB1, const Params p) {
   using C = Cfg<PAIR, BN>;
-  constexpr int STAGES = C::STAGES;
+  constexpr int PAIRS = C::PAIRS;
   constexpr bool kCluster = PAIR == 2;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_s = smem_u32(smem_raw);
   const uint32_t ring = (raw_s + 1023u) & ~1023u;
   uint8_t* ring_ptr = smem_raw + (ring - raw_s);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(ring_ptr + STAGES * C::STAGE_BYTES);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * STAGES + 5);
+  uint8_t* sf_ring = ring_ptr + 2 * PAIRS * C::SLOT_BYTES;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sf_ring + C::SF_RING * C::SF_BYTES);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 3 * PAIRS + 5 + 2 * C::SF_RING);
   volatile uint32_t* abort_flag = tmem_slot + 1;
-  uint32_t* s_off = reinterpret_cast<uint32_t*>(ring_ptr + STAGES * C::STAGE_BYTES + 256);
+  uint32_t* s_off = reinterpret_cast<uint32_t*>(reinterpret_cast<uint8_t*>(bars) + 512);
   uint32_t* s_pref = s_off + (p.E + 1);
-  uint32_t* s_piece = s_pref + (p.E + 1);  // PAIR == 1 only: a pair's tile is two pieces
+  uint32_t* s_unit = s_pref + (p.E + 1);  // PAIR == 1 only: a pair's tile is a unit
 
   const uint32_t bar0 = smem_u32(bars);
-  auto full_bar = [&](int s) { return bar0 + 8u * s; };
-  auto empty_bar = [&](int s) { return bar0 + 8u * (STAGES + s); };
-  auto tfull_bar = [&](int a) { return bar0 + 8u * (2 * STAGES + a); };
-  auto tempty_bar = [&](int a) { return bar0 + 8u * (2 * STAGES + 2 + a); };
-  const uint32_t drain_bar = bar0 + 8u * (2 * STAGES + 4);
+  auto full_bar = [&](int q) { return bar0 + 8u * q; };               // a pair's copies and scales are there
+  auto empty_bar = [&](int q, int h) { return bar0 + 8u * (PAIRS + 2 * q + h); };  // slot h's MMAs are done
+  auto tfull_bar = [&](int a) { return bar0 + 8u * (3 * PAIRS + a); };
+  auto tempty_bar = [&](int a) { return bar0 + 8u * (3 * PAIRS + 2 + a); };
+  const uint32_t drain_bar = bar0 + 8u * (3 * PAIRS + 4);
+  auto sfull_bar = [&](int q) { return bar0 + 8u * (3 * PAIRS + 5 + q); };              // scales copied
+  auto sempty_bar = [&](int q) { return bar0 + 8u * (3 * PAIRS + 5 + C::SF_RING + q); };  // and read by four warps
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int E = p.E;
   const uint32_t rank = kCluster ? cluster_rank() : 0u;
   const bool leader = rank == 0;
   const uint32_t cluster_id = blockIdx.x / PAIR, num_clusters = gridDim.x / PAIR;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < STAGES; ++s) {
-      mbar_init(full_bar(s), 1);
-      mbar_init(empty_bar(s), 1);
+    for (int q = 0; q < PAIRS; ++q) {
+      mbar_init(full_bar(q), 1 + 4 * PAIR);  // the copies, and one arrival per scale warp
+      mbar_init(empty_bar(q, 0), 1);
+      mbar_init(empty_bar(q, 1), 1);
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(tfull_bar(a), 1);
       mbar_init(tempty_bar(a), 4 * PAIR);
+    }
+    for (int q = 0; q < C::SF_RING; ++q) {
+      mbar_init(sfull_bar(q), 1);
+      mbar_init(sempty_bar(q), 4);
     }
     mbar_init(drain_bar, 1);
     *abort_flag = 0u;
@@ -217,8 +254,6 @@ gemm_mx4_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant_
     if (p.thin_a) prefetch_map(&mapA32);
     prefetch_map(&mapB0);
     prefetch_map(&mapB1);
-    prefetch_map(&mapSA);
-    prefetch_map(&mapSB);
   }
   if (warp == 1) tmem_alloc<PAIR>(smem_u32(tmem_slot), TMEM_COLS);
   pdl_wait();
@@ -228,7 +263,7 @@ gemm_mx4_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant_
   if (warp == 2 || (warp == 3 && PAIR == 1)) {
     // warp 2: tiles of experts < e; warp 3: 256-row units of scales of experts < e
     const uint32_t unit = warp == 2 ? (uint32_t)C::TILE_M : 256u;
-    uint32_t* dst = warp == 2 ? s_pref : s_piece;
+    uint32_t* dst = warp == 2 ? s_pref : s_unit;
     const int per = (E + 31) / 32;
     uint32_t loc = 0;
     for (int i = 0; i < per; ++i) {
@@ -255,127 +290,226 @@ gemm_mx4_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant_
   __syncthreads();
   if constexpr (kCluster) cluster_sync();
   tc_fence_after();
-  const uint32_t tmem_base = *tmem_slot;
-  const uint32_t total_tiles = s_pref[E] * (uint32_t)p.nb;
-  auto tile_at = [&](uint32_t tile) { return decode_tile(tile, p, s_pref, s_piece, s_off, C::TILE_M); };
+  const uint32_t tmem_base = __shfl_sync(0xffffffffu, *tmem_slot, 0);
+  const uint32_t total_tiles = __shfl_sync(0xffffffffu, s_pref[E] * (uint32_t)p.nb, 0);
+  auto tile_at = [&](uint32_t tile) { return decode_tile(tile, p, s_pref, s_unit, s_off, C::TILE_M); };
   const uint32_t full0_leader = kCluster ? mapa(full_bar(0), 0) : full_bar(0);
   const uint32_t tempty0_leader = kCluster ? mapa(tempty_bar(0), 0) : tempty_bar(0);
+  const int spans = (p.steps + 1) / 2;
 
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer
-    if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0;
-      uint32_t last_fill[STAGES];
-      bool filled[STAGES];
-      for (int s = 0; s < STAGES; ++s) filled[s] = false, last_fill[s] = 0;
-      bool ok = true;
-      for (uint32_t tile = cluster_id; ok && tile < total_tiles; tile += num_clusters) {
-        const Tile t = tile_at(tile);
-        const int a_row = (int)(t.m0 + (int64_t)rank * BM);
-        const CUtensorMap* ma = t.thin ? &mapA32 : &mapA;
-        const uint32_t stage_tx = (t.thin ? C::STAGE_BYTES - (A_BYTES - A_BYTES / 4) : C::STAGE_BYTES) * PAIR;
-        const int n0 = t.nb * BN;
-        const int sa_row = (int)((t.piece + rank) * (uint32_t)p.steps);
-        const int sb_row = t.e * p.steps * p.b_pieces + (n0 >> 7);
-        for (int kb = 0; kb < p.steps; ++kb) {
-          if (!mbar_wait<kCluster>(empty_bar(stage), phase ^ 1u, abort_flag, p.status)) {
-            ok = false;
-            break;
-          }
-          const uint32_t sa = ring + stage * C::STAGE_BYTES;
-          const uint32_t sb = sa + A_BYTES, sf = sb + C::B_BYTES;
-          const uint32_t fb = full0_leader + 8u * stage;
-          const int kx = kb * (int)ROW_BYTES;
-          if (leader) mbar_expect_tx(full_bar(stage), stage_tx);
-          tma_load_2d<PAIR>(sa, ma, kx, a_row, fb);
-          if (p.gate_up) {
+    // The whole warp runs the loop, so that what the copies and the MMAs take
+    // is known to be the same in every lane; one elected lane issues.
+    int pr = 0;
+    uint32_t phase = 0, fills = 0;
+    bool ok = true;
+    for (uint32_t tile = cluster_id; ok && tile < total_tiles; tile += num_clusters) {
+      const Tile t = tile_at(tile);
+      const int a_row = __shfl_sync(0xffffffffu, (int)(t.m0 + (int64_t)rank * BM), 0);
+      const int te = __shfl_sync(0xffffffffu, t.e, 0);
+      const int tnb = __shfl_sync(0xffffffffu, t.nb, 0);
+      const bool thin = __all_sync(0xffffffffu, t.thin);
+      const uint32_t slot_tx = (thin ? C::SLOT_BYTES - (A_BYTES - A_BYTES / 4) : C::SLOT_BYTES) * PAIR;
+      const int n0 = tnb * (p.gate_up ? BN / 2 : BN);  // first feature, or first output column
+      const int b_row = PAIR == 2 && !p.gate_up ? n0 + (int)rank * C::B_ROWS : n0;
+      for (int sp = 0; sp < spans; ++sp) {
+        const bool two = 2 * sp + 1 < p.steps;
 #pragma unroll
-            for (int q = 0; q < C::B_ROWS / 32; ++q) {
-              const int grp = (n0 >> 5) + (int)rank * (C::B_ROWS / 32) + q;  // gate, up, gate, up ...
-              tma_load_3d<PAIR>(sb + q * 32 * ROW_BYTES, (grp & 1) ? &mapB1 : &mapB0, kx, (grp >> 1) * 32, t.e, fb);
+        for (int h = 0; h < 2; ++h) {
+          ok = __all_sync(0xffffffffu, mbar_wait<kCluster>(empty_bar(pr, h), phase ^ 1u, abort_flag, p.status));
+          if (!ok) break;
+          if ((h == 0 || two) && elect_one()) {
+            const uint32_t sa = ring + (2 * pr + h) * C::SLOT_BYTES;
+            const uint32_t sb = sa + A_BYTES;
+            const uint32_t fb = full0_leader + 8u * pr;
+            const int kx = (2 * sp + h) * (int)ROW_BYTES;
+            if (leader && h == 0) mbar_expect_tx(full_bar(pr), two ? 2 * slot_tx : slot_tx);
+            if (thin) tma_load_2d<PAIR>(sa, &mapA32, kx, a_row, fb);
+            else tma_load_2d<PAIR>(sa, &mapA, kx, a_row, fb);
+            if (PAIR == 2) {  // gate rows and up rows, or the two halves of the down rows
+              if (leader) tma_load_3d<PAIR>(sb, &mapB0, kx, b_row, te, fb);
+              else tma_load_3d<PAIR>(sb, &mapB1, kx, b_row, te, fb);
+            } else {
+              tma_load_3d<PAIR>(sb, &mapB0, kx, b_row, te, fb);
+              if (p.gate_up) tma_load_3d<PAIR>(sb + C::B_BYTES / 2, &mapB1, kx, b_row, te, fb);
             }
-          } else {
-            tma_load_3d<PAIR>(sb, &mapB0, kx, n0 + (int)rank * C::B_ROWS, t.e, fb);
           }
-          tma_load_2d<PAIR>(sf, &mapSA, 0, sa_row + kb, fb);
-          tma_load_2d<PAIR>(sf + SF_BYTES, &mapSB, 0, sb_row + kb * p.b_pieces, fb);
-          filled[stage] = true;
-          last_fill[stage] = phase;
-          if (++stage == STAGES) {
-            stage = 0;
-            phase ^= 1u;
-          }
+          __syncwarp();
+        }
+        if (!ok) break;
+        ++fills;
+        if (++pr == PAIRS) {
+          pr = 0;
+          phase ^= 1u;
         }
       }
-      if (!ok && leader) {  // aborting: let the copies in flight land before exit
-        for (int s = 0; s < STAGES; ++s) {
-          if (!filled[s]) continue;
-          const uint64_t t0 = global_timer();
-          while (!mbar_test<kCluster>(full_bar(s), last_fill[s]) && global_timer() - t0 < kWaitLimitNs) {
-          }
+    }
+    if (!ok && leader && lane == 0) {  // aborting: let the copies in flight land before exit
+      for (uint32_t i = fills > PAIRS ? fills - PAIRS : 0; i < fills; ++i) {
+        const uint64_t t0 = global_timer();
+        while (!mbar_test<kCluster>(full_bar(i % PAIRS), (i / PAIRS) & 1u) && global_timer() - t0 < kWaitLimitNs) {
         }
       }
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer (leader CTA)
-    if (lane == 0 && leader) {
+    if (leader) {
       constexpr uint32_t idesc = make_idesc(C::TILE_M, BN);
-      const uint64_t hi = sw128_desc(0), sf_hi = scale_desc(0);
-      int stage = 0;
-      uint32_t phase = 0, acc = 0, acc_phase = 0, set = 0;
+      const uint64_t hi = sw128_desc(0);
+      int pr = 0;
+      uint32_t phase = 0, acc = 0, acc_phase = 0;
       bool ok = true;
       for (uint32_t tile = cluster_id; ok && tile < total_tiles; tile += num_clusters) {
-        const Tile t = tile_at(tile);
-        const uint32_t shift = (uint32_t)((t.nb * BN) & 127) >> 5;  // columns into the first scale piece
-        if (!mbar_wait<kCluster>(tempty_bar(acc), acc_phase ^ 1u, abort_flag, p.status)) break;
-        tc_fence_after();
+        ok = __all_sync(0xffffffffu, mbar_wait<kCluster>(tempty_bar(acc), acc_phase ^ 1u, abort_flag, p.status));
+        if (!ok) break;
         const uint32_t d_tmem = tmem_base + acc * BN;
-        for (int kb = 0; kb < p.steps; ++kb) {
-          if (!mbar_wait<kCluster>(full_bar(stage), phase, abort_flag, p.status)) {
-            ok = false;
-            break;
-          }
+        for (int sp = 0; sp < spans; ++sp) {
+          ok = __all_sync(0xffffffffu, mbar_wait<kCluster>(full_bar(pr), phase, abort_flag, p.status));
+          if (!ok) break;
           tc_fence_after();
-          const uint32_t sa = ring + stage * C::STAGE_BYTES;
-          const uint32_t sb = sa + A_BYTES, sf = sb + C::B_BYTES;
-          const uint32_t ta = tmem_base + C::SF_COL + set * C::SF_SET, tb = ta + 8;
+          if (elect_one()) {
+            const uint32_t sf = tmem_base + C::SF_COL + pr * C::SF_WORDS;
+            const uint32_t s0 = ring + 2 * pr * C::SLOT_BYTES;
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            copy_scales<PAIR>(ta + half * 4, sf_hi | ((sf + half * 512) & 0x3FFFFu) >> 4);
+            for (int h = 0; h < 2; ++h) {
+              if (h == 0 || 2 * sp + 1 < p.steps) {
+                const uint32_t sa = s0 + h * C::SLOT_BYTES, sb = sa + A_BYTES;
 #pragma unroll
-            for (int q = 0; q < C::SFB_PIECES; ++q)
-              copy_scales<PAIR>(tb + half * 8 + q * 4, sf_hi | ((sf + SF_BYTES * (1 + q) + half * 512) & 0x3FFFFu) >> 4);
+                for (int k = 0; k < 4; ++k) {  // scales: bytes 0-1 or 2-3 of word 2 h + k / 2
+                  const uint32_t id = idesc | (uint32_t)(k & 1) * ((2u << 29) | (2u << 4));
+                  const int w = 2 * h + (k >> 1);
+                  umma_mx4<PAIR>(d_tmem, hi | ((sa + k * 32) & 0x3FFFFu) >> 4, hi | ((sb + k * 32) & 0x3FFFFu) >> 4,
+                                 id, sf + w * 4, sf + 16 + w * C::GROUPS, (h | k) != 0 ? 1u : sp != 0);
+                }
+              }
+              umma_commit<PAIR>(empty_bar(pr, h));
+            }
+            if (sp == spans - 1) umma_commit<PAIR>(tfull_bar(acc));
           }
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint32_t id = idesc | (uint32_t)(k & 1) * ((2u << 29) | (2u << 4));
-            umma_mx4<PAIR>(d_tmem, hi | ((sa + k * 32) & 0x3FFFFu) >> 4, hi | ((sb + k * 32) & 0x3FFFFu) >> 4, id,
-                           ta + (k >> 1) * 4, tb + (k >> 1) * 8 + shift, (kb | k) != 0 ? 1u : 0u);
-          }
-          set ^= 1u;
-          umma_commit<PAIR>(empty_bar(stage));
-          if (++stage == STAGES) {
-            stage = 0;
+          __syncwarp();
+          if (++pr == PAIRS) {
+            pr = 0;
             phase ^= 1u;
           }
         }
-        if (!ok) break;
-        umma_commit<PAIR>(tfull_bar(acc));
         acc ^= 1u;
         if (acc == 0) acc_phase ^= 1u;
       }
-      umma_commit_local<PAIR>(drain_bar);
-      const uint64_t t0 = global_timer();
-      while (!mbar_test<false>(drain_bar, 0) && global_timer() - t0 < kWaitLimitNs) {
+      if (elect_one()) {
+        umma_commit_local<PAIR>(drain_bar);
+        const uint64_t t0 = global_timer();
+        while (!mbar_test<false>(drain_bar, 0) && global_timer() - t0 < kWaitLimitNs) {
+        }
+      }
+      __syncwarp();
+    }
+  } else if (warp >= 10) {
+    // ------------------------------------------------------------ scales
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    constexpr int G = C::GROUPS, W = C::SF_WORDS, RING = C::SF_RING;
+    const uint32_t ring0 = smem_u32(sf_ring);
+    // the next span to copy (warp 10)
+    uint32_t tile = cluster_id, isp = 0, islot = 0, iphase = 0, copies = 0;
+    const uint8_t *pa = nullptr, *pb0 = nullptr, *pb1 = nullptr;
+    uint32_t bytes0 = 0, bytes1 = 0;  // of each half of B inside the weights
+    const int64_t per = p.n_out / 32;  // groups of an expert
+    bool ok = true;
+    auto copy = [&]() {
+      if (tile >= total_tiles) return;
+      if (isp == 0) {
+        const Tile t = tile_at(tile);
+        pa = p.sa + ((int64_t)t.unit * spans * mx::kUnitGroups + t.group + rank * 4) * mx::kGroupBytes;
+        // the halves of the columns: gate and up features, or down columns
+        const int64_t g0 = p.gate_up ? (int64_t)t.nb * (G / 2) : (int64_t)t.nb * G;
+        const int64_t g1 = p.gate_up ? g0 : g0 + G / 2;
+        pb0 = p.sb0 + ((int64_t)t.e * spans * per + g0) * mx::kGroupBytes;
+        pb1 = p.sb1 + ((int64_t)t.e * spans * per + g1) * mx::kGroupBytes;
+        bytes0 = (uint32_t)max((int64_t)0, min(per - g0, (int64_t)(G / 2))) * mx::kGroupBytes;
+        bytes1 = (uint32_t)max((int64_t)0, min(per - g1, (int64_t)(G / 2))) * mx::kGroupBytes;
+      }
+      ok = __all_sync(0xffffffffu, mbar_wait<false>(sempty_bar(islot), iphase ^ 1u, abort_flag, p.status));
+      if (!ok) return;
+      if (elect_one()) {
+        const uint32_t dst = ring0 + islot * C::SF_BYTES, bar = sfull_bar(islot);
+        mbar_expect_tx(bar, 4 * mx::kGroupBytes + bytes0 + bytes1);
+        bulk_load(dst, pa, 4 * mx::kGroupBytes, bar);
+        if (bytes0) bulk_load(dst + 4 * mx::kGroupBytes, pb0, bytes0, bar);
+        if (bytes1) bulk_load(dst + (4 + G / 2) * mx::kGroupBytes, pb1, bytes1, bar);
+      }
+      __syncwarp();
+      ++copies;
+      pa += mx::kUnitGroups * mx::kGroupBytes;
+      pb0 += per * mx::kGroupBytes;
+      pb1 += per * mx::kGroupBytes;
+      if (++isp == (uint32_t)spans) {
+        isp = 0;
+        tile += num_clusters;
+      }
+      if (++islot == RING) {
+        islot = 0;
+        iphase ^= 1u;
+      }
+    };
+    if (warp == 10)
+      for (int i = 0; i < RING - 1; ++i) copy();
+    uint32_t pr = 0, phase = 0, slot = 0, sphase = 0;
+    for (uint32_t mine = cluster_id; ok && mine < total_tiles; mine += num_clusters) {
+      for (int sp = 0; sp < spans; ++sp) {
+        if (warp == 10) copy();
+        ok = ok && __all_sync(0xffffffffu, mbar_wait<false>(sfull_bar(slot), sphase, abort_flag, p.status));
+        if (!ok) break;
+        uint32_t w[W];
+        const uint4* src = reinterpret_cast<const uint4*>(sf_ring + slot * C::SF_BYTES) + lane;
+#pragma unroll
+        for (int j = 0; j < 4 + G; ++j) {
+          const uint4 v = src[j * 32];
+          const int at = j < 4 ? j : 12 + j, step = j < 4 ? 4 : G;
+          w[at] = v.x;
+          w[at + step] = v.y;
+          w[at + 2 * step] = v.z;
+          w[at + 3 * step] = v.w;
+        }
+        // the MMAs that read this set last are done
+        ok = __all_sync(0xffffffffu, mbar_wait<kCluster>(empty_bar(pr, 1), phase ^ 1u, abort_flag, p.status));
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t ta = tmem_base + lanes + C::SF_COL + pr * C::SF_WORDS;
+        tmem_st<32>(ta, w);
+        if constexpr (W > 32) tmem_st<8>(ta + 32, w + 32);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if constexpr (kCluster) mbar_arrive_cluster_relaxed(full0_leader + 8u * pr);
+          else mbar_arrive(full_bar(pr));
+          mbar_arrive(sempty_bar(slot));  // every lane has used what it read
+        }
+        if (++pr == PAIRS) {
+          pr = 0;
+          phase ^= 1u;
+        }
+        if (++slot == RING) {
+          slot = 0;
+          sphase ^= 1u;
+        }
+      }
+    }
+    if (!ok && warp == 10 && lane == 0) {  // aborting: let the copies in flight land before exit
+      for (uint32_t i = copies > RING ? copies - RING : 0; i < copies; ++i) {
+        const uint64_t t0 = global_timer();
+        while (!mbar_test<false>(sfull_bar(i % RING), (i / RING) & 1u) && global_timer() - t0 < kWaitLimitNs) {
+        }
       }
     }
   } else {
     // ------------------------------------------------------------ epilogue
+    // four warps for each accumulator: they have the time of two tiles
     const int quarter = warp & 3;
-    uint32_t acc = 0, acc_phase = 0;
-    for (uint32_t tile = cluster_id; tile < total_tiles; tile += num_clusters) {
-      const Tile t = tile_at(tile);
+    const uint32_t acc = (uint32_t)(warp - 2) >> 2;
+    uint32_t acc_phase = 0;
+    for (uint64_t tile = cluster_id + acc * num_clusters; tile < total_tiles; tile += 2 * num_clusters) {
+      const Tile t = tile_at((uint32_t)tile);
       const int row = quarter * 32 + lane;
       const int64_t grow = t.m0 + (int64_t)rank * BM + row;
       const bool row_ok = grow < (int64_t)s_off[t.e + 1];
@@ -397,15 +531,16 @@ gemm_mx4_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant_
       if (any && p.gate_up) {
         const int blocks = (int)(p.n_out / 32), b0 = t.nb * (BN / 64);
         uint8_t* hrow = p.hq + grow * (p.n_out / 2);
-        uint8_t* srow = p.hs + (int64_t)(t.piece + rank) * p.h_steps * 1024;
+        uint8_t* srow = p.hs + ((int64_t)t.unit * p.h_spans * mx::kUnitGroups + t.group + rank * 4 + quarter) * mx::kGroupBytes +
+                        lane * 16;
 #pragma unroll 1
         for (int b = 0; b < BN / 64; ++b) {
           const int blk = b0 + b;
           if (blk >= blocks) break;
           uint32_t g[32], u[32];
           __syncwarp();
-          tmem_ld32(taddr + b * 64, g);
-          tmem_ld32(taddr + b * 64 + 32, u);
+          tmem_ld32(taddr + b * 32, g);
+          tmem_ld32(taddr + BN / 2 + b * 32, u);
           tmem_wait_ld(g);
           reg_fence(u);
           float h[32];
@@ -429,10 +564,10 @@ gemm_mx4_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant_
           }
           if (row_ok) {
             *reinterpret_cast<uint4*>(hrow + blk * 16) = make_uint4(w[0], w[1], w[2], w[3]);
-            uint8_t* d = srow + (int64_t)(blk >> 3) * 1024;
-            d[mx::pair_byte((uint32_t)row, (uint32_t)blk & 7u)] = (uint8_t)sb;
-            if (blk == blocks - 1)  // the row's last pair: finite scales behind its end
-              for (int c = (blk & 7) + 1; c < 8; ++c) d[mx::pair_byte((uint32_t)row, (uint32_t)c)] = 0;
+            uint8_t* d = srow + (int64_t)(blk >> 4) * (mx::kUnitGroups * mx::kGroupBytes);
+            d[blk & 15] = (uint8_t)sb;
+            if (blk == blocks - 1)  // the row's last span: finite scales behind its end
+              for (int c = (blk & 15) + 1; c < 16; ++c) d[c] = 0;
           }
         }
       } else if (any) {
@@ -451,13 +586,26 @@ gemm_mx4_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant_
               d[v] = make_float4(__uint_as_float(o[4 * v]) * wscale, __uint_as_float(o[4 * v + 1]) * wscale,
                                  __uint_as_float(o[4 * v + 2]) * wscale, __uint_as_float(o[4 * v + 3]) * wscale);
           } else if (row_ok) {
-            uint4* d = reinterpret_cast<uint4*>(static_cast<T*>(p.out) + slot * p.n_out + c0 + c);
+            uint32_t* d = reinterpret_cast<uint32_t*>(static_cast<T*>(p.out) + slot * p.n_out + c0 + c);
+            uint32_t q[16];
 #pragma unroll
             for (int v = 0; v < 4; ++v) {
               float f[8];
 #pragma unroll
               for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(o[v * 8 + i]);
-              d[v] = pack8<T>(f);
+              const uint4 r = pack8<T>(f);
+              q[4 * v] = r.x;
+              q[4 * v + 1] = r.y;
+              q[4 * v + 2] = r.z;
+              q[4 * v + 3] = r.w;
+            }
+            if (p.v8_out) {  // whole 32-byte sectors
+              st_v8(d, q);
+              st_v8(d + 8, q + 8);
+            } else {
+#pragma unroll
+              for (int v = 0; v < 4; ++v)
+                reinterpret_cast<uint4*>(d)[v] = make_uint4(q[4 * v], q[4 * v + 1], q[4 * v + 2], q[4 * v + 3]);
             }
           }
         }
@@ -468,8 +616,7 @@ gemm_mx4_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant_
         if constexpr (kCluster) mbar_arrive_cluster(tempty0_leader + 8u * acc);
         else mbar_arrive(tempty_bar(acc));
       }
-      acc ^= 1u;
-      if (acc == 0) acc_phase ^= 1u;
+      acc_phase ^= 1u;
     }
   }
 
@@ -505,22 +652,10 @@ bool encode_weights(CUtensorMap* m, const void* base, uint64_t E, uint64_t rows,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
-// n kilobytes of scales, `box_kb` of them a load
-bool encode_scales(CUtensorMap* m, const void* base, uint64_t n, uint32_t box_kb) {
-  auto fn = encode_fn();
-  if (!fn) return false;
-  cuuint64_t dims[2] = {SF_BYTES / 4, n};
-  cuuint64_t strides[1] = {SF_BYTES};
-  cuuint32_t box[2] = {SF_BYTES / 4, box_kb};
-  cuuint32_t estr[2] = {1u, 1u};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void*>(base), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 template <int PAIR, int BN>
 size_t smem_bytes(int E) {
-  return 1024 + (size_t)Cfg<PAIR, BN>::STAGES * Cfg<PAIR, BN>::STAGE_BYTES + 256 +
+  using C = Cfg<PAIR, BN>;
+  return 1024 + (size_t)C::PAIRS * 2 * C::SLOT_BYTES + (size_t)C::SF_RING * C::SF_BYTES + 512 +
          4 * (size_t)(PAIR == 2 ? 2 : 3) * (E + 1);
 }
 
@@ -565,24 +700,24 @@ template <typename T, int PAIR, int BN>
 cudaError_t launch_t(const Mx4Args& a, const Mx4Weights* w, int num_sms, cudaStream_t s) {
   using C = Cfg<PAIR, BN>;
   const int64_t K = a.gate_up ? a.H : a.I;
-  CUtensorMap mA, mA32, mSA;
-  const uint64_t a_kb = mx4_row_scale_bytes(a.N, a.E, K) / SF_BYTES;
-  if (!encode_rows(&mA, a.a, a.N, K / 2, BM) || !encode_rows(&mA32, a.a, a.N, K / 2, 32) ||
-      !encode_scales(&mSA, a.a_scales, a_kb, 1))
-    return cudaErrorInvalidValue;
+  CUtensorMap mA, mA32;
+  if (!encode_rows(&mA, a.a, a.N, K / 2, BM) || !encode_rows(&mA32, a.a, a.N, K / 2, 32)) return cudaErrorInvalidValue;
   Params p{};
   p.offsets = a.offsets;
   p.E = a.E;
-  p.steps = (int)mx::depth_steps(K);
+  p.steps = (int)((K + 255) / 256);
   p.gate_up = a.gate_up;
   p.n_out = a.gate_up ? a.I : a.H;
   const int64_t cols = a.gate_up ? 2 * a.I : a.H;  // columns of the product
   p.nb = (int)((cols + BN - 1) / BN);
-  p.b_pieces = (int)(a.gate_up ? mx4_gate_up_pieces(a.I) : mx4_down_pieces(a.H));
-  p.h_steps = (int)mx::depth_steps(a.I);
+  p.sa = static_cast<const uint8_t*>(a.a_scales);
+  p.sb0 = a.gate_up ? w->sg : w->sd;
+  p.sb1 = a.gate_up ? w->su : w->sd;
+  p.h_spans = (int)mx::spans(a.I);
   p.hq = static_cast<uint8_t*>(a.hq);
   p.hs = static_cast<uint8_t*>(a.hs);
   p.out = a.out;
+  p.v8_out = reinterpret_cast<uintptr_t>(a.out) % 32 == 0;
   p.perm = a.perm;
   p.weights = a.weights;
   p.wdt = (int)a.wdt;
@@ -598,9 +733,8 @@ cudaError_t launch_t(const Mx4Args& a, const Mx4Weights* w, int num_sms, cudaStr
   // panel width: about one wave of clusters spread over an expert's expected m-tiles
   const int64_t mt_per_expert = std::max<int64_t>(1, (a.N + (int64_t)TM * a.E - 1) / ((int64_t)TM * a.E));
   p.panel = (int)std::max<int64_t>(1, std::min<int64_t>(p.nb, (nclu + mt_per_expert - 1) / mt_per_expert));
-  const CUtensorMap& b0 = a.gate_up ? w->gate32 : PAIR == 2 ? w->down96 : w->down64;
-  const CUtensorMap& b1 = a.gate_up ? w->up32 : b0;
-  const CUtensorMap& sb = a.gate_up ? (C::SFB_PIECES == 2 ? w->sgu2 : w->sgu1) : (C::SFB_PIECES == 2 ? w->sd2 : w->sd1);
+  const CUtensorMap& b0 = PAIR == 2 ? (a.gate_up ? w->gate96 : w->down96) : (a.gate_up ? w->gate64 : w->down128);
+  const CUtensorMap& b1 = !a.gate_up ? b0 : PAIR == 2 ? w->up96 : w->up64;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -615,26 +749,22 @@ cudaError_t launch_t(const Mx4Args& a, const Mx4Weights* w, int num_sms, cudaStr
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, gemm_mx4_kernel<T, PAIR, BN>, mA, mA32, b0, b1, mSA, sb, p);
+  return cudaLaunchKernelEx(&cfg, gemm_mx4_kernel<T, PAIR, BN>, mA, mA32, b0, b1, p);
 }
 
 }  // namespace mx4
 
-int64_t mx4_gate_up_pieces(int64_t I) { return (2 * I + 127) / 128; }
-int64_t mx4_down_pieces(int64_t H) { return (H + 127) / 128; }
-size_t mx4_gate_up_scale_bytes(int64_t E, int64_t I, int64_t H) {
-  return (size_t)(E * mx::depth_steps(H) * mx4_gate_up_pieces(I)) * mx4::SF_BYTES;
-}
-size_t mx4_down_scale_bytes(int64_t E, int64_t I, int64_t H) {
-  return (size_t)(E * mx::depth_steps(I) * mx4_down_pieces(H)) * mx4::SF_BYTES;
+size_t mx4_weight_scale_bytes(int64_t rows, int64_t C) {
+  return (size_t)(rows / mx::kGroupRows) * mx::spans(C) * mx::kGroupBytes;
 }
 size_t mx4_row_scale_bytes(int64_t N, int64_t E, int64_t C) {
-  // every expert's rows begin an even piece of their own
-  return (size_t)(2 * ((N + 255) / 256 + std::min<int64_t>(E, N))) * mx::depth_steps(C) * mx4::SF_BYTES;
+  // every expert's rows begin a 256-row unit of their own
+  return (size_t)(mx::kUnitGroups * ((N + 255) / 256 + std::min<int64_t>(E, N))) * mx::spans(C) * mx::kGroupBytes;
 }
 
-Mx4Weights* mx4_weights_create(const void* gate, const void* up, const void* down, const void* sgu, const void* sd,
-                               int64_t E, int64_t I, int64_t H, const char** err) {
+Mx4Weights* mx4_weights_create(const void* gate, const void* up, const void* down, const uint8_t* sg,
+                               const uint8_t* su, const uint8_t* sd, int64_t E, int64_t I, int64_t H,
+                               const char** err) {
   if (!tc::encode_fn()) {
     *err = "cuTensorMapEncodeTiled is not available from the driver";
     return nullptr;
@@ -647,12 +777,13 @@ Mx4Weights* mx4_weights_create(const void* gate, const void* up, const void* dow
   w->E = E;
   w->I = I;
   w->H = H;
-  const uint64_t ngu = mx4_gate_up_scale_bytes(E, I, H) / mx4::SF_BYTES, nd = mx4_down_scale_bytes(E, I, H) / mx4::SF_BYTES;
-  if (!mx4::encode_weights(&w->gate32, gate, E, I, H / 2, 32) || !mx4::encode_weights(&w->up32, up, E, I, H / 2, 32) ||
-      !mx4::encode_weights(&w->down96, down, E, H, I / 2, 96) ||
-      !mx4::encode_weights(&w->down64, down, E, H, I / 2, 64) || !mx4::encode_scales(&w->sgu2, sgu, ngu, 2) ||
-      !mx4::encode_scales(&w->sgu1, sgu, ngu, 1) || !mx4::encode_scales(&w->sd2, sd, nd, 2) ||
-      !mx4::encode_scales(&w->sd1, sd, nd, 1)) {
+  w->sg = sg;
+  w->su = su;
+  w->sd = sd;
+  using mx4::encode_weights;
+  if (!encode_weights(&w->gate96, gate, E, I, H / 2, 96) || !encode_weights(&w->up96, up, E, I, H / 2, 96) ||
+      !encode_weights(&w->down96, down, E, H, I / 2, 96) || !encode_weights(&w->gate64, gate, E, I, H / 2, 64) ||
+      !encode_weights(&w->up64, up, E, I, H / 2, 64) || !encode_weights(&w->down128, down, E, H, I / 2, 128)) {
     *err = "cuTensorMapEncodeTiled rejected a 4-bit expert weight tensor";
     delete w;
     return nullptr;
@@ -667,8 +798,8 @@ cudaError_t launch_gemm_mx4(const Mx4Args& a, const Mx4Weights* w, int num_sms, 
   const bool pair = a.N >= (int64_t)128 * a.E;
   if (a.dt == MOE_BF16)
     return pair ? mx4::launch_t<__nv_bfloat16, 2, 192>(a, w, num_sms, s)
-                : mx4::launch_t<__nv_bfloat16, 1, 64>(a, w, num_sms, s);
-  return pair ? mx4::launch_t<__half, 2, 192>(a, w, num_sms, s) : mx4::launch_t<__half, 1, 64>(a, w, num_sms, s);
+                : mx4::launch_t<__nv_bfloat16, 1, 128>(a, w, num_sms, s);
+  return pair ? mx4::launch_t<__half, 2, 192>(a, w, num_sms, s) : mx4::launch_t<__half, 1, 128>(a, w, num_sms, s);
 }
 
 }  // namespace moe

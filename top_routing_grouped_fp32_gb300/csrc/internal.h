@@ -134,23 +134,21 @@ cudaError_t launch_mx_dequantize(const uint8_t* values, const uint8_t* scales, m
 // (slot_row: source row t goes to rows slot_row[t k + j]; else rows are in order)
 cudaError_t launch_mx4_rows(const void* x, moe_dtype dt, int64_t rows, int64_t C, const uint32_t* slot_row, int k,
                             const uint32_t* offsets, int E, uint8_t* values, uint8_t* scales, cudaStream_t s);
-// weight scales [E, rows, C/32] in the order of the products (s1: up beside gate)
-cudaError_t launch_mx4_weight_scales(const uint8_t* s0, const uint8_t* s1, int64_t E, int64_t rows, int64_t C,
-                                     int64_t pieces, uint8_t* out, cudaStream_t s);
+// weight scales [E, rows, C/32] in the order of the products
+cudaError_t launch_mx4_weight_scales(const uint8_t* scales, int64_t E, int64_t rows, int64_t C, uint8_t* out,
+                                     cudaStream_t s);
 cudaError_t launch_slot_sum_f32(const float* slots, int64_t T, int k, int64_t H, void* y, moe_dtype dt,
                                 cudaStream_t s);
 
 // ---- 4-bit experts (gemm_mx4.cu) ----------------------------------------------
 struct Mx4Weights;  // prebuilt tensor maps of one 4-bit expert-weight set
-// gate, up [E,I,H/2] and down [E,H,I/2] packed; sgu, sd: scales in product order
-Mx4Weights* mx4_weights_create(const void* gate, const void* up, const void* down, const void* sgu, const void* sd,
-                               int64_t E, int64_t I, int64_t H, const char** err);
+// gate, up [E,I,H/2] and down [E,H,I/2] packed; sg, su, sd: scales in product order
+Mx4Weights* mx4_weights_create(const void* gate, const void* up, const void* down, const uint8_t* sg,
+                               const uint8_t* su, const uint8_t* sd, int64_t E, int64_t I, int64_t H,
+                               const char** err);
 void mx4_weights_destroy(Mx4Weights* w);
-// bytes of the re-ordered scales of gate and up together, and of down
-size_t mx4_gate_up_scale_bytes(int64_t E, int64_t I, int64_t H);
-size_t mx4_down_scale_bytes(int64_t E, int64_t I, int64_t H);
-int64_t mx4_gate_up_pieces(int64_t I);
-int64_t mx4_down_pieces(int64_t H);
+// bytes of the re-ordered scales of rows of C values
+size_t mx4_weight_scale_bytes(int64_t rows, int64_t C);
 // bytes of the scales of N activation rows of C values in product order
 size_t mx4_row_scale_bytes(int64_t N, int64_t E, int64_t C);
 struct Mx4Args {

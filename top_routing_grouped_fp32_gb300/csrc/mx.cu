@@ -218,8 +218,8 @@ mx_dequantize_rows(const uint8_t* __restrict__ values, const uint8_t* __restrict
 }
 
 // ---- activations of the 4-bit products ---------------------------------------
-// 256-row units of experts < e (ceil per expert): expert e's scale pieces begin
-// at twice that.  One block; s_off [E+1] is filled, s_unit [E+1] written.
+// 256-row units of experts < e (ceil per expert): where expert e's scales begin.
+// One block; s_off [E+1] is filled, s_unit [E+1] written.
 __device__ __forceinline__ void unit_starts(const uint32_t* s_off, int E, uint32_t* s_unit) {
   if (threadIdx.x < 32) {
     const int lane = threadIdx.x, per = (E + 31) / 32;
@@ -268,13 +268,14 @@ mx4_rows_kernel(const T* __restrict__ x, int64_t rows, int64_t C, const uint32_t
   const int lane = threadIdx.x & 31;
   const int64_t src = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
   if (src >= rows) return;
-  const int64_t steps = mx::depth_steps(C), vb = C / 2;
+  const int64_t spans = mx::spans(C), vb = C / 2;
   const uint32_t first = s_off[0], last = s_off[E];
-  for (int64_t st0 = 0; st0 < steps; st0 += 4) {
-    uint32_t q[4], w[4];
+  for (int64_t sp = 0; sp < spans; sp += 2) {
+    uint32_t q[4];
+    uint4 w[2];  // lane 0: the two spans' scales
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      const int64_t c = (st0 + u) * 256 + lane * 8;
+      const int64_t c = sp * 512 + u * 256 + lane * 8;
       float v[8];
       if (c < C) load8(x + src * C + c, v);
       else
@@ -288,7 +289,9 @@ mx4_rows_kernel(const T* __restrict__ x, int64_t rows, int64_t C, const uint32_t
       uint32_t word = b << (8 * ((lane >> 2) & 3));  // four blocks of 16 lanes in one word
       word |= __shfl_xor_sync(0xffffffffu, word, 4);
       word |= __shfl_xor_sync(0xffffffffu, word, 8);
-      w[u] = word;
+      const uint32_t next = __shfl_down_sync(0xffffffffu, word, 16);
+      if (u & 1) w[u >> 1].z = word, w[u >> 1].w = next;
+      else w[u >> 1].x = word, w[u >> 1].y = next;
     }
     for (int j = 0; j < k; ++j) {
       const uint32_t r = slot_row ? __ldg(slot_row + src * k + j) : (uint32_t)src;
@@ -300,44 +303,37 @@ mx4_rows_kernel(const T* __restrict__ x, int64_t rows, int64_t C, const uint32_t
       }
       const uint32_t local = r - s_off[lo];
       uint8_t* vr = values + (int64_t)r * vb;
-      uint8_t* sr = scales + ((int64_t)(2 * s_unit[lo] + (local >> 7)) * steps + st0) * 1024 +
-                    mx::pair_byte(local & 127u, (uint32_t)(lane >> 4) * 4u);
+      uint8_t* sr = scales + (((int64_t)(s_unit[lo] + (local >> 8)) * spans + sp) * mx::kUnitGroups + (local >> 5 & 7u)) * mx::kGroupBytes +
+                    (local & 31u) * 16;
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
-        const int64_t c = (st0 + u) * 256 + lane * 8;
+        const int64_t c = sp * 512 + u * 256 + lane * 8;
         if (c < C) *reinterpret_cast<uint32_t*>(vr + c / 2) = q[u];
-        if (st0 + u < steps && (lane & 15) == 0) *reinterpret_cast<uint32_t*>(sr + u * 1024) = w[u];
+      }
+      if (lane == 0) {
+        *reinterpret_cast<uint4*>(sr) = w[0];
+        if (sp + 1 < spans) *reinterpret_cast<uint4*>(sr + mx::kUnitGroups * mx::kGroupBytes) = w[1];
       }
     }
   }
 }
 
-// Weight scales [E, rows, C/32] (two such tensors, interleaved by 32 rows, for
-// gate and up) in the order of the products: [E][step][128-row piece] pairs.
-// A thread per (expert, step, row of a piece, half of a pair).
+// Weight scales [E, rows, C/32] in the order of the products (rows a multiple
+// of 32): a thread per row and span.
 __global__ void __launch_bounds__(kThreads)
-mx4_weight_scales_kernel(const uint8_t* __restrict__ s0, const uint8_t* __restrict__ s1, int64_t E, int64_t rows,
-                         int64_t C, int64_t steps, int64_t pieces, uint8_t* __restrict__ out) {
+mx4_weight_scales_kernel(const uint8_t* __restrict__ scales, int64_t E, int64_t rows, int64_t nb, int64_t spans,
+                         uint4* __restrict__ out) {
   const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  if (i >= E * steps * pieces * 256) return;
-  const uint32_t half = (uint32_t)(i & 1), r = (uint32_t)(i >> 1) & 127u;
-  const int64_t pair = i >> 8;  // (e * steps + step) * pieces + piece
-  const int64_t piece = pair % pieces, step = pair / pieces % steps, e = pair / pieces / steps;
-  int64_t n = piece * 128 + r;  // row of the product's operand
-  const uint8_t* s = s0;
-  if (s1) {  // 32-row groups: gate, up, gate, up ...
-    const int64_t grp = n >> 5;
-    if (grp & 1) s = s1;
-    n = (grp >> 1) * 32 + (n & 31);
-  }
-  const int64_t nb = C / 32, c0 = step * 8 + half * 4;
-  uint32_t w = 0;
+  if (i >= E * rows * spans) return;
+  const int64_t r = i % rows, span = i / rows % spans, e = i / rows / spans;
+  const uint8_t* s = scales + (e * rows + r) * nb;
+  uint32_t w[4] = {};
 #pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    const uint32_t b = n < rows && c0 + c < nb ? s[(e * rows + n) * nb + c0 + c] : 127u;
-    w |= b << (8 * c);
+  for (int c = 0; c < 16; ++c) {
+    const uint32_t b = span * 16 + c < nb ? s[span * 16 + c] : 127u;
+    w[c >> 2] |= b << (8 * (c & 3));
   }
-  *reinterpret_cast<uint32_t*>(out + pair * 1024 + mx::pair_byte(r, half * 4u)) = w;
+  out[i] = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // y[t] = sum_j slots[t k + j] (FP32, ascending j), rounded once
@@ -424,11 +420,11 @@ cudaError_t launch_mx4_rows(const void* x, moe_dtype dt, int64_t rows, int64_t C
                                      static_cast<const __half*>(x), rows, C, slot_row, k, offsets, E, values, scales);
 }
 
-cudaError_t launch_mx4_weight_scales(const uint8_t* s0, const uint8_t* s1, int64_t E, int64_t rows, int64_t C,
-                                     int64_t pieces, uint8_t* out, cudaStream_t s) {
-  const int64_t steps = mx::depth_steps(C), n = E * steps * pieces * 256;
-  mx4_weight_scales_kernel<<<(unsigned)((n + kThreads - 1) / kThreads), kThreads, 0, s>>>(s0, s1, E, rows, C, steps,
-                                                                                         pieces, out);
+cudaError_t launch_mx4_weight_scales(const uint8_t* scales, int64_t E, int64_t rows, int64_t C, uint8_t* out,
+                                     cudaStream_t s) {
+  const int64_t spans = mx::spans(C), n = E * rows * spans;
+  mx4_weight_scales_kernel<<<(unsigned)((n + kThreads - 1) / kThreads), kThreads, 0, s>>>(scales, E, rows, C / 32, spans,
+                                                                                         reinterpret_cast<uint4*>(out));
   return cudaGetLastError();
 }
 

@@ -98,20 +98,17 @@ __device__ __forceinline__ void from_e4m3x4(uint32_t q, float* v) {
   }
 }
 
-// ---- scales as the tensor cores read them -------------------------------------
-// The scale bytes of 128 rows by 4 blocks (128 columns) form one 512-byte piece,
-// row r and block c at byte 16 (r % 32) + 4 (r / 32) + c: a 32-lane by 16-byte
-// copy into tensor memory then puts the four bytes of row r into lane r % 32 of
-// column r / 32.  Two pieces side by side along a row (256 columns, one depth
-// step of the products) are one kilobyte and are loaded together.  Rows end on
-// whole pairs; bytes of blocks past the row's end are finite scales (their
-// elements are zero).
-constexpr int kPieceRows = 128, kStepCols = 256;
-__host__ __device__ inline int64_t depth_steps(int64_t C) { return (C + kStepCols - 1) / kStepCols; }
-// byte of (row r of its 128-row piece, block c) inside a pair
-__device__ __forceinline__ uint32_t pair_byte(uint32_t r, uint32_t c) {
-  return (c >> 2) * 512u + (r & 31u) * 16u + (r >> 5) * 4u + (c & 3u);
-}
+// ---- scales in the order of the products ---------------------------------------
+// The scale bytes of 32 rows by one span of 512 columns (16 blocks) form a
+// group: 16 bytes a row, so that lane r of a warp reads row r's four words of
+// four bytes at once, as tensor memory wants them (a column a word, 128 columns
+// of the row each).  The groups of one span lie together, for an expert's
+// weight rows and for 256 activation rows, so that a tile's scales of a span
+// are contiguous; the spans follow one another.  Bytes of blocks past a row's
+// end are finite scales (their elements are zero).
+constexpr int kSpanCols = 512, kGroupRows = 32, kGroupBytes = 512;
+constexpr int kUnitRows = 256, kUnitGroups = kUnitRows / kGroupRows;  // activations
+__host__ __device__ inline int64_t spans(int64_t C) { return (C + kSpanCols - 1) / kSpanCols; }
 
 }  // namespace mx
 }  // namespace moe
