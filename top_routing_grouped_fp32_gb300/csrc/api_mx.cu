@@ -121,12 +121,18 @@ moe_status mx4_forward(moe_mx4_experts_t x, const void* xin, const void* logits,
   void* w = at<void>(ws, L.weights);
   float* slots = at<float>(ws, L.slots);
   MOE_TRY_CUDA(route(idx, w, s), "routing kernel launch");
-  MOE_TRY_CUDA(moe::launch_dispatch(idx, T, E, k, offsets, nullptr, perm, at<void>(ws, L.scratch), status_word(ws),
-                                    s, slot_row),
-               "dispatch kernel launch");
-  MOE_TRY_CUDA(moe::launch_mx4_rows(xin, x->dt, T, x->H, slot_row, k, offsets, E, at<uint8_t>(ws, L.xq),
-                                    at<uint8_t>(ws, L.xs), s),
-               "4-bit row launch");
+  if (T * k <= moe::mx4_small_slots()) {
+    MOE_TRY_CUDA(moe::launch_mx4_dispatch_rows(xin, x->dt, T, x->H, idx, k, E, offsets, perm, status_word(ws),
+                                               at<uint8_t>(ws, L.xq), at<uint8_t>(ws, L.xs), x->num_sms, s),
+                 "4-bit dispatch launch");
+  } else {
+    MOE_TRY_CUDA(moe::launch_dispatch(idx, T, E, k, offsets, nullptr, perm, at<void>(ws, L.scratch), status_word(ws),
+                                      s, slot_row),
+                 "dispatch kernel launch");
+    MOE_TRY_CUDA(moe::launch_mx4_rows(xin, x->dt, T, x->H, slot_row, k, offsets, E, at<uint8_t>(ws, L.xq),
+                                      at<uint8_t>(ws, L.xs), x->num_sms, s),
+                 "4-bit row launch");
+  }
   if ((st = run_mx4(x, T * k, offsets, ws, L, slots, perm, w, ldt, s)) != MOE_OK) return st;
   MOE_TRY_CUDA(moe::launch_slot_sum_f32(slots, T, k, x->H, y, x->dt, s), "combine kernel launch");
   return ok();
@@ -257,7 +263,7 @@ moe_status moe_mx4_experts_forward(moe_mx4_experts_t x, const void* x_disp, int6
   MOE_TRY_CUDA(moe::launch_sanitize_offsets(offsets, (int)x->E, N, off_ok, status_word(ws), stream),
                "offsets check launch");
   MOE_TRY_CUDA(moe::launch_mx4_rows(x_disp, x->dt, N, x->H, nullptr, 1, off_ok, (int)x->E, at<uint8_t>(ws, L.xq),
-                                    at<uint8_t>(ws, L.xs), stream),
+                                    at<uint8_t>(ws, L.xs), x->num_sms, stream),
                "4-bit row launch");
   st = run_mx4(x, N, off_ok, ws, L, expert_out, nullptr, nullptr, MOE_F32, stream);
   return st == MOE_OK ? ok() : st;

@@ -105,6 +105,28 @@ template <typename T> __device__ __forceinline__ void unpack8(uint4 v, float* f)
   for (int i = 0; i < 8; ++i) f[i] = to_f32<T>(e[i]);
 }
 
+// ---- places in a table of running sums ------------------------------------------
+// The last e < n with table[e] <= v (table[0] <= v; entries do not decrease;
+// n <= 1024), by a converged warp: two rounds of one load and a vote.
+__device__ __forceinline__ int warp_search(const uint32_t* table, int n, uint32_t v) {
+  const int lane = threadIdx.x & 31;
+  const int c = lane * 32;
+  const uint32_t coarse = __ballot_sync(0xffffffffu, c < n && table[c] <= v);  // a run of low bits
+  const int base = (31 - __clz(coarse)) * 32;
+  const int f = base + lane;
+  const uint32_t fine = __ballot_sync(0xffffffffu, f < n && table[f] <= v);
+  return base + 31 - __clz(fine);
+}
+// a / b for a < 2^31, b >= 1: an FP32 quotient (off by one part in 2^21), then
+// single steps (none or one for quotients below 2^20)
+__device__ __forceinline__ uint32_t small_div(uint32_t a, uint32_t b) {
+  uint32_t q = (uint32_t)__fdividef((float)a, (float)b);
+  int32_t r = (int32_t)(a - q * b);
+  while (r < 0) --q, r += (int32_t)b;
+  while (r >= (int32_t)b) ++q, r -= (int32_t)b;
+  return q;
+}
+
 // Records the first device-side error in a workspace status word.
 __device__ __forceinline__ void set_status(uint32_t* status, uint32_t code) {
   if (status) atomicCAS(status, 0u, code);

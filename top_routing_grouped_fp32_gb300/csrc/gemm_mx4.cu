@@ -22,13 +22,14 @@
 //     over in pairs (512 columns, a span): one wait for eight MMAs.  The TMA and
 //     the MMA warp run their loops as whole warps and elect a lane to issue, so
 //     that operands are known to be uniform;
-//   * four more warps bring the scales of a span at a time: bulk copies several
-//     spans ahead put them into a ring of their own, each warp reads them (16
-//     bytes a lane for 32 rows), writes them to its quarter of the TMEM lanes
-//     with tcgen05.st (the MMA reads scales from all four), one set of columns
-//     for each slot pair, and arrives on the barrier of the pair's copies.
-//     (Read ahead into registers instead, two spans do not fit beside eight
-//     epilogue warps, and with one the loads' latency is the kernel's pace.)
+//   * four more warps bring the scales of a span at a time: together they copy
+//     them several spans ahead into a ring of their own (cp.async, beside the
+//     TMA unit, which is busy), then each warp reads them (16 bytes a lane for
+//     32 rows), writes them to its quarter of the TMEM lanes with tcgen05.st
+//     (the MMA reads scales from all four), one set of columns for each slot
+//     pair, and arrives on the barrier of the pair's copies.  (Read ahead into
+//     registers instead, two spans do not fit beside eight epilogue warps, and
+//     with one the loads' latency is the kernel's pace.)
 //     Copying them from shared memory (tcgen05.cp) instead holds up the MMAs:
 //     about 100 cycles a copy, six copies a stage, 404 us against 250 us of
 //     MMAs alone for the headline gate/up, and loading them by TMA takes a
@@ -171,24 +172,22 @@ struct Tile {
   bool thin;
 };
 
+// By a converged warp: every role asks for a tile at its start, and what that
+// takes is time without copies.
 __device__ __forceinline__ Tile decode_tile(uint32_t tile, const Params& p, const uint32_t* s_pref,
                                             const uint32_t* s_unit, const uint32_t* s_off, int tile_m) {
-  const uint32_t q = tile / (uint32_t)p.nb;
-  int lo = 0, hi = p.E;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (s_pref[mid] <= q) lo = mid; else hi = mid;
-  }
+  const uint32_t q = small_div(tile, (uint32_t)p.nb);
+  const int lo = warp_search(s_pref, p.E, q);
   const uint32_t mte = s_pref[lo + 1] - s_pref[lo];
   const uint32_t L = tile - s_pref[lo] * (uint32_t)p.nb;
   const uint32_t w = (uint32_t)p.panel;
-  const uint32_t pid = L / (mte * w);
+  const uint32_t pid = small_div(L, mte * w);
   const uint32_t rem = L - pid * mte * w;
   const uint32_t width = min(w, (uint32_t)p.nb - pid * w);
-  const uint32_t mt = rem / width;
+  const uint32_t mt = small_div(rem, width);
   Tile t;
   t.e = lo;
-  t.nb = (int)(pid * w + rem % width);
+  t.nb = (int)(pid * w + rem - mt * width);
   t.m0 = (int64_t)s_off[lo] + (int64_t)mt * tile_m;
   t.unit = tile_m == 256 ? s_pref[lo] + mt : s_unit[lo] + (mt >> 1);
   t.group = tile_m == 256 ? 0u : 4u * (mt & 1u);
@@ -241,7 +240,7 @@ gemm_mx4_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant_
       mbar_init(tempty_bar(a), 4 * PAIR);
     }
     for (int q = 0; q < C::SF_RING; ++q) {
-      mbar_init(sfull_bar(q), 1);
+      mbar_init(sfull_bar(q), 128);  // every thread of the scale warps
       mbar_init(sempty_bar(q), 4);
     }
     mbar_init(drain_bar, 1);
@@ -409,39 +408,41 @@ gemm_mx4_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant_
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     constexpr int G = C::GROUPS, W = C::SF_WORDS, RING = C::SF_RING;
     const uint32_t ring0 = smem_u32(sf_ring);
-    // the next span to copy (warp 10)
-    uint32_t tile = cluster_id, isp = 0, islot = 0, iphase = 0, copies = 0;
-    const uint8_t *pa = nullptr, *pb0 = nullptr, *pb1 = nullptr;
-    uint32_t bytes0 = 0, bytes1 = 0;  // of each half of B inside the weights
+    // the next span to copy: this warp's groups of A's 4 and B's G
+    const int wi = warp - 10;
+    constexpr int MINE = (G + 3) / 4;
+    uint32_t tile = cluster_id, isp = 0, islot = 0, iphase = 0;
+    const uint8_t* pa = nullptr;
+    const uint8_t* pb[MINE];
     const int64_t per = p.n_out / 32;  // groups of an expert
     bool ok = true;
     auto copy = [&]() {
       if (tile >= total_tiles) return;
       if (isp == 0) {
         const Tile t = tile_at(tile);
-        pa = p.sa + ((int64_t)t.unit * spans * mx::kUnitGroups + t.group + rank * 4) * mx::kGroupBytes;
-        // the halves of the columns: gate and up features, or down columns
-        const int64_t g0 = p.gate_up ? (int64_t)t.nb * (G / 2) : (int64_t)t.nb * G;
-        const int64_t g1 = p.gate_up ? g0 : g0 + G / 2;
-        pb0 = p.sb0 + ((int64_t)t.e * spans * per + g0) * mx::kGroupBytes;
-        pb1 = p.sb1 + ((int64_t)t.e * spans * per + g1) * mx::kGroupBytes;
-        bytes0 = (uint32_t)max((int64_t)0, min(per - g0, (int64_t)(G / 2))) * mx::kGroupBytes;
-        bytes1 = (uint32_t)max((int64_t)0, min(per - g1, (int64_t)(G / 2))) * mx::kGroupBytes;
+        pa = p.sa + ((int64_t)t.unit * spans * mx::kUnitGroups + t.group + rank * 4 + wi) * mx::kGroupBytes + lane * 16;
+#pragma unroll
+        for (int i = 0; i < MINE; ++i) {
+          const int j = wi + 4 * i;  // the halves of the columns: gate and up features, or down columns
+          const bool second = p.gate_up && j >= G / 2;
+          const int64_t g = p.gate_up ? (int64_t)t.nb * (G / 2) + (second ? j - G / 2 : j) : (int64_t)t.nb * G + j;
+          pb[i] = j < G && g < per
+                      ? (second ? p.sb1 : p.sb0) + ((int64_t)t.e * spans * per + g) * mx::kGroupBytes + lane * 16
+                      : nullptr;
+        }
       }
       ok = __all_sync(0xffffffffu, mbar_wait<false>(sempty_bar(islot), iphase ^ 1u, abort_flag, p.status));
       if (!ok) return;
-      if (elect_one()) {
-        const uint32_t dst = ring0 + islot * C::SF_BYTES, bar = sfull_bar(islot);
-        mbar_expect_tx(bar, 4 * mx::kGroupBytes + bytes0 + bytes1);
-        bulk_load(dst, pa, 4 * mx::kGroupBytes, bar);
-        if (bytes0) bulk_load(dst + 4 * mx::kGroupBytes, pb0, bytes0, bar);
-        if (bytes1) bulk_load(dst + (4 + G / 2) * mx::kGroupBytes, pb1, bytes1, bar);
-      }
-      __syncwarp();
-      ++copies;
+      const uint32_t dst = ring0 + islot * C::SF_BYTES + wi * mx::kGroupBytes + lane * 16;
+      async_copy16(dst, pa);
       pa += mx::kUnitGroups * mx::kGroupBytes;
-      pb0 += per * mx::kGroupBytes;
-      pb1 += per * mx::kGroupBytes;
+#pragma unroll
+      for (int i = 0; i < MINE; ++i)
+        if (pb[i]) {
+          async_copy16(dst + (4 + 4 * i) * mx::kGroupBytes, pb[i]);
+          pb[i] += per * mx::kGroupBytes;
+        }
+      async_copy_arrive(sfull_bar(islot));
       if (++isp == (uint32_t)spans) {
         isp = 0;
         tile += num_clusters;
@@ -451,12 +452,11 @@ gemm_mx4_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant_
         iphase ^= 1u;
       }
     };
-    if (warp == 10)
-      for (int i = 0; i < RING - 1; ++i) copy();
+    for (int i = 0; i < RING - 1; ++i) copy();
     uint32_t pr = 0, phase = 0, slot = 0, sphase = 0;
     for (uint32_t mine = cluster_id; ok && mine < total_tiles; mine += num_clusters) {
       for (int sp = 0; sp < spans; ++sp) {
-        if (warp == 10) copy();
+        copy();
         ok = ok && __all_sync(0xffffffffu, mbar_wait<false>(sfull_bar(slot), sphase, abort_flag, p.status));
         if (!ok) break;
         uint32_t w[W];
@@ -495,13 +495,7 @@ gemm_mx4_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant_
         }
       }
     }
-    if (!ok && warp == 10 && lane == 0) {  // aborting: let the copies in flight land before exit
-      for (uint32_t i = copies > RING ? copies - RING : 0; i < copies; ++i) {
-        const uint64_t t0 = global_timer();
-        while (!mbar_test<false>(sfull_bar(i % RING), (i / RING) & 1u) && global_timer() - t0 < kWaitLimitNs) {
-        }
-      }
-    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
   } else {
     // ------------------------------------------------------------ epilogue
     // four warps for each accumulator: they have the time of two tiles
@@ -613,7 +607,8 @@ gemm_mx4_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant_
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
-        if constexpr (kCluster) mbar_arrive_cluster(tempty0_leader + 8u * acc);
+        // its TMEM reads are done; a release would wait for the tile's stores
+        if constexpr (kCluster) mbar_arrive_cluster_relaxed(tempty0_leader + 8u * acc);
         else mbar_arrive(tempty_bar(acc));
       }
       acc_phase ^= 1u;

@@ -915,7 +915,8 @@ grouped_gemm_tc(const __grid_constant__ CUtensorMap mapA, const __grid_constant_
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
-        if constexpr (kCluster) mbar_arrive_cluster(tempty0_leader + 8u * acc);
+        // its TMEM reads are done; a release would wait for the tile's stores
+        if constexpr (kCluster) mbar_arrive_cluster_relaxed(tempty0_leader + 8u * acc);
         else mbar_arrive(tempty_bar(acc));
       }
       acc ^= 1u;

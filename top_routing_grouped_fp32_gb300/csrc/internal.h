@@ -133,7 +133,14 @@ cudaError_t launch_mx_dequantize(const uint8_t* values, const uint8_t* scales, m
 // 16-bit rows to e2m1 in dispatch order, scales in the order of the products
 // (slot_row: source row t goes to rows slot_row[t k + j]; else rows are in order)
 cudaError_t launch_mx4_rows(const void* x, moe_dtype dt, int64_t rows, int64_t C, const uint32_t* slot_row, int k,
-                            const uint32_t* offsets, int E, uint8_t* values, uint8_t* scales, cudaStream_t s);
+                            const uint32_t* offsets, int E, uint8_t* values, uint8_t* scales, int num_sms,
+                            cudaStream_t s);
+// the same with the dispatch, for T k <= mx4_small_slots(): sorts idx [T, k],
+// writes offsets [E+1], perm [T k] and zeroes *status
+int64_t mx4_small_slots();
+cudaError_t launch_mx4_dispatch_rows(const void* x, moe_dtype dt, int64_t T, int64_t C, const uint32_t* idx, int k,
+                                     int E, uint32_t* offsets, uint32_t* perm, uint32_t* status, uint8_t* values,
+                                     uint8_t* scales, int num_sms, cudaStream_t s);
 // weight scales [E, rows, C/32] in the order of the products
 cudaError_t launch_mx4_weight_scales(const uint8_t* scales, int64_t E, int64_t rows, int64_t C, uint8_t* out,
                                      cudaStream_t s);

@@ -7,6 +7,8 @@
 // three tensors and rows do not matter: four lanes share a block (8 values
 // each), a warp holds 32 blocks.  Other rows take a warp per row and a lane per
 // value.
+#include <algorithm>
+
 #include "common.cuh"
 #include "internal.h"
 #include "mx.cuh"
@@ -94,42 +96,44 @@ mx_quantize_blocks(const T* __restrict__ x, int64_t blocks, uint8_t* __restrict_
   if (b0 + lane < blocks) scales[b0 + lane] = (uint8_t)mine;
 }
 
-// any row length and alignment: a warp per row, a lane per value of a block
+// any row length and alignment: a warp per row and kSegment columns, a lane per
+// value of a block, all blocks in flight
+constexpr int kSegBlocks = 16, kSegment = 32 * kSegBlocks;
 template <typename T, int FMT>
 __global__ void __launch_bounds__(kThreads)
-mx_quantize_rows(const T* __restrict__ x, int64_t R, int64_t C, uint8_t* __restrict__ values,
+mx_quantize_rows(const T* __restrict__ x, int64_t R, int64_t C, int segs, uint8_t* __restrict__ values,
                  uint8_t* __restrict__ scales) {
   const int lane = threadIdx.x & 31;
-  const int64_t r = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  const int64_t w = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  const int64_t r = w / segs;
   if (r >= R) return;
-  const T* xr = x + r * C;
+  const int64_t c0 = (w - r * segs) * kSegment;
   const int64_t nb = (C + 31) / 32;
-  uint8_t* sr = scales + r * nb;
-  uint8_t* vr = values + r * (FMT == MOE_MXFP4 ? (C + 1) / 2 : C);
-  constexpr int U = 4;  // blocks in flight
-  for (int64_t b0 = 0; b0 < nb; b0 += U) {
-    float v[U];
+  const T* xr = x + r * C + c0;
+  uint8_t* sr = scales + r * nb + c0 / 32;
+  uint8_t* vr = values + (FMT == MOE_MXFP4 ? r * ((C + 1) / 2) + c0 / 2 : r * C + c0);
+  const int left = (int)min((int64_t)kSegment, C - c0);
+  float v[kSegBlocks];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t c = (b0 + u) * 32 + lane;
-      v[u] = c < C ? to_f32<T>(xr[c]) : 0.f;
-    }
+  for (int u = 0; u < kSegBlocks; ++u) v[u] = u * 32 + lane < left ? to_f32<T>(xr[u * 32 + lane]) : 0.f;
+  uint32_t mine = 0;  // lane u: the byte of block u
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t c = (b0 + u) * 32 + lane;
-      const uint32_t a = __reduce_max_sync(0xffffffffu, mx::abs_bits(v[u]));
-      const uint32_t b = mx::scale_byte<FMT>(a);
-      const float q[4] = {b == 255u ? 0.f : v[u] * mx::inverse_scale(b), 0.f, 0.f, 0.f};
-      if constexpr (FMT == MOE_MXFP8) {
-        if (c < C) vr[c] = (uint8_t)mx::to_e4m3x4(q);
-      } else {
-        const float q1 = __shfl_down_sync(0xffffffffu, q[0], 1);
-        const float both[8] = {q[0], q1, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        if (c < C && (lane & 1) == 0) vr[c >> 1] = (uint8_t)mx::to_e2m1x8(both);
-      }
-      if (b0 + u < nb && lane == 0) sr[b0 + u] = (uint8_t)b;
+  for (int u = 0; u < kSegBlocks; ++u) {
+    if (u * 32 >= left) break;
+    const int c = u * 32 + lane;
+    const uint32_t a = __reduce_max_sync(0xffffffffu, mx::abs_bits(v[u]));
+    const uint32_t b = mx::scale_byte<FMT>(a);
+    const float q[4] = {b == 255u ? 0.f : v[u] * mx::inverse_scale(b), 0.f, 0.f, 0.f};
+    if constexpr (FMT == MOE_MXFP8) {
+      if (c < left) vr[c] = (uint8_t)mx::to_e4m3x4(q);
+    } else {
+      const float q1 = __shfl_down_sync(0xffffffffu, q[0], 1);
+      const float both[8] = {q[0], q1, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      if (c < left && (lane & 1) == 0) vr[c >> 1] = (uint8_t)mx::to_e2m1x8(both);
     }
+    if (lane == u) mine = b;
   }
+  if (lane * 32 < left) sr[lane] = (uint8_t)mine;
 }
 
 template <int FMT>
@@ -189,31 +193,37 @@ mx_dequantize_gather(const uint8_t* __restrict__ values, const uint8_t* __restri
   }
 }
 
-// any row length and alignment, with or without a map
+// any row length and alignment, with or without a map: as mx_quantize_rows
 template <typename T, int FMT>
 __global__ void __launch_bounds__(kThreads)
 mx_dequantize_rows(const uint8_t* __restrict__ values, const uint8_t* __restrict__ scales, int64_t R, int64_t C,
-                   const uint32_t* __restrict__ perm, uint32_t k, int64_t n, T* __restrict__ out) {
+                   int segs, const uint32_t* __restrict__ perm, uint32_t k, int64_t n, T* __restrict__ out) {
   const int lane = threadIdx.x & 31;
-  const int64_t r = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  const int64_t w = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  const int64_t r = w / segs;
   if (r >= n) return;
+  const int64_t c0 = (w - r * segs) * kSegment;
   const int64_t src = perm ? (int64_t)(__ldg(perm + r) / k) : r;
-  const int64_t nb = (C + 31) / 32, vb = FMT == MOE_MXFP4 ? (C + 1) / 2 : C;
-  T* o = out + r * C;
-#pragma unroll 4
-  for (int64_t c = lane; c < C; c += 32) {
-    float f = 0.f;
-    if (src < R) {
-      const float s = mx::scale_value(__ldg(scales + src * nb + (c >> 5)));
-      float v[8];
-      if constexpr (FMT == MOE_MXFP4) {
-        mx::from_e2m1x8((uint32_t)__ldg(values + src * vb + (c >> 1)) >> (4 * (c & 1)), v);
-      } else {
-        mx::from_e4m3x4((uint32_t)__ldg(values + src * vb + c), v);
-      }
-      f = v[0] * s;
-    }
-    o[c] = from_f32<T>(f);
+  const int left = src < R ? (int)min((int64_t)kSegment, C - c0) : 0;  // values to read
+  const int64_t nb = (C + 31) / 32;
+  const uint8_t* vr = values + (FMT == MOE_MXFP4 ? src * ((C + 1) / 2) + c0 / 2 : src * C + c0);
+  uint32_t q[kSegBlocks];
+#pragma unroll
+  for (int u = 0; u < kSegBlocks; ++u) {
+    const int c = u * 32 + lane;
+    q[u] = c < left ? (uint32_t)__ldg(vr + (FMT == MOE_MXFP4 ? c >> 1 : c)) : 0u;
+  }
+  // lane u: the byte of block u
+  const uint32_t mine = lane * 32 < left ? (uint32_t)__ldg(scales + src * nb + c0 / 32 + lane) : 0u;
+  T* o = out + r * C + c0;
+  const int end = (int)min((int64_t)kSegment, C - c0);
+#pragma unroll
+  for (int u = 0; u < kSegBlocks; ++u) {
+    const float s = mx::scale_value(__shfl_sync(0xffffffffu, mine, u));
+    float v[8];
+    if constexpr (FMT == MOE_MXFP4) mx::from_e2m1x8(q[u] >> (4 * (lane & 1)), v);
+    else mx::from_e4m3x4(q[u], v);
+    if (u * 32 + lane < end) o[u * 32 + lane] = from_f32<T>(v[0] * s);
   }
 }
 
@@ -246,73 +256,151 @@ __device__ __forceinline__ void unit_starts(const uint32_t* s_off, int E, uint32
   }
 }
 
+constexpr int kSmallSlots = 256;
+
 // Rows of C values (C a multiple of 32) to e2m1 in dispatch order, scales in
-// the order of the products.  A warp per source row; a lane holds 8 values of
-// each 256.  With slot_row, source row t goes to the dispatch rows
+// the order of the products.  A warp per source row, 8 values a lane, 1024
+// columns at a time; the next columns (or the next row's) are asked for before
+// these are rounded.  A block makes its table of expert starts once and takes
+// many rows.  With slot_row, source row t goes to the dispatch rows
 // slot_row[t k + j]: a token is read and rounded once however many experts it
 // goes to.
-template <typename T>
-__global__ void __launch_bounds__(kThreads)
+// SMALL: dispatch too, for batches of at most kSmallSlots slots: every block
+// sorts the slots idx [rows, k] itself (a count, a scan, and for each slot the
+// number of equal experts before it, so in the order of moe_dispatch) and the
+// first one writes offsets and perm.  A decode step is a chain of short
+// kernels; this takes two out of it (27.5 -> 23.6 us for one token over 64
+// experts of 2048 x 1408, replayed from a graph).
+struct SmallDispatch {
+  const uint32_t* idx;
+  uint32_t* offsets;
+  uint32_t* perm;
+  uint32_t* status;
+};
+template <typename T, bool SMALL>
+__global__ void __launch_bounds__(kThreads, 3)
 mx4_rows_kernel(const T* __restrict__ x, int64_t rows, int64_t C, const uint32_t* __restrict__ slot_row, int k,
                 const uint32_t* __restrict__ offsets, int E, uint8_t* __restrict__ values,
-                uint8_t* __restrict__ scales) {
+                uint8_t* __restrict__ scales, const SmallDispatch sd) {
   extern __shared__ uint32_t s_mem[];
   uint32_t* s_off = s_mem;
   uint32_t* s_unit = s_mem + E + 1;
-  pdl_wait();
-  pdl_trigger();
-  for (int i = threadIdx.x; i <= E; i += kThreads) s_off[i] = offsets[i];
-  __syncthreads();
-  unit_starts(s_off, E, s_unit);
-  __syncthreads();
+  uint32_t* s_expert = s_unit + E + 1;     // SMALL
+  uint32_t* s_row = s_expert + kSmallSlots;
   const int lane = threadIdx.x & 31;
-  const int64_t src = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  if (src >= rows) return;
-  const int64_t spans = mx::spans(C), vb = C / 2;
-  const uint32_t first = s_off[0], last = s_off[E];
-  for (int64_t sp = 0; sp < spans; sp += 2) {
-    uint32_t q[4];
-    uint4 w[2];  // lane 0: the two spans' scales
+  const int64_t warps = (int64_t)gridDim.x * kWarps;
+  int64_t src = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  const int64_t vb = C / 2;
+  const int chunks = (int)((C + 1023) / 1024);
+  uint4 raw[4];
+  auto load = [&](int64_t row, int chunk) {
+    const T* p = x + row * C + (int64_t)chunk * 1024;
+    const int left = (int)(C - (int64_t)chunk * 1024);
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      const int64_t c = sp * 512 + u * 256 + lane * 8;
-      float v[8];
-      if (c < C) load8(x + src * C + c, v);
-      else
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = 0.f;
-      uint32_t a = max8(v);
-      a = max(a, __shfl_xor_sync(0xffffffffu, a, 1));
-      a = max(a, __shfl_xor_sync(0xffffffffu, a, 2));
-      const uint32_t b = mx::scale_byte<MOE_MXFP4>(a);
-      q[u] = encode8<MOE_MXFP4>(v, b).x;
-      uint32_t word = b << (8 * ((lane >> 2) & 3));  // four blocks of 16 lanes in one word
-      word |= __shfl_xor_sync(0xffffffffu, word, 4);
-      word |= __shfl_xor_sync(0xffffffffu, word, 8);
-      const uint32_t next = __shfl_down_sync(0xffffffffu, word, 16);
-      if (u & 1) w[u >> 1].z = word, w[u >> 1].w = next;
-      else w[u >> 1].x = word, w[u >> 1].y = next;
+      const int c = u * 256 + lane * 8;
+      raw[u] = c < left ? *reinterpret_cast<const uint4*>(p + c) : make_uint4(0u, 0u, 0u, 0u);
     }
-    for (int j = 0; j < k; ++j) {
-      const uint32_t r = slot_row ? __ldg(slot_row + src * k + j) : (uint32_t)src;
-      if (r < first || r >= last) continue;
-      int lo = 0, hi = E;  // s_off[lo] <= r < s_off[hi]
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (s_off[mid] <= r) lo = mid; else hi = mid;
+  };
+  pdl_wait();
+  pdl_trigger();
+  if (src < rows) load(src, 0);
+  if constexpr (SMALL) {
+    static_assert(kSmallSlots <= kThreads, "a thread per slot");
+    const int n = (int)rows * k, i = threadIdx.x;
+    // counts one place up, so that their running sum is the offsets
+    for (int e = i; e <= E; e += kThreads) s_off[e] = 0;
+    const uint32_t mine = i < n ? min(sd.idx[i], (uint32_t)(E - 1)) : 0u;
+    if (i < n) s_expert[i] = mine;
+    __syncthreads();
+    if (i < n) atomicAdd(&s_off[mine + 1], 1u);
+    uint32_t before = 0;
+    for (int j = 0; j < i && i < n; ++j) before += s_expert[j] == mine ? 1u : 0u;
+    __syncthreads();
+    if (i < 32) {  // running sum of the counts, in runs of consecutive experts a lane
+      const int per = (E + 32) / 32;
+      uint32_t loc = 0;
+      for (int q = 0; q < per; ++q)
+        if (i * per + q <= E) loc += s_off[i * per + q];
+      uint32_t incl = loc;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const uint32_t o = __shfl_up_sync(0xffffffffu, incl, d);
+        if (i >= d) incl += o;
       }
-      const uint32_t local = r - s_off[lo];
-      uint8_t* vr = values + (int64_t)r * vb;
-      uint8_t* sr = scales + (((int64_t)(s_unit[lo] + (local >> 8)) * spans + sp) * mx::kUnitGroups + (local >> 5 & 7u)) * mx::kGroupBytes +
-                    (local & 31u) * 16;
+      uint32_t run = incl - loc;
+      for (int q = 0; q < per; ++q) {
+        const int e = i * per + q;
+        if (e <= E) {
+          run += s_off[e];
+          s_off[e] = run;
+        }
+      }
+    }
+    __syncthreads();
+    if (i < n) s_row[i] = s_off[mine] + before;
+    if (blockIdx.x == 0) {
+      for (int e = i; e <= E; e += kThreads) sd.offsets[e] = s_off[e];
+      if (i < n) sd.perm[s_off[mine] + before] = (uint32_t)i;
+      if (i == 0) *sd.status = 0u;
+    }
+  } else {
+    for (int i = threadIdx.x; i <= E; i += kThreads) s_off[i] = offsets[i];
+    __syncthreads();
+  }
+  unit_starts(s_off, E, s_unit);
+  __syncthreads();
+  const uint32_t first = s_off[0], last = s_off[E];
+  const int64_t spans = mx::spans(C);
+  for (; src < rows; src += warps) {
+    for (int chunk = 0; chunk < chunks; ++chunk) {
+      float v[4][8];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) unpack8<T>(raw[u], v[u]);
+      if (chunk + 1 < chunks) load(src, chunk + 1);
+      else if (src + warps < rows) load(src + warps, 0);
+      uint32_t q[4], w[8];  // w: the chunk's two spans of scales
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
-        const int64_t c = sp * 512 + u * 256 + lane * 8;
-        if (c < C) *reinterpret_cast<uint32_t*>(vr + c / 2) = q[u];
+        uint32_t a = max8(v[u]);
+        a = max(a, __shfl_xor_sync(0xffffffffu, a, 1));
+        a = max(a, __shfl_xor_sync(0xffffffffu, a, 2));
+        const uint32_t b = mx::scale_byte<MOE_MXFP4>(a);
+        q[u] = encode8<MOE_MXFP4>(v[u], b).x;
+        uint32_t word = b << (8 * ((lane >> 2) & 3));  // four blocks of 16 lanes in one word
+        word |= __shfl_xor_sync(0xffffffffu, word, 4);
+        word |= __shfl_xor_sync(0xffffffffu, word, 8);
+        w[2 * u] = word;
+        w[2 * u + 1] = __shfl_xor_sync(0xffffffffu, word, 16);
       }
-      if (lane == 0) {
-        *reinterpret_cast<uint4*>(sr) = w[0];
-        if (sp + 1 < spans) *reinterpret_cast<uint4*>(sr + mx::kUnitGroups * mx::kGroupBytes) = w[1];
+      const int left = (int)(C - (int64_t)chunk * 1024);
+      for (int j = 0; j < k; ++j) {
+        uint32_t r;
+        int e;
+        if constexpr (SMALL) {
+          r = s_row[src * k + j];
+          e = (int)s_expert[src * k + j];
+        } else {
+          r = slot_row ? __ldg(slot_row + src * k + j) : (uint32_t)src;
+          if (r < first || r >= last) continue;
+          e = warp_search(s_off, E, r);
+        }
+        const uint32_t local = r - s_off[e];
+        uint8_t* vr = values + (int64_t)r * vb + (int64_t)chunk * 512;
+        uint8_t* sr = scales +
+                      (((int64_t)(s_unit[e] + (local >> 8)) * spans + 2 * chunk) * mx::kUnitGroups + (local >> 5 & 7u)) *
+                          mx::kGroupBytes +
+                      (local & 31u) * 16;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int c = u * 256 + lane * 8;
+          if (c < left) *reinterpret_cast<uint32_t*>(vr + c / 2) = q[u];
+        }
+        if (lane == 0) {
+          *reinterpret_cast<uint4*>(sr) = make_uint4(w[0], w[1], w[2], w[3]);
+          if (left > 512)
+            *reinterpret_cast<uint4*>(sr + mx::kUnitGroups * mx::kGroupBytes) = make_uint4(w[4], w[5], w[6], w[7]);
+        }
       }
     }
   }
@@ -366,7 +454,9 @@ cudaError_t quantize_t(const void* x, int64_t R, int64_t C, uint8_t* values, uin
     const int64_t grid = (blocks + 32 * kWarps - 1) / (32 * kWarps);
     mx_quantize_blocks<T, FMT><<<(unsigned)grid, kThreads, 0, s>>>(xp, blocks, values, scales);
   } else {
-    mx_quantize_rows<T, FMT><<<(unsigned)((R + kWarps - 1) / kWarps), kThreads, 0, s>>>(xp, R, C, values, scales);
+    const int segs = (int)((C + kSegment - 1) / kSegment);
+    mx_quantize_rows<T, FMT><<<(unsigned)((R * segs + kWarps - 1) / kWarps), kThreads, 0, s>>>(xp, R, C, segs, values,
+                                                                                              scales);
   }
   return cudaGetLastError();
 }
@@ -383,7 +473,9 @@ cudaError_t dequantize_t(const uint8_t* values, const uint8_t* scales, int64_t R
   } else if (whole) {
     mx_dequantize_gather<T, FMT><<<by_row, kThreads, 0, s>>>(values, scales, R, C, perm, (uint32_t)k, n, o);
   } else {
-    mx_dequantize_rows<T, FMT><<<by_row, kThreads, 0, s>>>(values, scales, R, C, perm, (uint32_t)k, n, o);
+    const int segs = (int)((C + kSegment - 1) / kSegment);
+    mx_dequantize_rows<T, FMT><<<(unsigned)((n * segs + kWarps - 1) / kWarps), kThreads, 0, s>>>(
+        values, scales, R, C, segs, perm, (uint32_t)k, n, o);
   }
   return cudaGetLastError();
 }
@@ -408,16 +500,36 @@ cudaError_t launch_mx_dequantize(const uint8_t* values, const uint8_t* scales, m
 }
 #undef MOE_MX_DISPATCH
 
+template <typename T, bool SMALL>
+static cudaError_t rows_t(const void* x, int64_t rows, int64_t C, const uint32_t* slot_row, int k,
+                          const uint32_t* offsets, int E, uint8_t* values, uint8_t* scales, const SmallDispatch& sd,
+                          int num_sms, cudaStream_t s) {
+  // three blocks stay on an SM
+  const unsigned grid = (unsigned)std::min<int64_t>((rows + kWarps - 1) / kWarps, (int64_t)num_sms * 3);
+  const size_t smem = 4 * (2 * (size_t)(E + 1) + (SMALL ? 2 * kSmallSlots : 0));
+  return launch_pdl(mx4_rows_kernel<T, SMALL>, dim3(grid), dim3(kThreads), smem, s, static_cast<const T*>(x), rows, C,
+                    slot_row, k, offsets, E, values, scales, sd);
+}
+
 cudaError_t launch_mx4_rows(const void* x, moe_dtype dt, int64_t rows, int64_t C, const uint32_t* slot_row, int k,
-                            const uint32_t* offsets, int E, uint8_t* values, uint8_t* scales, cudaStream_t s) {
-  const unsigned grid = (unsigned)((rows + kWarps - 1) / kWarps);
-  const size_t smem = 8 * (size_t)(E + 1);
+                            const uint32_t* offsets, int E, uint8_t* values, uint8_t* scales, int num_sms,
+                            cudaStream_t s) {
   if (!slot_row) k = 1;
-  return dt == MOE_BF16 ? launch_pdl(mx4_rows_kernel<__nv_bfloat16>, dim3(grid), dim3(kThreads), smem, s,
-                                     static_cast<const __nv_bfloat16*>(x), rows, C, slot_row, k, offsets, E, values,
-                                     scales)
-                        : launch_pdl(mx4_rows_kernel<__half>, dim3(grid), dim3(kThreads), smem, s,
-                                     static_cast<const __half*>(x), rows, C, slot_row, k, offsets, E, values, scales);
+  const SmallDispatch sd{};
+  return dt == MOE_BF16
+             ? rows_t<__nv_bfloat16, false>(x, rows, C, slot_row, k, offsets, E, values, scales, sd, num_sms, s)
+             : rows_t<__half, false>(x, rows, C, slot_row, k, offsets, E, values, scales, sd, num_sms, s);
+}
+
+int64_t mx4_small_slots() { return kSmallSlots; }
+
+cudaError_t launch_mx4_dispatch_rows(const void* x, moe_dtype dt, int64_t T, int64_t C, const uint32_t* idx, int k,
+                                     int E, uint32_t* offsets, uint32_t* perm, uint32_t* status, uint8_t* values,
+                                     uint8_t* scales, int num_sms, cudaStream_t s) {
+  if (T * k > kSmallSlots) return cudaErrorInvalidValue;
+  const SmallDispatch sd{idx, offsets, perm, status};
+  return dt == MOE_BF16 ? rows_t<__nv_bfloat16, true>(x, T, C, nullptr, k, nullptr, E, values, scales, sd, num_sms, s)
+                        : rows_t<__half, true>(x, T, C, nullptr, k, nullptr, E, values, scales, sd, num_sms, s);
 }
 
 cudaError_t launch_mx4_weight_scales(const uint8_t* scales, int64_t E, int64_t rows, int64_t C, uint8_t* out,
