@@ -83,7 +83,12 @@ constexpr int BK = 64;         // 64 16-bit elements = one 128-byte swizzle row
 constexpr int UMMA_K = 16;
 constexpr uint32_t A_BYTES = BM * BK * 2;        // 16 KiB
 constexpr uint32_t B_HALF_BYTES = 128 * BK * 2;  // 16 KiB
-constexpr int THREADS = 192;
+// TMA warp, MMA warp, and four epilogue warps, or four for each accumulator in
+// the checkpointed backward, whose epilogues do more than its products
+template <int CK>
+constexpr int kEpilogues = CK == 2 ? 2 : 1;
+template <int CK>
+constexpr int kThreads = 64 + 128 * kEpilogues<CK>;
 constexpr uint32_t TMEM_COLS = 2 * BN;
 constexpr int MAX_E = 1024;
 
@@ -128,6 +133,10 @@ struct Params {
   // kWgrad: per-expert product over the padded row range [pad[e], pad[e+1])
   int wgrad;
   int mb;              // m-tiles per expert
+  // kWgrad with a_tail: A's rows are read where they are, not from a padded
+  // copy; a segment's last rows, short of 64, come from a copy of their own
+  // (64 rows an expert, zeros behind them; the mapA64 slot)
+  int a_tail;
   int64_t m_total;     // M of the product
   int64_t split;       // output rows per buffer (M, or I for the [dgate; dup] pair)
   // forward products on CTA pairs: a segment's last m-tile holding at most
@@ -214,6 +223,20 @@ __device__ __forceinline__ uint64_t sw128_mn_desc(uint32_t saddr) {
          | ((uint64_t)1 << 46)
          | ((uint64_t)2 << 61);
 }
+// 16 words of a lane's own row: whole 32-byte sectors where `sectors` says that
+// rows are aligned so and all words are inside, else the first `valid` (a
+// multiple of 4)
+__device__ __forceinline__ void row_store(uint32_t* dst, const uint32_t* w, int valid, int sectors) {
+  if (sectors && valid == 16) {
+    st_v8(dst, w);
+    st_v8(dst + 8, w + 8);
+  } else {
+#pragma unroll
+    for (int v = 0; v < 4; ++v)
+      if (4 * v < valid)
+        *reinterpret_cast<uint4*>(dst + 4 * v) = make_uint4(w[4 * v], w[4 * v + 1], w[4 * v + 2], w[4 * v + 3]);
+  }
+}
 // A 32-column block of a row in 8 bits: `left` of its columns (a multiple of 8)
 // lie inside the row; those behind hold zeros and do not move the scale.
 __device__ __forceinline__ void store_mx8(const uint32_t (&r)[32], uint8_t* dst, int64_t left, uint8_t* scale) {
@@ -277,24 +300,22 @@ struct Tile {
   bool thin;   // single-CTA tile of at most 32 rows: see Params::thin_a
 };
 
+// By a converged warp.
 __device__ __forceinline__ Tile decode_tile(uint32_t tile, const Params& p, const uint32_t* s_pref,
                                             const uint32_t* s_off, int tile_m) {
-  const uint32_t q = tile / (uint32_t)p.nb;
-  int lo = 0, hi = p.E;  // s_pref[lo] <= q < s_pref[hi]
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (s_pref[mid] <= q) lo = mid; else hi = mid;
-  }
+  const uint32_t q = small_div(tile, (uint32_t)p.nb);
+  const int lo = warp_search(s_pref, p.E, q);
   const uint32_t mte = s_pref[lo + 1] - s_pref[lo];
   const uint32_t L = tile - s_pref[lo] * (uint32_t)p.nb;
   const uint32_t w = (uint32_t)p.panel;
-  const uint32_t pid = L / (mte * w);
+  const uint32_t pid = small_div(L, mte * w);
   const uint32_t rem = L - pid * mte * w;
   const uint32_t width = min(w, (uint32_t)p.nb - pid * w);
+  const uint32_t mt = small_div(rem, width);
   Tile t;
   t.e = lo;
-  t.nb = (int)(pid * w + rem % width);
-  t.m0 = (int64_t)s_off[lo] + (int64_t)(rem / width) * tile_m;
+  t.nb = (int)(pid * w + rem - mt * width);
+  t.m0 = (int64_t)s_off[lo] + (int64_t)mt * tile_m;
   t.kx0 = 0;
   t.nk = p.k_blocks;
   t.half = p.half_tails && (int64_t)s_off[lo + 1] - t.m0 <= BM;
@@ -324,7 +345,7 @@ __device__ __forceinline__ Tile decode_wgrad(uint32_t tile, const Params& p, int
 // da product of the checkpointed backward (kSwigluBwd on da's own accumulators)
 // and weight gradients stored in T.
 template <typename T, int PAIR, int KS, int CK>
-__global__ void __launch_bounds__(THREADS, 1)
+__global__ void __launch_bounds__(kThreads<CK>, 1)
 grouped_gemm_tc(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapB0,
                 const __grid_constant__ CUtensorMap mapB1, const __grid_constant__ CUtensorMap mapA64,
                 const Params p) {
@@ -349,7 +370,7 @@ grouped_gemm_tc(const __grid_constant__ CUtensorMap mapA, const __grid_constant_
   auto tempty_bar = [&](int a) { return bar0 + 8u * (2 * STAGES + 2 + a); };
   const uint32_t drain_bar = bar0 + 8u * (2 * STAGES + 4);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int E = p.E;
   const uint32_t rank = kCluster ? cluster_rank() : 0u;  // this CTA's half of the pair tile
   const bool leader = rank == 0;
@@ -371,7 +392,7 @@ grouped_gemm_tc(const __grid_constant__ CUtensorMap mapA, const __grid_constant_
   }
   if (warp == 0 && lane == 0) {
     prefetch_map(&mapA);
-    if (p.half_tails || p.thin_a) prefetch_map(&mapA64);
+    if (p.half_tails || p.thin_a || p.a_tail) prefetch_map(&mapA64);
     prefetch_map(&mapB0);
     prefetch_map(&mapB1);
   }
@@ -380,7 +401,7 @@ grouped_gemm_tc(const __grid_constant__ CUtensorMap mapA, const __grid_constant_
   // from here on the kernel reads what earlier kernels wrote
   pdl_wait();
   pdl_trigger();
-  for (int i = threadIdx.x; i <= E; i += THREADS) s_off[i] = p.offsets[i];
+  for (int i = threadIdx.x; i <= E; i += kThreads<CK>) s_off[i] = p.offsets[i];
   __syncthreads();
   if (warp == 2) {  // s_pref[e] = number of (128*PAIR)-row tiles of experts < e
     const int per = (E + 31) / 32;
@@ -409,9 +430,9 @@ grouped_gemm_tc(const __grid_constant__ CUtensorMap mapA, const __grid_constant_
   __syncthreads();
   if constexpr (kCluster) cluster_sync();  // the peer's barriers exist before any remote use
   tc_fence_after();
-  const uint32_t tmem_base = *tmem_slot;
-  const uint32_t total_tiles =
-      p.wgrad ? (uint32_t)E * (uint32_t)(p.mb * p.nb) : s_pref[E] * (uint32_t)p.nb;
+  const uint32_t tmem_base = __shfl_sync(0xffffffffu, *tmem_slot, 0);
+  const uint32_t total_tiles = __shfl_sync(
+      0xffffffffu, p.wgrad ? (uint32_t)E * (uint32_t)(p.mb * p.nb) : s_pref[E] * (uint32_t)p.nb, 0);
   auto tile_at = [&](uint32_t tile) {
     return p.wgrad ? decode_wgrad(tile, p, C::TILE_M) : decode_tile(tile, p, s_pref, s_off, C::TILE_M);
   };
@@ -421,38 +442,45 @@ grouped_gemm_tc(const __grid_constant__ CUtensorMap mapA, const __grid_constant_
 
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer
-    if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0;
-      uint32_t last_fill[STAGES];
-      bool filled[STAGES];
-      for (int s = 0; s < STAGES; ++s) filled[s] = false, last_fill[s] = 0;
-      bool ok = true;
-      for (uint32_t tile = cluster_id; ok && tile < total_tiles; tile += num_clusters) {
-        const Tile t = tile_at(tile);
-        // A's row (K-major) or M column (MN-major) of this CTA's half: 128
-        // rows, or 64 for a half tile
-        int a_row = (int)(t.m0 + (int64_t)rank * (t.half ? BM / 2 : BM));
-        if (p.a_row_pad) a_row += (int)(__ldg(p.pad + t.e) - s_off[t.e]);
-        const int b0row = t.nb * p.cols_per_tile;
-        const int b1row = b0row + p.b1_row_off;
-        // interleaved gate/up B (pairs): this CTA's 64 gate rows and the same 64 up rows
-        const int birow = b0row + (int)rank * 64;
-        const CUtensorMap* ma = (t.half || t.thin) ? &mapA64 : &mapA;
-        const uint32_t stage_tx = t.half   ? (C::STAGE_BYTES - KS * A_BYTES / 2) * PAIR
-                                  : t.thin ? (C::STAGE_BYTES - KS * (A_BYTES - A_BYTES / 4)) * PAIR
-                                           : C::STAGE_BYTES * PAIR;
-        for (int kb = 0; kb < t.nk; ++kb) {
-          if (!mbar_wait<kCluster>(empty_bar(stage), phase ^ 1u, abort_flag, p.status)) {
-            ok = false;
-            break;
-          }
+    // This warp and the next run their loops whole, so that the operands of
+    // copies and MMAs are known to be the same in every lane, and elect one
+    // lane to issue (issued by a single lane in a branch of its own, four MMAs
+    // take as long to issue as to run).
+    int stage = 0;
+    uint32_t phase = 0, fills = 0;
+    bool ok = true;
+    for (uint32_t tile = cluster_id; ok && tile < total_tiles; tile += num_clusters) {
+      const Tile t = tile_at(tile);
+      const int te = __shfl_sync(0xffffffffu, t.e, 0);
+      const int tnb = __shfl_sync(0xffffffffu, t.nb, 0);
+      const int kx0 = __shfl_sync(0xffffffffu, t.kx0, 0);
+      const int nk = __shfl_sync(0xffffffffu, t.nk, 0);
+      const bool half = __all_sync(0xffffffffu, t.half), thin = __all_sync(0xffffffffu, t.thin);
+      // A's row (K-major) or M column (MN-major) of this CTA's half: 128
+      // rows, or 64 for a half tile
+      int row = (int)(t.m0 + (int64_t)rank * (half ? BM / 2 : BM));
+      if (p.a_row_pad) row += (int)(__ldg(p.pad + t.e) - s_off[t.e]);
+      const int a_row = __shfl_sync(0xffffffffu, row, 0);
+      const int a_k0 = p.a_tail ? __shfl_sync(0xffffffffu, (int)s_off[t.e], 0) : 0;
+      const bool a_cut = p.a_tail && __all_sync(0xffffffffu, ((s_off[t.e + 1] - s_off[t.e]) & 63u) != 0);
+      const int b0row = tnb * p.cols_per_tile;
+      const int b1row = b0row + p.b1_row_off;
+      // interleaved gate/up B (pairs): this CTA's 64 gate rows and the same 64 up rows
+      const int birow = b0row + (int)rank * 64;
+      const CUtensorMap* ma = (half || thin) ? &mapA64 : &mapA;
+      const uint32_t stage_tx = half   ? (C::STAGE_BYTES - KS * A_BYTES / 2) * PAIR
+                                : thin ? (C::STAGE_BYTES - KS * (A_BYTES - A_BYTES / 4)) * PAIR
+                                       : C::STAGE_BYTES * PAIR;
+      for (int kb = 0; kb < nk; ++kb) {
+        ok = __all_sync(0xffffffffu, mbar_wait<kCluster>(empty_bar(stage), phase ^ 1u, abort_flag, p.status));
+        if (!ok) break;
+        if (elect_one()) {
           const uint32_t sa = ring + stage * C::STAGE_BYTES;
           const uint32_t fb = full0_leader + 8u * stage;
           // K coordinates of this k-block: A's, and B's (row or column)
           const bool second = p.kb_split > 0 && kb >= p.kb_split;  // [dg | du] . [W_gate ; W_up]: up half
-          const int kx = second ? p.a_k2 + (kb - p.kb_split) * BK : t.kx0 + kb * BK * KS;
-          const int kb_b = second ? (kb - p.kb_split) * BK : t.kx0 + kb * BK;
+          const int kx = second ? p.a_k2 + (kb - p.kb_split) * BK : kx0 + kb * BK * KS;
+          const int kb_b = second ? (kb - p.kb_split) * BK : kx0 + kb * BK;
           const CUtensorMap* mb = second ? &mapB1 : &mapB0;
           if (leader) mbar_expect_tx(full_bar(stage), stage_tx);
           if constexpr (KS == 2) {  // K-major A and B only: KS sub-blocks of 64
@@ -462,20 +490,23 @@ grouped_gemm_tc(const __grid_constant__ CUtensorMap mapA, const __grid_constant_
               const uint32_t sbs = sa + KS * A_BYTES + sub * C::B_BYTES;
               tma_load_2d<PAIR>(sa + sub * A_BYTES, ma, kxs, a_row, fb);
               if constexpr (PAIR == 1) {
-                tma_load_3d<PAIR>(sbs, &mapB0, kxs, b0row, t.e, fb);
-                tma_load_3d<PAIR>(sbs + B_HALF_BYTES, &mapB1, kxs, b1row, t.e, fb);
+                tma_load_3d<PAIR>(sbs, &mapB0, kxs, b0row, te, fb);
+                tma_load_3d<PAIR>(sbs + B_HALF_BYTES, &mapB1, kxs, b1row, te, fb);
               } else if (p.b_inter) {
-                tma_load_3d<PAIR>(sbs, &mapB0, kxs, birow, t.e, fb);
-                tma_load_3d<PAIR>(sbs + B_HALF_BYTES / 2, &mapB1, kxs, birow, t.e, fb);
+                tma_load_3d<PAIR>(sbs, &mapB0, kxs, birow, te, fb);
+                tma_load_3d<PAIR>(sbs + B_HALF_BYTES / 2, &mapB1, kxs, birow, te, fb);
               } else if (leader) {
-                tma_load_3d<PAIR>(sbs, &mapB0, kxs, b0row, t.e, fb);
+                tma_load_3d<PAIR>(sbs, &mapB0, kxs, b0row, te, fb);
               } else {
-                tma_load_3d<PAIR>(sbs, &mapB1, kxs, b1row, t.e, fb);
+                tma_load_3d<PAIR>(sbs, &mapB1, kxs, b1row, te, fb);
               }
             }
           } else if (p.a_mn) {  // two 64-column boxes of this CTA's 128 M values
-            tma_load_2d<PAIR>(sa, &mapA, a_row, kx, fb);
-            tma_load_2d<PAIR>(sa + MN_BOX_BYTES, &mapA, a_row + 64, kx, fb);
+            const bool cut = a_cut && kb == nk - 1;
+            const CUtensorMap* mk = cut ? &mapA64 : &mapA;
+            const int ka = cut ? te * BK : p.a_tail ? a_k0 + kb * BK : kx;
+            tma_load_2d<PAIR>(sa, mk, a_row, ka, fb);
+            tma_load_2d<PAIR>(sa + MN_BOX_BYTES, mk, a_row + 64, ka, fb);
           } else {
             tma_load_2d<PAIR>(sa, ma, kx, a_row, fb);
           }
@@ -483,46 +514,45 @@ grouped_gemm_tc(const __grid_constant__ CUtensorMap mapA, const __grid_constant_
             // loaded above
           } else if (p.b_form == kBKmajor3d) {
             if constexpr (PAIR == 1) {
-              tma_load_3d<PAIR>(sa + A_BYTES, &mapB0, kx, b0row, t.e, fb);
-              tma_load_3d<PAIR>(sa + A_BYTES + B_HALF_BYTES, &mapB1, kx, b1row, t.e, fb);
+              tma_load_3d<PAIR>(sa + A_BYTES, &mapB0, kx, b0row, te, fb);
+              tma_load_3d<PAIR>(sa + A_BYTES + B_HALF_BYTES, &mapB1, kx, b1row, te, fb);
             } else if (p.b_inter) {
-              tma_load_3d<PAIR>(sa + A_BYTES, &mapB0, kx, birow, t.e, fb);
-              tma_load_3d<PAIR>(sa + A_BYTES + B_HALF_BYTES / 2, &mapB1, kx, birow, t.e, fb);
+              tma_load_3d<PAIR>(sa + A_BYTES, &mapB0, kx, birow, te, fb);
+              tma_load_3d<PAIR>(sa + A_BYTES + B_HALF_BYTES / 2, &mapB1, kx, birow, te, fb);
             } else if (leader) {
-              tma_load_3d<PAIR>(sa + A_BYTES, &mapB0, kx, b0row, t.e, fb);
+              tma_load_3d<PAIR>(sa + A_BYTES, &mapB0, kx, b0row, te, fb);
             } else {
-              tma_load_3d<PAIR>(sa + A_BYTES, &mapB1, kx, b1row, t.e, fb);
+              tma_load_3d<PAIR>(sa + A_BYTES, &mapB1, kx, b1row, te, fb);
             }
           } else {  // MN-major B: this CTA's N columns in boxes of 64
-            const int n0 = t.nb * 256 + (PAIR == 2 ? (int)rank * 128 : 0);
+            const int n0 = tnb * 256 + (PAIR == 2 ? (int)rank * 128 : 0);
 #pragma unroll
             for (int j = 0; j < (PAIR == 2 ? 2 : 4); ++j) {
               const uint32_t dst = sa + A_BYTES + j * MN_BOX_BYTES;
-              if (p.b_form == kBMNmajor3d) tma_load_3d<PAIR>(dst, mb, n0 + 64 * j, kb_b, t.e, fb);
+              if (p.b_form == kBMNmajor3d) tma_load_3d<PAIR>(dst, mb, n0 + 64 * j, kb_b, te, fb);
               else tma_load_2d<PAIR>(dst, mb, n0 + 64 * j, kb_b, fb);
             }
           }
-          filled[stage] = true;
-          last_fill[stage] = phase;
-          if (++stage == STAGES) {
-            stage = 0;
-            phase ^= 1u;
-          }
+        }
+        __syncwarp();
+        ++fills;
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1u;
         }
       }
-      if (!ok && leader) {  // aborting: let the copies in flight land before exit
-        for (int s = 0; s < STAGES; ++s) {
-          if (!filled[s]) continue;
-          const uint64_t t0 = global_timer();
-          while (!mbar_test<kCluster>(full_bar(s), last_fill[s]) &&
-                 global_timer() - t0 < kWaitLimitNs) {
-          }
+    }
+    if (!ok && leader && lane == 0) {  // aborting: let the copies in flight land before exit
+      for (uint32_t i = fills > STAGES ? fills - STAGES : 0; i < fills; ++i) {
+        const uint64_t t0 = global_timer();
+        while (!mbar_test<kCluster>(full_bar(i % STAGES), (i / STAGES) & 1u) &&
+               global_timer() - t0 < kWaitLimitNs) {
         }
       }
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer (leader CTA)
-    if (lane == 0 && leader) {
+    if (leader) {
       const uint32_t idesc = make_idesc(sizeof(T) == 2 && !std::is_same<T, __half>::value, C::TILE_M) |
                              ((uint32_t)(p.a_mn != 0) << 15) | ((uint32_t)(p.b_form != kBKmajor3d) << 16);
       // half tile: M = 128 over the pair (the M field is bits 24-28, M >> 4)
@@ -538,51 +568,58 @@ grouped_gemm_tc(const __grid_constant__ CUtensorMap mapA, const __grid_constant_
       bool ok = true;
       for (uint32_t tile = cluster_id; ok && tile < total_tiles; tile += num_clusters) {
         const Tile tt = tile_at(tile);
-        const int nk = tt.nk;  // 0 for an expert without rows (weight gradients)
-        const uint32_t id = tt.half ? idesc_half : idesc;
-        if (!mbar_wait<kCluster>(tempty_bar(acc), acc_phase ^ 1u, abort_flag, p.status)) break;
+        const int nk = __shfl_sync(0xffffffffu, tt.nk, 0);  // 0 for an expert without rows (weight gradients)
+        const uint32_t id = __all_sync(0xffffffffu, tt.half) ? idesc_half : idesc;
+        ok = __all_sync(0xffffffffu, mbar_wait<kCluster>(tempty_bar(acc), acc_phase ^ 1u, abort_flag, p.status));
+        if (!ok) break;
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + acc * BN;
         for (int kb = 0; kb < nk; ++kb) {
-          if (!mbar_wait<kCluster>(full_bar(stage), phase, abort_flag, p.status)) {
-            ok = false;
-            break;
-          }
+          ok = __all_sync(0xffffffffu, mbar_wait<kCluster>(full_bar(stage), phase, abort_flag, p.status));
+          if (!ok) break;
           tc_fence_after();
-          const uint32_t sa = ring + stage * C::STAGE_BYTES;
-          const uint32_t sb = sa + KS * A_BYTES;
+          if (elect_one()) {
+            const uint32_t sa = ring + stage * C::STAGE_BYTES;
+            const uint32_t sb = sa + KS * A_BYTES;
 #pragma unroll
-          for (int q = 0; q < KS * (BK / UMMA_K); ++q) {
-            const int sub = q / (BK / UMMA_K), kk = q % (BK / UMMA_K);
-            const uint32_t ak = sa + sub * A_BYTES + kk * a_step, bk = sb + sub * C::B_BYTES + kk * b_step;
-            umma_f16<PAIR>(d_tmem, a_hi | ((ak & 0x3FFFFu) >> 4), b_hi | ((bk & 0x3FFFFu) >> 4), id,
-                           (kb | q) != 0 ? 1u : 0u);
+            for (int q = 0; q < KS * (BK / UMMA_K); ++q) {
+              const int sub = q / (BK / UMMA_K), kk = q % (BK / UMMA_K);
+              const uint32_t ak = sa + sub * A_BYTES + kk * a_step, bk = sb + sub * C::B_BYTES + kk * b_step;
+              umma_f16<PAIR>(d_tmem, a_hi | ((ak & 0x3FFFFu) >> 4), b_hi | ((bk & 0x3FFFFu) >> 4), id,
+                             (kb | q) != 0 ? 1u : 0u);
+            }
+            umma_commit<PAIR>(empty_bar(stage));  // ring stage free (in every CTA) once done
           }
-          umma_commit<PAIR>(empty_bar(stage));  // ring stage free (in every CTA) once done
+          __syncwarp();
           if (++stage == STAGES) {
             stage = 0;
             phase ^= 1u;
           }
         }
         if (!ok) break;
-        umma_commit<PAIR>(tfull_bar(acc));  // accumulator ready for the epilogues
+        if (elect_one()) umma_commit<PAIR>(tfull_bar(acc));  // accumulator ready for the epilogues
+        __syncwarp();
         acc ^= 1u;
         if (acc == 0) acc_phase ^= 1u;
       }
-      // every MMA this thread issued must be complete before TMEM is freed
-      umma_commit_local<PAIR>(drain_bar);
-      const uint64_t t0 = global_timer();
-      while (!mbar_test<false>(drain_bar, 0) && global_timer() - t0 < kWaitLimitNs) {
+      // every MMA this warp issued must be complete before TMEM is freed
+      if (elect_one()) {
+        umma_commit_local<PAIR>(drain_bar);
+        const uint64_t t0 = global_timer();
+        while (!mbar_test<false>(drain_bar, 0) && global_timer() - t0 < kWaitLimitNs) {
+        }
       }
+      __syncwarp();
     }
   } else {
     // ------------------------------------------------------------ epilogue
     const int quarter = warp & 3;  // this warp may access TMEM lanes 32*quarter .. +31
     uint32_t* stg = staging + quarter * (STG_BYTES_PER_WARP / 4);
-    uint32_t acc = 0, acc_phase = 0;
+    constexpr int EG = kEpilogues<CK>;  // with two groups of warps, each keeps to its accumulator
+    uint32_t acc = EG == 2 ? (uint32_t)(warp - 2) >> 2 : 0u, acc_phase = 0;
     T* out = static_cast<T*>(p.out);
-    for (uint32_t tile = cluster_id; tile < total_tiles; tile += num_clusters) {
-      const Tile t = tile_at(tile);
+    for (uint64_t tile = cluster_id + acc * num_clusters; tile < total_tiles; tile += EG * num_clusters) {
+      const Tile t = tile_at((uint32_t)tile);
       // full tile: lane l of quarter q is row 32q + l of this CTA's 128, all
       // N columns.  Half tile (M = 128 over the pair): the CTA's 64 rows sit
       // in lanes 0-63 with N columns 0-127 and again in lanes 64-127 with N
@@ -667,9 +704,11 @@ grouped_gemm_tc(const __grid_constant__ CUtensorMap mapA, const __grid_constant_
               put4(wa + 4 * v, pack8<T>(fa));
             }
             const int vw = min(16, valid_words<T>(I - col0 - 32 * ci));
-            staged_store<16>(stg, wdg, dgp ? dgp + 16 * ci : nullptr, vw, lane);
-            staged_store<16>(stg, wdu, dup_p ? dup_p + 16 * ci : nullptr, vw, lane);
-            staged_store<16>(stg, wa, ap ? ap + 16 * ci : nullptr, vw, lane);
+            if (store) {
+              row_store(dgp + 16 * ci, wdg, vw, p.v8_out);
+              row_store(dup_p + 16 * ci, wdu, vw, p.v8_out);
+              row_store(ap + 16 * ci, wa, vw, p.v8_out);
+            }
           }
         } else {
           // kWgrad: rows of a weight-gradient tile, rounded once to T (an
@@ -683,11 +722,15 @@ grouped_gemm_tc(const __grid_constant__ CUtensorMap mapA, const __grid_constant_
               rowt = static_cast<T*>(p.out2) + ((int64_t)t.e * (p.m_total - p.split) + grow - p.split) * p.n_out + col0;
           }
           uint32_t* rowp = reinterpret_cast<uint32_t*>(rowt);
-#pragma unroll 1
-          for (int c = 0; c < 256; c += 32) {
-            uint32_t o[32], w[16];
-            tmem_ld32(taddr + c, o);
-            tmem_wait_ld(o);
+          // the next 32 columns are read from TMEM while these are packed and stored
+          uint32_t ob[2][32];
+          tmem_ld32(taddr, ob[0]);
+          tmem_wait_ld(ob[0]);
+#pragma unroll
+          for (int ci = 0; ci < 8; ++ci) {
+            if (ci + 1 < 8) tmem_ld32(taddr + 32 * ci + 32, ob[(ci + 1) & 1]);
+            const uint32_t* o = ob[ci & 1];
+            uint32_t w[16];
 #pragma unroll
             for (int v = 0; v < 4; ++v) {
               float f[8];
@@ -695,7 +738,9 @@ grouped_gemm_tc(const __grid_constant__ CUtensorMap mapA, const __grid_constant_
               for (int i = 0; i < 8; ++i) f[i] = t.nk == 0 ? 0.f : __uint_as_float(o[v * 8 + i]);
               put4(w + 4 * v, pack8<T>(f));
             }
-            staged_store<16>(stg, w, rowp ? rowp + c / 2 : nullptr, valid_words<T>(p.n_out - col0 - c), lane);
+            const int vw = min(16, valid_words<T>(p.n_out - col0 - 32 * ci));
+            if (rowp && vw > 0) row_store(rowp + 16 * ci, w, vw, p.v8_out);
+            if (ci + 1 < 8) tmem_wait_ld(ob[(ci + 1) & 1]);
           }
         }
       } else if (p.mode == kGateUpSwiglu) {
@@ -919,8 +964,8 @@ grouped_gemm_tc(const __grid_constant__ CUtensorMap mapA, const __grid_constant_
         if constexpr (kCluster) mbar_arrive_cluster_relaxed(tempty0_leader + 8u * acc);
         else mbar_arrive(tempty_bar(acc));
       }
-      acc ^= 1u;
-      if (acc == 0) acc_phase ^= 1u;
+      if constexpr (EG == 1) acc ^= 1u;
+      if (EG == 2 || acc == 0) acc_phase ^= 1u;
     }
   }
 
@@ -1026,7 +1071,7 @@ cudaError_t resident_clusters(int num_sms, int* out) {
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     cfg.gridDim = dim3(PAIR * (num_sms / PAIR));
-    cfg.blockDim = dim3(THREADS);
+    cfg.blockDim = dim3(kThreads<CK>);
     cfg.dynamicSmemBytes = smem_bytes<PAIR, KS>(MAX_E);
     cfg.attrs = attr;
     cfg.numAttrs = 1;
@@ -1068,7 +1113,7 @@ cudaError_t launch_t(int64_t N, int E, const CUtensorMap& mA, const CUtensorMap&
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // see pdl_wait
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.gridDim = dim3(nclu * PAIR);
-  cfg.blockDim = dim3(THREADS);
+  cfg.blockDim = dim3(kThreads<CK>);
   cfg.dynamicSmemBytes = smem_bytes<PAIR, KS>(E);
   cfg.stream = s;
   cfg.attrs = attr;
@@ -1284,42 +1329,12 @@ cudaError_t backward_t(const ExpertsBwdArgs& a, const TcWeights* w, char* ws, in
   return cudaSuccess;
 }
 
-// Work beside the caller's stream: run() forks it off `s` onto a stream of its
-// own, join() makes `s` wait for it.  While `s` is being captured into a graph
-// run() works on `s` itself.
-struct SideStream {
-  cudaEvent_t done = nullptr;
-  ~SideStream() {
-    if (done) cudaEventDestroy(done);
-  }
-  template <typename F>
-  cudaError_t run(cudaStream_t s, F&& work) {
-    cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
-    cudaError_t err = cudaStreamIsCapturing(s, &capture);
-    if (err != cudaSuccess) return err;
-    if (capture != cudaStreamCaptureStatusNone) return work(s);
-    cudaStream_t side = nullptr;
-    cudaEvent_t fork = nullptr;
-    if ((err = cudaStreamCreateWithFlags(&side, cudaStreamNonBlocking)) != cudaSuccess) return err;
-    err = cudaEventCreateWithFlags(&fork, cudaEventDisableTiming);
-    if (err == cudaSuccess) err = cudaEventCreateWithFlags(&done, cudaEventDisableTiming);
-    if (err == cudaSuccess) err = cudaEventRecord(fork, s);
-    if (err == cudaSuccess) err = cudaStreamWaitEvent(side, fork, 0);
-    if (err == cudaSuccess) err = work(side);
-    if (err == cudaSuccess) err = cudaEventRecord(done, side);
-    cudaStreamDestroy(side);  // its resources go once the work is done
-    if (fork) cudaEventDestroy(fork);
-    return err;
-  }
-  cudaError_t join(cudaStream_t s) { return done ? cudaStreamWaitEvent(s, done, 0) : cudaSuccess; }
-};
-
 // The checkpointed backward: products 1 and 2 above become one (da stays in
 // the accumulators, g and u come from the checkpoint), x's padded rows are read
 // from its 8-bit tokens, and the weight gradients are stored in T.
 struct CkLayout {
   int64_t npad;
-  size_t pad, dgduP, actP, xP, doutP, total;
+  size_t pad, dgduP, actP, xP, tails, total;
 };
 
 CkLayout ck_layout(int64_t N, int E, int64_t H, int64_t I) {
@@ -1335,7 +1350,7 @@ CkLayout ck_layout(int64_t N, int E, int64_t H, int64_t I) {
   L.dgduP = take((size_t)L.npad * 2 * I * 2);
   L.actP = take((size_t)L.npad * I * 2);
   L.xP = take((size_t)L.npad * H * 2);
-  L.doutP = take((size_t)L.npad * H * 2);
+  L.tails = take((size_t)E * BK * H * 2);
   L.total = off;
   return L;
 }
@@ -1350,27 +1365,19 @@ cudaError_t backward_ck_t(const ExpertsCkBwdArgs& a, char* ws, int num_sms, cuda
   void* dgduP = ws + L.dgduP;
   void* actP = ws + L.actP;
   void* xP = ws + L.xP;
-  void* doutP = ws + L.doutP;
-  CUtensorMap mDo, mDo64, mDgduP, mDgduP64, mWdMN, mWgMN, mWuMN, mDgduMN, mXMN, mDoMN, mActMN;
+  void* tails = ws + L.tails;
+  CUtensorMap mDo, mDo64, mDgduP, mDgduP64, mWdMN, mWgMN, mWuMN, mDgduMN, mXMN, mDoMN, mTailMN, mActMN;
   if (!encode_2d(&mDo, a.dout, dt, N, H) || !encode_2d(&mDo64, a.dout, dt, N, H, 64) ||
       !encode_2d(&mDgduP, dgduP, dt, L.npad, 2 * I) || !encode_2d(&mDgduP64, dgduP, dt, L.npad, 2 * I, 64) ||
       !encode_3d_mn(&mWdMN, a.down, dt, E, H, I) || !encode_3d_mn(&mWgMN, a.gate, dt, E, I, H) ||
       !encode_3d_mn(&mWuMN, a.up, dt, E, I, H) || !encode_2d_mn(&mDgduMN, dgduP, dt, L.npad, 2 * I) ||
-      !encode_2d_mn(&mXMN, xP, dt, L.npad, H) || !encode_2d_mn(&mDoMN, doutP, dt, L.npad, H) ||
+      !encode_2d_mn(&mXMN, xP, dt, L.npad, H) || !encode_2d_mn(&mDoMN, a.dout, dt, N, H) || !encode_2d_mn(&mTailMN, tails, dt, (uint64_t)E * BK, H) ||
       !encode_2d_mn(&mActMN, actP, dt, L.npad, I))
     return cudaErrorInvalidValue;
   cudaError_t err;
 #define MOE_TC_TRY(x) \
   if ((err = (x)) != cudaSuccess) return err
   MOE_TC_TRY(launch_pad_offsets(a.offsets, E, pad, s));
-  auto pad_both = [&](cudaStream_t q) {
-    cudaError_t e = launch_pad_rows_mx8(a.x, a.x_scales, a.T, H, a.perm, a.k, a.offsets, pad, E, L.npad, xP, dt, q);
-    return e == cudaSuccess ? launch_pad_rows(a.dout, H, a.offsets, pad, E, L.npad, doutP, q) : e;
-  };
-  // the padded rows are needed by the weight gradients only: on a side stream
-  // they co-run with the products before (on `s` itself while it is captured)
-  SideStream side;
-  MOE_TC_TRY(side.run(s, pad_both));
   const bool pair = N >= (int64_t)BM * E;
   Params base{};
   base.offsets = a.offsets;
@@ -1393,6 +1400,7 @@ cudaError_t backward_ck_t(const ExpertsCkBwdArgs& a, char* ws, int num_sms, cuda
   p.ck_u = const_cast<uint8_t*>(a.u);
   p.ck_gs = const_cast<uint8_t*>(a.g_scales);
   p.ck_us = const_cast<uint8_t*>(a.u_scales);
+  p.v8_out = I % 16 == 0;
   MOE_TC_TRY((launch_any<T, kUse>(pair, N, E, mDo, mWdMN, mWdMN, p, num_sms, s, &mDo64)));
   // dinput = dg W_gate + du W_up
   const int kbI = (int)((I + BK - 1) / BK);
@@ -1405,9 +1413,13 @@ cudaError_t backward_ck_t(const ExpertsCkBwdArgs& a, char* ws, int num_sms, cuda
   p.n_out = H;
   p.nb = (int)((H + 255) / 256);
   p.out = a.dinput;
+  p.v8_out = H % 16 == 0 && reinterpret_cast<uintptr_t>(a.dinput) % 32 == 0;
   MOE_TC_TRY(launch_any<T>(pair, N, E, mDgduP, mWgMN, mWuMN, p, num_sms, s, &mDgduP64));
-  // weight gradients over the padded rows
-  MOE_TC_TRY(side.join(s));
+  // weight gradients over the padded rows.  (On a stream beside the products
+  // before, these copies take the same time off them: 2473 us against 2465 us
+  // in order, headline shape.)
+  MOE_TC_TRY(launch_pad_rows_mx8(a.x, a.x_scales, a.T, H, a.perm, a.k, a.offsets, pad, E, L.npad, xP, dt, s));
+  MOE_TC_TRY(launch_tail_rows(a.dout, H, a.offsets, E, tails, s));
   constexpr int TM = Cfg<2>::TILE_M;
   p = base;
   p.half_tails = 0;
@@ -1422,6 +1434,7 @@ cudaError_t backward_ck_t(const ExpertsCkBwdArgs& a, char* ws, int num_sms, cuda
   p.nb = (int)((H + 255) / 256);
   p.out = a.dgate;
   p.out2 = a.dup;
+  p.v8_out = H % 16 == 0 && (reinterpret_cast<uintptr_t>(a.dgate) | reinterpret_cast<uintptr_t>(a.dup)) % 32 == 0;
   MOE_TC_TRY((launch_t<T, 2, 1, kUse>(N, E, mDgduMN, mXMN, mXMN, p, num_sms, s)));
   p.m_total = H;
   p.split = H;
@@ -1430,7 +1443,9 @@ cudaError_t backward_ck_t(const ExpertsCkBwdArgs& a, char* ws, int num_sms, cuda
   p.nb = (int)((I + 255) / 256);
   p.out = a.ddown;
   p.out2 = a.ddown;
-  MOE_TC_TRY((launch_t<T, 2, 1, kUse>(N, E, mDoMN, mActMN, mActMN, p, num_sms, s)));
+  p.v8_out = I % 16 == 0 && reinterpret_cast<uintptr_t>(a.ddown) % 32 == 0;
+  p.a_tail = 1;
+  MOE_TC_TRY((launch_t<T, 2, 1, kUse>(N, E, mDoMN, mActMN, mActMN, p, num_sms, s, &mTailMN)));
 #undef MOE_TC_TRY
   return cudaSuccess;
 }

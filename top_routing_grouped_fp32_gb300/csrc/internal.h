@@ -255,7 +255,9 @@ cudaError_t launch_pad_offsets(const uint32_t* offsets, int E, uint32_t* pad, cu
 cudaError_t launch_pad_rows(const void* src, int64_t C, const uint32_t* offsets, const uint32_t* pad,
                             int E, int64_t npad_max, void* dst, cudaStream_t s);
 
-// the same from 8-bit tokens: dispatched row r is token perm[r] / k (zeros past T)
+// the last (rows of e) % 64 rows of each expert's segment, at row 64 e, zeros behind
+cudaError_t launch_tail_rows(const void* src, int64_t C, const uint32_t* offsets, int E, void* dst, cudaStream_t s);
+// pad_rows from 8-bit tokens: dispatched row r is token perm[r] / k (zeros past T)
 cudaError_t launch_pad_rows_mx8(const uint8_t* x, const uint8_t* scales, int64_t T, int64_t C, const uint32_t* perm,
                                 int k, const uint32_t* offsets, const uint32_t* pad, int E, int64_t npad_max,
                                 void* dst, moe_dtype dt, cudaStream_t s);

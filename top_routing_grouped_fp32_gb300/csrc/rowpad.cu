@@ -106,6 +106,26 @@ pad_rows_kernel(const uint4* __restrict__ src, int64_t vecs, const uint32_t* __r
   }
 }
 
+// The last count_e % 64 rows of every expert's segment: dst row 64 e + j, zeros
+// behind them (rows of C 16-bit elements, one warp per row).
+__global__ void __launch_bounds__(32 * kRowsPerBlock)
+tail_rows_kernel(const uint4* __restrict__ src, int64_t vecs, const uint32_t* __restrict__ offsets, int E,
+                 uint4* __restrict__ dst) {
+  const int row = blockIdx.x * kRowsPerBlock + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31, e = row >> 6, j = row & 63;
+  if (e >= E) return;
+  const uint32_t end = offsets[e + 1];
+  const int tail = (int)((end - offsets[e]) & 63u);
+  if (tail == 0) return;  // not read
+  uint4* d = dst + (int64_t)row * vecs;
+  if (j < tail) {
+    const uint4* s = src + ((int64_t)end - tail + j) * vecs;
+    for (int64_t v = lane; v < vecs; v += 32) d[v] = __ldg(s + v);
+  } else {
+    for (int64_t v = lane; v < vecs; v += 32) d[v] = make_uint4(0u, 0u, 0u, 0u);
+  }
+}
+
 // pad_rows of 8-bit tokens (e4m3, a scale a 32-column block), read through the
 // dispatch map and written as T: a warp per row, 8 values a lane.
 template <typename T>
@@ -145,6 +165,12 @@ pad_rows_mx8_kernel(const uint2* __restrict__ x, const uint8_t* __restrict__ sca
 }
 
 }  // namespace
+
+cudaError_t launch_tail_rows(const void* src, int64_t C, const uint32_t* offsets, int E, void* dst, cudaStream_t s) {
+  tail_rows_kernel<<<(unsigned)(E * 64 / kRowsPerBlock), 32 * kRowsPerBlock, 0, s>>>(
+      static_cast<const uint4*>(src), C / 8, offsets, E, static_cast<uint4*>(dst));
+  return cudaGetLastError();
+}
 
 cudaError_t launch_pad_rows_mx8(const uint8_t* x, const uint8_t* scales, int64_t T, int64_t C, const uint32_t* perm,
                                 int k, const uint32_t* offsets, const uint32_t* pad, int E, int64_t npad_max,

@@ -84,25 +84,26 @@ class MxRows:
         remembered and compared with what the tensors are now."""
         v, s, d = self.values, self.scales, self.__dict__
         known = d.get("_known")
-        if (known is not None and known[0] is v and known[1] is s and known[2] == (self.format, self.cols)
-                and known[3] == (shape, format, device) and v.shape == known[4] and s.shape == known[5]
-                and v.dtype is torch.uint8 and s.dtype is torch.uint8 and v.is_contiguous() and s.is_contiguous()
-                and v.get_device() == known[6] and s.get_device() == known[6]):
-            return v.data_ptr(), s.data_ptr()
-        key = (shape, format, device)
+        if known is not None:
+            kv, ks, fmt, cols, whole, vs, ss, index = known
+            if (kv is v and ks is s and fmt == self.format and cols == self.cols
+                    and (shape is None or whole == shape) and (format is None or fmt == format)
+                    and v.shape == vs and s.shape == ss and v.dtype is torch.uint8 and s.dtype is torch.uint8
+                    and v.is_contiguous() and s.is_contiguous() and v.get_device() == index
+                    and s.get_device() == index and (device is None or device.index == index)):
+                return v.data_ptr(), s.data_ptr()
         if format is not None and self.format != format:
             raise MoeError(3, f"{what} must be {format} (got {self.format})")
         _format(self.format)
-        if shape is None:
-            shape = self.shape
-        if self.shape != tuple(shape):
-            raise MoeError(2, f"{what} must have shape {tuple(shape)} (got {self.shape})")
+        whole = torch.Size(self.shape)
+        if shape is not None and whole != tuple(shape):
+            raise MoeError(2, f"{what} must have shape {tuple(shape)} (got {tuple(whole)})")
         device = v.device if device is None else device
         if not v.is_cuda:
             raise ValueError(f"{what}.values: expected a CUDA tensor")
-        vs, ss = _shapes(shape, self.format)
+        vs, ss = _shapes(whole, self.format)
         got = (_p(v, f"{what}.values", _U8, vs, device), _p(s, f"{what}.scales", _U8, ss, device))
-        d["_known"] = (v, s, (self.format, self.cols), key, v.shape, s.shape, v.get_device())
+        d["_known"] = (v, s, self.format, self.cols, whole, v.shape, s.shape, v.get_device())
         return got
 
 
@@ -110,16 +111,17 @@ def moe_mx_quantize(x: torch.Tensor, format: str, out: MxRows | None = None, str
     """Rows of x [..., C] (F32/F16/BF16) in "mxfp4" or "mxfp8" form."""
     lib = _load()
     fmt = _format(format)
-    if x.dim() < 1:
+    shape = x.shape
+    if len(shape) < 1:
         raise MoeError(2, "x must have at least one dimension")
     code, xp, dev = _code(x, "x"), _dense(x, "x"), x.device
-    C = x.shape[-1]
+    C = shape[-1]
     R = x.numel() // C if C else 0
     current, raw = _on(dev, stream)
     with current:
         if out is None:
-            out = MxRows.empty(x.shape, format, dev)
-        v, s = out._checked("out", x.shape, format, dev)
+            out = MxRows.empty(shape, format, dev)
+        v, s = out._checked("out", shape, format, dev)
         _check(lib.moe_mx_quantize(xp, code, R, C, fmt, v, s, raw))
     return out
 
@@ -131,23 +133,25 @@ def moe_mx_dequantize(mx: MxRows, dtype: torch.dtype, perm: torch.Tensor | None 
     lib = _load()
     fmt = _format(mx.format)
     v, s = mx._checked("mx")
+    shape = mx.__dict__["_known"][4]
     dev, C = mx.values.device, mx.cols
-    R = mx.values.shape[:-1].numel()
-    if dtype not in _CODES:
+    R = shape[:-1].numel()
+    code = _CODES.get(dtype)
+    if code is None:
         raise MoeError(3, f"dtype {dtype} is not F32/F16/BF16")
     if perm is None:
-        shape, n, pp = mx.shape, R, None
+        n, pp = R, None
     else:
-        if mx.values.dim() != 2 or perm.dim() != 1:
+        if len(shape) != 2 or perm.dim() != 1:
             raise MoeError(2, "perm [N] needs rows [T, C]")
         n = perm.shape[0]
-        shape, pp = (n, C), _p(perm, "perm", _I32, (n,), dev)
+        shape, pp = torch.Size((n, C)), _p(perm, "perm", _I32, (n,), dev)
     current, raw = _on(dev, stream)
     with current:
         if out is None:
             out = torch.empty(shape, dtype=dtype, device=dev)
         _check(lib.moe_mx_dequantize(v, s, fmt, R, C, pp, top_k, n, _p(out, "out", (dtype,), shape, dev),
-                                     _CODES[dtype], raw))
+                                     code, raw))
     return out
 
 
