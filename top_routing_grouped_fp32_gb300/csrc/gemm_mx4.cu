@@ -537,23 +537,31 @@ gemm_mx4_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant_
           tmem_ld32(taddr + BN / 2 + b * 32, u);
           tmem_wait_ld(g);
           reg_fence(u);
-          float h[32];
+          float2 h[16];
           uint32_t a = 0;
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const float gg = __uint_as_float(g[i]), uu = __uint_as_float(u[i]);
+          for (int i = 0; i < 16; ++i) {
+            const float2 gg = make_float2(__uint_as_float(g[2 * i]), __uint_as_float(g[2 * i + 1]));
+            const float2 uu = make_float2(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1]));
+            const float2 t = mul2(gg, both(-kLog2e));
+            const float2 n = add2(make_float2(exp2_fast(t.x), exp2_fast(t.y)), both(1.f));
             // a few ulp of FP32: far below an e2m1 step
-            h[i] = __fdividef(gg * uu, 1.f + __expf(-gg));
-            a = max(a, mx::abs_bits(h[i]));
+            h[i] = mul2(mul2(gg, uu), make_float2(rcp_fast(n.x), rcp_fast(n.y)));
+            a = max(a, max(mx::abs_bits(h[i].x), mx::abs_bits(h[i].y)));
           }
           const uint32_t sb = mx::scale_byte<MOE_MXFP4>(a);
-          const float inv = mx::inverse_scale(sb);
+          // (a block with a NaN has scale NaN; its elements then do not matter)
+          const float2 inv = both(mx::inverse_scale(sb));
           uint32_t w[4];
 #pragma unroll
           for (int v = 0; v < 4; ++v) {
             float q[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) q[i] = sb == 255u ? 0.f : h[v * 8 + i] * inv;
+            for (int i = 0; i < 4; ++i) {
+              const float2 y = mul2(h[4 * v + i], inv);
+              q[2 * i] = y.x;
+              q[2 * i + 1] = y.y;
+            }
             w[v] = mx::to_e2m1x8(q);
           }
           if (row_ok) {

@@ -325,14 +325,15 @@ __device__ __forceinline__ Tile decode_tile(uint32_t tile, const Params& p, cons
 
 // Weight-gradient tiles: expert-major, then m-tile, then n-block; the K range
 // is the expert's padded column range of the transposed operands.
-__device__ __forceinline__ Tile decode_wgrad(uint32_t tile, const Params& p, int tile_m) {
+__device__ __forceinline__ Tile decode_wgrad(uint32_t tile, const Params& p, const uint32_t* s_pad, int tile_m) {
   const uint32_t per = (uint32_t)(p.mb * p.nb);
   Tile t;
-  t.e = (int)(tile / per);
+  t.e = (int)small_div(tile, per);
   const uint32_t rem = tile - (uint32_t)t.e * per;
-  t.m0 = (int64_t)(rem / (uint32_t)p.nb) * tile_m;
-  t.nb = (int)(rem % (uint32_t)p.nb);
-  const uint32_t k0 = __ldg(p.pad + t.e), k1 = __ldg(p.pad + t.e + 1);
+  const uint32_t m = small_div(rem, (uint32_t)p.nb);
+  t.m0 = (int64_t)m * tile_m;
+  t.nb = (int)(rem - m * (uint32_t)p.nb);
+  const uint32_t k0 = s_pad[t.e], k1 = s_pad[t.e + 1];
   t.kx0 = (int)k0;
   t.nk = (int)((k1 - k0) / BK);
   t.half = false;
@@ -403,7 +404,9 @@ grouped_gemm_tc(const __grid_constant__ CUtensorMap mapA, const __grid_constant_
   pdl_trigger();
   for (int i = threadIdx.x; i <= E; i += kThreads<CK>) s_off[i] = p.offsets[i];
   __syncthreads();
-  if (warp == 2) {  // s_pref[e] = number of (128*PAIR)-row tiles of experts < e
+  if (p.wgrad) {  // s_pref[e] = first padded row of expert e
+    for (int i = threadIdx.x; i <= E; i += kThreads<CK>) s_pref[i] = p.pad[i];
+  } else if (warp == 2) {  // s_pref[e] = number of (128*PAIR)-row tiles of experts < e
     const int per = (E + 31) / 32;
     uint32_t loc = 0;
     for (int i = 0; i < per; ++i) {
@@ -434,7 +437,7 @@ grouped_gemm_tc(const __grid_constant__ CUtensorMap mapA, const __grid_constant_
   const uint32_t total_tiles = __shfl_sync(
       0xffffffffu, p.wgrad ? (uint32_t)E * (uint32_t)(p.mb * p.nb) : s_pref[E] * (uint32_t)p.nb, 0);
   auto tile_at = [&](uint32_t tile) {
-    return p.wgrad ? decode_wgrad(tile, p, C::TILE_M) : decode_tile(tile, p, s_pref, s_off, C::TILE_M);
+    return p.wgrad ? decode_wgrad(tile, p, s_pref, C::TILE_M) : decode_tile(tile, p, s_pref, s_off, C::TILE_M);
   };
   // the leader CTA's barriers, as seen from this CTA
   const uint32_t full0_leader = kCluster ? mapa(full_bar(0), 0) : full_bar(0);
@@ -685,23 +688,25 @@ grouped_gemm_tc(const __grid_constant__ CUtensorMap mapA, const __grid_constant_
             }
             if (ci + 1 < nch) load(ci + 1);
             tmem_wait_ld(d);
+            if (!row_ok)  // rows not stored may hold anything; g and u are 0 there
+#pragma unroll
+              for (int i = 0; i < 32; ++i) d[i] = 0u;
+            // two values an instruction: at one, this arithmetic takes longer
+            // than the product (631 against 373 us for the headline's da)
             uint32_t wdg[16], wdu[16], wa[16];
 #pragma unroll
-            for (int v = 0; v < 4; ++v) {
-              float fdg[8], fdu[8], fa[8];
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const float gg = g[v * 8 + i] * gs, uu = u[v * 8 + i] * us;  // 0 in rows not stored
-                const float dv = row_ok ? __uint_as_float(d[v * 8 + i]) : 0.f;
-                const float sg = __fdividef(1.f, 1.f + __expf(-gg));  // 16-bit outputs
-                const float silu = gg * sg;
-                fdg[i] = dv * uu * (sg + silu * (1.f - sg));
-                fdu[i] = dv * silu;
-                fa[i] = silu * uu;
-              }
-              put4(wdg + 4 * v, pack8<T>(fdg));
-              put4(wdu + 4 * v, pack8<T>(fdu));
-              put4(wa + 4 * v, pack8<T>(fa));
+            for (int i = 0; i < 16; ++i) {
+              const float2 gg = mul2(make_float2(g[2 * i], g[2 * i + 1]), both(gs));
+              const float2 uu = mul2(make_float2(u[2 * i], u[2 * i + 1]), both(us));
+              const float2 dv = make_float2(__uint_as_float(d[2 * i]), __uint_as_float(d[2 * i + 1]));
+              const float2 t = mul2(gg, both(-kLog2e));
+              const float2 n = add2(make_float2(exp2_fast(t.x), exp2_fast(t.y)), both(1.f));
+              const float2 sg = make_float2(rcp_fast(n.x), rcp_fast(n.y));  // 16-bit outputs
+              const float2 silu = mul2(gg, sg);
+              const float2 slope = fma2(silu, fma2(sg, both(-1.f), both(1.f)), sg);
+              wdg[i] = pack2<T>(mul2(mul2(dv, uu), slope));
+              wdu[i] = pack2<T>(mul2(dv, silu));
+              wa[i] = pack2<T>(mul2(silu, uu));
             }
             const int vw = min(16, valid_words<T>(I - col0 - 32 * ci));
             if (store) {
