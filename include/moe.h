@@ -576,7 +576,8 @@ moe_status moe_distill_loss_backward(const void* logits, moe_dtype logits_dtype,
  * is not below R): tokens in dispatch order.  top_k is 1 where perm is NULL.
  * Any C in [1, 2^20]; rows are dense and may start at any element (16-byte
  * aligned x, out and values with C a multiple of 32 are the fast case).  R and
- * n below 2^31; R == 0 or n == 0 is valid and enqueues nothing.
+ * n below 2^31; R == 0 or n == 0 is valid and enqueues nothing.  Outputs do not
+ * overlap inputs or each other (MOE_ERR_INVALID_ARG).
  * ---------------------------------------------------------------------- */
 typedef enum { MOE_MXFP4 = 0, MOE_MXFP8 = 1 } moe_mx_format;
 
@@ -660,8 +661,10 @@ moe_status moe_mx4_forward_sigmoid_grouped(moe_mx4_experts_t experts, const void
  * All gradients are in the weights' dtype (dinput [N,H], dgate and dup
  * [E,I,H], ddown [E,H,I]; experts without rows get zeros).  da and all sums
  * are FP32; dg, du and a are rounded once to the dtype as operands of the
- * products, x^ too (its four significant bits fit).  N = T*top_k.  g and u are
- * not recomputed: six of the eight products of moe_experts_backward are left.
+ * products, x^ too (its four significant bits fit; a value past the dtype's
+ * range is infinite).  N = T*top_k.  The gradients overlap neither dout nor
+ * each other (MOE_ERR_INVALID_ARG).  g and u are not recomputed: six of the
+ * eight products of moe_experts_backward are left.
  * ---------------------------------------------------------------------- */
 moe_status moe_experts_forward_checkpoint(moe_experts_t experts, const void* x_disp, int64_t N,
                                           const uint32_t* offsets, void* expert_out,

@@ -811,6 +811,19 @@ moe_status moe_experts_backward_checkpoint(moe_experts_t x, const uint8_t* x_val
   if (!aligned16(x_values) || !aligned16(gate_values) || !aligned16(up_values) || !aligned16(dout) ||
       !aligned16(dinput))
     return fail(MOE_ERR_INVALID_ARG, "x, the checkpoint's values, dout and dinput must be 16-byte aligned");
+  // dout is read until the last product
+  const uint64_t rb = (uint64_t)N * x->H * 2, wb_ = (uint64_t)x->E * x->I * x->H * 2;
+  const struct {
+    const void* p;
+    uint64_t n;
+  } outs[4] = {{dinput, rb}, {dgate, wb_}, {dup, wb_}, {ddown, wb_}};
+  for (int i = 0; i < 4; ++i) {
+    if (overlap(outs[i].p, outs[i].n, dout, rb))
+      return fail(MOE_ERR_INVALID_ARG, "the gradients must not overlap dout");
+    for (int j = 0; j < i; ++j)
+      if (overlap(outs[i].p, outs[i].n, outs[j].p, outs[j].n))
+        return fail(MOE_ERR_INVALID_ARG, "the gradients must not overlap one another");
+  }
   if ((st = check_ws(ws, ws_bytes, moe_experts_backward_checkpoint_workspace_size(x, N))) != MOE_OK) return st;
   MOE_TRY_CUDA(cudaMemsetAsync(ws, 0, 4, stream), "cudaMemsetAsync");
   if (N == 0) {  // no rows: every weight gradient is zero

@@ -66,6 +66,12 @@ inline bool valid_dtype(moe_dtype d) { return d == MOE_F32 || d == MOE_F16 || d 
 inline bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 inline bool aligned256(const void* p) { return reinterpret_cast<uintptr_t>(p) % 256 == 0; }
 
+// Whether na bytes from a and nb bytes from b share any.
+inline bool overlap(const void* a, uint64_t na, const void* b, uint64_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y ? y - x < na : x - y < nb;
+}
+
 // Checks shared by the calls that take (T, E, top_k).
 inline moe_status check_tek(int64_t T, int64_t E, int32_t k) {
   if (T < 0) return fail(MOE_ERR_SHAPE, "T must be >= 0 (got %lld)", (long long)T);

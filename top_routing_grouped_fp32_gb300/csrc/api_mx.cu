@@ -22,6 +22,11 @@ using namespace moe::api;
 
 bool valid_format(moe_mx_format f) { return f == MOE_MXFP4 || f == MOE_MXFP8; }
 
+uint64_t value_bytes(int64_t R, int64_t C, moe_mx_format f) {
+  return (uint64_t)R * (f == MOE_MXFP4 ? (C + 1) / 2 : C);
+}
+uint64_t scale_bytes(int64_t R, int64_t C) { return (uint64_t)R * ((C + 31) / 32); }
+
 moe_status check_rows(int64_t n, const char* name) {
   if (n < 0) return fail(MOE_ERR_SHAPE, "%s must be >= 0 (got %lld)", name, (long long)n);
   if (n > kMaxRows) return fail(MOE_ERR_UNSUPPORTED, "%s=%lld exceeds 2^31-1", name, (long long)n);
@@ -151,6 +156,10 @@ moe_status moe_mx_quantize(const void* x, moe_dtype dt, int64_t R, int64_t C, mo
   if ((st = check_rows(R, "R")) != MOE_OK || (st = check_dim(C, "C")) != MOE_OK) return st;
   if (R == 0) return ok();
   if (!x || !values || !scales) return fail(MOE_ERR_INVALID_ARG, "x, values and scales must be non-NULL");
+  if (reinterpret_cast<uintptr_t>(x) % dtype_size(dt) != 0) return fail(MOE_ERR_INVALID_ARG, "x is misaligned for its dtype");
+  const uint64_t xb = (uint64_t)R * C * dtype_size(dt), vb = value_bytes(R, C, fmt), sb = scale_bytes(R, C);
+  if (overlap(values, vb, x, xb) || overlap(scales, sb, x, xb) || overlap(values, vb, scales, sb))
+    return fail(MOE_ERR_INVALID_ARG, "x, values and scales must not overlap");
   MOE_TRY_CUDA(moe::launch_mx_quantize(x, dt, R, C, fmt, values, scales, stream), "quantise launch");
   return ok();
 }
@@ -165,12 +174,18 @@ moe_status moe_mx_dequantize(const uint8_t* values, const uint8_t* scales, moe_m
       (st = check_dim(C, "C")) != MOE_OK)
     return st;
   if (top_k < 1) return fail(MOE_ERR_INVALID_ARG, "top_k must be >= 1 (got %d)", top_k);
+  if (n == 0) return ok();  // (an empty map has no address)
   if (!perm && n != R)
     return fail(MOE_ERR_SHAPE, "n=%lld must be R=%lld without perm", (long long)n, (long long)R);
   if (!perm && top_k != 1) return fail(MOE_ERR_INVALID_ARG, "top_k=%d needs perm", top_k);
-  if (n == 0) return ok();
   if (!out || (R > 0 && (!values || !scales)))
     return fail(MOE_ERR_INVALID_ARG, "values, scales and out must be non-NULL");
+  if (reinterpret_cast<uintptr_t>(out) % dtype_size(dt) != 0 || reinterpret_cast<uintptr_t>(perm) % 4 != 0)
+    return fail(MOE_ERR_INVALID_ARG, "out or perm is misaligned");
+  const uint64_t ob = (uint64_t)n * C * dtype_size(dt);
+  if (overlap(out, ob, values, value_bytes(R, C, fmt)) || overlap(out, ob, scales, scale_bytes(R, C)) ||
+      (perm && overlap(out, ob, perm, (uint64_t)n * 4)))
+    return fail(MOE_ERR_INVALID_ARG, "out must not overlap values, scales or perm");
   MOE_TRY_CUDA(moe::launch_mx_dequantize(values, scales, fmt, R, C, perm, top_k, n, out, dt, stream),
                "dequantise launch");
   return ok();

@@ -173,6 +173,9 @@ struct Params {
 constexpr int STG_STRIDE = 36;                         // words per staged row
 constexpr uint32_t STG_BYTES_PER_WARP = 32 * STG_STRIDE * 4;
 constexpr uint32_t STG_BYTES = 4 * STG_BYTES_PER_WARP;  // 18 KiB
+constexpr uint32_t STG16_BYTES_PER_WARP = 32 * 20 * 4;   // rows of 16 words
+template <int CK>
+constexpr uint32_t kStgBytes = CK == 2 ? 8 * STG16_BYTES_PER_WARP : STG_BYTES;
 
 __device__ __forceinline__ void put4(uint32_t* w, uint4 q) {
   w[0] = q.x;
@@ -223,20 +226,6 @@ __device__ __forceinline__ uint64_t sw128_mn_desc(uint32_t saddr) {
          | ((uint64_t)1 << 46)
          | ((uint64_t)2 << 61);
 }
-// 16 words of a lane's own row: whole 32-byte sectors where `sectors` says that
-// rows are aligned so and all words are inside, else the first `valid` (a
-// multiple of 4)
-__device__ __forceinline__ void row_store(uint32_t* dst, const uint32_t* w, int valid, int sectors) {
-  if (sectors && valid == 16) {
-    st_v8(dst, w);
-    st_v8(dst + 8, w + 8);
-  } else {
-#pragma unroll
-    for (int v = 0; v < 4; ++v)
-      if (4 * v < valid)
-        *reinterpret_cast<uint4*>(dst + 4 * v) = make_uint4(w[4 * v], w[4 * v + 1], w[4 * v + 2], w[4 * v + 3]);
-  }
-}
 // A 32-column block of a row in 8 bits: `left` of its columns (a multiple of 8)
 // lie inside the row; those behind hold zeros and do not move the scale.
 __device__ __forceinline__ void store_mx8(const uint32_t (&r)[32], uint8_t* dst, int64_t left, uint8_t* scale) {
@@ -265,10 +254,10 @@ __device__ __forceinline__ void store_mx8(const uint32_t (&r)[32], uint8_t* dst,
 }
 // The elements of such a block (zeros past `left`)
 __device__ __forceinline__ void load_mx8(const uint8_t* src, int64_t left, uint32_t (&w)[8]) {
-  if (left >= 32 && reinterpret_cast<uintptr_t>(src) % 16 == 0) {
-    const uint4 a = __ldg(reinterpret_cast<const uint4*>(src)), b = __ldg(reinterpret_cast<const uint4*>(src) + 1);
-    put4(w, a);
-    put4(w + 4, b);
+  if (left >= 32 && reinterpret_cast<uintptr_t>(src) % 32 == 0) {
+    asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                 : "l"(src));
   } else {
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
@@ -358,10 +347,10 @@ grouped_gemm_tc(const __grid_constant__ CUtensorMap mapA, const __grid_constant_
   const uint32_t ring = (raw_s + 1023u) & ~1023u;  // 1024-byte aligned for the swizzle
   uint8_t* ring_ptr = smem_raw + (ring - raw_s);
   uint32_t* staging = reinterpret_cast<uint32_t*>(ring_ptr + STAGES * C::STAGE_BYTES);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(ring_ptr + STAGES * C::STAGE_BYTES + STG_BYTES);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(ring_ptr + STAGES * C::STAGE_BYTES + kStgBytes<CK>);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * STAGES + 5);
   volatile uint32_t* abort_flag = tmem_slot + 1;
-  uint32_t* s_off = reinterpret_cast<uint32_t*>(ring_ptr + STAGES * C::STAGE_BYTES + STG_BYTES + 256);
+  uint32_t* s_off = reinterpret_cast<uint32_t*>(ring_ptr + STAGES * C::STAGE_BYTES + kStgBytes<CK> + 256);
   uint32_t* s_pref = s_off + (p.E + 1);
 
   const uint32_t bar0 = smem_u32(bars);
@@ -617,7 +606,7 @@ grouped_gemm_tc(const __grid_constant__ CUtensorMap mapA, const __grid_constant_
   } else {
     // ------------------------------------------------------------ epilogue
     const int quarter = warp & 3;  // this warp may access TMEM lanes 32*quarter .. +31
-    uint32_t* stg = staging + quarter * (STG_BYTES_PER_WARP / 4);
+    uint32_t* stg = CK == kUse ? staging + (warp - 2) * (STG16_BYTES_PER_WARP / 4) : staging + quarter * (STG_BYTES_PER_WARP / 4);
     constexpr int EG = kEpilogues<CK>;  // with two groups of warps, each keeps to its accumulator
     uint32_t acc = EG == 2 ? (uint32_t)(warp - 2) >> 2 : 0u, acc_phase = 0;
     T* out = static_cast<T*>(p.out);
@@ -709,11 +698,9 @@ grouped_gemm_tc(const __grid_constant__ CUtensorMap mapA, const __grid_constant_
               wa[i] = pack2<T>(mul2(silu, uu));
             }
             const int vw = min(16, valid_words<T>(I - col0 - 32 * ci));
-            if (store) {
-              row_store(dgp + 16 * ci, wdg, vw, p.v8_out);
-              row_store(dup_p + 16 * ci, wdu, vw, p.v8_out);
-              row_store(ap + 16 * ci, wa, vw, p.v8_out);
-            }
+            staged_store<16>(stg, wdg, dgp ? dgp + 16 * ci : nullptr, vw, lane);
+            staged_store<16>(stg, wdu, dup_p ? dup_p + 16 * ci : nullptr, vw, lane);
+            staged_store<16>(stg, wa, ap ? ap + 16 * ci : nullptr, vw, lane);
           }
         } else {
           // kWgrad: rows of a weight-gradient tile, rounded once to T (an
@@ -744,7 +731,7 @@ grouped_gemm_tc(const __grid_constant__ CUtensorMap mapA, const __grid_constant_
               put4(w + 4 * v, pack8<T>(f));
             }
             const int vw = min(16, valid_words<T>(p.n_out - col0 - 32 * ci));
-            if (rowp && vw > 0) row_store(rowp + 16 * ci, w, vw, p.v8_out);
+            staged_store<16>(stg, w, rowp ? rowp + 16 * ci : nullptr, vw, lane);
             if (ci + 1 < 8) tmem_wait_ld(ob[(ci + 1) & 1]);
           }
         }
@@ -1049,9 +1036,9 @@ bool encode_3d(CUtensorMap* m, const void* base, moe_dtype dt, uint64_t E, uint6
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int PAIR, int KS = 1>
+template <int PAIR, int KS = 1, int CK = kNone>
 size_t smem_bytes(int E) {
-  return 1024 + (size_t)Cfg<PAIR, KS>::STAGES * Cfg<PAIR, KS>::STAGE_BYTES + STG_BYTES + 256 +
+  return 1024 + (size_t)Cfg<PAIR, KS>::STAGES * Cfg<PAIR, KS>::STAGE_BYTES + kStgBytes<CK> + 256 +
          8 * (size_t)(E + 1);
 }
 
@@ -1063,7 +1050,7 @@ cudaError_t resident_clusters(int num_sms, int* out) {
   static int clusters = 0;
   std::call_once(once, [num_sms] {
     err = cudaFuncSetAttribute(grouped_gemm_tc<T, PAIR, KS, CK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               (int)smem_bytes<PAIR, KS>(MAX_E));
+                               (int)smem_bytes<PAIR, KS, CK>(MAX_E));
     if (err != cudaSuccess) return;
     if (PAIR == 1) {
       clusters = num_sms;
@@ -1077,7 +1064,7 @@ cudaError_t resident_clusters(int num_sms, int* out) {
     attr[0].val.clusterDim.z = 1;
     cfg.gridDim = dim3(PAIR * (num_sms / PAIR));
     cfg.blockDim = dim3(kThreads<CK>);
-    cfg.dynamicSmemBytes = smem_bytes<PAIR, KS>(MAX_E);
+    cfg.dynamicSmemBytes = smem_bytes<PAIR, KS, CK>(MAX_E);
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     err = cudaOccupancyMaxActiveClusters(&clusters, grouped_gemm_tc<T, PAIR, KS, CK>, &cfg);
@@ -1119,7 +1106,7 @@ cudaError_t launch_t(int64_t N, int E, const CUtensorMap& mA, const CUtensorMap&
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.gridDim = dim3(nclu * PAIR);
   cfg.blockDim = dim3(kThreads<CK>);
-  cfg.dynamicSmemBytes = smem_bytes<PAIR, KS>(E);
+  cfg.dynamicSmemBytes = smem_bytes<PAIR, KS, CK>(E);
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
@@ -1405,7 +1392,6 @@ cudaError_t backward_ck_t(const ExpertsCkBwdArgs& a, char* ws, int num_sms, cuda
   p.ck_u = const_cast<uint8_t*>(a.u);
   p.ck_gs = const_cast<uint8_t*>(a.g_scales);
   p.ck_us = const_cast<uint8_t*>(a.u_scales);
-  p.v8_out = I % 16 == 0;
   MOE_TC_TRY((launch_any<T, kUse>(pair, N, E, mDo, mWdMN, mWdMN, p, num_sms, s, &mDo64)));
   // dinput = dg W_gate + du W_up
   const int kbI = (int)((I + BK - 1) / BK);
@@ -1439,7 +1425,6 @@ cudaError_t backward_ck_t(const ExpertsCkBwdArgs& a, char* ws, int num_sms, cuda
   p.nb = (int)((H + 255) / 256);
   p.out = a.dgate;
   p.out2 = a.dup;
-  p.v8_out = H % 16 == 0 && (reinterpret_cast<uintptr_t>(a.dgate) | reinterpret_cast<uintptr_t>(a.dup)) % 32 == 0;
   MOE_TC_TRY((launch_t<T, 2, 1, kUse>(N, E, mDgduMN, mXMN, mXMN, p, num_sms, s)));
   p.m_total = H;
   p.split = H;
@@ -1448,7 +1433,6 @@ cudaError_t backward_ck_t(const ExpertsCkBwdArgs& a, char* ws, int num_sms, cuda
   p.nb = (int)((I + 255) / 256);
   p.out = a.ddown;
   p.out2 = a.ddown;
-  p.v8_out = I % 16 == 0 && reinterpret_cast<uintptr_t>(a.ddown) % 32 == 0;
   p.a_tail = 1;
   MOE_TC_TRY((launch_t<T, 2, 1, kUse>(N, E, mDoMN, mActMN, mActMN, p, num_sms, s, &mTailMN)));
 #undef MOE_TC_TRY

@@ -5,9 +5,9 @@
 // output written once, a few operations a value between.  Where rows are whole
 // blocks and the pointers are aligned, blocks lie one behind the other in all
 // three tensors and rows do not matter: four lanes share a block (8 values
-// each), a warp holds 32 blocks.  Other rows take a warp per row and a lane per
-// value.
+// each), a warp holds 32 blocks.  Other rows take a lane per value.
 #include <algorithm>
+#include <type_traits>
 
 #include "common.cuh"
 #include "internal.h"
@@ -54,6 +54,21 @@ __device__ __forceinline__ uint2 encode8(const float* v, uint32_t b) {
   else return make_uint2(mx::to_e4m3x4(q), mx::to_e4m3x4(q + 4));
 }
 
+// The bits of the largest magnitude, as FP32, of a block that four lanes hold 8
+// 16-bit values of each: two values an instruction; NaN wins.
+template <typename T>
+__device__ __forceinline__ uint32_t block_max(uint4 raw) {
+  using T2 = typename std::conditional<std::is_same<T, __half>::value, __half2, __nv_bfloat162>::type;
+  auto two = [](uint32_t w) {
+    w &= 0x7FFF7FFFu;
+    return *reinterpret_cast<T2*>(&w);
+  };
+  T2 m = __hmax2_nan(__hmax2_nan(two(raw.x), two(raw.y)), __hmax2_nan(two(raw.z), two(raw.w)));
+  m = __hmax2_nan(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  m = __hmax2_nan(m, __shfl_xor_sync(0xffffffffu, m, 2));
+  return max(mx::abs_bits(to_f32<T>(m.x)), mx::abs_bits(to_f32<T>(m.y)));
+}
+
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 
@@ -96,44 +111,58 @@ mx_quantize_blocks(const T* __restrict__ x, int64_t blocks, uint8_t* __restrict_
   if (b0 + lane < blocks) scales[b0 + lane] = (uint8_t)mine;
 }
 
-// any row length and alignment: a warp per row and kSegment columns, a lane per
-// value of a block, all blocks in flight
-constexpr int kSegBlocks = 16, kSegment = 32 * kSegBlocks;
+// Any row length and alignment: a warp takes kRun blocks, one behind the other
+// through the rows (so short rows fill it too), a lane per value, all blocks in
+// flight.  Lane u looks block u up.
+constexpr int kRun = 16;
+__device__ __forceinline__ int64_t shfl64(int64_t v, int u) {
+  return __shfl_sync(0xffffffffu, (long long)v, u);
+}
+// row and block-in-row of block i of rows of nb blocks
+__device__ __forceinline__ void place_of(int64_t i, int64_t nb, int64_t* row, int64_t* blk) {
+  *row = i < ((int64_t)1 << 32) ? (int64_t)((uint32_t)i / (uint32_t)nb) : i / nb;
+  *blk = i - *row * nb;
+}
+
 template <typename T, int FMT>
 __global__ void __launch_bounds__(kThreads)
-mx_quantize_rows(const T* __restrict__ x, int64_t R, int64_t C, int segs, uint8_t* __restrict__ values,
+mx_quantize_rows(const T* __restrict__ x, int64_t blocks, int64_t C, uint8_t* __restrict__ values,
                  uint8_t* __restrict__ scales) {
   const int lane = threadIdx.x & 31;
-  const int64_t w = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  const int64_t r = w / segs;
-  if (r >= R) return;
-  const int64_t c0 = (w - r * segs) * kSegment;
+  const int64_t b0 = ((int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5)) * kRun;
+  if (b0 >= blocks) return;
   const int64_t nb = (C + 31) / 32;
-  const T* xr = x + r * C + c0;
-  uint8_t* sr = scales + r * nb + c0 / 32;
-  uint8_t* vr = values + (FMT == MOE_MXFP4 ? r * ((C + 1) / 2) + c0 / 2 : r * C + c0);
-  const int left = (int)min((int64_t)kSegment, C - c0);
-  float v[kSegBlocks];
+  int64_t r, b;
+  place_of(min(b0 + (lane & (kRun - 1)), blocks - 1), nb, &r, &b);
+  const int64_t in = r * C + b * 32;
+  const int64_t at = FMT == MOE_MXFP4 ? r * ((C + 1) / 2) + b * 16 : in;
+  const int left = (int)min(C - b * 32, (int64_t)32);
+  const int n = (int)min((int64_t)kRun, blocks - b0);
+  float v[kRun];
 #pragma unroll
-  for (int u = 0; u < kSegBlocks; ++u) v[u] = u * 32 + lane < left ? to_f32<T>(xr[u * 32 + lane]) : 0.f;
+  for (int u = 0; u < kRun; ++u) {
+    const int64_t p = shfl64(in, u);
+    const int l = __shfl_sync(0xffffffffu, left, u);
+    v[u] = u < n && lane < l ? to_f32<T>(x[p + lane]) : 0.f;
+  }
   uint32_t mine = 0;  // lane u: the byte of block u
 #pragma unroll
-  for (int u = 0; u < kSegBlocks; ++u) {
-    if (u * 32 >= left) break;
-    const int c = u * 32 + lane;
+  for (int u = 0; u < kRun; ++u) {
     const uint32_t a = __reduce_max_sync(0xffffffffu, mx::abs_bits(v[u]));
-    const uint32_t b = mx::scale_byte<FMT>(a);
-    const float q[4] = {b == 255u ? 0.f : v[u] * mx::inverse_scale(b), 0.f, 0.f, 0.f};
+    const uint32_t sb = mx::scale_byte<FMT>(a);
+    const float q[4] = {sb == 255u ? 0.f : v[u] * mx::inverse_scale(sb), 0.f, 0.f, 0.f};
+    const int64_t p = shfl64(at, u);
+    const int l = __shfl_sync(0xffffffffu, left, u);
     if constexpr (FMT == MOE_MXFP8) {
-      if (c < left) vr[c] = (uint8_t)mx::to_e4m3x4(q);
+      if (u < n && lane < l) values[p + lane] = (uint8_t)mx::to_e4m3x4(q);
     } else {
       const float q1 = __shfl_down_sync(0xffffffffu, q[0], 1);
-      const float both[8] = {q[0], q1, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      if (c < left && (lane & 1) == 0) vr[c >> 1] = (uint8_t)mx::to_e2m1x8(both);
+      const float two[8] = {q[0], q1, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      if (u < n && lane < l && (lane & 1) == 0) values[p + (lane >> 1)] = (uint8_t)mx::to_e2m1x8(two);
     }
-    if (lane == u) mine = b;
+    if (lane == u) mine = sb;
   }
-  if (lane * 32 < left) sr[lane] = (uint8_t)mine;
+  if (lane < n) scales[b0 + lane] = (uint8_t)mine;
 }
 
 template <int FMT>
@@ -197,33 +226,36 @@ mx_dequantize_gather(const uint8_t* __restrict__ values, const uint8_t* __restri
 template <typename T, int FMT>
 __global__ void __launch_bounds__(kThreads)
 mx_dequantize_rows(const uint8_t* __restrict__ values, const uint8_t* __restrict__ scales, int64_t R, int64_t C,
-                   int segs, const uint32_t* __restrict__ perm, uint32_t k, int64_t n, T* __restrict__ out) {
+                   const uint32_t* __restrict__ perm, uint32_t k, int64_t blocks, T* __restrict__ out) {
   const int lane = threadIdx.x & 31;
-  const int64_t w = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  const int64_t r = w / segs;
-  if (r >= n) return;
-  const int64_t c0 = (w - r * segs) * kSegment;
-  const int64_t src = perm ? (int64_t)(__ldg(perm + r) / k) : r;
-  const int left = src < R ? (int)min((int64_t)kSegment, C - c0) : 0;  // values to read
+  const int64_t b0 = ((int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5)) * kRun;
+  if (b0 >= blocks) return;
   const int64_t nb = (C + 31) / 32;
-  const uint8_t* vr = values + (FMT == MOE_MXFP4 ? src * ((C + 1) / 2) + c0 / 2 : src * C + c0);
-  uint32_t q[kSegBlocks];
+  int64_t r, b;
+  place_of(min(b0 + (lane & (kRun - 1)), blocks - 1), nb, &r, &b);
+  const int64_t src = perm ? (int64_t)(__ldg(perm + r) / k) : r;
+  const int left = (int)min(C - b * 32, (int64_t)32);
+  const int held = src < R ? left : 0;  // values to read
+  const int64_t at = FMT == MOE_MXFP4 ? src * ((C + 1) / 2) + b * 16 : src * C + b * 32;
+  const int64_t to = r * C + b * 32;
+  const uint32_t mine = src < R ? (uint32_t)__ldg(scales + src * nb + b) : 0u;
+  const int n = (int)min((int64_t)kRun, blocks - b0);
+  uint32_t q[kRun];
 #pragma unroll
-  for (int u = 0; u < kSegBlocks; ++u) {
-    const int c = u * 32 + lane;
-    q[u] = c < left ? (uint32_t)__ldg(vr + (FMT == MOE_MXFP4 ? c >> 1 : c)) : 0u;
+  for (int u = 0; u < kRun; ++u) {
+    const int64_t p = shfl64(at, u);
+    const int l = __shfl_sync(0xffffffffu, held, u);
+    q[u] = u < n && lane < l ? (uint32_t)__ldg(values + p + (FMT == MOE_MXFP4 ? lane >> 1 : lane)) : 0u;
   }
-  // lane u: the byte of block u
-  const uint32_t mine = lane * 32 < left ? (uint32_t)__ldg(scales + src * nb + c0 / 32 + lane) : 0u;
-  T* o = out + r * C + c0;
-  const int end = (int)min((int64_t)kSegment, C - c0);
 #pragma unroll
-  for (int u = 0; u < kSegBlocks; ++u) {
+  for (int u = 0; u < kRun; ++u) {
     const float s = mx::scale_value(__shfl_sync(0xffffffffu, mine, u));
+    const int64_t p = shfl64(to, u);
+    const int l = __shfl_sync(0xffffffffu, left, u);
     float v[8];
     if constexpr (FMT == MOE_MXFP4) mx::from_e2m1x8(q[u] >> (4 * (lane & 1)), v);
     else mx::from_e4m3x4(q[u], v);
-    if (u * 32 + lane < end) o[u * 32 + lane] = from_f32<T>(v[0] * s);
+    if (u < n && lane < l) out[p + lane] = from_f32<T>(v[0] * s);
   }
 }
 
@@ -278,7 +310,7 @@ struct SmallDispatch {
   uint32_t* status;
 };
 template <typename T, bool SMALL>
-__global__ void __launch_bounds__(kThreads, 3)
+__global__ void __launch_bounds__(kThreads, 4)
 mx4_rows_kernel(const T* __restrict__ x, int64_t rows, int64_t C, const uint32_t* __restrict__ slot_row, int k,
                 const uint32_t* __restrict__ offsets, int E, uint8_t* __restrict__ values,
                 uint8_t* __restrict__ scales, const SmallDispatch sd) {
@@ -354,19 +386,26 @@ mx4_rows_kernel(const T* __restrict__ x, int64_t rows, int64_t C, const uint32_t
   const int64_t spans = mx::spans(C);
   for (; src < rows; src += warps) {
     for (int chunk = 0; chunk < chunks; ++chunk) {
-      float v[4][8];
+      uint4 cur[4];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) unpack8<T>(raw[u], v[u]);
+      for (int u = 0; u < 4; ++u) cur[u] = raw[u];
       if (chunk + 1 < chunks) load(src, chunk + 1);
       else if (src + warps < rows) load(src + warps, 0);
       uint32_t q[4], w[8];  // w: the chunk's two spans of scales
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
-        uint32_t a = max8(v[u]);
-        a = max(a, __shfl_xor_sync(0xffffffffu, a, 1));
-        a = max(a, __shfl_xor_sync(0xffffffffu, a, 2));
-        const uint32_t b = mx::scale_byte<MOE_MXFP4>(a);
-        q[u] = encode8<MOE_MXFP4>(v[u], b).x;
+        const uint32_t b = mx::scale_byte<MOE_MXFP4>(block_max<T>(cur[u]));
+        // (a block with a NaN has scale NaN; its elements then do not matter)
+        const float2 inv = both(mx::inverse_scale(b));
+        float v[8];
+        unpack8<T>(cur[u], v);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 y = mul2(make_float2(v[2 * i], v[2 * i + 1]), inv);
+          v[2 * i] = y.x;
+          v[2 * i + 1] = y.y;
+        }
+        q[u] = mx::to_e2m1x8(v);
         uint32_t word = b << (8 * ((lane >> 2) & 3));  // four blocks of 16 lanes in one word
         word |= __shfl_xor_sync(0xffffffffu, word, 4);
         word |= __shfl_xor_sync(0xffffffffu, word, 8);
@@ -454,9 +493,8 @@ cudaError_t quantize_t(const void* x, int64_t R, int64_t C, uint8_t* values, uin
     const int64_t grid = (blocks + 32 * kWarps - 1) / (32 * kWarps);
     mx_quantize_blocks<T, FMT><<<(unsigned)grid, kThreads, 0, s>>>(xp, blocks, values, scales);
   } else {
-    const int segs = (int)((C + kSegment - 1) / kSegment);
-    mx_quantize_rows<T, FMT><<<(unsigned)((R * segs + kWarps - 1) / kWarps), kThreads, 0, s>>>(xp, R, C, segs, values,
-                                                                                              scales);
+    const int64_t blocks = R * ((C + 31) / 32), per = kWarps * kRun;
+    mx_quantize_rows<T, FMT><<<(unsigned)((blocks + per - 1) / per), kThreads, 0, s>>>(xp, blocks, C, values, scales);
   }
   return cudaGetLastError();
 }
@@ -473,9 +511,9 @@ cudaError_t dequantize_t(const uint8_t* values, const uint8_t* scales, int64_t R
   } else if (whole) {
     mx_dequantize_gather<T, FMT><<<by_row, kThreads, 0, s>>>(values, scales, R, C, perm, (uint32_t)k, n, o);
   } else {
-    const int segs = (int)((C + kSegment - 1) / kSegment);
-    mx_dequantize_rows<T, FMT><<<(unsigned)((n * segs + kWarps - 1) / kWarps), kThreads, 0, s>>>(
-        values, scales, R, C, segs, perm, (uint32_t)k, n, o);
+    const int64_t blocks = n * ((C + 31) / 32), per = kWarps * kRun;
+    mx_dequantize_rows<T, FMT><<<(unsigned)((blocks + per - 1) / per), kThreads, 0, s>>>(values, scales, R, C, perm,
+                                                                                         (uint32_t)k, blocks, o);
   }
   return cudaGetLastError();
 }
@@ -504,8 +542,8 @@ template <typename T, bool SMALL>
 static cudaError_t rows_t(const void* x, int64_t rows, int64_t C, const uint32_t* slot_row, int k,
                           const uint32_t* offsets, int E, uint8_t* values, uint8_t* scales, const SmallDispatch& sd,
                           int num_sms, cudaStream_t s) {
-  // three blocks stay on an SM
-  const unsigned grid = (unsigned)std::min<int64_t>((rows + kWarps - 1) / kWarps, (int64_t)num_sms * 3);
+  // four blocks stay on an SM
+  const unsigned grid = (unsigned)std::min<int64_t>((rows + kWarps - 1) / kWarps, (int64_t)num_sms * 4);
   const size_t smem = 4 * (2 * (size_t)(E + 1) + (SMALL ? 2 * kSmallSlots : 0));
   return launch_pdl(mx4_rows_kernel<T, SMALL>, dim3(grid), dim3(kThreads), smem, s, static_cast<const T*>(x), rows, C,
                     slot_row, k, offsets, E, values, scales, sd);
