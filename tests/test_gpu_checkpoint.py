@@ -144,6 +144,18 @@ def test_formulas_against_differences():
             assert abs((hi - lo) / (2 * h) - grad.reshape(-1)[i]) < 1e-7 * (1 + grad.abs().max())
 
 
+@pytest.mark.parametrize("T,E,k,H,I,skew", [(1100, 1, 1, 72, 40, 0.0), (1300, 2, 2, 264, 40, 0.7), (900, 3, 1, 40, 296, 2.0)])
+def test_few_tiles_over_many_rows(cuda_lib, T, E, k, H, I, skew):
+    """Weight gradients of few tiles: the rows of an expert are cut into parts that are joined."""
+    s = Step(cuda_lib, T, E, k, H, I, torch.bfloat16, skew=skew)
+    _, ck = s.forward()
+    ws = s.ex.backward_checkpoint_workspace(T * k)
+    ws.fill_(0xFF)
+    got = s.backward(ck, workspace=ws)
+    check(s, ck, got, s.dout)
+    assert all(torch.equal(a, b) for a, b in zip(got, s.backward(ck)))
+
+
 @pytest.mark.parametrize("T,E,k,I", [(40, 4, 2, 64), (500, 2, 1, 64)])
 def test_what_is_not_finite_stays_in_its_expert(cuda_lib, T, E, k, I):
     """A NaN in a row of dout, next to a segment's end, reaches its own dinput row and its own

@@ -359,10 +359,9 @@ static moe_status experts_forward(moe_experts_t x, const void* x_disp, int64_t N
   if (!aligned16(x_disp) || !aligned16(expert_out))
     return fail(MOE_ERR_INVALID_ARG, "x_disp and expert_out must be 16-byte aligned");
   if ((st = check_ws(ws, ws_bytes, moe_experts_workspace_size(x, N))) != MOE_OK) return st;
-  MOE_TRY_CUDA(cudaMemsetAsync(ws, 0, 4, stream), "cudaMemsetAsync");
   uint32_t* off_ok = reinterpret_cast<uint32_t*>(static_cast<char*>(ws) + kWsHeader +
                                                  align_up((size_t)N * x->I * dtype_size(x->dt), 1024));
-  MOE_TRY_CUDA(moe::launch_sanitize_offsets(offsets, (int)x->E, N, off_ok, status_word(ws), stream),
+  MOE_TRY_CUDA(moe::launch_check_offsets(offsets, (int)x->E, N, off_ok, status_word(ws), nullptr, stream),
                "offsets check launch");
   st = run_experts(x, x_disp, N, off_ok, static_cast<char*>(ws) + kWsHeader, expert_out,
                    moe::kDownPlain, nullptr, nullptr, MOE_F32, status_word(ws), stream, nullptr, ck);
@@ -825,9 +824,9 @@ moe_status moe_experts_backward_checkpoint(moe_experts_t x, const uint8_t* x_val
         return fail(MOE_ERR_INVALID_ARG, "the gradients must not overlap one another");
   }
   if ((st = check_ws(ws, ws_bytes, moe_experts_backward_checkpoint_workspace_size(x, N))) != MOE_OK) return st;
-  MOE_TRY_CUDA(cudaMemsetAsync(ws, 0, 4, stream), "cudaMemsetAsync");
   if (N == 0) {  // no rows: every weight gradient is zero
     const size_t wb = (size_t)x->E * x->I * x->H * 2;
+    MOE_TRY_CUDA(cudaMemsetAsync(ws, 0, 4, stream), "cudaMemsetAsync");
     MOE_TRY_CUDA(cudaMemsetAsync(dgate, 0, wb, stream), "cudaMemsetAsync");
     MOE_TRY_CUDA(cudaMemsetAsync(dup, 0, wb, stream), "cudaMemsetAsync");
     MOE_TRY_CUDA(cudaMemsetAsync(ddown, 0, wb, stream), "cudaMemsetAsync");
@@ -835,9 +834,8 @@ moe_status moe_experts_backward_checkpoint(moe_experts_t x, const uint8_t* x_val
   }
   char* base = static_cast<char*>(ws) + align_up(kWsHeader + offsets_copy_bytes(x), 1024);
   uint32_t* off_ok = reinterpret_cast<uint32_t*>(static_cast<char*>(ws) + kWsHeader);
-  MOE_TRY_CUDA(moe::launch_sanitize_offsets(offsets, (int)x->E, N, off_ok, status_word(ws), stream),
-               "offsets check launch");
   moe::ExpertsCkBwdArgs a{};
+  a.offsets_in = offsets;
   a.dt = x->dt;
   a.E = (int)x->E;
   a.k = top_k;
@@ -848,7 +846,7 @@ moe_status moe_experts_backward_checkpoint(moe_experts_t x, const uint8_t* x_val
   a.x = x_values;
   a.x_scales = x_scales;
   a.perm = perm;
-  a.offsets = off_ok;
+  a.offsets = off_ok;  // checked there
   a.g = gate_values;
   a.g_scales = gate_scales;
   a.u = up_values;

@@ -134,8 +134,8 @@ moe_status mx4_forward(moe_mx4_experts_t x, const void* xin, const void* logits,
     MOE_TRY_CUDA(moe::launch_dispatch(idx, T, E, k, offsets, nullptr, perm, at<void>(ws, L.scratch), status_word(ws),
                                       s, slot_row),
                  "dispatch kernel launch");
-    MOE_TRY_CUDA(moe::launch_mx4_rows(xin, x->dt, T, x->H, slot_row, k, offsets, E, at<uint8_t>(ws, L.xq),
-                                      at<uint8_t>(ws, L.xs), x->num_sms, s),
+    MOE_TRY_CUDA(moe::launch_mx4_rows(xin, x->dt, T, x->H, slot_row, k, offsets, E, nullptr, nullptr,
+                                      at<uint8_t>(ws, L.xq), at<uint8_t>(ws, L.xs), x->num_sms, s),
                  "4-bit row launch");
   }
   if ((st = run_mx4(x, T * k, offsets, ws, L, slots, perm, w, ldt, s)) != MOE_OK) return st;
@@ -274,11 +274,8 @@ moe_status moe_mx4_experts_forward(moe_mx4_experts_t x, const void* x_disp, int6
   const Mx4Layout L = staged_layout(x, N);
   if ((st = check_ws(ws, ws_bytes, L.total)) != MOE_OK) return st;
   uint32_t* off_ok = at<uint32_t>(ws, L.offsets);
-  MOE_TRY_CUDA(cudaMemsetAsync(ws, 0, 4, stream), "cudaMemsetAsync");
-  MOE_TRY_CUDA(moe::launch_sanitize_offsets(offsets, (int)x->E, N, off_ok, status_word(ws), stream),
-               "offsets check launch");
-  MOE_TRY_CUDA(moe::launch_mx4_rows(x_disp, x->dt, N, x->H, nullptr, 1, off_ok, (int)x->E, at<uint8_t>(ws, L.xq),
-                                    at<uint8_t>(ws, L.xs), x->num_sms, stream),
+  MOE_TRY_CUDA(moe::launch_mx4_rows(x_disp, x->dt, N, x->H, nullptr, 1, offsets, (int)x->E, off_ok, status_word(ws),
+                                    at<uint8_t>(ws, L.xq), at<uint8_t>(ws, L.xs), x->num_sms, stream),
                "4-bit row launch");
   st = run_mx4(x, N, off_ok, ws, L, expert_out, nullptr, nullptr, MOE_F32, stream);
   return st == MOE_OK ? ok() : st;

@@ -187,6 +187,44 @@ __device__ __forceinline__ uint32_t small_div(uint32_t a, uint32_t b) {
   return q;
 }
 
+// A caller's offsets [E+1] as kernels read them, by one warp: each clamped to
+// [previous, N], so that no segment runs backwards or past the N rows of the
+// buffers.  Returns whether an entry was clamped (the same in every lane).
+__device__ __forceinline__ bool clamp_offsets(const uint32_t* __restrict__ in, int E, int64_t N, uint32_t* out) {
+  const int lane = threadIdx.x & 31;
+  const int n = E + 1;
+  const int per = (n + 31) / 32;
+  const uint32_t cap = N < (int64_t)0xFFFFFFFFu ? (uint32_t)N : 0xFFFFFFFEu;
+  uint32_t run = 0;
+  for (int i = 0; i < per; ++i) {
+    const int e = lane * per + i;
+    if (e < n) {
+      const uint32_t v = in[e];
+      run = max(run, v < cap ? v : cap);
+    }
+  }
+  uint32_t incl = run;  // max over this lane's entries and every earlier lane's
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const uint32_t o = __shfl_up_sync(0xffffffffu, incl, d);
+    if (lane >= d) incl = max(incl, o);
+  }
+  uint32_t prev = __shfl_up_sync(0xffffffffu, incl, 1);
+  if (lane == 0) prev = 0;
+  bool bad = false;
+  for (int i = 0; i < per; ++i) {
+    const int e = lane * per + i;
+    if (e < n) {
+      const uint32_t v = in[e];
+      const uint32_t c = max(prev, v < cap ? v : cap);
+      out[e] = c;
+      bad |= c != v;
+      prev = c;
+    }
+  }
+  return __any_sync(0xffffffffu, bad);
+}
+
 // Records the first device-side error in a workspace status word.
 __device__ __forceinline__ void set_status(uint32_t* status, uint32_t code) {
   if (status) atomicCAS(status, 0u, code);

@@ -14,8 +14,8 @@
 // scales have at most four significant bits, so products are exact.
 //
 // The kernel is the segmented, persistent one of the 16-bit products (tiles
-// visited expert by expert, a TMA warp, an MMA thread, four epilogue warps,
-// two accumulators, bounded waits), with these differences:
+// visited expert by expert, a TMA warp, an MMA warp, epilogue warps, two
+// accumulators, bounded waits), with these differences:
 //   * a 128-byte swizzled row holds 256 values, so a ring slot is 256 deep, and
 //     its four MMAs take about 400 cycles: what the issuing thread does between
 //     them counts.  Slots are therefore filled and freed one by one but handed
@@ -31,17 +31,25 @@
 //     registers instead, two spans do not fit beside eight epilogue warps, and
 //     with one the loads' latency is the kernel's pace.)
 //     Copying them from shared memory (tcgen05.cp) instead holds up the MMAs:
-//     about 100 cycles a copy, six copies a stage, 404 us against 250 us of
-//     MMAs alone for the headline gate/up, and loading them by TMA takes a
-//     fifth of the loads' time;
+//     about 50 cycles a copy, six copies a slot (the headline's gate/up without
+//     its loads and epilogue: 367 us, 250 us of it MMAs), and loading them by
+//     TMA takes a fifth of the loads' time;
+//   * eight epilogue warps, four for each accumulator, and nothing released
+//     later than it must: an arrival on the peer's barrier that orders memory
+//     waits for every store and load in flight (2000 cycles of a tile's 6000);
 //   * N = 192 on CTA pairs: two accumulators of 256 columns would leave no
 //     TMEM for the scales, and accumulators that share columns would stop the
 //     MMAs at every tile's end until the epilogue has read the shared part;
 //   * a gate/up tile's columns are its gate features, then the same up
 //     features (on CTA pairs the leader stages the gate rows, its peer the up
 //     rows), so that a lane holds both values of a feature.
+// What bounds it: on CTA pairs the bytes that an SM takes in and its shared
+// memory moves (28 KiB a slot, 53 bytes a cycle in, as many read by each MMA
+// again; loads alone take 181 of the headline gate/up's 231 us, MMAs alone at
+// their rate 146).  N = 256 would move a tenth less, for TMEM see above.
 // Single CTAs serve batches that hold few rows an expert: they are bound by
-// reading weights, and many small tiles spread over the SMs.
+// reading weights (32 tokens over 256 experts of 7168 x 2048, top-8: 580 us,
+// 6.6 TB/s), and many small tiles spread over the SMs.
 #include <algorithm>
 #include <mutex>
 #include <new>
@@ -58,7 +66,6 @@ struct Mx4Weights {
   CUtensorMap gate96, up96, down96;  // boxes of 96 rows by 256 values
   CUtensorMap gate64, up64, down128;  // boxes of 64 and 128 rows
   const uint8_t *sg, *su, *sd;       // scales in product order
-  int64_t E, I, H;
 };
 
 namespace mx4 {
@@ -169,7 +176,7 @@ struct Tile {
   int64_t m0;
   uint32_t unit;  // 256-row unit of scales, and the tile's first group in it
   uint32_t group;
-  bool thin;
+  int a_rows;  // rows of A to load: 128, or 64 or 32 that hold all there are
 };
 
 // By a converged warp: every role asks for a tile at its start, and what that
@@ -191,13 +198,15 @@ __device__ __forceinline__ Tile decode_tile(uint32_t tile, const Params& p, cons
   t.m0 = (int64_t)s_off[lo] + (int64_t)mt * tile_m;
   t.unit = tile_m == 256 ? s_pref[lo] + mt : s_unit[lo] + (mt >> 1);
   t.group = tile_m == 256 ? 0u : 4u * (mt & 1u);
-  t.thin = p.thin_a && (int64_t)s_off[lo + 1] - t.m0 <= 32;
+  const int64_t left = (int64_t)s_off[lo + 1] - t.m0;
+  t.a_rows = !p.thin_a || left > 64 ? BM : left > 32 ? 64 : 32;
   return t;
 }
 
 template <typename T, int PAIR, int BN>
 __global__ void __launch_bounds__(THREADS, 1)
-gemm_mx4_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapA32,
+gemm_mx4_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapA64,
+                const __grid_constant__ CUtensorMap mapA32,
                 const __grid_constant__ CUtensorMap mapB0, const __grid_constant__ CUtensorMap mapB1, const Params p) {
   using C = Cfg<PAIR, BN>;
   constexpr int PAIRS = C::PAIRS;
@@ -250,7 +259,10 @@ gemm_mx4_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant_
   }
   if (warp == 0 && lane == 0) {
     prefetch_map(&mapA);
-    if (p.thin_a) prefetch_map(&mapA32);
+    if (p.thin_a) {
+      prefetch_map(&mapA64);
+      prefetch_map(&mapA32);
+    }
     prefetch_map(&mapB0);
     prefetch_map(&mapB1);
   }
@@ -308,8 +320,8 @@ gemm_mx4_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant_
       const int a_row = __shfl_sync(0xffffffffu, (int)(t.m0 + (int64_t)rank * BM), 0);
       const int te = __shfl_sync(0xffffffffu, t.e, 0);
       const int tnb = __shfl_sync(0xffffffffu, t.nb, 0);
-      const bool thin = __all_sync(0xffffffffu, t.thin);
-      const uint32_t slot_tx = (thin ? C::SLOT_BYTES - (A_BYTES - A_BYTES / 4) : C::SLOT_BYTES) * PAIR;
+      const int a_rows = __shfl_sync(0xffffffffu, t.a_rows, 0);
+      const uint32_t slot_tx = (C::B_BYTES + (uint32_t)a_rows * ROW_BYTES) * PAIR;
       const int n0 = tnb * (p.gate_up ? BN / 2 : BN);  // first feature, or first output column
       const int b_row = PAIR == 2 && !p.gate_up ? n0 + (int)rank * C::B_ROWS : n0;
       for (int sp = 0; sp < spans; ++sp) {
@@ -324,7 +336,8 @@ gemm_mx4_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant_
             const uint32_t fb = full0_leader + 8u * pr;
             const int kx = (2 * sp + h) * (int)ROW_BYTES;
             if (leader && h == 0) mbar_expect_tx(full_bar(pr), two ? 2 * slot_tx : slot_tx);
-            if (thin) tma_load_2d<PAIR>(sa, &mapA32, kx, a_row, fb);
+            if (a_rows == 32) tma_load_2d<PAIR>(sa, &mapA32, kx, a_row, fb);
+            else if (a_rows == 64) tma_load_2d<PAIR>(sa, &mapA64, kx, a_row, fb);
             else tma_load_2d<PAIR>(sa, &mapA, kx, a_row, fb);
             if (PAIR == 2) {  // gate rows and up rows, or the two halves of the down rows
               if (leader) tma_load_3d<PAIR>(sb, &mapB0, kx, b_row, te, fb);
@@ -703,8 +716,11 @@ template <typename T, int PAIR, int BN>
 cudaError_t launch_t(const Mx4Args& a, const Mx4Weights* w, int num_sms, cudaStream_t s) {
   using C = Cfg<PAIR, BN>;
   const int64_t K = a.gate_up ? a.H : a.I;
-  CUtensorMap mA, mA32;
-  if (!encode_rows(&mA, a.a, a.N, K / 2, BM) || !encode_rows(&mA32, a.a, a.N, K / 2, 32)) return cudaErrorInvalidValue;
+  CUtensorMap mA, mA64, mA32;
+  if (!encode_rows(&mA, a.a, a.N, K / 2, BM)) return cudaErrorInvalidValue;
+  mA64 = mA32 = mA;  // CTA pairs load whole tiles
+  if (PAIR == 1 && (!encode_rows(&mA64, a.a, a.N, K / 2, 64) || !encode_rows(&mA32, a.a, a.N, K / 2, 32)))
+    return cudaErrorInvalidValue;
   Params p{};
   p.offsets = a.offsets;
   p.E = a.E;
@@ -752,7 +768,7 @@ cudaError_t launch_t(const Mx4Args& a, const Mx4Weights* w, int num_sms, cudaStr
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, gemm_mx4_kernel<T, PAIR, BN>, mA, mA32, b0, b1, p);
+  return cudaLaunchKernelEx(&cfg, gemm_mx4_kernel<T, PAIR, BN>, mA, mA64, mA32, b0, b1, p);
 }
 
 }  // namespace mx4
@@ -777,9 +793,6 @@ Mx4Weights* mx4_weights_create(const void* gate, const void* up, const void* dow
     *err = "out of host memory";
     return nullptr;
   }
-  w->E = E;
-  w->I = I;
-  w->H = H;
   w->sg = sg;
   w->su = su;
   w->sd = sd;

@@ -137,6 +137,9 @@ struct Params {
   // copy; a segment's last rows, short of 64, come from a copy of their own
   // (64 rows an expert, zeros behind them; the mapA64 slot)
   int a_tail;
+  // kWgrad: parts that an expert's rows are cut into, each a tile of its own
+  // with an FP32 output [E, k_parts, ...]; 1: none
+  int k_parts;
   int64_t m_total;     // M of the product
   int64_t split;       // output rows per buffer (M, or I for the [dgate; dup] pair)
   // forward products on CTA pairs: a segment's last m-tile holding at most
@@ -285,6 +288,8 @@ struct Tile {
   int64_t m0;  // first row of the (pair) tile
   int kx0;     // first K coordinate (0, or pad[e] for weight gradients)
   int nk;      // k-blocks of this tile
+  int kb0;     // its first k-block in the expert (split weight gradients)
+  int eo;      // where its output lies: the expert, or (expert, part of K)
   bool half;   // M = 128 pair tile (64 rows per CTA): see Params::half_tails
   bool thin;   // single-CTA tile of at most 32 rows: see Params::thin_a
 };
@@ -307,6 +312,8 @@ __device__ __forceinline__ Tile decode_tile(uint32_t tile, const Params& p, cons
   t.m0 = (int64_t)s_off[lo] + (int64_t)mt * tile_m;
   t.kx0 = 0;
   t.nk = p.k_blocks;
+  t.kb0 = 0;
+  t.eo = lo;
   t.half = p.half_tails && (int64_t)s_off[lo + 1] - t.m0 <= BM;
   t.thin = p.thin_a && (int64_t)s_off[lo + 1] - t.m0 <= 32;
   return t;
@@ -317,14 +324,20 @@ __device__ __forceinline__ Tile decode_tile(uint32_t tile, const Params& p, cons
 __device__ __forceinline__ Tile decode_wgrad(uint32_t tile, const Params& p, const uint32_t* s_pad, int tile_m) {
   const uint32_t per = (uint32_t)(p.mb * p.nb);
   Tile t;
-  t.e = (int)small_div(tile, per);
-  const uint32_t rem = tile - (uint32_t)t.e * per;
+  t.eo = (int)small_div(tile, per);
+  t.e = p.k_parts > 1 ? (int)small_div((uint32_t)t.eo, (uint32_t)p.k_parts) : t.eo;
+  const uint32_t rem = tile - (uint32_t)t.eo * per;
   const uint32_t m = small_div(rem, (uint32_t)p.nb);
   t.m0 = (int64_t)m * tile_m;
   t.nb = (int)(rem - m * (uint32_t)p.nb);
   const uint32_t k0 = s_pad[t.e], k1 = s_pad[t.e + 1];
-  t.kx0 = (int)k0;
-  t.nk = (int)((k1 - k0) / BK);
+  // this part's share of the expert's k-blocks
+  const uint32_t nkb = (k1 - k0) / BK, part = (uint32_t)(t.eo - t.e * p.k_parts);
+  const uint32_t f0 = p.k_parts > 1 ? small_div(nkb * part, (uint32_t)p.k_parts) : 0u;
+  const uint32_t f1 = p.k_parts > 1 ? small_div(nkb * (part + 1), (uint32_t)p.k_parts) : nkb;
+  t.kx0 = (int)(k0 + f0 * BK);
+  t.kb0 = (int)f0;
+  t.nk = (int)(f1 - f0);
   t.half = false;
   t.thin = false;
   return t;
@@ -424,7 +437,7 @@ grouped_gemm_tc(const __grid_constant__ CUtensorMap mapA, const __grid_constant_
   tc_fence_after();
   const uint32_t tmem_base = __shfl_sync(0xffffffffu, *tmem_slot, 0);
   const uint32_t total_tiles = __shfl_sync(
-      0xffffffffu, p.wgrad ? (uint32_t)E * (uint32_t)(p.mb * p.nb) : s_pref[E] * (uint32_t)p.nb, 0);
+      0xffffffffu, p.wgrad ? (uint32_t)E * (uint32_t)(p.mb * p.nb * p.k_parts) : s_pref[E] * (uint32_t)p.nb, 0);
   auto tile_at = [&](uint32_t tile) {
     return p.wgrad ? decode_wgrad(tile, p, s_pref, C::TILE_M) : decode_tile(tile, p, s_pref, s_off, C::TILE_M);
   };
@@ -453,8 +466,9 @@ grouped_gemm_tc(const __grid_constant__ CUtensorMap mapA, const __grid_constant_
       int row = (int)(t.m0 + (int64_t)rank * (half ? BM / 2 : BM));
       if (p.a_row_pad) row += (int)(__ldg(p.pad + t.e) - s_off[t.e]);
       const int a_row = __shfl_sync(0xffffffffu, row, 0);
-      const int a_k0 = p.a_tail ? __shfl_sync(0xffffffffu, (int)s_off[t.e], 0) : 0;
-      const bool a_cut = p.a_tail && __all_sync(0xffffffffu, ((s_off[t.e + 1] - s_off[t.e]) & 63u) != 0);
+      const int a_k0 = p.a_tail ? __shfl_sync(0xffffffffu, (int)s_off[t.e] + t.kb0 * BK, 0) : 0;
+      // this tile's last k-block is the segment's, and is cut
+      const bool a_cut = p.a_tail && __all_sync(0xffffffffu, s_off[t.e] + (uint32_t)(t.kb0 + t.nk) * BK > s_off[t.e + 1]);
       const int b0row = tnb * p.cols_per_tile;
       const int b1row = b0row + p.b1_row_off;
       // interleaved gate/up B (pairs): this CTA's 64 gate rows and the same 64 up rows
@@ -877,10 +891,10 @@ grouped_gemm_tc(const __grid_constant__ CUtensorMap mapA, const __grid_constant_
         float* rowf = nullptr;
         if (row_ok) {
           if (grow < p.split)
-            rowf = static_cast<float*>(p.out) + ((int64_t)t.e * p.split + grow) * p.n_out + col0;
+            rowf = static_cast<float*>(p.out) + ((int64_t)t.eo * p.split + grow) * p.n_out + col0;
           else
             rowf = static_cast<float*>(p.out2) +
-                   ((int64_t)t.e * (p.m_total - p.split) + grow - p.split) * p.n_out + col0;
+                   ((int64_t)t.eo * (p.m_total - p.split) + grow - p.split) * p.n_out + col0;
         }
         uint32_t* rowp = reinterpret_cast<uint32_t*>(rowf);
         const bool empty = t.nk == 0;
@@ -1087,7 +1101,7 @@ cudaError_t launch_t(int64_t N, int E, const CUtensorMap& mA, const CUtensorMap&
   constexpr int TM = Cfg<PAIR>::TILE_M;
   int64_t tiles_max;
   if (p.wgrad) {
-    tiles_max = (int64_t)E * p.mb * p.nb;
+    tiles_max = (int64_t)E * p.mb * p.nb * p.k_parts;
   } else {
     const int64_t mt_max = (N + TM - 1) / TM + std::min<int64_t>(E, N);
     tiles_max = mt_max * p.nb;
@@ -1298,6 +1312,7 @@ cudaError_t backward_t(const ExpertsBwdArgs& a, const TcWeights* w, char* ws, in
   p = base;
   p.mode = kWgrad;
   p.wgrad = 1;
+  p.k_parts = 1;
   p.a_mn = 1;
   p.b_form = kBMNmajor2d;
   p.cols_per_tile = 256;
@@ -1326,8 +1341,19 @@ cudaError_t backward_t(const ExpertsBwdArgs& a, const TcWeights* w, char* ws, in
 // from its 8-bit tokens, and the weight gradients are stored in T.
 struct CkLayout {
   int64_t npad;
-  size_t pad, dgduP, actP, xP, tails, total;
+  size_t pad, dgduP, actP, xP, tails, parts, total;
 };
+
+// Parts that each expert's rows are cut into for a weight gradient of m x n:
+// one, or as many as fill the CTA pairs where the tiles of all experts are
+// fewer, with four k-blocks a part at least on average (below that the parts'
+// FP32 outputs cost more than they save).  Two experts of 664 x 112 with 10280
+// rows each: 185 us with one part.
+int wgrad_parts(int64_t N, int E, int64_t m, int64_t n) {
+  constexpr int64_t kPairs = 76;
+  const int64_t tiles = E * ((m + 255) / 256) * ((n + 255) / 256);
+  return (int)std::max<int64_t>(1, std::min(kPairs / tiles, N / ((int64_t)E * 4 * BK)));
+}
 
 CkLayout ck_layout(int64_t N, int E, int64_t H, int64_t I) {
   CkLayout L{};
@@ -1343,6 +1369,8 @@ CkLayout ck_layout(int64_t N, int E, int64_t H, int64_t I) {
   L.actP = take((size_t)L.npad * I * 2);
   L.xP = take((size_t)L.npad * H * 2);
   L.tails = take((size_t)E * BK * H * 2);
+  const int pgu = wgrad_parts(N, E, 2 * I, H), pd = wgrad_parts(N, E, H, I);
+  L.parts = take((size_t)std::max(pgu > 1 ? 2 * pgu : 0, pd > 1 ? pd : 0) * E * I * H * 4);
   L.total = off;
   return L;
 }
@@ -1369,7 +1397,7 @@ cudaError_t backward_ck_t(const ExpertsCkBwdArgs& a, char* ws, int num_sms, cuda
   cudaError_t err;
 #define MOE_TC_TRY(x) \
   if ((err = (x)) != cudaSuccess) return err
-  MOE_TC_TRY(launch_pad_offsets(a.offsets, E, pad, s));
+  MOE_TC_TRY(launch_check_offsets(a.offsets_in, E, N, a.offsets, a.status, pad, s));
   const bool pair = N >= (int64_t)BM * E;
   Params base{};
   base.offsets = a.offsets;
@@ -1416,25 +1444,35 @@ cudaError_t backward_ck_t(const ExpertsCkBwdArgs& a, char* ws, int num_sms, cuda
   p.half_tails = 0;
   p.mode = kWgrad;
   p.wgrad = 1;
+  p.k_parts = 1;
   p.a_mn = 1;
   p.b_form = kBMNmajor2d;
+  float* parts = reinterpret_cast<float*>(ws + L.parts);
+  auto gradient = [&](const CUtensorMap& mA, const CUtensorMap& mB, const CUtensorMap* mTail, void* o1, void* o2) {
+    p.mb = (int)((p.m_total + TM - 1) / TM);
+    p.nb = (int)((p.n_out + 255) / 256);
+    p.k_parts = wgrad_parts(N, E, p.m_total, p.n_out);
+    p.out = o1;
+    p.out2 = o2;
+    if (p.k_parts == 1) return launch_t<T, 2, 1, kUse>(N, E, mA, mB, mB, p, num_sms, s, mTail);
+    const int64_t n1 = p.split * p.n_out, n2 = (p.m_total - p.split) * p.n_out;
+    float* f2 = parts + (int64_t)p.k_parts * E * n1;
+    p.out = parts;
+    p.out2 = f2;
+    cudaError_t e = launch_t<T, 2>(N, E, mA, mB, mB, p, num_sms, s, mTail);
+    if (e == cudaSuccess) e = launch_join_parts(parts, E, p.k_parts, n1, o1, dt, s);
+    if (e == cudaSuccess && n2 > 0) e = launch_join_parts(f2, E, p.k_parts, n2, o2, dt, s);
+    return e;
+  };
   p.m_total = 2 * I;
   p.split = I;
-  p.mb = (int)((2 * I + TM - 1) / TM);
   p.n_out = H;
-  p.nb = (int)((H + 255) / 256);
-  p.out = a.dgate;
-  p.out2 = a.dup;
-  MOE_TC_TRY((launch_t<T, 2, 1, kUse>(N, E, mDgduMN, mXMN, mXMN, p, num_sms, s)));
+  MOE_TC_TRY(gradient(mDgduMN, mXMN, nullptr, a.dgate, a.dup));
   p.m_total = H;
   p.split = H;
-  p.mb = (int)((H + TM - 1) / TM);
   p.n_out = I;
-  p.nb = (int)((I + 255) / 256);
-  p.out = a.ddown;
-  p.out2 = a.ddown;
   p.a_tail = 1;
-  MOE_TC_TRY((launch_t<T, 2, 1, kUse>(N, E, mDoMN, mActMN, mActMN, p, num_sms, s, &mTailMN)));
+  MOE_TC_TRY(gradient(mDoMN, mActMN, &mTailMN, a.ddown, a.ddown));
 #undef MOE_TC_TRY
   return cudaSuccess;
 }

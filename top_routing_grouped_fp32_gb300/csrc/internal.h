@@ -130,11 +130,13 @@ cudaError_t launch_mx_quantize(const void* x, moe_dtype dt, int64_t R, int64_t C
 cudaError_t launch_mx_dequantize(const uint8_t* values, const uint8_t* scales, moe_mx_format fmt, int64_t R,
                                  int64_t C, const uint32_t* perm, int k, int64_t n, void* out, moe_dtype dt,
                                  cudaStream_t s);
-// 16-bit rows to e2m1 in dispatch order, scales in the order of the products
-// (slot_row: source row t goes to rows slot_row[t k + j]; else rows are in order)
+// 16-bit rows to e2m1 in dispatch order, scales in the order of the products.
+// With slot_row, source row t goes to rows slot_row[t k + j].  Without, rows are
+// in order and the offsets are a caller's: they are checked (clamp_offsets),
+// written to off_ok, and *status is set.
 cudaError_t launch_mx4_rows(const void* x, moe_dtype dt, int64_t rows, int64_t C, const uint32_t* slot_row, int k,
-                            const uint32_t* offsets, int E, uint8_t* values, uint8_t* scales, int num_sms,
-                            cudaStream_t s);
+                            const uint32_t* offsets, int E, uint32_t* off_ok, uint32_t* status, uint8_t* values,
+                            uint8_t* scales, int num_sms, cudaStream_t s);
 // the same with the dispatch, for T k <= mx4_small_slots(): sorts idx [T, k],
 // writes offsets [E+1], perm [T k] and zeroes *status
 int64_t mx4_small_slots();
@@ -250,6 +252,9 @@ cudaError_t launch_experts_backward(const ExpertsBwdArgs& a, cudaStream_t s);
 // clamped entry sets MOE_ERR_INVALID_INDEX in *status
 cudaError_t launch_sanitize_offsets(const uint32_t* offsets, int E, int64_t N, uint32_t* out,
                                    uint32_t* status, cudaStream_t s);
+// the same, also the status word's first value and, unless null, pad (below)
+cudaError_t launch_check_offsets(const uint32_t* offsets, int E, int64_t N, uint32_t* out, uint32_t* status,
+                                 uint32_t* pad, cudaStream_t s);
 // The 64-padded row space of the tensor-core backward (rowpad.cu)
 cudaError_t launch_pad_offsets(const uint32_t* offsets, int E, uint32_t* pad, cudaStream_t s);
 cudaError_t launch_pad_rows(const void* src, int64_t C, const uint32_t* offsets, const uint32_t* pad,
@@ -257,6 +262,8 @@ cudaError_t launch_pad_rows(const void* src, int64_t C, const uint32_t* offsets,
 
 // the last (rows of e) % 64 rows of each expert's segment, at row 64 e, zeros behind
 cudaError_t launch_tail_rows(const void* src, int64_t C, const uint32_t* offsets, int E, void* dst, cudaStream_t s);
+// out [E, n] in dt = sum over the k parts of parts [E, k, n], in order
+cudaError_t launch_join_parts(const float* parts, int E, int k, int64_t n, void* out, moe_dtype dt, cudaStream_t s);
 // pad_rows from 8-bit tokens: dispatched row r is token perm[r] / k (zeros past T)
 cudaError_t launch_pad_rows_mx8(const uint8_t* x, const uint8_t* scales, int64_t T, int64_t C, const uint32_t* perm,
                                 int k, const uint32_t* offsets, const uint32_t* pad, int E, int64_t npad_max,
@@ -287,7 +294,8 @@ struct ExpertsCkBwdArgs {
   const uint8_t* x;         // e4m3 tokens [T, H]
   const uint8_t* x_scales;  // [T, ceil(H/32)]
   const uint32_t* perm;
-  const uint32_t* offsets;
+  const uint32_t* offsets_in;  // the caller's
+  uint32_t* offsets;           // checked copy, written first
   const uint8_t* g;         // e4m3 [N, I]
   const uint8_t* g_scales;  // [N, ceil(I/32)]
   const uint8_t* u;

@@ -111,10 +111,54 @@ mx_quantize_blocks(const T* __restrict__ x, int64_t blocks, uint8_t* __restrict_
   if (b0 + lane < blocks) scales[b0 + lane] = (uint8_t)mine;
 }
 
-// Any row length and alignment: a warp takes kRun blocks, one behind the other
-// through the rows (so short rows fill it too), a lane per value, all blocks in
-// flight.  Lane u looks block u up.
+// Any row length and alignment, long rows: a warp per row and kSegment columns, a
+// lane per value of a block, all blocks in flight.
+constexpr int kSegBlocks = 16, kSegment = 32 * kSegBlocks;
+template <typename T, int FMT>
+__global__ void __launch_bounds__(kThreads)
+mx_quantize_segments(const T* __restrict__ x, int64_t R, int64_t C, int segs, uint8_t* __restrict__ values,
+                 uint8_t* __restrict__ scales) {
+  const int lane = threadIdx.x & 31;
+  const int64_t w = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  const int64_t r = w / segs;
+  if (r >= R) return;
+  const int64_t c0 = (w - r * segs) * kSegment;
+  const int64_t nb = (C + 31) / 32;
+  const T* xr = x + r * C + c0;
+  uint8_t* sr = scales + r * nb + c0 / 32;
+  uint8_t* vr = values + (FMT == MOE_MXFP4 ? r * ((C + 1) / 2) + c0 / 2 : r * C + c0);
+  const int left = (int)min((int64_t)kSegment, C - c0);
+  float v[kSegBlocks];
+#pragma unroll
+  for (int u = 0; u < kSegBlocks; ++u) v[u] = u * 32 + lane < left ? to_f32<T>(xr[u * 32 + lane]) : 0.f;
+  uint32_t mine = 0;  // lane u: the byte of block u
+#pragma unroll
+  for (int u = 0; u < kSegBlocks; ++u) {
+    if (u * 32 >= left) break;
+    const int c = u * 32 + lane;
+    const uint32_t a = __reduce_max_sync(0xffffffffu, mx::abs_bits(v[u]));
+    const uint32_t b = mx::scale_byte<FMT>(a);
+    const float q[4] = {b == 255u ? 0.f : v[u] * mx::inverse_scale(b), 0.f, 0.f, 0.f};
+    if constexpr (FMT == MOE_MXFP8) {
+      if (c < left) vr[c] = (uint8_t)mx::to_e4m3x4(q);
+    } else {
+      const float q1 = __shfl_down_sync(0xffffffffu, q[0], 1);
+      const float both[8] = {q[0], q1, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      if (c < left && (lane & 1) == 0) vr[c >> 1] = (uint8_t)mx::to_e2m1x8(both);
+    }
+    if (lane == u) mine = b;
+  }
+  if (lane * 32 < left) sr[lane] = (uint8_t)mine;
+}
+
+// Any row length and alignment, short rows: a warp takes kRun blocks, one behind
+// the other through the rows, a lane per value, all blocks in flight.  Lane u
+// looks block u up.
 constexpr int kRun = 16;
+// Segments that are mostly full are faster (4097 rows of 1001 FP16 values to 8
+// bits: 7.5 against 9 us), short rows leave most of one empty (1027166 rows of 102
+// FP32 values to 4 bits and back: 594 us in segments, 387 in runs).
+__host__ inline bool long_rows(int64_t C) { return C > kSegment * 5 / 8; }
 __device__ __forceinline__ int64_t shfl64(int64_t v, int u) {
   return __shfl_sync(0xffffffffu, (long long)v, u);
 }
@@ -259,6 +303,40 @@ mx_dequantize_rows(const uint8_t* __restrict__ values, const uint8_t* __restrict
   }
 }
 
+// the same of long rows, as mx_quantize_segments
+template <typename T, int FMT>
+__global__ void __launch_bounds__(kThreads)
+mx_dequantize_segments(const uint8_t* __restrict__ values, const uint8_t* __restrict__ scales, int64_t R, int64_t C,
+                   int segs, const uint32_t* __restrict__ perm, uint32_t k, int64_t n, T* __restrict__ out) {
+  const int lane = threadIdx.x & 31;
+  const int64_t w = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  const int64_t r = w / segs;
+  if (r >= n) return;
+  const int64_t c0 = (w - r * segs) * kSegment;
+  const int64_t src = perm ? (int64_t)(__ldg(perm + r) / k) : r;
+  const int left = src < R ? (int)min((int64_t)kSegment, C - c0) : 0;  // values to read
+  const int64_t nb = (C + 31) / 32;
+  const uint8_t* vr = values + (FMT == MOE_MXFP4 ? src * ((C + 1) / 2) + c0 / 2 : src * C + c0);
+  uint32_t q[kSegBlocks];
+#pragma unroll
+  for (int u = 0; u < kSegBlocks; ++u) {
+    const int c = u * 32 + lane;
+    q[u] = c < left ? (uint32_t)__ldg(vr + (FMT == MOE_MXFP4 ? c >> 1 : c)) : 0u;
+  }
+  // lane u: the byte of block u
+  const uint32_t mine = lane * 32 < left ? (uint32_t)__ldg(scales + src * nb + c0 / 32 + lane) : 0u;
+  T* o = out + r * C + c0;
+  const int end = (int)min((int64_t)kSegment, C - c0);
+#pragma unroll
+  for (int u = 0; u < kSegBlocks; ++u) {
+    const float s = mx::scale_value(__shfl_sync(0xffffffffu, mine, u));
+    float v[8];
+    if constexpr (FMT == MOE_MXFP4) mx::from_e2m1x8(q[u] >> (4 * (lane & 1)), v);
+    else mx::from_e4m3x4(q[u], v);
+    if (u * 32 + lane < end) o[u * 32 + lane] = from_f32<T>(v[0] * s);
+  }
+}
+
 // ---- activations of the 4-bit products ---------------------------------------
 // 256-row units of experts < e (ceil per expert): where expert e's scales begin.
 // One block; s_off [E+1] is filled, s_unit [E+1] written.
@@ -297,27 +375,29 @@ constexpr int kSmallSlots = 256;
 // many rows.  With slot_row, source row t goes to the dispatch rows
 // slot_row[t k + j]: a token is read and rounded once however many experts it
 // goes to.
-// SMALL: dispatch too, for batches of at most kSmallSlots slots: every block
+// kDispatch: dispatch too, for batches of at most kSmallSlots slots: every block
 // sorts the slots idx [rows, k] itself (a count, a scan, and for each slot the
 // number of equal experts before it, so in the order of moe_dispatch) and the
 // first one writes offsets and perm.  A decode step is a chain of short
 // kernels; this takes two out of it (27.5 -> 23.6 us for one token over 64
 // experts of 2048 x 1408, replayed from a graph).
-struct SmallDispatch {
-  const uint32_t* idx;
-  uint32_t* offsets;
-  uint32_t* perm;
-  uint32_t* status;
+// kOrder: rows in order, the caller's offsets checked by every block for itself.
+enum Rows { kSlots = 0, kOrder = 1, kDispatch = 2 };
+struct RowsArgs {
+  const uint32_t* idx;  // kDispatch
+  uint32_t* offsets;    // kDispatch, kOrder: written
+  uint32_t* perm;       // kDispatch
+  uint32_t* status;     // kDispatch, kOrder
 };
-template <typename T, bool SMALL>
+template <typename T, int ROWS>
 __global__ void __launch_bounds__(kThreads, 4)
 mx4_rows_kernel(const T* __restrict__ x, int64_t rows, int64_t C, const uint32_t* __restrict__ slot_row, int k,
                 const uint32_t* __restrict__ offsets, int E, uint8_t* __restrict__ values,
-                uint8_t* __restrict__ scales, const SmallDispatch sd) {
+                uint8_t* __restrict__ scales, const RowsArgs ra) {
   extern __shared__ uint32_t s_mem[];
   uint32_t* s_off = s_mem;
   uint32_t* s_unit = s_mem + E + 1;
-  uint32_t* s_expert = s_unit + E + 1;     // SMALL
+  uint32_t* s_expert = s_unit + E + 1;     // kDispatch
   uint32_t* s_row = s_expert + kSmallSlots;
   const int lane = threadIdx.x & 31;
   const int64_t warps = (int64_t)gridDim.x * kWarps;
@@ -337,12 +417,12 @@ mx4_rows_kernel(const T* __restrict__ x, int64_t rows, int64_t C, const uint32_t
   pdl_wait();
   pdl_trigger();
   if (src < rows) load(src, 0);
-  if constexpr (SMALL) {
+  if constexpr (ROWS == kDispatch) {
     static_assert(kSmallSlots <= kThreads, "a thread per slot");
     const int n = (int)rows * k, i = threadIdx.x;
     // counts one place up, so that their running sum is the offsets
     for (int e = i; e <= E; e += kThreads) s_off[e] = 0;
-    const uint32_t mine = i < n ? min(sd.idx[i], (uint32_t)(E - 1)) : 0u;
+    const uint32_t mine = i < n ? min(ra.idx[i], (uint32_t)(E - 1)) : 0u;
     if (i < n) s_expert[i] = mine;
     __syncthreads();
     if (i < n) atomicAdd(&s_off[mine + 1], 1u);
@@ -372,10 +452,18 @@ mx4_rows_kernel(const T* __restrict__ x, int64_t rows, int64_t C, const uint32_t
     __syncthreads();
     if (i < n) s_row[i] = s_off[mine] + before;
     if (blockIdx.x == 0) {
-      for (int e = i; e <= E; e += kThreads) sd.offsets[e] = s_off[e];
-      if (i < n) sd.perm[s_off[mine] + before] = (uint32_t)i;
-      if (i == 0) *sd.status = 0u;
+      for (int e = i; e <= E; e += kThreads) ra.offsets[e] = s_off[e];
+      if (i < n) ra.perm[s_off[mine] + before] = (uint32_t)i;
+      if (i == 0) *ra.status = 0u;
     }
+  } else if constexpr (ROWS == kOrder) {
+    if (threadIdx.x < 32) {
+      const bool bad = clamp_offsets(offsets, E, rows, s_off);
+      if (blockIdx.x == 0 && lane == 0) *ra.status = bad ? (uint32_t)MOE_ERR_INVALID_INDEX : 0u;
+    }
+    __syncthreads();
+    if (blockIdx.x == 0)
+      for (int i = threadIdx.x; i <= E; i += kThreads) ra.offsets[i] = s_off[i];
   } else {
     for (int i = threadIdx.x; i <= E; i += kThreads) s_off[i] = offsets[i];
     __syncthreads();
@@ -416,11 +504,11 @@ mx4_rows_kernel(const T* __restrict__ x, int64_t rows, int64_t C, const uint32_t
       for (int j = 0; j < k; ++j) {
         uint32_t r;
         int e;
-        if constexpr (SMALL) {
+        if constexpr (ROWS == kDispatch) {
           r = s_row[src * k + j];
           e = (int)s_expert[src * k + j];
         } else {
-          r = slot_row ? __ldg(slot_row + src * k + j) : (uint32_t)src;
+          r = ROWS == kSlots ? __ldg(slot_row + src * k + j) : (uint32_t)src;
           if (r < first || r >= last) continue;
           e = warp_search(s_off, E, r);
         }
@@ -493,6 +581,12 @@ cudaError_t quantize_t(const void* x, int64_t R, int64_t C, uint8_t* values, uin
     const int64_t grid = (blocks + 32 * kWarps - 1) / (32 * kWarps);
     mx_quantize_blocks<T, FMT><<<(unsigned)grid, kThreads, 0, s>>>(xp, blocks, values, scales);
   } else {
+    const int segs = (int)((C + kSegment - 1) / kSegment);
+    if (long_rows(C)) {
+      mx_quantize_segments<T, FMT><<<(unsigned)((R * segs + kWarps - 1) / kWarps), kThreads, 0, s>>>(xp, R, C, segs,
+                                                                                                   values, scales);
+      return cudaGetLastError();
+    }
     const int64_t blocks = R * ((C + 31) / 32), per = kWarps * kRun;
     mx_quantize_rows<T, FMT><<<(unsigned)((blocks + per - 1) / per), kThreads, 0, s>>>(xp, blocks, C, values, scales);
   }
@@ -511,6 +605,12 @@ cudaError_t dequantize_t(const uint8_t* values, const uint8_t* scales, int64_t R
   } else if (whole) {
     mx_dequantize_gather<T, FMT><<<by_row, kThreads, 0, s>>>(values, scales, R, C, perm, (uint32_t)k, n, o);
   } else {
+    const int segs = (int)((C + kSegment - 1) / kSegment);
+    if (long_rows(C)) {
+      mx_dequantize_segments<T, FMT><<<(unsigned)((n * segs + kWarps - 1) / kWarps), kThreads, 0, s>>>(
+          values, scales, R, C, segs, perm, (uint32_t)k, n, o);
+      return cudaGetLastError();
+    }
     const int64_t blocks = n * ((C + 31) / 32), per = kWarps * kRun;
     mx_dequantize_rows<T, FMT><<<(unsigned)((blocks + per - 1) / per), kThreads, 0, s>>>(values, scales, R, C, perm,
                                                                                          (uint32_t)k, blocks, o);
@@ -538,25 +638,27 @@ cudaError_t launch_mx_dequantize(const uint8_t* values, const uint8_t* scales, m
 }
 #undef MOE_MX_DISPATCH
 
-template <typename T, bool SMALL>
+template <typename T, int ROWS>
 static cudaError_t rows_t(const void* x, int64_t rows, int64_t C, const uint32_t* slot_row, int k,
-                          const uint32_t* offsets, int E, uint8_t* values, uint8_t* scales, const SmallDispatch& sd,
+                          const uint32_t* offsets, int E, uint8_t* values, uint8_t* scales, const RowsArgs& ra,
                           int num_sms, cudaStream_t s) {
   // four blocks stay on an SM
   const unsigned grid = (unsigned)std::min<int64_t>((rows + kWarps - 1) / kWarps, (int64_t)num_sms * 4);
-  const size_t smem = 4 * (2 * (size_t)(E + 1) + (SMALL ? 2 * kSmallSlots : 0));
-  return launch_pdl(mx4_rows_kernel<T, SMALL>, dim3(grid), dim3(kThreads), smem, s, static_cast<const T*>(x), rows, C,
-                    slot_row, k, offsets, E, values, scales, sd);
+  const size_t smem = 4 * (2 * (size_t)(E + 1) + (ROWS == kDispatch ? 2 * kSmallSlots : 0));
+  return launch_pdl(mx4_rows_kernel<T, ROWS>, dim3(grid), dim3(kThreads), smem, s, static_cast<const T*>(x), rows, C,
+                    slot_row, k, offsets, E, values, scales, ra);
 }
 
 cudaError_t launch_mx4_rows(const void* x, moe_dtype dt, int64_t rows, int64_t C, const uint32_t* slot_row, int k,
-                            const uint32_t* offsets, int E, uint8_t* values, uint8_t* scales, int num_sms,
-                            cudaStream_t s) {
-  if (!slot_row) k = 1;
-  const SmallDispatch sd{};
-  return dt == MOE_BF16
-             ? rows_t<__nv_bfloat16, false>(x, rows, C, slot_row, k, offsets, E, values, scales, sd, num_sms, s)
-             : rows_t<__half, false>(x, rows, C, slot_row, k, offsets, E, values, scales, sd, num_sms, s);
+                            const uint32_t* offsets, int E, uint32_t* off_ok, uint32_t* status, uint8_t* values,
+                            uint8_t* scales, int num_sms, cudaStream_t s) {
+  const RowsArgs ra{nullptr, off_ok, nullptr, status};
+  if (slot_row)
+    return dt == MOE_BF16
+               ? rows_t<__nv_bfloat16, kSlots>(x, rows, C, slot_row, k, offsets, E, values, scales, ra, num_sms, s)
+               : rows_t<__half, kSlots>(x, rows, C, slot_row, k, offsets, E, values, scales, ra, num_sms, s);
+  return dt == MOE_BF16 ? rows_t<__nv_bfloat16, kOrder>(x, rows, C, nullptr, 1, offsets, E, values, scales, ra, num_sms, s)
+                        : rows_t<__half, kOrder>(x, rows, C, nullptr, 1, offsets, E, values, scales, ra, num_sms, s);
 }
 
 int64_t mx4_small_slots() { return kSmallSlots; }
@@ -565,9 +667,9 @@ cudaError_t launch_mx4_dispatch_rows(const void* x, moe_dtype dt, int64_t T, int
                                      int E, uint32_t* offsets, uint32_t* perm, uint32_t* status, uint8_t* values,
                                      uint8_t* scales, int num_sms, cudaStream_t s) {
   if (T * k > kSmallSlots) return cudaErrorInvalidValue;
-  const SmallDispatch sd{idx, offsets, perm, status};
-  return dt == MOE_BF16 ? rows_t<__nv_bfloat16, true>(x, T, C, nullptr, k, nullptr, E, values, scales, sd, num_sms, s)
-                        : rows_t<__half, true>(x, T, C, nullptr, k, nullptr, E, values, scales, sd, num_sms, s);
+  const RowsArgs ra{idx, offsets, perm, status};
+  return dt == MOE_BF16 ? rows_t<__nv_bfloat16, kDispatch>(x, T, C, nullptr, k, nullptr, E, values, scales, ra, num_sms, s)
+                        : rows_t<__half, kDispatch>(x, T, C, nullptr, k, nullptr, E, values, scales, ra, num_sms, s);
 }
 
 cudaError_t launch_mx4_weight_scales(const uint8_t* scales, int64_t E, int64_t rows, int64_t C, uint8_t* out,

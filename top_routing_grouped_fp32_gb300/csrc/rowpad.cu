@@ -18,7 +18,7 @@
 namespace moe {
 namespace {
 
-__global__ void pad_offsets_kernel(const uint32_t* __restrict__ offsets, int E, uint32_t* __restrict__ pad) {
+__device__ __forceinline__ void pad_starts(const uint32_t* offsets, int E, uint32_t* pad) {
   // one warp: per-lane serial sums, then a warp scan (E <= 1024)
   const int lane = threadIdx.x;
   const int per = (E + 31) / 32;
@@ -42,45 +42,25 @@ __global__ void pad_offsets_kernel(const uint32_t* __restrict__ offsets, int E, 
   }
   if (lane == 31) pad[E] = incl;
 }
+__global__ void pad_offsets_kernel(const uint32_t* __restrict__ offsets, int E, uint32_t* __restrict__ pad) {
+  pad_starts(offsets, E, pad);
+}
 
-// The offsets of a staged expert call as its kernels read them: each clamped
-// to [previous, N], so that no segment runs backwards or past the N rows of
-// the buffers; a clamped entry marks the status word MOE_ERR_INVALID_INDEX.
-// One warp: per-lane serial running maxima, then a warp max-scan (E <= 1024).
+// The offsets of a staged expert call as its kernels read them (clamp_offsets);
+// a clamped entry marks the status word MOE_ERR_INVALID_INDEX.  One warp.
 __global__ void sanitize_offsets_kernel(const uint32_t* __restrict__ in, int E, int64_t N,
                                         uint32_t* __restrict__ out, uint32_t* __restrict__ status) {
-  const int lane = threadIdx.x;
-  const int n = E + 1;
-  const int per = (n + 31) / 32;
-  const uint32_t cap = N < (int64_t)0xFFFFFFFFu ? (uint32_t)N : 0xFFFFFFFEu;
-  uint32_t run = 0;
-  for (int i = 0; i < per; ++i) {
-    const int e = lane * per + i;
-    if (e < n) {
-      const uint32_t v = in[e];
-      run = max(run, v < cap ? v : cap);
-    }
-  }
-  uint32_t incl = run;  // max over this lane's entries and every earlier lane's
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const uint32_t o = __shfl_up_sync(0xffffffffu, incl, d);
-    if (lane >= d) incl = max(incl, o);
-  }
-  uint32_t prev = __shfl_up_sync(0xffffffffu, incl, 1);
-  if (lane == 0) prev = 0;
-  bool bad = false;
-  for (int i = 0; i < per; ++i) {
-    const int e = lane * per + i;
-    if (e < n) {
-      const uint32_t v = in[e];
-      const uint32_t c = max(prev, v < cap ? v : cap);
-      out[e] = c;
-      bad |= c != v;
-      prev = c;
-    }
-  }
-  if (__any_sync(0xffffffffu, bad) && lane == 0) set_status(status, (uint32_t)MOE_ERR_INVALID_INDEX);
+  if (clamp_offsets(in, E, N, out) && threadIdx.x == 0) set_status(status, (uint32_t)MOE_ERR_INVALID_INDEX);
+}
+
+// The same, the status word's first value and, with pad, where each expert's
+// rows begin in the 64-padded row space, in one launch.
+__global__ void check_offsets_kernel(const uint32_t* __restrict__ in, int E, int64_t N, uint32_t* __restrict__ out,
+                                     uint32_t* __restrict__ status, uint32_t* __restrict__ pad) {
+  const bool bad = clamp_offsets(in, E, N, out);
+  if (threadIdx.x == 0) *status = bad ? (uint32_t)MOE_ERR_INVALID_INDEX : 0u;
+  __syncwarp();
+  if (pad) pad_starts(out, E, pad);
 }
 
 constexpr int kRowsPerBlock = 8;  // one warp per row
@@ -164,7 +144,34 @@ pad_rows_mx8_kernel(const uint2* __restrict__ x, const uint8_t* __restrict__ sca
   }
 }
 
+// out[e, i] = sum over the parts of parts[e, part, i], in order, rounded once
+template <typename T>
+__global__ void __launch_bounds__(256)
+join_parts_kernel(const float4* __restrict__ parts, int k, int64_t vecs, int64_t total, uint4* __restrict__ out) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;  // 8 values
+  if (i >= total) return;
+  const int64_t e = i / vecs, v = i - e * vecs;
+  const float4* s = parts + ((e * k) * vecs + v) * 2;
+  float acc[8] = {};
+#pragma unroll 4
+  for (int j = 0; j < k; ++j, s += 2 * vecs) {
+    const float4 a = __ldg(s), b = __ldg(s + 1);
+    acc[0] += a.x; acc[1] += a.y; acc[2] += a.z; acc[3] += a.w;
+    acc[4] += b.x; acc[5] += b.y; acc[6] += b.z; acc[7] += b.w;
+  }
+  out[i] = pack8<T>(acc);
+}
+
 }  // namespace
+
+cudaError_t launch_join_parts(const float* parts, int E, int k, int64_t n, void* out, moe_dtype dt, cudaStream_t s) {
+  const int64_t total = E * (n / 8);
+  const unsigned blocks = (unsigned)((total + 255) / 256);
+  const float4* p = reinterpret_cast<const float4*>(parts);
+  if (dt == MOE_BF16) join_parts_kernel<__nv_bfloat16><<<blocks, 256, 0, s>>>(p, k, n / 8, total, static_cast<uint4*>(out));
+  else join_parts_kernel<__half><<<blocks, 256, 0, s>>>(p, k, n / 8, total, static_cast<uint4*>(out));
+  return cudaGetLastError();
+}
 
 cudaError_t launch_tail_rows(const void* src, int64_t C, const uint32_t* offsets, int E, void* dst, cudaStream_t s) {
   tail_rows_kernel<<<(unsigned)(E * 64 / kRowsPerBlock), 32 * kRowsPerBlock, 0, s>>>(
@@ -190,6 +197,12 @@ cudaError_t launch_pad_rows_mx8(const uint8_t* x, const uint8_t* scales, int64_t
 cudaError_t launch_sanitize_offsets(const uint32_t* offsets, int E, int64_t N, uint32_t* out,
                                    uint32_t* status, cudaStream_t s) {
   sanitize_offsets_kernel<<<1, 32, 0, s>>>(offsets, E, N, out, status);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_check_offsets(const uint32_t* offsets, int E, int64_t N, uint32_t* out, uint32_t* status,
+                                 uint32_t* pad, cudaStream_t s) {
+  check_offsets_kernel<<<1, 32, 0, s>>>(offsets, E, N, out, status, pad);
   return cudaGetLastError();
 }
 
