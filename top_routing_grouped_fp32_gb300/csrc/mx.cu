@@ -54,6 +54,60 @@ __device__ __forceinline__ uint2 encode8(const float* v, uint32_t b) {
   else return make_uint2(mx::to_e4m3x4(q), mx::to_e4m3x4(q + 4));
 }
 
+// N blocks with a lane per value (v[u] of block u): each largest magnitude goes to
+// a lane of its own, so that the scales are worked out once for all of them; put(u,
+// byte) stores this lane's element of block u (of e2m1 its pair with the next
+// lane's).  Returns the scale byte of block `lane`.
+template <int FMT, int N, typename Put>
+__device__ __forceinline__ uint32_t encode_blocks(float* v, int lane, Put put) {
+  uint32_t a = 0;
+#pragma unroll
+  for (int u = 0; u < N; ++u) {
+    const uint32_t m = __reduce_max_sync(0xffffffffu, mx::abs_bits(v[u]));
+    if (lane == u) a = m;
+  }
+  const uint32_t sb = mx::scale_byte<FMT>(a);
+  const float inv = mx::inverse_scale(sb);
+  if (__any_sync(0xffffffffu, sb == 255u)) {
+#pragma unroll
+    for (int u = 0; u < N; ++u)
+      if (__shfl_sync(0xffffffffu, sb, u) == 255u) v[u] = 0.f;
+  }
+#pragma unroll
+  for (int u = 0; u < N; u += 2) {
+    const float q0 = v[u] * __shfl_sync(0xffffffffu, inv, u), q1 = v[u + 1] * __shfl_sync(0xffffffffu, inv, u + 1);
+    if constexpr (FMT == MOE_MXFP8) {
+      uint32_t two;
+      asm("{\n\t.reg .b16 a;\n\tcvt.rn.satfinite.e4m3x2.f32 a, %2, %1;\n\tcvt.u32.u16 %0, a;\n\t}" : "=r"(two) : "f"(q0), "f"(q1));
+      put(u, two & 0xFFu);
+      put(u + 1, two >> 8);
+    } else {
+      const float n0 = __shfl_down_sync(0xffffffffu, q0, 1), n1 = __shfl_down_sync(0xffffffffu, q1, 1);
+      uint32_t two;
+      asm("{\n\t.reg .b8 a, b, z;\n\tcvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+          "mov.b32 %0, {a, b, a, b};\n\t}"
+          : "=r"(two)
+          : "f"(q0), "f"(n0), "f"(q1), "f"(n1));
+      put(u, two & 0xFFu);
+      put(u + 1, two >> 8 & 0xFFu);
+    }
+  }
+  return sb;
+}
+// The values of two blocks: q0, q1 the bytes that hold this lane's elements
+template <int FMT>
+__device__ __forceinline__ float2 decode_pair(uint32_t q0, uint32_t q1, int lane) {
+  uint32_t h;
+  if constexpr (FMT == MOE_MXFP8) {
+    asm("{\n\t.reg .b16 a;\n\tcvt.u16.u32 a, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\t}" : "=r"(h) : "r"(q0 | q1 << 8));
+  } else {
+    const int s = 4 * (lane & 1);
+    const uint32_t both4 = (q0 >> s & 15u) | (q1 >> s & 15u) << 4;
+    asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, a;\n\t}" : "=r"(h) : "r"(both4));
+  }
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+
 // The bits of the largest magnitude, as FP32, of a block that four lanes hold 8
 // 16-bit values of each: two values an instruction; NaN wins.
 template <typename T>
@@ -131,24 +185,15 @@ mx_quantize_segments(const T* __restrict__ x, int64_t R, int64_t C, int segs, ui
   float v[kSegBlocks];
 #pragma unroll
   for (int u = 0; u < kSegBlocks; ++u) v[u] = u * 32 + lane < left ? to_f32<T>(xr[u * 32 + lane]) : 0.f;
-  uint32_t mine = 0;  // lane u: the byte of block u
-#pragma unroll
-  for (int u = 0; u < kSegBlocks; ++u) {
-    if (u * 32 >= left) break;
+  const uint32_t mine = encode_blocks<FMT, kSegBlocks>(v, lane, [&](int u, uint32_t byte) {
     const int c = u * 32 + lane;
-    const uint32_t a = __reduce_max_sync(0xffffffffu, mx::abs_bits(v[u]));
-    const uint32_t b = mx::scale_byte<FMT>(a);
-    const float q[4] = {b == 255u ? 0.f : v[u] * mx::inverse_scale(b), 0.f, 0.f, 0.f};
     if constexpr (FMT == MOE_MXFP8) {
-      if (c < left) vr[c] = (uint8_t)mx::to_e4m3x4(q);
+      if (c < left) vr[c] = (uint8_t)byte;
     } else {
-      const float q1 = __shfl_down_sync(0xffffffffu, q[0], 1);
-      const float both[8] = {q[0], q1, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      if (c < left && (lane & 1) == 0) vr[c >> 1] = (uint8_t)mx::to_e2m1x8(both);
+      if (c < left && (lane & 1) == 0) vr[c >> 1] = (uint8_t)byte;
     }
-    if (lane == u) mine = b;
-  }
-  if (lane * 32 < left) sr[lane] = (uint8_t)mine;
+  });
+  if (lane < kSegBlocks && lane * 32 < left) sr[lane] = (uint8_t)mine;
 }
 
 // Any row length and alignment, short rows: a warp takes kRun blocks, one behind
@@ -156,8 +201,9 @@ mx_quantize_segments(const T* __restrict__ x, int64_t R, int64_t C, int segs, ui
 // looks block u up.
 constexpr int kRun = 16;
 // Segments that are mostly full are faster (4097 rows of 1001 FP16 values to 8
-// bits: 7.5 against 9 us), short rows leave most of one empty (1027166 rows of 102
-// FP32 values to 4 bits and back: 594 us in segments, 387 in runs).
+// bits and back in 8194 rows: 15 against 21 us), short rows leave most of one empty
+// (1027166 rows of 102 FP32 values to 4 bits and back: 594 against 384 us, both
+// before the scales of a run were worked out together; 304 us now).
 __host__ inline bool long_rows(int64_t C) { return C > kSegment * 5 / 8; }
 __device__ __forceinline__ int64_t shfl64(int64_t v, int u) {
   return __shfl_sync(0xffffffffu, (long long)v, u);
@@ -189,23 +235,15 @@ mx_quantize_rows(const T* __restrict__ x, int64_t blocks, int64_t C, uint8_t* __
     const int l = __shfl_sync(0xffffffffu, left, u);
     v[u] = u < n && lane < l ? to_f32<T>(x[p + lane]) : 0.f;
   }
-  uint32_t mine = 0;  // lane u: the byte of block u
-#pragma unroll
-  for (int u = 0; u < kRun; ++u) {
-    const uint32_t a = __reduce_max_sync(0xffffffffu, mx::abs_bits(v[u]));
-    const uint32_t sb = mx::scale_byte<FMT>(a);
-    const float q[4] = {sb == 255u ? 0.f : v[u] * mx::inverse_scale(sb), 0.f, 0.f, 0.f};
+  const uint32_t mine = encode_blocks<FMT, kRun>(v, lane, [&](int u, uint32_t byte) {
     const int64_t p = shfl64(at, u);
     const int l = __shfl_sync(0xffffffffu, left, u);
     if constexpr (FMT == MOE_MXFP8) {
-      if (u < n && lane < l) values[p + lane] = (uint8_t)mx::to_e4m3x4(q);
+      if (u < n && lane < l) values[p + lane] = (uint8_t)byte;
     } else {
-      const float q1 = __shfl_down_sync(0xffffffffu, q[0], 1);
-      const float two[8] = {q[0], q1, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      if (u < n && lane < l && (lane & 1) == 0) values[p + (lane >> 1)] = (uint8_t)mx::to_e2m1x8(two);
+      if (u < n && lane < l && (lane & 1) == 0) values[p + (lane >> 1)] = (uint8_t)byte;
     }
-    if (lane == u) mine = sb;
-  }
+  });
   if (lane < n) scales[b0 + lane] = (uint8_t)mine;
 }
 
@@ -282,7 +320,7 @@ mx_dequantize_rows(const uint8_t* __restrict__ values, const uint8_t* __restrict
   const int held = src < R ? left : 0;  // values to read
   const int64_t at = FMT == MOE_MXFP4 ? src * ((C + 1) / 2) + b * 16 : src * C + b * 32;
   const int64_t to = r * C + b * 32;
-  const uint32_t mine = src < R ? (uint32_t)__ldg(scales + src * nb + b) : 0u;
+  const float mine = mx::scale_value(src < R ? (uint32_t)__ldg(scales + src * nb + b) : 0u);
   const int n = (int)min((int64_t)kRun, blocks - b0);
   uint32_t q[kRun];
 #pragma unroll
@@ -292,14 +330,16 @@ mx_dequantize_rows(const uint8_t* __restrict__ values, const uint8_t* __restrict
     q[u] = u < n && lane < l ? (uint32_t)__ldg(values + p + (FMT == MOE_MXFP4 ? lane >> 1 : lane)) : 0u;
   }
 #pragma unroll
-  for (int u = 0; u < kRun; ++u) {
-    const float s = mx::scale_value(__shfl_sync(0xffffffffu, mine, u));
-    const int64_t p = shfl64(to, u);
-    const int l = __shfl_sync(0xffffffffu, left, u);
-    float v[8];
-    if constexpr (FMT == MOE_MXFP4) mx::from_e2m1x8(q[u] >> (4 * (lane & 1)), v);
-    else mx::from_e4m3x4(q[u], v);
-    if (u < n && lane < l) out[p + lane] = from_f32<T>(v[0] * s);
+  for (int u = 0; u < kRun; u += 2) {
+    const float2 v = decode_pair<FMT>(q[u], q[u + 1], lane);
+    const float f[2] = {v.x, v.y};
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      const float s = __shfl_sync(0xffffffffu, mine, u + w);
+      const int64_t p = shfl64(to, u + w);
+      const int l = __shfl_sync(0xffffffffu, left, u + w);
+      if (u + w < n && lane < l) out[p + lane] = from_f32<T>(f[w] * s);
+    }
   }
 }
 
@@ -323,17 +363,16 @@ mx_dequantize_segments(const uint8_t* __restrict__ values, const uint8_t* __rest
     const int c = u * 32 + lane;
     q[u] = c < left ? (uint32_t)__ldg(vr + (FMT == MOE_MXFP4 ? c >> 1 : c)) : 0u;
   }
-  // lane u: the byte of block u
-  const uint32_t mine = lane * 32 < left ? (uint32_t)__ldg(scales + src * nb + c0 / 32 + lane) : 0u;
+  // lane u: the scale of block u
+  const float mine = mx::scale_value(lane * 32 < left ? (uint32_t)__ldg(scales + src * nb + c0 / 32 + lane) : 0u);
   T* o = out + r * C + c0;
   const int end = (int)min((int64_t)kSegment, C - c0);
 #pragma unroll
-  for (int u = 0; u < kSegBlocks; ++u) {
-    const float s = mx::scale_value(__shfl_sync(0xffffffffu, mine, u));
-    float v[8];
-    if constexpr (FMT == MOE_MXFP4) mx::from_e2m1x8(q[u] >> (4 * (lane & 1)), v);
-    else mx::from_e4m3x4(q[u], v);
-    if (u * 32 + lane < end) o[u * 32 + lane] = from_f32<T>(v[0] * s);
+  for (int u = 0; u < kSegBlocks; u += 2) {
+    const float2 v = decode_pair<FMT>(q[u], q[u + 1], lane);
+    const float s0 = __shfl_sync(0xffffffffu, mine, u), s1 = __shfl_sync(0xffffffffu, mine, u + 1);
+    if (u * 32 + lane < end) o[u * 32 + lane] = from_f32<T>(v.x * s0);
+    if (u * 32 + 32 + lane < end) o[u * 32 + 32 + lane] = from_f32<T>(v.y * s1);
   }
 }
 
@@ -369,9 +408,10 @@ __device__ __forceinline__ void unit_starts(const uint32_t* s_off, int E, uint32
 constexpr int kSmallSlots = 256;
 
 // Rows of C values (C a multiple of 32) to e2m1 in dispatch order, scales in
-// the order of the products.  A warp per source row, 8 values a lane, 1024
-// columns at a time; the next columns (or the next row's) are asked for before
-// these are rounded.  A block makes its table of expert starts once and takes
+// the order of the products.  A warp takes 1024 columns of a source row at a
+// time, 8 values a lane, and asks for its next ones before these are rounded;
+// neighbouring warps take a row's neighbouring columns, so that a few long rows
+// spread over the SMs too.  A block makes its table of expert starts once and takes
 // many rows.  With slot_row, source row t goes to the dispatch rows
 // slot_row[t k + j]: a token is read and rounded once however many experts it
 // goes to.
@@ -400,10 +440,14 @@ mx4_rows_kernel(const T* __restrict__ x, int64_t rows, int64_t C, const uint32_t
   uint32_t* s_expert = s_unit + E + 1;     // kDispatch
   uint32_t* s_row = s_expert + kSmallSlots;
   const int lane = threadIdx.x & 31;
-  const int64_t warps = (int64_t)gridDim.x * kWarps;
-  int64_t src = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
   const int64_t vb = C / 2;
   const int chunks = (int)((C + 1023) / 1024);
+  // this warp's row and part of it, and the step to its next ones
+  const uint32_t warps = gridDim.x * kWarps, w0 = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  const int64_t step_row = warps / (uint32_t)chunks;
+  const int step_chunk = (int)(warps % (uint32_t)chunks);
+  int64_t src = w0 / (uint32_t)chunks;
+  int chunk = (int)(w0 % (uint32_t)chunks);
   uint4 raw[4];
   auto load = [&](int64_t row, int chunk) {
     const T* p = x + row * C + (int64_t)chunk * 1024;
@@ -416,7 +460,7 @@ mx4_rows_kernel(const T* __restrict__ x, int64_t rows, int64_t C, const uint32_t
   };
   pdl_wait();
   pdl_trigger();
-  if (src < rows) load(src, 0);
+  if (src < rows) load(src, chunk);
   if constexpr (ROWS == kDispatch) {
     static_assert(kSmallSlots <= kThreads, "a thread per slot");
     const int n = (int)rows * k, i = threadIdx.x;
@@ -472,64 +516,69 @@ mx4_rows_kernel(const T* __restrict__ x, int64_t rows, int64_t C, const uint32_t
   __syncthreads();
   const uint32_t first = s_off[0], last = s_off[E];
   const int64_t spans = mx::spans(C);
-  for (; src < rows; src += warps) {
-    for (int chunk = 0; chunk < chunks; ++chunk) {
-      uint4 cur[4];
+  while (src < rows) {
+    uint4 cur[4];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) cur[u] = raw[u];
-      if (chunk + 1 < chunks) load(src, chunk + 1);
-      else if (src + warps < rows) load(src + warps, 0);
-      uint32_t q[4], w[8];  // w: the chunk's two spans of scales
+    for (int u = 0; u < 4; ++u) cur[u] = raw[u];
+    int64_t next = src + step_row;
+    int next_chunk = chunk + step_chunk;
+    if (next_chunk >= chunks) {
+      next_chunk -= chunks;
+      ++next;
+    }
+    if (next < rows) load(next, next_chunk);
+    uint32_t q[4], w[8];  // w: the chunk's two spans of scales
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const uint32_t b = mx::scale_byte<MOE_MXFP4>(block_max<T>(cur[u]));
+      // (a block with a NaN has scale NaN; its elements then do not matter)
+      const float2 inv = both(mx::inverse_scale(b));
+      float v[8];
+      unpack8<T>(cur[u], v);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 y = mul2(make_float2(v[2 * i], v[2 * i + 1]), inv);
+        v[2 * i] = y.x;
+        v[2 * i + 1] = y.y;
+      }
+      q[u] = mx::to_e2m1x8(v);
+      uint32_t word = b << (8 * ((lane >> 2) & 3));  // four blocks of 16 lanes in one word
+      word |= __shfl_xor_sync(0xffffffffu, word, 4);
+      word |= __shfl_xor_sync(0xffffffffu, word, 8);
+      w[2 * u] = word;
+      w[2 * u + 1] = __shfl_xor_sync(0xffffffffu, word, 16);
+    }
+    const int left = (int)(C - (int64_t)chunk * 1024);
+    for (int j = 0; j < k; ++j) {
+      uint32_t r;
+      int e;
+      if constexpr (ROWS == kDispatch) {
+        r = s_row[src * k + j];
+        e = (int)s_expert[src * k + j];
+      } else {
+        r = ROWS == kSlots ? __ldg(slot_row + src * k + j) : (uint32_t)src;
+        if (r < first || r >= last) continue;
+        e = warp_search(s_off, E, r);
+      }
+      const uint32_t local = r - s_off[e];
+      uint8_t* vr = values + (int64_t)r * vb + (int64_t)chunk * 512;
+      uint8_t* sr = scales +
+                    (((int64_t)(s_unit[e] + (local >> 8)) * spans + 2 * chunk) * mx::kUnitGroups + (local >> 5 & 7u)) *
+                        mx::kGroupBytes +
+                    (local & 31u) * 16;
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
-        const uint32_t b = mx::scale_byte<MOE_MXFP4>(block_max<T>(cur[u]));
-        // (a block with a NaN has scale NaN; its elements then do not matter)
-        const float2 inv = both(mx::inverse_scale(b));
-        float v[8];
-        unpack8<T>(cur[u], v);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 y = mul2(make_float2(v[2 * i], v[2 * i + 1]), inv);
-          v[2 * i] = y.x;
-          v[2 * i + 1] = y.y;
-        }
-        q[u] = mx::to_e2m1x8(v);
-        uint32_t word = b << (8 * ((lane >> 2) & 3));  // four blocks of 16 lanes in one word
-        word |= __shfl_xor_sync(0xffffffffu, word, 4);
-        word |= __shfl_xor_sync(0xffffffffu, word, 8);
-        w[2 * u] = word;
-        w[2 * u + 1] = __shfl_xor_sync(0xffffffffu, word, 16);
+        const int c = u * 256 + lane * 8;
+        if (c < left) *reinterpret_cast<uint32_t*>(vr + c / 2) = q[u];
       }
-      const int left = (int)(C - (int64_t)chunk * 1024);
-      for (int j = 0; j < k; ++j) {
-        uint32_t r;
-        int e;
-        if constexpr (ROWS == kDispatch) {
-          r = s_row[src * k + j];
-          e = (int)s_expert[src * k + j];
-        } else {
-          r = ROWS == kSlots ? __ldg(slot_row + src * k + j) : (uint32_t)src;
-          if (r < first || r >= last) continue;
-          e = warp_search(s_off, E, r);
-        }
-        const uint32_t local = r - s_off[e];
-        uint8_t* vr = values + (int64_t)r * vb + (int64_t)chunk * 512;
-        uint8_t* sr = scales +
-                      (((int64_t)(s_unit[e] + (local >> 8)) * spans + 2 * chunk) * mx::kUnitGroups + (local >> 5 & 7u)) *
-                          mx::kGroupBytes +
-                      (local & 31u) * 16;
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int c = u * 256 + lane * 8;
-          if (c < left) *reinterpret_cast<uint32_t*>(vr + c / 2) = q[u];
-        }
-        if (lane == 0) {
-          *reinterpret_cast<uint4*>(sr) = make_uint4(w[0], w[1], w[2], w[3]);
-          if (left > 512)
-            *reinterpret_cast<uint4*>(sr + mx::kUnitGroups * mx::kGroupBytes) = make_uint4(w[4], w[5], w[6], w[7]);
-        }
+      if (lane == 0) {
+        *reinterpret_cast<uint4*>(sr) = make_uint4(w[0], w[1], w[2], w[3]);
+        if (left > 512)
+          *reinterpret_cast<uint4*>(sr + mx::kUnitGroups * mx::kGroupBytes) = make_uint4(w[4], w[5], w[6], w[7]);
       }
     }
+    src = next;
+    chunk = next_chunk;
   }
 }
 
@@ -643,7 +692,8 @@ static cudaError_t rows_t(const void* x, int64_t rows, int64_t C, const uint32_t
                           const uint32_t* offsets, int E, uint8_t* values, uint8_t* scales, const RowsArgs& ra,
                           int num_sms, cudaStream_t s) {
   // four blocks stay on an SM
-  const unsigned grid = (unsigned)std::min<int64_t>((rows + kWarps - 1) / kWarps, (int64_t)num_sms * 4);
+  const int64_t items = rows * ((C + 1023) / 1024);
+  const unsigned grid = (unsigned)std::min<int64_t>((items + kWarps - 1) / kWarps, (int64_t)num_sms * 4);
   const size_t smem = 4 * (2 * (size_t)(E + 1) + (ROWS == kDispatch ? 2 * kSmallSlots : 0));
   return launch_pdl(mx4_rows_kernel<T, ROWS>, dim3(grid), dim3(kThreads), smem, s, static_cast<const T*>(x), rows, C,
                     slot_row, k, offsets, E, values, scales, ra);
