@@ -156,6 +156,37 @@ def test_few_tiles_over_many_rows(cuda_lib, T, E, k, H, I, skew):
     assert all(torch.equal(a, b) for a, b in zip(got, s.backward(ck)))
 
 
+@pytest.mark.parametrize("T,E,k,H,I,skew", [(3, 4, 2, 72, 1000, 0.0), (30, 6, 2, 296, 808, 3.0), (1, 1, 1, 8, 2056, 0.0),
+                                            (300, 2, 1, 264, 1032, 0.5), (513, 1, 1, 40, 520, 0.0)])
+@pytest.mark.parametrize("dt", sorted(DT))
+def test_few_tiles_over_long_rows(cuda_lib, T, E, k, H, I, skew, dt):
+    """dinput of few tiles: its sums over the intermediate size are cut into parts that are joined."""
+    s = Step(cuda_lib, T, E, k, H, I, DT[dt], skew=skew)
+    _, ck = s.forward()
+    ws = s.ex.backward_checkpoint_workspace(T * k)
+    ws.fill_(0xFF)
+    got = s.backward(ck, workspace=ws)
+    check(s, ck, got, s.dout)
+    assert cuda_lib.moe_get_device_status(ws) == 0
+    assert all(torch.equal(a, b) for a, b in zip(got, s.backward(ck)))
+
+
+@pytest.mark.parametrize("I", [64, 1032])
+def test_rows_behind_the_last_of_two_segments(cuda_lib, I):
+    """An expert without rows, and rows behind the last segment, which no part of a sum may touch."""
+    moe = cuda_lib
+    s = Step(moe, 50, 2, 2, 64, I, torch.bfloat16)
+    _, ck = s.forward()
+    off = torch.tensor([0, 0, 33], dtype=torch.int32, device="cuda")
+    grads = [torch.full(t, 3.0, dtype=torch.bfloat16, device="cuda") for t in
+             ((100, 64), (2, I, 64), (2, I, 64), (2, 64, I))]
+    dout = s.dout.clone()
+    dout[33:] = float("nan")
+    s.ex.backward_checkpoint(s.x_mx, s.d.perm, off, ck, dout, 2, grads=tuple(grads))
+    assert (grads[0][33:] == 3).all() and torch.isfinite(grads[0][:33]).all()
+    assert all(not g[0].any() and torch.isfinite(g[1]).all() and g[1].any() for g in grads[1:])
+
+
 @pytest.mark.parametrize("T,E,k,I", [(40, 4, 2, 64), (500, 2, 1, 64)])
 def test_what_is_not_finite_stays_in_its_expert(cuda_lib, T, E, k, I):
     """A NaN in a row of dout, next to a segment's end, reaches its own dinput row and its own

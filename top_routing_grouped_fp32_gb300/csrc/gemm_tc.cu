@@ -137,8 +137,8 @@ struct Params {
   // copy; a segment's last rows, short of 64, come from a copy of their own
   // (64 rows an expert, zeros behind them; the mapA64 slot)
   int a_tail;
-  // kWgrad: parts that an expert's rows are cut into, each a tile of its own
-  // with an FP32 output [E, k_parts, ...]; 1: none
+  // parts that K is cut into, each a tile of its own with an FP32 output: of
+  // kWgrad [E, k_parts, ...], of kPartial [k_parts, m_total, n_out]; 0 or 1: none
   int k_parts;
   int64_t m_total;     // M of the product
   int64_t split;       // output rows per buffer (M, or I for the [dgate; dup] pair)
@@ -288,8 +288,8 @@ struct Tile {
   int64_t m0;  // first row of the (pair) tile
   int kx0;     // first K coordinate (0, or pad[e] for weight gradients)
   int nk;      // k-blocks of this tile
-  int kb0;     // its first k-block in the expert (split weight gradients)
-  int eo;      // where its output lies: the expert, or (expert, part of K)
+  int kb0;     // its first k-block, where K is cut into parts
+  int eo;      // weight gradients: (expert, part of K), where its output lies; else the part of K
   bool half;   // M = 128 pair tile (64 rows per CTA): see Params::half_tails
   bool thin;   // single-CTA tile of at most 32 rows: see Params::thin_a
 };
@@ -297,6 +297,12 @@ struct Tile {
 // By a converged warp.
 __device__ __forceinline__ Tile decode_tile(uint32_t tile, const Params& p, const uint32_t* s_pref,
                                             const uint32_t* s_off, int tile_m) {
+  uint32_t part = 0;
+  if (p.k_parts > 1) {  // the tiles of one part of K, then those of the next
+    const uint32_t base = s_pref[p.E] * (uint32_t)p.nb;
+    part = small_div(tile, base);
+    tile -= part * base;
+  }
   const uint32_t q = small_div(tile, (uint32_t)p.nb);
   const int lo = warp_search(s_pref, p.E, q);
   const uint32_t mte = s_pref[lo + 1] - s_pref[lo];
@@ -311,9 +317,9 @@ __device__ __forceinline__ Tile decode_tile(uint32_t tile, const Params& p, cons
   t.nb = (int)(pid * w + rem - mt * width);
   t.m0 = (int64_t)s_off[lo] + (int64_t)mt * tile_m;
   t.kx0 = 0;
-  t.nk = p.k_blocks;
-  t.kb0 = 0;
-  t.eo = lo;
+  t.kb0 = p.k_parts > 1 ? (int)((uint32_t)p.k_blocks * part / (uint32_t)p.k_parts) : 0;
+  t.nk = (p.k_parts > 1 ? (int)((uint32_t)p.k_blocks * (part + 1) / (uint32_t)p.k_parts) : p.k_blocks) - t.kb0;
+  t.eo = (int)part;
   t.half = p.half_tails && (int64_t)s_off[lo + 1] - t.m0 <= BM;
   t.thin = p.thin_a && (int64_t)s_off[lo + 1] - t.m0 <= 32;
   return t;
@@ -437,7 +443,7 @@ grouped_gemm_tc(const __grid_constant__ CUtensorMap mapA, const __grid_constant_
   tc_fence_after();
   const uint32_t tmem_base = __shfl_sync(0xffffffffu, *tmem_slot, 0);
   const uint32_t total_tiles = __shfl_sync(
-      0xffffffffu, p.wgrad ? (uint32_t)E * (uint32_t)(p.mb * p.nb * p.k_parts) : s_pref[E] * (uint32_t)p.nb, 0);
+      0xffffffffu, p.wgrad ? (uint32_t)E * (uint32_t)(p.mb * p.nb * p.k_parts) : s_pref[E] * (uint32_t)(p.nb * max(p.k_parts, 1)), 0);
   auto tile_at = [&](uint32_t tile) {
     return p.wgrad ? decode_wgrad(tile, p, s_pref, C::TILE_M) : decode_tile(tile, p, s_pref, s_off, C::TILE_M);
   };
@@ -477,7 +483,9 @@ grouped_gemm_tc(const __grid_constant__ CUtensorMap mapA, const __grid_constant_
       const uint32_t stage_tx = half   ? (C::STAGE_BYTES - KS * A_BYTES / 2) * PAIR
                                 : thin ? (C::STAGE_BYTES - KS * (A_BYTES - A_BYTES / 4)) * PAIR
                                        : C::STAGE_BYTES * PAIR;
-      for (int kb = 0; kb < nk; ++kb) {
+      // k-blocks of weight gradients count from the tile's first row, others from the row's start
+      const int kfirst = p.wgrad ? 0 : __shfl_sync(0xffffffffu, t.kb0, 0);
+      for (int kb = kfirst; kb < kfirst + nk; ++kb) {
         ok = __all_sync(0xffffffffu, mbar_wait<kCluster>(empty_bar(stage), phase ^ 1u, abort_flag, p.status));
         if (!ok) break;
         if (elect_one()) {
@@ -715,6 +723,24 @@ grouped_gemm_tc(const __grid_constant__ CUtensorMap mapA, const __grid_constant_
             staged_store<16>(stg, wdg, dgp ? dgp + 16 * ci : nullptr, vw, lane);
             staged_store<16>(stg, wdu, dup_p ? dup_p + 16 * ci : nullptr, vw, lane);
             staged_store<16>(stg, wa, ap ? ap + 16 * ci : nullptr, vw, lane);
+          }
+        } else if (p.mode == kPartial) {
+          // one part of a long K: FP32 sums, joined afterwards
+          const int64_t col0 = (int64_t)t.nb * 256 + (int64_t)nhalf * 128;
+          float* row = static_cast<float*>(p.out) + ((int64_t)t.eo * p.m_total + grow) * p.n_out + col0;
+#pragma unroll 1
+          for (int c = 0; c < (t.half ? 128 : 256); c += 32) {
+            if (col0 + c >= p.n_out) break;
+            uint32_t o[32];
+            __syncwarp();
+            tmem_ld32(taddr + c, o);
+            tmem_wait_ld(o);
+            const int vw = valid_words<float>(p.n_out - col0 - c);
+            if (row_ok)
+#pragma unroll
+              for (int v = 0; v < 8; ++v)
+                if (4 * v < vw)
+                  *reinterpret_cast<uint4*>(row + c + 4 * v) = make_uint4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]);
           }
         } else {
           // kWgrad: rows of a weight-gradient tile, rounded once to T (an
@@ -1104,7 +1130,7 @@ cudaError_t launch_t(int64_t N, int E, const CUtensorMap& mA, const CUtensorMap&
     tiles_max = (int64_t)E * p.mb * p.nb * p.k_parts;
   } else {
     const int64_t mt_max = (N + TM - 1) / TM + std::min<int64_t>(E, N);
-    tiles_max = mt_max * p.nb;
+    tiles_max = mt_max * p.nb * std::max(p.k_parts, 1);
   }
   const int nclu = (int)std::max<int64_t>(1, std::min<int64_t>(clusters, tiles_max));
   // panel width: about one wave of clusters spread over an expert's expected m-tiles
@@ -1355,6 +1381,18 @@ int wgrad_parts(int64_t N, int E, int64_t m, int64_t n) {
   return (int)std::max<int64_t>(1, std::min(kPairs / tiles, N / ((int64_t)E * 4 * BK)));
 }
 
+// Parts that dinput's K = 2 I is cut into where its tiles are fewer than the SMs
+// (few rows, H short): as many as fill them, of eight k-blocks at least.  A
+// captured backward of 30 rows over five experts of 696 x 3688 takes 86 us,
+// 135 with one part; of 1 row of 64 x 512, the smallest that is cut, 41 and 46.
+int dinput_parts(int64_t N, int E, int64_t H, int64_t I) {
+  constexpr int64_t kSms = 152;
+  const bool pair = N >= (int64_t)BM * E;
+  const int64_t mt = N / (pair ? 2 * BM : BM) + std::min<int64_t>(E, N);
+  const int64_t tiles = std::max<int64_t>(1, mt * ((H + 255) / 256));
+  return (int)std::max<int64_t>(1, std::min((pair ? kSms / 2 : kSms) / tiles, 2 * ((I + BK - 1) / BK) / 8));
+}
+
 CkLayout ck_layout(int64_t N, int E, int64_t H, int64_t I) {
   CkLayout L{};
   L.npad = N + 63 * (int64_t)E;
@@ -1370,7 +1408,9 @@ CkLayout ck_layout(int64_t N, int E, int64_t H, int64_t I) {
   L.xP = take((size_t)L.npad * H * 2);
   L.tails = take((size_t)E * BK * H * 2);
   const int pgu = wgrad_parts(N, E, 2 * I, H), pd = wgrad_parts(N, E, H, I);
-  L.parts = take((size_t)std::max(pgu > 1 ? 2 * pgu : 0, pd > 1 ? pd : 0) * E * I * H * 4);
+  const int px = dinput_parts(N, E, H, I);
+  L.parts = take(std::max((size_t)std::max(pgu > 1 ? 2 * pgu : 0, pd > 1 ? pd : 0) * E * I * H * 4,
+                          px > 1 ? (size_t)px * N * H * 4 : 0));
   L.total = off;
   return L;
 }
@@ -1433,7 +1473,18 @@ cudaError_t backward_ck_t(const ExpertsCkBwdArgs& a, char* ws, int num_sms, cuda
   p.nb = (int)((H + 255) / 256);
   p.out = a.dinput;
   p.v8_out = H % 16 == 0 && reinterpret_cast<uintptr_t>(a.dinput) % 32 == 0;
-  MOE_TC_TRY(launch_any<T>(pair, N, E, mDgduP, mWgMN, mWuMN, p, num_sms, s, &mDgduP64));
+  float* parts = reinterpret_cast<float*>(ws + L.parts);
+  const int px = dinput_parts(N, E, H, I);
+  if (px > 1) {
+    p.mode = kPartial;
+    p.k_parts = px;
+    p.m_total = N;
+    p.out = parts;
+    MOE_TC_TRY((launch_any<T, kUse>(pair, N, E, mDgduP, mWgMN, mWuMN, p, num_sms, s, &mDgduP64)));
+    MOE_TC_TRY(launch_join_rows(parts, px, N, H, a.offsets, E, a.dinput, dt, s));
+  } else {
+    MOE_TC_TRY(launch_any<T>(pair, N, E, mDgduP, mWgMN, mWuMN, p, num_sms, s, &mDgduP64));
+  }
   // weight gradients over the padded rows.  (On a stream beside the products
   // before, these copies take the same time off them: 2473 us against 2465 us
   // in order, headline shape.)
@@ -1447,7 +1498,6 @@ cudaError_t backward_ck_t(const ExpertsCkBwdArgs& a, char* ws, int num_sms, cuda
   p.k_parts = 1;
   p.a_mn = 1;
   p.b_form = kBMNmajor2d;
-  float* parts = reinterpret_cast<float*>(ws + L.parts);
   auto gradient = [&](const CUtensorMap& mA, const CUtensorMap& mB, const CUtensorMap* mTail, void* o1, void* o2) {
     p.mb = (int)((p.m_total + TM - 1) / TM);
     p.nb = (int)((p.n_out + 255) / 256);

@@ -199,6 +199,7 @@ enum GemmMode {
   // backward products (tcgen05 path only; da = dout W_down and dinput use kDownPlain)
   kSwigluBwd = 4,   // g, u recomputed, then [dg | du] (out) and a (out2), 16-bit
   kWgrad = 5,       // per-expert FP32 weight-gradient tiles over the padded rows
+  kPartial = 6,     // one part of K, FP32 rows
 };
 
 struct GemmArgs {
@@ -264,6 +265,9 @@ cudaError_t launch_pad_rows(const void* src, int64_t C, const uint32_t* offsets,
 cudaError_t launch_tail_rows(const void* src, int64_t C, const uint32_t* offsets, int E, void* dst, cudaStream_t s);
 // out [E, n] in dt = sum over the k parts of parts [E, k, n], in order
 cudaError_t launch_join_parts(const float* parts, int E, int k, int64_t n, void* out, moe_dtype dt, cudaStream_t s);
+// rows of the segments of out [N, H] in dt = sum over the k parts [k, N, H], in order
+cudaError_t launch_join_rows(const float* parts, int k, int64_t N, int64_t H, const uint32_t* offsets, int E, void* out,
+                             moe_dtype dt, cudaStream_t s);
 // pad_rows from 8-bit tokens: dispatched row r is token perm[r] / k (zeros past T)
 cudaError_t launch_pad_rows_mx8(const uint8_t* x, const uint8_t* scales, int64_t T, int64_t C, const uint32_t* perm,
                                 int k, const uint32_t* offsets, const uint32_t* pad, int E, int64_t npad_max,

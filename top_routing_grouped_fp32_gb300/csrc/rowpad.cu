@@ -144,12 +144,18 @@ pad_rows_mx8_kernel(const uint2* __restrict__ x, const uint8_t* __restrict__ sca
   }
 }
 
-// out[e, i] = sum over the parts of parts[e, part, i], in order, rounded once
+// out[e, i] = sum over the parts of parts[e, part, i], in order, rounded once.
+// With offsets (E = 1: rows of row_vecs vectors) only rows inside the segments.
 template <typename T>
 __global__ void __launch_bounds__(256)
-join_parts_kernel(const float4* __restrict__ parts, int k, int64_t vecs, int64_t total, uint4* __restrict__ out) {
+join_parts_kernel(const float4* __restrict__ parts, int k, int64_t vecs, int64_t total,
+                  const uint32_t* __restrict__ offsets, int last, int64_t row_vecs, uint4* __restrict__ out) {
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;  // 8 values
   if (i >= total) return;
+  if (offsets) {
+    const int64_t row = i / row_vecs;
+    if (row < (int64_t)offsets[0] || row >= (int64_t)offsets[last]) return;
+  }
   const int64_t e = i / vecs, v = i - e * vecs;
   const float4* s = parts + ((e * k) * vecs + v) * 2;
   float acc[8] = {};
@@ -164,13 +170,24 @@ join_parts_kernel(const float4* __restrict__ parts, int k, int64_t vecs, int64_t
 
 }  // namespace
 
-cudaError_t launch_join_parts(const float* parts, int E, int k, int64_t n, void* out, moe_dtype dt, cudaStream_t s) {
+static cudaError_t join(const float* parts, int E, int k, int64_t n, const uint32_t* offsets, int last,
+                        int64_t row_vecs, void* out, moe_dtype dt, cudaStream_t s) {
   const int64_t total = E * (n / 8);
   const unsigned blocks = (unsigned)((total + 255) / 256);
   const float4* p = reinterpret_cast<const float4*>(parts);
-  if (dt == MOE_BF16) join_parts_kernel<__nv_bfloat16><<<blocks, 256, 0, s>>>(p, k, n / 8, total, static_cast<uint4*>(out));
-  else join_parts_kernel<__half><<<blocks, 256, 0, s>>>(p, k, n / 8, total, static_cast<uint4*>(out));
+  uint4* o = static_cast<uint4*>(out);
+  if (dt == MOE_BF16) join_parts_kernel<__nv_bfloat16><<<blocks, 256, 0, s>>>(p, k, n / 8, total, offsets, last, row_vecs, o);
+  else join_parts_kernel<__half><<<blocks, 256, 0, s>>>(p, k, n / 8, total, offsets, last, row_vecs, o);
   return cudaGetLastError();
+}
+
+cudaError_t launch_join_parts(const float* parts, int E, int k, int64_t n, void* out, moe_dtype dt, cudaStream_t s) {
+  return join(parts, E, k, n, nullptr, 0, 1, out, dt, s);
+}
+
+cudaError_t launch_join_rows(const float* parts, int k, int64_t N, int64_t H, const uint32_t* offsets, int E, void* out,
+                             moe_dtype dt, cudaStream_t s) {
+  return join(parts, 1, k, N * H, offsets, E, H / 8, out, dt, s);
 }
 
 cudaError_t launch_tail_rows(const void* src, int64_t C, const uint32_t* offsets, int E, void* dst, cudaStream_t s) {
