@@ -64,6 +64,24 @@ def test_dispatched_rows(cuda_lib, H, I, counts, dt):
     assert torch.equal(out, ex.forward_dispatched(x, off))
 
 
+@pytest.mark.parametrize("H,I,counts", [
+    (64, 2688, [9000, 0, 300, 12800]), (1056, 2720, [5121, 255, 16000, 600]), (2048, 2688, [11000, 11001]),
+    (5376, 96, [9000, 0, 300, 12800]), (5408, 544, [1, 7000, 511, 14500]), (5408, 1568, [22001, 0, 0])])
+def test_many_rows(cuda_lib, H, I, counts):
+    """Weights' tiles kept for several of the rows' (three and four spans of 512 columns, cut and whole),
+    and loaded again (one and two)."""
+    moe = cuda_lib
+    ex, mx = make(moe, len(counts), H, I)
+    n = sum(counts)
+    x, off = rows(n, H, torch.bfloat16), segments(counts)
+    ws = ex.workspace(n)
+    ws.fill_(0xFF)
+    out = ex.forward_dispatched(x, off, workspace=ws)
+    check(moe, mx, x, off, out, torch.bfloat16)
+    assert moe.moe_get_device_status(ws) == 0
+    assert torch.equal(out, ex.forward_dispatched(x, off))
+
+
 @pytest.mark.parametrize("counts", [[3, 0, 20], [300, 0, 260]])
 def test_rows_outside_the_segments_are_left(cuda_lib, counts):
     moe = cuda_lib

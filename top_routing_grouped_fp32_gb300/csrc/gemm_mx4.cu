@@ -22,14 +22,14 @@
 //     over in pairs (512 columns, a span): one wait for eight MMAs.  The TMA and
 //     the MMA warp run their loops as whole warps and elect a lane to issue, so
 //     that operands are known to be uniform;
-//   * four more warps bring the scales of a span at a time: together they copy
-//     them several spans ahead into a ring of their own (cp.async, beside the
-//     TMA unit, which is busy), then each warp reads them (16 bytes a lane for
-//     32 rows), writes them to its quarter of the TMEM lanes with tcgen05.st
-//     (the MMA reads scales from all four), one set of columns for each slot
-//     pair, and arrives on the barrier of the pair's copies.  (Read ahead into
-//     registers instead, two spans do not fit beside eight epilogue warps, and
-//     with one the loads' latency is the kernel's pace.)
+//   * six more warps bring the scales: two copy them several spans ahead into
+//     a ring of their own (cp.async, beside the TMA unit, which is busy); each
+//     of the four others reads a span's (16 bytes a lane for 32 rows), writes
+//     them to its quarter of the TMEM lanes with tcgen05.st (the MMA reads
+//     scales from all four), one set of columns for each slot pair, and arrives
+//     on the barrier of the pair's copies.  Copied by the same four, 430 cycles
+//     a span, the scales were the kernel's pace (1070 cycles a span; the
+//     headline's products 502 -> 479 us with the rows, the wide ones' 544 -> 506).
 //     Copying them from shared memory (tcgen05.cp) instead holds up the MMAs:
 //     about 50 cycles a copy, six copies a slot (the headline's gate/up without
 //     its loads and epilogue: 367 us, 250 us of it MMAs), and loading them by
@@ -43,10 +43,12 @@
 //   * a gate/up tile's columns are its gate features, then the same up
 //     features (on CTA pairs the leader stages the gate rows, its peer the up
 //     rows), so that a lane holds both values of a feature.
-// What bounds it: on CTA pairs the bytes that an SM takes in and its shared
-// memory moves (28 KiB a slot, 53 bytes a cycle in, as many read by each MMA
-// again; loads alone take 181 of the headline gate/up's 231 us, MMAs alone at
-// their rate 146).  N = 256 would move a tenth less, for TMEM see above.
+// Where rows are 1025 to 2048 values long (HELD), an n-tile's B stays in shared
+// memory for up to four m-tiles, and the ring carries A alone.
+// What bounds it: on CTA pairs the depth that shared memory leaves the ring, three
+// spans: a span takes 1066 to 1120 cycles at prompt batches, 800 of them MMAs; the
+// MMA warp waits for copies, and these for free slots.  And power: these kernels
+// run below the top clock.  N = 256 would move a tenth less, for TMEM see above.
 // Single CTAs serve batches that hold few rows an expert: they are bound by
 // reading weights (32 tokens over 256 experts of 7168 x 2048, top-8: 580 us,
 // 6.6 TB/s), and many small tiles spread over the SMs.
@@ -75,23 +77,29 @@ using namespace tc;
 constexpr int BM = 128;
 constexpr uint32_t ROW_BYTES = 128;              // 256 values of a row
 constexpr uint32_t A_BYTES = BM * ROW_BYTES;     // 16 KiB
-constexpr int THREADS = 448;  // TMA, MMA, eight epilogue and four scale warps
+constexpr int THREADS = 512;  // TMA, MMA, eight epilogue and six scale warps
 constexpr uint32_t TMEM_COLS = 512;
 constexpr int MAX_E = 1024;
 
-template <int PAIR, int BN>
+constexpr int HELD_MIN = 3, HELD_SPANS = 4;  // spans of B that HELD keeps
+
+template <int PAIR, int BN, bool HELD>
 struct Cfg {
   static constexpr int B_ROWS = BN / PAIR;
   static constexpr uint32_t B_BYTES = B_ROWS * ROW_BYTES;
-  static constexpr uint32_t SLOT_BYTES = A_BYTES + B_BYTES;  // 256 columns
-  // pairs of slots in what 227 KiB hold beside the tables of MAX_E experts and the barriers
-  static constexpr int PAIRS =
-      (int)((232448 - 1024 - 512 - 4 * (PAIR == 2 ? 2 : 3) * (MAX_E + 1)) / SLOT_BYTES) / 2;
+  static constexpr uint32_t SLOT_BYTES = A_BYTES + (HELD ? 0 : B_BYTES);  // 256 columns
+  static constexpr uint32_t HELD_BYTES = HELD ? 2 * HELD_SPANS * B_BYTES : 0;
+  static constexpr int TABLES = PAIR == 2 && !HELD ? 2 : 3;
   static constexpr uint32_t SF_BYTES = (4 + BN / 32) * mx::kGroupBytes;  // a span's scales
-  // depth of their ring, in what is left
-  static constexpr int SF_RING = std::min<int>(
-      8, (int)(232448 - 1024 - 512 - 4 * (PAIR == 2 ? 2 : 3) * (MAX_E + 1) - 2 * PAIRS * SLOT_BYTES) / (int)SF_BYTES);
+  // what 227 KiB hold beside the tables of MAX_E experts and the barriers
+  static constexpr int ROOM = 232448 - 1024 - 512 - 4 * TABLES * (MAX_E + 1) - (int)HELD_BYTES;
+  static constexpr int PAIRS = (ROOM - (HELD ? 4 * (int)SF_BYTES : 0)) / (int)SLOT_BYTES / 2;  // of slots
+  // depth of the scales' ring, in what is left
+  static constexpr int SF_RING = std::min<int>(8, (ROOM - 2 * PAIRS * (int)SLOT_BYTES) / (int)SF_BYTES);
   static_assert(SF_RING >= 4, "scales are read ahead");
+  // A held span is read last a row's spans before it is written again, which the
+  // wait for A's slots of PAIRS spans ago then covers.
+  static_assert(!HELD || PAIRS <= HELD_MIN, "spans between two uses of a held span's place");
   static constexpr int TILE_M = BM * PAIR;
   static constexpr int GROUPS = BN / 32;  // 32-row groups of B
   // TMEM columns: two accumulators, then a set of a span's scales for each slot
@@ -107,6 +115,7 @@ struct Params {
   int E;
   int nb;         // n-tiles per m-tile
   int panel;
+  int chunk;      // HELD: m-tiles that share an n-tile's B, at most
   int steps;      // slots of a row: 256 columns each
   int gate_up;
   const uint8_t* sa;   // scales in product order
@@ -177,6 +186,7 @@ struct Tile {
   uint32_t unit;  // 256-row unit of scales, and the tile's first group in it
   uint32_t group;
   int a_rows;  // rows of A to load: 128, or 64 or 32 that hold all there are
+  int count;   // HELD: m-tiles in a row, from this one, with one B
 };
 
 // By a converged warp: every role asks for a tile at its start, and what that
@@ -200,28 +210,49 @@ __device__ __forceinline__ Tile decode_tile(uint32_t tile, const Params& p, cons
   t.group = tile_m == 256 ? 0u : 4u * (mt & 1u);
   const int64_t left = (int64_t)s_off[lo + 1] - t.m0;
   t.a_rows = !p.thin_a || left > 64 ? BM : left > 32 ? 64 : 32;
+  t.count = 1;
+  return t;
+}
+// HELD: an n-tile's neighbours take other n-tiles of the same rows.  s_chunk:
+// chunks of m-tiles of experts < e
+__device__ __forceinline__ Tile decode_chunk(uint32_t tile, const Params& p, const uint32_t* s_pref,
+                                             const uint32_t* s_chunk, const uint32_t* s_off, int tile_m) {
+  const uint32_t q = small_div(tile, (uint32_t)p.nb);
+  const int lo = warp_search(s_chunk, p.E, q);
+  const uint32_t mte = s_pref[lo + 1] - s_pref[lo], chunks = s_chunk[lo + 1] - s_chunk[lo], c = q - s_chunk[lo];
+  const uint32_t each = small_div(mte, chunks), more = mte - each * chunks;  // the first `more` have one more
+  const uint32_t m0 = c * each + min(c, more);
+  Tile t;
+  t.e = lo;
+  t.nb = (int)(tile - q * (uint32_t)p.nb);
+  t.m0 = (int64_t)s_off[lo] + (int64_t)m0 * tile_m;
+  t.unit = s_pref[lo] + m0;
+  t.group = 0;
+  t.a_rows = BM;
+  t.count = (int)(each + (c < more ? 1u : 0u));
   return t;
 }
 
-template <typename T, int PAIR, int BN>
+template <typename T, int PAIR, int BN, bool HELD>
 __global__ void __launch_bounds__(THREADS, 1)
 gemm_mx4_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapA64,
                 const __grid_constant__ CUtensorMap mapA32,
                 const __grid_constant__ CUtensorMap mapB0, const __grid_constant__ CUtensorMap mapB1, const Params p) {
-  using C = Cfg<PAIR, BN>;
+  using C = Cfg<PAIR, BN, HELD>;
   constexpr int PAIRS = C::PAIRS;
   constexpr bool kCluster = PAIR == 2;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_s = smem_u32(smem_raw);
   const uint32_t ring = (raw_s + 1023u) & ~1023u;
   uint8_t* ring_ptr = smem_raw + (ring - raw_s);
-  uint8_t* sf_ring = ring_ptr + 2 * PAIRS * C::SLOT_BYTES;
+  const uint32_t held = ring + 2 * PAIRS * C::SLOT_BYTES;
+  uint8_t* sf_ring = ring_ptr + 2 * PAIRS * C::SLOT_BYTES + C::HELD_BYTES;
   uint64_t* bars = reinterpret_cast<uint64_t*>(sf_ring + C::SF_RING * C::SF_BYTES);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 3 * PAIRS + 5 + 2 * C::SF_RING);
   volatile uint32_t* abort_flag = tmem_slot + 1;
   uint32_t* s_off = reinterpret_cast<uint32_t*>(reinterpret_cast<uint8_t*>(bars) + 512);
   uint32_t* s_pref = s_off + (p.E + 1);
-  uint32_t* s_unit = s_pref + (p.E + 1);  // PAIR == 1 only: a pair's tile is a unit
+  uint32_t* s_unit = s_pref + (p.E + 1);  // PAIR == 1 (a pair's tile is a unit), or HELD's chunks
 
   const uint32_t bar0 = smem_u32(bars);
   auto full_bar = [&](int q) { return bar0 + 8u * q; };               // a pair's copies and scales are there
@@ -249,7 +280,7 @@ gemm_mx4_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant_
       mbar_init(tempty_bar(a), 4 * PAIR);
     }
     for (int q = 0; q < C::SF_RING; ++q) {
-      mbar_init(sfull_bar(q), 128);  // every thread of the scale warps
+      mbar_init(sfull_bar(q), 64);  // every thread that copies
       mbar_init(sempty_bar(q), 4);
     }
     mbar_init(drain_bar, 1);
@@ -271,9 +302,9 @@ gemm_mx4_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant_
   pdl_trigger();
   for (int i = threadIdx.x; i <= E; i += THREADS) s_off[i] = p.offsets[i];
   __syncthreads();
-  if (warp == 2 || (warp == 3 && PAIR == 1)) {
-    // warp 2: tiles of experts < e; warp 3: 256-row units of scales of experts < e
-    const uint32_t unit = warp == 2 ? (uint32_t)C::TILE_M : 256u;
+  if (warp == 2 || (warp == 3 && C::TABLES == 3)) {
+    // warp 2: tiles of experts < e; warp 3: 256-row units of scales, or chunks, of experts < e
+    const uint32_t unit = warp == 2 ? (uint32_t)C::TILE_M : HELD ? (uint32_t)(C::TILE_M * p.chunk) : 256u;
     uint32_t* dst = warp == 2 ? s_pref : s_unit;
     const int per = (E + 31) / 32;
     uint32_t loc = 0;
@@ -302,8 +333,14 @@ gemm_mx4_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant_
   if constexpr (kCluster) cluster_sync();
   tc_fence_after();
   const uint32_t tmem_base = __shfl_sync(0xffffffffu, *tmem_slot, 0);
-  const uint32_t total_tiles = __shfl_sync(0xffffffffu, s_pref[E] * (uint32_t)p.nb, 0);
-  auto tile_at = [&](uint32_t tile) { return decode_tile(tile, p, s_pref, s_unit, s_off, C::TILE_M); };
+  // (HELD: "tiles" are chunks of m-tiles)
+  const uint32_t total_tiles = __shfl_sync(0xffffffffu, (HELD ? s_unit : s_pref)[E] * (uint32_t)p.nb, 0);
+  auto tile_at = [&](uint32_t tile) {
+    return HELD ? decode_chunk(tile, p, s_pref, s_unit, s_off, C::TILE_M)
+                : decode_tile(tile, p, s_pref, s_unit, s_off, C::TILE_M);
+  };
+  // the m-tiles of a chunk
+  auto count_of = [&](const Tile& t) { return HELD ? __shfl_sync(0xffffffffu, t.count, 0) : 1; };
   const uint32_t full0_leader = kCluster ? mapa(full_bar(0), 0) : full_bar(0);
   const uint32_t tempty0_leader = kCluster ? mapa(tempty_bar(0), 0) : tempty_bar(0);
   const int spans = (p.steps + 1) / 2;
@@ -321,25 +358,28 @@ gemm_mx4_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant_
       const int te = __shfl_sync(0xffffffffu, t.e, 0);
       const int tnb = __shfl_sync(0xffffffffu, t.nb, 0);
       const int a_rows = __shfl_sync(0xffffffffu, t.a_rows, 0);
-      const uint32_t slot_tx = (C::B_BYTES + (uint32_t)a_rows * ROW_BYTES) * PAIR;
+      const int count = count_of(t);
       const int n0 = tnb * (p.gate_up ? BN / 2 : BN);  // first feature, or first output column
       const int b_row = PAIR == 2 && !p.gate_up ? n0 + (int)rank * C::B_ROWS : n0;
-      for (int sp = 0; sp < spans; ++sp) {
+      int sp = 0, m = 0;
+      for (int i = 0; i < spans * count; ++i) {
         const bool two = 2 * sp + 1 < p.steps;
+        const uint32_t slot_tx = ((m == 0 ? C::B_BYTES : 0u) + (uint32_t)a_rows * ROW_BYTES) * PAIR;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           ok = __all_sync(0xffffffffu, mbar_wait<kCluster>(empty_bar(pr, h), phase ^ 1u, abort_flag, p.status));
           if (!ok) break;
           if ((h == 0 || two) && elect_one()) {
             const uint32_t sa = ring + (2 * pr + h) * C::SLOT_BYTES;
-            const uint32_t sb = sa + A_BYTES;
+            const uint32_t sb = HELD ? held + (2 * sp + h) * C::B_BYTES : sa + A_BYTES;
             const uint32_t fb = full0_leader + 8u * pr;
             const int kx = (2 * sp + h) * (int)ROW_BYTES;
             if (leader && h == 0) mbar_expect_tx(full_bar(pr), two ? 2 * slot_tx : slot_tx);
             if (a_rows == 32) tma_load_2d<PAIR>(sa, &mapA32, kx, a_row, fb);
             else if (a_rows == 64) tma_load_2d<PAIR>(sa, &mapA64, kx, a_row, fb);
-            else tma_load_2d<PAIR>(sa, &mapA, kx, a_row, fb);
-            if (PAIR == 2) {  // gate rows and up rows, or the two halves of the down rows
+            else tma_load_2d<PAIR>(sa, &mapA, kx, a_row + m * C::TILE_M, fb);
+            if (HELD && m != 0) {  // B is there
+            } else if (PAIR == 2) {  // gate rows and up rows, or the two halves of the down rows
               if (leader) tma_load_3d<PAIR>(sb, &mapB0, kx, b_row, te, fb);
               else tma_load_3d<PAIR>(sb, &mapB1, kx, b_row, te, fb);
             } else {
@@ -354,6 +394,10 @@ gemm_mx4_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant_
         if (++pr == PAIRS) {
           pr = 0;
           phase ^= 1u;
+        }
+        if (++sp == spans) {
+          sp = 0;
+          ++m;
         }
       }
     }
@@ -372,7 +416,8 @@ gemm_mx4_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant_
       int pr = 0;
       uint32_t phase = 0, acc = 0, acc_phase = 0;
       bool ok = true;
-      for (uint32_t tile = cluster_id; ok && tile < total_tiles; tile += num_clusters) {
+      int count = HELD && cluster_id < total_tiles ? count_of(tile_at(cluster_id)) : 1;
+      for (uint32_t tile = cluster_id; ok && tile < total_tiles;) {
         ok = __all_sync(0xffffffffu, mbar_wait<kCluster>(tempty_bar(acc), acc_phase ^ 1u, abort_flag, p.status));
         if (!ok) break;
         const uint32_t d_tmem = tmem_base + acc * BN;
@@ -386,7 +431,8 @@ gemm_mx4_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant_
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               if (h == 0 || 2 * sp + 1 < p.steps) {
-                const uint32_t sa = s0 + h * C::SLOT_BYTES, sb = sa + A_BYTES;
+                const uint32_t sa = s0 + h * C::SLOT_BYTES;
+                const uint32_t sb = HELD ? held + (2 * sp + h) * C::B_BYTES : sa + A_BYTES;
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {  // scales: bytes 0-1 or 2-3 of word 2 h + k / 2
                   const uint32_t id = idesc | (uint32_t)(k & 1) * ((2u << 29) | (2u << 4));
@@ -407,6 +453,10 @@ gemm_mx4_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant_
         }
         acc ^= 1u;
         if (acc == 0) acc_phase ^= 1u;
+        if (--count == 0) {
+          tile += num_clusters;
+          count = HELD && tile < total_tiles ? count_of(tile_at(tile)) : 1;
+        }
       }
       if (elect_one()) {
         umma_commit_local<PAIR>(drain_bar);
@@ -416,61 +466,59 @@ gemm_mx4_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant_
       }
       __syncwarp();
     }
+  } else if (warp >= 14) {
+    // ------------------------------------------------------------ scales: copies
+    constexpr int G = C::GROUPS, MINE = (4 + G) / 2;  // of A's 4 and B's G groups, every other one
+    static_assert(G % 2 == 0, "");
+    const int wi = warp - 14;
+    const uint32_t dst0 = smem_u32(sf_ring) + wi * mx::kGroupBytes + lane * 16;
+    const int64_t per = p.n_out / 32;  // groups of an expert
+    uint32_t slot = 0, phase = 0;
+    bool ok = true;
+    for (uint32_t tile = cluster_id; ok && tile < total_tiles; tile += num_clusters) {
+      const Tile t = tile_at(tile);
+      const int count = count_of(t);
+      const uint8_t* pa =
+          p.sa + ((int64_t)t.unit * spans * mx::kUnitGroups + t.group + rank * 4 + wi) * mx::kGroupBytes + lane * 16;
+      const uint8_t* pb[MINE - 2];
+#pragma unroll
+      for (int i = 0; i < MINE - 2; ++i) {
+        const int j = wi + 2 * i;  // the halves of the columns: gate and up features, or down columns
+        const bool second = p.gate_up && j >= G / 2;
+        const int64_t g = p.gate_up ? (int64_t)t.nb * (G / 2) + (second ? j - G / 2 : j) : (int64_t)t.nb * G + j;
+        pb[i] = g < per ? (second ? p.sb1 : p.sb0) + ((int64_t)t.e * spans * per + g) * mx::kGroupBytes + lane * 16
+                        : nullptr;
+      }
+      int sp = 0;
+      for (int i = 0; i < spans * count; ++i) {
+        ok = __all_sync(0xffffffffu, mbar_wait<false>(sempty_bar(slot), phase ^ 1u, abort_flag, p.status));
+        if (!ok) break;
+        const uint32_t dst = dst0 + slot * C::SF_BYTES;
+        async_copy16(dst, pa);
+        async_copy16(dst + 2 * mx::kGroupBytes, pa + 2 * mx::kGroupBytes);
+        pa += mx::kUnitGroups * mx::kGroupBytes;
+#pragma unroll
+        for (int j = 0; j < MINE - 2; ++j)
+          if (pb[j]) async_copy16(dst + (4 + 2 * j) * mx::kGroupBytes, pb[j] + sp * per * mx::kGroupBytes);
+        async_copy_arrive(sfull_bar(slot));
+        if (++sp == spans) sp = 0;
+        if (++slot == C::SF_RING) {
+          slot = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
   } else if (warp >= 10) {
-    // ------------------------------------------------------------ scales
+    // ------------------------------------------------------------ scales: to TMEM
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     constexpr int G = C::GROUPS, W = C::SF_WORDS, RING = C::SF_RING;
-    const uint32_t ring0 = smem_u32(sf_ring);
-    // the next span to copy: this warp's groups of A's 4 and B's G
-    const int wi = warp - 10;
-    constexpr int MINE = (G + 3) / 4;
-    uint32_t tile = cluster_id, isp = 0, islot = 0, iphase = 0;
-    const uint8_t* pa = nullptr;
-    const uint8_t* pb[MINE];
-    const int64_t per = p.n_out / 32;  // groups of an expert
     bool ok = true;
-    auto copy = [&]() {
-      if (tile >= total_tiles) return;
-      if (isp == 0) {
-        const Tile t = tile_at(tile);
-        pa = p.sa + ((int64_t)t.unit * spans * mx::kUnitGroups + t.group + rank * 4 + wi) * mx::kGroupBytes + lane * 16;
-#pragma unroll
-        for (int i = 0; i < MINE; ++i) {
-          const int j = wi + 4 * i;  // the halves of the columns: gate and up features, or down columns
-          const bool second = p.gate_up && j >= G / 2;
-          const int64_t g = p.gate_up ? (int64_t)t.nb * (G / 2) + (second ? j - G / 2 : j) : (int64_t)t.nb * G + j;
-          pb[i] = j < G && g < per
-                      ? (second ? p.sb1 : p.sb0) + ((int64_t)t.e * spans * per + g) * mx::kGroupBytes + lane * 16
-                      : nullptr;
-        }
-      }
-      ok = __all_sync(0xffffffffu, mbar_wait<false>(sempty_bar(islot), iphase ^ 1u, abort_flag, p.status));
-      if (!ok) return;
-      const uint32_t dst = ring0 + islot * C::SF_BYTES + wi * mx::kGroupBytes + lane * 16;
-      async_copy16(dst, pa);
-      pa += mx::kUnitGroups * mx::kGroupBytes;
-#pragma unroll
-      for (int i = 0; i < MINE; ++i)
-        if (pb[i]) {
-          async_copy16(dst + (4 + 4 * i) * mx::kGroupBytes, pb[i]);
-          pb[i] += per * mx::kGroupBytes;
-        }
-      async_copy_arrive(sfull_bar(islot));
-      if (++isp == (uint32_t)spans) {
-        isp = 0;
-        tile += num_clusters;
-      }
-      if (++islot == RING) {
-        islot = 0;
-        iphase ^= 1u;
-      }
-    };
-    for (int i = 0; i < RING - 1; ++i) copy();
     uint32_t pr = 0, phase = 0, slot = 0, sphase = 0;
     for (uint32_t mine = cluster_id; ok && mine < total_tiles; mine += num_clusters) {
-      for (int sp = 0; sp < spans; ++sp) {
-        copy();
-        ok = ok && __all_sync(0xffffffffu, mbar_wait<false>(sfull_bar(slot), sphase, abort_flag, p.status));
+      const int all = HELD ? spans * count_of(tile_at(mine)) : spans;
+      for (int sp = 0; sp < all; ++sp) {
+        ok = __all_sync(0xffffffffu, mbar_wait<false>(sfull_bar(slot), sphase, abort_flag, p.status));
         if (!ok) break;
         uint32_t w[W];
         const uint4* src = reinterpret_cast<const uint4*>(sf_ring + slot * C::SF_BYTES) + lane;
@@ -508,131 +556,137 @@ gemm_mx4_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant_
         }
       }
     }
-    asm volatile("cp.async.wait_all;" ::: "memory");
   } else {
     // ------------------------------------------------------------ epilogue
     // four warps for each accumulator: they have the time of two tiles
     const int quarter = warp & 3;
     const uint32_t acc = (uint32_t)(warp - 2) >> 2;
     uint32_t acc_phase = 0;
-    for (uint64_t tile = cluster_id + acc * num_clusters; tile < total_tiles; tile += 2 * num_clusters) {
-      const Tile t = tile_at((uint32_t)tile);
-      const int row = quarter * 32 + lane;
-      const int64_t grow = t.m0 + (int64_t)rank * BM + row;
-      const bool row_ok = grow < (int64_t)s_off[t.e + 1];
-      int64_t slot = grow;
-      float wscale = 1.f;
-      if (p.perm != nullptr && row_ok) {
-        const uint32_t s = __ldg(p.perm + grow);
-        slot = s;
-        wscale = load_dyn(p.weights, p.wdt, s);
-      }
-      int ok = 1;
-      if (lane == 0) ok = mbar_wait<kCluster>(tfull_bar(acc), acc_phase, abort_flag, p.status) ? 1 : 0;
-      ok = __shfl_sync(0xffffffffu, ok, 0);
-      if (!ok) break;
-      tc_fence_after();
-      const uint32_t taddr = tmem_base + ((uint32_t)(quarter * 32) << 16) + acc * BN;
-      // the warps' 32 rows have rows to store, or nothing is read
-      const bool any = __any_sync(0xffffffffu, row_ok);
-      if (any && p.gate_up) {
-        const int blocks = (int)(p.n_out / 32), b0 = t.nb * (BN / 64);
-        uint8_t* hrow = p.hq + grow * (p.n_out / 2);
-        uint8_t* srow = p.hs + ((int64_t)t.unit * p.h_spans * mx::kUnitGroups + t.group + rank * 4 + quarter) * mx::kGroupBytes +
-                        lane * 16;
-#pragma unroll 1
-        for (int b = 0; b < BN / 64; ++b) {
-          const int blk = b0 + b;
-          if (blk >= blocks) break;
-          uint32_t g[32], u[32];
-          __syncwarp();
-          tmem_ld32(taddr + b * 32, g);
-          tmem_ld32(taddr + BN / 2 + b * 32, u);
-          tmem_wait_ld(g);
-          reg_fence(u);
-          float2 h[16];
-          uint32_t a = 0;
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const float2 gg = make_float2(__uint_as_float(g[2 * i]), __uint_as_float(g[2 * i + 1]));
-            const float2 uu = make_float2(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1]));
-            const float2 t = mul2(gg, both(-kLog2e));
-            const float2 n = add2(make_float2(exp2_fast(t.x), exp2_fast(t.y)), both(1.f));
-            // a few ulp of FP32: far below an e2m1 step
-            h[i] = mul2(mul2(gg, uu), make_float2(rcp_fast(n.x), rcp_fast(n.y)));
-            a = max(a, max(mx::abs_bits(h[i].x), mx::abs_bits(h[i].y)));
-          }
-          const uint32_t sb = mx::scale_byte<MOE_MXFP4>(a);
-          // (a block with a NaN has scale NaN; its elements then do not matter)
-          const float2 inv = both(mx::inverse_scale(sb));
-          uint32_t w[4];
-#pragma unroll
-          for (int v = 0; v < 4; ++v) {
-            float q[8];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float2 y = mul2(h[4 * v + i], inv);
-              q[2 * i] = y.x;
-              q[2 * i + 1] = y.y;
-            }
-            w[v] = mx::to_e2m1x8(q);
-          }
-          if (row_ok) {
-            *reinterpret_cast<uint4*>(hrow + blk * 16) = make_uint4(w[0], w[1], w[2], w[3]);
-            uint8_t* d = srow + (int64_t)(blk >> 4) * (mx::kUnitGroups * mx::kGroupBytes);
-            d[blk & 15] = (uint8_t)sb;
-            if (blk == blocks - 1)  // the row's last span: finite scales behind its end
-              for (int c = (blk & 15) + 1; c < 16; ++c) d[c] = 0;
-          }
+    int ok = 1, parity = 0;
+    for (uint64_t tile = cluster_id + (HELD ? 0 : acc * num_clusters); ok && tile < total_tiles;
+         tile += (HELD ? 1 : 2) * num_clusters) {
+      Tile t = tile_at((uint32_t)tile);
+      const int count = count_of(t);
+      // HELD: every other one of the m-tiles that follow one another
+      for (int m = 0; m < count; ++m, t.m0 += C::TILE_M, ++t.unit, parity ^= 1) {
+        if (HELD && parity != (int)acc) continue;
+        const int row = quarter * 32 + lane;
+        const int64_t grow = t.m0 + (int64_t)rank * BM + row;
+        const bool row_ok = grow < (int64_t)s_off[t.e + 1];
+        int64_t slot = grow;
+        float wscale = 1.f;
+        if (p.perm != nullptr && row_ok) {
+          const uint32_t s = __ldg(p.perm + grow);
+          slot = s;
+          wscale = load_dyn(p.weights, p.wdt, s);
         }
-      } else if (any) {
-        const int64_t c0 = (int64_t)t.nb * BN;
+        if (lane == 0) ok = mbar_wait<kCluster>(tfull_bar(acc), acc_phase, abort_flag, p.status) ? 1 : 0;
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t taddr = tmem_base + ((uint32_t)(quarter * 32) << 16) + acc * BN;
+        // the warps' 32 rows have rows to store, or nothing is read
+        const bool any = __any_sync(0xffffffffu, row_ok);
+        if (any && p.gate_up) {
+          const int blocks = (int)(p.n_out / 32), b0 = t.nb * (BN / 64);
+          uint8_t* hrow = p.hq + grow * (p.n_out / 2);
+          uint8_t* srow =
+              p.hs + ((int64_t)t.unit * p.h_spans * mx::kUnitGroups + t.group + rank * 4 + quarter) * mx::kGroupBytes +
+              lane * 16;
 #pragma unroll 1
-        for (int c = 0; c < BN; c += 32) {
-          if (c0 + c >= p.n_out) break;
-          uint32_t o[32];
-          __syncwarp();
-          tmem_ld32(taddr + c, o);
-          tmem_wait_ld(o);
-          if (row_ok && p.perm != nullptr) {
-            float4* d = reinterpret_cast<float4*>(static_cast<float*>(p.out) + slot * p.n_out + c0 + c);
+          for (int b = 0; b < BN / 64; ++b) {
+            const int blk = b0 + b;
+            if (blk >= blocks) break;
+            uint32_t g[32], u[32];
+            __syncwarp();
+            tmem_ld32(taddr + b * 32, g);
+            tmem_ld32(taddr + BN / 2 + b * 32, u);
+            tmem_wait_ld(g);
+            reg_fence(u);
+            float2 h[16];
+            uint32_t a = 0;
 #pragma unroll
-            for (int v = 0; v < 8; ++v)
-              d[v] = make_float4(__uint_as_float(o[4 * v]) * wscale, __uint_as_float(o[4 * v + 1]) * wscale,
-                                 __uint_as_float(o[4 * v + 2]) * wscale, __uint_as_float(o[4 * v + 3]) * wscale);
-          } else if (row_ok) {
-            uint32_t* d = reinterpret_cast<uint32_t*>(static_cast<T*>(p.out) + slot * p.n_out + c0 + c);
-            uint32_t q[16];
+            for (int i = 0; i < 16; ++i) {
+              const float2 gg = make_float2(__uint_as_float(g[2 * i]), __uint_as_float(g[2 * i + 1]));
+              const float2 uu = make_float2(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1]));
+              const float2 t = mul2(gg, both(-kLog2e));
+              const float2 n = add2(make_float2(exp2_fast(t.x), exp2_fast(t.y)), both(1.f));
+              // a few ulp of FP32: far below an e2m1 step
+              h[i] = mul2(mul2(gg, uu), make_float2(rcp_fast(n.x), rcp_fast(n.y)));
+              a = max(a, max(mx::abs_bits(h[i].x), mx::abs_bits(h[i].y)));
+            }
+            const uint32_t sb = mx::scale_byte<MOE_MXFP4>(a);
+            // (a block with a NaN has scale NaN; its elements then do not matter)
+            const float2 inv = both(mx::inverse_scale(sb));
+            uint32_t w[4];
 #pragma unroll
             for (int v = 0; v < 4; ++v) {
-              float f[8];
+              float q[8];
 #pragma unroll
-              for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(o[v * 8 + i]);
-              const uint4 r = pack8<T>(f);
-              q[4 * v] = r.x;
-              q[4 * v + 1] = r.y;
-              q[4 * v + 2] = r.z;
-              q[4 * v + 3] = r.w;
+              for (int i = 0; i < 4; ++i) {
+                const float2 y = mul2(h[4 * v + i], inv);
+                q[2 * i] = y.x;
+                q[2 * i + 1] = y.y;
+              }
+              w[v] = mx::to_e2m1x8(q);
             }
-            if (p.v8_out) {  // whole 32-byte sectors
-              st_v8(d, q);
-              st_v8(d + 8, q + 8);
-            } else {
+            if (row_ok) {
+              *reinterpret_cast<uint4*>(hrow + blk * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+              uint8_t* d = srow + (int64_t)(blk >> 4) * (mx::kUnitGroups * mx::kGroupBytes);
+              d[blk & 15] = (uint8_t)sb;
+              if (blk == blocks - 1)  // the row's last span: finite scales behind its end
+                for (int c = (blk & 15) + 1; c < 16; ++c) d[c] = 0;
+            }
+          }
+        } else if (any) {
+          const int64_t c0 = (int64_t)t.nb * BN;
+#pragma unroll 1
+          for (int c = 0; c < BN; c += 32) {
+            if (c0 + c >= p.n_out) break;
+            uint32_t o[32];
+            __syncwarp();
+            tmem_ld32(taddr + c, o);
+            tmem_wait_ld(o);
+            if (row_ok && p.perm != nullptr) {
+              float4* d = reinterpret_cast<float4*>(static_cast<float*>(p.out) + slot * p.n_out + c0 + c);
 #pragma unroll
-              for (int v = 0; v < 4; ++v)
-                reinterpret_cast<uint4*>(d)[v] = make_uint4(q[4 * v], q[4 * v + 1], q[4 * v + 2], q[4 * v + 3]);
+              for (int v = 0; v < 8; ++v)
+                d[v] = make_float4(__uint_as_float(o[4 * v]) * wscale, __uint_as_float(o[4 * v + 1]) * wscale,
+                                   __uint_as_float(o[4 * v + 2]) * wscale, __uint_as_float(o[4 * v + 3]) * wscale);
+            } else if (row_ok) {
+              uint32_t* d = reinterpret_cast<uint32_t*>(static_cast<T*>(p.out) + slot * p.n_out + c0 + c);
+              uint32_t q[16];
+#pragma unroll
+              for (int v = 0; v < 4; ++v) {
+                float f[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(o[v * 8 + i]);
+                const uint4 r = pack8<T>(f);
+                q[4 * v] = r.x;
+                q[4 * v + 1] = r.y;
+                q[4 * v + 2] = r.z;
+                q[4 * v + 3] = r.w;
+              }
+              if (p.v8_out) {  // whole 32-byte sectors
+                st_v8(d, q);
+                st_v8(d + 8, q + 8);
+              } else {
+#pragma unroll
+                for (int v = 0; v < 4; ++v)
+                  reinterpret_cast<uint4*>(d)[v] = make_uint4(q[4 * v], q[4 * v + 1], q[4 * v + 2], q[4 * v + 3]);
+              }
             }
           }
         }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          // its TMEM reads are done; a release would wait for the tile's stores
+          if constexpr (kCluster) mbar_arrive_cluster_relaxed(tempty0_leader + 8u * acc);
+          else mbar_arrive(tempty_bar(acc));
+        }
+        acc_phase ^= 1u;
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        // its TMEM reads are done; a release would wait for the tile's stores
-        if constexpr (kCluster) mbar_arrive_cluster_relaxed(tempty0_leader + 8u * acc);
-        else mbar_arrive(tempty_bar(acc));
-      }
-      acc_phase ^= 1u;
     }
   }
 
@@ -668,16 +722,16 @@ bool encode_weights(CUtensorMap* m, const void* base, uint64_t E, uint64_t rows,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
-template <int PAIR, int BN>
+template <int PAIR, int BN, bool HELD>
 size_t smem_bytes(int E) {
-  using C = Cfg<PAIR, BN>;
-  return 1024 + (size_t)C::PAIRS * 2 * C::SLOT_BYTES + (size_t)C::SF_RING * C::SF_BYTES + 512 +
-         4 * (size_t)(PAIR == 2 ? 2 : 3) * (E + 1);
+  using C = Cfg<PAIR, BN, HELD>;
+  return 1024 + (size_t)C::PAIRS * 2 * C::SLOT_BYTES + C::HELD_BYTES + (size_t)C::SF_RING * C::SF_BYTES + 512 +
+         4 * (size_t)C::TABLES * (E + 1);
 }
 
 // Clusters of PAIR CTAs that can be resident at once (one CTA per SM), asked
 // once per device.
-template <typename T, int PAIR, int BN>
+template <typename T, int PAIR, int BN, bool HELD>
 cudaError_t resident_clusters(int num_sms, int* out) {
   static std::mutex lock;
   static int clusters[64] = {};
@@ -687,8 +741,8 @@ cudaError_t resident_clusters(int num_sms, int* out) {
   std::lock_guard<std::mutex> g(lock);
   int n = clusters[dev & 63];
   if (n == 0) {
-    const size_t smem = smem_bytes<PAIR, BN>(MAX_E);
-    err = cudaFuncSetAttribute(gemm_mx4_kernel<T, PAIR, BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const size_t smem = smem_bytes<PAIR, BN, HELD>(MAX_E);
+    err = cudaFuncSetAttribute(gemm_mx4_kernel<T, PAIR, BN, HELD>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (err != cudaSuccess) return err;
     n = num_sms;
     if (PAIR == 2) {
@@ -703,7 +757,7 @@ cudaError_t resident_clusters(int num_sms, int* out) {
       cfg.dynamicSmemBytes = smem;
       cfg.attrs = attr;
       cfg.numAttrs = 1;
-      err = cudaOccupancyMaxActiveClusters(&n, gemm_mx4_kernel<T, PAIR, BN>, &cfg);
+      err = cudaOccupancyMaxActiveClusters(&n, gemm_mx4_kernel<T, PAIR, BN, HELD>, &cfg);
       if (err != cudaSuccess) return err;
     }
     clusters[dev & 63] = n;
@@ -712,9 +766,9 @@ cudaError_t resident_clusters(int num_sms, int* out) {
   return cudaSuccess;
 }
 
-template <typename T, int PAIR, int BN>
-cudaError_t launch_t(const Mx4Args& a, const Mx4Weights* w, int num_sms, cudaStream_t s) {
-  using C = Cfg<PAIR, BN>;
+template <typename T, int PAIR, int BN, bool HELD = false>
+cudaError_t launch_t(const Mx4Args& a, const Mx4Weights* w, int num_sms, cudaStream_t s, int chunk = 1) {
+  using C = Cfg<PAIR, BN, HELD>;
   const int64_t K = a.gate_up ? a.H : a.I;
   CUtensorMap mA, mA64, mA32;
   if (!encode_rows(&mA, a.a, a.N, K / 2, BM)) return cudaErrorInvalidValue;
@@ -741,9 +795,10 @@ cudaError_t launch_t(const Mx4Args& a, const Mx4Weights* w, int num_sms, cudaStr
   p.weights = a.weights;
   p.wdt = (int)a.wdt;
   p.thin_a = PAIR == 1;
+  p.chunk = chunk;
   p.status = a.status;
   int clusters = 0;
-  cudaError_t err = resident_clusters<T, PAIR, BN>(num_sms, &clusters);
+  cudaError_t err = resident_clusters<T, PAIR, BN, HELD>(num_sms, &clusters);
   if (err != cudaSuccess) return err;
   if (clusters < 1) return cudaErrorLaunchOutOfResources;
   constexpr int TM = C::TILE_M;
@@ -764,11 +819,26 @@ cudaError_t launch_t(const Mx4Args& a, const Mx4Weights* w, int num_sms, cudaStr
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.gridDim = dim3(nclu * PAIR);
   cfg.blockDim = dim3(THREADS);
-  cfg.dynamicSmemBytes = smem_bytes<PAIR, BN>(a.E);
+  cfg.dynamicSmemBytes = smem_bytes<PAIR, BN, HELD>(a.E);
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, gemm_mx4_kernel<T, PAIR, BN>, mA, mA64, mA32, b0, b1, p);
+  return cudaLaunchKernelEx(&cfg, gemm_mx4_kernel<T, PAIR, BN, HELD>, mA, mA64, mA32, b0, b1, p);
+}
+
+// m-tiles that share a B held in shared memory, or 1: B is loaded for each.  Held,
+// an SM takes in 44 instead of 62 KiB a span, but by larger pieces of work: six
+// chunks a CTA pair at least.  2048 x 1408, us of both products and the rows,
+// loaded and held: 98304 rows over 64 experts 483 and 446, 32768 over eight 172
+// and 157, 8192 over eight 61 and 66 (here not held).  Rows of one or two spans
+// lose (65536 of 1024 x 512 over 32 experts: 123 and 129), longer ones than four
+// have no room.
+int held_chunk(const Mx4Args& a, int num_sms) {
+  const int64_t K = a.gate_up ? a.H : a.I, cols = a.gate_up ? 2 * a.I : a.H;
+  if (mx::spans(K) < HELD_MIN || mx::spans(K) > HELD_SPANS) return 1;
+  const int64_t tiles = (a.N + 255) / 256 * ((cols + 191) / 192) / std::max(1, num_sms / 2);
+  const int64_t mean = (a.N + 256 * (int64_t)a.E - 1) / (256 * (int64_t)a.E);  // m-tiles of an expert
+  return (int)std::max<int64_t>(1, std::min<int64_t>({tiles / 6, mean, 4}));
 }
 
 }  // namespace mx4
@@ -812,6 +882,10 @@ void mx4_weights_destroy(Mx4Weights* w) { delete w; }
 cudaError_t launch_gemm_mx4(const Mx4Args& a, const Mx4Weights* w, int num_sms, cudaStream_t s) {
   // CTA pairs where experts hold at least a full 128-row tile on average
   const bool pair = a.N >= (int64_t)128 * a.E;
+  const int chunk = pair ? mx4::held_chunk(a, num_sms) : 1;
+  if (chunk > 1)
+    return a.dt == MOE_BF16 ? mx4::launch_t<__nv_bfloat16, 2, 192, true>(a, w, num_sms, s, chunk)
+                            : mx4::launch_t<__half, 2, 192, true>(a, w, num_sms, s, chunk);
   if (a.dt == MOE_BF16)
     return pair ? mx4::launch_t<__nv_bfloat16, 2, 192>(a, w, num_sms, s)
                 : mx4::launch_t<__nv_bfloat16, 1, 128>(a, w, num_sms, s);
