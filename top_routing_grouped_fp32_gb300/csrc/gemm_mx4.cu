@@ -45,10 +45,13 @@
 //     rows), so that a lane holds both values of a feature.
 // Where rows are 1025 to 2048 values long (HELD), an n-tile's B stays in shared
 // memory for up to four m-tiles, and the ring carries A alone.
-// What bounds it: on CTA pairs the depth that shared memory leaves the ring, three
-// spans: a span takes 1066 to 1120 cycles at prompt batches, 800 of them MMAs; the
-// MMA warp waits for copies, and these for free slots.  And power: these kernels
-// run below the top clock.  N = 256 would move a tenth less, for TMEM see above.
+// What bounds it: on CTA pairs power (200 us of the headline's gate/up are 1.7 GHz
+// of 2.07) and the depth that shared memory leaves the ring, three spans.  A span
+// takes 1070 to 1100 cycles at prompt batches, 800 of them MMAs; the MMA warp waits
+// 500 for copies, and these for free slots, or with HELD 260 for copies and 180 for
+// the epilogue (all eight warps on each tile, half its columns each, end that wait,
+// but not the time: 441 and 440 us).  N = 256 would move a tenth less, for TMEM see
+// above.
 // Single CTAs serve batches that hold few rows an expert: they are bound by
 // reading weights (32 tokens over 256 experts of 7168 x 2048, top-8: 580 us,
 // 6.6 TB/s), and many small tiles spread over the SMs.
