@@ -662,9 +662,12 @@ moe_status moe_mx4_forward_sigmoid_grouped(moe_mx4_experts_t experts, const void
  * [E,I,H], ddown [E,H,I]; experts without rows get zeros).  da and all sums
  * are FP32; dg, du and a are rounded once to the dtype as operands of the
  * products, x^ too (its four significant bits fit; a value past the dtype's
- * range is infinite).  N = T*top_k.  The gradients overlap neither dout nor
- * each other (MOE_ERR_INVALID_ARG).  g and u are not recomputed: six of the
+ * range is infinite).  N = T*top_k.  g and u are not recomputed: six of the
  * eight products of moe_experts_backward are left.
+ *
+ * g, u and their scales overlap neither x_disp, expert_out, offsets nor each
+ * other, the gradients neither dout, x, perm, offsets, the checkpoint nor each
+ * other (MOE_ERR_INVALID_ARG).
  * ---------------------------------------------------------------------- */
 moe_status moe_experts_forward_checkpoint(moe_experts_t experts, const void* x_disp, int64_t N,
                                           const uint32_t* offsets, void* expert_out,

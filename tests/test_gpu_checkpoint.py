@@ -307,3 +307,38 @@ def test_refusals(cuda_lib):
         with pytest.raises(moe.MoeError) as e:
             call()
         assert e.value.status == status, e.value
+
+
+def test_what_overlaps_is_refused(cuda_lib):
+    """Gradients over what is still read, and a checkpoint over the forward's rows."""
+    moe = cuda_lib
+    s = Step(moe, 64, 2, 2, 64, 64, torch.bfloat16)
+    out, ck = s.forward()
+    grads = s.backward(ck)
+    pool = torch.zeros(1 << 17, dtype=torch.uint8, device="cuda")  # [N, H] and [E, I, H] in 16 bits take 16 KiB each
+
+    def at(i, n, shape, dtype):
+        return pool[i:i + n].view(dtype).view(shape)
+    dinput = at(16384, 16384, (128, 64), torch.bfloat16)
+    x = moe.MxRows(at(16384 + 16368, 4096, (64, 64), torch.uint8), s.x_mx.scales, "mxfp8", 64)
+    x_scales = moe.MxRows(s.x_mx.values, at(16384 - 127, 128, (64, 2), torch.uint8), "mxfp8", 64)
+    perm = at(16384, 512, (128,), torch.int32)
+    offsets = at(16384 + 16380, 12, (3,), torch.int32)
+    gate = moe.MxRows(at(16384 - 8176, 8192, (128, 64), torch.uint8), ck.gate.scales, "mxfp8", 64)
+    up = moe.MxRows(ck.up.values, at(32767, 256, (128, 2), torch.uint8), "mxfp8", 64)
+    args = (s.x_mx, s.d.perm, s.d.offsets, ck, s.dout, 2)
+    for i, v in ((0, x), (0, x_scales), (1, perm), (2, offsets), (3, moe.ExpertCheckpoint(gate, ck.up)),
+                 (3, moe.ExpertCheckpoint(ck.gate, up))):
+        with pytest.raises(moe.MoeError, match="overlap") as e:
+            s.ex.backward_checkpoint(*(v if j == i else a for j, a in enumerate(args)), grads=(dinput, *grads[1:]))
+        assert e.value.status == 1
+    for kept in (moe.ExpertCheckpoint(gate, ck.up), moe.ExpertCheckpoint(ck.gate, up), moe.ExpertCheckpoint(ck.gate, ck.gate)):
+        with pytest.raises(moe.MoeError, match="overlap"):
+            s.ex.forward_checkpoint(s.d.x_disp, s.d.offsets, out=dinput, checkpoint=kept)
+    assert not pool.any()
+    # next to each other is not over each other
+    x.values = at(32768, 4096, (64, 64), torch.uint8)
+    x.values.copy_(s.x_mx.values)
+    got = s.ex.backward_checkpoint(x, *args[1:], grads=(dinput, *(torch.empty_like(g) for g in grads[1:])))
+    assert all(torch.equal(a, b) for a, b in zip(got, grads))
+    assert torch.equal(s.ex.forward_checkpoint(s.d.x_disp, s.d.offsets, out=s.d.x_disp)[0], out)

@@ -385,6 +385,13 @@ moe_status moe_experts_forward_checkpoint(moe_experts_t x, const void* x_disp, i
     return fail(MOE_ERR_INVALID_ARG, "the checkpoint's values and scales must be non-NULL");
   if (!aligned16(gate_values) || !aligned16(up_values))
     return fail(MOE_ERR_INVALID_ARG, "checkpoint values must be 16-byte aligned");
+  if (N > 0 && N <= kMaxRows) {
+    const uint64_t gb = (uint64_t)N * x->I, gsb = (uint64_t)N * ((x->I + 31) / 32), rb = (uint64_t)N * x->H * 2;
+    const Range held[4] = {{gate_values, gb}, {gate_scales, gsb}, {up_values, gb}, {up_scales, gsb}};
+    const Range rest[3] = {{x_disp, rb}, {expert_out, rb}, {offsets, (uint64_t)(x->E + 1) * 4}};
+    if (!apart(held, rest) || !apart(held))
+      return fail(MOE_ERR_INVALID_ARG, "the checkpoint must not overlap x_disp, expert_out, offsets or itself");
+  }
   const Checkpoint ck{gate_values, gate_scales, up_values, up_scales};
   return experts_forward(x, x_disp, N, offsets, expert_out, &ck, ws, ws_bytes, stream);
 }
@@ -810,19 +817,16 @@ moe_status moe_experts_backward_checkpoint(moe_experts_t x, const uint8_t* x_val
   if (!aligned16(x_values) || !aligned16(gate_values) || !aligned16(up_values) || !aligned16(dout) ||
       !aligned16(dinput))
     return fail(MOE_ERR_INVALID_ARG, "x, the checkpoint's values, dout and dinput must be 16-byte aligned");
-  // dout is read until the last product
+  // (dout, x and perm are read after the first gradient is written)
   const uint64_t rb = (uint64_t)N * x->H * 2, wb_ = (uint64_t)x->E * x->I * x->H * 2;
-  const struct {
-    const void* p;
-    uint64_t n;
-  } outs[4] = {{dinput, rb}, {dgate, wb_}, {dup, wb_}, {ddown, wb_}};
-  for (int i = 0; i < 4; ++i) {
-    if (overlap(outs[i].p, outs[i].n, dout, rb))
-      return fail(MOE_ERR_INVALID_ARG, "the gradients must not overlap dout");
-    for (int j = 0; j < i; ++j)
-      if (overlap(outs[i].p, outs[i].n, outs[j].p, outs[j].n))
-        return fail(MOE_ERR_INVALID_ARG, "the gradients must not overlap one another");
-  }
+  const uint64_t gb = (uint64_t)N * x->I, gsb = (uint64_t)N * ((x->I + 31) / 32);
+  const Range outs[4] = {{dinput, rb}, {dgate, wb_}, {dup, wb_}, {ddown, wb_}};
+  const Range ins[9] = {{dout, rb}, {x_values, (uint64_t)T * x->H}, {x_scales, (uint64_t)T * ((x->H + 31) / 32)},
+                        {perm, (uint64_t)N * 4}, {offsets, (uint64_t)(x->E + 1) * 4}, {gate_values, gb},
+                        {gate_scales, gsb}, {up_values, gb}, {up_scales, gsb}};
+  if (!apart(outs, ins))
+    return fail(MOE_ERR_INVALID_ARG, "the gradients must not overlap dout, x, perm, offsets or the checkpoint");
+  if (!apart(outs)) return fail(MOE_ERR_INVALID_ARG, "the gradients must not overlap one another");
   if ((st = check_ws(ws, ws_bytes, moe_experts_backward_checkpoint_workspace_size(x, N))) != MOE_OK) return st;
   if (N == 0) {  // no rows: every weight gradient is zero
     const size_t wb = (size_t)x->E * x->I * x->H * 2;

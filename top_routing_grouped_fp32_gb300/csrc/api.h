@@ -72,6 +72,26 @@ inline bool overlap(const void* a, uint64_t na, const void* b, uint64_t nb) {
   return x < y ? y - x < na : x - y < nb;
 }
 
+struct Range {
+  const void* p;
+  uint64_t n;
+};
+// Whether no range of a shares bytes with one of b, or with another of a.
+template <int NA, int NB>
+bool apart(const Range (&a)[NA], const Range (&b)[NB]) {
+  for (const Range& x : a)
+    for (const Range& y : b)
+      if (overlap(x.p, x.n, y.p, y.n)) return false;
+  return true;
+}
+template <int N>
+bool apart(const Range (&a)[N]) {
+  for (int i = 0; i < N; ++i)
+    for (int j = 0; j < i; ++j)
+      if (overlap(a[i].p, a[i].n, a[j].p, a[j].n)) return false;
+  return true;
+}
+
 // Checks shared by the calls that take (T, E, top_k).
 inline moe_status check_tek(int64_t T, int64_t E, int32_t k) {
   if (T < 0) return fail(MOE_ERR_SHAPE, "T must be >= 0 (got %lld)", (long long)T);

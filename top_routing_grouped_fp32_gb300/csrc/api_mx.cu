@@ -3,7 +3,6 @@
 // activations in 8 bits.  Checks, workspaces and the order of the launches.
 #include <algorithm>
 #include <climits>
-#include <functional>
 #include <new>
 
 #include "api.h"
@@ -108,10 +107,10 @@ moe_status run_mx4(const moe_mx4_experts* x, int64_t N, const uint32_t* offsets,
   return MOE_OK;
 }
 
-using RouteFn = std::function<cudaError_t(uint32_t* idx, void* w, cudaStream_t s)>;
-
+// Route: cudaError_t(uint32_t* idx, void* weights, cudaStream_t)
+template <typename Route>
 moe_status mx4_forward(moe_mx4_experts_t x, const void* xin, const void* logits, moe_dtype ldt, int64_t T, int32_t k,
-                       const RouteFn& route, void* y, void* ws, size_t ws_bytes, cudaStream_t s) {
+                       const Route& route, void* y, void* ws, size_t ws_bytes, cudaStream_t s) {
   if (T == 0) return ok();
   if (!xin || !logits || !y) return fail(MOE_ERR_INVALID_ARG, "x, logits and y must be non-NULL");
   if (!aligned16(xin) || !aligned16(y)) return fail(MOE_ERR_INVALID_ARG, "x and y must be 16-byte aligned");
@@ -282,7 +281,7 @@ moe_status moe_mx4_experts_forward(moe_mx4_experts_t x, const void* x_disp, int6
 }
 
 size_t moe_mx4_forward_workspace_size(moe_mx4_experts_t x, int64_t T, int32_t top_k, moe_dtype ldt) {
-  if (!x || T < 0 || top_k < 1 || !valid_dtype(ldt)) return 0;
+  if (!x || T < 0 || top_k < 1 || T > kMaxRows / top_k || !valid_dtype(ldt)) return 0;
   return fused_layout(x, T, top_k, ldt).total;
 }
 
@@ -293,7 +292,7 @@ moe_status moe_mx4_forward(moe_mx4_experts_t x, const void* xin, const void* log
   if (!valid_dtype(ldt)) return fail(MOE_ERR_DTYPE, "logits dtype %d is not F32/F16/BF16", (int)ldt);
   if ((st = check_tek(T, x->E, top_k)) != MOE_OK) return st;
   const int E = (int)x->E;
-  RouteFn route = [=](uint32_t* idx, void* w, cudaStream_t s) {
+  auto route = [=](uint32_t* idx, void* w, cudaStream_t s) {
     return moe::launch_route(logits, ldt, T, E, top_k, renormalize, idx, w, nullptr, nullptr, s);
   };
   return mx4_forward(x, xin, logits, ldt, T, top_k, route, y, ws, ws_bytes, stream);
@@ -308,7 +307,7 @@ moe_status moe_mx4_forward_sigmoid_grouped(moe_mx4_experts_t x, const void* xin,
   if ((st = check_group_options(T, x->E, opt)) != MOE_OK) return st;
   const int E = (int)x->E;
   const moe_group_routing_options o = *opt;
-  RouteFn route = [=](uint32_t* idx, void* w, cudaStream_t s) {
+  auto route = [=](uint32_t* idx, void* w, cudaStream_t s) {
     return moe::launch_route_sigmoid_grouped(logits, ldt, T, E, bias, o.top_k, o.groups, o.selected_groups,
                                              o.group_top_two, o.renormalize, o.scale, idx, w, nullptr, s);
   };
