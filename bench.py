@@ -58,10 +58,10 @@ FALLBACK_PEAKS = {"hbm_gbs": 6800.0, "bf16_tflops": 1900.0, "bf16_tflops_sustain
 # white space left out) it was taken on; it is reported as null once that
 # code changes.
 GEMM_TRAFFIC = {
-    # one launch each on the headline workload: gate/up reads 1.144826368 GB and
-    # writes 265.207296 MB, down reads 0.647081728 GB and writes 370.187520 MB
-    "finegrained_bf16": {"bytes_per_launch": (1144826368 + 265207296 + 647081728 + 370187520) / 2,
-                         "code_sha256": "110465fc4e51af2e717df1817e7f34f4248e467603e1a8138916212ba5606719"},
+    # one launch each on the headline workload: gate/up reads 1.143486720 GB and
+    # writes 264.835840 MB, down reads 0.646882816 GB and writes 370.289664 MB
+    "finegrained_bf16": {"bytes_per_launch": (1143486720 + 264835840 + 646882816 + 370289664) / 2,
+                         "code_sha256": "bb2a2ffc8dbff5fb998026b1949b32779a9b80c749382357c433be0cfe673fcd"},
 }
 
 
