@@ -160,6 +160,11 @@ def test_the_fused_forward_is_the_stages_together(cuda_lib, T, E, k, H, I, ldt):
     assert torch.equal(y, ex.forward(x, logits, k, True))
 
 
+def test_the_fused_forward_of_many_rows(cuda_lib):
+    """Both products keep weights' tiles for several of the rows', the second into weighted slots."""
+    test_the_fused_forward_is_the_stages_together(cuda_lib, 12288, 4, 2, 2048, 1056, "bf16")
+
+
 def test_sigmoid_routing(cuda_lib):
     moe = cuda_lib
     T, E, k = 65, 32, 4
