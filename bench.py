@@ -58,10 +58,10 @@ FALLBACK_PEAKS = {"hbm_gbs": 6800.0, "bf16_tflops": 1900.0, "bf16_tflops_sustain
 # white space left out) it was taken on; it is reported as null once that
 # code changes.
 GEMM_TRAFFIC = {
-    # one launch each on the headline workload: gate/up reads 1.143486720 GB and
-    # writes 264.835840 MB, down reads 0.646882816 GB and writes 370.289664 MB
-    "finegrained_bf16": {"bytes_per_launch": (1143486720 + 264835840 + 646882816 + 370289664) / 2,
-                         "code_sha256": "bb2a2ffc8dbff5fb998026b1949b32779a9b80c749382357c433be0cfe673fcd"},
+    # one launch each on the headline workload: gate/up reads 1.156529152 GB and
+    # writes 265.518080 MB, down reads 0.646879488 GB and writes 369.922816 MB
+    "finegrained_bf16": {"bytes_per_launch": (1156529152 + 265518080 + 646879488 + 369922816) / 2,
+                         "code_sha256": "6292576f371b7f6cf9f41b5d1f0a6c720859c6b4996ed15e8a31119c48382654"},
 }
 
 

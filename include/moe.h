@@ -663,7 +663,9 @@ moe_status moe_mx4_forward_sigmoid_grouped(moe_mx4_experts_t experts, const void
  * are FP32; dg, du and a are rounded once to the dtype as operands of the
  * products, x^ too (its four significant bits fit; a value past the dtype's
  * range is infinite).  N = T*top_k.  g and u are not recomputed: six of the
- * eight products of moe_experts_backward are left.
+ * eight products of moe_experts_backward are left.  workspace:
+ * moe_experts_backward_checkpoint_workspace_size(experts, N) bytes, which also
+ * serve every smaller batch.
  *
  * g, u and their scales overlap neither x_disp, expert_out, offsets nor each
  * other, the gradients neither dout, x, perm, offsets, the checkpoint nor each

@@ -359,6 +359,7 @@ class SwiGluExperts:
         return out, checkpoint
 
     def backward_checkpoint_workspace(self, N: int) -> torch.Tensor:
+        """A workspace for backward_checkpoint of up to N rows."""
         return _workspace(self._lib.moe_experts_backward_checkpoint_workspace_size(self.handle, N),
                           self.gate.device)
 

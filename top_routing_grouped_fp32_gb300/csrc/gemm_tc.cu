@@ -61,6 +61,7 @@
 #include "common.cuh"
 #include "internal.h"
 #include "mx.cuh"
+#include "parts.h"
 #include "tcgen05.cuh"
 
 namespace moe {
@@ -80,6 +81,7 @@ namespace tc {
 constexpr int BM = 128;        // rows per CTA
 constexpr int BN = 256;        // FP32 accumulator columns per tile
 constexpr int BK = 64;         // 64 16-bit elements = one 128-byte swizzle row
+static_assert(BM == parts::kRows && BN == parts::kCols && BK == parts::kDepth, "what parts.h counts in");
 constexpr int UMMA_K = 16;
 constexpr uint32_t A_BYTES = BM * BK * 2;        // 16 KiB
 constexpr uint32_t B_HALF_BYTES = 128 * BK * 2;  // 16 KiB
@@ -1396,29 +1398,6 @@ struct CkLayout {
   size_t pad, dgduP, actP, xP, tails, parts, total;
 };
 
-// Parts that each expert's rows are cut into for a weight gradient of m x n:
-// one, or as many as fill the CTA pairs where the tiles of all experts are
-// fewer, with four k-blocks a part at least on average (below that the parts'
-// FP32 outputs cost more than they save).  Two experts of 664 x 112 with 10280
-// rows each: 185 us with one part.
-int wgrad_parts(int64_t N, int E, int64_t m, int64_t n) {
-  constexpr int64_t kPairs = 76;
-  const int64_t tiles = E * ((m + 255) / 256) * ((n + 255) / 256);
-  return (int)std::max<int64_t>(1, std::min(kPairs / tiles, N / ((int64_t)E * 4 * BK)));
-}
-
-// Parts that dinput's K = 2 I is cut into where its tiles are fewer than the SMs
-// (few rows, H short): as many as fill them, of eight k-blocks at least.  A
-// captured backward of 30 rows over five experts of 696 x 3688 takes 86 us,
-// 135 with one part; of 1 row of 64 x 512, the smallest that is cut, 41 and 46.
-int dinput_parts(int64_t N, int E, int64_t H, int64_t I) {
-  constexpr int64_t kSms = 152;
-  const bool pair = N >= (int64_t)BM * E;
-  const int64_t mt = N / (pair ? 2 * BM : BM) + std::min<int64_t>(E, N);
-  const int64_t tiles = std::max<int64_t>(1, mt * ((H + 255) / 256));
-  return (int)std::max<int64_t>(1, std::min((pair ? kSms / 2 : kSms) / tiles, 2 * ((I + BK - 1) / BK) / 8));
-}
-
 CkLayout ck_layout(int64_t N, int E, int64_t H, int64_t I) {
   CkLayout L{};
   L.npad = N + 63 * (int64_t)E;
@@ -1433,10 +1412,7 @@ CkLayout ck_layout(int64_t N, int E, int64_t H, int64_t I) {
   L.actP = take((size_t)L.npad * I * 2);
   L.xP = take((size_t)L.npad * H * 2);
   L.tails = take((size_t)E * BK * H * 2);
-  const int pgu = wgrad_parts(N, E, 2 * I, H), pd = wgrad_parts(N, E, H, I);
-  const int px = dinput_parts(N, E, H, I);
-  L.parts = take(std::max((size_t)std::max(pgu > 1 ? 2 * pgu : 0, pd > 1 ? pd : 0) * E * I * H * 4,
-                          px > 1 ? (size_t)px * N * H * 4 : 0));
+  L.parts = take((size_t)parts::room(N, E, H, I) * 4);
   L.total = off;
   return L;
 }
@@ -1499,15 +1475,15 @@ cudaError_t backward_ck_t(const ExpertsCkBwdArgs& a, char* ws, int num_sms, cuda
   p.nb = (int)((H + 255) / 256);
   p.out = a.dinput;
   p.v8_out = H % 16 == 0 && reinterpret_cast<uintptr_t>(a.dinput) % 32 == 0;
-  float* parts = reinterpret_cast<float*>(ws + L.parts);
-  const int px = dinput_parts(N, E, H, I);
+  float* sums = reinterpret_cast<float*>(ws + L.parts);
+  const int px = parts::dinput(N, E, H, I);
   if (px > 1) {
     p.mode = kPartial;
     p.k_parts = px;
     p.m_total = N;
-    p.out = parts;
+    p.out = sums;
     MOE_TC_TRY((launch_any<T, kUse>(pair, N, E, mDgduP, mWgMN, mWuMN, p, num_sms, s, &mDgduP64)));
-    MOE_TC_TRY(launch_join_rows(parts, px, N, H, a.offsets, E, a.dinput, dt, s));
+    MOE_TC_TRY(launch_join_rows(sums, px, N, H, a.offsets, E, a.dinput, dt, s));
   } else {
     MOE_TC_TRY(launch_any<T>(pair, N, E, mDgduP, mWgMN, mWuMN, p, num_sms, s, &mDgduP64));
   }
@@ -1527,16 +1503,16 @@ cudaError_t backward_ck_t(const ExpertsCkBwdArgs& a, char* ws, int num_sms, cuda
   auto gradient = [&](const CUtensorMap& mA, const CUtensorMap& mB, const CUtensorMap* mTail, void* o1, void* o2) {
     p.mb = (int)((p.m_total + TM - 1) / TM);
     p.nb = (int)((p.n_out + 255) / 256);
-    p.k_parts = wgrad_parts(N, E, p.m_total, p.n_out);
+    p.k_parts = parts::weight_gradient(N, E, p.m_total, p.n_out);
     p.out = o1;
     p.out2 = o2;
     if (p.k_parts == 1) return launch_t<T, 2, 1, kUse>(N, E, mA, mB, mB, p, num_sms, s, mTail);
     const int64_t n1 = p.split * p.n_out, n2 = (p.m_total - p.split) * p.n_out;
-    float* f2 = parts + (int64_t)p.k_parts * E * n1;
-    p.out = parts;
+    float* f2 = sums + (int64_t)p.k_parts * E * n1;
+    p.out = sums;
     p.out2 = f2;
     cudaError_t e = launch_t<T, 2>(N, E, mA, mB, mB, p, num_sms, s, mTail);
-    if (e == cudaSuccess) e = launch_join_parts(parts, E, p.k_parts, n1, o1, dt, s);
+    if (e == cudaSuccess) e = launch_join_parts(sums, E, p.k_parts, n1, o1, dt, s);
     if (e == cudaSuccess && n2 > 0) e = launch_join_parts(f2, E, p.k_parts, n2, o2, dt, s);
     return e;
   };
