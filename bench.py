@@ -58,10 +58,10 @@ FALLBACK_PEAKS = {"hbm_gbs": 6800.0, "bf16_tflops": 1900.0, "bf16_tflops_sustain
 # white space left out) it was taken on; it is reported as null once that
 # code changes.
 GEMM_TRAFFIC = {
-    # one launch each on the headline workload: gate/up reads 1.156529152 GB and
-    # writes 265.518080 MB, down reads 0.646879488 GB and writes 369.922816 MB
-    "finegrained_bf16": {"bytes_per_launch": (1156529152 + 265518080 + 646879488 + 369922816) / 2,
-                         "code_sha256": "6292576f371b7f6cf9f41b5d1f0a6c720859c6b4996ed15e8a31119c48382654"},
+    # one launch each on the headline workload: gate/up reads 1.246657024 GB and
+    # writes 267.535360 MB, down reads 0.646885120 GB and writes 370.009600 MB
+    "finegrained_bf16": {"bytes_per_launch": (1246657024 + 267535360 + 646885120 + 370009600) / 2,
+                         "code_sha256": "162fbb165d910440397fdac75f1799753adf19db823920a8e01866ceac3df018"},
 }
 
 

@@ -789,7 +789,7 @@ moe_status moe_experts_backward_with_strategy(moe_experts_t x, const void* x_dis
 
 size_t moe_experts_backward_checkpoint_workspace_size(moe_experts_t x, int64_t N) {
   if (!x || N < 0 || !bwd_tc_ok(x, N)) return 0;
-  return kWsHeader + align_up(moe::experts_backward_ck_workspace(N, (int)x->E, x->H, x->I), 1024) +
+  return kWsHeader + align_up(moe::experts_backward_ck_workspace(N, (int)x->E, x->H, x->I, x->num_sms), 1024) +
          offsets_copy_bytes(x) + 1024;
 }
 

@@ -1398,7 +1398,7 @@ struct CkLayout {
   size_t pad, dgduP, actP, xP, tails, parts, total;
 };
 
-CkLayout ck_layout(int64_t N, int E, int64_t H, int64_t I) {
+CkLayout ck_layout(int64_t N, int E, int64_t H, int64_t I, int num_sms) {
   CkLayout L{};
   L.npad = N + 63 * (int64_t)E;
   size_t off = 0;
@@ -1412,7 +1412,7 @@ CkLayout ck_layout(int64_t N, int E, int64_t H, int64_t I) {
   L.actP = take((size_t)L.npad * I * 2);
   L.xP = take((size_t)L.npad * H * 2);
   L.tails = take((size_t)E * BK * H * 2);
-  L.parts = take((size_t)parts::room(N, E, H, I) * 4);
+  L.parts = take((size_t)parts::room(N, E, H, I, num_sms) * 4);
   L.total = off;
   return L;
 }
@@ -1422,7 +1422,7 @@ cudaError_t backward_ck_t(const ExpertsCkBwdArgs& a, char* ws, int num_sms, cuda
   const int64_t N = a.N, H = a.H, I = a.I;
   const int E = a.E;
   const moe_dtype dt = a.dt;
-  const CkLayout L = ck_layout(N, E, H, I);
+  const CkLayout L = ck_layout(N, E, H, I, num_sms);
   uint32_t* pad = reinterpret_cast<uint32_t*>(ws + L.pad);
   void* dgduP = ws + L.dgduP;
   void* actP = ws + L.actP;
@@ -1476,7 +1476,7 @@ cudaError_t backward_ck_t(const ExpertsCkBwdArgs& a, char* ws, int num_sms, cuda
   p.out = a.dinput;
   p.v8_out = H % 16 == 0 && reinterpret_cast<uintptr_t>(a.dinput) % 32 == 0;
   float* sums = reinterpret_cast<float*>(ws + L.parts);
-  const int px = parts::dinput(N, E, H, I);
+  const int px = parts::dinput(N, E, H, I, num_sms);
   if (px > 1) {
     p.mode = kPartial;
     p.k_parts = px;
@@ -1503,7 +1503,7 @@ cudaError_t backward_ck_t(const ExpertsCkBwdArgs& a, char* ws, int num_sms, cuda
   auto gradient = [&](const CUtensorMap& mA, const CUtensorMap& mB, const CUtensorMap* mTail, void* o1, void* o2) {
     p.mb = (int)((p.m_total + TM - 1) / TM);
     p.nb = (int)((p.n_out + 255) / 256);
-    p.k_parts = parts::weight_gradient(N, E, p.m_total, p.n_out);
+    p.k_parts = parts::weight_gradient(N, E, p.m_total, p.n_out, num_sms);
     p.out = o1;
     p.out2 = o2;
     if (p.k_parts == 1) return launch_t<T, 2, 1, kUse>(N, E, mA, mB, mB, p, num_sms, s, mTail);
@@ -1644,8 +1644,8 @@ cudaError_t launch_experts_backward_tc(const ExpertsBwdArgs& a, const TcWeights*
   return tc::backward_t<__half>(a, w, base, num_sms, s);
 }
 
-size_t experts_backward_ck_workspace(int64_t N, int E, int64_t H, int64_t I) {
-  return tc::ck_layout(N, E, H, I).total;
+size_t experts_backward_ck_workspace(int64_t N, int E, int64_t H, int64_t I, int num_sms) {
+  return tc::ck_layout(N, E, H, I, num_sms).total;
 }
 
 cudaError_t launch_experts_backward_ck(const ExpertsCkBwdArgs& a, void* ws, int num_sms, cudaStream_t s) {

@@ -314,7 +314,7 @@ struct ExpertsCkBwdArgs {
   void* ddown;
   uint32_t* status;
 };
-size_t experts_backward_ck_workspace(int64_t N, int E, int64_t H, int64_t I);
+size_t experts_backward_ck_workspace(int64_t N, int E, int64_t H, int64_t I, int num_sms);
 cudaError_t launch_experts_backward_ck(const ExpertsCkBwdArgs& a, void* ws, int num_sms, cudaStream_t s);
 // a kernel whose bounded wait is made to expire (failure-path self-test)
 cudaError_t launch_bounded_wait_selftest(uint32_t* status, uint64_t limit_ns, cudaStream_t s);
