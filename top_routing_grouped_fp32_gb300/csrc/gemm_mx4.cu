@@ -56,7 +56,6 @@
 // reading weights (32 tokens over 256 experts of 7168 x 2048, top-8: 580 us,
 // 6.6 TB/s), and many small tiles spread over the SMs.
 #include <algorithm>
-#include <mutex>
 #include <new>
 #include <type_traits>
 
@@ -732,43 +731,6 @@ size_t smem_bytes(int E) {
          4 * (size_t)C::TABLES * (E + 1);
 }
 
-// Clusters of PAIR CTAs that can be resident at once (one CTA per SM), asked
-// once per device.
-template <typename T, int PAIR, int BN, bool HELD>
-cudaError_t resident_clusters(int num_sms, int* out) {
-  static std::mutex lock;
-  static int clusters[64] = {};
-  int dev = 0;
-  cudaError_t err = cudaGetDevice(&dev);
-  if (err != cudaSuccess) return err;
-  std::lock_guard<std::mutex> g(lock);
-  int n = clusters[dev & 63];
-  if (n == 0) {
-    const size_t smem = smem_bytes<PAIR, BN, HELD>(MAX_E);
-    err = cudaFuncSetAttribute(gemm_mx4_kernel<T, PAIR, BN, HELD>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (err != cudaSuccess) return err;
-    n = num_sms;
-    if (PAIR == 2) {
-      cudaLaunchConfig_t cfg = {};
-      cudaLaunchAttribute attr[1];
-      attr[0].id = cudaLaunchAttributeClusterDimension;
-      attr[0].val.clusterDim.x = PAIR;
-      attr[0].val.clusterDim.y = 1;
-      attr[0].val.clusterDim.z = 1;
-      cfg.gridDim = dim3(PAIR * (num_sms / PAIR));
-      cfg.blockDim = dim3(THREADS);
-      cfg.dynamicSmemBytes = smem;
-      cfg.attrs = attr;
-      cfg.numAttrs = 1;
-      err = cudaOccupancyMaxActiveClusters(&n, gemm_mx4_kernel<T, PAIR, BN, HELD>, &cfg);
-      if (err != cudaSuccess) return err;
-    }
-    clusters[dev & 63] = n;
-  }
-  *out = n;
-  return cudaSuccess;
-}
-
 template <typename T, int PAIR, int BN, bool HELD = false>
 cudaError_t launch_t(const Mx4Args& a, const Mx4Weights* w, int num_sms, cudaStream_t s, int chunk = 1) {
   using C = Cfg<PAIR, BN, HELD>;
@@ -800,8 +762,10 @@ cudaError_t launch_t(const Mx4Args& a, const Mx4Weights* w, int num_sms, cudaStr
   p.thin_a = PAIR == 1;
   p.chunk = chunk;
   p.status = a.status;
+  static PerDevice known;
   int clusters = 0;
-  cudaError_t err = resident_clusters<T, PAIR, BN, HELD>(num_sms, &clusters);
+  cudaError_t err = resident_clusters<PAIR>(gemm_mx4_kernel<T, PAIR, BN, HELD>, THREADS, smem_bytes<PAIR, BN, HELD>(MAX_E),
+                                            num_sms, known, &clusters);
   if (err != cudaSuccess) return err;
   if (clusters < 1) return cudaErrorLaunchOutOfResources;
   constexpr int TM = C::TILE_M;

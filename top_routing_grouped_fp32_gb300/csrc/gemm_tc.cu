@@ -1110,37 +1110,6 @@ size_t smem_bytes(int E) {
          8 * (size_t)(E + 1);
 }
 
-// Clusters of PAIR CTAs that can be resident at once (one CTA per SM).
-template <typename T, int PAIR, int KS = 1, int CK = kNone>
-cudaError_t resident_clusters(int num_sms, int* out) {
-  static std::once_flag once;
-  static cudaError_t err = cudaSuccess;
-  static int clusters = 0;
-  std::call_once(once, [num_sms] {
-    err = cudaFuncSetAttribute(grouped_gemm_tc<T, PAIR, KS, CK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               (int)smem_bytes<PAIR, KS, CK>(MAX_E));
-    if (err != cudaSuccess) return;
-    if (PAIR == 1) {
-      clusters = num_sms;
-      return;
-    }
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = PAIR;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.gridDim = dim3(PAIR * (num_sms / PAIR));
-    cfg.blockDim = dim3(kThreads<CK>);
-    cfg.dynamicSmemBytes = smem_bytes<PAIR, KS, CK>(MAX_E);
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    err = cudaOccupancyMaxActiveClusters(&clusters, grouped_gemm_tc<T, PAIR, KS, CK>, &cfg);
-  });
-  *out = clusters;
-  return err;
-}
-
 // mA64: A with 64-row boxes, for the half tiles of p.half_tails (else unused)
 template <typename T, int PAIR, int KS = 1, int CK = kNone>
 cudaError_t launch_t(int64_t N, int E, const CUtensorMap& mA, const CUtensorMap& mB0,
@@ -1148,8 +1117,10 @@ cudaError_t launch_t(int64_t N, int E, const CUtensorMap& mA, const CUtensorMap&
                      const CUtensorMap* mA64 = nullptr) {
   if (!mA64 || PAIR != 2) p.half_tails = 0;
   if (!mA64 || PAIR != 1) p.thin_a = 0;
+  static PerDevice known;
   int clusters = 0;
-  cudaError_t err = resident_clusters<T, PAIR, KS, CK>(num_sms, &clusters);
+  cudaError_t err = resident_clusters<PAIR>(grouped_gemm_tc<T, PAIR, KS, CK>, kThreads<CK>, smem_bytes<PAIR, KS, CK>(MAX_E),
+                                            num_sms, known, &clusters);
   if (err != cudaSuccess) return err;
   if (clusters < 1) return cudaErrorLaunchOutOfResources;
   constexpr int TM = Cfg<PAIR>::TILE_M;

@@ -6,6 +6,7 @@
 #include <cudaTypedefs.h>
 
 #include "common.cuh"
+#include "per_device.h"
 
 namespace moe {
 namespace tc {
@@ -295,6 +296,35 @@ __device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr) {
          | ((uint64_t)(1024 >> 4) << 32)           // stride offset between 8-row groups
          | ((uint64_t)1 << 46)                     // descriptor version
          | ((uint64_t)2 << 61);                    // 128-byte swizzle
+}
+
+// Clusters of PAIR CTAs that the current device holds at once of a kernel that
+// takes an SM's shared memory.  That it may is asked for here, and is the
+// device's, too.
+template <int PAIR, typename... KArgs>
+cudaError_t resident_clusters(void (*kernel)(KArgs...), int threads, size_t smem, int num_sms, PerDevice& known,
+                              int* out) {
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
+  return known.get(dev, out, [&](int* n) -> cudaError_t {
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    *n = num_sms;
+    if (PAIR == 1) return e;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = PAIR;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3(PAIR * (num_sms / PAIR));
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaOccupancyMaxActiveClusters(n, kernel, &cfg);
+  });
 }
 
 }  // namespace tc
