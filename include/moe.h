@@ -596,8 +596,10 @@ moe_status moe_mx_dequantize(const uint8_t* values, const uint8_t* scales, moe_m
  *   hq = Q4(silu(g) * u), out = hq . W_down[e]^T (FP32, rounded once to dtype).
  * dtype (F16 or BF16, else MOE_ERR_DTYPE) is that of x and the outputs.  H and
  * I are multiples of 32 (else MOE_ERR_UNSUPPORTED); other limits as for
- * moe_experts_create.  Row NaN or infinity makes that row NaN; a weight block
- * with scale byte 255 makes its output column (gate, up: the rows) NaN.
+ * moe_experts_create.  Row NaN or infinity makes that row NaN, and so does a g,
+ * u or h that FP32 cannot hold (silu(g) of a g far below 0 is 0, whatever u is);
+ * a weight block with scale byte 255 makes its output column (gate, up: the
+ * rows) NaN.
  *
  * The handle does not own the weights: gate, up and down values (16-byte
  * aligned) must stay alive and unchanged while it is used.  Their scales are

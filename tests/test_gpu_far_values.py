@@ -1,0 +1,46 @@
+"""SwiGLU and its gradient where a product of finite values leaves FP32's range
+on the way to a value that does not: silu(g) of a negative g is small or 0,
+whatever u is.  All values are powers of two, so that sums are exact and what is
+expected is the formula's value with the roundings that it goes through."""
+import pytest
+import torch
+
+import mx_reference as ref
+
+pytestmark = pytest.mark.gpu
+BF16, F64 = torch.bfloat16, torch.float64
+H, I = 32, 64
+
+
+def weights(gate, up, down):
+    """Experts of one kind of feature each for even and odd features (gate, up [2]); x = 1."""
+    w = [torch.empty((1, I, H), device="cuda") for _ in range(2)] + [torch.full((1, H, I), down, device="cuda")]
+    for t, pair in zip(w, (gate, up)):
+        t[:, 0::2], t[:, 1::2] = pair[0], pair[1]
+    return w
+
+
+def h_of(g, u):
+    g, u = torch.tensor(g, dtype=F64), torch.tensor(u, dtype=F64)
+    return ref.silu(g) * u
+
+
+# g and u of the even and of the odd features; |g u| of the even ones is 2^134 and 2^130, silu(g) u 0 and -1.5e32
+FAR = [((-2.0 ** 67, 4.0), (2.0 ** 67, 4.0)), ((-16.0, -16.0), (2.0 ** 126, 2.0 ** 126))]
+
+
+@pytest.mark.parametrize("n", [3, 300])
+@pytest.mark.parametrize("g,u", FAR)
+@pytest.mark.parametrize("dt", [torch.float16, BF16])
+def test_experts4(cuda_lib, n, g, u, dt):
+    moe = cuda_lib
+    h = h_of(g, u).repeat(I // 2)[None]
+    down = 2.0 ** -4 if h.abs().max() < 1e3 else 2.0 ** -120
+    mx = [moe.moe_mx_quantize(t, "mxfp4") for t in weights([v / H for v in g], [v / H for v in u], down)]
+    ex = moe.Mx4SwiGluExperts(*mx, dtype=dt)
+    x = torch.ones((n, H), dtype=dt, device="cuda")
+    out = ex.forward_dispatched(x, torch.tensor([0, n], dtype=torch.int32, device="cuda"))
+    want = (ref.rounded(h, "mxfp4").sum() * down).item()
+    assert abs(want) > 1e-7 and (out.double() == want).all(), (out.min(), out.max(), want)
+    y = ex.forward(x, torch.zeros((n, 1), device="cuda"), 1, True)
+    assert (y.double() == want).all()

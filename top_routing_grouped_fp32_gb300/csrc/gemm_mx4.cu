@@ -613,8 +613,9 @@ gemm_mx4_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant_
               const float2 uu = make_float2(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1]));
               const float2 t = mul2(gg, both(-kLog2e));
               const float2 n = add2(make_float2(exp2_fast(t.x), exp2_fast(t.y)), both(1.f));
-              // a few ulp of FP32: far below an e2m1 step
-              h[i] = mul2(mul2(gg, uu), make_float2(rcp_fast(n.x), rcp_fast(n.y)));
+              // a few ulp of FP32: far below an e2m1 step.  silu(g) first: g u may
+              // leave FP32's range where silu(g) u does not (g far below 0)
+              h[i] = mul2(mul2(gg, make_float2(rcp_fast(n.x), rcp_fast(n.y))), uu);
               a = max(a, max(mx::abs_bits(h[i].x), mx::abs_bits(h[i].y)));
             }
             const uint32_t sb = mx::scale_byte<MOE_MXFP4>(a);
