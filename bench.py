@@ -58,10 +58,10 @@ FALLBACK_PEAKS = {"hbm_gbs": 6800.0, "bf16_tflops": 1900.0, "bf16_tflops_sustain
 # white space left out) it was taken on; it is reported as null once that
 # code changes.
 GEMM_TRAFFIC = {
-    # one launch each on the headline workload: gate/up reads 1.142722304 GB and
-    # writes 264.786432 MB, down reads 0.646919168 GB and writes 369.974528 MB
-    "finegrained_bf16": {"bytes_per_launch": (1142722304 + 264786432 + 646919168 + 369974528) / 2,
-                         "code_sha256": "bb3259087c91cf1608a74f0c118cd5cdda9afd53c9c8e02051f9c50536a70cb1"},
+    # one launch each on the headline workload: gate/up reads 1.146031104 GB and
+    # writes 265.224448 MB, down reads 0.646924288 GB and writes 370.237184 MB
+    "finegrained_bf16": {"bytes_per_launch": (1146031104 + 265224448 + 646924288 + 370237184) / 2,
+                         "code_sha256": "85b1f982c7e403e79c89503543aa27b180cab9f70a97f6a7533c0155075b6e4b"},
 }
 
 

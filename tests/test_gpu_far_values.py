@@ -44,3 +44,19 @@ def test_experts4(cuda_lib, n, g, u, dt):
     assert abs(want) > 1e-7 and (out.double() == want).all(), (out.min(), out.max(), want)
     y = ex.forward(x, torch.zeros((n, 1), device="cuda"), 1, True)
     assert (y.double() == want).all()
+
+
+@pytest.mark.parametrize("n", [3, 300])
+@pytest.mark.parametrize("g,u", FAR)
+def test_forward_of_16_bit_experts(cuda_lib, n, g, u):
+    moe = cuda_lib
+    h = h_of(g, u).repeat(I // 2)
+    down = 2.0 ** -4 if h.abs().max() < 1e3 else 2.0 ** -120
+    ex = moe.SwiGluExperts(*(t.to(BF16) for t in weights([v / H for v in g], [v / H for v in u], down)))
+    x, off = torch.ones((n, H), dtype=BF16, device="cuda"), torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    want = h.sum().item() * down
+    # all terms of a sum have one sign: half a step for h, half a step for the result, FP32 in between
+    tol = abs(want) * (2 * 2.0 ** -8 + 2.0 ** -16)
+    for out in (ex.forward_dispatched(x, off), ex.forward_checkpoint(x, off)[0],
+                ex.forward(x, torch.zeros((n, 1), device="cuda"), 1, True)):
+        assert ((out.double() - want).abs() <= tol).all(), (out.min(), out.max(), want)

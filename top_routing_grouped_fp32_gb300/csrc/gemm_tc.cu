@@ -55,6 +55,7 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <limits>
 #include <mutex>
 #include <type_traits>
 
@@ -93,6 +94,7 @@ template <int CK>
 constexpr int kThreads = 64 + 128 * kEpilogues<CK>;
 constexpr uint32_t TMEM_COLS = 2 * BN;
 constexpr int MAX_E = 1024;
+constexpr float kFltMax = std::numeric_limits<float>::max();
 
 // KS: 64-deep K sub-blocks per ring stage.  KS = 2 (forward CTA-pair GEMMs,
 // K-major operands) halves the barrier round trips and commits per MMA: one
@@ -820,6 +822,7 @@ grouped_gemm_tc(const __grid_constant__ CUtensorMap mapA, const __grid_constant_
           const int b = i32 / fw, c = i32 - b * fw;
           const uint32_t gcol = (uint32_t)(b * 2 * fw + c);
           uint32_t g[32], u[32];
+          __syncwarp();
           tmem_ld32(taddr + gcol, g);
           tmem_ld32(taddr + gcol + fw, u);
           tmem_wait_ld(g);
@@ -835,13 +838,22 @@ grouped_gemm_tc(const __grid_constant__ CUtensorMap mapA, const __grid_constant_
             uint32_t hw[16];
 #pragma unroll
             for (int v = 0; v < 4; ++v) {
-              float f[8];
+              float f[8], top = 0.f;
 #pragma unroll
               for (int i = 0; i < 8; ++i) {
                 const float gg = __uint_as_float(g[v * 8 + i]);
                 const float uu = __uint_as_float(u[v * 8 + i]);
                 // 16-bit output: the fast divide's ~2 ulp are far below its rounding
                 f[i] = __fdividef(gg * uu, 1.f + __expf(-gg));
+                top = fmaxf(top, fabsf(gg * uu));
+              }
+              if (top > kFltMax) {  // g u leaves FP32's range: silu(g) u need not, for g below 0
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                  const float gg = __uint_as_float(g[v * 8 + i]);
+                  const float uu = __uint_as_float(u[v * 8 + i]);
+                  if (fabsf(gg * uu) > kFltMax) f[i] = gg / (1.f + __expf(-gg)) * uu;
+                }
               }
               put4(hw + 4 * v, pack8<T>(f));
             }
