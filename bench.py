@@ -58,10 +58,10 @@ FALLBACK_PEAKS = {"hbm_gbs": 6800.0, "bf16_tflops": 1900.0, "bf16_tflops_sustain
 # white space left out) it was taken on; it is reported as null once that
 # code changes.
 GEMM_TRAFFIC = {
-    # one launch each on the headline workload: gate/up reads 1.146031104 GB and
-    # writes 265.224448 MB, down reads 0.646924288 GB and writes 370.237184 MB
-    "finegrained_bf16": {"bytes_per_launch": (1146031104 + 265224448 + 646924288 + 370237184) / 2,
-                         "code_sha256": "85b1f982c7e403e79c89503543aa27b180cab9f70a97f6a7533c0155075b6e4b"},
+    # one launch each on the headline workload: gate/up reads 1.146209792 GB and
+    # writes 265.118464 MB, down reads 0.646886656 GB and writes 370.119680 MB
+    "finegrained_bf16": {"bytes_per_launch": (1146209792 + 265118464 + 646886656 + 370119680) / 2,
+                         "code_sha256": "9e12d8a3ad4c7d49c1bb1718801072b255327dd825b2ed9439326971591bd327"},
 }
 
 

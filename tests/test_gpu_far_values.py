@@ -60,3 +60,30 @@ def test_forward_of_16_bit_experts(cuda_lib, n, g, u):
     for out in (ex.forward_dispatched(x, off), ex.forward_checkpoint(x, off)[0],
                 ex.forward(x, torch.zeros((n, 1), device="cuda"), 1, True)):
         assert ((out.double() - want).abs() <= tol).all(), (out.min(), out.max(), want)
+
+
+@pytest.mark.parametrize("n", [3, 300])
+@pytest.mark.parametrize("far", [-128.0, -16.0])
+def test_backward_from_a_checkpoint(cuda_lib, n, far):
+    """da u of the first block of features is 2^141; da u silu'(g) is 0 or -5e36."""
+    moe = cuda_lib
+    one = torch.ones((n, 32), device="cuda")
+    g, u = torch.cat([far * one, one], 1), torch.cat([2.0 ** 66 * one, one], 1)
+    w_down = torch.cat([torch.full((1, H, 32), v, device="cuda") for v in (2.0 ** 30, 2.0 ** -40)], 2)
+    w = [torch.full((1, I, H), 2.0 ** -3, device="cuda")] * 2 + [w_down]
+    ex = moe.SwiGluExperts(*(t.to(BF16) for t in w))
+    ck = moe.ExpertCheckpoint(moe.moe_mx_quantize(g, "mxfp8"), moe.moe_mx_quantize(u, "mxfp8"))
+    x = torch.full((n, H), 2.0 ** -10, dtype=BF16, device="cuda")
+    dout = torch.full((n, H), 2.0 ** 40, dtype=BF16, device="cuda")
+    perm, off = torch.arange(n, dtype=torch.int32, device="cuda"), torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    got = ex.backward_checkpoint(moe.moe_mx_quantize(x, "mxfp8"), perm, off, ck, dout, 1)
+    g, u, x, dout = (t.to(F64) for t in (g, u, x, dout))
+    gate, up, down = (t[0].to(F64) for t in w)
+    da, s = dout @ down, torch.sigmoid(g)
+    dg, du, a = da * u * s * (1 + g * (1 - s)), da * g * s, g * s * u
+    want = (dg @ gate + du @ up, dg.t() @ x, du.t() @ x, dout.t() @ a)
+    # where a sum's terms differ in sign one of them outweighs the other by 2^60.  Half a step for each of the two
+    # roundings; a sigmoid below 2^-126 may count as 0, which moves none of these by more than 1e-6
+    for name, o, r in zip(("dinput", "dgate", "dup", "ddown"), got, want):
+        o = o.to(F64).view(r.shape)
+        assert ((o - r).abs() <= r.abs() * (2 * 2.0 ** -8 + 2.0 ** -15) + 1e-6).all(), (name, (o - r).abs().max())

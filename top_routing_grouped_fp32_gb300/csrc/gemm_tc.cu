@@ -744,7 +744,8 @@ grouped_gemm_tc(const __grid_constant__ CUtensorMap mapA, const __grid_constant_
               const float2 sg = make_float2(rcp_fast(n.x), rcp_fast(n.y));  // 16-bit outputs
               const float2 silu = mul2(gg, sg);
               const float2 slope = fma2(silu, fma2(sg, both(-1.f), both(1.f)), sg);
-              wdg[i] = pack2<T>(mul2(mul2(dv, uu), slope));
+              // (da u may leave FP32's range where the slope brings it back)
+              wdg[i] = pack2<T>(mul2(dv, mul2(uu, slope)));
               wdu[i] = pack2<T>(mul2(dv, silu));
               wa[i] = pack2<T>(mul2(silu, uu));
             }
