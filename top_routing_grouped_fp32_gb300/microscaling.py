@@ -160,7 +160,11 @@ class Mx4SwiGluExperts:
     [E,H,I] in "mxfp4" form; rows x and the outputs in ``dtype`` (float16 or
     bfloat16), rounded to 4 bits on the way in and between the products.  The
     object keeps the weights' values and its own re-ordered copy of the scales
-    alive; the scales it was given may go."""
+    alive; the scales it was given may go.  The re-ordering is enqueued on
+    ``stream`` (or the current one): calls on other streams have to be ordered
+    behind it.  When the object goes, its memory is handed out again only after
+    what its calls have enqueued by then, on whichever streams; a graph that was
+    captured needs the object for as long as it is replayed."""
 
     def __init__(self, gate: MxRows, up: MxRows, down: MxRows, dtype: torch.dtype = torch.bfloat16, stream=None):
         self.handle = None
@@ -181,15 +185,24 @@ class Mx4SwiGluExperts:
             _check(lib.moe_mx4_experts_create(*ptrs, _CODES[dtype], E, I, H, scales.data_ptr(), scales.nbytes, raw,
                                               ctypes.byref(h)))
         self._keep = (gate.values, up.values, down.values, scales)
-        if stream is not None:  # their memory may be reused on the current stream only after the re-ordering
-            for m in (gate, up, down):
-                m.scales.record_stream(stream)
+        self._streams = set()
+        self._read_on(stream, raw)
+        for m in (gate, up, down):  # read by the re-ordering
+            m.scales.record_stream(stream or torch.cuda.current_stream(dev))
         self.handle = h
 
     def __del__(self):
         if getattr(self, "handle", None) is not None:
             self._lib.moe_mx4_experts_destroy(self.handle)
             self.handle = None
+
+    def _read_on(self, stream, raw):
+        """Notes a stream that a call reads the weights on: what that stream holds when
+        they are freed comes before another use of their memory."""
+        if raw not in self._streams:
+            self._streams.add(raw)
+            for t in self._keep:
+                t.record_stream(stream or torch.cuda.current_stream(self.device))
 
     def workspace(self, N: int) -> torch.Tensor:
         """A workspace for forward_dispatched of up to N rows."""
@@ -213,6 +226,7 @@ class Mx4SwiGluExperts:
                 out = torch.empty((N, self.H), dtype=self.dtype, device=dev)
             if workspace is None:
                 workspace = self.workspace(N)
+            self._read_on(stream, raw)
             _check(self._lib.moe_mx4_experts_forward(self.handle, *args, _p(out, "out", dt, (N, self.H), dev),
                                                      *_ws(workspace, dev), raw))
         return out
@@ -231,6 +245,7 @@ class Mx4SwiGluExperts:
                 y = torch.empty((T, self.H), dtype=self.dtype, device=dev)
             if workspace is None:
                 workspace = self.forward_workspace(T, top_k, logits.dtype)
+            self._read_on(stream, raw)
             _check(call(self.handle, xp, lp, code, T, *route, _p(y, "y", dt, (T, self.H), dev),
                         *_ws(workspace, dev), raw))
         return y
