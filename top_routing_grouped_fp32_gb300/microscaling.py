@@ -80,13 +80,13 @@ class MxRows:
 
     def _checked(self, what: str, shape=None, format=None, device=None):
         """Pointers of values and scales; ``shape`` and ``format`` as the call needs them.
-        A call's rows are mostly those of the call before: what was checked is
-        remembered and compared with what the tensors are now."""
+        A call's rows are mostly like those of the call before: what was checked
+        of them is remembered (not the tensors) and compared with what they are now."""
         v, s, d = self.values, self.scales, self.__dict__
         known = d.get("_known")
         if known is not None:
-            kv, ks, fmt, cols, whole, vs, ss, index = known
-            if (kv is v and ks is s and fmt == self.format and cols == self.cols
+            fmt, cols, whole, vs, ss, index = known
+            if (fmt == self.format and cols == self.cols
                     and (shape is None or whole == shape) and (format is None or fmt == format)
                     and v.shape == vs and s.shape == ss and v.dtype is torch.uint8 and s.dtype is torch.uint8
                     and v.is_contiguous() and s.is_contiguous() and v.get_device() == index
@@ -103,7 +103,7 @@ class MxRows:
             raise ValueError(f"{what}.values: expected a CUDA tensor")
         vs, ss = _shapes(whole, self.format)
         got = (_p(v, f"{what}.values", _U8, vs, device), _p(s, f"{what}.scales", _U8, ss, device))
-        d["_known"] = (v, s, self.format, self.cols, whole, v.shape, s.shape, v.get_device())
+        d["_known"] = (self.format, self.cols, whole, v.shape, s.shape, v.get_device())
         return got
 
 
@@ -133,7 +133,7 @@ def moe_mx_dequantize(mx: MxRows, dtype: torch.dtype, perm: torch.Tensor | None 
     lib = _load()
     fmt = _format(mx.format)
     v, s = mx._checked("mx")
-    shape = mx.__dict__["_known"][4]
+    shape = mx.__dict__["_known"][2]
     dev, C = mx.values.device, mx.cols
     R = shape[:-1].numel()
     code = _CODES.get(dtype)
