@@ -80,7 +80,7 @@ def _p(t, what: str, dtypes, shape, device):
     if t.shape != shape:
         raise MoeError(2, f"{what} must have shape {tuple(shape)} (got {tuple(t.shape)})")
     if t.device != device:
-        raise ValueError(f"{what} is on {t.device}, the logits are on {device}")
+        raise ValueError(f"{what} is on {t.device}, the call's other tensors are on {device}")
     raise ValueError(f"{what}: expected a contiguous tensor")
 
 
@@ -140,7 +140,7 @@ def _num_seqs(seq_offsets) -> int:
 
 
 # the current device, and the current stream's handle without a Stream object around
-# it, where torch offers them (CUDA is initialised: the logits are on a device)
+# it, where torch offers them (CUDA is initialised: the tensors are on a device)
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 _current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                               lambda index: torch.cuda.current_stream(index).cuda_stream)
@@ -151,7 +151,7 @@ def _on(device: torch.device, stream):
     are current, and the stream's handle."""
     if stream is not None:
         if stream.device != device:
-            raise ValueError(f"stream is on {stream.device}, the logits are on {device}")
+            raise ValueError(f"stream is on {stream.device}, the call's tensors are on {device}")
         return torch.cuda.stream(stream), stream.cuda_stream
     index = device.index
     return _NOTHING if _current_device() == index else torch.cuda.device(device), _current_raw_stream(index)
