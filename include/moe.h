@@ -604,8 +604,9 @@ moe_status moe_mx_dequantize(const uint8_t* values, const uint8_t* scales, moe_m
  * The handle does not own the weights: gate, up and down values (16-byte
  * aligned) must stay alive and unchanged while it is used.  Their scales are
  * re-ordered once, on `stream`, into the caller's scale_buffer of
- * moe_mx4_experts_scale_bytes(E, I, H) bytes (256-byte aligned), which must
- * stay alive too; the given scales are not read after that.  Calls on other
+ * moe_mx4_experts_scale_bytes(E, I, H) bytes (256-byte aligned; it overlaps
+ * none of them, else MOE_ERR_INVALID_ARG), which must stay alive too; the given
+ * scales are not read after that.  Calls on other
  * streams must be ordered behind it by the caller.
  * ---------------------------------------------------------------------- */
 typedef struct moe_mx4_experts* moe_mx4_experts_t;

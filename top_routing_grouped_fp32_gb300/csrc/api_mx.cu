@@ -218,6 +218,12 @@ moe_status moe_mx4_experts_create(const uint8_t* gate, const uint8_t* gate_scale
   if (buffer_bytes < moe_mx4_experts_scale_bytes(E, I, H))
     return fail(MOE_ERR_INVALID_ARG, "scale_buffer too small: %zu bytes given, %zu needed", buffer_bytes,
                 moe_mx4_experts_scale_bytes(E, I, H));
+  // (each tensor's scales are re-ordered while the others' wait, and the values are used as they are)
+  const uint64_t vb = value_bytes(E * I, H, MOE_MXFP4), sb = scale_bytes(E * I, H), db = scale_bytes(E * H, I);
+  const Range scratch[1] = {{buffer, moe_mx4_experts_scale_bytes(E, I, H)}};
+  const Range held[6] = {{gate, vb}, {up, vb}, {down, vb}, {gate_scales, sb}, {up_scales, sb}, {down_scales, db}};
+  if (!apart(scratch, held))
+    return fail(MOE_ERR_INVALID_ARG, "scale_buffer must not overlap the weights or their scales");
   int dev = -1;
   MOE_TRY_CUDA(cudaGetDevice(&dev), "cudaGetDevice");
   const void* ptrs[7] = {gate, up, down, gate_scales, up_scales, down_scales, buffer};
