@@ -665,7 +665,8 @@ moe_status moe_mx4_forward_sigmoid_grouped(moe_mx4_experts_t experts, const void
  * [E,I,H], ddown [E,H,I]; experts without rows get zeros).  da and all sums
  * are FP32; dg, du and a are rounded once to the dtype as operands of the
  * products, x^ too (its four significant bits fit; a value past the dtype's
- * range is infinite).  N = T*top_k.  g and u are not recomputed: six of the
+ * range is infinite).  N = T*top_k, N + 63 E below 2^31 - 1 (else
+ * MOE_ERR_UNSUPPORTED).  g and u are not recomputed: six of the
  * eight products of moe_experts_backward are left.  workspace:
  * moe_experts_backward_checkpoint_workspace_size(experts, N) bytes, which also
  * serve every smaller batch.

@@ -805,8 +805,10 @@ moe_status moe_experts_backward_checkpoint(moe_experts_t x, const uint8_t* x_val
   if (top_k < 1 || top_k > kMaxK) return fail(MOE_ERR_INVALID_ARG, "top_k must be in 1..=64");
   if (T > kMaxRows / top_k) return fail(MOE_ERR_UNSUPPORTED, "T*top_k exceeds 2^31-1");
   const int64_t N = T * top_k;
-  if (!bwd_tc_ok(x, N))
+  if (!x->tc)
     return fail(MOE_ERR_UNSUPPORTED, "checkpoints need F16/BF16 experts with H, I multiples of 8");
+  if (!bwd_tc_ok(x, N))
+    return fail(MOE_ERR_UNSUPPORTED, "T*top_k=%lld rows, each expert's padded to 64, may exceed 2^31-1", (long long)N);
   if (!offsets || !dgate || !dup || !ddown)
     return fail(MOE_ERR_INVALID_ARG, "offsets, dgate, dup and ddown must be non-NULL");
   if (!aligned16(dgate) || !aligned16(dup) || !aligned16(ddown))
