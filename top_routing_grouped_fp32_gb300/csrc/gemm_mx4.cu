@@ -370,7 +370,10 @@ gemm_mx4_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant_
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           ok = __all_sync(0xffffffffu, mbar_wait<kCluster>(empty_bar(pr, h), phase ^ 1u, abort_flag, p.status));
-          if (!ok) break;
+          if (!ok) {
+            fills += h;  // the pair's first copies are in flight
+            break;
+          }
           if ((h == 0 || two) && elect_one()) {
             const uint32_t sa = ring + (2 * pr + h) * C::SLOT_BYTES;
             const uint32_t sb = HELD ? held + (2 * sp + h) * C::B_BYTES : sa + A_BYTES;
