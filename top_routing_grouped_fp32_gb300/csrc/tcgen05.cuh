@@ -78,11 +78,8 @@ __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 // arrival on a barrier of another CTA of the cluster (shared::cluster address)
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t cbar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cbar) : "memory");
-}
-// the same without ordering other memory accesses: for tensor-memory accesses
-// that were waited for (a release would wait for every load in flight)
+// without ordering other memory accesses: for tensor-memory accesses that were
+// waited for (a release would wait for every load in flight)
 __device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cbar) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cbar) : "memory");
 }
