@@ -662,7 +662,8 @@ moe_status moe_mx4_forward_sigmoid_grouped(moe_mx4_experts_t experts, const void
  *   dinput = dg W_gate + du W_up, dgate = sum_r dg_r^T x^_r,
  *   dup = sum_r du_r^T x^_r, ddown = sum_r dout_r^T a_r.
  * All gradients are in the weights' dtype (dinput [N,H], dgate and dup
- * [E,I,H], ddown [E,H,I]; experts without rows get zeros).  da and all sums
+ * [E,I,H], ddown [E,H,I]; experts without rows get zeros; moe_experts_backward
+ * gives weight gradients in FP32).  da and all sums
  * are FP32; dg, du and a are rounded once to the dtype as operands of the
  * products, x^ too (its four significant bits fit; a value past the dtype's
  * range is infinite).  N = T*top_k, N + 63 E below 2^31 - 1 (else

@@ -46,7 +46,9 @@
 // Where rows are 1025 to 2048 values long (HELD), an n-tile's B stays in shared
 // memory for up to four m-tiles, and the ring carries A alone.
 // What bounds it: on CTA pairs power (200 us of the headline's gate/up are 1.7 GHz
-// of 2.07) and the depth that shared memory leaves the ring, three spans.  A span
+// of 2.07), the MMAs' step of 64 (two thirds of the nominal 4-bit rate; PTX has one
+// of 96 for this architecture, not tried here) and the depth that shared memory
+// leaves the ring, three spans.  A span
 // takes 1070 to 1100 cycles at prompt batches, 800 of them MMAs; the MMA warp waits
 // 500 for copies, and these for free slots, or with HELD 260 for copies and 180 for
 // the epilogue (all eight warps on each tile, half its columns each, end that wait,

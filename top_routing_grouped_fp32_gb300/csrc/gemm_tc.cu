@@ -773,8 +773,9 @@ grouped_gemm_tc(const __grid_constant__ CUtensorMap mapA, const __grid_constant_
                   *reinterpret_cast<uint4*>(row + c + 4 * v) = make_uint4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]);
           }
         } else {
-          // kWgrad: rows of a weight-gradient tile, rounded once to T (an
-          // expert without rows gets zeros)
+          // kWgrad: rows of a weight-gradient tile, rounded once to T: an FP32
+          // gradient would double the stores, which set the pace where experts
+          // are many and small (an expert without rows gets zeros)
           const int64_t col0 = (int64_t)t.nb * 256;
           T* rowt = nullptr;
           if (row_ok) {
